@@ -11,6 +11,11 @@ in the library's CUDA kernels; torch only owns the memory and the stream.
     gemm_*_strided_batched(opA, opB, M, N, K, alpha, A, lda, strideA, B, ldb, strideB,
                            beta, C, ldc, strideC, batch)
     gemm_*_host(... same as the single calls, A, B, C in host memory ...)
+
+Routed products (a router, the experts' products, low-rank adapters; see routed.py):
+
+    moe_route, moe_plan, moe_dispatch, grouped_linear, moe_combine, lora_linear and the
+    gradients moe_route_backward, moe_combine_backward, gated_silu_backward, grouped_weight_grad
 """
 from __future__ import annotations
 
@@ -27,6 +32,22 @@ __all__ = [
     "gemm_kernel_launches", "gemm_measure_fp32_fma_peak", "gemm_sgemm_configs",
     "library_path", "load", "matmul",
 ]
+_ROUTED = (
+    "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch", "moe_combine",
+    "moe_combine_backward", "gated_silu_backward", "grouped_linear", "grouped_weight_grad",
+    "lora_linear",
+)
+__all__ += _ROUTED
+
+
+def __getattr__(name):
+    # routed.py needs torch at import; this package does not until a call is made
+    if name in _ROUTED:
+        from . import routed
+
+        globals()[name] = getattr(routed, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _op(op) -> int:

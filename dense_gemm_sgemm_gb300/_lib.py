@@ -48,6 +48,24 @@ SIGNATURES = {
     "gemm_tile_raster": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_i64),
                                 ctypes.POINTER(_i64)]),
     "gemm_sgemm_config": (_int, [_int, _vp]),
+    "gemm_moe_route": (_int, [_int, _i64, _i64, _vp, _i64, _vp, _int, _int, _int, _int, _int, _int,
+                              _f32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "gemm_moe_route_backward": (_int, [_int, _i64, _i64, _vp, _vp, _i64, _vp, _int, _int, _int, _f32,
+                                       _vp, _i64, _vp]),
+    "gemm_moe_plan": (_int, [_i64, _i64, _int, _vp, _vp, _vp, _vp, _vp]),
+    "gemm_moe_dispatch": (_int, [_int, _i64, _i64, _int, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "gemm_moe_combine": (_int, [_int, _int, _i64, _i64, _int, _vp, _i64, _i64, _vp, _vp, _vp, _i64,
+                                _vp]),
+    "gemm_moe_combine_backward": (_int, [_int, _int, _i64, _i64, _int, _vp, _i64, _vp, _i64, _i64, _vp,
+                                         _vp, _vp, _i64, _vp, _vp]),
+    "gemm_gated_silu_backward": (_int, [_int, _int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "gemm_grouped_linear": (_int, [_int, _int, _i64, _vp, _int, _int, _i64, _i64, _vp, _i64, _i64, _vp,
+                                   _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "gemm_grouped_weight_grad": (_int, [_int, _int, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64,
+                                        _vp, _i64, _i64, _vp]),
+    "gemm_lora_linear": (_int, [_int, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp,
+                                _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
+                                _vp]),
 }
 
 class SgemmConfig(ctypes.Structure):

@@ -1,0 +1,421 @@
+// Products with few rows per weight matrix: a decoding step's experts, a decoding step's linear
+// layer with adapters, and the inner product of the adapters (semantics: include/gemm_gb300.h).
+//
+// With a handful of rows a product is bound by reading its weights once: at 8 rows a weight matrix
+// brings 8 flops per byte, where the tensor cores could do 280.  So the weights never touch shared
+// memory.  A warp computes D[feature][token] = W X^T with mma.sync m16n8k16: the weight rows are
+// the m side (16 or 32 rows a warp), up to 8 * NT tokens the n side.  The order of k inside a
+// product is free as long as both operands agree, so lane (g, t) loads 16 contiguous bytes --
+// W[g][8 t .. 8 t + 7] of a 32-wide k step, X likewise -- and the four registers of the load are
+// the fragments of two MMAs: every weight byte goes from global memory to its register in one
+// 16-byte load, several steps ahead of use.  K is split over warps of the CTA where rows alone do
+// not fill the machine; their partial sums meet in shared memory in a fixed order.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "routed_internal.h"
+
+namespace gemm {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRowStride = 36;  // floats between tokens of a warp's partial tile: 8 t + g, no bank twice
+constexpr unsigned kFull = 0xffffffffu;
+
+template <class T>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Weights are read once: no line of L1 for them.
+__device__ __forceinline__ uint4 load_stream(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Elements [k, k + 8) of a row of K elements: zeros beyond K, nothing read there.
+template <class T> __device__ __forceinline__ uint4 load_tail(const T *row, int64_t k, int64_t K)
+{
+    if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4 *>(row + k));
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(row);
+    uint16_t *dst = reinterpret_cast<uint16_t *>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K) dst[i] = __ldg(src + k + i);
+    return v;
+}
+
+// acc[mt][nt] += W X^T over k in [kb, ke) (kb a multiple of 32, ke one or K).  w[mt][h]: the row of
+// this lane's group in the lower and upper half of tile mt; x[nt]: the token row of this lane's
+// group, NULL for a column of zeros.
+template <class T, int MT, int NT>
+__device__ __forceinline__ void warp_product(const T *const (&w)[MT][2], const T *const (&x)[NT], int64_t kb,
+                                             int64_t ke, int64_t K, int lane, float (&acc)[MT][NT][4])
+{
+    constexpr int U = MT * 2 * 4 * 4 + NT * 4 * 4 <= 96 ? 4 : MT * 2 * 4 * 2 + NT * 4 * 2 <= 96 ? 2 : 1;
+    const int t8 = (lane & 3) * 8;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    auto multiply = [&](const uint4 (&a)[MT][2], const uint4 (&b)[NT]) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_16816<T>(acc[m][n], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, b[n].x, b[n].y);
+                mma_16816<T>(acc[m][n], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, b[n].z, b[n].w);
+            }
+    };
+    int64_t k = kb;
+    for (; k + 32 * U <= ke; k += 32 * U) {
+        uint4 a[U][MT][2], b[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) a[u][m][h] = load_stream(w[m][h] + k + 32 * u + t8);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                b[u][n] = x[n] != nullptr ? __ldg(reinterpret_cast<const uint4 *>(x[n] + k + 32 * u + t8)) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(a[u], b[u]);
+    }
+    for (; k < ke; k += 32) {
+        uint4 a[MT][2], b[NT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) a[m][h] = load_tail(w[m][h], k + t8, K);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) b[n] = x[n] != nullptr ? load_tail(x[n], k + t8, K) : zero;
+        multiply(a, b);
+    }
+}
+
+// Partial tile of a warp to shared memory as [token][feature row].
+template <int MT, int NT>
+__device__ __forceinline__ void put_partial(float *part, const float (&acc)[MT][NT][4], int lane)
+{
+    constexpr int kStride = MT <= 2 ? kRowStride : 68;  // 64 rows; again 8 t + g
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                part[(n * 8 + 2 * t + (c & 1)) * kStride + m * 16 + g + 8 * (c >> 1)] = acc[m][n][c];
+}
+
+__device__ __forceinline__ int32_t clamp_to(int32_t v, int64_t hi) { return v < 0 ? 0 : v > hi ? int32_t(hi) : v; }
+
+// First position and rows of the i-th group that has rows; false when there are fewer.
+__device__ __forceinline__ bool nonempty_group(const GroupedArgs &a, int i, int lane, int &group, int &first, int &rows)
+{
+    if (a.offsets == nullptr) {
+        group = 0;
+        first = 0;
+        rows = int(a.y_rows);
+        return i == 0 && rows > 0;
+    }
+    int seen = 0;
+    for (int e0 = 0; e0 < a.groups; e0 += 32) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < a.groups) {
+            lo = clamp_to(__ldg(a.offsets + e), a.y_rows);
+            hi = clamp_to(__ldg(a.offsets + e + 1), a.y_rows);
+        }
+        const unsigned has = __ballot_sync(kFull, hi > lo);
+        const int n = __popc(has);
+        if (seen + n > i) {
+            const int at = __fns(has, 0, i - seen + 1);
+            group = e0 + at;
+            first = __shfl_sync(kFull, lo, at);
+            rows = __shfl_sync(kFull, hi, at) - first;
+            return true;
+        }
+        seen += n;
+    }
+    return false;
+}
+
+// CTA: (8 / KS) runs of feature rows (32, or 16 gate rows with their 16 up rows) of one group times
+// all of its tokens, 8 * NT at a time; KS warps share a run, each summing its part of K.
+template <class T, class Y, int NT, bool GATED>
+__global__ void __launch_bounds__(kThreads) few_rows_kernel(const GroupedArgs a, const int ks)
+{
+    extern __shared__ float parts[];  // kWarps x (8 NT) x kRowStride
+    constexpr int kTokens = 8 * NT;
+    constexpr int kFeat = GATED ? 16 : 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+    int group, first, rows;
+    if (!nonempty_group(a, blockIdx.y, lane, group, first, rows)) return;
+    const int block_feat = kWarps / ks * kFeat;
+    const int64_t f0 = int64_t(blockIdx.x) * block_feat + warp / ks * kFeat;  // of this warp
+    const T *W = static_cast<const T *>(a.W) + int64_t(group) * a.stridew;
+    const T *w[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int64_t f = f0 + 8 * h + g + (GATED ? 0 : 16 * m);
+            if (f >= a.N) f = a.N - 1;  // computed, not stored
+            w[m][h] = W + (GATED && m == 1 ? f + a.N : f) * a.ldw;
+        }
+    const int64_t chunks = (a.K + 31) / 32, part = warp % ks;
+    const int64_t kb = chunks * part / ks * 32;
+    int64_t ke = chunks * (part + 1) / ks * 32;
+    if (ke > a.K) ke = a.K;
+    for (int n0 = int(blockIdx.z) * kTokens; n0 < rows; n0 += int(gridDim.z) * kTokens) {
+        const T *x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int i = n0 + 8 * n + g;
+            int64_t r = -1;
+            if (i < rows) r = a.rows != nullptr ? __ldg(a.rows + first + i) : first + i;
+            x[n] = r >= 0 && r < a.x_rows ? static_cast<const T *>(a.X) + r * a.ldx : nullptr;
+        }
+        float acc[2][NT][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[m][n][c] = 0.0f;
+        warp_product<T, 2, NT>(w, x, kb, ke, a.K, lane, acc);
+        __syncthreads();  // the partial tiles of the previous tokens have been read
+        put_partial<2, NT>(parts + warp * kTokens * kRowStride, acc, lane);
+        // adapters: their inner products come from the kernel before this one
+        if (a.ad.b != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+        __syncthreads();
+        for (int i = threadIdx.x; i < block_feat * kTokens; i += kThreads) {
+            const int f = i % block_feat, n = i / block_feat;
+            const int64_t feat = int64_t(blockIdx.x) * block_feat + f;
+            if (n0 + n >= rows || feat >= a.N) continue;
+            const int64_t p = first + n0 + n;
+            const float *src = parts + ((f / kFeat) * ks * kTokens + n) * kRowStride + f % kFeat;
+            float v = 0.0f, u = 0.0f;
+            for (int q = 0; q < ks; ++q) {
+                v += src[q * kTokens * kRowStride];
+                if (GATED) u += src[q * kTokens * kRowStride + 16];
+            }
+            if (GATED) {
+                if (a.pre != nullptr) {
+                    T *pre = static_cast<T *>(a.pre) + p * a.ldp + feat;
+                    pre[0] = from_f32<T>(v);
+                    pre[a.N] = from_f32<T>(u);
+                }
+                v = v * sigmoid(v) * u;
+            }
+            if (a.ad.b != nullptr) {
+                const int which = __ldcg(a.ad.which + p);
+                if (unsigned(which) < unsigned(a.ad.count)) {
+                    const T *b = static_cast<const T *>(a.ad.b) + int64_t(which) * a.ad.strideb + feat * a.ad.ldb;
+                    const float *inner = a.ad.inner + p * a.ad.rank;
+                    for (int j = 0; j < a.ad.rank; j += 8) {
+                        const uint4 q = load_tail(b, j, a.ad.rank);
+                        const T *e = reinterpret_cast<const T *>(&q);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            if (j + c < a.ad.rank) v = fmaf(to_f32(e[c]), __ldcg(inner + j + c), v);
+                    }
+                }
+            }
+            static_cast<Y *>(a.Y)[p * a.ldy + feat] = from_f32<Y>(v);
+        }
+    }
+    // a CTA without tokens of its own still orders this launch behind the one before it
+    if (a.ad.b != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Inner products of the adapters: inner[t][r] = scale * sum_k X[t][k] A_a[r][k] for 64 (16 MT) ranks
+// of up to 8 * NT tokens of one request, K split over the CTA's 8 warps.
+//
+// CTA i takes item i of an enumeration that needs no scan: cutting the tokens both at multiples of
+// 8 NT and at the request boundaries, request s has the items t = segments[s] / (8 NT) + s ..
+// segments[s + 1] / (8 NT) + s, so the request of item i is the last s whose first item is <= i.
+template <class T, int MT, int NT>
+__global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
+{
+    extern __shared__ float parts[];  // kWarps x (8 NT) x stride
+    constexpr int kTokens = 8 * NT;
+    constexpr int kStride = MT <= 2 ? kRowStride : 68;
+    // the product that follows may start reading its weights now; it waits before it reads inner
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+    auto seg = [&](int q) { return clamp_to(__ldg(a.segments + q), a.T); };
+    if (blockIdx.y == 0) {  // tokens of no request
+        if (blockIdx.x == 0)
+            for (int t = threadIdx.x; t < seg(0); t += kThreads) a.which[t] = -1;
+        if (blockIdx.x == gridDim.x - 1)
+            for (int t = seg(a.requests) + threadIdx.x; t < a.T; t += kThreads) a.which[t] = -1;
+    }
+    const int item = blockIdx.x;
+    int lo = 0, hi = a.requests - 1;  // last request whose first item is <= item
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (seg(mid) / kTokens + mid <= item) lo = mid;
+        else hi = mid - 1;
+    }
+    const int tile = item - lo;
+    if (tile < 0) return;
+    const int t0 = max(seg(lo), tile * kTokens);
+    const int t1 = int(min(int64_t(seg(lo + 1)), int64_t(tile + 1) * kTokens));
+    if (t0 >= t1) return;
+    int ad = __ldg(a.adapters + lo);
+    if (unsigned(ad) >= unsigned(a.n_adapters)) ad = -1;
+    if (blockIdx.y == 0)
+        for (int t = t0 + int(threadIdx.x); t < t1; t += kThreads) a.which[t] = ad;
+    if (ad < 0) return;
+
+    const int r0 = blockIdx.y * 16 * MT;
+    const T *A = static_cast<const T *>(a.A) + int64_t(ad) * a.stridea;
+    const T *w[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[m][h] = A + int64_t(min(r0 + 16 * m + 8 * h + g, a.R - 1)) * a.lda;
+    const T *x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int t = t0 + 8 * n + g;
+        x[n] = t < t1 ? static_cast<const T *>(a.X) + int64_t(t) * a.ldx : nullptr;
+    }
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[m][n][c] = 0.0f;
+    const int64_t chunks = (a.K + 31) / 32;
+    const int64_t kb = chunks * warp / kWarps * 32, ke = min(chunks * (warp + 1) / kWarps * 32, a.K);
+    warp_product<T, MT, NT>(w, x, kb, ke, a.K, lane, acc);
+    put_partial<MT, NT>(parts + warp * kTokens * kStride, acc, lane);
+    __syncthreads();
+    const float scale = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
+    const int ranks = min(16 * MT, a.R - r0);
+    for (int i = threadIdx.x; i < ranks * (t1 - t0); i += kThreads) {
+        const int r = i % ranks, n = i / ranks;
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) v += parts[(q * kTokens + n) * kStride + r];
+        a.inner[int64_t(t0 + n) * a.R + r0 + r] = scale * v;
+    }
+}
+
+template <class K> cudaError_t allow_smem(K *kernel, size_t bytes)
+{
+    return bytes > 48 * 1024
+               ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))
+               : cudaSuccess;
+}
+
+// Launch; `after`: the launch may begin before the one ahead of it on the stream has ended.
+template <class K, class... Args>
+cudaError_t launch_after(K *kernel, dim3 grid, size_t smem, cudaStream_t stream, bool after, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = after ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) count_launches();
+    return e;
+}
+
+template <class T, class Y, int NT, bool GATED>
+cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, int64_t groups, int64_t depth, cudaStream_t stream)
+{
+    constexpr int kFeat = GATED ? 16 : 32;
+    const int64_t runs = (a.N + kFeat - 1) / kFeat;
+    // K is split until there are 16 warps for every SM or a part is shorter than 256
+    int ks = 1;
+    while (ks < kWarps && groups * runs * depth * ks < 16 * int64_t(dev.num_sms) && a.K / (2 * ks) >= 256) ks *= 2;
+    const int64_t per = kWarps / ks;
+    const size_t smem = size_t(kWarps) * 8 * NT * kRowStride * sizeof(float);
+    auto *kernel = few_rows_kernel<T, Y, NT, GATED>;
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(unsigned((runs + per - 1) / per), unsigned(groups), unsigned(depth));
+    return launch_after(kernel, grid, smem, stream, a.ad.b != nullptr, a, ks);
+}
+
+template <class T, class Y> cudaError_t few_rows_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+{
+    const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;  // at most that many have rows
+    const int64_t mean = (a.y_rows + groups - 1) / groups;
+    auto go = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        // CTAs side by side for the tokens of the average group, at most 64
+        int64_t depth = (mean + 8 * NT - 1) / (8 * NT);
+        if (depth > 64) depth = 64;
+        return a.gated ? launch_few_rows<T, Y, NT, true>(dev, a, groups, depth, stream)
+                       : launch_few_rows<T, Y, NT, false>(dev, a, groups, depth, stream);
+    };
+    if (mean <= 8) return go(std::integral_constant<int, 1>{});
+    if (mean <= 32) return go(std::integral_constant<int, 4>{});
+    return go(std::integral_constant<int, 8>{});
+}
+
+template <class T, int MT, int NT> cudaError_t launch_shrink_t(const ShrinkArgs &a, cudaStream_t stream)
+{
+    constexpr int kStride = MT <= 2 ? kRowStride : 68;
+    const size_t smem = size_t(kWarps) * 8 * NT * kStride * sizeof(float);
+    auto *kernel = shrink_kernel<T, MT, NT>;
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(unsigned(a.T / (8 * NT) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
+    return launch_after(kernel, grid, smem, stream, false, a);
+}
+
+template <class T> cudaError_t shrink_t(const ShrinkArgs &a, cudaStream_t stream)
+{
+    // requests of one or a few tokens: 8 at a time (a 32-token tile would read its X rows in vain)
+    const bool small = a.T <= 8 * int64_t(a.requests);
+    if (a.R <= 16) return small ? launch_shrink_t<T, 1, 1>(a, stream) : launch_shrink_t<T, 1, 4>(a, stream);
+    if (a.R <= 32) return small ? launch_shrink_t<T, 2, 1>(a, stream) : launch_shrink_t<T, 2, 4>(a, stream);
+    return small ? launch_shrink_t<T, 4, 1>(a, stream) : launch_shrink_t<T, 4, 4>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+{
+    if (a.type == GEMM_TYPE_F16)
+        return a.y_type == GEMM_TYPE_F32 ? few_rows_t<__half, float>(dev, a, stream) : few_rows_t<__half, __half>(dev, a, stream);
+    return a.y_type == GEMM_TYPE_F32 ? few_rows_t<__nv_bfloat16, float>(dev, a, stream)
+                                     : few_rows_t<__nv_bfloat16, __nv_bfloat16>(dev, a, stream);
+}
+
+cudaError_t launch_shrink(const ShrinkArgs &a, cudaStream_t stream)
+{
+    return a.type == GEMM_TYPE_F16 ? shrink_t<__half>(a, stream) : shrink_t<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace gemm

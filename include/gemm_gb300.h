@@ -287,6 +287,182 @@ GEMM_API gemm_status_t gemm_sgemm_config(int index, gemm_sgemm_config_t *out);
 GEMM_API gemm_status_t gemm_tile_raster(int64_t t, int64_t tiles_m, int64_t tiles_n, int log_group,
                                int64_t *tile_m, int64_t *tile_n);
 
+/* ------------------------------------------------------------------------------------------
+ * Routed products: linear layers whose weights differ from row to row, because a router gave
+ * each token its experts or because each request brings an adapter of its own, and what decides
+ * which rows meet which weights.  The source pages have no counterpart; rows, leading dimensions,
+ * streams, statuses and asynchrony are those of the GEMM calls above.
+ *
+ * Every array is device memory owned by the caller, index arrays are int32, and no call keeps
+ * anything from one call for the next: no scratch memory is allocated, so every call may be
+ * captured into a graph.  Index values are checked on the device: an expert, adapter, row or
+ * position outside its range counts as "none" and is skipped, never followed.
+ *
+ * Vocabulary.  T tokens, E experts, k experts per token.  SLOT t * k + j is the j-th choice of
+ * token t.  The plan orders the slots by expert (stable: slots of one expert in ascending order)
+ * and calls a slot's place in that order its POSITION: expert e owns positions
+ * offsets[e] .. offsets[e + 1] - 1, tokens[position] is the slot's token, where[slot] its
+ * position.  Slots without an expert (-1) have no position (where = -1); arrays of T * k
+ * positions are then used only up to offsets[E].
+ */
+typedef enum { GEMM_TYPE_F32 = 0, GEMM_TYPE_F16 = 1, GEMM_TYPE_BF16 = 2 } gemm_type_t;
+typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score_t;
+
+/*
+ * Routing to experts.  For each row x of logits (T x E, leading dimension ld, fp32 or 16-bit,
+ * computed in fp32):
+ *     s = softmax(x) or 1 / (1 + exp(-x)),   c = s + bias   (bias: E floats, or NULL)
+ *     groups > 1: the E experts form `groups` runs of E / groups; a run's value is the sum of its
+ *       group_top (1 or 2) largest c, and only the groups_kept runs of largest value stay
+ *     ids[t]     = the top_k experts of largest c that stay, largest first
+ *     weights[t] = scale * s[ids], divided by their sum first when renormalise is not 0
+ * The bias (a load-balancing term) takes part in the choice only.  Without a bias the choice goes
+ * by the logit, whose order is that of s.  Ties go to the lowest index, of experts and of runs.
+ *
+ * Masks: a logit of -inf or NaN, or a c of -inf or NaN, takes its expert out of the choice (and a
+ * masked logit out of the softmax); +inf counts as the largest finite value.  Where fewer than
+ * top_k experts are left the remaining ids are -1 with weight 0; a row with none is all -1.
+ * Weights whose sum is 0 are 0.
+ *
+ * With offsets (E + 1), tokens (T * top_k) and where (T * top_k) the call also writes the plan;
+ * all three NULL leaves it out.
+ * Limits: 1 <= E <= 1024, 1 <= top_k <= min(32, E / groups * groups_kept), groups <= 32 dividing
+ * E, T * max(E, top_k) < 2^31.  T == 0 writes offsets only.
+ */
+GEMM_API gemm_status_t gemm_moe_route(gemm_type_t type, int64_t T, int64_t E, const void *logits,
+                                      int64_t ld, const float *bias, gemm_score_t score, int groups,
+                                      int groups_kept, int group_top, int top_k, int renormalise,
+                                      float scale, int32_t *ids, float *weights, int32_t *offsets,
+                                      int32_t *tokens, int32_t *where, void *stream);
+
+/*
+ * Gradient of the weights of gemm_moe_route with respect to the logits, the choice held fixed:
+ * dlogits (T x E, leading dimension ldd, the type of the logits) from dweights (T x top_k), the
+ * logits and the ids of the forward call, with the same score, renormalise and scale.  With
+ * s, S = sum over the row's ids of s[id]:
+ *     ds[id_j] = scale * dw_j,  or renormalised  scale / S * (dw_j - sum_i dw_i s[id_i] / S)
+ *     dx = s * (ds - sum(ds * s))  (softmax)     dx = ds * s * (1 - s)  (sigmoid)
+ * Every element of dlogits is written; masked logits and rows without an expert get 0.
+ */
+GEMM_API gemm_status_t gemm_moe_route_backward(gemm_type_t type, int64_t T, int64_t E,
+                                               const float *dweights, const void *logits, int64_t ld,
+                                               const int32_t *ids, gemm_score_t score, int top_k,
+                                               int renormalise, float scale, void *dlogits,
+                                               int64_t ldd, void *stream);
+
+/*
+ * The plan of given choices ids (T x top_k, -1 or out of range: none; a token may name an expert
+ * twice).  Limits: 1 <= E <= 1024, 1 <= top_k <= 1024, T * top_k < 2^31.
+ */
+GEMM_API gemm_status_t gemm_moe_plan(int64_t T, int64_t E, int top_k, const int32_t *ids,
+                                     int32_t *offsets, int32_t *tokens, int32_t *where, void *stream);
+
+/*
+ * Rows out to their positions: out[where[t * k + j]] = w[t * k + j] * x[t], for all slots that have
+ * a position below `positions`; weights NULL: 1.  x is T x H, out positions x H, both of `type`.
+ */
+GEMM_API gemm_status_t gemm_moe_dispatch(gemm_type_t type, int64_t T, int64_t H, int top_k,
+                                         const void *x, int64_t ldx, const int32_t *where,
+                                         const float *weights, int64_t positions, void *out,
+                                         int64_t ldo, void *stream);
+
+/*
+ * Rows back to their tokens: y[t] = sum over j of weights[t * k + j] * rows[where[t * k + j]]
+ * (weights NULL: 1), summed in fp32 in the order of j.  rows is positions x H of rows_type, y
+ * T x H of y_type.  A token without a position gets 0.
+ */
+GEMM_API gemm_status_t gemm_moe_combine(gemm_type_t rows_type, gemm_type_t y_type, int64_t T, int64_t H,
+                                        int top_k, const void *rows, int64_t ldr, int64_t positions,
+                                        const int32_t *where, const float *weights, void *y,
+                                        int64_t ldy, void *stream);
+
+/*
+ * Gradient of gemm_moe_combine: drows[where[slot]] = weights[slot] * dy[t] (drows and dy of `type`)
+ * and dweights[slot] = the dot product of dy[t] and rows[where[slot]] in fp32 (0 for a slot without
+ * a position).
+ */
+GEMM_API gemm_status_t gemm_moe_combine_backward(gemm_type_t type, gemm_type_t rows_type, int64_t T,
+                                                 int64_t H, int top_k, const void *dy, int64_t lddy,
+                                                 const void *rows, int64_t ldr, int64_t positions,
+                                                 const int32_t *where, const float *weights,
+                                                 void *drows, int64_t lddr, float *dweights,
+                                                 void *stream);
+
+/*
+ * Gradient of the gated activation h = silu(gate) * up, pre = [gate | up] (rows x 2 I):
+ *     dgate = dh * up * g (1 + gate (1 - g)),   dup = dh * gate * g,   g = 1 / (1 + exp(-gate))
+ * pre and dpre (rows x 2 I) are of `type`, dh (rows x I) of dh_type (`type` or fp32); computed in
+ * fp32.  dpre may be pre.
+ */
+GEMM_API gemm_status_t gemm_gated_silu_backward(gemm_type_t type, gemm_type_t dh_type, int64_t rows,
+                                                int64_t I, const void *pre, int64_t ldp, const void *dh,
+                                                int64_t lddh, void *dpre, int64_t lddp, void *stream);
+
+/*
+ * Grouped linear layer: for every group g and every position p of offsets[g] .. offsets[g + 1] - 1
+ *     Y[p] = X[r(p)] * op(W_g),   r(p) = rows[p], or p when rows is NULL,
+ * fp16 or bf16 inputs (`type`, not fp32), fp32 accumulation on the tensor cores, Y of y_type (fp32
+ * or `type`), N columns.  W_g = W + g * strideW; opW = GEMM_OP_T reads it as stored N x K (a linear
+ * layer's weight: Y = X W^T), opW = GEMM_OP_N as stored K x N (the layer's input gradient
+ * dX = dY W).  X has x_rows rows; a position whose row is outside [0, x_rows) is computed as if its
+ * row were zeros.  Y has y_rows rows; positions at or beyond it are not written.
+ *
+ * gated (opW = GEMM_OP_T only): W_g holds 2 N rows, N gate rows and then N up rows, and
+ *     Y[p] = silu(gate) * up,   gate = X[r(p)] * W_gate^T,   up = X[r(p)] * W_up^T,
+ * with both factors in fp32.  pre (y_rows x 2 N of `type`, or NULL) receives [gate | up], which
+ * gemm_gated_silu_backward needs.
+ *
+ * offsets (groups + 1 values) must not decrease; values are clamped to [0, y_rows].  Y must not
+ * overlap the inputs.  K == 0 writes zeros.
+ * Alignment: X, W and pre 16-byte aligned, ldx, ldw, strideW and ldp multiples of 8 elements, Y
+ * 16-byte aligned with ldy a multiple of 8 (else GEMM_ERR_MISALIGNED); N and K are free.
+ * Limits: groups <= 1024, y_rows and x_rows < 2^31, N and K < 2^24.
+ */
+GEMM_API gemm_status_t gemm_grouped_linear(gemm_type_t type, gemm_type_t y_type, int64_t groups,
+                                           const int32_t *offsets, gemm_op_t opW, int gated,
+                                           int64_t N, int64_t K, const void *X, int64_t ldx,
+                                           int64_t x_rows, const int32_t *rows, const void *W,
+                                           int64_t ldw, int64_t strideW, void *Y, int64_t ldy,
+                                           int64_t y_rows, void *pre, int64_t ldp, void *stream);
+
+/*
+ * Weight gradient of the grouped linear layer: for every group
+ *     dW_g = sum over positions p of the group of dY[p]^T * X[p]       (N x K, leading dimension lddw)
+ * dY (positions x N) and X (positions x K) of `type` (fp16 or bf16), fp32 accumulation, dW of
+ * dw_type (fp32 or `type`).  A group without positions gets zeros.  Where X's rows were gathered,
+ * gemm_moe_dispatch lays them out first.
+ * Alignment: dY, X, dW 16-byte aligned, all leading dimensions and strideDW multiples of 8
+ * elements.  Limits as above.
+ */
+GEMM_API gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw_type, int64_t groups,
+                                                const int32_t *offsets, int64_t N, int64_t K,
+                                                const void *dY, int64_t lddy, const void *X,
+                                                int64_t ldx, int64_t positions, void *dW,
+                                                int64_t lddw, int64_t strideDW, void *stream);
+
+/*
+ * A shared linear layer with the low-rank adapters of many requests beside it:
+ *     Y[t] = X[t] W^T + scales[a] * (X[t] A_a^T) B_a^T,     a = the adapter of token t,
+ * X (T x K), W (N x K), A_a = A + a * strideA (R x K) and B_a = B + a * strideB (N x R) of `type`
+ * (fp16 or bf16), Y (T x N) of y_type (fp32 or `type`).  Tokens lie request by request: request q
+ * owns tokens segments[q] .. segments[q + 1] - 1 (requests + 1 values that do not decrease,
+ * clamped to [0, T]) and uses adapter adapters[q]; an adapter outside [0, n_adapters) means none,
+ * as does lying in no request.  scales: n_adapters floats, NULL: 1.  An adapter of a rank below R
+ * is padded with zero rows of A_a.  The inner product X A^T stays in fp32.
+ *
+ * work: T * (R + 1) floats for the call to use (not kept; NULL when there are no requests, no
+ * adapters or R == 0).
+ * Alignment: X, W, A, B, Y 16-byte aligned; ldx, ldw, lda, ldb, ldy, strideA, strideB multiples of
+ * 8 elements.  Limits: R <= 128, T < 2^24, requests < 2^24, N and K < 2^24.
+ */
+GEMM_API gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, int64_t N,
+                                        int64_t K, const void *X, int64_t ldx, const void *W,
+                                        int64_t ldw, int64_t requests, const int32_t *segments,
+                                        const int32_t *adapters, int64_t n_adapters, int64_t R,
+                                        const void *A, int64_t lda, int64_t strideA, const void *B,
+                                        int64_t ldb, int64_t strideB, const float *scales, void *Y,
+                                        int64_t ldy, float *work, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
