@@ -1,0 +1,1005 @@
+// Grouped products with many rows per weight matrix on the tcgen05 tensor cores: the grouped linear
+// layer (either storage of W, gated or not), the linear layer with adapters, and the weight gradient
+// (semantics: include/gemm_gb300.h).
+//
+// Forward and input gradient.  A group's rows are many or few and never a multiple of a tile, so the
+// features take the MMA's m side, where tiles are fixed, and the tokens its n side, which is any
+// multiple of 32 up to 256: D[feature][token] = W_g X^T.  Two CTAs on neighbouring SMs form a 256 x n
+// tile (tcgen05.mma.cta_group::2; each loads its own 128 weight rows and half of the tokens).  Warps:
+//   0     TMA producer: per 64-wide K slice the weight boxes and the token rows, contiguous rows in
+//         boxes of 16, gathered rows four at a time (tile::gather4) by all lanes;
+//   1     MMA issuer (of the pair's first CTA) and TMEM owner, two 256-column accumulators;
+//   2-5   epilogue: one TMEM lane is one feature, so 32 tokens x 32 features pass through shared
+//         memory per warp and leave as 16-byte pieces of token rows.
+// gated: a CTA's 128 rows are 64 gate rows and their 64 up rows; the warps that hold a gate and its
+// up exchange halves through shared memory.  Adapters: the epilogue adds inner[token] . B[feature]
+// in fp32 while the tensor cores work on the next tile, so the low-rank product costs no MMA and
+// needs no tokens of one adapter in a row; the kernel ahead of it computes `inner` meanwhile.
+//
+// Weight gradient.  dW_g[n][k] sums over the group's positions, the K dimension of this product,
+// both operands "transposed" (MN-major).  Slices are 64 positions; the last one of a group also holds
+// rows of the next group, which a cleaner warp overwrites with zeros in shared memory before the MMAs
+// read them (multiplying them by zero would let their infinities through).
+//
+// Every wait is bounded: when one expires the kernel raises the device's error word, stops all
+// roles, waits (bounded) for its own copies and MMAs in flight, frees its TMEM and returns.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdlib>
+#include <cstring>
+
+#include "routed_internal.h"
+#include "tcgen05_ptx.cuh"
+#include "tensor_map.h"
+
+namespace gemm {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kStageA = 128 * 128;  // bytes: 128 weight rows (or 64 k rows x 2 boxes) of 128 bytes
+constexpr int kStageB = 128 * 128;  // bytes: up to 128 token rows
+constexpr int kEpiBytes = 4 * 32 * 32 * 4;  // a 32 x 32 fp32 staging tile per epilogue warp
+constexpr int kBarBytes = 256;
+constexpr int kTmemCols = 512, kAccCols = 256;
+constexpr int kMaxGroups = 1024;
+constexpr int kTableBytes = 2 * (kMaxGroups + 2) * 4;  // first position and first unit of every group
+constexpr int kSmemBytes = kStages * (kStageA + kStageB) + kEpiBytes + kBarBytes + kTableBytes + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ int clamp_to(int v, int64_t hi) { return v < 0 ? 0 : v > hi ? int(hi) : v; }
+
+// ------------------------------------------------------------------ shared pieces
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+// Columns from c0 of four rows (one-row boxes); a row outside the tensor arrives as zeros.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int4 r)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+        : "memory");
+}
+
+// The waits' limit and where they report.
+struct Watch {
+    volatile int *abort_flag;
+    unsigned int *status;
+    uint64_t timeout_ns;
+    __device__ __forceinline__ void raise() const
+    {
+        *abort_flag = 1;
+        atomicOr(status, 1u);
+    }
+    template <bool CLUSTER = false> __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const
+    {
+        if (mbar_wait<CLUSTER>(bar, parity, abort_flag, timeout_ns)) return true;
+        raise();
+        return false;
+    }
+};
+
+// OR of `pred` over the four epilogue warps.
+__device__ __forceinline__ bool epilogue_any(bool pred)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(static_cast<uint32_t>(pred))
+                 : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ uint16_t to_16(float v, bool bf16)
+{
+    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+// Ring position of a role: stage and the parity its next phase completes.
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Barriers and the rest of shared memory.
+struct Shared {
+    uint32_t a, b, bar0;
+    uint8_t *epi;
+    volatile uint32_t *tmem_slot;
+    volatile int *abort_flag;
+    int *first, *start;
+    __device__ __forceinline__ explicit Shared(uint8_t *raw)
+    {
+        const uint32_t r = smem_u32(raw), base = (r + 1023u) & ~1023u;  // 128-byte swizzle atoms
+        uint8_t *p = raw + (base - r);
+        a = base;
+        b = base + kStages * kStageA;
+        epi = p + kStages * (kStageA + kStageB);
+        uint8_t *bars = epi + kEpiBytes;
+        bar0 = smem_u32(bars);
+        tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBarBytes - 16);
+        abort_flag = reinterpret_cast<volatile int *>(bars + kBarBytes - 8);
+        first = reinterpret_cast<int *>(bars + kBarBytes);
+        start = first + kMaxGroups + 2;
+    }
+    __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
+    __device__ __forceinline__ uint32_t acc_full(int i) const { return bar0 + 8u * (2 * kStages + i); }
+    __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + 2 + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4); }
+    __device__ __forceinline__ uint32_t ragged(int s) const { return bar0 + 8u * (2 * kStages + 5 + s); }
+};
+static_assert(8 * (3 * kStages + 5) <= kBarBytes - 16, "barrier area");
+
+// Barriers, the groups' first positions and first units, TMEM; ends with the pair in step.
+// units_of(rows): work units of a group of that many rows.
+template <class F>
+__device__ __forceinline__ uint32_t set_up(const Shared &sh, int full_arrivals, const int32_t *offsets, int groups,
+                                           int64_t positions, F units_of)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(sh.full(s), full_arrivals);
+            mbar_init(sh.empty(s), 1);  // the MMA issuer's commit
+            mbar_init(sh.ragged(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sh.acc_full(i), 1);
+            mbar_init(sh.acc_empty(i), 8);  // the epilogue warps of both CTAs
+        }
+        mbar_init(sh.drain(), 1);
+        *sh.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int g = threadIdx.x; g <= groups; g += blockDim.x)
+        sh.first[g] = offsets != nullptr ? clamp_to(__ldg(offsets + g), positions) : g == 0 ? 0 : int(positions);
+    cluster_sync();  // a pair allocates TMEM together, and its barriers exist before the peer uses them
+    if (warp == 1) tmem_alloc<true>(smem_u32(const_cast<uint32_t *>(sh.tmem_slot)), kTmemCols);
+    if (warp == 0) {
+        int carry = 0;
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int g = g0 + lane;
+            int n = g < groups ? units_of(max(0, sh.first[g + 1] - sh.first[g])) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kFull, n, o);
+                if (lane >= o) n += v;
+            }
+            if (g < groups) sh.start[g + 1] = carry + n;
+            carry += __shfl_sync(kFull, n, 31);
+        }
+        if (lane == 0) sh.start[0] = 0;
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    return *sh.tmem_slot;
+}
+
+__device__ __forceinline__ void tear_down(uint32_t tmem)
+{
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves or frees TMEM while the other may still use it
+    tc_fence_after();
+    if ((threadIdx.x >> 5) == 1) tmem_free<true>(tmem, kTmemCols);
+}
+
+// The end of a producer: after a failure its copies get time to land before the shared memory goes
+// away (they complete on the first CTA's barriers); otherwise it waits for the last release of every
+// slot, so that no commit is on its way to this CTA's barriers when it exits.
+__device__ __forceinline__ void finish_producer(const Shared &sh, const Watch &watch, Ring ring, bool ok)
+{
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+        return;
+    }
+    for (int i = 0; i < kStages; ++i) {
+        if (!watch.wait(sh.empty(ring.stage), ring.phase ^ 1u)) return;
+        ring.next();
+    }
+}
+
+// The end of an issuer that gave up: its MMAs in flight finish before TMEM is released.
+__device__ __forceinline__ void drain_issuer(const Shared &sh)
+{
+    umma_commit<true>(sh.drain());
+    const volatile int no_abort = 0;
+    mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
+}
+
+__device__ __forceinline__ void commit_both(uint32_t bar)
+{
+    umma_commit<true>(bar);
+    umma_commit<true>(map_to_rank(bar, 1));
+}
+
+// ------------------------------------------------------------------ Y = X op(W)
+constexpr int kThreads = 192;
+constexpr int kPlain = 0, kGated = 1, kAdapted = 2;
+
+struct LinearParams {
+    const int32_t *offsets;
+    int groups, shared_w;
+    int64_t y_rows, x_rows, N;
+    int ftiles, num_kb, cap;  // feature tiles of a group, K slices, tokens of a tile at most
+    const int32_t *rows;
+    void *Y;
+    int64_t ldy;
+    int y_f32, bf16;
+    void *pre;
+    int64_t ldp;
+    Adapters ad;
+    unsigned int *status;
+    uint64_t timeout_ns;
+    int inject_stall;  // test hook: the producer never fills its first slice
+};
+
+// A unit: one feature tile of one tile of a group's tokens.
+struct LinearUnit {
+    int group, feature_tile, first, tokens, width;
+};
+__device__ __forceinline__ LinearUnit linear_unit(const LinearParams &p, const Shared &sh, int u, int &group)
+{
+    while (u >= sh.start[group + 1]) ++group;
+    const int rows = sh.first[group + 1] - sh.first[group];
+    const int tiles = (rows + p.cap - 1) / p.cap;
+    const int width = ((rows + tiles - 1) / tiles + 31) & ~31;  // even tiles; at most cap, none is empty
+    const int r = u - sh.start[group], t = r / p.ftiles;
+    LinearUnit x;
+    x.group = group;
+    x.feature_tile = r - t * p.ftiles;
+    x.first = sh.first[group] + t * width;
+    x.tokens = min(width, rows - t * width);
+    x.width = (x.tokens + 31) & ~31;
+    return x;
+}
+
+// 32 tokens of this warp's 32 features (v: this lane's feature) to rows `first` .. of an array, as
+// 16-byte pieces.  `tile`: the warp's staging tile.
+__device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile, int lane, uint8_t *base, int64_t ld_bytes,
+                                             int first, int tokens, int64_t feature0, int64_t N, bool f32, bool bf16)
+{
+    __syncwarp();
+    if (f32) {
+        float *t = reinterpret_cast<float *>(tile);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i * 32 + lane] = v[i];
+    } else {
+        uint16_t *t = reinterpret_cast<uint16_t *>(tile);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i * 32 + lane] = to_16(v[i], bf16);
+    }
+    __syncwarp();
+    const int size = f32 ? 4 : 2, pieces = 2 * size;  // 16-byte pieces of 32 elements
+    const int per = 32 / pieces;                      // tokens of one pass of the warp
+    const int piece = lane % pieces;
+    const int64_t f = feature0 + piece * (16 / size);
+    for (int i = lane / pieces; i < tokens && i < 32; i += per) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(tile + (i * pieces + piece) * 16);
+        uint8_t *dst = base + int64_t(first + i) * ld_bytes + f * size;
+        if (f + 16 / size <= N) {
+            *reinterpret_cast<uint4 *>(dst) = q;
+        } else if (f < N) {
+            const uint16_t *e = reinterpret_cast<const uint16_t *>(&q);
+            for (int j = 0; j < int(N - f) * size / 2; ++j) reinterpret_cast<uint16_t *>(dst)[j] = e[j];
+        }
+    }
+}
+
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+
+// v[i] += inner[token i] . B[feature] of each token's adapter, 32 ranks at a time: the tokens' inner
+// products in the staging tile, this lane's row of B in registers until the adapter changes.
+__device__ __forceinline__ void add_adapters(float (&v)[32], const LinearParams &p, float *tile, int lane, int first,
+                                             int tokens, int64_t feature)
+{
+    const Adapters &ad = p.ad;
+    int mine = -1;
+    if (lane < tokens) mine = __ldcg(ad.which + first + lane);
+    if (unsigned(mine) >= unsigned(ad.count)) mine = -1;
+    if (__ballot_sync(kFull, mine >= 0) == 0u) return;
+    for (int r0 = 0; r0 < ad.rank; r0 += 32) {
+        __syncwarp();
+        const int r = r0 + lane;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+            const int a = __shfl_sync(kFull, mine, i);  // by all lanes, before any condition on the lane
+            const bool there = a >= 0 && r < ad.rank;
+            tile[i * 32 + lane] = there ? __ldcg(ad.inner + int64_t(first + i) * ad.rank + r) : 0.0f;
+        }
+        __syncwarp();
+        float b[32];
+        int now = -1;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int a = __shfl_sync(kFull, mine, i);
+            if (a < 0) continue;
+            if (a != now) {
+                now = a;
+                const uint16_t *row = static_cast<const uint16_t *>(ad.b) + int64_t(a) * ad.strideb + feature * ad.ldb;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                    const int j0 = r0 + 8 * c;
+                    if (feature < p.N) {
+                        if (j0 + 8 <= ad.rank) {
+                            q = __ldg(reinterpret_cast<const uint4 *>(row + j0));
+                        } else {
+                            uint16_t *e = reinterpret_cast<uint16_t *>(&q);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (j0 + j < ad.rank) e[j] = __ldg(row + j0 + j);
+                        }
+                    }
+                    const uint16_t *e = reinterpret_cast<const uint16_t *>(&q);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        b[8 * c + j] = p.bf16 ? __uint_as_float(uint32_t(e[j]) << 16) : __half2float(__ushort_as_half(e[j]));
+                }
+            }
+            const float4 *t = reinterpret_cast<const float4 *>(tile + i * 32);
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float4 x = t[q];
+                s0 = fmaf(b[4 * q], x.x, s0);
+                s1 = fmaf(b[4 * q + 1], x.y, s1);
+                s0 = fmaf(b[4 * q + 2], x.z, s0);
+                s1 = fmaf(b[4 * q + 3], x.w, s1);
+            }
+            v[i] += s0 + s1;
+        }
+    }
+}
+
+// W_MN: W stored K x N (features contiguous).
+template <int W_MN, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                      const LinearParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const Shared sh(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cap = p.cap, ftiles = p.ftiles;
+    const uint32_t tmem = set_up(sh, 1, p.offsets, p.groups, p.y_rows,
+                                 [=](int rows) { return (rows + cap - 1) / cap * ftiles; });
+    const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
+    const int units = sh.start[p.groups], unit0 = int(cluster_id_x()), step = int(cluster_count_x());
+    constexpr int kFeatures = EPI == kGated ? 128 : 256;  // of a unit
+
+    if (warp == 0) {
+        // ---------------- producer
+        Ring ring;
+        bool ok = true;
+        int group = 0;
+        if (lane == 0) {
+            tma_prefetch_desc(&map_w);
+            tma_prefetch_desc(&map_x);
+        }
+        for (int u = unit0; ok && u < units; u += step) {
+            const LinearUnit x = linear_unit(p, sh, u, group);
+            const int half = x.width / 2;                     // tokens this CTA loads
+            const int row0 = x.first + int(rank) * half, end = x.first + x.tokens;
+            const int f0 = x.feature_tile * kFeatures + int(rank) * (kFeatures / 2);
+            const int wg = p.shared_w ? 0 : x.group;
+            int4 from = make_int4(0, 0, 0, 0);
+            if (p.rows != nullptr && 4 * lane < half) {       // a row outside x is read as zeros
+                int r[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int q = row0 + 4 * lane + i;
+                    r[i] = q < end ? __ldg(p.rows + q) : -1;
+                    if (r[i] < 0 || r[i] >= p.x_rows) r[i] = int(p.x_rows);
+                }
+                from = make_int4(r[0], r[1], r[2], r[3]);
+            }
+            const uint32_t bytes = 2u * (kStageA + uint32_t(half) * 128u);
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                bool got = true;
+                if (lane == 0) got = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                if (__any_sync(kFull, !got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = map_to_rank(sh.full(ring.stage), 0);
+                if (lane == 0 && rank == 0) mbar_expect_tx(sh.full(ring.stage), bytes);
+                const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
+                const int k0 = kb * 64;
+                if (!(p.inject_stall && kb == 0 && u == unit0)) {
+                    if (lane == 0) {
+                        if (W_MN) {  // two boxes of 64 features x 64 k
+                            tma_load_3d_pair(a, &map_w, full, f0, k0, wg);
+                            tma_load_3d_pair(a + 8192, &map_w, full, f0 + 64, k0, wg);
+                        } else if (EPI == kGated) {  // 64 gate rows and their up rows
+                            tma_load_3d_pair(a, &map_w, full, k0, f0, wg);
+                            tma_load_3d_pair(a + 8192, &map_w, full, k0, int(p.N) + f0, wg);
+                        } else {
+                            tma_load_3d_pair(a, &map_w, full, k0, f0, wg);
+                        }
+                    }
+                    __syncwarp();
+                    if (p.rows != nullptr) {
+                        if (4 * lane < half) tma_gather4_pair(b + 512u * lane, &map_x, full, k0, from);
+                    } else if (16 * lane < half) {
+                        tma_load_2d_pair(b + 2048u * lane, &map_x, full, k0, row0 + 16 * lane);
+                    }
+                    __syncwarp();
+                }
+                ring.next();
+            }
+        }
+        if (lane == 0) finish_producer(sh, watch, ring, ok);
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer
+            const uint32_t fmt = p.bf16 ? (1u << 7) | (1u << 10) : 0u;
+            Ring ring;
+            int acc = 0, group = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int u = unit0; ok && u < units; u += step) {
+                const LinearUnit x = linear_unit(p, sh, u, group);
+                const uint32_t idesc = make_idesc(W_MN, 0, x.width, 256) | fmt;
+                ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + uint32_t(acc * kAccCols);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    ok = watch.wait(sh.full(ring.stage), ring.phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f16<true>(d, W_MN ? smem_desc(a + k * 2048, 8192, 1024) : smem_desc(a + k * 32, 16, 1024),
+                                       smem_desc(b + k * 32, 16, 1024), idesc, kb > 0 || k > 0 ? 1u : 0u);
+                    commit_both(sh.empty(ring.stage));
+                    ring.next();
+                }
+                if (!ok) break;
+                commit_both(sh.acc_full(acc));
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            if (!ok) drain_issuer(sh);
+        }
+    } else {
+        // ---------------- epilogue: TMEM lanes 32 * quarter .. of this CTA's 128 rows
+        const int quarter = warp & 3;
+        uint8_t *tile = sh.epi + quarter * 4096;
+        int acc = 0, group = 0;
+        uint32_t acc_phase = 0;
+        // the adapters' inner products come from the kernel ahead of this one
+        if (EPI == kAdapted) asm volatile("griddepcontrol.wait;" ::: "memory");
+        uint8_t *Y = static_cast<uint8_t *>(p.Y);
+        const int64_t ldy = p.ldy * (p.y_f32 ? 4 : 2);
+        for (int u = unit0; u < units; u += step) {
+            const LinearUnit x = linear_unit(p, sh, u, group);
+            const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
+            if (epilogue_any(!got)) {
+                watch.raise();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * kAccCols);
+            if (EPI == kGated) {
+                // quarters 0, 1 hold gate rows, 2, 3 the up rows of the same features; of two
+                // pieces of 32 tokens the gate's warp finishes the first, the up's warp the second
+                const bool up = quarter >= 2;
+                const int64_t f = int64_t(x.feature_tile) * 128 + int64_t(rank) * 64 + (quarter & 1) * 32;
+                float *own = reinterpret_cast<float *>(tile);
+                const float *other = reinterpret_cast<const float *>(sh.epi + (quarter ^ 2) * 4096);
+#pragma unroll 1
+                for (int c = 0; c < x.width; c += 64) {
+                    const bool two = c + 32 < x.width;
+                    float v0[32], v1[32];
+                    __syncwarp();
+                    tmem_ld_32(taddr + c, v0);
+                    if (two) tmem_ld_32(taddr + c + 32, v1);
+                    if (p.pre != nullptr) {
+                        uint8_t *pre = static_cast<uint8_t *>(p.pre) + (up ? p.N * 2 : 0);
+                        // N of the up half may end between two 16-byte pieces of pre: element by element then
+                        const int64_t n = f + 32 <= p.N && p.N % 8 == 0 ? p.N : -1;
+                        if (n > 0) {
+                            store_tokens(v0, tile, lane, pre, p.ldp * 2, x.first + c, x.tokens - c, f, n, false, p.bf16);
+                            if (two)
+                                store_tokens(v1, tile, lane, pre, p.ldp * 2, x.first + c + 32, x.tokens - c - 32, f, n, false, p.bf16);
+                        } else if (f + lane < p.N) {
+                            uint16_t *dst = reinterpret_cast<uint16_t *>(pre) + int64_t(x.first + c) * p.ldp + f + lane;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                if (c + i < x.tokens) dst[i * p.ldp] = to_16(v0[i], p.bf16);
+                                if (two && c + 32 + i < x.tokens) dst[(32 + i) * p.ldp] = to_16(v1[i], p.bf16);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (up) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) own[i * 32 + lane] = v0[i];
+                    } else if (two) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) own[i * 32 + lane] = v1[i];
+                    }
+                    asm volatile("bar.sync %0, 64;" ::"r"(2 + (quarter & 1)) : "memory");
+                    if (!up) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v0[i] = silu(v0[i]) * other[i * 32 + lane];
+                    } else if (two) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v0[i] = silu(other[i * 32 + lane]) * v1[i];
+                    }
+                    asm volatile("bar.sync %0, 64;" ::"r"(2 + (quarter & 1)) : "memory");
+                    const int at = up ? c + 32 : c;
+                    if (!up || two)
+                        store_tokens(v0, tile, lane, Y, ldy, x.first + at, x.tokens - at, f, p.N, p.y_f32, p.bf16);
+                }
+            } else {
+                const int64_t f = int64_t(x.feature_tile) * 256 + int64_t(rank) * 128 + quarter * 32;
+#pragma unroll 1
+                for (int c = 0; c < x.width; c += 32) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld_32(taddr + c, v);
+                    if (EPI == kAdapted)
+                        add_adapters(v, p, reinterpret_cast<float *>(tile), lane, x.first + c, min(32, x.tokens - c), f + lane);
+                    store_tokens(v, tile, lane, Y, ldy, x.first + c, x.tokens - c, f, p.N, p.y_f32, p.bf16);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(sh.acc_empty(acc), 0));
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    }
+    tear_down(tmem);
+}
+
+// ------------------------------------------------------------------ dW = dY^T X
+constexpr int kGradThreads = 224;  // warp 6 is the cleaner
+
+struct GradParams {
+    const int32_t *offsets;
+    int groups;
+    int64_t positions, N, K;
+    int ntiles, ktiles;
+    void *dW;
+    int64_t lddw, stridedw;
+    int dw_f32, bf16;
+    unsigned int *status;
+    uint64_t timeout_ns;
+    int inject_stall;
+};
+
+struct GradUnit {
+    int group, tn, tk, first, rows;
+};
+__device__ __forceinline__ GradUnit grad_unit(const GradParams &p, const Shared &sh, int u)
+{
+    // every group has the same number of units
+    const int per = p.ntiles * p.ktiles, g = u / per, r = u - g * per;
+    return GradUnit{g, r / p.ktiles, r % p.ktiles, sh.first[g], max(0, sh.first[g + 1] - sh.first[g])};
+}
+
+// A pair's tile is 256 (n) x 256 (k): each CTA holds 128 columns of dY and 128 of X as two boxes of
+// 64 columns x 64 positions each.  A slice is complete when both CTAs have said so on the first CTA's
+// full barrier: the producer for a whole slice, the cleaner for a group's last one.
+__global__ void __launch_bounds__(kGradThreads, 1)
+grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const GradParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const Shared sh(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const uint32_t tmem = set_up(sh, 2, p.offsets, p.groups, p.positions, [](int) { return 0; });
+    const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
+    const int units = p.groups * p.ntiles * p.ktiles, unit0 = int(cluster_id_x()), step = int(cluster_count_x());
+    constexpr uint32_t kSliceBytes = kStageA + kStageB;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer
+            Ring ring;
+            bool ok = true;
+            tma_prefetch_desc(&map_dy);
+            tma_prefetch_desc(&map_x);
+            for (int u = unit0; ok && u < units; u += step) {
+                const GradUnit x = grad_unit(p, sh, u);
+                const int n0 = x.tn * 256 + int(rank) * 128, k0 = x.tk * 256 + int(rank) * 128;
+                for (int s = 0; s < x.rows; s += 64) {
+                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                    if (!ok) break;
+                    const bool ragged = x.rows - s < 64;
+                    uint32_t bar;
+                    if (ragged) {  // lands on this CTA's own barrier, for its cleaner
+                        mbar_expect_tx(sh.ragged(ring.stage), kSliceBytes);
+                        bar = map_to_rank(sh.ragged(ring.stage), rank);
+                    } else {
+                        bar = map_to_rank(sh.full(ring.stage), 0);
+                        if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2 * kSliceBytes);
+                        else mbar_arrive_cluster(bar);
+                    }
+                    if (!(p.inject_stall && s == 0 && u == unit0)) {
+                        const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
+                        tma_load_2d_pair(a, &map_dy, bar, n0, x.first + s);
+                        tma_load_2d_pair(a + 8192, &map_dy, bar, n0 + 64, x.first + s);
+                        tma_load_2d_pair(b, &map_x, bar, k0, x.first + s);
+                        tma_load_2d_pair(b + 8192, &map_x, bar, k0 + 64, x.first + s);
+                    }
+                    ring.next();
+                }
+            }
+            finish_producer(sh, watch, ring, ok);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer
+            const uint32_t idesc = make_idesc(1, 1, 256, 256) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u);
+            Ring ring;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int u = unit0; ok && u < units; u += step) {
+                const GradUnit x = grad_unit(p, sh, u);
+                if (x.rows == 0) continue;  // the epilogue writes zeros by itself
+                ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + uint32_t(acc * kAccCols);
+                for (int s = 0; s < x.rows; s += 64) {
+                    ok = watch.wait<true>(sh.full(ring.stage), ring.phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
+                    const int steps = min(4, (x.rows - s + 15) / 16);  // 16 positions an MMA
+                    for (int k = 0; k < steps; ++k)
+                        umma_f16<true>(d, smem_desc(a + k * 2048, 8192, 1024), smem_desc(b + k * 2048, 8192, 1024), idesc,
+                                       s > 0 || k > 0 ? 1u : 0u);
+                    commit_both(sh.empty(ring.stage));
+                    ring.next();
+                }
+                if (!ok) break;
+                commit_both(sh.acc_full(acc));
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            if (!ok) drain_issuer(sh);
+        }
+    } else if (warp == 6) {
+        // ---------------- cleaner: zeros for the positions behind the group's last, up to the MMA's
+        // granularity of 16
+        Ring ring;
+        uint32_t parity = 0;  // of each stage's ragged barrier, one bit a stage
+        bool ok = true;
+        for (int u = unit0; ok && u < units; u += step) {
+            const GradUnit x = grad_unit(p, sh, u);
+            for (int s = 0; s < x.rows; s += 64) {
+                const int left = x.rows - s;
+                if (left < 64) {
+                    bool got = true;
+                    if (lane == 0) got = watch.wait(sh.ragged(ring.stage), (parity >> ring.stage) & 1u);
+                    if (__any_sync(kFull, !got)) {
+                        ok = false;
+                        break;
+                    }
+                    parity ^= 1u << ring.stage;
+                    const int end = (left + 15) & ~15, pieces = (end - left) * 8;  // 16-byte pieces of a box
+                    const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
+                    for (int i = lane; i < 4 * pieces; i += 32) {
+                        const int box = i / pieces;
+                        const uint32_t at = (box < 2 ? a : b) + (box & 1) * 8192u + uint32_t(left) * 128u +
+                                            uint32_t(i - box * pieces) * 16u;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(sh.full(ring.stage), 0));
+                }
+                ring.next();
+            }
+        }
+    } else {
+        // ---------------- epilogue: TMEM lane = row of dW; 32 x 32 pieces pass through the staging
+        // tile (16-byte pieces, XOR-swizzled by row) so that stores are 128- or 64-byte row segments
+        const int quarter = warp & 3;
+        float4 *tile = reinterpret_cast<float4 *>(sh.epi + quarter * 4096);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int u = unit0; u < units; u += step) {
+            const GradUnit x = grad_unit(p, sh, u);
+            if (x.rows > 0) {
+                const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
+                if (epilogue_any(!got)) {
+                    watch.raise();
+                    break;
+                }
+                tc_fence_after();
+            }
+            const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * kAccCols);
+            const int64_t n0 = int64_t(x.tn) * 256 + int64_t(rank) * 128 + quarter * 32;
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+                const int64_t k0 = int64_t(x.tk) * 256 + c;
+                float v[32];
+                __syncwarp();
+                if (x.rows > 0) {
+                    tmem_ld_32(taddr + c, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                }
+                if (k0 >= p.K || n0 >= p.N) continue;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    tile[lane * 8 + (j ^ (lane & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                __syncwarp();
+                const int q = lane & 7;
+                const int64_t k = k0 + 4 * q;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    const float4 o = tile[r * 8 + (q ^ (r & 7))];
+                    if (n0 + r >= p.N || k >= p.K) continue;
+                    const int64_t at = int64_t(x.group) * p.stridedw + (n0 + r) * p.lddw + k;
+                    if (p.dw_f32) {
+                        float *dst = static_cast<float *>(p.dW) + at;
+                        if (k + 4 <= p.K) {
+                            *reinterpret_cast<float4 *>(dst) = o;
+                        } else {
+                            const float e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (k + j < p.K) dst[j] = e[j];
+                        }
+                    } else {
+                        uint16_t *dst = static_cast<uint16_t *>(p.dW) + at;
+                        const uint16_t e[4] = {to_16(o.x, p.bf16), to_16(o.y, p.bf16), to_16(o.z, p.bf16), to_16(o.w, p.bf16)};
+                        if (k + 4 <= p.K) {
+                            *reinterpret_cast<uint2 *>(dst) = make_uint2(uint32_t(e[0]) | uint32_t(e[1]) << 16,
+                                                                         uint32_t(e[2]) | uint32_t(e[3]) << 16);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (k + j < p.K) dst[j] = e[j];
+                        }
+                    }
+                }
+            }
+            if (x.rows == 0) continue;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(sh.acc_empty(acc), 0));
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    }
+    tear_down(tmem);
+}
+
+// ------------------------------------------------------------------ host side
+// Row-major 16-bit matrices (a stack of `count`, `stride` elements apart; count 0: one matrix, 2-D
+// map), read in boxes of 64 columns x box_rows with the 128-byte swizzle.
+bool make_map(CUtensorMap *map, const void *ptr, bool bf16, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+              int64_t count, int64_t stride)
+{
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint32_t rank = count > 0 ? 3 : 2;
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(count)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(ptr),
+              dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Two-CTA clusters of `kernel` that can be resident at once; 0 on failure.  `cache`: of this kernel.
+template <class K> int resident_pairs(K *kernel, int threads, int dev, std::atomic<int> (&cache)[64])
+{
+    const int known = cache[dev & 63].load(std::memory_order_acquire);
+    if (known > 0) return known;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cache[dev & 63].store(n, std::memory_order_release);
+    return n;
+}
+
+template <class K, class P>
+cudaError_t launch_pairs(K *kernel, int threads, int64_t pairs, bool after, cudaStream_t stream, const CUtensorMap &a,
+                         const CUtensorMap &b, const P &p)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(2 * pairs));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, b, p);
+    if (e == cudaSuccess) count_launches();
+    return e;
+}
+
+// GEMM_GB300_TEST_INJECT_STALL: a producer never fills its first slice, and waits are short.
+void test_hooks(uint64_t &timeout_ns, int &inject_stall)
+{
+    timeout_ns = 2000000000ull;
+    inject_stall = 0;
+    if (const char *e = std::getenv("GEMM_GB300_TEST_INJECT_STALL"); e && e[0] == '1') {
+        inject_stall = 1;
+        timeout_ns = 20000000ull;
+    }
+}
+
+// Tokens of a tile: the multiple of 32 for which the group's tiles take the least time.  A K slice
+// of a tile costs its MMAs (2 cycles a token) or its loads, and the tiles run in waves of all pairs.
+int tile_cap(const GroupedArgs &a, int64_t ftiles, int pairs)
+{
+    const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;
+    const int64_t mean = (a.y_rows + groups - 1) / groups;
+    int best = 256;
+    double least = 1e300;
+    for (int cap = 256; cap >= 32; cap -= 32) {
+        const int64_t tiles = (mean + cap - 1) / cap;
+        const int64_t width = ((mean + tiles - 1) / tiles + 31) / 32 * 32;
+        const int64_t waves = (groups * tiles * ftiles + pairs - 1) / pairs;
+        const double slice = width > 128 ? 2.0 * double(width) : 256.0;
+        const double cost = double(waves) * slice;
+        if (cost < 0.98 * least) {
+            least = cost;
+            best = cap;
+        }
+    }
+    return best;
+}
+
+template <int W_MN, int EPI>
+cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+{
+    static std::atomic<int> cache[64];
+    auto *kernel = grouped_linear_kernel<W_MN, EPI>;
+    const int pairs = resident_pairs(kernel, kThreads, dev.device, cache);
+    unsigned int *status = device_status_word(dev.device);
+    if (pairs <= 0 || status == nullptr) return cudaErrorInitializationError;
+    const bool bf16 = a.type == GEMM_TYPE_BF16;
+    const int64_t w_rows = a.opW == GEMM_OP_T ? (a.gated ? 2 * a.N : a.N) : a.K;
+    const int64_t w_cols = a.opW == GEMM_OP_T ? a.K : a.N;
+    const bool shared_w = a.groups == 1 || a.stridew == 0;
+    CUtensorMap mw, mx;
+    std::memset(&mw, 0, sizeof(mw));
+    std::memset(&mx, 0, sizeof(mx));
+    if (!make_map(&mw, a.W, bf16, w_rows, w_cols, a.ldw, W_MN || EPI == kGated ? 64 : 128, shared_w ? 1 : a.groups,
+                  shared_w ? w_rows * a.ldw : a.stridew) ||
+        !make_map(&mx, a.X, bf16, a.x_rows, a.K, a.ldx, a.rows != nullptr ? 1 : 16, 0, 0))
+        return cudaErrorInvalidValue;
+    const int features = EPI == kGated ? 128 : 256;
+    LinearParams p{};
+    p.offsets = a.offsets;
+    p.groups = a.groups;
+    p.shared_w = shared_w;
+    p.y_rows = a.y_rows;
+    p.x_rows = a.x_rows;
+    p.N = a.N;
+    p.ftiles = int((a.N + features - 1) / features);
+    p.num_kb = int((a.K + 63) / 64);
+    p.cap = tile_cap(a, p.ftiles, pairs);
+    p.rows = a.rows;
+    p.Y = a.Y;
+    p.ldy = a.ldy;
+    p.y_f32 = a.y_type == GEMM_TYPE_F32;
+    p.bf16 = bf16;
+    p.pre = a.pre;
+    p.ldp = a.ldp;
+    p.ad = a.ad;
+    p.status = status;
+    test_hooks(p.timeout_ns, p.inject_stall);
+    // no more pairs than there can be units
+    const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles;
+    return launch_pairs(kernel, kThreads, most < pairs ? most : pairs, EPI == kAdapted, stream, mw, mx, p);
+}
+
+}  // namespace
+
+cudaError_t launch_many_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+{
+    if (dev.smem_optin < size_t(kSmemBytes)) return cudaErrorInvalidDevice;
+    if (a.opW == GEMM_OP_N) return launch_linear<1, kPlain>(dev, a, stream);
+    if (a.gated) return launch_linear<0, kGated>(dev, a, stream);
+    if (a.ad.b != nullptr) return launch_linear<0, kAdapted>(dev, a, stream);
+    return launch_linear<0, kPlain>(dev, a, stream);
+}
+
+cudaError_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, cudaStream_t stream)
+{
+    static std::atomic<int> cache[64];
+    if (dev.smem_optin < size_t(kSmemBytes)) return cudaErrorInvalidDevice;
+    const int pairs = resident_pairs(grouped_grad_kernel, kGradThreads, dev.device, cache);
+    unsigned int *status = device_status_word(dev.device);
+    if (pairs <= 0 || status == nullptr) return cudaErrorInitializationError;
+    const bool bf16 = a.type == GEMM_TYPE_BF16;
+    CUtensorMap md, mx;
+    std::memset(&md, 0, sizeof(md));
+    std::memset(&mx, 0, sizeof(mx));
+    // without positions no copy is made: the maps stay empty
+    if (a.positions > 0 && (!make_map(&md, a.dY, bf16, a.positions, a.N, a.lddy, 64, 0, 0) ||
+                            !make_map(&mx, a.X, bf16, a.positions, a.K, a.ldx, 64, 0, 0)))
+        return cudaErrorInvalidValue;
+    GradParams p{};
+    p.offsets = a.offsets;
+    p.groups = a.groups;
+    p.positions = a.positions;
+    p.N = a.N;
+    p.K = a.K;
+    p.ntiles = int((a.N + 255) / 256);
+    p.ktiles = int((a.K + 255) / 256);
+    p.dW = a.dW;
+    p.lddw = a.lddw;
+    p.stridedw = a.stridedw;
+    p.dw_f32 = a.dw_type == GEMM_TYPE_F32;
+    p.bf16 = bf16;
+    p.status = status;
+    test_hooks(p.timeout_ns, p.inject_stall);
+    const int64_t units = int64_t(a.groups) * p.ntiles * p.ktiles;
+    if (units >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    return launch_pairs(grouped_grad_kernel, kGradThreads, units < pairs ? units : pairs, false, stream, md, mx, p);
+}
+
+}  // namespace gemm

@@ -249,7 +249,7 @@ gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw_type, in
     const gemm_status_t s = usable(dev);
     if (s != GEMM_OK) return s;
     const WeightGradArgs a{type, dw_type, int(groups), offsets, N, K, dY, lddy, X, ldx, positions, dW, lddw, strideDW};
-    return launch_weight_grad(dev, a, static_cast<cudaStream_t>(stream));
+    return from_cuda(launch_weight_grad(dev, a, static_cast<cudaStream_t>(stream)));
 }
 
 gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, int64_t N, int64_t K, const void *X,

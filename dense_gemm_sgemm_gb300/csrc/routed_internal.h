@@ -108,6 +108,8 @@ struct GroupedArgs {
 // Few rows per group (opW = T): weights straight from global memory to mma.sync fragments.
 cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 
+// Many rows per group, or opW = N: tcgen05 tiles fed by TMA.
+cudaError_t launch_many_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 
 struct WeightGradArgs {
@@ -122,7 +124,7 @@ struct WeightGradArgs {
     void *dW;
     int64_t lddw, stridedw;
 };
-gemm_status_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, cudaStream_t stream);
+cudaError_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, cudaStream_t stream);
 
 struct ShrinkArgs {
     int type;
