@@ -1,17 +1,62 @@
 // Grouped products: which kernel takes which call.
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdlib>
+
 #include "routed_internal.h"
 
 namespace gemm {
 
-gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+cudaError_t allow_smem_once(const void *kernel, int bytes)
 {
+    // Open addressing over a fixed table (a few dozen kernels): no allocation, so no exception.
+    constexpr int kSlots = 1024;
+    static std::atomic<uintptr_t> done[kSlots];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // kernels are distinct host functions: their addresses differ by more than the device number
+    const uintptr_t key = reinterpret_cast<uintptr_t>(kernel) * 64 + uintptr_t(dev & 63);
+    for (int i = 0; i < kSlots; ++i) {
+        std::atomic<uintptr_t> &slot = done[(key / 64 + key + uintptr_t(i)) % kSlots];
+        uintptr_t held = slot.load(std::memory_order_acquire);
+        if (held == key) return cudaSuccess;
+        if (held != 0) continue;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        slot.compare_exchange_strong(held, key, std::memory_order_acq_rel);
+        return cudaSuccess;
+    }
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &call, cudaStream_t stream)
+{
+    GroupedArgs a = call;
     const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;  // at most that many have rows
-    const bool few = a.opW == GEMM_OP_T && a.y_rows <= 16 * groups;
-    cudaError_t e;
-    if (few || a.K == 0 || a.x_rows == 0) e = launch_few_rows(dev, a, stream);
-    else e = launch_many_rows(dev, a, stream);
+    // GEMM_GB300_GROUPED_FEW=n (sweeps only): the few-rows kernel up to n rows a group
+    int64_t limit = 16;
+    if (const char *v = std::getenv("GEMM_GB300_GROUPED_FEW"); v && v[0]) limit = std::atoi(v);
+    const bool few = a.opW == GEMM_OP_T && a.y_rows <= limit * groups;
+    cudaError_t e = cudaSuccess;
+    if (few || a.K == 0 || a.x_rows == 0) {
+        e = launch_few_rows(dev, a, stream);
+    } else {
+        // Gathered rows: TMA takes 82 cycles for four of them, as long as the MMAs of a slice of 160
+        // tokens, where a box of 128 contiguous rows costs next to nothing.  So large groups pay for
+        // laying the rows out first (64 groups of 512 rows, 2 x 1024 x 2048 gated: gathered 617 us,
+        // contiguous 206 us and the copy), small ones gather.
+        if (a.rows != nullptr && a.work != nullptr && a.y_rows > 64 * groups) {
+            const int64_t ld = (a.K + 7) / 8 * 8;
+            e = launch_gather(a, a.work, ld, stream);
+            a.X = a.work;
+            a.ldx = ld;
+            a.x_rows = a.y_rows;
+            a.rows = nullptr;
+        }
+        if (e == cudaSuccess) e = launch_many_rows(dev, a, stream);
+    }
     if (e != cudaSuccess) cudaGetLastError();
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }

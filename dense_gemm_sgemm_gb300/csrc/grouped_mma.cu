@@ -323,13 +323,6 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     }
 }
 
-template <class K> cudaError_t allow_smem(K *kernel, size_t bytes)
-{
-    return bytes > 48 * 1024
-               ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes))
-               : cudaSuccess;
-}
-
 // Launch; `after`: the launch may begin before the one ahead of it on the stream has ended.
 template <class K, class... Args>
 cudaError_t launch_after(K *kernel, dim3 grid, size_t smem, cudaStream_t stream, bool after, Args... args)
@@ -360,7 +353,7 @@ cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, int64_t
     const int64_t per = kWarps / ks;
     const size_t smem = size_t(kWarps) * 8 * NT * kRowStride * sizeof(float);
     auto *kernel = few_rows_kernel<T, Y, NT, GATED>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned((runs + per - 1) / per), unsigned(groups), unsigned(depth));
     return launch_after(kernel, grid, smem, stream, a.ad.b != nullptr, a, ks);
@@ -388,7 +381,7 @@ template <class T, int MT, int NT> cudaError_t launch_shrink_t(const ShrinkArgs 
     constexpr int kStride = MT <= 2 ? kRowStride : 68;
     const size_t smem = size_t(kWarps) * 8 * NT * kStride * sizeof(float);
     auto *kernel = shrink_kernel<T, MT, NT>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned(a.T / (8 * NT) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
     return launch_after(kernel, grid, smem, stream, false, a);

@@ -6,10 +6,11 @@
 // features take the MMA's m side, where tiles are fixed, and the tokens its n side, which is any
 // multiple of 32 up to 256: D[feature][token] = W_g X^T.  Two CTAs on neighbouring SMs form a 256 x n
 // tile (tcgen05.mma.cta_group::2; each loads its own 128 weight rows and half of the tokens).  Warps:
-//   0     TMA producer: per 64-wide K slice the weight boxes and the token rows, contiguous rows in
-//         boxes of 16, gathered rows four at a time (tile::gather4) by all lanes;
+//   0     TMA producer of the weights, per 64-wide K slice;
+//   10    TMA producer of the token rows: contiguous rows in boxes of 128, 64, 32 and 16, gathered
+//         rows four at a time (tile::gather4) by all lanes;
 //   1     MMA issuer (of the pair's first CTA) and TMEM owner, two 256-column accumulators;
-//   2-5   epilogue: one TMEM lane is one feature, so 32 tokens x 32 features pass through shared
+//   2-9   epilogue: one TMEM lane is one feature, so 32 tokens x 32 features pass through shared
 //         memory per warp and leave as 16-byte pieces of token rows.
 // gated: a CTA's 128 rows are 64 gate rows and their 64 up rows; the warps that hold a gate and its
 // up exchange halves through shared memory.  Adapters: the epilogue adds inner[token] . B[feature]
@@ -36,15 +37,17 @@
 namespace gemm {
 namespace {
 
-constexpr int kStages = 6;
-constexpr int kStageA = 128 * 128;  // bytes: 128 weight rows (or 64 k rows x 2 boxes) of 128 bytes
-constexpr int kStageB = 128 * 128;  // bytes: up to 128 token rows
-constexpr int kEpiBytes = 4 * 32 * 32 * 4;  // a 32 x 32 fp32 staging tile per epilogue warp
-constexpr int kBarBytes = 256;
+constexpr int kStageA = 128 * 128;     // bytes: 128 weight rows (or 64 k rows x 2 boxes) of 128 bytes
+constexpr int kMaxStageB = 128 * 128;  // bytes: up to 128 token rows
+constexpr int kRingBytes = 5 * (kStageA + kMaxStageB);
+constexpr int kMaxStages = 9;  // of the smallest stage: 16 token rows, 18 KB
+constexpr int kEpiWarps = 8;  // two for every 32 TMEM lanes, taking the columns in turn
+constexpr int kEpiBytes = kEpiWarps * 32 * 32 * 4;  // a 32 x 32 fp32 staging tile each
+constexpr int kBarBytes = 512;
 constexpr int kTmemCols = 512, kAccCols = 256;
 constexpr int kMaxGroups = 1024;
 constexpr int kTableBytes = 2 * (kMaxGroups + 2) * 4;  // first position and first unit of every group
-constexpr int kSmemBytes = kStages * (kStageA + kStageB) + kEpiBytes + kBarBytes + kTableBytes + 1024;
+constexpr int kSmemBytes = kRingBytes + kEpiBytes + kBarBytes + kTableBytes + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -87,14 +90,14 @@ struct Watch {
     }
 };
 
-// OR of `pred` over the four epilogue warps.
+// OR of `pred` over the epilogue warps.
 __device__ __forceinline__ bool epilogue_any(bool pred)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\t"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
                  "selp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(static_cast<uint32_t>(pred))
+                 : "r"(static_cast<uint32_t>(pred)), "n"(32 * kEpiWarps)
                  : "memory");
     return r != 0;
 }
@@ -104,13 +107,26 @@ __device__ __forceinline__ uint16_t to_16(float v, bool bf16)
     return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
+__device__ __forceinline__ uint32_t pack_16(float lo, float hi, bool bf16)
+{
+    return uint32_t(to_16(lo, bf16)) | uint32_t(to_16(hi, bf16)) << 16;
+}
+
+// The ring: as many stages of kStageA + b_bytes as fit.  A slice takes about 1.5 us from its copies'
+// issue to its release, so the bytes in flight are what small tiles are short of.
+__host__ __device__ constexpr int ring_stages(int b_bytes)
+{
+    return kRingBytes / (kStageA + b_bytes) < kMaxStages ? kRingBytes / (kStageA + b_bytes) : kMaxStages;
+}
+
 // Ring position of a role: stage and the parity its next phase completes.
 struct Ring {
-    int stage = 0;
+    int stages, stage = 0;
     uint32_t phase = 0;
+    __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
     __device__ __forceinline__ void next()
     {
-        if (++stage == kStages) {
+        if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -124,13 +140,15 @@ struct Shared {
     volatile uint32_t *tmem_slot;
     volatile int *abort_flag;
     int *first, *start;
-    __device__ __forceinline__ explicit Shared(uint8_t *raw)
+    int stages, b_bytes;
+    __device__ __forceinline__ Shared(uint8_t *raw, int stage_b_bytes)
+        : stages(ring_stages(stage_b_bytes)), b_bytes(stage_b_bytes)
     {
         const uint32_t r = smem_u32(raw), base = (r + 1023u) & ~1023u;  // 128-byte swizzle atoms
         uint8_t *p = raw + (base - r);
         a = base;
-        b = base + kStages * kStageA;
-        epi = p + kStages * (kStageA + kStageB);
+        b = base + stages * kStageA;
+        epi = p + kRingBytes;
         uint8_t *bars = epi + kEpiBytes;
         bar0 = smem_u32(bars);
         tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBarBytes - 16);
@@ -139,30 +157,34 @@ struct Shared {
         start = first + kMaxGroups + 2;
     }
     __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
-    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
-    __device__ __forceinline__ uint32_t acc_full(int i) const { return bar0 + 8u * (2 * kStages + i); }
-    __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + 2 + i); }
-    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4); }
-    __device__ __forceinline__ uint32_t ragged(int s) const { return bar0 + 8u * (2 * kStages + 5 + s); }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kMaxStages + s); }
+    __device__ __forceinline__ uint32_t ragged(int s) const { return bar0 + 8u * (2 * kMaxStages + s); }
+    __device__ __forceinline__ uint32_t cleaned(int s) const { return bar0 + 8u * (3 * kMaxStages + s); }
+    __device__ __forceinline__ uint32_t acc_full(int i) const { return bar0 + 8u * (4 * kMaxStages + i); }
+    __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (4 * kMaxStages + 2 + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (4 * kMaxStages + 4); }
+    __device__ __forceinline__ uint32_t stage_a(int s) const { return a + uint32_t(s * kStageA); }
+    __device__ __forceinline__ uint32_t stage_b(int s) const { return b + uint32_t(s * b_bytes); }
 };
-static_assert(8 * (3 * kStages + 5) <= kBarBytes - 16, "barrier area");
+static_assert(8 * (4 * kMaxStages + 5) <= kBarBytes - 16, "barrier area");
 
 // Barriers, the groups' first positions and first units, TMEM; ends with the pair in step.
 // units_of(rows): work units of a group of that many rows.
 template <class F>
-__device__ __forceinline__ uint32_t set_up(const Shared &sh, int full_arrivals, const int32_t *offsets, int groups,
-                                           int64_t positions, F units_of)
+__device__ __forceinline__ uint32_t set_up(const Shared &sh, const int32_t *offsets, int groups, int64_t positions,
+                                           F units_of)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(sh.full(s), full_arrivals);
+        for (int s = 0; s < sh.stages; ++s) {
+            mbar_init(sh.full(s), 1);
             mbar_init(sh.empty(s), 1);  // the MMA issuer's commit
             mbar_init(sh.ragged(s), 1);
+            mbar_init(sh.cleaned(s), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sh.acc_full(i), 1);
-            mbar_init(sh.acc_empty(i), 8);  // the epilogue warps of both CTAs
+            mbar_init(sh.acc_empty(i), 2 * kEpiWarps);  // the epilogue warps of both CTAs
         }
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
@@ -214,7 +236,7 @@ __device__ __forceinline__ void finish_producer(const Shared &sh, const Watch &w
         }
         return;
     }
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < sh.stages; ++i) {
         if (!watch.wait(sh.empty(ring.stage), ring.phase ^ 1u)) return;
         ring.next();
     }
@@ -228,15 +250,31 @@ __device__ __forceinline__ void drain_issuer(const Shared &sh)
     mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
 }
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Arrives on the barrier at this address in both CTAs of the pair once the MMAs issued so far have
+// completed.
 __device__ __forceinline__ void commit_both(uint32_t bar)
 {
-    umma_commit<true>(bar);
-    umma_commit<true>(map_to_rank(bar, 1));
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(uint16_t(3))
+                 : "memory");
 }
 
 // ------------------------------------------------------------------ Y = X op(W)
-constexpr int kThreads = 192;
+constexpr int kTokenWarp = 2 + kEpiWarps;
+constexpr int kThreads = 32 * (kTokenWarp + 1);
 constexpr int kPlain = 0, kGated = 1, kAdapted = 2;
+
+// The token rows as boxes of 128, 64, 32 and 16 rows; gathered: rows[0] has one-row boxes.
+struct TokenMaps {
+    CUtensorMap rows[4];
+};
 
 struct LinearParams {
     const int32_t *offsets;
@@ -246,7 +284,7 @@ struct LinearParams {
     const int32_t *rows;
     void *Y;
     int64_t ldy;
-    int y_f32, bf16;
+    int bf16;
     void *pre;
     int64_t ldp;
     Adapters ad;
@@ -276,12 +314,15 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearParams &p, const S
 }
 
 // 32 tokens of this warp's 32 features (v: this lane's feature) to rows `first` .. of an array, as
-// 16-byte pieces.  `tile`: the warp's staging tile.
+// 16-byte pieces: all pieces are read from the staging tile before the first is stored.
+template <bool F32>
 __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile, int lane, uint8_t *base, int64_t ld_bytes,
-                                             int first, int tokens, int64_t feature0, int64_t N, bool f32, bool bf16)
+                                             int first, int tokens, int64_t feature0, int64_t N, bool bf16)
 {
+    constexpr int kSize = F32 ? 4 : 2, kPieces = 2 * kSize;  // 16-byte pieces of 32 features
+    constexpr int kPasses = kPieces;                         // 32 / kPieces tokens a pass
     __syncwarp();
-    if (f32) {
+    if (F32) {
         float *t = reinterpret_cast<float *>(tile);
 #pragma unroll
         for (int i = 0; i < 32; ++i) t[i * 32 + lane] = v[i];
@@ -291,26 +332,81 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile
         for (int i = 0; i < 32; ++i) t[i * 32 + lane] = to_16(v[i], bf16);
     }
     __syncwarp();
-    const int size = f32 ? 4 : 2, pieces = 2 * size;  // 16-byte pieces of 32 elements
-    const int per = 32 / pieces;                      // tokens of one pass of the warp
-    const int piece = lane % pieces;
-    const int64_t f = feature0 + piece * (16 / size);
-    for (int i = lane / pieces; i < tokens && i < 32; i += per) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(tile + (i * pieces + piece) * 16);
-        uint8_t *dst = base + int64_t(first + i) * ld_bytes + f * size;
-        if (f + 16 / size <= N) {
-            *reinterpret_cast<uint4 *>(dst) = q;
-        } else if (f < N) {
-            const uint16_t *e = reinterpret_cast<const uint16_t *>(&q);
-            for (int j = 0; j < int(N - f) * size / 2; ++j) reinterpret_cast<uint16_t *>(dst)[j] = e[j];
+    const int piece = lane % kPieces, i0 = lane / kPieces;
+    uint4 q[kPasses];
+#pragma unroll
+    for (int j = 0; j < kPasses; ++j)
+        q[j] = *reinterpret_cast<const uint4 *>(tile + (j * 32 + lane) * 16);
+    const int64_t f = feature0 + piece * (16 / kSize);
+    uint8_t *dst = base + int64_t(first + i0) * ld_bytes + f * kSize;
+    if (f + 16 / kSize <= N) {
+#pragma unroll
+        for (int j = 0; j < kPasses; ++j, dst += (32 / kPieces) * ld_bytes)
+            if (i0 + j * (32 / kPieces) < tokens) *reinterpret_cast<uint4 *>(dst) = q[j];
+    } else if (f < N) {
+#pragma unroll 1
+        for (int j = 0; j < kPasses; ++j, dst += (32 / kPieces) * ld_bytes) {
+            if (i0 + j * (32 / kPieces) >= tokens) break;
+            const uint16_t *e = reinterpret_cast<const uint16_t *>(tile + (j * 32 + lane) * 16);
+            for (int c = 0; c < int(N - f) * kSize / 2; ++c) reinterpret_cast<uint16_t *>(dst)[c] = e[c];
         }
     }
 }
 
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
+// Two fp32 multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(float2 &c, float2 a, float2 b)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<uint64_t &>(c))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+}
+
+// Ranks [r0, r0 + 32) of this lane's row of an adapter's B, zeros past the last rank.
+__device__ __forceinline__ void adapter_row(const LinearParams &p, int a, int64_t feature, int r0, float2 (&b)[16])
+{
+    const Adapters &ad = p.ad;
+    const uint16_t *row = static_cast<const uint16_t *>(ad.b) + int64_t(a) * ad.strideb + feature * ad.ldb;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        const int j0 = r0 + 8 * c;
+        if (feature < p.N) {
+            if (j0 + 8 <= ad.rank) {
+                q = __ldg(reinterpret_cast<const uint4 *>(row + j0));
+            } else {
+                uint16_t *e = reinterpret_cast<uint16_t *>(&q);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j0 + j < ad.rank) e[j] = __ldg(row + j0 + j);
+            }
+        }
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            b[4 * c + j] = p.bf16 ? make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u))
+                                  : __half22float2(reinterpret_cast<const __half2 &>(w[j]));
+    }
+}
+
+__device__ __forceinline__ float adapter_dot(const float2 (&b)[16], const float *inner)
+{
+    const float4 *t = reinterpret_cast<const float4 *>(inner);
+    float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float4 x = t[q];
+        fma2(s0, b[2 * q], make_float2(x.x, x.y));
+        fma2(s1, b[2 * q + 1], make_float2(x.z, x.w));
+    }
+    return (s0.x + s1.x) + (s0.y + s1.y);
+}
+
 // v[i] += inner[token i] . B[feature] of each token's adapter, 32 ranks at a time: the tokens' inner
-// products in the staging tile, this lane's row of B in registers until the adapter changes.
+// products in the staging tile, this lane's row of B in registers.  Where the 32 tokens share one
+// adapter, as in a prompt, they are independent chains without a branch between them (16 packed
+// multiply-adds a token and 32 ranks); else the row is read again where the adapter changes.
 __device__ __forceinline__ void add_adapters(float (&v)[32], const LinearParams &p, float *tile, int lane, int first,
                                              int tokens, int64_t feature)
 {
@@ -318,93 +414,108 @@ __device__ __forceinline__ void add_adapters(float (&v)[32], const LinearParams 
     int mine = -1;
     if (lane < tokens) mine = __ldcg(ad.which + first + lane);
     if (unsigned(mine) >= unsigned(ad.count)) mine = -1;
-    if (__ballot_sync(kFull, mine >= 0) == 0u) return;
+    const unsigned live = __ballot_sync(kFull, mine >= 0);
+    if (live == 0u) return;
+    const int one = __shfl_sync(kFull, mine, __ffs(live) - 1);
+    const bool same = __all_sync(kFull, mine == one || lane >= tokens);
     for (int r0 = 0; r0 < ad.rank; r0 += 32) {
         __syncwarp();
-        const int r = r0 + lane;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
-            const int a = __shfl_sync(kFull, mine, i);  // by all lanes, before any condition on the lane
-            const bool there = a >= 0 && r < ad.rank;
-            tile[i * 32 + lane] = there ? __ldcg(ad.inner + int64_t(first + i) * ad.rank + r) : 0.0f;
-        }
+        const bool there = r0 + lane < ad.rank;
+        const float *src = ad.inner + int64_t(first) * ad.rank + r0 + lane;
+        float t[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i] = there && (live >> i & 1u) ? __ldcg(src + i * ad.rank) : 0.0f;
+        float2 b[16];
+        adapter_row(p, one, feature, r0, b);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) tile[i * 32 + lane] = t[i];
         __syncwarp();
-        float b[32];
-        int now = -1;
+        if (same) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int a = __shfl_sync(kFull, mine, i);
-            if (a < 0) continue;
-            if (a != now) {
-                now = a;
-                const uint16_t *row = static_cast<const uint16_t *>(ad.b) + int64_t(a) * ad.strideb + feature * ad.ldb;
+            for (int i = 0; i < 32; ++i) v[i] += adapter_dot(b, tile + i * 32);
+        } else {
+            int now = one;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                    const int j0 = r0 + 8 * c;
-                    if (feature < p.N) {
-                        if (j0 + 8 <= ad.rank) {
-                            q = __ldg(reinterpret_cast<const uint4 *>(row + j0));
-                        } else {
-                            uint16_t *e = reinterpret_cast<uint16_t *>(&q);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (j0 + j < ad.rank) e[j] = __ldg(row + j0 + j);
-                        }
-                    }
-                    const uint16_t *e = reinterpret_cast<const uint16_t *>(&q);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        b[8 * c + j] = p.bf16 ? __uint_as_float(uint32_t(e[j]) << 16) : __half2float(__ushort_as_half(e[j]));
+            for (int i = 0; i < 32; ++i) {
+                const int a = __shfl_sync(kFull, mine, i);
+                if (a < 0) continue;
+                if (a != now) {
+                    now = a;
+                    adapter_row(p, a, feature, r0, b);
                 }
+                v[i] += adapter_dot(b, tile + i * 32);
             }
-            const float4 *t = reinterpret_cast<const float4 *>(tile + i * 32);
-            float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 x = t[q];
-                s0 = fmaf(b[4 * q], x.x, s0);
-                s1 = fmaf(b[4 * q + 1], x.y, s1);
-                s0 = fmaf(b[4 * q + 2], x.z, s0);
-                s1 = fmaf(b[4 * q + 3], x.w, s1);
-            }
-            v[i] += s0 + s1;
         }
     }
 }
 
 // W_MN: W stored K x N (features contiguous).
-template <int W_MN, int EPI>
+template <int W_MN, int EPI, bool Y_F32>
 __global__ void __launch_bounds__(kThreads, 1)
-grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                      const LinearParams p)
+grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x, const LinearParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    const Shared sh(smem_raw);
+    const Shared sh(smem_raw, p.cap * 64);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int cap = p.cap, ftiles = p.ftiles;
-    const uint32_t tmem = set_up(sh, 1, p.offsets, p.groups, p.y_rows,
+    const uint32_t tmem = set_up(sh, p.offsets, p.groups, p.y_rows,
                                  [=](int rows) { return (rows + cap - 1) / cap * ftiles; });
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
     const int units = sh.start[p.groups], unit0 = int(cluster_id_x()), step = int(cluster_count_x());
     constexpr int kFeatures = EPI == kGated ? 128 : 256;  // of a unit
 
     if (warp == 0) {
-        // ---------------- producer
-        Ring ring;
+        // ---------------- weight producer (warps in step, one elected lane copying)
+        const bool leader = elect_one();
+        const uint32_t full0 = map_to_rank(sh.full(0), 0);  // the first CTA's
+        Ring ring(sh.stages);
         bool ok = true;
         int group = 0;
-        if (lane == 0) {
-            tma_prefetch_desc(&map_w);
-            tma_prefetch_desc(&map_x);
+        if (leader) tma_prefetch_desc(&map_w);
+        for (int u = unit0; ok && u < units; u += step) {
+            const LinearUnit x = linear_unit(p, sh, u, group);
+            const int f0 = x.feature_tile * kFeatures + int(rank) * (kFeatures / 2);
+            const int wg = p.shared_w ? 0 : x.group;
+            const uint32_t bytes = 2u * (kStageA + uint32_t(x.width) * 64u);
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                if (__any_sync(kFull, !ok)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    if (rank == 0) mbar_expect_tx(sh.full(ring.stage), bytes);
+                    if (!(p.inject_stall && kb == 0 && u == unit0)) {
+                        const uint32_t full = full0 + 8u * ring.stage, a = sh.stage_a(ring.stage);
+                        if (W_MN) {  // two boxes of 64 features x 64 k
+                            tma_load_3d_pair(a, &map_w, full, f0, kb * 64, wg);
+                            tma_load_3d_pair(a + 8192, &map_w, full, f0 + 64, kb * 64, wg);
+                        } else if (EPI == kGated) {  // 64 gate rows and their up rows
+                            tma_load_3d_pair(a, &map_w, full, kb * 64, f0, wg);
+                            tma_load_3d_pair(a + 8192, &map_w, full, kb * 64, int(p.N) + f0, wg);
+                        } else {
+                            tma_load_3d_pair(a, &map_w, full, kb * 64, f0, wg);
+                        }
+                    }
+                }
+                __syncwarp();
+                ring.next();
+            }
         }
+        if (leader) finish_producer(sh, watch, ring, ok);
+    } else if (warp == kTokenWarp) {
+        // ---------------- token producer
+        const bool leader = elect_one();
+        const uint32_t full0 = map_to_rank(sh.full(0), 0);
+        Ring ring(sh.stages);
+        bool ok = true;
+        int group = 0;
+        if (leader) tma_prefetch_desc(&map_x.rows[0]);
         for (int u = unit0; ok && u < units; u += step) {
             const LinearUnit x = linear_unit(p, sh, u, group);
             const int half = x.width / 2;                     // tokens this CTA loads
             const int row0 = x.first + int(rank) * half, end = x.first + x.tokens;
-            const int f0 = x.feature_tile * kFeatures + int(rank) * (kFeatures / 2);
-            const int wg = p.shared_w ? 0 : x.group;
             int4 from = make_int4(0, 0, 0, 0);
             if (p.rows != nullptr && 4 * lane < half) {       // a row outside x is read as zeros
                 int r[4];
@@ -416,47 +527,39 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 }
                 from = make_int4(r[0], r[1], r[2], r[3]);
             }
-            const uint32_t bytes = 2u * (kStageA + uint32_t(half) * 128u);
             for (int kb = 0; kb < p.num_kb; ++kb) {
-                bool got = true;
-                if (lane == 0) got = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                if (__any_sync(kFull, !got)) {
+                ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                if (__any_sync(kFull, !ok)) {
                     ok = false;
                     break;
                 }
-                const uint32_t full = map_to_rank(sh.full(ring.stage), 0);
-                if (lane == 0 && rank == 0) mbar_expect_tx(sh.full(ring.stage), bytes);
-                const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
-                const int k0 = kb * 64;
-                if (!(p.inject_stall && kb == 0 && u == unit0)) {
-                    if (lane == 0) {
-                        if (W_MN) {  // two boxes of 64 features x 64 k
-                            tma_load_3d_pair(a, &map_w, full, f0, k0, wg);
-                            tma_load_3d_pair(a + 8192, &map_w, full, f0 + 64, k0, wg);
-                        } else if (EPI == kGated) {  // 64 gate rows and their up rows
-                            tma_load_3d_pair(a, &map_w, full, k0, f0, wg);
-                            tma_load_3d_pair(a + 8192, &map_w, full, k0, int(p.N) + f0, wg);
-                        } else {
-                            tma_load_3d_pair(a, &map_w, full, k0, f0, wg);
+                const uint32_t full = full0 + 8u * ring.stage, b = sh.stage_b(ring.stage);
+                if (p.rows != nullptr) {
+                    if (4 * lane < half) tma_gather4_pair(b + 512u * lane, &map_x.rows[0], full, kb * 64, from);
+                } else if (leader) {  // `half` rows in powers of two, largest first
+                    int at = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (half & (128 >> i)) {
+                            tma_load_2d_pair(b + 128u * at, &map_x.rows[i], full, kb * 64, row0 + at);
+                            at += 128 >> i;
                         }
-                    }
-                    __syncwarp();
-                    if (p.rows != nullptr) {
-                        if (4 * lane < half) tma_gather4_pair(b + 512u * lane, &map_x, full, k0, from);
-                    } else if (16 * lane < half) {
-                        tma_load_2d_pair(b + 2048u * lane, &map_x, full, k0, row0 + 16 * lane);
-                    }
-                    __syncwarp();
                 }
+                __syncwarp();
                 ring.next();
             }
         }
-        if (lane == 0) finish_producer(sh, watch, ring, ok);
+        if (leader && !ok) finish_producer(sh, watch, ring, false);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // ---------------- MMA issuer
+        if (rank == 0) {
+            // ---------------- MMA issuer: the warp in step, one elected lane issuing
+            const bool leader = elect_one();
             const uint32_t fmt = p.bf16 ? (1u << 7) | (1u << 10) : 0u;
-            Ring ring;
+            // descriptors of stage 0; a later stage or K step only moves the start address
+            const uint64_t a0 = W_MN ? smem_desc(sh.a, 8192, 1024) : smem_desc(sh.a, 16, 1024);
+            const uint64_t b0 = smem_desc(sh.b, 16, 1024);
+            constexpr uint64_t kStepA = W_MN ? 2048 >> 4 : 32 >> 4, kStepB = 32 >> 4;
+            Ring ring(sh.stages);
             int acc = 0, group = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
@@ -471,33 +574,36 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     ok = watch.wait(sh.full(ring.stage), ring.phase);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
+                    if (leader) {
+                        const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
+                        const uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_f16<true>(d, W_MN ? smem_desc(a + k * 2048, 8192, 1024) : smem_desc(a + k * 32, 16, 1024),
-                                       smem_desc(b + k * 32, 16, 1024), idesc, kb > 0 || k > 0 ? 1u : 0u);
-                    commit_both(sh.empty(ring.stage));
+                        for (int k = 0; k < 4; ++k)
+                            umma_f16<true>(d, a + k * kStepA, b + k * kStepB, idesc, kb > 0 || k > 0 ? 1u : 0u);
+                        commit_both(sh.empty(ring.stage));
+                    }
+                    __syncwarp();
                     ring.next();
                 }
                 if (!ok) break;
-                commit_both(sh.acc_full(acc));
+                if (leader) commit_both(sh.acc_full(acc));
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
-            if (!ok) drain_issuer(sh);
+            if (!ok && leader) drain_issuer(sh);
         }
     } else {
         // ---------------- epilogue: TMEM lanes 32 * quarter .. of this CTA's 128 rows
-        const int quarter = warp & 3;
-        uint8_t *tile = sh.epi + quarter * 4096;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint8_t *tile = sh.epi + (warp - 2) * 4096;
         int acc = 0, group = 0;
         uint32_t acc_phase = 0;
         // the adapters' inner products come from the kernel ahead of this one
         if (EPI == kAdapted) asm volatile("griddepcontrol.wait;" ::: "memory");
         uint8_t *Y = static_cast<uint8_t *>(p.Y);
-        const int64_t ldy = p.ldy * (p.y_f32 ? 4 : 2);
+        const int64_t ldy = p.ldy * (Y_F32 ? 4 : 2);
         for (int u = unit0; u < units; u += step) {
             const LinearUnit x = linear_unit(p, sh, u, group);
             const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
@@ -512,10 +618,11 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 // pieces of 32 tokens the gate's warp finishes the first, the up's warp the second
                 const bool up = quarter >= 2;
                 const int64_t f = int64_t(x.feature_tile) * 128 + int64_t(rank) * 64 + (quarter & 1) * 32;
+                const int meet = 2 + 2 * half + (quarter & 1);  // named barrier of the two warps
                 float *own = reinterpret_cast<float *>(tile);
-                const float *other = reinterpret_cast<const float *>(sh.epi + (quarter ^ 2) * 4096);
+                const float *other = reinterpret_cast<const float *>(sh.epi + ((warp - 2) ^ 2) * 4096);
 #pragma unroll 1
-                for (int c = 0; c < x.width; c += 64) {
+                for (int c = 64 * half; c < x.width; c += 128) {
                     const bool two = c + 32 < x.width;
                     float v0[32], v1[32];
                     __syncwarp();
@@ -523,13 +630,12 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     if (two) tmem_ld_32(taddr + c + 32, v1);
                     if (p.pre != nullptr) {
                         uint8_t *pre = static_cast<uint8_t *>(p.pre) + (up ? p.N * 2 : 0);
-                        // N of the up half may end between two 16-byte pieces of pre: element by element then
-                        const int64_t n = f + 32 <= p.N && p.N % 8 == 0 ? p.N : -1;
-                        if (n > 0) {
-                            store_tokens(v0, tile, lane, pre, p.ldp * 2, x.first + c, x.tokens - c, f, n, false, p.bf16);
+                        if (f + 32 <= p.N && p.N % 8 == 0) {
+                            store_tokens<false>(v0, tile, lane, pre, p.ldp * 2, x.first + c, x.tokens - c, f, p.N, p.bf16);
                             if (two)
-                                store_tokens(v1, tile, lane, pre, p.ldp * 2, x.first + c + 32, x.tokens - c - 32, f, n, false, p.bf16);
-                        } else if (f + lane < p.N) {
+                                store_tokens<false>(v1, tile, lane, pre, p.ldp * 2, x.first + c + 32, x.tokens - c - 32, f,
+                                                    p.N, p.bf16);
+                        } else if (f + lane < p.N) {  // the up half's pieces may not be 16-byte aligned
                             uint16_t *dst = reinterpret_cast<uint16_t *>(pre) + int64_t(x.first + c) * p.ldp + f + lane;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
@@ -546,7 +652,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 #pragma unroll
                         for (int i = 0; i < 32; ++i) own[i * 32 + lane] = v1[i];
                     }
-                    asm volatile("bar.sync %0, 64;" ::"r"(2 + (quarter & 1)) : "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(meet) : "memory");
                     if (!up) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v0[i] = silu(v0[i]) * other[i * 32 + lane];
@@ -554,21 +660,21 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v0[i] = silu(other[i * 32 + lane]) * v1[i];
                     }
-                    asm volatile("bar.sync %0, 64;" ::"r"(2 + (quarter & 1)) : "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(meet) : "memory");
                     const int at = up ? c + 32 : c;
                     if (!up || two)
-                        store_tokens(v0, tile, lane, Y, ldy, x.first + at, x.tokens - at, f, p.N, p.y_f32, p.bf16);
+                        store_tokens<Y_F32>(v0, tile, lane, Y, ldy, x.first + at, x.tokens - at, f, p.N, p.bf16);
                 }
             } else {
                 const int64_t f = int64_t(x.feature_tile) * 256 + int64_t(rank) * 128 + quarter * 32;
 #pragma unroll 1
-                for (int c = 0; c < x.width; c += 32) {
+                for (int c = 32 * half; c < x.width; c += 64) {
                     float v[32];
                     __syncwarp();
                     tmem_ld_32(taddr + c, v);
                     if (EPI == kAdapted)
                         add_adapters(v, p, reinterpret_cast<float *>(tile), lane, x.first + c, min(32, x.tokens - c), f + lane);
-                    store_tokens(v, tile, lane, Y, ldy, x.first + c, x.tokens - c, f, p.N, p.y_f32, p.bf16);
+                    store_tokens<Y_F32>(v, tile, lane, Y, ldy, x.first + c, x.tokens - c, f, p.N, p.bf16);
                 }
             }
             tc_fence_before();
@@ -584,7 +690,8 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 }
 
 // ------------------------------------------------------------------ dW = dY^T X
-constexpr int kGradThreads = 224;  // warp 6 is the cleaner
+constexpr int kCleaner = kTokenWarp + 1;  // warp
+constexpr int kGradThreads = kThreads + 32;
 
 struct GradParams {
     const int32_t *offsets;
@@ -593,7 +700,7 @@ struct GradParams {
     int ntiles, ktiles;
     void *dW;
     int64_t lddw, stridedw;
-    int dw_f32, bf16;
+    int bf16;
     unsigned int *status;
     uint64_t timeout_ns;
     int inject_stall;
@@ -610,60 +717,64 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, const Shared 
 }
 
 // A pair's tile is 256 (n) x 256 (k): each CTA holds 128 columns of dY and 128 of X as two boxes of
-// 64 columns x 64 positions each.  A slice is complete when both CTAs have said so on the first CTA's
-// full barrier: the producer for a whole slice, the cleaner for a group's last one.
+// 64 columns x 64 positions each.  A whole slice lands on the first CTA's full barrier; a group's last
+// one on each CTA's own ragged barrier, from which the cleaners pass it on: the second CTA's to the
+// first's (cleaned), the first's to the full barrier.
+template <bool DW_F32>
 __global__ void __launch_bounds__(kGradThreads, 1)
 grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const GradParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    const Shared sh(smem_raw);
+    const Shared sh(smem_raw, kMaxStageB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const uint32_t tmem = set_up(sh, 2, p.offsets, p.groups, p.positions, [](int) { return 0; });
+    const uint32_t tmem = set_up(sh, p.offsets, p.groups, p.positions, [](int) { return 0; });
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
     const int units = p.groups * p.ntiles * p.ktiles, unit0 = int(cluster_id_x()), step = int(cluster_count_x());
-    constexpr uint32_t kSliceBytes = kStageA + kStageB;
+    constexpr uint32_t kSliceBytes = kStageA + kMaxStageB;
 
-    if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- producer
-            Ring ring;
-            bool ok = true;
-            tma_prefetch_desc(&map_dy);
-            tma_prefetch_desc(&map_x);
-            for (int u = unit0; ok && u < units; u += step) {
-                const GradUnit x = grad_unit(p, sh, u);
-                const int n0 = x.tn * 256 + int(rank) * 128, k0 = x.tk * 256 + int(rank) * 128;
-                for (int s = 0; s < x.rows; s += 64) {
-                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                    if (!ok) break;
-                    const bool ragged = x.rows - s < 64;
-                    uint32_t bar;
-                    if (ragged) {  // lands on this CTA's own barrier, for its cleaner
-                        mbar_expect_tx(sh.ragged(ring.stage), kSliceBytes);
-                        bar = map_to_rank(sh.ragged(ring.stage), rank);
-                    } else {
-                        bar = map_to_rank(sh.full(ring.stage), 0);
-                        if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2 * kSliceBytes);
-                        else mbar_arrive_cluster(bar);
+    if (warp == 0 || warp == kTokenWarp) {
+        // ---------------- producers, of dY and of X (warps in step, one elected lane copying)
+        const bool leader = elect_one(), of_x = warp != 0;
+        const CUtensorMap *map = of_x ? &map_x : &map_dy;
+        const uint32_t full0 = map_to_rank(sh.full(0), 0), ragged0 = map_to_rank(sh.ragged(0), rank);
+        Ring ring(sh.stages);
+        bool ok = true;
+        if (leader) tma_prefetch_desc(map);
+        for (int u = unit0; ok && u < units; u += step) {
+            const GradUnit x = grad_unit(p, sh, u);
+            const int c0 = (of_x ? x.tk : x.tn) * 256 + int(rank) * 128;
+            for (int s = 0; s < x.rows; s += 64) {
+                ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                if (__any_sync(kFull, !ok)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    const bool ragged = x.rows - s < 64;  // lands on this CTA's own barrier, for its cleaner
+                    const uint32_t bar = (ragged ? ragged0 : full0) + 8u * ring.stage;
+                    if (!of_x) {
+                        if (ragged) mbar_expect_tx(sh.ragged(ring.stage), kSliceBytes);
+                        else if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2 * kSliceBytes);
                     }
                     if (!(p.inject_stall && s == 0 && u == unit0)) {
-                        const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
-                        tma_load_2d_pair(a, &map_dy, bar, n0, x.first + s);
-                        tma_load_2d_pair(a + 8192, &map_dy, bar, n0 + 64, x.first + s);
-                        tma_load_2d_pair(b, &map_x, bar, k0, x.first + s);
-                        tma_load_2d_pair(b + 8192, &map_x, bar, k0 + 64, x.first + s);
+                        const uint32_t dst = of_x ? sh.stage_b(ring.stage) : sh.stage_a(ring.stage);
+                        tma_load_2d_pair(dst, map, bar, c0, x.first + s);
+                        tma_load_2d_pair(dst + 8192, map, bar, c0 + 64, x.first + s);
                     }
-                    ring.next();
                 }
+                __syncwarp();
+                ring.next();
             }
-            finish_producer(sh, watch, ring, ok);
         }
+        if (leader && (!ok || !of_x)) finish_producer(sh, watch, ring, ok);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ---------------- MMA issuer
+            const bool leader = elect_one();
             const uint32_t idesc = make_idesc(1, 1, 256, 256) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u);
-            Ring ring;
+            const uint64_t a0 = smem_desc(sh.a, 8192, 1024), b0 = smem_desc(sh.b, 8192, 1024);
+            Ring ring(sh.stages);
             int acc = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
@@ -675,31 +786,36 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                 tc_fence_after();
                 const uint32_t d = tmem + uint32_t(acc * kAccCols);
                 for (int s = 0; s < x.rows; s += 64) {
-                    ok = watch.wait<true>(sh.full(ring.stage), ring.phase);
+                    ok = watch.wait(sh.full(ring.stage), ring.phase);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
-                    const int steps = min(4, (x.rows - s + 15) / 16);  // 16 positions an MMA
-                    for (int k = 0; k < steps; ++k)
-                        umma_f16<true>(d, smem_desc(a + k * 2048, 8192, 1024), smem_desc(b + k * 2048, 8192, 1024), idesc,
-                                       s > 0 || k > 0 ? 1u : 0u);
-                    commit_both(sh.empty(ring.stage));
+                    if (leader) {
+                        const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
+                        const uint64_t b = b0 + uint32_t(ring.stage * (kMaxStageB >> 4));
+                        const int steps = min(4, (x.rows - s + 15) / 16);  // 16 positions an MMA
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < steps)
+                                umma_f16<true>(d, a + k * (2048 >> 4), b + k * (2048 >> 4), idesc, s > 0 || k > 0 ? 1u : 0u);
+                        commit_both(sh.empty(ring.stage));
+                    }
+                    __syncwarp();
                     ring.next();
                 }
                 if (!ok) break;
-                commit_both(sh.acc_full(acc));
+                if (leader) commit_both(sh.acc_full(acc));
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
-            if (!ok) drain_issuer(sh);
+            if (!ok && leader) drain_issuer(sh);
         }
-    } else if (warp == 6) {
+    } else if (warp == kCleaner) {
         // ---------------- cleaner: zeros for the positions behind the group's last, up to the MMA's
         // granularity of 16
-        Ring ring;
-        uint32_t parity = 0;  // of each stage's ragged barrier, one bit a stage
+        Ring ring(sh.stages);
+        uint32_t parity = 0;  // of each stage's ragged and cleaned barriers, one bit a stage
         bool ok = true;
         for (int u = unit0; ok && u < units; u += step) {
             const GradUnit x = grad_unit(p, sh, u);
@@ -712,9 +828,8 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                         ok = false;
                         break;
                     }
-                    parity ^= 1u << ring.stage;
                     const int end = (left + 15) & ~15, pieces = (end - left) * 8;  // 16-byte pieces of a box
-                    const uint32_t a = sh.a + ring.stage * kStageA, b = sh.b + ring.stage * kStageB;
+                    const uint32_t a = sh.stage_a(ring.stage), b = sh.stage_b(ring.stage);
                     for (int i = lane; i < 4 * pieces; i += 32) {
                         const int box = i / pieces;
                         const uint32_t at = (box < 2 ? a : b) + (box & 1) * 8192u + uint32_t(left) * 128u +
@@ -723,7 +838,20 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(sh.full(ring.stage), 0));
+                    got = true;
+                    if (lane == 0) {
+                        if (rank == 1) {
+                            mbar_arrive_cluster(map_to_rank(sh.cleaned(ring.stage), 0));
+                        } else {
+                            got = watch.wait<true>(sh.cleaned(ring.stage), (parity >> ring.stage) & 1u);
+                            if (got) mbar_arrive(sh.full(ring.stage));
+                        }
+                    }
+                    if (__any_sync(kFull, !got)) {
+                        ok = false;
+                        break;
+                    }
+                    parity ^= 1u << ring.stage;
                 }
                 ring.next();
             }
@@ -731,8 +859,8 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
     } else {
         // ---------------- epilogue: TMEM lane = row of dW; 32 x 32 pieces pass through the staging
         // tile (16-byte pieces, XOR-swizzled by row) so that stores are 128- or 64-byte row segments
-        const int quarter = warp & 3;
-        float4 *tile = reinterpret_cast<float4 *>(sh.epi + quarter * 4096);
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        float4 *tile = reinterpret_cast<float4 *>(sh.epi + (warp - 2) * 4096);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int u = unit0; u < units; u += step) {
@@ -748,7 +876,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
             const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * kAccCols);
             const int64_t n0 = int64_t(x.tn) * 256 + int64_t(rank) * 128 + quarter * 32;
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
+            for (int c = 32 * half; c < 256; c += 64) {
                 const int64_t k0 = int64_t(x.tk) * 256 + c;
                 float v[32];
                 __syncwarp();
@@ -763,34 +891,51 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                 for (int j = 0; j < 8; ++j)
                     tile[lane * 8 + (j ^ (lane & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 __syncwarp();
-                const int q = lane & 7;
-                const int64_t k = k0 + 4 * q;
+                if (DW_F32) {
+                    const int q = lane & 7;
+                    const int64_t k = k0 + 4 * q;
+                    float4 o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3);
-                    const float4 o = tile[r * 8 + (q ^ (r & 7))];
-                    if (n0 + r >= p.N || k >= p.K) continue;
-                    const int64_t at = int64_t(x.group) * p.stridedw + (n0 + r) * p.lddw + k;
-                    if (p.dw_f32) {
-                        float *dst = static_cast<float *>(p.dW) + at;
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3);
+                        o[i] = tile[r * 8 + (q ^ (r & 7))];
+                    }
+                    float *dst = static_cast<float *>(p.dW) + int64_t(x.group) * p.stridedw + (n0 + (lane >> 3)) * p.lddw + k;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i, dst += 4 * p.lddw) {
+                        if (n0 + 4 * i + (lane >> 3) >= p.N) continue;
                         if (k + 4 <= p.K) {
-                            *reinterpret_cast<float4 *>(dst) = o;
+                            *reinterpret_cast<float4 *>(dst) = o[i];
                         } else {
-                            const float e[4] = {o.x, o.y, o.z, o.w};
+                            const float e[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 if (k + j < p.K) dst[j] = e[j];
                         }
-                    } else {
-                        uint16_t *dst = static_cast<uint16_t *>(p.dW) + at;
-                        const uint16_t e[4] = {to_16(o.x, p.bf16), to_16(o.y, p.bf16), to_16(o.z, p.bf16), to_16(o.w, p.bf16)};
-                        if (k + 4 <= p.K) {
-                            *reinterpret_cast<uint2 *>(dst) = make_uint2(uint32_t(e[0]) | uint32_t(e[1]) << 16,
-                                                                         uint32_t(e[2]) | uint32_t(e[3]) << 16);
-                        } else {
+                    }
+                } else {
+                    // lane: 8 columns of rows 8 i + lane / 4, two staged pieces to one 16-byte store
+                    const int q = lane & 3;
+                    const int64_t k = k0 + 8 * q;
+                    uint4 o[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (k + j < p.K) dst[j] = e[j];
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2);
+                        const float4 a = tile[r * 8 + ((2 * q) ^ (r & 7))], b = tile[r * 8 + ((2 * q + 1) ^ (r & 7))];
+                        o[i] = make_uint4(pack_16(a.x, a.y, p.bf16), pack_16(a.z, a.w, p.bf16), pack_16(b.x, b.y, p.bf16),
+                                          pack_16(b.z, b.w, p.bf16));
+                    }
+                    uint16_t *dst = static_cast<uint16_t *>(p.dW) + int64_t(x.group) * p.stridedw + (n0 + (lane >> 2)) * p.lddw + k;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i, dst += 8 * p.lddw) {
+                        if (n0 + 8 * i + (lane >> 2) >= p.N) continue;
+                        if (k + 8 <= p.K) {
+                            *reinterpret_cast<uint4 *>(dst) = o[i];
+                        } else {
+                            const uint32_t e[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (k + j < p.K) dst[j] = uint16_t(e[j / 2] >> (16 * (j & 1)));
                         }
                     }
                 }
@@ -855,9 +1000,9 @@ template <class K> int resident_pairs(K *kernel, int threads, int dev, std::atom
     return n;
 }
 
-template <class K, class P>
+template <class K, class M, class P>
 cudaError_t launch_pairs(K *kernel, int threads, int64_t pairs, bool after, cudaStream_t stream, const CUtensorMap &a,
-                         const CUtensorMap &b, const P &p)
+                         const M &b, const P &p)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(2 * pairs));
@@ -889,10 +1034,15 @@ void test_hooks(uint64_t &timeout_ns, int &inject_stall)
     }
 }
 
-// Tokens of a tile: the multiple of 32 for which the group's tiles take the least time.  A K slice
-// of a tile costs its MMAs (2 cycles a token) or its loads, and the tiles run in waves of all pairs.
+// Tokens of a tile: the multiple of 32 for which the average group's tiles take the least time in
+// waves of all pairs.  A K slice of a tile of w tokens takes the longer of its MMAs and of its copies
+// and hand-overs; measured with 64 groups of 512 rows, K = 4096, in SM cycles: 375 (w = 32), 431 (128),
+// 532 (192), 698 (256, where the chip's power limit sets the clock).
 int tile_cap(const GroupedArgs &a, int64_t ftiles, int pairs)
 {
+    // GEMM_GB300_GROUPED_CAP=n (sweeps only): tiles of at most n tokens
+    if (const char *e = std::getenv("GEMM_GB300_GROUPED_CAP"); e && std::atoi(e) >= 32 && std::atoi(e) <= 256)
+        return std::atoi(e) / 32 * 32;
     const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;
     const int64_t mean = (a.y_rows + groups - 1) / groups;
     int best = 256;
@@ -901,8 +1051,8 @@ int tile_cap(const GroupedArgs &a, int64_t ftiles, int pairs)
         const int64_t tiles = (mean + cap - 1) / cap;
         const int64_t width = ((mean + tiles - 1) / tiles + 31) / 32 * 32;
         const int64_t waves = (groups * tiles * ftiles + pairs - 1) / pairs;
-        const double slice = width > 128 ? 2.0 * double(width) : 256.0;
-        const double cost = double(waves) * slice;
+        const double mma = 2.73 * double(width), copies = 360.0 + 0.55 * double(width);
+        const double cost = double(waves) * (mma > copies ? mma : copies);
         if (cost < 0.98 * least) {
             least = cost;
             best = cap;
@@ -911,11 +1061,11 @@ int tile_cap(const GroupedArgs &a, int64_t ftiles, int pairs)
     return best;
 }
 
-template <int W_MN, int EPI>
-cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+template <int W_MN, int EPI, bool Y_F32>
+cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
 {
     static std::atomic<int> cache[64];
-    auto *kernel = grouped_linear_kernel<W_MN, EPI>;
+    auto *kernel = grouped_linear_kernel<W_MN, EPI, Y_F32>;
     const int pairs = resident_pairs(kernel, kThreads, dev.device, cache);
     unsigned int *status = device_status_word(dev.device);
     if (pairs <= 0 || status == nullptr) return cudaErrorInitializationError;
@@ -923,13 +1073,15 @@ cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStrea
     const int64_t w_rows = a.opW == GEMM_OP_T ? (a.gated ? 2 * a.N : a.N) : a.K;
     const int64_t w_cols = a.opW == GEMM_OP_T ? a.K : a.N;
     const bool shared_w = a.groups == 1 || a.stridew == 0;
-    CUtensorMap mw, mx;
+    CUtensorMap mw;
+    TokenMaps mx;
     std::memset(&mw, 0, sizeof(mw));
     std::memset(&mx, 0, sizeof(mx));
-    if (!make_map(&mw, a.W, bf16, w_rows, w_cols, a.ldw, W_MN || EPI == kGated ? 64 : 128, shared_w ? 1 : a.groups,
-                  shared_w ? w_rows * a.ldw : a.stridew) ||
-        !make_map(&mx, a.X, bf16, a.x_rows, a.K, a.ldx, a.rows != nullptr ? 1 : 16, 0, 0))
-        return cudaErrorInvalidValue;
+    bool ok = make_map(&mw, a.W, bf16, w_rows, w_cols, a.ldw, W_MN || EPI == kGated ? 64 : 128, shared_w ? 1 : a.groups,
+                       shared_w ? w_rows * a.ldw : a.stridew);
+    for (int i = 0; ok && i < (a.rows != nullptr ? 1 : 4); ++i)
+        ok = make_map(&mx.rows[i], a.X, bf16, a.x_rows, a.K, a.ldx, a.rows != nullptr ? 1 : 128 >> i, 0, 0);
+    if (!ok) return cudaErrorInvalidValue;
     const int features = EPI == kGated ? 128 : 256;
     LinearParams p{};
     p.offsets = a.offsets;
@@ -944,7 +1096,6 @@ cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStrea
     p.rows = a.rows;
     p.Y = a.Y;
     p.ldy = a.ldy;
-    p.y_f32 = a.y_type == GEMM_TYPE_F32;
     p.bf16 = bf16;
     p.pre = a.pre;
     p.ldp = a.ldp;
@@ -954,6 +1105,12 @@ cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStrea
     // no more pairs than there can be units
     const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles;
     return launch_pairs(kernel, kThreads, most < pairs ? most : pairs, EPI == kAdapted, stream, mw, mx, p);
+}
+
+template <int W_MN, int EPI> cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+{
+    return a.y_type == GEMM_TYPE_F32 ? launch_linear_t<W_MN, EPI, true>(dev, a, stream)
+                                     : launch_linear_t<W_MN, EPI, false>(dev, a, stream);
 }
 
 }  // namespace
@@ -969,9 +1126,11 @@ cudaError_t launch_many_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaSt
 
 cudaError_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, cudaStream_t stream)
 {
-    static std::atomic<int> cache[64];
+    static std::atomic<int> cache[2][64];
     if (dev.smem_optin < size_t(kSmemBytes)) return cudaErrorInvalidDevice;
-    const int pairs = resident_pairs(grouped_grad_kernel, kGradThreads, dev.device, cache);
+    const bool f32 = a.dw_type == GEMM_TYPE_F32;
+    auto *kernel = f32 ? grouped_grad_kernel<true> : grouped_grad_kernel<false>;
+    const int pairs = resident_pairs(kernel, kGradThreads, dev.device, cache[f32]);
     unsigned int *status = device_status_word(dev.device);
     if (pairs <= 0 || status == nullptr) return cudaErrorInitializationError;
     const bool bf16 = a.type == GEMM_TYPE_BF16;
@@ -993,13 +1152,12 @@ cudaError_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, c
     p.dW = a.dW;
     p.lddw = a.lddw;
     p.stridedw = a.stridedw;
-    p.dw_f32 = a.dw_type == GEMM_TYPE_F32;
     p.bf16 = bf16;
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
     const int64_t units = int64_t(a.groups) * p.ntiles * p.ktiles;
     if (units >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    return launch_pairs(grouped_grad_kernel, kGradThreads, units < pairs ? units : pairs, false, stream, md, mx, p);
+    return launch_pairs(kernel, kGradThreads, units < pairs ? units : pairs, false, stream, md, mx, p);
 }
 
 }  // namespace gemm

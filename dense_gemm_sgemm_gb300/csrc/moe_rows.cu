@@ -96,6 +96,28 @@ dispatch_kernel(int64_t slots, int64_t cols, int k, const X *x, int64_t ldx, con
     }
 }
 
+// Warp: one position.  out[p] = x[rows[p]], zeros where the row is outside x, for the positions of a
+// group.  16-bit elements in 16-byte pieces; the last piece of an odd row length element by element.
+__global__ void __launch_bounds__(kThreads)
+gather_kernel(const int32_t *offsets, int groups, int64_t positions, const uint16_t *x, int64_t ldx, int64_t x_rows,
+              const int32_t *rows, int64_t K, uint16_t *out, int64_t ldo)
+{
+    const int64_t p = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (p >= positions || p >= __ldg(offsets + groups)) return;
+    const int r = __ldg(rows + p);
+    const bool there = r >= 0 && r < x_rows;
+    const uint16_t *src = x + int64_t(there ? r : 0) * ldx;
+    uint16_t *dst = out + p * ldo;
+#pragma unroll 4
+    for (int64_t c = 8 * lane; c + 8 <= K; c += 256) {
+        const uint4 v = there ? __ldg(reinterpret_cast<const uint4 *>(src + c)) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(dst + c) = v;
+    }
+    const int64_t c = (K & ~int64_t(7)) + lane;
+    if (c < K) dst[c] = there ? src[c] : uint16_t(0);
+}
+
 template <class X, class D, int VEC>
 __global__ void __launch_bounds__(kThreads)
 gated_silu_backward_kernel(int64_t rows, int64_t cols, int64_t I, const X *pre, int64_t ldp, const D *dh, int64_t lddh,
@@ -199,6 +221,15 @@ cudaError_t launch_dispatch(int type, int rows_type, int64_t T, int64_t H, int t
             return counted();
         });
     });
+}
+
+cudaError_t launch_gather(const GroupedArgs &a, void *out, int64_t ldo, cudaStream_t stream)
+{
+    unsigned blocks;
+    if (!grid_of(a.y_rows, kThreads / 32, blocks)) return cudaErrorInvalidConfiguration;
+    gather_kernel<<<blocks, kThreads, 0, stream>>>(a.offsets, a.groups, a.y_rows, static_cast<const uint16_t *>(a.X), a.ldx,
+                                                   a.x_rows, a.rows, a.K, static_cast<uint16_t *>(out), ldo);
+    return counted();
 }
 
 cudaError_t launch_gated_silu_backward(int type, int dh_type, int64_t rows, int64_t I, const void *pre, int64_t ldp,

@@ -379,7 +379,7 @@ template <int V>
 cudaError_t launch_plan_t(const RouteArgs &a, cudaStream_t stream)
 {
     const size_t smem = (size_t(kPlanWarps) + 2 + (V > 0 ? kPlanWarps : 0)) * size_t(a.E) * 4;
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize, 140 * 1024);
+    cudaError_t e = allow_smem_once(plan_kernel<V>, 140 * 1024);
     if (e != cudaSuccess) return e;
     // CTAs enough that a warp has at most a few tokens to route, or 1024 slots to sort; a power of 2
     const int64_t per_cta = V > 0 ? 2 * kPlanWarps : 1024;

@@ -201,7 +201,8 @@ static bool tiled(const void *p, int64_t ld) { return aligned(p, 16) && ld % 8 =
 gemm_status_t gemm_grouped_linear(gemm_type_t type, gemm_type_t y_type, int64_t groups, const int32_t *offsets,
                                   gemm_op_t opW, int gated, int64_t N, int64_t K, const void *X, int64_t ldx,
                                   int64_t x_rows, const int32_t *rows, const void *W, int64_t ldw, int64_t strideW,
-                                  void *Y, int64_t ldy, int64_t y_rows, void *pre, int64_t ldp, void *stream)
+                                  void *Y, int64_t ldy, int64_t y_rows, void *pre, int64_t ldp, void *work,
+                                  void *stream)
 {
     if (!is_type16(type) || (y_type != type && y_type != GEMM_TYPE_F32) || (opW != GEMM_OP_N && opW != GEMM_OP_T) ||
         (gated && opW != GEMM_OP_T) || (!gated && pre != nullptr) || groups < 0 || N < 0 || K < 0 || x_rows < 0 ||
@@ -218,13 +219,13 @@ gemm_status_t gemm_grouped_linear(gemm_type_t type, gemm_type_t y_type, int64_t 
         return GEMM_ERR_INVALID_VALUE;
     if (groups > 1 && w_rows > 0 && strideW != 0 && strideW < (w_rows - 1) * ldw + w_cols) return GEMM_ERR_INVALID_VALUE;
     if ((K > 0 && (!tiled(X, ldx) || !tiled(W, ldw) || strideW % 8 != 0)) || !tiled(Y, ldy) ||
-        !words(offsets, rows) || (pre != nullptr && !tiled(pre, ldp)))
+        !words(offsets, rows) || (pre != nullptr && !tiled(pre, ldp)) || !aligned(work, 16))
         return GEMM_ERR_MISALIGNED;
     DeviceInfo dev;
     const gemm_status_t s = usable(dev);
     if (s != GEMM_OK) return s;
     const GroupedArgs a{type, y_type, int(groups), offsets, opW, gated != 0, N, K, X, ldx, x_rows, rows, W, ldw, strideW,
-                        Y, ldy, y_rows, pre, ldp, Adapters{}};
+                        Y, ldy, y_rows, pre, ldp, Adapters{}, work};
     return launch_grouped(dev, a, static_cast<cudaStream_t>(stream));
 }
 
@@ -283,7 +284,7 @@ gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, 
     if (s != GEMM_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     GroupedArgs a{type, y_type, 1, nullptr, GEMM_OP_T, 0, N, K, X, ldx, T, nullptr, W, ldw, 0, Y, ldy, T, nullptr, 0,
-                  Adapters{}};
+                  Adapters{}, nullptr};
     if (adapted) {
         int32_t *which = reinterpret_cast<int32_t *>(work + T * R);
         const ShrinkArgs sh{type, T, K, X, ldx, int(requests), segments, adapters, int(n_adapters), int(R), A, lda, strideA,

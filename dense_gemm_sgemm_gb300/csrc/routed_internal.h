@@ -50,6 +50,14 @@ template <> __device__ __forceinline__ void store8(float *p, const float (&v)[8]
 // 1 / (1 + exp(-x)); 0 and 1 at the ends, no NaN for finite x.
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
+// Lets `kernel` use up to `bytes` of dynamic shared memory; asks the runtime once per kernel and
+// device (the call costs as much as a launch), so every call of one kernel names the same bytes.
+cudaError_t allow_smem_once(const void *kernel, int bytes);
+template <class... P> cudaError_t allow_smem_once(void (*kernel)(P...), int bytes)
+{
+    return allow_smem_once(reinterpret_cast<const void *>(kernel), bytes);
+}
+
 struct RouteArgs {
     int type;
     int64_t T;
@@ -104,12 +112,15 @@ struct GroupedArgs {
     void *pre;
     int64_t ldp;
     Adapters ad;
+    void *work;  // y_rows x (K rounded up to 8) elements, or NULL
 };
 // Few rows per group (opW = T): weights straight from global memory to mma.sync fragments.
 cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 
 // Many rows per group, or opW = N: tcgen05 tiles fed by TMA.
 cudaError_t launch_many_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
+// X[rows[p]] to row p of `out`, for the positions of the groups.
+cudaError_t launch_gather(const GroupedArgs &a, void *out, int64_t ldo, cudaStream_t stream);
 gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 
 struct WeightGradArgs {

@@ -62,18 +62,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 }
 
 // Waits for the phase of parity `parity` to complete.  Gives up (returns false) when the
-// CTA-wide abort flag is raised or after timeout_ns nanoseconds.
+// CTA-wide abort flag is raised or after timeout_ns nanoseconds.  The timer is read only every 16
+// polls: a read takes several hundred cycles, as long as a slice of a small tile.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int *abort_flag,
                                           uint64_t timeout_ns)
 {
-    if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
         if ((it & 15u) == 0) {
             if (*abort_flag) return false;
-            if (global_timer_ns() - t0 > timeout_ns) return false;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > timeout_ns) return false;
         }
     }
 }

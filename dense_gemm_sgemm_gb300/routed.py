@@ -28,15 +28,23 @@ _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _SCORE = {"softmax": 0, "sigmoid": 1}
 
 
+_calls = {}
+
+
 def _run(name, *args):
-    status = getattr(load(), name)(*args)
+    call = _calls.get(name)
+    if call is None:
+        call = _calls[name] = getattr(load(), name)
+    status = call(*args)
     if status != 0:
         raise GemmError(status, name)
 
 
-def _stream(stream):
+def _stream(stream, tensor):
+    """The given stream, or the current one of the tensor's device (the raw handle: building a
+    torch.cuda.Stream costs as much as the launch)."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(tensor.get_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -53,16 +61,18 @@ def _matrix(t, what, cols=None, rows=None, dtype=None, dims=2):
         raise TypeError(f"{what}: a torch tensor is wanted")
     if not t.is_cuda:
         raise ValueError(f"{what}: must live in CUDA device memory")
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != dims or (shape[-1] > 1 and strides[-1] != 1):
         raise ValueError(f"{what}: {dims}-D with unit column stride wanted")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if cols is not None and t.shape[-1] != cols:
-        raise ValueError(f"{what}: {cols} columns wanted, got {t.shape[-1]}")
-    if rows is not None and t.shape[-2] != rows:
-        raise ValueError(f"{what}: {rows} rows wanted, got {t.shape[-2]}")
-    # the stride of a single row means nothing; a size-1 dimension may carry any
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.shape[-1], 1) if t.stride(-2) < t.shape[-1] else t.stride(-2)
+    if cols is not None and shape[-1] != cols:
+        raise ValueError(f"{what}: {cols} columns wanted, got {shape[-1]}")
+    if rows is not None and shape[-2] != rows:
+        raise ValueError(f"{what}: {rows} rows wanted, got {shape[-2]}")
+    ld = strides[-2]
+    # the stride of a single row means nothing
+    return ld if shape[-2] > 1 else max(ld, shape[-1], 1)
 
 
 def _array(t, what, dtype, count=None):
@@ -98,14 +108,16 @@ def moe_route(logits, top_k, *, bias=None, score="softmax", groups=1, groups_kep
     ld = _matrix(logits, "logits")
     T, E = logits.shape
     dev = logits.device
-    out = torch.empty(3 * T * top_k + E + 1, dtype=torch.int32, device=dev)
-    ids, where, tokens, offsets = out.split((T * top_k, T * top_k, T * top_k, E + 1))
     weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    where = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    tokens = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
     _run("gemm_moe_route", _type(logits, "logits"), T, E, logits.data_ptr(), ld,
          _array(bias, "bias", torch.float32, E), _score(score), groups, groups_kept, group_top, top_k,
          int(renormalise), scale, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-         tokens.data_ptr(), where.data_ptr(), _stream(stream))
-    return ids.view(T, top_k), weights, offsets, tokens, where.view(T, top_k)
+         tokens.data_ptr(), where.data_ptr(), _stream(stream, logits))
+    return ids, weights, offsets, tokens, where
 
 
 def _score(score):
@@ -125,7 +137,7 @@ def moe_route_backward(dweights, logits, ids, *, score="softmax", renormalise=Tr
     _run("gemm_moe_route_backward", _type(logits, "logits"), T, E,
          _array(dweights, "dweights", torch.float32, T * top_k), logits.data_ptr(), ld,
          _array(ids, "ids", torch.int32, T * top_k), _score(score), top_k, int(renormalise), scale,
-         out.data_ptr(), E, _stream(stream))
+         out.data_ptr(), E, _stream(stream, logits))
     return out
 
 
@@ -137,7 +149,7 @@ def moe_plan(ids, experts, stream=None):
     where = torch.empty((T, top_k), dtype=torch.int32, device=ids.device)
     offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
     _run("gemm_moe_plan", T, experts, top_k, addr, offsets.data_ptr(), tokens.data_ptr(),
-         where.data_ptr(), _stream(stream))
+         where.data_ptr(), _stream(stream, ids))
     return offsets, tokens, where
 
 
@@ -150,7 +162,7 @@ def moe_dispatch(x, where, weights=None, stream=None):
     _run("gemm_moe_dispatch", _type(x, "x"), T, H, top_k, x.data_ptr(), ld,
          _array(where, "where", torch.int32, T * top_k),
          _array(weights, "weights", torch.float32, T * top_k), T * top_k, out.data_ptr(),
-         out.stride(0), _stream(stream))
+         out.stride(0), _stream(stream, x))
     return out
 
 
@@ -163,7 +175,7 @@ def moe_combine(rows, where, weights=None, out_dtype=None, stream=None):
     _run("gemm_moe_combine", _type(rows, "rows"), _type(y, "out_dtype"), T, H, top_k, rows.data_ptr(),
          ld, rows.shape[0], _array(where, "where", torch.int32),
          _array(weights, "weights", torch.float32, T * top_k), y.data_ptr(), y.stride(0),
-         _stream(stream))
+         _stream(stream, rows))
     return y
 
 
@@ -177,7 +189,7 @@ def moe_combine_backward(dy, rows, where, weights=None, stream=None):
     _run("gemm_moe_combine_backward", _type(dy, "dy"), _type(rows, "rows"), T, H, top_k, dy.data_ptr(),
          ldd, rows.data_ptr(), ldr, rows.shape[0], _array(where, "where", torch.int32, T * top_k),
          _array(weights, "weights", torch.float32, T * top_k), drows.data_ptr(), drows.stride(0),
-         dweights.data_ptr(), _stream(stream))
+         dweights.data_ptr(), _stream(stream, dy))
     return drows, dweights
 
 
@@ -190,7 +202,7 @@ def gated_silu_backward(pre, dh, stream=None):
     ldh = _matrix(dh, "dh", cols=two // 2, rows=rows)
     out = _padded(rows, two, pre.dtype, pre.device)
     _run("gemm_gated_silu_backward", _type(pre, "pre"), _type(dh, "dh"), rows, two // 2, pre.data_ptr(),
-         ldp, dh.data_ptr(), ldh, out.data_ptr(), out.stride(0), _stream(stream))
+         ldp, dh.data_ptr(), ldh, out.data_ptr(), out.stride(0), _stream(stream, pre))
     return out
 
 
@@ -220,11 +232,16 @@ def grouped_linear(x, w, offsets, *, rows=None, opW="T", gated=False, out_dtype=
     ldp = 0
     if pre is not None:
         ldp = _matrix(pre, "pre", cols=2 * N, rows=y_rows, dtype=x.dtype)
+    # space to lay gathered rows out in, where the library would use it
+    work = None
+    if rows is not None and y_rows > 64 * groups:
+        space = torch.empty(y_rows * ((K + 7) // 8 * 8), dtype=x.dtype, device=x.device)
+        work = space.data_ptr()
     _run("gemm_grouped_linear", _type(x, "x"), _type(y, "out_dtype"), groups,
          _array(offsets, "offsets", torch.int32, groups + 1), GEMM_OP_T if opW == "T" else GEMM_OP_N,
          int(gated), N, K, x.data_ptr(), ldx, x_rows, _array(rows, "rows", torch.int32), w.data_ptr(),
          ldw, w.stride(0), y.data_ptr(), y.stride(0), y_rows, 0 if pre is None else pre.data_ptr(), ldp,
-         _stream(stream))
+         work, _stream(stream, x))
     return y
 
 
@@ -237,7 +254,7 @@ def grouped_weight_grad(dy, x, offsets, *, out_dtype=torch.float32, stream=None)
     dw = torch.empty((groups, N, ld), dtype=out_dtype, device=dy.device)
     _run("gemm_grouped_weight_grad", _type(dy, "dy"), _type(dw, "out_dtype"), groups,
          _array(offsets, "offsets", torch.int32), N, K, dy.data_ptr(), ldd, x.data_ptr(), ldx,
-         dy.shape[0], dw.data_ptr(), ld, N * ld, _stream(stream))
+         dy.shape[0], dw.data_ptr(), ld, N * ld, _stream(stream, dy))
     return dw if ld == K else dw[:, :, :K]
 
 
@@ -264,5 +281,5 @@ def lora_linear(x, w, a, b, segments, adapters, *, scales=None, out_dtype=None, 
          w.data_ptr(), ldw, requests, _array(segments, "segments", torch.int32, requests + 1),
          _array(adapters, "adapters", torch.int32), count, R, a.data_ptr(), lda, a.stride(0),
          b.data_ptr(), ldb, b.stride(0), _array(scales, "scales", torch.float32, count), y.data_ptr(),
-         y.stride(0), work.data_ptr(), _stream(stream))
+         y.stride(0), work.data_ptr(), _stream(stream, x))
     return y

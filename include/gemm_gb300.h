@@ -414,7 +414,12 @@ GEMM_API gemm_status_t gemm_gated_silu_backward(gemm_type_t type, gemm_type_t dh
  *
  * offsets (groups + 1 values) must not decrease; values are clamped to [0, y_rows].  Y must not
  * overlap the inputs.  K == 0 writes zeros.
- * Alignment: X, W and pre 16-byte aligned, ldx, ldw, strideW and ldp multiples of 8 elements, Y
+ *
+ * work: y_rows * (K rounded up to a multiple of 8) elements of `type` for the call to use, or NULL.
+ * With it, gathered rows (rows not NULL) of more than 64 positions per group on average are laid
+ * out contiguously first, which is faster than gathering them in the product; the result is the
+ * same.
+ * Alignment: X, W, pre and work 16-byte aligned, ldx, ldw, strideW and ldp multiples of 8 elements, Y
  * 16-byte aligned with ldy a multiple of 8 (else GEMM_ERR_MISALIGNED); N and K are free.
  * Limits: groups <= 1024, y_rows and x_rows < 2^31, N and K < 2^24.
  */
@@ -423,7 +428,8 @@ GEMM_API gemm_status_t gemm_grouped_linear(gemm_type_t type, gemm_type_t y_type,
                                            int64_t N, int64_t K, const void *X, int64_t ldx,
                                            int64_t x_rows, const int32_t *rows, const void *W,
                                            int64_t ldw, int64_t strideW, void *Y, int64_t ldy,
-                                           int64_t y_rows, void *pre, int64_t ldp, void *stream);
+                                           int64_t y_rows, void *pre, int64_t ldp, void *work,
+                                           void *stream);
 
 /*
  * Weight gradient of the grouped linear layer: for every group
