@@ -8,27 +8,41 @@
 
 namespace gemm {
 
-cudaError_t allow_smem_once(const void *kernel, int bytes)
+namespace {
+// Sets a function attribute of a kernel on the current device unless `done` holds that it was set.
+// Open addressing over a fixed table, several times the number of kernels: no allocation, so no
+// exception can leave a C entry point.
+constexpr int kSlots = 512;
+cudaError_t set_once(std::atomic<uintptr_t> (&done)[kSlots], const void *kernel, cudaFuncAttribute attribute, int value)
 {
-    // Open addressing over a fixed table (a few dozen kernels): no allocation, so no exception.
-    constexpr int kSlots = 1024;
-    static std::atomic<uintptr_t> done[kSlots];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    // kernels are distinct host functions: their addresses differ by more than the device number
-    const uintptr_t key = reinterpret_cast<uintptr_t>(kernel) * 64 + uintptr_t(dev & 63);
+    // host functions start on 16-byte boundaries at least: the device number takes the low bits
+    const uintptr_t key = reinterpret_cast<uintptr_t>(kernel) * 4 + uintptr_t(dev & 63);
     for (int i = 0; i < kSlots; ++i) {
-        std::atomic<uintptr_t> &slot = done[(key / 64 + key + uintptr_t(i)) % kSlots];
+        std::atomic<uintptr_t> &slot = done[(key / 64 + key % 64 + uintptr_t(i)) % kSlots];
         uintptr_t held = slot.load(std::memory_order_acquire);
         if (held == key) return cudaSuccess;
         if (held != 0) continue;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        slot.compare_exchange_strong(held, key, std::memory_order_acq_rel);
-        return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, attribute, value);
+        if (e == cudaSuccess) slot.compare_exchange_strong(held, key, std::memory_order_acq_rel);
+        return e;
     }
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return cudaFuncSetAttribute(kernel, attribute, value);
+}
+}  // namespace
+
+cudaError_t allow_smem_once(const void *kernel, int bytes)
+{
+    static std::atomic<uintptr_t> done[kSlots];
+    return set_once(done, kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+cudaError_t allow_large_cluster_once(const void *kernel)
+{
+    static std::atomic<uintptr_t> done[kSlots];
+    return set_once(done, kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &call, cudaStream_t stream)

@@ -1,19 +1,19 @@
 // Routing to experts: scores, top-k within the kept groups, the plan that orders the slots by
 // expert, and the gradient of the weights (semantics: include/gemm_gb300.h).
 //
-// One warp routes one token.  Lane l holds the experts v * 32 + l in registers, so a row of logits
-// is read once in coalesced pieces; maxima, sums and the choice itself are warp reductions.  A
-// choice compares 32-bit keys (the fp32 value with its bits mapped to unsigned order, 0 for an
-// expert that is out), so one pick is two integer warp reductions: the largest key, then the lowest
-// index that has it.  The kernel is bound by reading the logits for many tokens and by the launch
-// for few.
+// One warp routes one token.  Lane l holds the experts V l .. V l + V - 1 in registers, read with
+// 16-byte loads where the row allows it; maxima, sums and the choice itself are warp reductions.  A
+// choice compares 32-bit keys (the fp32 value with its bits mapped to unsigned order, 0 for an expert
+// that is out), so one pick is one integer warp maximum and a ballot, whose lowest lane holds the
+// lowest index.  Runs of experts that are whole lanes, a power of two of them, are reduced by
+// shuffles, others through shared memory.  Bound by instructions, about 900 a token of 256 experts.
 //
-// The plan is a stable counting sort of the slots by expert in one launch: one cluster of up to 8
-// CTAs, every warp owning a contiguous run of slots and a histogram row of its own in shared
-// memory.  Pass 1 counts (match.any gives the lanes of a warp that hold the same expert), the
-// histograms are scanned over warps, CTAs (through distributed shared memory) and experts, pass 2
-// places every slot at the running count of its warp.  No atomics, so the order never varies.  With
-// few tokens the same launch routes them first (the warp's slots are then its own tokens').
+// The plan is a stable counting sort of the slots by expert in one launch: one cluster of CTAs, every
+// warp owning a contiguous run of slots and a histogram row of its own in shared memory.  Pass 1
+// counts (match.any gives the lanes of a warp that hold the same expert) and leaves each slot's rank
+// in its warp in `where`; the histograms are scanned over warps, CTAs (through distributed shared
+// memory) and experts; pass 2 adds them.  No atomics, so the order never varies.  With few tokens
+// the same launch routes them first (the warp's slots are then its own tokens').
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -26,9 +26,12 @@ namespace cg = cooperative_groups;
 namespace gemm {
 namespace {
 
-constexpr int kRouteWarps = 8;       // warps per CTA of the routing kernels
-constexpr int kPlanWarps = 16;       // warps per CTA of the plan kernel
-constexpr int kPlanMaxCluster = 8;   // portable cluster size
+constexpr int kRouteWarps = 8;  // warps per CTA of the routing kernels
+// Warps per CTA of the plan kernel and CTAs of its cluster.  The form that routes as well needs the
+// registers of 16 warps; the other takes all it can get (16 CTAs of 32 warps; 8 of 16 measured 38 us
+// on 131072 slots, see launch_plan_t).
+template <int V> constexpr int plan_warps = V > 0 ? 16 : 32;
+template <int V> constexpr int plan_cluster = V > 0 ? 8 : 16;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Unsigned order of fp32 values; NaN and -inf (out of the choice) are 0, below every other value.
@@ -52,26 +55,56 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ float load_logit(int type, const void *p, int64_t i)
+// Elements of this lane of row t.  `wide`: rows start on 16-byte boundaries.
+template <class T, int V>
+__device__ __forceinline__ void load_lane(const T *row, int E, int lane, bool wide, float (&x)[V])
 {
-    if (type == GEMM_TYPE_F32) return static_cast<const float *>(p)[i];
-    if (type == GEMM_TYPE_F16) return __half2float(static_cast<const __half *>(p)[i]);
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+    constexpr int kPiece = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
+    if (wide && lane * V + V <= E && kPiece * sizeof(T) == 16) {
+#pragma unroll
+        for (int v = 0; v < V; v += kPiece) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(row + lane * V + v));
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) x[v + i] = to_f32(reinterpret_cast<const T *>(&q)[i]);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = lane * V + v < E ? to_f32(row[lane * V + v]) : -INFINITY;
+    }
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_lane(T *row, int E, int lane, bool wide, const float (&x)[V])
+{
+    constexpr int kPiece = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
+    if (wide && lane * V + V <= E && kPiece * sizeof(T) == 16) {
+#pragma unroll
+        for (int v = 0; v < V; v += kPiece) {
+            uint4 q;
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) reinterpret_cast<T *>(&q)[i] = from_f32<T>(x[v + i]);
+            *reinterpret_cast<uint4 *>(row + lane * V + v) = q;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane * V + v < E) row[lane * V + v] = from_f32<T>(x[v]);
+    }
 }
 
 // This lane's logits of row t with masks applied: -inf where masked, +inf as the largest finite
 // value.
 template <int V>
-__device__ __forceinline__ void load_row(int type, const void *logits, int64_t ld, int64_t t, int E, int lane,
-                                         float (&x)[V])
+__device__ __forceinline__ void load_row(const RouteArgs &a, int64_t t, int lane, float (&x)[V])
 {
+    if (a.type == GEMM_TYPE_F32)
+        load_lane<float, V>(static_cast<const float *>(a.logits) + t * a.ld, a.E, lane, a.wide, x);
+    else if (a.type == GEMM_TYPE_F16)
+        load_lane<__half, V>(static_cast<const __half *>(a.logits) + t * a.ld, a.E, lane, a.wide, x);
+    else
+        load_lane<__nv_bfloat16, V>(static_cast<const __nv_bfloat16 *>(a.logits) + t * a.ld, a.E, lane, a.wide, x);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = v * 32 + lane;
-        float a = e < E ? load_logit(type, logits, t * ld + e) : -INFINITY;
-        if (isnan(a)) a = -INFINITY;
-        x[v] = fminf(a, FLT_MAX);
-    }
+    for (int v = 0; v < V; ++v) x[v] = isnan(x[v]) ? -INFINITY : fminf(x[v], FLT_MAX);
 }
 
 // Scores of the row; 0 for masked logits.
@@ -100,35 +133,32 @@ __device__ __forceinline__ void scores(int score, const float (&x)[V], float (&s
     }
 }
 
-// Routes token t with one warp.  `scratch`: E floats of shared memory of this warp.
+// Keys of the runs, on the first lane of each (`lanes` lanes a run) or on lane g for run g.
 template <int V>
-__device__ void route_token(const RouteArgs &a, int64_t t, int lane, float *scratch)
+__device__ __forceinline__ uint32_t run_keys(const RouteArgs &a, const float (&value)[V], int lane, int lanes, float *scratch)
 {
-    const int E = a.E;
-    float x[V], s[V];
-    load_row<V>(a.type, a.logits, a.ld, t, E, lane, x);
-    scores<V>(a.score, x, s);
-    uint32_t key[V];  // of the value the choice goes by
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = v * 32 + lane;
-        float c = x[v];
-        if (a.bias != nullptr && e < E && c > -INFINITY) c = s[v] + a.bias[e];
-        key[v] = e < E ? order_key(c) : 0u;
-    }
-    if (a.groups > 1) {
-        // Lane g takes run g: its group_top largest values.  The members are read from shared
-        // memory starting at a different one in every lane, so that the lanes hit different banks.
-        const int size = E / a.groups;
+    float b1 = -INFINITY, b2 = -INFINITY;
+    if (lanes > 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = v * 32 + lane;
-            if (e < E) scratch[e] = key[v] == 0u ? -INFINITY : a.bias != nullptr ? s[v] + a.bias[e] : s[v];
+            b2 = fmaxf(b2, fminf(b1, value[v]));
+            b1 = fmaxf(b1, value[v]);
         }
+        for (int o = 1; o < lanes; o <<= 1) {
+            const float c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
+            b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
+            b1 = fmaxf(b1, c1);
+        }
+        if (lane % lanes != 0) b1 = -INFINITY;
+    } else {
+        // Lane g takes run g.  The members are read starting at a different one in every lane, so
+        // that the lanes hit different banks.
+        const int size = a.E / a.groups;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane * V + v < a.E) scratch[lane * V + v] = value[v];
         __syncwarp();
-        uint32_t gkey = 0u;
         if (lane < a.groups) {
-            float b1 = -INFINITY, b2 = -INFINITY;
             int i = lane % size;
             for (int n = 0; n < size; ++n) {
                 const float c = scratch[lane * size + i];
@@ -136,47 +166,85 @@ __device__ void route_token(const RouteArgs &a, int64_t t, int lane, float *scra
                 b1 = fmaxf(b1, c);
                 if (++i == size) i = 0;
             }
-            gkey = order_key(a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1);
         }
-        uint32_t kept = 0u;
+        __syncwarp();  // scratch is read before the next token overwrites it
+    }
+    return order_key(a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1);
+}
+
+// Routes token t with one warp.  `scratch`: E floats of shared memory of this warp.
+template <int V>
+__device__ void route_token(const RouteArgs &a, int64_t t, int lane, float *scratch)
+{
+    const int E = a.E;
+    float x[V], s[V];
+    load_row<V>(a, t, lane, x);
+    scores<V>(a.score, x, s);
+    uint32_t key[V];  // of the value the choice goes by
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = lane * V + v;
+        float c = x[v];
+        if (a.bias != nullptr && e < E && c > -INFINITY) c = s[v] + __ldg(a.bias + e);
+        key[v] = e < E ? order_key(c) : 0u;
+    }
+    if (a.groups > 1) {
+        const int size = E / a.groups;
+        // whole lanes a run, a power of two of them: reduced by shuffles
+        const int lanes = size % V == 0 && ((size / V) & (size / V - 1)) == 0 ? size / V : 0;
+        float value[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane * V + v;
+            value[v] = key[v] == 0u ? -INFINITY : a.bias != nullptr ? s[v] + __ldg(a.bias + e) : s[v];
+        }
+        uint32_t gkey = run_keys<V>(a, value, lane, lanes, scratch);
+        uint32_t kept = 0u;  // bit of the lane that holds the run's key
         for (int n = 0; n < a.groups_kept; ++n) {
             const uint32_t best = __reduce_max_sync(kFull, gkey);
             if (best == 0u) break;
-            const int g = __ffs(__ballot_sync(kFull, gkey == best)) - 1;
-            kept |= 1u << g;
-            if (lane == g) gkey = 0u;
+            const int at = __ffs(__ballot_sync(kFull, gkey == best)) - 1;
+            kept |= 1u << at;
+            if (lane == at) gkey = 0u;
         }
+        if (lanes > 0) {
+            if (!((kept >> (lane & ~(lanes - 1))) & 1u)) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = v * 32 + lane;
-            if (e < E && !((kept >> (e / size)) & 1u)) key[v] = 0u;
+                for (int v = 0; v < V; ++v) key[v] = 0u;
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = lane * V + v;
+                if (e < E && !((kept >> (e / size)) & 1u)) key[v] = 0u;
+            }
         }
-        __syncwarp();  // scratch is read before the next token overwrites it
     }
     // Lane j keeps choice j.
     int my_id = -1;
     float my_s = 0.0f, sum = 0.0f;
     for (int j = 0; j < a.top_k; ++j) {
         uint32_t best = key[0];
-        int at = 0;
 #pragma unroll
-        for (int v = 1; v < V; ++v)
-            if (key[v] > best) {
-                best = key[v];
-                at = v;
-            }
+        for (int v = 1; v < V; ++v) best = max(best, key[v]);
         const uint32_t top = __reduce_max_sync(kFull, best);
         if (top == 0u) break;
-        const unsigned mine = best == top ? unsigned(at * 32 + lane) : 0xffffffffu;
-        const int e = int(__reduce_min_sync(kFull, mine));
+        const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+        int at = 0;
         float sv = 0.0f;
+        if (lane == owner) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (v * 32 + lane == e) {
-                sv = s[v];
-                key[v] = 0u;
-            }
-        sv = __shfl_sync(kFull, sv, e & 31);
+            for (int v = V - 1; v >= 0; --v)  // the lowest of equals
+                if (key[v] == top) {
+                    at = v;
+                    sv = s[v];
+                }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v == at) key[v] = 0u;
+        }
+        const int e = __shfl_sync(kFull, owner * V + at, owner);
+        sv = __shfl_sync(kFull, sv, owner);
         if (lane == j) {
             my_id = e;
             my_s = sv;
@@ -195,57 +263,67 @@ template <int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a)
 {
     extern __shared__ float route_smem[];
+    // the plan's kernel may take its place now; it waits for this one's choices
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kRouteWarps + warp;
     if (t < a.T) route_token<V>(a, t, lane, route_smem + warp * a.E);
 }
 
-// The plan (see the head of this file).  V > 0: the launch routes the tokens first.  Shared memory:
-// kPlanWarps x E histogram rows, E totals of this CTA, E bases, and for V > 0 kPlanWarps x E floats.
+// The plan (see the head of this file).  V > 0: the launch routes the tokens first.  Shared memory,
+// with W warps: W x E histogram rows, E totals of this CTA, E bases, and for V > 0 W x E floats.
 template <int V>
-__global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArgs a)
 {
     extern __shared__ uint32_t plan_smem[];
+    constexpr int kWarps = plan_warps<V>;
     const int E = a.E, k = a.top_k;
-    uint32_t *hist = plan_smem, *total = hist + kPlanWarps * E, *base = total + E;
-    __shared__ uint32_t warp_total[kPlanWarps];
+    uint32_t *hist = plan_smem, *total = hist + kWarps * E, *base = total + E;
+    __shared__ uint32_t warp_total[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t warps = int64_t(ranks) * kPlanWarps, w = int64_t(rank) * kPlanWarps + warp;
+    const int64_t warps = int64_t(ranks) * kWarps, w = int64_t(rank) * kWarps + warp;
     // this warp's tokens [t0, t1) and slots
     const int64_t t0 = a.T * w / warps, t1 = a.T * (w + 1) / warps;
     const int64_t s0 = t0 * k, s1 = t1 * k;
 
-    for (int i = threadIdx.x; i < kPlanWarps * E; i += blockDim.x) hist[i] = 0u;
+    for (int i = threadIdx.x; i < kWarps * E; i += blockDim.x) hist[i] = 0u;
     if constexpr (V > 0) {
         float *scratch = reinterpret_cast<float *>(base + E) + warp * E;
         for (int64_t t = t0; t < t1; ++t) route_token<V>(a, t, lane, scratch);
     }
+    // the choices come from the kernel ahead of this one, if it was launched so
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
 
     uint32_t *mine = hist + warp * E;
-    auto expert_of = [&](int64_t s) {
-        const int e = s < s1 ? a.ids[s] : -1;
-        return e >= 0 && e < E ? e : -1;
-    };
-    // slots 4 x 32 at a time, so that four loads are in flight
-    for (int64_t s = s0; s < s1; s += 128) {
-        int e[4];
+    // slots 8 x 32 at a time, so that their loads are in flight together
+    for (int64_t s = s0; s < s1; s += 256) {
+        int e[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = expert_of(s + 32 * i + lane);
+        for (int i = 0; i < 8; ++i) {
+            const int64_t slot = s + 32 * i + lane;
+            e[i] = slot < s1 ? a.ids[slot] : -1;
+            if (e[i] < 0 || e[i] >= E) e[i] = -1;
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
+            if (s + 32 * i >= s1) break;  // the same for the warp
+            const int64_t slot = s + 32 * i + lane;
             const unsigned same = __match_any_sync(kFull, e[i]);
-            if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
+            const uint32_t before = e[i] >= 0 ? mine[e[i]] : 0u;
             __syncwarp();
+            if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] = before + __popc(same);
+            __syncwarp();
+            if (slot < s1) a.where[slot] = e[i] >= 0 ? int32_t(before + __popc(same & ((1u << lane) - 1u))) : -1;
         }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         uint32_t run = 0;
 #pragma unroll
-        for (int i = 0; i < kPlanWarps; ++i) {
+        for (int i = 0; i < kWarps; ++i) {
             const uint32_t n = hist[i * E + e];
             hist[i * E + e] = run;
             run += n;
@@ -288,24 +366,22 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const RouteArgs a
         first += all[i];
     }
     __syncthreads();
-    for (int64_t s = s0; s < s1; s += 128) {
-        int e[4];
+    // where holds the ranks that this very thread wrote above
+    for (int64_t s = s0; s < s1; s += 256) {
+        int e[8], rank_in_warp[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = expert_of(s + 32 * i + lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             const int64_t slot = s + 32 * i + lane;
-            const unsigned same = __match_any_sync(kFull, e[i]);
-            if (e[i] >= 0) {
-                const uint32_t p = base[e[i]] + mine[e[i]] + __popc(same & ((1u << lane) - 1u));
-                a.where[slot] = int32_t(p);
-                a.tokens[p] = int32_t(slot / k);
-            } else if (slot < s1) {
-                a.where[slot] = -1;
-            }
-            __syncwarp();
-            if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] += __popc(same);
-            __syncwarp();
+            rank_in_warp[i] = slot < s1 ? a.where[slot] : -1;
+            e[i] = slot < s1 ? a.ids[slot] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t slot = s + 32 * i + lane;
+            if (rank_in_warp[i] < 0) continue;  // no slot, or none of the experts
+            const uint32_t p = base[e[i]] + mine[e[i]] + uint32_t(rank_in_warp[i]);
+            a.where[slot] = int32_t(p);
+            a.tokens[p] = int32_t(slot / k);
         }
     }
     cluster.sync();  // no CTA leaves while another may still read its totals
@@ -313,14 +389,14 @@ __global__ void __launch_bounds__(kPlanWarps * 32) plan_kernel(const RouteArgs a
 
 template <int V>
 __global__ void __launch_bounds__(kRouteWarps * 32)
-route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *ids, void *dlogits, int64_t ldd)
+route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *ids, void *dlogits, int64_t ldd, bool wide)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kRouteWarps + warp;
     if (t >= a.T) return;
     const int E = a.E, k = a.top_k;
     float x[V], s[V], ds[V];
-    load_row<V>(a.type, a.logits, a.ld, t, E, lane, x);
+    load_row<V>(a, t, lane, x);
     scores<V>(a.score, x, s);
 #pragma unroll
     for (int v = 0; v < V; ++v) ds[v] = 0.0f;
@@ -337,8 +413,8 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
         float sv = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (v * 32 + lane == e) sv = s[v];
-        sv = __shfl_sync(kFull, sv, e & 31);
+            if (lane * V + v == e) sv = s[v];
+        sv = __shfl_sync(kFull, sv, e >= 0 ? e / V : 0);
         if (lane == j && id >= 0) sel = sv;
     }
     float g = a.scale * dw;
@@ -353,7 +429,7 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
         const float gj = __shfl_sync(kFull, g, j);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (v * 32 + lane == e) ds[v] += gj;
+            if (lane * V + v == e) ds[v] += gj;
     }
     float mean = 0.0f;  // sum of ds * s; 0 by its definition when the weights are renormalised
     if (a.score == GEMM_SCORE_SOFTMAX && !a.renormalise) {
@@ -361,42 +437,54 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
         for (int v = 0; v < V; ++v) mean += ds[v] * s[v];
         mean = warp_sum(mean);
     }
+    float d[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = v * 32 + lane;
-        if (e >= E) continue;
         // a masked logit has score 0 and so gradient 0
-        float d = a.score == GEMM_SCORE_SOFTMAX ? s[v] * (ds[v] - mean) : ds[v] * s[v] * (1.0f - s[v]);
-        if (!(x[v] > -INFINITY)) d = 0.0f;
-        const int64_t i = t * ldd + e;
-        if (a.type == GEMM_TYPE_F32) static_cast<float *>(dlogits)[i] = d;
-        else if (a.type == GEMM_TYPE_F16) static_cast<__half *>(dlogits)[i] = __float2half_rn(d);
-        else static_cast<__nv_bfloat16 *>(dlogits)[i] = __float2bfloat16_rn(d);
+        d[v] = a.score == GEMM_SCORE_SOFTMAX ? s[v] * (ds[v] - mean) : ds[v] * s[v] * (1.0f - s[v]);
+        if (!(x[v] > -INFINITY)) d[v] = 0.0f;
     }
+    if (a.type == GEMM_TYPE_F32) store_lane<float, V>(static_cast<float *>(dlogits) + t * ldd, E, lane, wide, d);
+    else if (a.type == GEMM_TYPE_F16) store_lane<__half, V>(static_cast<__half *>(dlogits) + t * ldd, E, lane, wide, d);
+    else store_lane<__nv_bfloat16, V>(static_cast<__nv_bfloat16 *>(dlogits) + t * ldd, E, lane, wide, d);
 }
 
+// after: the launch may begin before the routing kernel ahead of it has ended.
 template <int V>
-cudaError_t launch_plan_t(const RouteArgs &a, cudaStream_t stream)
+cudaError_t launch_plan_t(const RouteArgs &a, bool after, cudaStream_t stream)
 {
-    const size_t smem = (size_t(kPlanWarps) + 2 + (V > 0 ? kPlanWarps : 0)) * size_t(a.E) * 4;
+    constexpr int kWarps = plan_warps<V>;
+    const size_t smem = (size_t(kWarps) + 2 + (V > 0 ? kWarps : 0)) * size_t(a.E) * 4;
     cudaError_t e = allow_smem_once(plan_kernel<V>, 140 * 1024);
     if (e != cudaSuccess) return e;
-    // CTAs enough that a warp has at most a few tokens to route, or 1024 slots to sort; a power of 2
-    const int64_t per_cta = V > 0 ? 2 * kPlanWarps : 1024;
+    // CTAs enough that a warp has at most a few tokens to route, or 256 slots to sort at once; a
+    // power of 2
+    const int64_t per_cta = V > 0 ? 2 * kWarps : 128 * kWarps;
     int ranks = 1;
-    while (ranks < kPlanMaxCluster && a.T * (V > 0 ? 1 : a.top_k) > ranks * per_cta) ranks *= 2;
+    while (ranks < plan_cluster<V> && a.T * (V > 0 ? 1 : a.top_k) > ranks * per_cta) ranks *= 2;
+    if (plan_cluster<V> > 8 && ranks > 8) {
+        e = allow_large_cluster_once(plan_kernel<V>);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ranks);
-    cfg.blockDim = dim3(kPlanWarps * 32);
+    cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ranks;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2]{};
+    int n = 0;
+    if (ranks > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = ranks;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (after) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
     e = cudaLaunchKernelEx(&cfg, plan_kernel<V>, a);
     if (e == cudaSuccess) count_launches();
     return e;
@@ -415,6 +503,11 @@ cudaError_t by_values_per_lane(int E, F f)
 
 }  // namespace
 
+static bool wide_rows(int type, const void *p, int64_t ld)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (type == GEMM_TYPE_F32 ? 4 : 8) == 0;
+}
+
 // Few tokens: one launch routes and plans (the routing then runs on the plan's 8 CTAs only, so
 // only up to kFusedTokens tokens, and E <= 256 so that two E-sized shared rows per warp fit).
 constexpr int64_t kFusedTokens = 512;
@@ -430,18 +523,20 @@ cudaError_t launch_plan(int64_t T, int E, int top_k, const int32_t *ids, int32_t
     a.offsets = offsets;
     a.tokens = tokens;
     a.where = where;
-    return launch_plan_t<0>(a, stream);
+    return launch_plan_t<0>(a, false, stream);
 }
 
-cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream)
+cudaError_t launch_route(const RouteArgs &call, cudaStream_t stream)
 {
+    RouteArgs a = call;
+    a.wide = wide_rows(a.type, a.logits, a.ld);
     const bool plan = a.offsets != nullptr;
     if (plan && (a.T == 0 || (a.T <= kFusedTokens && a.E <= 256))) {
         if (a.T == 0) return launch_plan(0, a.E, a.top_k, a.ids, a.offsets, a.tokens, a.where, stream);
-        if (a.E <= 32) return launch_plan_t<1>(a, stream);
-        if (a.E <= 64) return launch_plan_t<2>(a, stream);
-        if (a.E <= 128) return launch_plan_t<4>(a, stream);
-        return launch_plan_t<8>(a, stream);
+        if (a.E <= 32) return launch_plan_t<1>(a, false, stream);
+        if (a.E <= 64) return launch_plan_t<2>(a, false, stream);
+        if (a.E <= 128) return launch_plan_t<4>(a, false, stream);
+        return launch_plan_t<8>(a, false, stream);
     }
     if (a.T == 0) return cudaSuccess;
     const cudaError_t e = by_values_per_lane(a.E, [&](auto v) {
@@ -451,16 +546,19 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream)
     });
     if (e != cudaSuccess) return e;
     count_launches();
-    return plan ? launch_plan(a.T, a.E, a.top_k, a.ids, a.offsets, a.tokens, a.where, stream) : cudaSuccess;
+    return plan ? launch_plan_t<0>(a, true, stream) : cudaSuccess;
 }
 
-cudaError_t launch_route_backward(const RouteArgs &a, const float *dweights, const int32_t *ids, void *dlogits,
+cudaError_t launch_route_backward(const RouteArgs &call, const float *dweights, const int32_t *ids, void *dlogits,
                                   int64_t ldd, cudaStream_t stream)
 {
+    RouteArgs a = call;
+    a.wide = wide_rows(a.type, a.logits, a.ld);
+    const bool wide = wide_rows(a.type, dlogits, ldd);
     const cudaError_t e = by_values_per_lane(a.E, [&](auto v) {
         const unsigned blocks = unsigned((a.T + kRouteWarps - 1) / kRouteWarps);
         route_backward_kernel<decltype(v)::value>
-            <<<blocks, kRouteWarps * 32, 0, stream>>>(a, dweights, ids, dlogits, ldd);
+            <<<blocks, kRouteWarps * 32, 0, stream>>>(a, dweights, ids, dlogits, ldd, wide);
         return cudaGetLastError();
     });
     if (e == cudaSuccess) count_launches();

@@ -64,7 +64,7 @@ gemm_status_t gemm_moe_route(gemm_type_t type, int64_t T, int64_t E, const void 
     DeviceInfo dev;
     if ((s = usable(dev)) != GEMM_OK) return s;
     const RouteArgs a{type, T, int(E), logits, ld, bias, score, groups, groups_kept, group_top, top_k, renormalise != 0,
-                      scale, ids, weights, offsets, tokens, where};
+                      scale, ids, weights, offsets, tokens, where, false};
     return from_cuda(launch_route(a, static_cast<cudaStream_t>(stream)));
 }
 

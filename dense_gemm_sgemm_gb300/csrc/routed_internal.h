@@ -58,6 +58,13 @@ template <class... P> cudaError_t allow_smem_once(void (*kernel)(P...), int byte
     return allow_smem_once(reinterpret_cast<const void *>(kernel), bytes);
 }
 
+// Likewise lets `kernel` run in clusters of more than the portable 8 CTAs.
+cudaError_t allow_large_cluster_once(const void *kernel);
+template <class... P> cudaError_t allow_large_cluster_once(void (*kernel)(P...))
+{
+    return allow_large_cluster_once(reinterpret_cast<const void *>(kernel));
+}
+
 struct RouteArgs {
     int type;
     int64_t T;
@@ -70,6 +77,7 @@ struct RouteArgs {
     int32_t *ids;
     float *weights;
     int32_t *offsets, *tokens, *where;
+    bool wide;  // set by the launcher: rows of logits start on 16-byte boundaries
 };
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream);
 cudaError_t launch_plan(int64_t T, int E, int top_k, const int32_t *ids, int32_t *offsets, int32_t *tokens,
