@@ -45,16 +45,21 @@ cudaError_t allow_large_cluster_once(const void *kernel)
     return set_once(done, kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
-gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &call, cudaStream_t stream)
+bool takes_few_rows(const GroupedArgs &a)
 {
-    GroupedArgs a = call;
     const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;  // at most that many have rows
     // GEMM_GB300_GROUPED_FEW=n (sweeps only): the few-rows kernel up to n rows a group
     int64_t limit = 16;
     if (const char *v = std::getenv("GEMM_GB300_GROUPED_FEW"); v && v[0]) limit = std::atoi(v);
-    const bool few = a.opW == GEMM_OP_T && a.y_rows <= limit * groups;
+    return a.K == 0 || a.x_rows == 0 || (a.opW == GEMM_OP_T && a.y_rows <= limit * groups);
+}
+
+gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &call, cudaStream_t stream)
+{
+    GroupedArgs a = call;
+    const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;
     cudaError_t e = cudaSuccess;
-    if (few || a.K == 0 || a.x_rows == 0) {
+    if (takes_few_rows(a)) {
         e = launch_few_rows(dev, a, stream);
     } else {
         // Gathered rows: TMA takes 82 cycles for four of them, as long as the MMAs of a slice of 160

@@ -24,22 +24,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRowStride = 36;  // floats between tokens of a warp's partial tile: 8 t + g, no bank twice
 constexpr unsigned kFull = 0xffffffffu;
 
-template <class T>
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1)
-{
-    if constexpr (std::is_same<T, __half>::value)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // Weights are read once: no line of L1 for them.
 __device__ __forceinline__ uint4 load_stream(const void *p)
 {
@@ -47,19 +31,6 @@ __device__ __forceinline__ uint4 load_stream(const void *p)
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
-    return v;
-}
-
-// Elements [k, k + 8) of a row of K elements: zeros beyond K, nothing read there.
-template <class T> __device__ __forceinline__ uint4 load_tail(const T *row, int64_t k, int64_t K)
-{
-    if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4 *>(row + k));
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    const uint16_t *src = reinterpret_cast<const uint16_t *>(row);
-    uint16_t *dst = reinterpret_cast<uint16_t *>(&v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (k + i < K) dst[i] = __ldg(src + k + i);
     return v;
 }
 
@@ -230,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(const GroupedArgs a,
                 const int which = __ldcg(a.ad.which + p);
                 if (unsigned(which) < unsigned(a.ad.count)) {
                     const T *b = static_cast<const T *>(a.ad.b) + int64_t(which) * a.ad.strideb + feat * a.ad.ldb;
-                    const float *inner = a.ad.inner + p * a.ad.rank;
+                    const float *inner = static_cast<const float *>(a.ad.inner) + p * a.ad.rank;
                     for (int j = 0; j < a.ad.rank; j += 8) {
                         const uint4 q = load_tail(b, j, a.ad.rank);
                         const T *e = reinterpret_cast<const T *>(&q);
@@ -247,13 +218,28 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(const GroupedArgs a,
     if (a.ad.b != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// x = part 0 + part 1 + .. up to the last part's rounding.
+template <class T, int PARTS> __device__ __forceinline__ void split(float x, uint16_t (&part)[PARTS])
+{
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        const T a = from_f32<T>(x);
+        const float f = to_f32(a);
+        x = fabsf(f) < INFINITY ? x - f : 0.0f;  // an infinity is all in the first part
+        part[i] = reinterpret_cast<const uint16_t &>(a);
+    }
+}
+
 // Inner products of the adapters: inner[t][r] = scale * sum_k X[t][k] A_a[r][k] for 64 (16 MT) ranks
 // of up to 8 * NT tokens of one request, K split over the CTA's 8 warps.
 //
 // CTA i takes item i of an enumeration that needs no scan: cutting the tokens both at multiples of
 // 8 NT and at the request boundaries, request s has the items t = segments[s] / (8 NT) + s ..
 // segments[s + 1] / (8 NT) + s, so the request of item i is the last s whose first item is <= i.
-template <class T, int MT, int NT>
+//
+// PARTS = 0 writes the few-rows form of the inner products, else the tcgen05 form (InnerLayout), for
+// which 8 NT is 32.
+template <class T, int MT, int NT, int PARTS>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
 {
     extern __shared__ float parts[];  // kWarps x (8 NT) x stride
@@ -263,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     auto seg = [&](int q) { return clamp_to(__ldg(a.segments + q), a.T); };
-    if (blockIdx.y == 0) {  // tokens of no request
+    if (PARTS == 0 && blockIdx.y == 0) {  // tokens of no request
         if (blockIdx.x == 0)
             for (int t = threadIdx.x; t < seg(0); t += kThreads) a.which[t] = -1;
         if (blockIdx.x == gridDim.x - 1)
@@ -283,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     if (t0 >= t1) return;
     int ad = __ldg(a.adapters + lo);
     if (unsigned(ad) >= unsigned(a.n_adapters)) ad = -1;
-    if (blockIdx.y == 0)
+    if (PARTS == 0 && blockIdx.y == 0)
         for (int t = t0 + int(threadIdx.x); t < t1; t += kThreads) a.which[t] = ad;
     if (ad < 0) return;
 
@@ -314,12 +300,32 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     __syncthreads();
     const float scale = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
     const int ranks = min(16 * MT, a.R - r0);
-    for (int i = threadIdx.x; i < ranks * (t1 - t0); i += kThreads) {
-        const int r = i % ranks, n = i / ranks;
-        float v = 0.0f;
+    if constexpr (PARTS > 0) {
+        static_assert(kTokens == 32, "blocks of 32 tokens");
+        const InnerLayout in = inner_layout(a.T, a.requests, a.R, a.type, a.y_type);
+        uint16_t *plane = static_cast<uint16_t *>(a.planes) + int64_t(r0 / 64) * in.plane_rows * 64;
+        for (int i = threadIdx.x; i < 32 * 16 * MT; i += kThreads) {
+            const int r = i % (16 * MT), n = i / (16 * MT), t = t0 - tile * 32;  // tile's first own row
+            float v = 0.0f;
+            if (r < ranks && n >= t && n < t + t1 - t0) {
 #pragma unroll
-        for (int q = 0; q < kWarps; ++q) v += parts[(q * kTokens + n) * kStride + r];
-        a.inner[int64_t(t0 + n) * a.R + r0 + r] = scale * v;
+                for (int q = 0; q < kWarps; ++q) v += parts[(q * kTokens + n - t) * kStride + r];
+                v *= scale;
+            }
+            uint16_t part[PARTS];
+            split<T, PARTS>(v, part);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+                plane[int64_t(q) * in.blocks * in.plane_rows * 64 + (int64_t(item) * 32 + n) * 64 + r0 % 64 + r] = part[q];
+        }
+    } else {
+        for (int i = threadIdx.x; i < ranks * (t1 - t0); i += kThreads) {
+            const int r = i % ranks, n = i / ranks;
+            float v = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) v += parts[(q * kTokens + n) * kStride + r];
+            a.inner[int64_t(t0 + n) * a.R + r0 + r] = scale * v;
+        }
     }
 }
 
@@ -376,24 +382,32 @@ template <class T, class Y> cudaError_t few_rows_t(const DeviceInfo &dev, const 
     return go(std::integral_constant<int, 8>{});
 }
 
-template <class T, int MT, int NT> cudaError_t launch_shrink_t(const ShrinkArgs &a, cudaStream_t stream)
+template <class T, int MT, int NT, int PARTS> cudaError_t launch_shrink_t(const ShrinkArgs &a, cudaStream_t stream)
 {
     constexpr int kStride = MT <= 2 ? kRowStride : 68;
     const size_t smem = size_t(kWarps) * 8 * NT * kStride * sizeof(float);
-    auto *kernel = shrink_kernel<T, MT, NT>;
+    auto *kernel = shrink_kernel<T, MT, NT, PARTS>;
     const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned(a.T / (8 * NT) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
     return launch_after(kernel, grid, smem, stream, false, a);
 }
 
+template <class T, int NT, int PARTS> cudaError_t shrink_by_rank(const ShrinkArgs &a, cudaStream_t stream)
+{
+    if (a.R <= 16) return launch_shrink_t<T, 1, NT, PARTS>(a, stream);
+    if (a.R <= 32) return launch_shrink_t<T, 2, NT, PARTS>(a, stream);
+    return launch_shrink_t<T, 4, NT, PARTS>(a, stream);
+}
+
 template <class T> cudaError_t shrink_t(const ShrinkArgs &a, cudaStream_t stream)
 {
+    if (a.inner == nullptr) {
+        if (inner_layout(a.T, a.requests, a.R, a.type, a.y_type).parts == 2) return shrink_by_rank<T, 4, 2>(a, stream);
+        return shrink_by_rank<T, 4, 3>(a, stream);
+    }
     // requests of one or a few tokens: 8 at a time (a 32-token tile would read its X rows in vain)
-    const bool small = a.T <= 8 * int64_t(a.requests);
-    if (a.R <= 16) return small ? launch_shrink_t<T, 1, 1>(a, stream) : launch_shrink_t<T, 1, 4>(a, stream);
-    if (a.R <= 32) return small ? launch_shrink_t<T, 2, 1>(a, stream) : launch_shrink_t<T, 2, 4>(a, stream);
-    return small ? launch_shrink_t<T, 4, 1>(a, stream) : launch_shrink_t<T, 4, 4>(a, stream);
+    return a.T <= 8 * int64_t(a.requests) ? shrink_by_rank<T, 1, 0>(a, stream) : shrink_by_rank<T, 4, 0>(a, stream);
 }
 
 }  // namespace

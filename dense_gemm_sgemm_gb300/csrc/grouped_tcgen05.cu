@@ -13,9 +13,12 @@
 //   2-9   epilogue: one TMEM lane is one feature, so 32 tokens x 32 features pass through shared
 //         memory per warp and leave as 16-byte pieces of token rows.
 // gated: a CTA's 128 rows are 64 gate rows and their 64 up rows; the warps that hold a gate and its
-// up exchange halves through shared memory.  Adapters: the epilogue adds inner[token] . B[feature]
-// in fp32 while the tensor cores work on the next tile, so the low-rank product costs no MMA and
-// needs no tokens of one adapter in a row; the kernel ahead of it computes `inner` meanwhile.
+// up exchange halves through shared memory.  Adapters: behind a tile's last K slice come the slices
+// of its requests' low-rank products, B_a on the m side and the inner products on the n side, over the
+// columns of the request only (see TileRequests); the kernel ahead computes the inner products in
+// 16-bit parts that sum to them (launch_shrink).  On the CUDA cores of the epilogue this product was
+// bound by broadcasting the inner products from shared memory (8192 tokens, rank 64, 4096 x 4096:
+// 341 us), with mma.sync there by tcgen05, which goes first (371 us).
 //
 // Weight gradient.  dW_g[n][k] sums over the group's positions, the K dimension of this product,
 // both operands "transposed" (MN-major).  Slices are 64 positions; the last one of a group also holds
@@ -271,10 +274,21 @@ constexpr int kTokenWarp = 2 + kEpiWarps;
 constexpr int kThreads = 32 * (kTokenWarp + 1);
 constexpr int kPlain = 0, kGated = 1, kAdapted = 2;
 
-// The token rows as boxes of 128, 64, 32 and 16 rows; gathered: rows[0] has one-row boxes.
+// Rows as boxes of 128, 64, 32 and 16; gathered: rows[0] has one-row boxes.
 struct TokenMaps {
     CUtensorMap rows[4];
 };
+// Copies `count` rows (a multiple of 16, at most 128) from row `first`, in powers of two.
+__device__ __forceinline__ void load_rows(uint32_t dst, const TokenMaps &map, uint32_t bar, int column, int first, int count)
+{
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (count & (128 >> i)) {
+            tma_load_2d_pair(dst + 128u * at, &map.rows[i], bar, column, first + at);
+            at += 128 >> i;
+        }
+}
 
 struct LinearParams {
     const int32_t *offsets;
@@ -287,7 +301,11 @@ struct LinearParams {
     int bf16;
     void *pre;
     int64_t ldp;
-    Adapters ad;
+    // adapters: requests, and the planes of the inner products' parts (launch_shrink), each of
+    // plane_rows rows of 64 ranks
+    const int32_t *segments, *adapters;
+    int requests, n_adapters, rank, parts;
+    int plane_rows;
     unsigned int *status;
     uint64_t timeout_ns;
     int inject_stall;  // test hook: the producer never fills its first slice
@@ -355,104 +373,65 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile
 
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// Two fp32 multiply-adds in one instruction.
-__device__ __forceinline__ void fma2(float2 &c, float2 a, float2 b)
-{
-    asm("fma.rn.f32x2 %0, %1, %2, %0;"
-        : "+l"(reinterpret_cast<uint64_t &>(c))
-        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
-}
-
-// Ranks [r0, r0 + 32) of this lane's row of an adapter's B, zeros past the last rank.
-__device__ __forceinline__ void adapter_row(const LinearParams &p, int a, int64_t feature, int r0, float2 (&b)[16])
-{
-    const Adapters &ad = p.ad;
-    const uint16_t *row = static_cast<const uint16_t *>(ad.b) + int64_t(a) * ad.strideb + feature * ad.ldb;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        const int j0 = r0 + 8 * c;
-        if (feature < p.N) {
-            if (j0 + 8 <= ad.rank) {
-                q = __ldg(reinterpret_cast<const uint4 *>(row + j0));
-            } else {
-                uint16_t *e = reinterpret_cast<uint16_t *>(&q);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j0 + j < ad.rank) e[j] = __ldg(row + j0 + j);
-            }
+// The requests that share a tile's tokens and have an adapter, in order; the roles' warps walk them in
+// step, 32 requests looked up at a time.
+struct TileRequests {
+    const LinearParams &p;
+    int t0, t1, q0, lane;
+    unsigned left;
+    int lo, hi, ad;  // of request q0 + lane: its tokens within the tile and its adapter
+    __device__ __forceinline__ TileRequests(const LinearParams &params, const LinearUnit &x, int l)
+        : p(params), t0(x.first), t1(x.first + x.tokens), lane(l)
+    {
+        int a = 0, b = p.requests;  // first request that ends behind the tile's first token
+        while (a < b) {
+            const int mid = (a + b) / 2;
+            if (clamp_to(__ldg(p.segments + mid + 1), p.y_rows) <= t0) a = mid + 1;
+            else b = mid;
         }
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            b[4 * c + j] = p.bf16 ? make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u))
-                                  : __half22float2(reinterpret_cast<const __half2 &>(w[j]));
+        q0 = a;
+        look_up();
     }
-}
-
-__device__ __forceinline__ float adapter_dot(const float2 (&b)[16], const float *inner)
-{
-    const float4 *t = reinterpret_cast<const float4 *>(inner);
-    float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const float4 x = t[q];
-        fma2(s0, b[2 * q], make_float2(x.x, x.y));
-        fma2(s1, b[2 * q + 1], make_float2(x.z, x.w));
-    }
-    return (s0.x + s1.x) + (s0.y + s1.y);
-}
-
-// v[i] += inner[token i] . B[feature] of each token's adapter, 32 ranks at a time: the tokens' inner
-// products in the staging tile, this lane's row of B in registers.  Where the 32 tokens share one
-// adapter, as in a prompt, they are independent chains without a branch between them (16 packed
-// multiply-adds a token and 32 ranks); else the row is read again where the adapter changes.
-__device__ __forceinline__ void add_adapters(float (&v)[32], const LinearParams &p, float *tile, int lane, int first,
-                                             int tokens, int64_t feature)
-{
-    const Adapters &ad = p.ad;
-    int mine = -1;
-    if (lane < tokens) mine = __ldcg(ad.which + first + lane);
-    if (unsigned(mine) >= unsigned(ad.count)) mine = -1;
-    const unsigned live = __ballot_sync(kFull, mine >= 0);
-    if (live == 0u) return;
-    const int one = __shfl_sync(kFull, mine, __ffs(live) - 1);
-    const bool same = __all_sync(kFull, mine == one || lane >= tokens);
-    for (int r0 = 0; r0 < ad.rank; r0 += 32) {
-        __syncwarp();
-        const bool there = r0 + lane < ad.rank;
-        const float *src = ad.inner + int64_t(first) * ad.rank + r0 + lane;
-        float t[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) t[i] = there && (live >> i & 1u) ? __ldcg(src + i * ad.rank) : 0.0f;
-        float2 b[16];
-        adapter_row(p, one, feature, r0, b);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) tile[i * 32 + lane] = t[i];
-        __syncwarp();
-        if (same) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += adapter_dot(b, tile + i * 32);
-        } else {
-            int now = one;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int a = __shfl_sync(kFull, mine, i);
-                if (a < 0) continue;
-                if (a != now) {
-                    now = a;
-                    adapter_row(p, a, feature, r0, b);
-                }
-                v[i] += adapter_dot(b, tile + i * 32);
-            }
+    __device__ __forceinline__ void look_up()
+    {
+        const int q = q0 + lane;
+        lo = hi = 0;
+        ad = -1;
+        if (q < p.requests) {
+            lo = max(clamp_to(__ldg(p.segments + q), p.y_rows), t0);
+            hi = min(clamp_to(__ldg(p.segments + q + 1), p.y_rows), t1);
+            ad = __ldg(p.adapters + q);
         }
+        left = __ballot_sync(kFull, lo < hi && unsigned(ad) < unsigned(p.n_adapters));
+        more = __any_sync(kFull, q == q0 + 31 && q + 1 < p.requests && clamp_to(__ldg(p.segments + q + 1), p.y_rows) < t1);
     }
-}
+    bool more;
+    // Next request: its adapter, the columns [c0, c0 + n) of the tile that hold its tokens, multiples of
+    // 32, and the first of the rows of its inner products.
+    __device__ __forceinline__ bool next(int &adapter, int &c0, int &n, int &row)
+    {
+        while (left == 0u) {
+            if (!more) return false;
+            q0 += 32;
+            look_up();
+        }
+        const int at = __ffs(left) - 1;
+        left &= left - 1u;
+        adapter = __shfl_sync(kFull, ad, at);
+        const int b0 = __shfl_sync(kFull, lo, at) / 32, b1 = (__shfl_sync(kFull, hi, at) + 31) / 32;
+        c0 = b0 * 32 - t0;
+        n = (b1 - b0) * 32;
+        row = (b0 + q0 + at) * 32;
+        return true;
+    }
+};
 
 // W_MN: W stored K x N (features contiguous).
 template <int W_MN, int EPI, bool Y_F32>
 __global__ void __launch_bounds__(kThreads, 1)
-grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x, const LinearParams p)
+grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x,
+                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TokenMaps map_inner,
+                      const LinearParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const Shared sh(smem_raw, p.cap * 64);
@@ -464,6 +443,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
     const int units = sh.start[p.groups], unit0 = int(cluster_id_x()), step = int(cluster_count_x());
     constexpr int kFeatures = EPI == kGated ? 128 : 256;  // of a unit
+    const int blocks = EPI == kAdapted ? (p.rank + 63) / 64 : 0;  // of 64 ranks
 
     if (warp == 0) {
         // ---------------- weight producer (warps in step, one elected lane copying)
@@ -502,6 +482,24 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 __syncwarp();
                 ring.next();
             }
+            if (EPI == kAdapted && ok) {
+                TileRequests requests(p, x, lane);
+                int ad, c0, n, row;
+                while (ok && requests.next(ad, c0, n, row))
+                    for (int i = 0; i < p.parts * blocks; ++i) {
+                        ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                        if (__any_sync(kFull, !ok)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) {
+                            if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2u * (kStageA + uint32_t(n) * 64u));
+                            tma_load_3d_pair(sh.stage_a(ring.stage), &map_b, full0 + 8u * ring.stage, i % blocks * 64, f0, ad);
+                        }
+                        __syncwarp();
+                        ring.next();
+                    }
+            }
         }
         if (leader) finish_producer(sh, watch, ring, ok);
     } else if (warp == kTokenWarp) {
@@ -536,20 +534,35 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 const uint32_t full = full0 + 8u * ring.stage, b = sh.stage_b(ring.stage);
                 if (p.rows != nullptr) {
                     if (4 * lane < half) tma_gather4_pair(b + 512u * lane, &map_x.rows[0], full, kb * 64, from);
-                } else if (leader) {  // `half` rows in powers of two, largest first
-                    int at = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (half & (128 >> i)) {
-                            tma_load_2d_pair(b + 128u * at, &map_x.rows[i], full, kb * 64, row0 + at);
-                            at += 128 >> i;
-                        }
+                } else if (leader) {
+                    load_rows(b, map_x, full, kb * 64, row0, half);
                 }
                 __syncwarp();
                 ring.next();
             }
+            if (EPI == kAdapted && ok) {
+                // the inner products come from the kernel ahead of this one
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                TileRequests requests(p, x, lane);
+                int ad, c0, n, row;
+                while (ok && requests.next(ad, c0, n, row))
+                    for (int i = 0; i < p.parts * blocks; ++i) {
+                        ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                        if (__any_sync(kFull, !ok)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader)
+                            load_rows(sh.stage_b(ring.stage), map_inner, full0 + 8u * ring.stage, 0,
+                                      i * p.plane_rows + row + int(rank) * (n / 2), n / 2);
+                        __syncwarp();
+                        ring.next();
+                    }
+            }
         }
         if (leader && !ok) finish_producer(sh, watch, ring, false);
+        // a CTA without tiles of its own still orders this launch behind the one ahead of it
+        if (EPI == kAdapted) asm volatile("griddepcontrol.wait;" ::: "memory");
     } else if (warp == 1) {
         if (rank == 0) {
             // ---------------- MMA issuer: the warp in step, one elected lane issuing
@@ -585,6 +598,29 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     __syncwarp();
                     ring.next();
                 }
+                if (EPI == kAdapted && ok) {
+                    TileRequests requests(p, x, lane);
+                    int ad, c0, n, row;
+                    while (ok && requests.next(ad, c0, n, row)) {
+                        const uint32_t part_idesc = make_idesc(0, 0, n, 256) | fmt;
+                        for (int i = 0; i < p.parts * blocks; ++i) {
+                            ok = watch.wait(sh.full(ring.stage), ring.phase);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (leader) {
+                                const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
+                                const uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
+                                const int steps = (p.rank - i % blocks * 64 + 15) / 16;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (k < steps) umma_f16<true>(d + uint32_t(c0), a + k * kStepA, b + k * kStepB, part_idesc, 1u);
+                                commit_both(sh.empty(ring.stage));
+                            }
+                            __syncwarp();
+                            ring.next();
+                        }
+                    }
+                }
                 if (!ok) break;
                 if (leader) commit_both(sh.acc_full(acc));
                 if (++acc == 2) {
@@ -600,14 +636,12 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         uint8_t *tile = sh.epi + (warp - 2) * 4096;
         int acc = 0, group = 0;
         uint32_t acc_phase = 0;
-        // the adapters' inner products come from the kernel ahead of this one
-        if (EPI == kAdapted) asm volatile("griddepcontrol.wait;" ::: "memory");
         uint8_t *Y = static_cast<uint8_t *>(p.Y);
         const int64_t ldy = p.ldy * (Y_F32 ? 4 : 2);
         for (int u = unit0; u < units; u += step) {
             const LinearUnit x = linear_unit(p, sh, u, group);
             const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
-            if (epilogue_any(!got)) {
+            if (epilogue_any(!got)) {  // the warps give up together
                 watch.raise();
                 break;
             }
@@ -672,8 +706,6 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     float v[32];
                     __syncwarp();
                     tmem_ld_32(taddr + c, v);
-                    if (EPI == kAdapted)
-                        add_adapters(v, p, reinterpret_cast<float *>(tile), lane, x.first + c, min(32, x.tokens - c), f + lane);
                     store_tokens<Y_F32>(v, tile, lane, Y, ldy, x.first + c, x.tokens - c, f, p.N, p.bf16);
                 }
             }
@@ -1000,9 +1032,8 @@ template <class K> int resident_pairs(K *kernel, int threads, int dev, std::atom
     return n;
 }
 
-template <class K, class M, class P>
-cudaError_t launch_pairs(K *kernel, int threads, int64_t pairs, bool after, cudaStream_t stream, const CUtensorMap &a,
-                         const M &b, const P &p)
+template <class K, class... Args>
+cudaError_t launch_pairs(K *kernel, int threads, int64_t pairs, bool after, cudaStream_t stream, const Args &...args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(2 * pairs));
@@ -1018,7 +1049,7 @@ cudaError_t launch_pairs(K *kernel, int threads, int64_t pairs, bool after, cuda
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, b, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e == cudaSuccess) count_launches();
     return e;
 }
@@ -1081,6 +1112,16 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
                        shared_w ? w_rows * a.ldw : a.stridew);
     for (int i = 0; ok && i < (a.rows != nullptr ? 1 : 4); ++i)
         ok = make_map(&mx.rows[i], a.X, bf16, a.x_rows, a.K, a.ldx, a.rows != nullptr ? 1 : 128 >> i, 0, 0);
+    CUtensorMap mb;
+    TokenMaps mi;
+    std::memset(&mb, 0, sizeof(mb));
+    std::memset(&mi, 0, sizeof(mi));
+    if (EPI == kAdapted) {
+        const InnerLayout in = inner_layout(a.y_rows, a.ad.requests, a.ad.rank, a.type, a.y_type);
+        ok = ok && make_map(&mb, a.ad.b, bf16, a.N, a.ad.rank, a.ad.ldb, 128, a.ad.count, a.ad.count > 1 ? a.ad.strideb : a.N * a.ad.ldb);
+        for (int i = 0; ok && i < 4; ++i)
+            ok = make_map(&mi.rows[i], a.ad.inner, bf16, in.plane_rows * in.parts * in.blocks, 64, 64, 128 >> i, 0, 0);
+    }
     if (!ok) return cudaErrorInvalidValue;
     const int features = EPI == kGated ? 128 : 256;
     LinearParams p{};
@@ -1099,12 +1140,21 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
     p.bf16 = bf16;
     p.pre = a.pre;
     p.ldp = a.ldp;
-    p.ad = a.ad;
+    if (EPI == kAdapted) {
+        const InnerLayout in = inner_layout(a.y_rows, a.ad.requests, a.ad.rank, a.type, a.y_type);
+        p.segments = a.ad.segments;
+        p.adapters = a.ad.adapters;
+        p.requests = a.ad.requests;
+        p.n_adapters = a.ad.count;
+        p.rank = a.ad.rank;
+        p.parts = in.parts;
+        p.plane_rows = int(in.plane_rows);
+    }
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
     // no more pairs than there can be units
     const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles;
-    return launch_pairs(kernel, kThreads, most < pairs ? most : pairs, EPI == kAdapted, stream, mw, mx, p);
+    return launch_pairs(kernel, kThreads, most < pairs ? most : pairs, EPI == kAdapted, stream, mw, mx, mb, mi, p);
 }
 
 template <int W_MN, int EPI> cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)

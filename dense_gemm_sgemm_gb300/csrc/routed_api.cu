@@ -253,11 +253,19 @@ gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw_type, in
     return from_cuda(launch_weight_grad(dev, a, static_cast<cudaStream_t>(stream)));
 }
 
+int64_t gemm_lora_work_bytes(int64_t T, int64_t requests, int64_t R)
+{
+    if (T <= 0 || requests <= 0 || R <= 0 || T > kMaxDim24 || requests > kMaxDim24 || R > 128) return 0;
+    const int64_t few = 4 * T * (R + 1);
+    const int64_t many = inner_layout(T, requests, R, GEMM_TYPE_BF16, GEMM_TYPE_F32).bytes();
+    return few > many ? few : many;
+}
+
 gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, int64_t N, int64_t K, const void *X,
                                int64_t ldx, const void *W, int64_t ldw, int64_t requests, const int32_t *segments,
                                const int32_t *adapters, int64_t n_adapters, int64_t R, const void *A, int64_t lda,
                                int64_t strideA, const void *B, int64_t ldb, int64_t strideB, const float *scales, void *Y,
-                               int64_t ldy, float *work, void *stream)
+                               int64_t ldy, void *work, void *stream)
 {
     if (!is_type16(type) || (y_type != type && y_type != GEMM_TYPE_F32) || T < 0 || N < 0 || K < 0 || requests < 0 ||
         n_adapters < 0 || R < 0 || strideA < 0 || strideB < 0)
@@ -265,6 +273,7 @@ gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, 
     if (T > kMaxDim24 || N > kMaxDim24 || K > kMaxDim24 || requests > kMaxDim24 || n_adapters > kMaxInt || R > 128 ||
         strideA > kMaxStride || strideB > kMaxStride)
         return GEMM_ERR_UNSUPPORTED;
+    if (requests > 0 && (T / 32 + requests) * 32 * 6 > kMaxInt) return GEMM_ERR_UNSUPPORTED;
     const bool adapted = requests > 0 && n_adapters > 0 && R > 0 && K > 0;
     if (!ld_ok(ldx, K) || !ld_ok(ldw, K) || !ld_ok(ldy, N) || (adapted && (!ld_ok(lda, K) || !ld_ok(ldb, R))))
         return GEMM_ERR_INVALID_VALUE;
@@ -276,7 +285,7 @@ gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, 
         if (segments == nullptr || adapters == nullptr || A == nullptr || B == nullptr || work == nullptr)
             return GEMM_ERR_INVALID_VALUE;
         if (!tiled(A, lda) || !tiled(B, ldb) || strideA % 8 != 0 || strideB % 8 != 0 ||
-            !words(segments, adapters, scales, work))
+            !words(segments, adapters, scales) || !aligned(work, 16))
             return GEMM_ERR_MISALIGNED;
     }
     DeviceInfo dev;
@@ -286,12 +295,13 @@ gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, 
     GroupedArgs a{type, y_type, 1, nullptr, GEMM_OP_T, 0, N, K, X, ldx, T, nullptr, W, ldw, 0, Y, ldy, T, nullptr, 0,
                   Adapters{}, nullptr};
     if (adapted) {
-        int32_t *which = reinterpret_cast<int32_t *>(work + T * R);
+        const bool few = takes_few_rows(a);
+        int32_t *which = static_cast<int32_t *>(work) + T * R;
         const ShrinkArgs sh{type, T, K, X, ldx, int(requests), segments, adapters, int(n_adapters), int(R), A, lda, strideA,
-                            scales, work, which};
+                            scales, few ? static_cast<float *>(work) : nullptr, which, work, y_type};
         const cudaError_t e = launch_shrink(sh, st);
         if (e != cudaSuccess) return from_cuda(e);
-        a.ad = Adapters{B, ldb, strideB, int(R), int(n_adapters), work, which};
+        a.ad = Adapters{B, ldb, strideB, int(R), int(n_adapters), work, which, int(requests), segments, adapters};
     }
     return launch_grouped(dev, a, st);
 }

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "gemm_internal.h"
 
 namespace gemm {
@@ -45,6 +47,38 @@ template <> __device__ __forceinline__ void store8(float *p, const float (&v)[8]
 {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Elements [k, k + 8) of a 16-bit row of K elements, 16-byte aligned: zeros beyond K, nothing read there.
+template <class T> __device__ __forceinline__ uint4 load_tail(const T *row, int64_t k, int64_t K)
+{
+    if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4 *>(row + k));
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(row);
+    uint16_t *dst = reinterpret_cast<uint16_t *>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K) dst[i] = __ldg(src + k + i);
+    return v;
+}
+
+// c += A B with mma.sync m16n8k16, fp32 accumulation.  Lane (g, t) = (lane / 4, lane % 4) holds two
+// k each of A's rows g (a0, a2) and g + 8 (a1, a3), of B's column g (b0, b1), and of c the columns
+// 2 t, 2 t + 1 of rows g and g + 8.
+template <class T>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 1 / (1 + exp(-x)); 0 and 1 at the ends, no NaN for finite x.
@@ -97,12 +131,31 @@ cudaError_t launch_gated_silu_backward(int type, int dh_type, int64_t rows, int6
 
 // A product of a grouped linear layer or of a linear layer with adapters: positions are split into
 // groups by offsets (NULL: one group of all y_rows positions), every group has its own W.
+// The products scale * X A^T of each token with its adapter reach the second product in one of two
+// forms.  For the few-rows kernel: fp32, a row of `rank` for every token, and its adapter in `which`.
+// For the tcgen05 kernel: 16-bit parts that sum to the fp32 value, part i of 64 ranks in plane i *
+// blocks + block, rows of 64; tokens in blocks of 32, where block b of request q is rows 32 (b + q) ..
+// of a plane and tokens of other requests are zeros, so that one request's blocks are contiguous.
+struct InnerLayout {
+    int parts, blocks;
+    int64_t plane_rows;
+    __host__ __device__ int64_t bytes() const { return plane_rows * 128 * parts * blocks; }
+};
+// Parts: fp16's two hold 22 bits.  bf16's two hold 16, 2^8 times finer than a 16-bit output; an fp32
+// output takes three.
+__host__ __device__ inline InnerLayout inner_layout(int64_t tokens, int64_t requests, int64_t rank, int type, int y_type)
+{
+    return InnerLayout{type == GEMM_TYPE_BF16 && y_type == GEMM_TYPE_F32 ? 3 : 2, int((rank + 63) / 64),
+                       (tokens / 32 + requests) * 32};
+}
 struct Adapters {
-    const void *b;         // NULL: no adapters
+    const void *b;  // NULL: no adapters
     int64_t ldb, strideb;
     int rank, count;
-    const float *inner;    // y_rows x rank: scale * X A^T of each position's adapter
-    const int32_t *which;  // y_rows: adapter of each position, -1: none
+    const void *inner;
+    const int32_t *which;  // few-rows kernel: adapter of each position, -1: none
+    int requests;          // tcgen05 kernel
+    const int32_t *segments, *adapters;
 };
 struct GroupedArgs {
     int type, y_type;
@@ -129,6 +182,7 @@ cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
 cudaError_t launch_many_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 // X[rows[p]] to row p of `out`, for the positions of the groups.
 cudaError_t launch_gather(const GroupedArgs &a, void *out, int64_t ldo, cudaStream_t stream);
+bool takes_few_rows(const GroupedArgs &a);
 gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 
 struct WeightGradArgs {
@@ -156,8 +210,10 @@ struct ShrinkArgs {
     const void *A;
     int64_t lda, stridea;
     const float *scales;
-    float *inner;
+    float *inner;    // few-rows form, NULL: the other
     int32_t *which;
+    void *planes;    // tcgen05 form
+    int y_type;
 };
 cudaError_t launch_shrink(const ShrinkArgs &a, cudaStream_t stream);
 

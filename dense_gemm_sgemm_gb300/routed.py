@@ -276,7 +276,7 @@ def lora_linear(x, w, a, b, segments, adapters, *, scales=None, out_dtype=None, 
         raise ValueError(f"b: {count} adapters wanted, got {b.shape[0]}")
     requests = adapters.numel()
     y = _padded(T, N, out_dtype or dt, x.device)
-    work = torch.empty(T * (R + 1), dtype=torch.float32, device=x.device)
+    work = torch.empty(load().gemm_lora_work_bytes(T, requests, R), dtype=torch.uint8, device=x.device)
     _run("gemm_lora_linear", _type(x, "x"), _type(y, "out_dtype"), T, N, K, x.data_ptr(), ldx,
          w.data_ptr(), ldw, requests, _array(segments, "segments", torch.int32, requests + 1),
          _array(adapters, "adapters", torch.int32), count, R, a.data_ptr(), lda, a.stride(0),

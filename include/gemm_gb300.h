@@ -454,20 +454,26 @@ GEMM_API gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw
  * owns tokens segments[q] .. segments[q + 1] - 1 (requests + 1 values that do not decrease,
  * clamped to [0, T]) and uses adapter adapters[q]; an adapter outside [0, n_adapters) means none,
  * as does lying in no request.  scales: n_adapters floats, NULL: 1.  An adapter of a rank below R
- * is padded with zero rows of A_a.  The inner product X A^T stays in fp32.
+ * is padded with zero rows of A_a.
  *
- * work: T * (R + 1) floats for the call to use (not kept; NULL when there are no requests, no
- * adapters or R == 0).
- * Alignment: X, W, A, B, Y 16-byte aligned; ldx, ldw, lda, ldb, ldy, strideA, strideB multiples of
- * 8 elements.  Limits: R <= 128, T < 2^24, requests < 2^24, N and K < 2^24.
+ * The inner products scales[a] * X A^T are summed in fp32.  For many tokens they enter the second
+ * product as sums of 16-bit parts: of bf16 to 16 bits (24 when Y is fp32), of fp16 to 22 bits, where
+ * they share fp16's range (beyond 65504 infinite, below 2^-14 kept to 2^-25).
+ *
+ * work: gemm_lora_work_bytes(T, requests, R) bytes for the call to use (not kept; NULL when there are
+ * no requests, no adapters, or R or K is 0).
+ * Alignment: X, W, A, B, Y and work 16-byte aligned; ldx, ldw, lda, ldb, ldy, strideA, strideB
+ * multiples of 8 elements.  Limits: R <= 128, T < 2^24, requests < 2^24, N and K < 2^24, and
+ * (T / 32 + requests) * 32 * 6 < 2^31.
  */
+GEMM_API int64_t gemm_lora_work_bytes(int64_t T, int64_t requests, int64_t R);
 GEMM_API gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, int64_t N,
                                         int64_t K, const void *X, int64_t ldx, const void *W,
                                         int64_t ldw, int64_t requests, const int32_t *segments,
                                         const int32_t *adapters, int64_t n_adapters, int64_t R,
                                         const void *A, int64_t lda, int64_t strideA, const void *B,
                                         int64_t ldb, int64_t strideB, const float *scales, void *Y,
-                                        int64_t ldy, float *work, void *stream);
+                                        int64_t ldy, void *work, void *stream);
 
 #ifdef __cplusplus
 }
