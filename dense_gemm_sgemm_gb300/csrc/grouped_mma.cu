@@ -138,6 +138,10 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(const GroupedArgs a,
     constexpr int kTokens = 8 * NT;
     constexpr int kFeat = GATED ? 16 : 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+    // a linear layer with adapters follows their inner products' kernel, which waited itself: only those
+    // are waited for, below
+    if (a.ad.b == nullptr) chain_wait();
+    else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int group, first, rows;
     if (!nonempty_group(a, blockIdx.y, lane, group, first, rows)) return;
     const int block_feat = kWarps / ks * kFeat;
@@ -245,8 +249,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     extern __shared__ float parts[];  // kWarps x (8 NT) x stride
     constexpr int kTokens = 8 * NT;
     constexpr int kStride = MT <= 2 ? kRowStride : 68;
-    // the product that follows may start reading its weights now; it waits before it reads inner
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain_wait();  // the product that follows may start on its weights and rows; it waits for inner
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     auto seg = [&](int q) { return clamp_to(__ldg(a.segments + q), a.T); };
     if (PARTS == 0 && blockIdx.y == 0) {  // tokens of no request
@@ -329,25 +332,6 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     }
 }
 
-// Launch; `after`: the launch may begin before the one ahead of it on the stream has ended.
-template <class K, class... Args>
-cudaError_t launch_after(K *kernel, dim3 grid, size_t smem, cudaStream_t stream, bool after, Args... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = after ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (e == cudaSuccess) count_launches();
-    return e;
-}
-
 template <class T, class Y, int NT, bool GATED>
 cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, int64_t groups, int64_t depth, cudaStream_t stream)
 {
@@ -362,7 +346,7 @@ cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, int64_t
     const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned((runs + per - 1) / per), unsigned(groups), unsigned(depth));
-    return launch_after(kernel, grid, smem, stream, a.ad.b != nullptr, a, ks);
+    return launch_chained(kernel, grid, kThreads, smem, 1, stream, a, ks);
 }
 
 template <class T, class Y> cudaError_t few_rows_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
@@ -390,7 +374,7 @@ template <class T, int MT, int NT, int PARTS> cudaError_t launch_shrink_t(const 
     const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned(a.T / (8 * NT) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
-    return launch_after(kernel, grid, smem, stream, false, a);
+    return launch_chained(kernel, grid, kThreads, smem, 1, stream, a);
 }
 
 template <class T, int NT, int PARTS> cudaError_t shrink_by_rank(const ShrinkArgs &a, cudaStream_t stream)

@@ -172,8 +172,8 @@ struct Shared {
 static_assert(8 * (4 * kMaxStages + 5) <= kBarBytes - 16, "barrier area");
 
 // Barriers, the groups' first positions and first units, TMEM; ends with the pair in step.
-// units_of(rows): work units of a group of that many rows.
-template <class F>
+// units_of(rows): work units of a group of that many rows.  CHAIN: waits for the kernel ahead.
+template <bool CHAIN, class F>
 __device__ __forceinline__ uint32_t set_up(const Shared &sh, const int32_t *offsets, int groups, int64_t positions,
                                            F units_of)
 {
@@ -193,10 +193,13 @@ __device__ __forceinline__ uint32_t set_up(const Shared &sh, const int32_t *offs
         *sh.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int g = threadIdx.x; g <= groups; g += blockDim.x)
-        sh.first[g] = offsets != nullptr ? clamp_to(__ldg(offsets + g), positions) : g == 0 ? 0 : int(positions);
     cluster_sync();  // a pair allocates TMEM together, and its barriers exist before the peer uses them
     if (warp == 1) tmem_alloc<true>(smem_u32(const_cast<uint32_t *>(sh.tmem_slot)), kTmemCols);
+    if (CHAIN) chain_wait();
+    else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int g = threadIdx.x; g <= groups; g += blockDim.x)
+        sh.first[g] = offsets != nullptr ? clamp_to(__ldg(offsets + g), positions) : g == 0 ? 0 : int(positions);
+    __syncthreads();
     if (warp == 0) {
         int carry = 0;
         for (int g0 = 0; g0 < groups; g0 += 32) {
@@ -438,12 +441,12 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int cap = p.cap, ftiles = p.ftiles;
-    const uint32_t tmem = set_up(sh, p.offsets, p.groups, p.y_rows,
+    const uint32_t tmem = set_up<EPI != kAdapted>(sh, p.offsets, p.groups, p.y_rows,
                                  [=](int rows) { return (rows + cap - 1) / cap * ftiles; });
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
     const int units = sh.start[p.groups], unit0 = int(cluster_id_x()), step = int(cluster_count_x());
     constexpr int kFeatures = EPI == kGated ? 128 : 256;  // of a unit
-    const int blocks = EPI == kAdapted ? (p.rank + 63) / 64 : 0;  // of 64 ranks
+    const int blocks = EPI == kAdapted ? (p.rank + 63) / 64 : 1;  // of 64 ranks
 
     if (warp == 0) {
         // ---------------- weight producer (warps in step, one elected lane copying)
@@ -541,7 +544,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 ring.next();
             }
             if (EPI == kAdapted && ok) {
-                // the inner products come from the kernel ahead of this one
+                // the inner products come from the kernel ahead, which itself waited for what x comes from
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 TileRequests requests(p, x, lane);
                 int ad, c0, n, row;
@@ -760,7 +763,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
     const Shared sh(smem_raw, kMaxStageB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const uint32_t tmem = set_up(sh, p.offsets, p.groups, p.positions, [](int) { return 0; });
+    const uint32_t tmem = set_up<true>(sh, p.offsets, p.groups, p.positions, [](int) { return 0; });
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
     const int units = p.groups * p.ntiles * p.ktiles, unit0 = int(cluster_id_x()), step = int(cluster_count_x());
     constexpr uint32_t kSliceBytes = kStageA + kMaxStageB;
@@ -1032,28 +1035,6 @@ template <class K> int resident_pairs(K *kernel, int threads, int dev, std::atom
     return n;
 }
 
-template <class K, class... Args>
-cudaError_t launch_pairs(K *kernel, int threads, int64_t pairs, bool after, cudaStream_t stream, const Args &...args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(2 * pairs));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = after ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (e == cudaSuccess) count_launches();
-    return e;
-}
-
 // GEMM_GB300_TEST_INJECT_STALL: a producer never fills its first slice, and waits are short.
 void test_hooks(uint64_t &timeout_ns, int &inject_stall)
 {
@@ -1154,7 +1135,8 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
     test_hooks(p.timeout_ns, p.inject_stall);
     // no more pairs than there can be units
     const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles;
-    return launch_pairs(kernel, kThreads, most < pairs ? most : pairs, EPI == kAdapted, stream, mw, mx, mb, mi, p);
+    return launch_chained(kernel, dim3(unsigned(2 * (most < pairs ? most : pairs))), kThreads, kSmemBytes, 2, stream, mw, mx, mb,
+                          mi, p);
 }
 
 template <int W_MN, int EPI> cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
@@ -1207,7 +1189,8 @@ cudaError_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, c
     test_hooks(p.timeout_ns, p.inject_stall);
     const int64_t units = int64_t(a.groups) * p.ntiles * p.ktiles;
     if (units >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    return launch_pairs(kernel, kGradThreads, units < pairs ? units : pairs, false, stream, md, mx, p);
+    return launch_chained(kernel, dim3(unsigned(2 * (units < pairs ? units : pairs))), kGradThreads, kSmemBytes, 2, stream, md, mx,
+                          p);
 }
 
 }  // namespace gemm

@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kThreads)
 combine_kernel(int64_t T, int64_t cols, int k, const R *rows, int64_t ldr, int64_t positions, const int32_t *where,
                const float *weights, Y *y, int64_t ldy)
 {
+    chain_wait();
     const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
     const int64_t t = i / cols, c = (i - t * cols) * VEC;
     if (t >= T) return;
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(kThreads)
 dispatch_kernel(int64_t slots, int64_t cols, int k, const X *x, int64_t ldx, const R *rows, int64_t ldr,
                 int64_t positions, const int32_t *where, const float *weights, X *out, int64_t ldo, float *dweights)
 {
+    chain_wait();
     const int64_t s = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (s >= slots) return;
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(kThreads)
 gather_kernel(const int32_t *offsets, int groups, int64_t positions, const uint16_t *x, int64_t ldx, int64_t x_rows,
               const int32_t *rows, int64_t K, uint16_t *out, int64_t ldo)
 {
+    chain_wait();
     const int64_t p = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (p >= positions || p >= __ldg(offsets + groups)) return;
@@ -123,6 +126,7 @@ __global__ void __launch_bounds__(kThreads)
 gated_silu_backward_kernel(int64_t rows, int64_t cols, int64_t I, const X *pre, int64_t ldp, const D *dh, int64_t lddh,
                            X *dpre, int64_t lddp)
 {
+    chain_wait();
     const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
     const int64_t r = i / cols, c = (i - r * cols) * VEC;
     if (r >= rows) return;
@@ -166,12 +170,6 @@ template <class F> cudaError_t by_type(int type, F f)
 {
     return type == GEMM_TYPE_F32 ? f(float{}) : by_type16(type, f);
 }
-cudaError_t counted()
-{
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches();
-    return e;
-}
 // Grid of n threads or warps in CTAs of `per`; 2^31 CTAs are more than any memory holds rows for.
 bool grid_of(int64_t n, int64_t per, unsigned &blocks)
 {
@@ -195,9 +193,8 @@ cudaError_t launch_combine(int rows_type, int y_type, int64_t T, int64_t H, int 
             using R = decltype(r);
             using Y = decltype(o);
             auto *kernel = vec ? combine_kernel<R, Y, 8> : combine_kernel<R, Y, 1>;
-            kernel<<<blocks, kThreads, 0, stream>>>(T, cols, top_k, static_cast<const R *>(rows), ldr, positions, where,
+            return launch_chained(kernel, dim3(blocks), kThreads, 0, 1, stream, T, cols, top_k, static_cast<const R *>(rows), ldr, positions, where,
                                                     weights, static_cast<Y *>(y), ldy);
-            return counted();
         });
     });
 }
@@ -215,10 +212,9 @@ cudaError_t launch_dispatch(int type, int rows_type, int64_t T, int64_t H, int t
             using X = decltype(a);
             using R = decltype(r);
             auto *kernel = vec ? dispatch_kernel<X, R, 8> : dispatch_kernel<X, R, 1>;
-            kernel<<<blocks, kThreads, 0, stream>>>(T * top_k, cols, top_k, static_cast<const X *>(x), ldx,
+            return launch_chained(kernel, dim3(blocks), kThreads, 0, 1, stream, T * top_k, cols, top_k, static_cast<const X *>(x), ldx,
                                                     static_cast<const R *>(rows), ldr, positions, where, weights,
                                                     static_cast<X *>(out), ldo, dweights);
-            return counted();
         });
     });
 }
@@ -227,9 +223,8 @@ cudaError_t launch_gather(const GroupedArgs &a, void *out, int64_t ldo, cudaStre
 {
     unsigned blocks;
     if (!grid_of(a.y_rows, kThreads / 32, blocks)) return cudaErrorInvalidConfiguration;
-    gather_kernel<<<blocks, kThreads, 0, stream>>>(a.offsets, a.groups, a.y_rows, static_cast<const uint16_t *>(a.X), a.ldx,
+    return launch_chained(gather_kernel, dim3(blocks), kThreads, 0, 1, stream, a.offsets, a.groups, a.y_rows, static_cast<const uint16_t *>(a.X), a.ldx,
                                                    a.x_rows, a.rows, a.K, static_cast<uint16_t *>(out), ldo);
-    return counted();
 }
 
 cudaError_t launch_gated_silu_backward(int type, int dh_type, int64_t rows, int64_t I, const void *pre, int64_t ldp,
@@ -244,9 +239,8 @@ cudaError_t launch_gated_silu_backward(int type, int dh_type, int64_t rows, int6
         auto go = [&](auto d) {
             using D = decltype(d);
             auto *kernel = vec ? gated_silu_backward_kernel<X, D, 8> : gated_silu_backward_kernel<X, D, 1>;
-            kernel<<<blocks, kThreads, 0, stream>>>(rows, cols, I, static_cast<const X *>(pre), ldp,
+            return launch_chained(kernel, dim3(blocks), kThreads, 0, 1, stream, rows, cols, I, static_cast<const X *>(pre), ldp,
                                                     static_cast<const D *>(dh), lddh, static_cast<X *>(dpre), lddp);
-            return counted();
         };
         return dh_type == GEMM_TYPE_F32 ? go(float{}) : go(X{});
     });

@@ -263,8 +263,7 @@ template <int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a)
 {
     extern __shared__ float route_smem[];
-    // the plan's kernel may take its place now; it waits for this one's choices
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kRouteWarps + warp;
     if (t < a.T) route_token<V>(a, t, lane, route_smem + warp * a.E);
@@ -289,12 +288,11 @@ __global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArg
     const int64_t s0 = t0 * k, s1 = t1 * k;
 
     for (int i = threadIdx.x; i < kWarps * E; i += blockDim.x) hist[i] = 0u;
+    chain_wait();
     if constexpr (V > 0) {
         float *scratch = reinterpret_cast<float *>(base + E) + warp * E;
         for (int64_t t = t0; t < t1; ++t) route_token<V>(a, t, lane, scratch);
     }
-    // the choices come from the kernel ahead of this one, if it was launched so
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
 
     uint32_t *mine = hist + warp * E;
@@ -391,6 +389,7 @@ template <int V>
 __global__ void __launch_bounds__(kRouteWarps * 32)
 route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *ids, void *dlogits, int64_t ldd, bool wide)
 {
+    chain_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * kRouteWarps + warp;
     if (t >= a.T) return;
@@ -449,9 +448,8 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
     else store_lane<__nv_bfloat16, V>(static_cast<__nv_bfloat16 *>(dlogits) + t * ldd, E, lane, wide, d);
 }
 
-// after: the launch may begin before the routing kernel ahead of it has ended.
 template <int V>
-cudaError_t launch_plan_t(const RouteArgs &a, bool after, cudaStream_t stream)
+cudaError_t launch_plan_t(const RouteArgs &a, cudaStream_t stream)
 {
     constexpr int kWarps = plan_warps<V>;
     const size_t smem = (size_t(kWarps) + 2 + (V > 0 ? kWarps : 0)) * size_t(a.E) * 4;
@@ -466,28 +464,7 @@ cudaError_t launch_plan_t(const RouteArgs &a, bool after, cudaStream_t stream)
         e = allow_large_cluster_once(plan_kernel<V>);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ranks);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2]{};
-    int n = 0;
-    if (ranks > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = ranks;
-        attr[n].val.clusterDim.y = 1;
-        attr[n++].val.clusterDim.z = 1;
-    }
-    if (after) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    e = cudaLaunchKernelEx(&cfg, plan_kernel<V>, a);
-    if (e == cudaSuccess) count_launches();
-    return e;
+    return launch_chained(plan_kernel<V>, dim3(ranks), kWarps * 32, smem, ranks, stream, a);
 }
 
 template <class F>
@@ -523,7 +500,7 @@ cudaError_t launch_plan(int64_t T, int E, int top_k, const int32_t *ids, int32_t
     a.offsets = offsets;
     a.tokens = tokens;
     a.where = where;
-    return launch_plan_t<0>(a, false, stream);
+    return launch_plan_t<0>(a, stream);
 }
 
 cudaError_t launch_route(const RouteArgs &call, cudaStream_t stream)
@@ -533,20 +510,19 @@ cudaError_t launch_route(const RouteArgs &call, cudaStream_t stream)
     const bool plan = a.offsets != nullptr;
     if (plan && (a.T == 0 || (a.T <= kFusedTokens && a.E <= 256))) {
         if (a.T == 0) return launch_plan(0, a.E, a.top_k, a.ids, a.offsets, a.tokens, a.where, stream);
-        if (a.E <= 32) return launch_plan_t<1>(a, false, stream);
-        if (a.E <= 64) return launch_plan_t<2>(a, false, stream);
-        if (a.E <= 128) return launch_plan_t<4>(a, false, stream);
-        return launch_plan_t<8>(a, false, stream);
+        if (a.E <= 32) return launch_plan_t<1>(a, stream);
+        if (a.E <= 64) return launch_plan_t<2>(a, stream);
+        if (a.E <= 128) return launch_plan_t<4>(a, stream);
+        return launch_plan_t<8>(a, stream);
     }
     if (a.T == 0) return cudaSuccess;
     const cudaError_t e = by_values_per_lane(a.E, [&](auto v) {
         const unsigned blocks = unsigned((a.T + kRouteWarps - 1) / kRouteWarps);
-        route_kernel<decltype(v)::value><<<blocks, kRouteWarps * 32, size_t(kRouteWarps) * a.E * 4, stream>>>(a);
-        return cudaGetLastError();
+        return launch_chained(route_kernel<decltype(v)::value>, dim3(blocks), kRouteWarps * 32,
+                              size_t(kRouteWarps) * a.E * 4, 1, stream, a);
     });
     if (e != cudaSuccess) return e;
-    count_launches();
-    return plan ? launch_plan_t<0>(a, true, stream) : cudaSuccess;
+    return plan ? launch_plan_t<0>(a, stream) : cudaSuccess;
 }
 
 cudaError_t launch_route_backward(const RouteArgs &call, const float *dweights, const int32_t *ids, void *dlogits,
@@ -555,14 +531,11 @@ cudaError_t launch_route_backward(const RouteArgs &call, const float *dweights, 
     RouteArgs a = call;
     a.wide = wide_rows(a.type, a.logits, a.ld);
     const bool wide = wide_rows(a.type, dlogits, ldd);
-    const cudaError_t e = by_values_per_lane(a.E, [&](auto v) {
+    return by_values_per_lane(a.E, [&](auto v) {
         const unsigned blocks = unsigned((a.T + kRouteWarps - 1) / kRouteWarps);
-        route_backward_kernel<decltype(v)::value>
-            <<<blocks, kRouteWarps * 32, 0, stream>>>(a, dweights, ids, dlogits, ldd, wide);
-        return cudaGetLastError();
+        return launch_chained(route_backward_kernel<decltype(v)::value>, dim3(blocks), kRouteWarps * 32, 0, 1, stream, a,
+                              dweights, ids, dlogits, ldd, wide);
     });
-    if (e == cudaSuccess) count_launches();
-    return e;
 }
 
 }  // namespace gemm

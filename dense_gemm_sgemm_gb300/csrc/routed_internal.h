@@ -11,6 +11,36 @@
 
 namespace gemm {
 
+// The routed products' kernels follow one another closely: each is launched so that it may take its
+// place on the SMs before the kernel ahead of it on the stream has ended, and begins with
+// chain_wait(), which returns once that kernel has ended and its writes are visible, and which lets
+// the next kernel take its place in turn.  Before it a kernel may only set up its own SM.
+__device__ __forceinline__ void chain_wait()
+{
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class K, class... Args>
+cudaError_t launch_chained(K *kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const Args &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) count_launches();
+    return e;
+}
+
 // 16-bit storage types and their conversions; everything is computed in fp32.
 template <class T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32(float v) { return v; }

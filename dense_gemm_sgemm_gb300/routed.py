@@ -24,78 +24,102 @@ __all__ = [
     "lora_linear",
 ]
 
+_F32, _I32 = torch.float32, torch.int32
 _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _SCORE = {"softmax": 0, "sigmoid": 1}
+# the raw handle: building a torch.cuda.Stream for every call costs as much as a launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-_calls = {}
+class _Calls:
+    """The library's functions, each looked up at its first call."""
+
+    def __getattr__(self, name):
+        fn = getattr(load(), name)
+        setattr(self, name, fn)
+        return fn
 
 
-def _run(name, *args):
-    call = _calls.get(name)
-    if call is None:
-        call = _calls[name] = getattr(load(), name)
-    status = call(*args)
-    if status != 0:
-        raise GemmError(status, name)
+_lib = _Calls()
+
+
+def _raise(status, name):
+    raise GemmError(status, name)
 
 
 def _stream(stream, tensor):
-    """The given stream, or the current one of the tensor's device (the raw handle: building a
-    torch.cuda.Stream costs as much as the launch)."""
+    """The given stream, or the current one of the tensor's device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(tensor.get_device())
+        return _raw_stream(tensor.get_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _type(t, what):
-    try:
-        return _TYPE[t.dtype]
-    except KeyError:
-        raise TypeError(f"{what}: fp32, fp16 or bf16 wanted, got {t.dtype}") from None
+# The checks' first lines are one condition each: a decoding step's calls are bound by the host.
+def _type(dtype, what):
+    kind = _TYPE.get(dtype)
+    if kind is None:
+        raise TypeError(f"{what}: fp32, fp16 or bf16 wanted, got {dtype}")
+    return kind
 
 
-def _matrix(t, what, cols=None, rows=None, dtype=None, dims=2):
-    """Leading dimension of a CUDA tensor with unit column stride (dims = 3: a stack of them)."""
+def _refuse(t, what, dims):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: a torch tensor is wanted")
     if not t.is_cuda:
         raise ValueError(f"{what}: must live in CUDA device memory")
+    raise ValueError(f"{what}: {dims}-D with unit column stride wanted")
+
+
+def _matrix(t, what, dims=2):
+    """(shape, leading dimension) of a CUDA matrix, or stack of them, with unit column stride."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == dims):
+        _refuse(t, what, dims)
     shape, strides = t.shape, t.stride()
-    if len(shape) != dims or (shape[-1] > 1 and strides[-1] != 1):
-        raise ValueError(f"{what}: {dims}-D with unit column stride wanted")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if cols is not None and shape[-1] != cols:
-        raise ValueError(f"{what}: {cols} columns wanted, got {shape[-1]}")
-    if rows is not None and shape[-2] != rows:
-        raise ValueError(f"{what}: {rows} rows wanted, got {shape[-2]}")
+    if strides[-1] != 1 and shape[-1] > 1:
+        _refuse(t, what, dims)
     ld = strides[-2]
-    # the stride of a single row means nothing
-    return ld if shape[-2] > 1 else max(ld, shape[-1], 1)
+    if shape[-2] <= 1:  # the stride of a single row means nothing
+        ld = max(ld, shape[-1], 1)
+    return shape, ld
 
 
-def _array(t, what, dtype, count=None):
-    if t is None:
-        return 0
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: a torch tensor is wanted")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: must live in CUDA device memory")
+def _same(got, wanted, what):
+    if got != wanted:
+        raise ValueError(f"{what}: {wanted} wanted, got {got}")
+
+
+def _same_type(t, dtype, what):
     if t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+
+
+def _array(t, what, dtype, count):
+    """Address of a contiguous CUDA array of `count` values."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and t.numel() == count):
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: a torch tensor is wanted")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: must live in CUDA device memory")
+    _same_type(t, dtype, what)
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
-    if count is not None and t.numel() != count:
-        raise ValueError(f"{what}: {count} values wanted, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{what}: {count} values wanted, got {t.numel()}")
 
 
 def _padded(rows, cols, dtype, device):
-    """Matrix whose rows start on 16-byte boundaries (leading dimension a multiple of 8)."""
-    ld = (cols + 7) // 8 * 8
+    """(matrix, leading dimension): rows start on 16-byte boundaries, multiples of 8 elements."""
+    ld = (cols + 7) & ~7
     t = torch.empty((rows, ld), dtype=dtype, device=device)
-    return t if ld == cols else t[:, :cols]
+    return (t, ld) if ld == cols else (t[:, :cols], ld)
+
+
+def _score(score):
+    kind = _SCORE.get(score)
+    if kind is None:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return kind
 
 
 def moe_route(logits, top_k, *, bias=None, score="softmax", groups=1, groups_kept=1, group_top=1,
@@ -105,104 +129,117 @@ def moe_route(logits, top_k, *, bias=None, score="softmax", groups=1, groups_kep
     logits T x E (fp32, fp16 or bf16); ids int32 and weights fp32 are T x top_k; offsets (E + 1),
     tokens and where are the plan (gemm_moe_route).
     """
-    ld = _matrix(logits, "logits")
-    T, E = logits.shape
-    dev = logits.device
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    where = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    tokens = torch.empty(T * top_k, dtype=torch.int32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    _run("gemm_moe_route", _type(logits, "logits"), T, E, logits.data_ptr(), ld,
-         _array(bias, "bias", torch.float32, E), _score(score), groups, groups_kept, group_top, top_k,
-         int(renormalise), scale, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-         tokens.data_ptr(), where.data_ptr(), _stream(stream, logits))
+    (T, E), ld = _matrix(logits, "logits")
+    bias = None if bias is None else _array(bias, "bias", _F32, E)
+    # one allocation, five views: a view costs half of an allocation and its release
+    shape, rows, slots = (T, top_k), (top_k, 1), T * top_k
+    space = torch.empty(4 * slots + E + 1, dtype=_I32, device=logits.device)
+    weights = space.view(_F32).as_strided(shape, rows, 0)
+    ids = space.as_strided(shape, rows, slots)
+    where = space.as_strided(shape, rows, 2 * slots)
+    tokens = space.as_strided((slots,), (1,), 3 * slots)
+    offsets = space.as_strided((E + 1,), (1,), 4 * slots)
+    at = space.data_ptr()
+    status = _lib.gemm_moe_route(
+        _type(logits.dtype, "logits"), T, E, logits.data_ptr(), ld, bias, _score(score), groups,
+        groups_kept, group_top, top_k, renormalise, scale, at + 4 * slots, at, at + 16 * slots,
+        at + 12 * slots, at + 8 * slots, _stream(stream, logits))
+    if status:
+        _raise(status, "gemm_moe_route")
     return ids, weights, offsets, tokens, where
-
-
-def _score(score):
-    try:
-        return _SCORE[score]
-    except KeyError:
-        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}") from None
 
 
 def moe_route_backward(dweights, logits, ids, *, score="softmax", renormalise=True, scale=1.0,
                        stream=None):
     """Gradient of moe_route's weights with respect to the logits, ids held fixed."""
-    ld = _matrix(logits, "logits")
-    T, E = logits.shape
+    (T, E), ld = _matrix(logits, "logits")
     top_k = ids.shape[1]
     out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _run("gemm_moe_route_backward", _type(logits, "logits"), T, E,
-         _array(dweights, "dweights", torch.float32, T * top_k), logits.data_ptr(), ld,
-         _array(ids, "ids", torch.int32, T * top_k), _score(score), top_k, int(renormalise), scale,
-         out.data_ptr(), E, _stream(stream, logits))
+    status = _lib.gemm_moe_route_backward(
+        _type(logits.dtype, "logits"), T, E, _array(dweights, "dweights", _F32, T * top_k),
+        logits.data_ptr(), ld, _array(ids, "ids", _I32, T * top_k), _score(score), top_k, renormalise,
+        scale, out.data_ptr(), E, _stream(stream, logits))
+    if status:
+        _raise(status, "gemm_moe_route_backward")
     return out
 
 
 def moe_plan(ids, experts, stream=None):
     """(offsets, tokens, where) of given choices ids (T x k int32; -1: none)."""
-    addr = _array(ids, "ids", torch.int32)
-    T, top_k = ids.shape
-    tokens = torch.empty(T * top_k, dtype=torch.int32, device=ids.device)
-    where = torch.empty((T, top_k), dtype=torch.int32, device=ids.device)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-    _run("gemm_moe_plan", T, experts, top_k, addr, offsets.data_ptr(), tokens.data_ptr(),
-         where.data_ptr(), _stream(stream, ids))
+    (T, top_k), _ = _matrix(ids, "ids")
+    tokens = torch.empty(T * top_k, dtype=_I32, device=ids.device)
+    where = torch.empty((T, top_k), dtype=_I32, device=ids.device)
+    offsets = torch.empty(experts + 1, dtype=_I32, device=ids.device)
+    status = _lib.gemm_moe_plan(T, experts, top_k, _array(ids, "ids", _I32, T * top_k), offsets.data_ptr(),
+                                tokens.data_ptr(), where.data_ptr(), _stream(stream, ids))
+    if status:
+        _raise(status, "gemm_moe_plan")
     return offsets, tokens, where
 
 
 def moe_dispatch(x, where, weights=None, stream=None):
     """Rows of x (T x H) at the positions of their slots, times the slots' weights if given."""
-    ld = _matrix(x, "x")
-    T, H = x.shape
+    (T, H), ld = _matrix(x, "x")
     top_k = where.shape[1]
-    out = _padded(T * top_k, H, x.dtype, x.device)
-    _run("gemm_moe_dispatch", _type(x, "x"), T, H, top_k, x.data_ptr(), ld,
-         _array(where, "where", torch.int32, T * top_k),
-         _array(weights, "weights", torch.float32, T * top_k), T * top_k, out.data_ptr(),
-         out.stride(0), _stream(stream, x))
+    slots = T * top_k
+    out, ldo = _padded(slots, H, x.dtype, x.device)
+    status = _lib.gemm_moe_dispatch(
+        _type(x.dtype, "x"), T, H, top_k, x.data_ptr(), ld, _array(where, "where", _I32, slots),
+        None if weights is None else _array(weights, "weights", _F32, slots), slots, out.data_ptr(), ldo,
+        _stream(stream, x))
+    if status:
+        _raise(status, "gemm_moe_dispatch")
     return out
 
 
 def moe_combine(rows, where, weights=None, out_dtype=None, stream=None):
     """y[t] = sum over j of weights[t, j] * rows[where[t, j]] (weights None: 1)."""
-    ld = _matrix(rows, "rows")
+    (positions, H), ld = _matrix(rows, "rows")
     T, top_k = where.shape
-    H = rows.shape[1]
-    y = _padded(T, H, out_dtype or rows.dtype, rows.device)
-    _run("gemm_moe_combine", _type(rows, "rows"), _type(y, "out_dtype"), T, H, top_k, rows.data_ptr(),
-         ld, rows.shape[0], _array(where, "where", torch.int32),
-         _array(weights, "weights", torch.float32, T * top_k), y.data_ptr(), y.stride(0),
-         _stream(stream, rows))
+    slots = T * top_k
+    out_dtype = out_dtype or rows.dtype
+    y, ldy = _padded(T, H, out_dtype, rows.device)
+    status = _lib.gemm_moe_combine(
+        _type(rows.dtype, "rows"), _type(out_dtype, "out_dtype"), T, H, top_k, rows.data_ptr(), ld,
+        positions, _array(where, "where", _I32, slots),
+        None if weights is None else _array(weights, "weights", _F32, slots), y.data_ptr(), ldy,
+        _stream(stream, rows))
+    if status:
+        _raise(status, "gemm_moe_combine")
     return y
 
 
 def moe_combine_backward(dy, rows, where, weights=None, stream=None):
     """(drows, dweights) of moe_combine: drows of dy's type, dweights fp32 and shaped as where."""
-    T, H = dy.shape
-    ldd, ldr = _matrix(dy, "dy"), _matrix(rows, "rows", cols=H)
+    (T, H), ldd = _matrix(dy, "dy")
+    (positions, cols), ldr = _matrix(rows, "rows")
+    _same(cols, H, "columns of rows")
     top_k = where.shape[1]
-    drows = _padded(rows.shape[0], H, dy.dtype, dy.device)
-    dweights = torch.empty((T, top_k), dtype=torch.float32, device=dy.device)
-    _run("gemm_moe_combine_backward", _type(dy, "dy"), _type(rows, "rows"), T, H, top_k, dy.data_ptr(),
-         ldd, rows.data_ptr(), ldr, rows.shape[0], _array(where, "where", torch.int32, T * top_k),
-         _array(weights, "weights", torch.float32, T * top_k), drows.data_ptr(), drows.stride(0),
-         dweights.data_ptr(), _stream(stream, dy))
+    slots = T * top_k
+    drows, ldo = _padded(positions, H, dy.dtype, dy.device)
+    dweights = torch.empty((T, top_k), dtype=_F32, device=dy.device)
+    status = _lib.gemm_moe_combine_backward(
+        _type(dy.dtype, "dy"), _type(rows.dtype, "rows"), T, H, top_k, dy.data_ptr(), ldd, rows.data_ptr(),
+        ldr, positions, _array(where, "where", _I32, slots),
+        None if weights is None else _array(weights, "weights", _F32, slots), drows.data_ptr(), ldo,
+        dweights.data_ptr(), _stream(stream, dy))
+    if status:
+        _raise(status, "gemm_moe_combine_backward")
     return drows, dweights
 
 
 def gated_silu_backward(pre, dh, stream=None):
     """dpre = [dgate | dup] of h = silu(gate) * up from pre = [gate | up] and dh."""
-    ldp = _matrix(pre, "pre")
-    rows, two = pre.shape
-    if two % 2:
-        raise ValueError("pre: an even number of columns is wanted")
-    ldh = _matrix(dh, "dh", cols=two // 2, rows=rows)
-    out = _padded(rows, two, pre.dtype, pre.device)
-    _run("gemm_gated_silu_backward", _type(pre, "pre"), _type(dh, "dh"), rows, two // 2, pre.data_ptr(),
-         ldp, dh.data_ptr(), ldh, out.data_ptr(), out.stride(0), _stream(stream, pre))
+    (rows, two), ldp = _matrix(pre, "pre")
+    shape, ldh = _matrix(dh, "dh")
+    _same(two % 2, 0, "odd columns of pre")
+    _same(tuple(shape), (rows, two // 2), "shape of dh")
+    out, ldo = _padded(rows, two, pre.dtype, pre.device)
+    status = _lib.gemm_gated_silu_backward(
+        _type(pre.dtype, "pre"), _type(dh.dtype, "dh"), rows, two // 2, pre.data_ptr(), ldp, dh.data_ptr(),
+        ldh, out.data_ptr(), ldo, _stream(stream, pre))
+    if status:
+        _raise(status, "gemm_gated_silu_backward")
     return out
 
 
@@ -215,46 +252,58 @@ def grouped_linear(x, w, offsets, *, rows=None, opW="T", gated=False, out_dtype=
     x.  out_dtype: x's type or torch.float32.  pre (gated only): positions x 2N, receives
     [gate | up].
     """
-    ldx = _matrix(x, "x")
-    x_rows, K = x.shape
-    if opW not in ("T", "N"):
+    (x_rows, K), ldx = _matrix(x, "x")
+    (groups, w_rows, w_cols), ldw = _matrix(w, "w", 3)
+    dtype = x.dtype
+    _same_type(w, dtype, "w")
+    if opW == "T":
+        op, N, inner = GEMM_OP_T, w_rows, w_cols
+    elif opW == "N":
+        op, N, inner = GEMM_OP_N, w_cols, w_rows
+    else:
         raise ValueError(f"opW must be 'T' or 'N', got {opW!r}")
-    ldw = _matrix(w, "w", dtype=x.dtype, dims=3, cols=K if opW == "T" else None,
-                  rows=K if opW == "N" else None)
-    groups = w.shape[0]
-    N = w.shape[1] if opW == "T" else w.shape[2]
+    _same(inner, K, "inner dimension of w")
     if gated:
-        if N % 2:
-            raise ValueError("w: gated weights have gate and up rows, an even number")
+        _same(N % 2, 0, "odd rows of gated w")
         N //= 2
     y_rows = x_rows if rows is None else rows.numel()
-    y = _padded(y_rows, N, out_dtype or x.dtype, x.device)
-    ldp = 0
+    out_dtype = out_dtype or dtype
+    y, ldy = _padded(y_rows, N, out_dtype, x.device)
+    at, ldp, work = None, 0, None
     if pre is not None:
-        ldp = _matrix(pre, "pre", cols=2 * N, rows=y_rows, dtype=x.dtype)
-    # space to lay gathered rows out in, where the library would use it
-    work = None
-    if rows is not None and y_rows > 64 * groups:
-        space = torch.empty(y_rows * ((K + 7) // 8 * 8), dtype=x.dtype, device=x.device)
-        work = space.data_ptr()
-    _run("gemm_grouped_linear", _type(x, "x"), _type(y, "out_dtype"), groups,
-         _array(offsets, "offsets", torch.int32, groups + 1), GEMM_OP_T if opW == "T" else GEMM_OP_N,
-         int(gated), N, K, x.data_ptr(), ldx, x_rows, _array(rows, "rows", torch.int32), w.data_ptr(),
-         ldw, w.stride(0), y.data_ptr(), y.stride(0), y_rows, 0 if pre is None else pre.data_ptr(), ldp,
-         work, _stream(stream, x))
+        shape, ldp = _matrix(pre, "pre")
+        _same_type(pre, dtype, "pre")
+        _same(tuple(shape), (y_rows, 2 * N), "shape of pre")
+        at = pre.data_ptr()
+    if rows is not None:
+        rows = _array(rows, "rows", _I32, y_rows)
+        if y_rows > 64 * groups:  # space to lay gathered rows out in, where the library would use it
+            space = torch.empty(y_rows * ((K + 7) & ~7), dtype=dtype, device=x.device)
+            work = space.data_ptr()
+    status = _lib.gemm_grouped_linear(
+        _type(dtype, "x"), _type(out_dtype, "out_dtype"), groups, _array(offsets, "offsets", _I32, groups + 1),
+        op, gated, N, K, x.data_ptr(), ldx, x_rows, rows, w.data_ptr(), ldw, w.stride(0), y.data_ptr(), ldy,
+        y_rows, at, ldp, work, _stream(stream, x))
+    if status:
+        _raise(status, "gemm_grouped_linear")
     return y
 
 
 def grouped_weight_grad(dy, x, offsets, *, out_dtype=torch.float32, stream=None):
     """dW[g] = sum over the positions p of group g of dy[p]^T x[p]: groups x N x K."""
-    ldd, ldx = _matrix(dy, "dy"), _matrix(x, "x", rows=dy.shape[0], dtype=dy.dtype)
-    N, K = dy.shape[1], x.shape[1]
+    (positions, N), ldd = _matrix(dy, "dy")
+    (x_rows, K), ldx = _matrix(x, "x")
+    _same_type(x, dy.dtype, "x")
+    _same(x_rows, positions, "rows of x")
     groups = offsets.numel() - 1
-    ld = (K + 7) // 8 * 8
+    ld = (K + 7) & ~7
     dw = torch.empty((groups, N, ld), dtype=out_dtype, device=dy.device)
-    _run("gemm_grouped_weight_grad", _type(dy, "dy"), _type(dw, "out_dtype"), groups,
-         _array(offsets, "offsets", torch.int32), N, K, dy.data_ptr(), ldd, x.data_ptr(), ldx,
-         dy.shape[0], dw.data_ptr(), ld, N * ld, _stream(stream, dy))
+    status = _lib.gemm_grouped_weight_grad(
+        _type(dy.dtype, "dy"), _type(out_dtype, "out_dtype"), groups,
+        _array(offsets, "offsets", _I32, groups + 1), N, K, dy.data_ptr(), ldd, x.data_ptr(), ldx, positions,
+        dw.data_ptr(), ld, N * ld, _stream(stream, dy))
+    if status:
+        _raise(status, "gemm_grouped_weight_grad")
     return dw if ld == K else dw[:, :, :K]
 
 
@@ -264,22 +313,27 @@ def lora_linear(x, w, a, b, segments, adapters, *, scales=None, out_dtype=None, 
     x T x K, w N x K, a adapters x R x K, b adapters x N x R of one 16-bit type; request q owns
     tokens segments[q] .. segments[q + 1] - 1 and uses adapters[q] (int32; -1: none).
     """
-    ldx = _matrix(x, "x")
-    T, K = x.shape
-    dt = x.dtype
-    ldw = _matrix(w, "w", cols=K, dtype=dt)
-    N = w.shape[0]
-    lda = _matrix(a, "a", cols=K, dtype=dt, dims=3)
-    count, R = a.shape[0], a.shape[1]
-    ldb = _matrix(b, "b", cols=R, rows=N, dtype=dt, dims=3)
-    if b.shape[0] != count:
-        raise ValueError(f"b: {count} adapters wanted, got {b.shape[0]}")
+    (T, K), ldx = _matrix(x, "x")
+    (N, cols), ldw = _matrix(w, "w")
+    (count, R, a_cols), lda = _matrix(a, "a", 3)
+    shape, ldb = _matrix(b, "b", 3)
+    dtype = x.dtype
+    if w.dtype != dtype or a.dtype != dtype or b.dtype != dtype:
+        for t, what in ((w, "w"), (a, "a"), (b, "b")):
+            _same_type(t, dtype, what)
+    _same(cols, K, "columns of w")
+    _same(a_cols, K, "columns of a")
+    _same(tuple(shape), (count, N, R), "shape of b")
     requests = adapters.numel()
-    y = _padded(T, N, out_dtype or dt, x.device)
-    work = torch.empty(load().gemm_lora_work_bytes(T, requests, R), dtype=torch.uint8, device=x.device)
-    _run("gemm_lora_linear", _type(x, "x"), _type(y, "out_dtype"), T, N, K, x.data_ptr(), ldx,
-         w.data_ptr(), ldw, requests, _array(segments, "segments", torch.int32, requests + 1),
-         _array(adapters, "adapters", torch.int32), count, R, a.data_ptr(), lda, a.stride(0),
-         b.data_ptr(), ldb, b.stride(0), _array(scales, "scales", torch.float32, count), y.data_ptr(),
-         y.stride(0), work.data_ptr(), _stream(stream, x))
+    out_dtype = out_dtype or dtype
+    y, ldy = _padded(T, N, out_dtype, x.device)
+    work = torch.empty(_lib.gemm_lora_work_bytes(T, requests, R), dtype=torch.uint8, device=x.device)
+    status = _lib.gemm_lora_linear(
+        _type(dtype, "x"), _type(out_dtype, "out_dtype"), T, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw,
+        requests, _array(segments, "segments", _I32, requests + 1), _array(adapters, "adapters", _I32, requests),
+        count, R, a.data_ptr(), lda, a.stride(0), b.data_ptr(), ldb, b.stride(0),
+        None if scales is None else _array(scales, "scales", _F32, count), y.data_ptr(), ldy, work.data_ptr(),
+        _stream(stream, x))
+    if status:
+        _raise(status, "gemm_lora_linear")
     return y
