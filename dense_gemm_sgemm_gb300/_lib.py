@@ -63,7 +63,7 @@ SIGNATURES = {
                                    _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
     "gemm_grouped_weight_grad": (_int, [_int, _int, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64,
                                         _vp, _i64, _i64, _vp]),
-    "gemm_lora_work_bytes": (_i64, [_i64, _i64, _i64]),
+    "gemm_lora_work_bytes": (_i64, [_i64, _i64, _i64, _i64, _i64]),
     "gemm_lora_linear": (_int, [_int, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp,
                                 _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
                                 _vp]),

@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     const int ranks = min(16 * MT, a.R - r0);
     if constexpr (PARTS > 0) {
         static_assert(kTokens == 32, "blocks of 32 tokens");
-        const InnerLayout in = inner_layout(a.T, a.requests, a.R, a.type, a.y_type);
+        const InnerLayout in = inner_layout(a.T, a.requests, a.R, PARTS);
         uint16_t *plane = static_cast<uint16_t *>(a.planes) + int64_t(r0 / 64) * in.plane_rows * 64;
         for (int i = threadIdx.x; i < 32 * 16 * MT; i += kThreads) {
             const int r = i % (16 * MT), n = i / (16 * MT), t = t0 - tile * 32;  // tile's first own row
@@ -387,7 +387,7 @@ template <class T, int NT, int PARTS> cudaError_t shrink_by_rank(const ShrinkArg
 template <class T> cudaError_t shrink_t(const ShrinkArgs &a, cudaStream_t stream)
 {
     if (a.inner == nullptr) {
-        if (inner_layout(a.T, a.requests, a.R, a.type, a.y_type).parts == 2) return shrink_by_rank<T, 4, 2>(a, stream);
+        if (a.n_parts == 2) return shrink_by_rank<T, 4, 2>(a, stream);
         return shrink_by_rank<T, 4, 3>(a, stream);
     }
     // requests of one or a few tokens: 8 at a time (a 32-token tile would read its X rows in vain)

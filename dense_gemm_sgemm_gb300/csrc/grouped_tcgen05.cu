@@ -298,6 +298,10 @@ struct LinearParams {
     int groups, shared_w;
     int64_t y_rows, x_rows, N;
     int ftiles, num_kb, cap;  // feature tiles of a group, K slices, tokens of a tile at most
+    // splits > 1: units of a part of the K slices (and of the requests' slices) each, whose fp32 sums
+    // are split_stride elements apart in Y and are added up by the next kernel
+    int splits;
+    int64_t split_stride;
     const int32_t *rows;
     void *Y;
     int64_t ldy;
@@ -314,9 +318,9 @@ struct LinearParams {
     int inject_stall;  // test hook: the producer never fills its first slice
 };
 
-// A unit: one feature tile of one tile of a group's tokens.
+// A unit: one feature tile of one tile of a group's tokens, over K slices [kb0, kb1).
 struct LinearUnit {
-    int group, feature_tile, first, tokens, width;
+    int group, feature_tile, first, tokens, width, split, kb0, kb1;
 };
 __device__ __forceinline__ LinearUnit linear_unit(const LinearParams &p, const Shared &sh, int u, int &group)
 {
@@ -324,8 +328,13 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearParams &p, const S
     const int rows = sh.first[group + 1] - sh.first[group];
     const int tiles = (rows + p.cap - 1) / p.cap;
     const int width = ((rows + tiles - 1) / tiles + 31) & ~31;  // even tiles; at most cap, none is empty
-    const int r = u - sh.start[group], t = r / p.ftiles;
+    int r = u - sh.start[group];
     LinearUnit x;
+    x.split = r % p.splits;
+    x.kb0 = p.num_kb * x.split / p.splits;
+    x.kb1 = p.num_kb * (x.split + 1) / p.splits;
+    r /= p.splits;
+    const int t = r / p.ftiles;
     x.group = group;
     x.feature_tile = r - t * p.ftiles;
     x.first = sh.first[group] + t * width;
@@ -376,15 +385,19 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile
 
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// The requests that share a tile's tokens and have an adapter, in order; the roles' warps walk them in
-// step, 32 requests looked up at a time.
+// The requests that share a tile's tokens and have an adapter, in order, those of the unit's split of
+// them; the roles' warps walk them in step, 32 requests looked up at a time.
+//
+// A request's slices: for every 64 ranks, its inner products' parts in turn, as many parts behind one
+// another in the token half of a stage as fit (all of them for a short request), each multiplied with
+// the same adapter rows.
 struct TileRequests {
     const LinearParams &p;
-    int t0, t1, q0, lane;
+    int t0, t1, q0, lane, skip;
     unsigned left;
     int lo, hi, ad;  // of request q0 + lane: its tokens within the tile and its adapter
     __device__ __forceinline__ TileRequests(const LinearParams &params, const LinearUnit &x, int l)
-        : p(params), t0(x.first), t1(x.first + x.tokens), lane(l)
+        : p(params), t0(x.first), t1(x.first + x.tokens), lane(l), skip(x.split)
     {
         int a = 0, b = p.requests;  // first request that ends behind the tile's first token
         while (a < b) {
@@ -413,11 +426,16 @@ struct TileRequests {
     // 32, and the first of the rows of its inner products.
     __device__ __forceinline__ bool next(int &adapter, int &c0, int &n, int &row)
     {
-        while (left == 0u) {
-            if (!more) return false;
-            q0 += 32;
-            look_up();
+        for (;; --skip) {
+            while (left == 0u) {
+                if (!more) return false;
+                q0 += 32;
+                look_up();
+            }
+            if (skip == 0) break;
+            left &= left - 1u;
         }
+        skip = p.splits - 1;
         const int at = __ffs(left) - 1;
         left &= left - 1u;
         adapter = __shfl_sync(kFull, ad, at);
@@ -427,6 +445,8 @@ struct TileRequests {
         row = (b0 + q0 + at) * 32;
         return true;
     }
+    // Parts in one slice of a request of n columns.
+    __device__ __forceinline__ int parts_a_slice(int n) const { return max(1, min(p.parts, p.cap / n)); }
 };
 
 // W_MN: W stored K x N (features contiguous).
@@ -440,7 +460,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const Shared sh(smem_raw, p.cap * 64);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int cap = p.cap, ftiles = p.ftiles;
+    const int cap = p.cap, ftiles = p.ftiles * p.splits;
     const uint32_t tmem = set_up<EPI != kAdapted>(sh, p.offsets, p.groups, p.y_rows,
                                  [=](int rows) { return (rows + cap - 1) / cap * ftiles; });
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
@@ -461,7 +481,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
             const int f0 = x.feature_tile * kFeatures + int(rank) * (kFeatures / 2);
             const int wg = p.shared_w ? 0 : x.group;
             const uint32_t bytes = 2u * (kStageA + uint32_t(x.width) * 64u);
-            for (int kb = 0; kb < p.num_kb; ++kb) {
+            for (int kb = x.kb0; kb < x.kb1; ++kb) {
                 ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                 if (__any_sync(kFull, !ok)) {
                     ok = false;
@@ -469,7 +489,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 }
                 if (leader) {
                     if (rank == 0) mbar_expect_tx(sh.full(ring.stage), bytes);
-                    if (!(p.inject_stall && kb == 0 && u == unit0)) {
+                    if (!(p.inject_stall && kb == x.kb0 && u == unit0)) {
                         const uint32_t full = full0 + 8u * ring.stage, a = sh.stage_a(ring.stage);
                         if (W_MN) {  // two boxes of 64 features x 64 k
                             tma_load_3d_pair(a, &map_w, full, f0, kb * 64, wg);
@@ -488,20 +508,23 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
             if (EPI == kAdapted && ok) {
                 TileRequests requests(p, x, lane);
                 int ad, c0, n, row;
-                while (ok && requests.next(ad, c0, n, row))
-                    for (int i = 0; i < p.parts * blocks; ++i) {
+                while (ok && requests.next(ad, c0, n, row)) {
+                    const int most = requests.parts_a_slice(n);
+                    for (int r0 = 0, i = 0; ok && r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
                         ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                         if (__any_sync(kFull, !ok)) {
                             ok = false;
                             break;
                         }
                         if (leader) {
-                            if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2u * (kStageA + uint32_t(n) * 64u));
-                            tma_load_3d_pair(sh.stage_a(ring.stage), &map_b, full0 + 8u * ring.stage, i % blocks * 64, f0, ad);
+                            const uint32_t rows = uint32_t(n) * uint32_t(min(most, p.parts - i));
+                            if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2u * (kStageA + rows * 64u));
+                            tma_load_3d_pair(sh.stage_a(ring.stage), &map_b, full0 + 8u * ring.stage, r0, f0, ad);
                         }
                         __syncwarp();
                         ring.next();
                     }
+                }
             }
         }
         if (leader) finish_producer(sh, watch, ring, ok);
@@ -528,7 +551,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 }
                 from = make_int4(r[0], r[1], r[2], r[3]);
             }
-            for (int kb = 0; kb < p.num_kb; ++kb) {
+            for (int kb = x.kb0; kb < x.kb1; ++kb) {
                 ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                 if (__any_sync(kFull, !ok)) {
                     ok = false;
@@ -548,19 +571,22 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 TileRequests requests(p, x, lane);
                 int ad, c0, n, row;
-                while (ok && requests.next(ad, c0, n, row))
-                    for (int i = 0; i < p.parts * blocks; ++i) {
+                while (ok && requests.next(ad, c0, n, row)) {
+                    const int most = requests.parts_a_slice(n);
+                    for (int r0 = 0, i = 0; ok && r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
                         ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                         if (__any_sync(kFull, !ok)) {
                             ok = false;
                             break;
                         }
                         if (leader)
-                            load_rows(sh.stage_b(ring.stage), map_inner, full0 + 8u * ring.stage, 0,
-                                      i * p.plane_rows + row + int(rank) * (n / 2), n / 2);
+                            for (int j = 0; j < most && i + j < p.parts; ++j)
+                                load_rows(sh.stage_b(ring.stage) + uint32_t(j * n) * 64u, map_inner, full0 + 8u * ring.stage, 0,
+                                          ((i + j) * blocks + r0 / 64) * p.plane_rows + row + int(rank) * (n / 2), n / 2);
                         __syncwarp();
                         ring.next();
                     }
+                }
             }
         }
         if (leader && !ok) finish_producer(sh, watch, ring, false);
@@ -586,7 +612,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem + uint32_t(acc * kAccCols);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                for (int kb = x.kb0; kb < x.kb1; ++kb) {
                     ok = watch.wait(sh.full(ring.stage), ring.phase);
                     if (!ok) break;
                     tc_fence_after();
@@ -595,7 +621,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                         const uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            umma_f16<true>(d, a + k * kStepA, b + k * kStepB, idesc, kb > 0 || k > 0 ? 1u : 0u);
+                            umma_f16<true>(d, a + k * kStepA, b + k * kStepB, idesc, kb > x.kb0 || k > 0 ? 1u : 0u);
                         commit_both(sh.empty(ring.stage));
                     }
                     __syncwarp();
@@ -606,17 +632,21 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     int ad, c0, n, row;
                     while (ok && requests.next(ad, c0, n, row)) {
                         const uint32_t part_idesc = make_idesc(0, 0, n, 256) | fmt;
-                        for (int i = 0; i < p.parts * blocks; ++i) {
+                        const int most = requests.parts_a_slice(n);
+                        for (int r0 = 0, i = 0; r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
                             ok = watch.wait(sh.full(ring.stage), ring.phase);
                             if (!ok) break;
                             tc_fence_after();
                             if (leader) {
                                 const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
-                                const uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
-                                const int steps = (p.rank - i % blocks * 64 + 15) / 16;
+                                uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
+                                const int steps = (p.rank - r0 + 15) / 16;
+                                for (int j = 0; j < most && i + j < p.parts; ++j, b += uint32_t(n * 64) >> 4) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (k < steps) umma_f16<true>(d + uint32_t(c0), a + k * kStepA, b + k * kStepB, part_idesc, 1u);
+                                    for (int k = 0; k < 4; ++k)
+                                        if (k < steps)
+                                            umma_f16<true>(d + uint32_t(c0), a + k * kStepA, b + k * kStepB, part_idesc, 1u);
+                                }
                                 commit_both(sh.empty(ring.stage));
                             }
                             __syncwarp();
@@ -704,12 +734,13 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 }
             } else {
                 const int64_t f = int64_t(x.feature_tile) * 256 + int64_t(rank) * 128 + quarter * 32;
+                uint8_t *out = EPI == kAdapted ? Y + x.split * p.split_stride * (Y_F32 ? 4 : 2) : Y;
 #pragma unroll 1
                 for (int c = 32 * half; c < x.width; c += 64) {
                     float v[32];
                     __syncwarp();
                     tmem_ld_32(taddr + c, v);
-                    store_tokens<Y_F32>(v, tile, lane, Y, ldy, x.first + c, x.tokens - c, f, p.N, p.bf16);
+                    store_tokens<Y_F32>(v, tile, lane, out, ldy, x.first + c, x.tokens - c, f, p.N, p.bf16);
                 }
             }
             tc_fence_before();
@@ -1046,35 +1077,49 @@ void test_hooks(uint64_t &timeout_ns, int &inject_stall)
     }
 }
 
+struct Tiling {
+    int cap, splits;
+};
+constexpr int kMostSplits = 8;
+
 // Tokens of a tile: the multiple of 32 for which the average group's tiles take the least time in
 // waves of all pairs.  A K slice of a tile of w tokens takes the longer of its MMAs and of its copies
 // and hand-overs; measured with 64 groups of 512 rows, K = 4096, in SM cycles: 375 (w = 32), 431 (128),
-// 532 (192), 698 (256, where the chip's power limit sets the clock).
-int tile_cap(const GroupedArgs &a, int64_t ftiles, int pairs)
+// 532 (192), 698 (256, where the chip's power limit sets the clock).  A tile costs about 8 slices more
+// than it has.  Where the tiles leave pairs idle, K may be split among them at the cost of one more
+// kernel, about 6000 cycles and the partial sums' way through L2 (work for `most_splits` of them).
+Tiling tiling_of(int64_t rows, int64_t groups, int64_t ftiles, int64_t num_kb, int pairs, int most_splits)
 {
-    // GEMM_GB300_GROUPED_CAP=n (sweeps only): tiles of at most n tokens
-    if (const char *e = std::getenv("GEMM_GB300_GROUPED_CAP"); e && std::atoi(e) >= 32 && std::atoi(e) <= 256)
-        return std::atoi(e) / 32 * 32;
-    const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;
-    const int64_t mean = (a.y_rows + groups - 1) / groups;
-    int best = 256;
+    if (rows < groups) groups = rows;
+    const int64_t mean = (rows + groups - 1) / groups;
+    Tiling best{256, 1};
     double least = 1e300;
+    // GEMM_GB300_GROUPED_CAP=n (sweeps only): tiles of at most n tokens
+    int only = 0;
+    if (const char *e = std::getenv("GEMM_GB300_GROUPED_CAP"); e && std::atoi(e) >= 32 && std::atoi(e) <= 256)
+        only = std::atoi(e) / 32 * 32;
     for (int cap = 256; cap >= 32; cap -= 32) {
+        if (only != 0 && cap != only) continue;
         const int64_t tiles = (mean + cap - 1) / cap;
         const int64_t width = ((mean + tiles - 1) / tiles + 31) / 32 * 32;
-        const int64_t waves = (groups * tiles * ftiles + pairs - 1) / pairs;
+        const int64_t units = groups * tiles * ftiles;
         const double mma = 2.73 * double(width), copies = 360.0 + 0.55 * double(width);
-        const double cost = double(waves) * (mma > copies ? mma : copies);
-        if (cost < 0.98 * least) {
-            least = cost;
-            best = cap;
+        for (int splits = 1; splits <= most_splits && (splits == 1 || (units * splits <= pairs && num_kb >= 4 * splits)); ++splits) {
+            const int64_t waves = (units * splits + pairs - 1) / pairs;
+            const int64_t slices = (num_kb + splits - 1) / splits + 8;
+            double cost = double(waves * slices) * (mma > copies ? mma : copies);
+            if (splits > 1) cost += 6000.0 + 0.002 * double(rows * ftiles * 256 * splits);
+            if (cost < 0.98 * least) {
+                least = cost;
+                best = Tiling{cap, splits};
+            }
         }
     }
     return best;
 }
 
 template <int W_MN, int EPI, bool Y_F32>
-cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
+cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, Tiling tiling, cudaStream_t stream)
 {
     static std::atomic<int> cache[64];
     auto *kernel = grouped_linear_kernel<W_MN, EPI, Y_F32>;
@@ -1098,7 +1143,7 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
     std::memset(&mb, 0, sizeof(mb));
     std::memset(&mi, 0, sizeof(mi));
     if (EPI == kAdapted) {
-        const InnerLayout in = inner_layout(a.y_rows, a.ad.requests, a.ad.rank, a.type, a.y_type);
+        const InnerLayout in = inner_layout(a.y_rows, a.ad.requests, a.ad.rank, a.ad.parts);
         ok = ok && make_map(&mb, a.ad.b, bf16, a.N, a.ad.rank, a.ad.ldb, 128, a.ad.count, a.ad.count > 1 ? a.ad.strideb : a.N * a.ad.ldb);
         for (int i = 0; ok && i < 4; ++i)
             ok = make_map(&mi.rows[i], a.ad.inner, bf16, in.plane_rows * in.parts * in.blocks, 64, 64, 128 >> i, 0, 0);
@@ -1114,7 +1159,9 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
     p.N = a.N;
     p.ftiles = int((a.N + features - 1) / features);
     p.num_kb = int((a.K + 63) / 64);
-    p.cap = tile_cap(a, p.ftiles, pairs);
+    p.cap = tiling.cap;
+    p.splits = tiling.splits;
+    p.split_stride = a.ldy * a.y_rows;
     p.rows = a.rows;
     p.Y = a.Y;
     p.ldy = a.ldy;
@@ -1122,7 +1169,7 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
     p.pre = a.pre;
     p.ldp = a.ldp;
     if (EPI == kAdapted) {
-        const InnerLayout in = inner_layout(a.y_rows, a.ad.requests, a.ad.rank, a.type, a.y_type);
+        const InnerLayout in = inner_layout(a.y_rows, a.ad.requests, a.ad.rank, a.ad.parts);
         p.segments = a.ad.segments;
         p.adapters = a.ad.adapters;
         p.requests = a.ad.requests;
@@ -1134,18 +1181,37 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
     // no more pairs than there can be units
-    const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles;
+    const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles * p.splits;
     return launch_chained(kernel, dim3(unsigned(2 * (most < pairs ? most : pairs))), kThreads, kSmemBytes, 2, stream, mw, mx, mb,
                           mi, p);
 }
 
 template <int W_MN, int EPI> cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
 {
-    return a.y_type == GEMM_TYPE_F32 ? launch_linear_t<W_MN, EPI, true>(dev, a, stream)
-                                     : launch_linear_t<W_MN, EPI, false>(dev, a, stream);
+    const int features = EPI == kGated ? 128 : 256;
+    const bool splittable = EPI == kAdapted && a.work != nullptr;
+    const Tiling tiling = tiling_of(a.y_rows, a.groups, (a.N + features - 1) / features, (a.K + 63) / 64, dev.num_sms / 2,
+                                    splittable ? kMostSplits : 1);
+    if (splittable && tiling.splits > 1) {
+        GroupedArgs b = a;  // the partial sums
+        b.Y = a.work;
+        b.y_type = GEMM_TYPE_F32;
+        b.ldy = (a.N + 7) / 8 * 8;
+        const cudaError_t e = launch_linear_t<W_MN, EPI, true>(dev, b, tiling, stream);
+        if (e != cudaSuccess) return e;
+        return launch_sum(a.y_type, a.y_rows, a.N, tiling.splits, static_cast<const float *>(b.Y), b.ldy, a.Y, a.ldy, stream);
+    }
+    return a.y_type == GEMM_TYPE_F32 ? launch_linear_t<W_MN, EPI, true>(dev, a, tiling, stream)
+                                     : launch_linear_t<W_MN, EPI, false>(dev, a, tiling, stream);
 }
 
 }  // namespace
+
+int64_t split_bytes(int64_t rows, int64_t N, int64_t K, int pairs)
+{
+    const Tiling t = tiling_of(rows, 1, (N + 255) / 256, (K + 63) / 64, pairs, kMostSplits);
+    return t.splits > 1 ? t.splits * rows * ((N + 7) / 8 * 8) * 4 : 0;
+}
 
 cudaError_t launch_many_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
 {

@@ -58,6 +58,27 @@ combine_kernel(int64_t T, int64_t cols, int k, const R *rows, int64_t ldr, int64
     put<Y, VEC>(y + t * ldy + c, acc);
 }
 
+// Thread: VEC columns of a row of the sum of `count` matrices, added in order.
+template <class Y, int VEC>
+__global__ void __launch_bounds__(kThreads)
+sum_kernel(int64_t rows, int64_t cols, int count, const float *part, int64_t ldp, Y *y, int64_t ldy)
+{
+    chain_wait();
+    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t r = i / cols, c = (i - r * cols) * VEC;
+    if (r >= rows) return;
+    float acc[VEC];
+    get<float, VEC>(part + r * ldp + c, acc);
+#pragma unroll 4
+    for (int n = 1; n < count; ++n) {
+        float v[VEC];
+        get<float, VEC>(part + (n * rows + r) * ldp + c, v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] += v[j];
+    }
+    put<Y, VEC>(y + r * ldy + c, acc);
+}
+
 // Warp: one slot.  out[where] = w * x[token]; dweights != NULL also takes the dot product of
 // x[token] and rows[where].
 template <class X, class R, int VEC>
@@ -216,6 +237,21 @@ cudaError_t launch_dispatch(int type, int rows_type, int64_t T, int64_t H, int t
                                                     static_cast<const R *>(rows), ldr, positions, where, weights,
                                                     static_cast<X *>(out), ldo, dweights);
         });
+    });
+}
+
+cudaError_t launch_sum(int y_type, int64_t rows, int64_t cols, int count, const float *part, int64_t ldp, void *y, int64_t ldy,
+                       cudaStream_t stream)
+{
+    const bool vec = cols % 8 == 0;  // both matrices' rows start on 16-byte boundaries
+    const int64_t pieces = vec ? cols / 8 : cols;
+    unsigned blocks;
+    if (!grid_of(rows * pieces, kThreads, blocks)) return cudaErrorInvalidConfiguration;
+    return by_type(y_type, [&](auto o) {
+        using Y = decltype(o);
+        auto *kernel = vec ? sum_kernel<Y, 8> : sum_kernel<Y, 1>;
+        return launch_chained(kernel, dim3(blocks), kThreads, 0, 1, stream, rows, pieces, count, part, ldp, static_cast<Y *>(y),
+                              ldy);
     });
 }
 

@@ -253,12 +253,24 @@ gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw_type, in
     return from_cuda(launch_weight_grad(dev, a, static_cast<cudaStream_t>(stream)));
 }
 
-int64_t gemm_lora_work_bytes(int64_t T, int64_t requests, int64_t R)
+// Partial sums for the device at hand or, without one, for 152 SMs.
+static int64_t lora_split_bytes(int64_t T, int64_t N, int64_t K)
 {
-    if (T <= 0 || requests <= 0 || R <= 0 || T > kMaxDim24 || requests > kMaxDim24 || R > 128) return 0;
-    const int64_t few = 4 * T * (R + 1);
-    const int64_t many = inner_layout(T, requests, R, GEMM_TYPE_BF16, GEMM_TYPE_F32).bytes();
-    return few > many ? few : many;
+    DeviceInfo dev;
+    return (split_bytes(T, N, K, current_device(dev) ? dev.num_sms / 2 : 76) + 15) / 16 * 16;
+}
+static int64_t lora_inner_bytes(int64_t T, int64_t requests, int64_t R)
+{
+    const int64_t few = 4 * T * (R + 1), many = inner_layout(T, requests, R, 3).bytes();
+    return ((few > many ? few : many) + 15) / 16 * 16;
+}
+
+int64_t gemm_lora_work_bytes(int64_t T, int64_t N, int64_t K, int64_t requests, int64_t R)
+{
+    if (T <= 0 || N <= 0 || K <= 0 || requests <= 0 || R <= 0 || T > kMaxDim24 || N > kMaxDim24 || K > kMaxDim24 ||
+        requests > kMaxDim24 || R > 128)
+        return 0;
+    return lora_inner_bytes(T, requests, R) + lora_split_bytes(T, N, K);
 }
 
 gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, int64_t N, int64_t K, const void *X,
@@ -295,13 +307,15 @@ gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, 
     GroupedArgs a{type, y_type, 1, nullptr, GEMM_OP_T, 0, N, K, X, ldx, T, nullptr, W, ldw, 0, Y, ldy, T, nullptr, 0,
                   Adapters{}, nullptr};
     if (adapted) {
-        const bool few = takes_few_rows(a);
+        const bool few = takes_few_rows(dev, a);
+        const int parts = inner_parts(type, y_type);
         int32_t *which = static_cast<int32_t *>(work) + T * R;
         const ShrinkArgs sh{type, T, K, X, ldx, int(requests), segments, adapters, int(n_adapters), int(R), A, lda, strideA,
-                            scales, few ? static_cast<float *>(work) : nullptr, which, work, y_type};
+                            scales, few ? static_cast<float *>(work) : nullptr, which, work, parts};
         const cudaError_t e = launch_shrink(sh, st);
         if (e != cudaSuccess) return from_cuda(e);
-        a.ad = Adapters{B, ldb, strideB, int(R), int(n_adapters), work, which, int(requests), segments, adapters};
+        a.ad = Adapters{B, ldb, strideB, int(R), int(n_adapters), work, which, int(requests), parts, segments, adapters};
+        a.work = static_cast<char *>(work) + lora_inner_bytes(T, requests, R);
     }
     return launch_grouped(dev, a, st);
 }

@@ -173,10 +173,10 @@ struct InnerLayout {
 };
 // Parts: fp16's two hold 22 bits.  bf16's two hold 16, 2^8 times finer than a 16-bit output; an fp32
 // output takes three.
-__host__ __device__ inline InnerLayout inner_layout(int64_t tokens, int64_t requests, int64_t rank, int type, int y_type)
+inline int inner_parts(int type, int y_type) { return type == GEMM_TYPE_BF16 && y_type == GEMM_TYPE_F32 ? 3 : 2; }
+__host__ __device__ inline InnerLayout inner_layout(int64_t tokens, int64_t requests, int64_t rank, int parts)
 {
-    return InnerLayout{type == GEMM_TYPE_BF16 && y_type == GEMM_TYPE_F32 ? 3 : 2, int((rank + 63) / 64),
-                       (tokens / 32 + requests) * 32};
+    return InnerLayout{parts, int((rank + 63) / 64), (tokens / 32 + requests) * 32};
 }
 struct Adapters {
     const void *b;  // NULL: no adapters
@@ -184,7 +184,7 @@ struct Adapters {
     int rank, count;
     const void *inner;
     const int32_t *which;  // few-rows kernel: adapter of each position, -1: none
-    int requests;          // tcgen05 kernel
+    int requests, parts;   // tcgen05 kernel
     const int32_t *segments, *adapters;
 };
 struct GroupedArgs {
@@ -203,8 +203,15 @@ struct GroupedArgs {
     void *pre;
     int64_t ldp;
     Adapters ad;
-    void *work;  // y_rows x (K rounded up to 8) elements, or NULL
+    // gathered rows: y_rows x (K rounded up to 8) elements; adapters: split_bytes() of partial sums; or
+    // NULL
+    void *work;
 };
+// Bytes of the partial sums of a linear layer with adapters on a device of 2 * pairs SMs.
+int64_t split_bytes(int64_t rows, int64_t N, int64_t K, int pairs);
+// y = the sum of `count` fp32 matrices of rows x cols, rows * ldp elements apart.
+cudaError_t launch_sum(int y_type, int64_t rows, int64_t cols, int count, const float *part, int64_t ldp, void *y, int64_t ldy,
+                       cudaStream_t stream);
 // Few rows per group (opW = T): weights straight from global memory to mma.sync fragments.
 cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 
@@ -212,7 +219,7 @@ cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStr
 cudaError_t launch_many_rows(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 // X[rows[p]] to row p of `out`, for the positions of the groups.
 cudaError_t launch_gather(const GroupedArgs &a, void *out, int64_t ldo, cudaStream_t stream);
-bool takes_few_rows(const GroupedArgs &a);
+bool takes_few_rows(const DeviceInfo &dev, const GroupedArgs &a);
 gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream);
 
 struct WeightGradArgs {
@@ -242,8 +249,8 @@ struct ShrinkArgs {
     const float *scales;
     float *inner;    // few-rows form, NULL: the other
     int32_t *which;
-    void *planes;    // tcgen05 form
-    int y_type;
+    void *planes;    // tcgen05 form, of `parts`
+    int n_parts;
 };
 cudaError_t launch_shrink(const ShrinkArgs &a, cudaStream_t stream);
 

@@ -327,7 +327,7 @@ def lora_linear(x, w, a, b, segments, adapters, *, scales=None, out_dtype=None, 
     requests = adapters.numel()
     out_dtype = out_dtype or dtype
     y, ldy = _padded(T, N, out_dtype, x.device)
-    work = torch.empty(_lib.gemm_lora_work_bytes(T, requests, R), dtype=torch.uint8, device=x.device)
+    work = torch.empty(_lib.gemm_lora_work_bytes(T, N, K, requests, R), dtype=torch.uint8, device=x.device)
     status = _lib.gemm_lora_linear(
         _type(dtype, "x"), _type(out_dtype, "out_dtype"), T, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw,
         requests, _array(segments, "segments", _I32, requests + 1), _array(adapters, "adapters", _I32, requests),

@@ -460,13 +460,14 @@ GEMM_API gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw
  * product as sums of 16-bit parts: of bf16 to 16 bits (24 when Y is fp32), of fp16 to 22 bits, where
  * they share fp16's range (beyond 65504 infinite, below 2^-14 kept to 2^-25).
  *
- * work: gemm_lora_work_bytes(T, requests, R) bytes for the call to use (not kept; NULL when there are
- * no requests, no adapters, or R or K is 0).
+ * work: gemm_lora_work_bytes(T, N, K, requests, R) bytes for the call to use (not kept; NULL when
+ * there are no requests, no adapters, or R or K is 0).  That function gives the bytes for the current
+ * device.
  * Alignment: X, W, A, B, Y and work 16-byte aligned; ldx, ldw, lda, ldb, ldy, strideA, strideB
  * multiples of 8 elements.  Limits: R <= 128, T < 2^24, requests < 2^24, N and K < 2^24, and
  * (T / 32 + requests) * 32 * 6 < 2^31.
  */
-GEMM_API int64_t gemm_lora_work_bytes(int64_t T, int64_t requests, int64_t R);
+GEMM_API int64_t gemm_lora_work_bytes(int64_t T, int64_t N, int64_t K, int64_t requests, int64_t R);
 GEMM_API gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, int64_t T, int64_t N,
                                         int64_t K, const void *X, int64_t ldx, const void *W,
                                         int64_t ldw, int64_t requests, const int32_t *segments,
