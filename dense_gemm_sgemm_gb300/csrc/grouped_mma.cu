@@ -24,7 +24,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRowStride = 36;  // floats between tokens of a warp's partial tile: 8 t + g, no bank twice
 constexpr unsigned kFull = 0xffffffffu;
 
-// Weights are read once: no line of L1 for them.
+// Rows that one warp reads once: no line of L1 for them.
 __device__ __forceinline__ uint4 load_stream(const void *p)
 {
     uint4 v;
@@ -37,11 +37,13 @@ __device__ __forceinline__ uint4 load_stream(const void *p)
 // acc[mt][nt] += W X^T over k in [kb, ke) (kb a multiple of 32, ke one or K).  w[mt][h]: the row of
 // this lane's group in the lower and upper half of tile mt; x[nt]: the token row of this lane's
 // group, NULL for a column of zeros.
-template <class T, int MT, int NT>
+//
+// Registers of loads in flight: 96, or 64 where a CTA's 16 warps leave a thread 128 registers.
+template <class T, int MT, int NT, int FLIGHT = 96>
 __device__ __forceinline__ void warp_product(const T *const (&w)[MT][2], const T *const (&x)[NT], int64_t kb,
                                              int64_t ke, int64_t K, int lane, float (&acc)[MT][NT][4])
 {
-    constexpr int U = MT * 2 * 4 * 4 + NT * 4 * 4 <= 96 ? 4 : MT * 2 * 4 * 2 + NT * 4 * 2 <= 96 ? 2 : 1;
+    constexpr int U = MT * 2 * 4 * 4 + NT * 4 * 4 <= FLIGHT ? 4 : MT * 2 * 4 * 2 + NT * 4 * 2 <= FLIGHT ? 2 : 1;
     const int t8 = (lane & 3) * 8;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     auto multiply = [&](const uint4 (&a)[MT][2], const uint4 (&b)[NT]) {
@@ -85,7 +87,6 @@ __device__ __forceinline__ void warp_product(const T *const (&w)[MT][2], const T
 template <int MT, int NT>
 __device__ __forceinline__ void put_partial(float *part, const float (&acc)[MT][NT][4], int lane)
 {
-    constexpr int kStride = MT <= 2 ? kRowStride : 68;  // 64 rows; again 8 t + g
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -93,7 +94,7 @@ __device__ __forceinline__ void put_partial(float *part, const float (&acc)[MT][
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                part[(n * 8 + 2 * t + (c & 1)) * kStride + m * 16 + g + 8 * (c >> 1)] = acc[m][n][c];
+                part[(n * 8 + 2 * t + (c & 1)) * kRowStride + m * 16 + g + 8 * (c >> 1)] = acc[m][n][c];
 }
 
 __device__ __forceinline__ int32_t clamp_to(int32_t v, int64_t hi) { return v < 0 ? 0 : v > hi ? int32_t(hi) : v; }
@@ -234,21 +235,24 @@ template <class T, int PARTS> __device__ __forceinline__ void split(float x, uin
     }
 }
 
-// Inner products of the adapters: inner[t][r] = scale * sum_k X[t][k] A_a[r][k] for 64 (16 MT) ranks
-// of up to 8 * NT tokens of one request, K split over the CTA's 8 warps.
+// Inner products of the adapters: inner[t][r] = scale * sum_k X[t][k] A_a[r][k] for 16 MT ranks of up to
+// 8 NT GROUPS tokens of one request: GROUPS sets of warps take 8 NT tokens each, and K is split over
+// the warps of a set.  Bound by latency for few tokens, so 16 warps share K; for a prompt by what the
+// CTAs draw from L2, so two sets share the reads of the adapter's rows.
 //
-// CTA i takes item i of an enumeration that needs no scan: cutting the tokens both at multiples of
-// 8 NT and at the request boundaries, request s has the items t = segments[s] / (8 NT) + s ..
-// segments[s + 1] / (8 NT) + s, so the request of item i is the last s whose first item is <= i.
+// CTA i takes item i of an enumeration that needs no scan: cutting the tokens both at multiples of the
+// tile and at the request boundaries, request s has the items t = segments[s] / tile + s ..
+// segments[s + 1] / tile + s, so the request of item i is the last s whose first item is <= i.
 //
 // PARTS = 0 writes the few-rows form of the inner products, else the tcgen05 form (InnerLayout), for
 // which 8 NT is 32.
-template <class T, int MT, int NT, int PARTS>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
+constexpr int kShrinkWarps = 16;
+template <class T, int MT, int NT, int PARTS, int GROUPS>
+__global__ void __launch_bounds__(32 * kShrinkWarps) shrink_kernel(const ShrinkArgs a)
 {
-    extern __shared__ float parts[];  // kWarps x (8 NT) x stride
-    constexpr int kTokens = 8 * NT;
-    constexpr int kStride = MT <= 2 ? kRowStride : 68;
+    extern __shared__ float parts[];  // kShrinkWarps x (8 NT) x kRowStride
+    constexpr int kThreads = 32 * kShrinkWarps;
+    constexpr int kSet = 8 * NT, kTokens = kSet * GROUPS, kSplit = kShrinkWarps / GROUPS;
     chain_wait();  // the product that follows may start on its weights and rows; it waits for inner
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     auto seg = [&](int q) { return clamp_to(__ldg(a.segments + q), a.T); };
@@ -259,11 +263,13 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
             for (int t = seg(a.requests) + threadIdx.x; t < a.T; t += kThreads) a.which[t] = -1;
     }
     const int item = blockIdx.x;
-    int lo = 0, hi = a.requests - 1;  // last request whose first item is <= item
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (seg(mid) / kTokens + mid <= item) lo = mid;
-        else hi = mid - 1;
+    int lo = 0;  // last request whose first item is <= item, 32 candidates at a time
+    for (int n = a.requests; n > 1;) {
+        const int step = (n + 31) / 32, q = lo + lane * step;
+        const bool before = lane * step < n && seg(q) / kTokens + q <= item;
+        const int c = max(__popc(__ballot_sync(kFull, before)) - 1, 0);
+        lo += c * step;
+        n = min(step, n - c * step);
     }
     const int tile = item - lo;
     if (tile < 0) return;
@@ -283,11 +289,13 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) w[m][h] = A + int64_t(min(r0 + 16 * m + 8 * h + g, a.R - 1)) * a.lda;
+    // tokens by their place in the tile, so that a set's columns are a block of the tile
+    const int set = warp / kSplit;
     const T *x[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int t = t0 + 8 * n + g;
-        x[n] = t < t1 ? static_cast<const T *>(a.X) + int64_t(t) * a.ldx : nullptr;
+        const int t = tile * kTokens + set * kSet + 8 * n + g;
+        x[n] = t >= t0 && t < t1 ? static_cast<const T *>(a.X) + int64_t(t) * a.ldx : nullptr;
     }
     float acc[MT][NT][4];
 #pragma unroll
@@ -297,37 +305,37 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const ShrinkArgs a)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[m][n][c] = 0.0f;
     const int64_t chunks = (a.K + 31) / 32;
-    const int64_t kb = chunks * warp / kWarps * 32, ke = min(chunks * (warp + 1) / kWarps * 32, a.K);
-    warp_product<T, MT, NT>(w, x, kb, ke, a.K, lane, acc);
-    put_partial<MT, NT>(parts + warp * kTokens * kStride, acc, lane);
+    const int64_t kb = chunks * (warp % kSplit) / kSplit * 32, ke = min(chunks * (warp % kSplit + 1) / kSplit * 32, a.K);
+    warp_product<T, MT, NT, 64>(w, x, kb, ke, a.K, lane, acc);
+    put_partial<MT, NT>(parts + warp * kSet * kRowStride, acc, lane);
     __syncthreads();
     const float scale = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
     const int ranks = min(16 * MT, a.R - r0);
+    auto sum = [&](int n, int r) {  // of token n of the tile
+        const float *src = parts + (n / kSet * kSplit * kSet + n % kSet) * kRowStride + r;
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kSplit; ++q) v += src[q * kSet * kRowStride];
+        return scale * v;
+    };
     if constexpr (PARTS > 0) {
-        static_assert(kTokens == 32, "blocks of 32 tokens");
+        static_assert(kSet == 32, "blocks of 32 tokens");
         const InnerLayout in = inner_layout(a.T, a.requests, a.R, PARTS);
         uint16_t *plane = static_cast<uint16_t *>(a.planes) + int64_t(r0 / 64) * in.plane_rows * 64;
-        for (int i = threadIdx.x; i < 32 * 16 * MT; i += kThreads) {
-            const int r = i % (16 * MT), n = i / (16 * MT), t = t0 - tile * 32;  // tile's first own row
-            float v = 0.0f;
-            if (r < ranks && n >= t && n < t + t1 - t0) {
-#pragma unroll
-                for (int q = 0; q < kWarps; ++q) v += parts[(q * kTokens + n - t) * kStride + r];
-                v *= scale;
-            }
+        const int64_t row0 = (int64_t(tile) * GROUPS + lo) * 32;  // of the tile's first block
+        for (int i = threadIdx.x; i < kTokens * 16 * MT; i += kThreads) {
+            const int r = i % (16 * MT), n = i / (16 * MT), t = tile * kTokens + n;
+            if ((t | 31) < t0 || (t & ~31) >= t1) continue;  // a block without tokens of the request
             uint16_t part[PARTS];
-            split<T, PARTS>(v, part);
+            split<T, PARTS>(r < ranks && t >= t0 && t < t1 ? sum(n, r) : 0.0f, part);
 #pragma unroll
             for (int q = 0; q < PARTS; ++q)
-                plane[int64_t(q) * in.blocks * in.plane_rows * 64 + (int64_t(item) * 32 + n) * 64 + r0 % 64 + r] = part[q];
+                plane[int64_t(q) * in.blocks * in.plane_rows * 64 + (row0 + n) * 64 + r0 % 64 + r] = part[q];
         }
     } else {
         for (int i = threadIdx.x; i < ranks * (t1 - t0); i += kThreads) {
-            const int r = i % ranks, n = i / ranks;
-            float v = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) v += parts[(q * kTokens + n) * kStride + r];
-            a.inner[int64_t(t0 + n) * a.R + r0 + r] = scale * v;
+            const int r = i % ranks, t = t0 + i / ranks;
+            a.inner[int64_t(t) * a.R + r0 + r] = sum(t - tile * kTokens, r);
         }
     }
 }
@@ -366,22 +374,23 @@ template <class T, class Y> cudaError_t few_rows_t(const DeviceInfo &dev, const 
     return go(std::integral_constant<int, 8>{});
 }
 
-template <class T, int MT, int NT, int PARTS> cudaError_t launch_shrink_t(const ShrinkArgs &a, cudaStream_t stream)
+template <class T, int MT, int NT, int PARTS, int GROUPS> cudaError_t launch_shrink_t(const ShrinkArgs &a, cudaStream_t stream)
 {
-    constexpr int kStride = MT <= 2 ? kRowStride : 68;
-    const size_t smem = size_t(kWarps) * 8 * NT * kStride * sizeof(float);
-    auto *kernel = shrink_kernel<T, MT, NT, PARTS>;
+    constexpr size_t smem = size_t(kShrinkWarps) * 8 * NT * kRowStride * sizeof(float);
+    auto *kernel = shrink_kernel<T, MT, NT, PARTS, GROUPS>;
     const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
-    const dim3 grid(unsigned(a.T / (8 * NT) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
-    return launch_chained(kernel, grid, kThreads, smem, 1, stream, a);
+    static_assert(smem <= 100 * 1024, "dynamic shared memory");
+    const dim3 grid(unsigned(a.T / (8 * NT * GROUPS) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
+    return launch_chained(kernel, grid, 32 * kShrinkWarps, smem, 1, stream, a);
 }
 
 template <class T, int NT, int PARTS> cudaError_t shrink_by_rank(const ShrinkArgs &a, cudaStream_t stream)
 {
-    if (a.R <= 16) return launch_shrink_t<T, 1, NT, PARTS>(a, stream);
-    if (a.R <= 32) return launch_shrink_t<T, 2, NT, PARTS>(a, stream);
-    return launch_shrink_t<T, 4, NT, PARTS>(a, stream);
+    if (a.R <= 16) return launch_shrink_t<T, 1, NT, PARTS, 1>(a, stream);
+    // two sets of 32 tokens where most requests fill them
+    if (NT == 4 && a.T >= 64 * int64_t(a.requests)) return launch_shrink_t<T, 2, NT, PARTS, 2>(a, stream);
+    return launch_shrink_t<T, 2, NT, PARTS, 1>(a, stream);
 }
 
 template <class T> cudaError_t shrink_t(const ShrinkArgs &a, cudaStream_t stream)

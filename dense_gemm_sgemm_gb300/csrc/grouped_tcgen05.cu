@@ -272,6 +272,16 @@ __device__ __forceinline__ void commit_both(uint32_t bar)
                  : "memory");
 }
 
+// The warp has its accumulator columns in registers: one arrival on the issuer's barrier, which may be
+// the peer's.  Released at CTA scope only: a release at cluster scope would wait for the warp's global
+// stores (8000 cycles a tile in all, against 3000).
+__device__ __forceinline__ void release_accumulator(uint32_t bar_cluster, int lane)
+{
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // ------------------------------------------------------------------ Y = X op(W)
 constexpr int kTokenWarp = 2 + kEpiWarps;
 constexpr int kThreads = 32 * (kTokenWarp + 1);
@@ -399,13 +409,15 @@ struct TileRequests {
     __device__ __forceinline__ TileRequests(const LinearParams &params, const LinearUnit &x, int l)
         : p(params), t0(x.first), t1(x.first + x.tokens), lane(l), skip(x.split)
     {
-        int a = 0, b = p.requests;  // first request that ends behind the tile's first token
-        while (a < b) {
-            const int mid = (a + b) / 2;
-            if (clamp_to(__ldg(p.segments + mid + 1), p.y_rows) <= t0) a = mid + 1;
-            else b = mid;
+        // requests that end at or before the tile's first token, 32 candidates at a time: whole runs, then the run that is left
+        q0 = 0;
+        for (int n = p.requests; n > 0;) {
+            const int run = (n + 31) / 32, last = (lane + 1) * run - 1;
+            const bool done = last < n && clamp_to(__ldg(p.segments + q0 + last + 1), p.y_rows) <= t0;
+            const int c = __popc(__ballot_sync(kFull, done));
+            q0 += c * run;
+            n = (c + 1) * run <= n ? run - 1 : n - c * run;
         }
-        q0 = a;
         look_up();
     }
     __device__ __forceinline__ void look_up()
@@ -669,6 +681,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         uint8_t *tile = sh.epi + (warp - 2) * 4096;
         int acc = 0, group = 0;
         uint32_t acc_phase = 0;
+        const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
         uint8_t *Y = static_cast<uint8_t *>(p.Y);
         const int64_t ldy = p.ldy * (Y_F32 ? 4 : 2);
         for (int u = unit0; u < units; u += step) {
@@ -688,6 +701,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 const int meet = 2 + 2 * half + (quarter & 1);  // named barrier of the two warps
                 float *own = reinterpret_cast<float *>(tile);
                 const float *other = reinterpret_cast<const float *>(sh.epi + ((warp - 2) ^ 2) * 4096);
+                if (64 * half >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
 #pragma unroll 1
                 for (int c = 64 * half; c < x.width; c += 128) {
                     const bool two = c + 32 < x.width;
@@ -695,6 +709,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     __syncwarp();
                     tmem_ld_32(taddr + c, v0);
                     if (two) tmem_ld_32(taddr + c + 32, v1);
+                    if (c + 128 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
                     if (p.pre != nullptr) {
                         uint8_t *pre = static_cast<uint8_t *>(p.pre) + (up ? p.N * 2 : 0);
                         if (f + 32 <= p.N && p.N % 8 == 0) {
@@ -735,17 +750,16 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
             } else {
                 const int64_t f = int64_t(x.feature_tile) * 256 + int64_t(rank) * 128 + quarter * 32;
                 uint8_t *out = EPI == kAdapted ? Y + x.split * p.split_stride * (Y_F32 ? 4 : 2) : Y;
+                if (32 * half >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
 #pragma unroll 1
                 for (int c = 32 * half; c < x.width; c += 64) {
                     float v[32];
                     __syncwarp();
                     tmem_ld_32(taddr + c, v);
+                    if (c + 64 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
                     store_tokens<Y_F32>(v, tile, lane, out, ldy, x.first + c, x.tokens - c, f, p.N, p.bf16);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(sh.acc_empty(acc), 0));
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
@@ -927,6 +941,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
         // tile (16-byte pieces, XOR-swizzled by row) so that stores are 128- or 64-byte row segments
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         float4 *tile = reinterpret_cast<float4 *>(sh.epi + (warp - 2) * 4096);
+        const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int u = unit0; u < units; u += step) {
@@ -948,6 +963,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                 __syncwarp();
                 if (x.rows > 0) {
                     tmem_ld_32(taddr + c, v);
+                    if (c + 64 >= 256) release_accumulator(acc_empty0 + 8u * acc, lane);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.0f;
@@ -1007,9 +1023,6 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                 }
             }
             if (x.rows == 0) continue;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(sh.acc_empty(acc), 0));
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
