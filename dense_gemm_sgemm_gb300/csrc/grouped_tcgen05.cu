@@ -11,7 +11,8 @@
 //         rows four at a time (tile::gather4) by all lanes;
 //   1     MMA issuer (of the pair's first CTA) and TMEM owner, two 256-column accumulators;
 //   2-9   epilogue: one TMEM lane is one feature, so 32 tokens x 32 features pass through shared
-//         memory per warp and leave as 16-byte pieces of token rows.
+//         memory per warp and leave by TMA stores, those of a group's last tokens as 16-byte pieces
+//         of its rows.
 // gated: a CTA's 128 rows are 64 gate rows and their 64 up rows; the warps that hold a gate and its
 // up exchange halves through shared memory.  Adapters: behind a tile's last K slice come the slices
 // of its requests' low-rank products, B_a on the m side and the inner products on the n side, over the
@@ -312,6 +313,7 @@ struct LinearParams {
     // are split_stride elements apart in Y and are added up by the next kernel
     int splits;
     int64_t split_stride;
+    int y_tma;  // Y is stored to by TMA, through map_y
     const int32_t *rows;
     void *Y;
     int64_t ldy;
@@ -353,8 +355,64 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearParams &p, const S
     return x;
 }
 
-// 32 tokens of this warp's 32 features (v: this lane's feature) to rows `first` .. of an array, as
-// 16-byte pieces: all pieces are read from the staging tile before the first is stored.
+// The epilogue warps' staging tiles and their TMA stores in flight: fp32 pieces fill a tile, 16-bit
+// pieces take its halves in turn.
+template <bool F32> struct Staging {
+    uint8_t *tile;
+    int lane, half = 0;
+    __device__ __forceinline__ Staging(uint8_t *t, int l) : tile(t), lane(l) {}
+    // The place of the next piece, once the store that last read it has done so.
+    __device__ __forceinline__ uint8_t *next()
+    {
+        if (lane == 0) {
+            if (F32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        }
+        __syncwarp();
+        half ^= F32 ? 0 : 2048;
+        return tile + half;
+    }
+    // The whole tile, free of stores.
+    __device__ __forceinline__ uint8_t *all() const
+    {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        return tile;
+    }
+    __device__ __forceinline__ void store(const CUtensorMap *map, const uint8_t *piece, int c0, int c1, int c2) const
+    {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(map, smem_u32(piece), c0, c1, c2);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+    // Every store has been written; to be called before the CTA ends.
+    __device__ __forceinline__ void finish() const
+    {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+};
+
+// v (this lane's feature, 32 tokens) as [token][feature].
+template <bool F32> __device__ __forceinline__ void stage_tokens(const float (&v)[32], uint8_t *piece, int lane, bool bf16)
+{
+    if (F32) {
+        float *t = reinterpret_cast<float *>(piece);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i * 32 + lane] = v[i];
+    } else {
+        uint16_t *t = reinterpret_cast<uint16_t *>(piece);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i * 32 + lane] = to_16(v[i], bf16);
+    }
+}
+
+// 32 tokens of this warp's 32 features to rows `first` .. of an array in 16-byte pieces of token rows,
+// the first `tokens` of them: for the last tokens of a group, whose 32 rows are not all its own, and for
+// arrays that TMA cannot store to.
 template <bool F32>
 __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile, int lane, uint8_t *base, int64_t ld_bytes,
                                              int first, int tokens, int64_t feature0, int64_t N, bool bf16)
@@ -362,15 +420,7 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile
     constexpr int kSize = F32 ? 4 : 2, kPieces = 2 * kSize;  // 16-byte pieces of 32 features
     constexpr int kPasses = kPieces;                         // 32 / kPieces tokens a pass
     __syncwarp();
-    if (F32) {
-        float *t = reinterpret_cast<float *>(tile);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) t[i * 32 + lane] = v[i];
-    } else {
-        uint16_t *t = reinterpret_cast<uint16_t *>(tile);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) t[i * 32 + lane] = to_16(v[i], bf16);
-    }
+    stage_tokens<F32>(v, tile, lane, bf16);
     __syncwarp();
     const int piece = lane % kPieces, i0 = lane / kPieces;
     uint4 q[kPasses];
@@ -466,7 +516,7 @@ template <int W_MN, int EPI, bool Y_F32>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x,
                       const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TokenMaps map_inner,
-                      const LinearParams p)
+                      const __grid_constant__ CUtensorMap map_y, const LinearParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const Shared sh(smem_raw, p.cap * 64);
@@ -679,11 +729,22 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         // ---------------- epilogue: TMEM lanes 32 * quarter .. of this CTA's 128 rows
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         uint8_t *tile = sh.epi + (warp - 2) * 4096;
+        Staging<Y_F32> staging(tile, lane);
         int acc = 0, group = 0;
         uint32_t acc_phase = 0;
         const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
-        uint8_t *Y = static_cast<uint8_t *>(p.Y);
         const int64_t ldy = p.ldy * (Y_F32 ? 4 : 2);
+        auto put = [&](const float (&v)[32], int first, int tokens, int64_t f, int split) {
+            if (f >= p.N) return;
+            if (p.y_tma && tokens >= 32) {
+                uint8_t *piece = staging.next();
+                stage_tokens<Y_F32>(v, piece, lane, p.bf16);
+                staging.store(&map_y, piece, int(f), first, split);
+            } else {
+                uint8_t *Y = static_cast<uint8_t *>(p.Y) + split * p.split_stride * (Y_F32 ? 4 : 2);
+                store_tokens<Y_F32>(v, staging.all(), lane, Y, ldy, first, tokens, f, p.N, p.bf16);
+            }
+        };
         for (int u = unit0; u < units; u += step) {
             const LinearUnit x = linear_unit(p, sh, u, group);
             const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
@@ -710,6 +771,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     tmem_ld_32(taddr + c, v0);
                     if (two) tmem_ld_32(taddr + c + 32, v1);
                     if (c + 128 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
+                    staging.all();
                     if (p.pre != nullptr) {
                         uint8_t *pre = static_cast<uint8_t *>(p.pre) + (up ? p.N * 2 : 0);
                         if (f + 32 <= p.N && p.N % 8 == 0) {
@@ -744,12 +806,10 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     }
                     asm volatile("bar.sync %0, 64;" ::"r"(meet) : "memory");
                     const int at = up ? c + 32 : c;
-                    if (!up || two)
-                        store_tokens<Y_F32>(v0, tile, lane, Y, ldy, x.first + at, x.tokens - at, f, p.N, p.bf16);
+                    if (!up || two) put(v0, x.first + at, x.tokens - at, f, 0);
                 }
             } else {
                 const int64_t f = int64_t(x.feature_tile) * 256 + int64_t(rank) * 128 + quarter * 32;
-                uint8_t *out = EPI == kAdapted ? Y + x.split * p.split_stride * (Y_F32 ? 4 : 2) : Y;
                 if (32 * half >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
 #pragma unroll 1
                 for (int c = 32 * half; c < x.width; c += 64) {
@@ -757,7 +817,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     __syncwarp();
                     tmem_ld_32(taddr + c, v);
                     if (c + 64 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
-                    store_tokens<Y_F32>(v, tile, lane, out, ldy, x.first + c, x.tokens - c, f, p.N, p.bf16);
+                    put(v, x.first + c, x.tokens - c, f, x.split);
                 }
             }
             if (++acc == 2) {
@@ -765,6 +825,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 acc_phase ^= 1u;
             }
         }
+        staging.finish();
     }
     tear_down(tmem);
 }
@@ -780,6 +841,7 @@ struct GradParams {
     int ntiles, ktiles;
     void *dW;
     int64_t lddw, stridedw;
+    int dw_tma;  // dW is stored to by TMA, through map_dw
     int bf16;
     unsigned int *status;
     uint64_t timeout_ns;
@@ -802,7 +864,8 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, const Shared 
 // first's (cleaned), the first's to the full barrier.
 template <bool DW_F32>
 __global__ void __launch_bounds__(kGradThreads, 1)
-grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const GradParams p)
+grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
+                    const __grid_constant__ CUtensorMap map_dw, const GradParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const Shared sh(smem_raw, kMaxStageB);
@@ -937,10 +1000,11 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
             }
         }
     } else {
-        // ---------------- epilogue: TMEM lane = row of dW; 32 x 32 pieces pass through the staging
-        // tile (16-byte pieces, XOR-swizzled by row) so that stores are 128- or 64-byte row segments
+        // ---------------- epilogue: TMEM lane = row of dW; 32 x 32 pieces pass through the staging tile
+        // to TMA stores or, where TMA cannot store, to 128- or 64-byte row segments
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         float4 *tile = reinterpret_cast<float4 *>(sh.epi + (warp - 2) * 4096);
+        Staging<DW_F32> staging(sh.epi + (warp - 2) * 4096, lane);
         const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -969,6 +1033,24 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                     for (int i = 0; i < 32; ++i) v[i] = 0.0f;
                 }
                 if (k0 >= p.K || n0 >= p.N) continue;
+                if (p.dw_tma) {  // laid out as the tensor map's 128- or 64-byte swizzle
+                    uint8_t *piece = staging.next();
+                    uint4 *row = reinterpret_cast<uint4 *>(piece) + lane * (DW_F32 ? 8 : 4);
+                    if (DW_F32) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            row[j ^ (lane & 7)] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                             __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            row[j ^ ((lane >> 1) & 3)] =
+                                make_uint4(pack_16(v[8 * j], v[8 * j + 1], p.bf16), pack_16(v[8 * j + 2], v[8 * j + 3], p.bf16),
+                                           pack_16(v[8 * j + 4], v[8 * j + 5], p.bf16), pack_16(v[8 * j + 6], v[8 * j + 7], p.bf16));
+                    }
+                    staging.store(&map_dw, piece, int(k0), int(n0), x.group);
+                    continue;
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     tile[lane * 8 + (j ^ (lane & 7))] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -1028,6 +1110,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                 acc_phase ^= 1u;
             }
         }
+        staging.finish();
     }
     tear_down(tmem);
 }
@@ -1048,6 +1131,26 @@ bool make_map(CUtensorMap *map, const void *ptr, bool bf16, int64_t rows, int64_
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(ptr),
               dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A stack of `count` row-major matrices stored to in boxes of 32 x 32.  False where TMA cannot: a box cut
+// by the right edge is written in whole 16-byte pieces, so the rows must end on one.
+bool make_store_map(CUtensorMap *map, void *ptr, int type, int64_t rows, int64_t cols, int64_t ld, int64_t count, int64_t stride,
+                    bool swizzled)
+{
+    auto fn = tensor_map_encoder();
+    const bool f32 = type == GEMM_TYPE_F32;
+    const int size = f32 ? 4 : 2;
+    if (fn == nullptr || cols * size % 16 != 0 || reinterpret_cast<uintptr_t>(ptr) % 16 != 0) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(count)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * size, cuuint64_t(count > 1 ? stride : rows * ld) * size};
+    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              3, ptr, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Two-CTA clusters of `kernel` that can be resident at once; 0 on failure.  `cache`: of this kernel.
@@ -1175,6 +1278,9 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, Tiling 
     p.cap = tiling.cap;
     p.splits = tiling.splits;
     p.split_stride = a.ldy * a.y_rows;
+    CUtensorMap my;
+    std::memset(&my, 0, sizeof(my));
+    p.y_tma = make_store_map(&my, a.Y, a.y_type, a.y_rows, a.N, a.ldy, p.splits, p.split_stride, false);
     p.rows = a.rows;
     p.Y = a.Y;
     p.ldy = a.ldy;
@@ -1196,7 +1302,7 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, Tiling 
     // no more pairs than there can be units
     const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles * p.splits;
     return launch_chained(kernel, dim3(unsigned(2 * (most < pairs ? most : pairs))), kThreads, kSmemBytes, 2, stream, mw, mx, mb,
-                          mi, p);
+                          mi, my, p);
 }
 
 template <int W_MN, int EPI> cudaError_t launch_linear(const DeviceInfo &dev, const GroupedArgs &a, cudaStream_t stream)
@@ -1263,13 +1369,16 @@ cudaError_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, c
     p.dW = a.dW;
     p.lddw = a.lddw;
     p.stridedw = a.stridedw;
+    CUtensorMap mw;
+    std::memset(&mw, 0, sizeof(mw));
+    p.dw_tma = make_store_map(&mw, a.dW, a.dw_type, a.N, a.K, a.lddw, a.groups, a.stridedw, true);
     p.bf16 = bf16;
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
     const int64_t units = int64_t(a.groups) * p.ntiles * p.ktiles;
     if (units >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     return launch_chained(kernel, dim3(unsigned(2 * (units < pairs ? units : pairs))), kGradThreads, kSmemBytes, 2, stream, md, mx,
-                          p);
+                          mw, p);
 }
 
 }  // namespace gemm
