@@ -132,8 +132,10 @@ __device__ __forceinline__ bool nonempty_group(const GroupedArgs &a, int i, int 
 
 // CTA: (8 / KS) runs of feature rows (32, or 16 gate rows with their 16 up rows) of one group times
 // all of its tokens, 8 * NT at a time; KS warps share a run, each summing its part of K.
+//
+// With one token column set (NT = 1) two CTAs share an SM: 128 KB of weights in flight.
 template <class T, class Y, int NT, bool GATED>
-__global__ void __launch_bounds__(kThreads) few_rows_kernel(const GroupedArgs a, const int ks)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(const GroupedArgs a, const int ks)
 {
     extern __shared__ float parts[];  // kWarps x (8 NT) x kRowStride
     constexpr int kTokens = 8 * NT;
@@ -345,9 +347,9 @@ cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, int64_t
 {
     constexpr int kFeat = GATED ? 16 : 32;
     const int64_t runs = (a.N + kFeat - 1) / kFeat;
-    // K is split until there are 16 warps for every SM or a part is shorter than 256
+    // K is split as far as all warps still run at once, 16 to an SM, and a part is not below 256
     int ks = 1;
-    while (ks < kWarps && groups * runs * depth * ks < 16 * int64_t(dev.num_sms) && a.K / (2 * ks) >= 256) ks *= 2;
+    while (ks < kWarps && 2 * groups * runs * depth * ks <= 16 * int64_t(dev.num_sms) && a.K / (2 * ks) >= 256) ks *= 2;
     const int64_t per = kWarps / ks;
     const size_t smem = size_t(kWarps) * 8 * NT * kRowStride * sizeof(float);
     auto *kernel = few_rows_kernel<T, Y, NT, GATED>;

@@ -511,6 +511,14 @@ struct TileRequests {
     __device__ __forceinline__ int parts_a_slice(int n) const { return max(1, min(p.parts, p.cap / n)); }
 };
 
+// Looked up at a unit's start, while its first slices are on their way; the other forms have none.
+struct NoRequests {
+    __device__ __forceinline__ NoRequests(const LinearParams &, const LinearUnit &, int) {}
+    __device__ __forceinline__ bool next(int &, int &, int &, int &) { return false; }
+    __device__ __forceinline__ int parts_a_slice(int) const { return 1; }
+};
+template <int EPI> using RequestsOf = typename std::conditional<EPI == kAdapted, TileRequests, NoRequests>::type;
+
 // W_MN: W stored K x N (features contiguous).
 template <int W_MN, int EPI, bool Y_F32>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -540,6 +548,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         if (leader) tma_prefetch_desc(&map_w);
         for (int u = unit0; ok && u < units; u += step) {
             const LinearUnit x = linear_unit(p, sh, u, group);
+            RequestsOf<EPI> requests(p, x, lane);
             const int f0 = x.feature_tile * kFeatures + int(rank) * (kFeatures / 2);
             const int wg = p.shared_w ? 0 : x.group;
             const uint32_t bytes = 2u * (kStageA + uint32_t(x.width) * 64u);
@@ -568,7 +577,6 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 ring.next();
             }
             if (EPI == kAdapted && ok) {
-                TileRequests requests(p, x, lane);
                 int ad, c0, n, row;
                 while (ok && requests.next(ad, c0, n, row)) {
                     const int most = requests.parts_a_slice(n);
@@ -600,6 +608,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         if (leader) tma_prefetch_desc(&map_x.rows[0]);
         for (int u = unit0; ok && u < units; u += step) {
             const LinearUnit x = linear_unit(p, sh, u, group);
+            RequestsOf<EPI> requests(p, x, lane);
             const int half = x.width / 2;                     // tokens this CTA loads
             const int row0 = x.first + int(rank) * half, end = x.first + x.tokens;
             int4 from = make_int4(0, 0, 0, 0);
@@ -631,7 +640,6 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
             if (EPI == kAdapted && ok) {
                 // the inner products come from the kernel ahead, which itself waited for what x comes from
                 asm volatile("griddepcontrol.wait;" ::: "memory");
-                TileRequests requests(p, x, lane);
                 int ad, c0, n, row;
                 while (ok && requests.next(ad, c0, n, row)) {
                     const int most = requests.parts_a_slice(n);
@@ -669,6 +677,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
             bool ok = true;
             for (int u = unit0; ok && u < units; u += step) {
                 const LinearUnit x = linear_unit(p, sh, u, group);
+                RequestsOf<EPI> requests(p, x, lane);
                 const uint32_t idesc = make_idesc(W_MN, 0, x.width, 256) | fmt;
                 ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
                 if (!ok) break;
@@ -690,7 +699,6 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     ring.next();
                 }
                 if (EPI == kAdapted && ok) {
-                    TileRequests requests(p, x, lane);
                     int ad, c0, n, row;
                     while (ok && requests.next(ad, c0, n, row)) {
                         const uint32_t part_idesc = make_idesc(0, 0, n, 256) | fmt;

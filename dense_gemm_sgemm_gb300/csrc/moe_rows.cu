@@ -23,6 +23,21 @@ template <class T, int VEC> __device__ __forceinline__ void put(T *p, const floa
     else p[0] = from_f32<T>(v[0]);
 }
 
+// Row and column piece of this thread among rows of `cols` pieces; a 32-bit division where the grid
+// allows it (the 64-bit one costs as much as the rest of the kernel's instructions).
+__device__ __forceinline__ void place(int64_t cols, int64_t &row, int64_t &piece)
+{
+    if (gridDim.x <= 0xffffffffu / kThreads) {
+        const unsigned i = blockIdx.x * kThreads + threadIdx.x, c = unsigned(cols);
+        row = i / c;
+        piece = i % c;
+    } else {
+        const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+        row = i / cols;
+        piece = i - row * cols;
+    }
+}
+
 // Thread: VEC columns of one token; the k rows of a token are read by the same threads.
 template <class R, class Y, int VEC>
 __global__ void __launch_bounds__(kThreads)
@@ -30,8 +45,9 @@ combine_kernel(int64_t T, int64_t cols, int k, const R *rows, int64_t ldr, int64
                const float *weights, Y *y, int64_t ldy)
 {
     chain_wait();
-    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t t = i / cols, c = (i - t * cols) * VEC;
+    int64_t t, c;
+    place(cols, t, c);
+    c *= VEC;
     if (t >= T) return;
     float acc[VEC];
 #pragma unroll
@@ -64,8 +80,9 @@ __global__ void __launch_bounds__(kThreads)
 sum_kernel(int64_t rows, int64_t cols, int count, const float *part, int64_t ldp, Y *y, int64_t ldy)
 {
     chain_wait();
-    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t r = i / cols, c = (i - r * cols) * VEC;
+    int64_t r, c;
+    place(cols, r, c);
+    c *= VEC;
     if (r >= rows) return;
     float acc[VEC];
     get<float, VEC>(part + r * ldp + c, acc);
@@ -148,8 +165,9 @@ gated_silu_backward_kernel(int64_t rows, int64_t cols, int64_t I, const X *pre, 
                            X *dpre, int64_t lddp)
 {
     chain_wait();
-    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t r = i / cols, c = (i - r * cols) * VEC;
+    int64_t r, c;
+    place(cols, r, c);
+    c *= VEC;
     if (r >= rows) return;
     float g[VEC], u[VEC], d[VEC], dg[VEC], du[VEC];
     // plain loads: dpre may be pre

@@ -10,8 +10,8 @@
 //
 // The plan is a stable counting sort of the slots by expert in one launch: one cluster of CTAs, every
 // warp owning a contiguous run of slots and a histogram row of its own in shared memory.  Pass 1
-// counts (match.any gives the lanes of a warp that hold the same expert) and leaves each slot's rank
-// in its warp in `where`; the histograms are scanned over warps, CTAs (through distributed shared
+// counts (match.any gives the lanes of a warp that hold the same expert) and keeps each slot's rank
+// in its warp; the histograms are scanned over warps, CTAs (through distributed shared
 // memory) and experts; pass 2 adds them.  No atomics, so the order never varies.  With few tokens
 // the same launch routes them first (the warp's slots are then its own tokens').
 #include <cooperative_groups.h>
@@ -283,9 +283,9 @@ __global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArg
     const int ranks = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t warps = int64_t(ranks) * kWarps, w = int64_t(rank) * kWarps + warp;
-    // this warp's tokens [t0, t1) and slots
+    // this warp's tokens [t0, t1) and slots (below 2^31 of them: 32-bit divisions)
     const int64_t t0 = a.T * w / warps, t1 = a.T * (w + 1) / warps;
-    const int64_t s0 = t0 * k, s1 = t1 * k;
+    const unsigned s0 = unsigned(t0 * k), s1 = unsigned(t1 * k);
 
     for (int i = threadIdx.x; i < kWarps * E; i += blockDim.x) hist[i] = 0u;
     chain_wait();
@@ -296,26 +296,35 @@ __global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArg
     __syncthreads();
 
     uint32_t *mine = hist + warp * E;
-    // slots 8 x 32 at a time, so that their loads are in flight together
-    for (int64_t s = s0; s < s1; s += 256) {
-        int e[8];
+    // Slots 8 x 32 at a time, so that their loads are in flight together.  The first 256 slots of a warp
+    // keep their experts and ranks in registers, the others leave their ranks in `where`.
+    int held[8], held_rank[8];
+    auto count = [&](unsigned s, int (&e)[8], int (&rank_in_warp)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t slot = s + 32 * i + lane;
+            const unsigned slot = s + 32 * i + lane;
             e[i] = slot < s1 ? a.ids[slot] : -1;
             if (e[i] < 0 || e[i] >= E) e[i] = -1;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (s + 32 * i >= s1) break;  // the same for the warp
-            const int64_t slot = s + 32 * i + lane;
+            rank_in_warp[i] = -1;
+            if (s + 32 * i >= s1) continue;  // the same for the warp
             const unsigned same = __match_any_sync(kFull, e[i]);
             const uint32_t before = e[i] >= 0 ? mine[e[i]] : 0u;
             __syncwarp();
             if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] = before + __popc(same);
             __syncwarp();
-            if (slot < s1) a.where[slot] = e[i] >= 0 ? int32_t(before + __popc(same & ((1u << lane) - 1u))) : -1;
+            if (e[i] >= 0) rank_in_warp[i] = int(before + __popc(same & ((1u << lane) - 1u)));
         }
+    };
+    count(s0, held, held_rank);
+    for (unsigned s = s0 + 256; s < s1; s += 256) {
+        int e[8], rank_in_warp[8];
+        count(s, e, rank_in_warp);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s + 32 * i + lane < s1) a.where[s + 32 * i + lane] = rank_in_warp[i];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
@@ -334,12 +343,16 @@ __global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArg
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int e = 2 * threadIdx.x + i;
-        if (e < E)
-            for (int r = 0; r < ranks; ++r) {
-                const uint32_t n = cluster.map_shared_rank(total, r)[e];
-                if (r < rank) before[i] += n;
-                all[i] += n;
+        if (e < E) {
+            uint32_t n[plan_cluster<V>];  // all of the remote reads in flight together
+#pragma unroll
+            for (int r = 0; r < plan_cluster<V>; ++r) n[r] = r < ranks ? cluster.map_shared_rank(total, r)[e] : 0u;
+#pragma unroll
+            for (int r = 0; r < plan_cluster<V>; ++r) {
+                if (r < rank) before[i] += n[r];
+                all[i] += n[r];
             }
+        }
     }
     uint32_t incl = all[0] + all[1];
 #pragma unroll
@@ -364,25 +377,33 @@ __global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArg
         first += all[i];
     }
     __syncthreads();
-    // where holds the ranks that this very thread wrote above
-    for (int64_t s = s0; s < s1; s += 256) {
+    // the totals have been read: no CTA leaves before all have come here (waited for below)
+    if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    auto put = [&](unsigned slot, int e, int rank_in_warp) {
+        if (rank_in_warp >= 0) {
+            const uint32_t p = base[e] + mine[e] + uint32_t(rank_in_warp);
+            a.where[slot] = int32_t(p);
+            a.tokens[p] = int32_t(slot / unsigned(k));
+        } else {
+            a.where[slot] = -1;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (s0 + 32 * i + lane < s1) put(s0 + 32 * i + lane, held[i], held_rank[i]);
+    for (unsigned s = s0 + 256; s < s1; s += 256) {
         int e[8], rank_in_warp[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t slot = s + 32 * i + lane;
+        for (int i = 0; i < 8; ++i) {  // the ranks that this very thread wrote above
+            const unsigned slot = s + 32 * i + lane;
             rank_in_warp[i] = slot < s1 ? a.where[slot] : -1;
             e[i] = slot < s1 ? a.ids[slot] : 0;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t slot = s + 32 * i + lane;
-            if (rank_in_warp[i] < 0) continue;  // no slot, or none of the experts
-            const uint32_t p = base[e[i]] + mine[e[i]] + uint32_t(rank_in_warp[i]);
-            a.where[slot] = int32_t(p);
-            a.tokens[p] = int32_t(slot / k);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (s + 32 * i + lane < s1) put(s + 32 * i + lane, e[i], rank_in_warp[i]);
     }
-    cluster.sync();  // no CTA leaves while another may still read its totals
+    if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 template <int V>
