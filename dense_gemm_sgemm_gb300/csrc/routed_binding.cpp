@@ -6,12 +6,14 @@
 #include <ATen/Functions.h>
 #include <ATen/core/Tensor.h>
 #include <Python.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <optional>
 
 #include "../../include/gemm_gb300.h"
 
@@ -108,16 +110,30 @@ bool truth(PyObject *o)
     if (v < 0) throw python_error();
     return v != 0;
 }
-// The given stream, or the current one of the tensor's device.
-void *stream_of(PyObject *o, const at::Tensor &t)
-{
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-    if (PyLong_Check(o)) return reinterpret_cast<void *>(uintptr_t(integer(o)));
-    PyObject *handle = PyObject_GetAttrString(o, "cuda_stream");
-    if (handle == nullptr) throw python_error();
-    const pybind11::object owned = pybind11::reinterpret_steal<pybind11::object>(handle);
-    return reinterpret_cast<void *>(uintptr_t(integer(handle)));
-}
+// The tensor's device and the given stream, or the device's current one, made current for the call:
+// what the call allocates -- its outputs and the space that it releases on return -- belongs to the
+// stream that its kernels run on.
+struct Stream {
+    c10::cuda::CUDAGuard device;
+    std::optional<c10::cuda::CUDAStreamGuard> current;
+    void *handle;
+    Stream(PyObject *o, const at::Tensor &t) : device(t.device())
+    {
+        if (o == Py_None) {
+            handle = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
+            return;
+        }
+        if (PyLong_Check(o)) {
+            handle = reinterpret_cast<void *>(uintptr_t(integer(o)));
+        } else {
+            PyObject *attr = PyObject_GetAttrString(o, "cuda_stream");
+            if (attr == nullptr) throw python_error();
+            const pybind11::object owned = pybind11::reinterpret_steal<pybind11::object>(attr);
+            handle = reinterpret_cast<void *>(uintptr_t(integer(attr)));
+        }
+        current.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), t.get_device()));
+    }
+};
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like)
 {
@@ -178,6 +194,7 @@ void count_args(Py_ssize_t n, Py_ssize_t wanted)
 // logits, top_k, bias, score, groups, groups_kept, group_top, renormalise, scale, stream
 BOUND(moe_route, 10)
     const Matrix x = matrix(a[0], "logits");
+    const Stream stream(a[9], x.t);
     const int64_t T = x.rows, E = x.cols, k = small(a[1]);
     TORCH_CHECK_VALUE(k >= 1 && k <= 1024, "top_k: ", k);
     const gemm_type_t type = type_of(x.t.scalar_type(), "logits");
@@ -188,11 +205,10 @@ BOUND(moe_route, 10)
     const int groups = small(a[4]), kept = small(a[5]), top = small(a[6]);
     const bool renormalise = truth(a[7]);
     const float scale = real(a[8]);
-    void *stream = stream_of(a[9], x.t);
     call("gemm_moe_route", [&] {
         return gemm_moe_route(type, T, E, x.data(), x.ld, bias, score, groups, kept, top, int(k), renormalise, scale,
                               ids.data_ptr<int32_t>(), weights.data_ptr<float>(), offsets.data_ptr<int32_t>(),
-                              tokens.data_ptr<int32_t>(), where.data_ptr<int32_t>(), stream);
+                              tokens.data_ptr<int32_t>(), where.data_ptr<int32_t>(), stream.handle);
     });
     return tuple(ids, weights, offsets, tokens, where);
 END_BOUND
@@ -200,6 +216,7 @@ END_BOUND
 // dweights, logits, ids, score, renormalise, scale, stream
 BOUND(moe_route_backward, 7)
     const Matrix x = matrix(a[1], "logits"), id = matrix(a[2], "ids");
+    const Stream stream(a[6], x.t);
     const int64_t T = x.rows, E = x.cols, k = id.cols;
     const gemm_type_t type = type_of(x.t.scalar_type(), "logits");
     const float *dw = floats(a[0], "dweights", T * k);
@@ -208,10 +225,9 @@ BOUND(moe_route_backward, 7)
     const auto score = static_cast<gemm_score_t>(small(a[3]));
     const bool renormalise = truth(a[4]);
     const float scale = real(a[5]);
-    void *stream = stream_of(a[6], x.t);
     call("gemm_moe_route_backward", [&] {
         return gemm_moe_route_backward(type, T, E, dw, x.data(), x.ld, ids, score, int(k), renormalise, scale, out.data_ptr(), E,
-                                       stream);
+                                       stream.handle);
     });
     return wrap(out);
 END_BOUND
@@ -219,14 +235,14 @@ END_BOUND
 // ids, experts, stream
 BOUND(moe_plan, 3)
     const Matrix id = matrix(a[0], "ids");
+    const Stream stream(a[2], id.t);
     const int64_t T = id.rows, k = id.cols, E = integer(a[1]);
     TORCH_CHECK_VALUE(E >= 1 && E <= 1024, "experts: ", E);
     const int32_t *ids = ints(a[0], "ids", T * k);
     at::Tensor offsets = fresh({E + 1}, at::kInt, id.t), tokens = fresh({T * k}, at::kInt, id.t), where = fresh({T, k}, at::kInt, id.t);
-    void *stream = stream_of(a[2], id.t);
     call("gemm_moe_plan", [&] {
         return gemm_moe_plan(T, E, int(k), ids, offsets.data_ptr<int32_t>(), tokens.data_ptr<int32_t>(),
-                             where.data_ptr<int32_t>(), stream);
+                             where.data_ptr<int32_t>(), stream.handle);
     });
     return tuple(offsets, tokens, where);
 END_BOUND
@@ -234,14 +250,14 @@ END_BOUND
 // x, where, weights, stream
 BOUND(moe_dispatch, 4)
     const Matrix x = matrix(a[0], "x"), slot = matrix(a[1], "where");
+    const Stream stream(a[3], x.t);
     const int64_t T = x.rows, H = x.cols, k = slot.cols, slots = T * k;
     const gemm_type_t type = type_of(x.t.scalar_type(), "x");
     const int32_t *where = ints(a[1], "where", slots);
     const float *weights = floats(a[2], "weights", slots, true);
     Padded out = padded(slots, H, x.t.scalar_type(), x.t);
-    void *stream = stream_of(a[3], x.t);
     call("gemm_moe_dispatch", [&] {
-        return gemm_moe_dispatch(type, T, H, int(k), x.data(), x.ld, where, weights, slots, out.t.data_ptr(), out.ld, stream);
+        return gemm_moe_dispatch(type, T, H, int(k), x.data(), x.ld, where, weights, slots, out.t.data_ptr(), out.ld, stream.handle);
     });
     return wrap(out.t);
 END_BOUND
@@ -249,6 +265,7 @@ END_BOUND
 // rows, where, weights, out_dtype, stream
 BOUND(moe_combine, 5)
     const Matrix r = matrix(a[0], "rows"), slot = matrix(a[1], "where");
+    const Stream stream(a[4], r.t);
     const int64_t T = slot.rows, k = slot.cols, slots = T * k;
     const gemm_type_t type = type_of(r.t.scalar_type(), "rows");
     const int32_t *where = ints(a[1], "where", slots);
@@ -256,10 +273,9 @@ BOUND(moe_combine, 5)
     const at::ScalarType dtype = dtype_of(a[3], r.t.scalar_type());
     const gemm_type_t y_type = type_of(dtype, "out_dtype");
     Padded y = padded(T, r.cols, dtype, r.t);
-    void *stream = stream_of(a[4], r.t);
     call("gemm_moe_combine", [&] {
         return gemm_moe_combine(type, y_type, T, r.cols, int(k), r.data(), r.ld, r.rows, where, weights, y.t.data_ptr(), y.ld,
-                                stream);
+                                stream.handle);
     });
     return wrap(y.t);
 END_BOUND
@@ -267,6 +283,7 @@ END_BOUND
 // dy, rows, where, weights, stream
 BOUND(moe_combine_backward, 5)
     const Matrix dy = matrix(a[0], "dy"), r = matrix(a[1], "rows"), slot = matrix(a[2], "where");
+    const Stream stream(a[4], dy.t);
     const int64_t T = dy.rows, H = dy.cols, k = slot.cols, slots = T * k;
     same(r.cols, H, "columns of rows");
     const gemm_type_t type = type_of(dy.t.scalar_type(), "dy"), rows_type = type_of(r.t.scalar_type(), "rows");
@@ -274,10 +291,9 @@ BOUND(moe_combine_backward, 5)
     const float *weights = floats(a[3], "weights", slots, true);
     Padded drows = padded(r.rows, H, dy.t.scalar_type(), dy.t);
     at::Tensor dweights = fresh({T, k}, at::kFloat, dy.t);
-    void *stream = stream_of(a[4], dy.t);
     call("gemm_moe_combine_backward", [&] {
         return gemm_moe_combine_backward(type, rows_type, T, H, int(k), dy.data(), dy.ld, r.data(), r.ld, r.rows, where, weights,
-                                         drows.t.data_ptr(), drows.ld, dweights.data_ptr<float>(), stream);
+                                         drows.t.data_ptr(), drows.ld, dweights.data_ptr<float>(), stream.handle);
     });
     return tuple(drows.t, dweights);
 END_BOUND
@@ -285,15 +301,15 @@ END_BOUND
 // pre, dh, stream
 BOUND(gated_silu_backward, 3)
     const Matrix pre = matrix(a[0], "pre"), dh = matrix(a[1], "dh");
+    const Stream stream(a[2], pre.t);
     same(pre.cols % 2, 0, "odd columns of pre");
     same(dh.rows, pre.rows, "rows of dh");
     same(dh.cols, pre.cols / 2, "columns of dh");
     const gemm_type_t type = type_of(pre.t.scalar_type(), "pre"), dh_type = type_of(dh.t.scalar_type(), "dh");
     Padded out = padded(pre.rows, pre.cols, pre.t.scalar_type(), pre.t);
-    void *stream = stream_of(a[2], pre.t);
     call("gemm_gated_silu_backward", [&] {
         return gemm_gated_silu_backward(type, dh_type, pre.rows, dh.cols, pre.data(), pre.ld, dh.data(), dh.ld, out.t.data_ptr(),
-                                        out.ld, stream);
+                                        out.ld, stream.handle);
     });
     return wrap(out.t);
 END_BOUND
@@ -301,6 +317,7 @@ END_BOUND
 // x, w, offsets, rows, op, gated, out_dtype, pre, stream
 BOUND(grouped_linear, 9)
     const Matrix x = matrix(a[0], "x"), w = matrix(a[1], "w", 3);
+    const Stream stream(a[8], x.t);
     const at::ScalarType in = x.t.scalar_type(), dtype = dtype_of(a[6], in);
     same_type(w.t, in, "w");
     const gemm_type_t type = type_of(in, "x"), y_type = type_of(dtype, "out_dtype");
@@ -332,11 +349,10 @@ BOUND(grouped_linear, 9)
     }
     at::Tensor work;  // space to lay gathered rows out in, where the library would use it
     if (rows != nullptr && y_rows > 64 * groups) work = fresh({y_rows * ((K + 7) & ~int64_t(7))}, in, x.t);
-    void *stream = stream_of(a[8], x.t);
     call("gemm_grouped_linear", [&] {
         return gemm_grouped_linear(type, y_type, groups, offsets, op, gated, N, K, x.data(), x.ld, x.rows, rows, w.data(), w.ld,
                                    w.t.stride(0), y.t.data_ptr(), y.ld, y_rows, pre, ldp,
-                                   work.defined() ? work.data_ptr() : nullptr, stream);
+                                   work.defined() ? work.data_ptr() : nullptr, stream.handle);
     });
     return wrap(y.t);
 END_BOUND
@@ -344,6 +360,7 @@ END_BOUND
 // dy, x, offsets, out_dtype, stream
 BOUND(grouped_weight_grad, 5)
     const Matrix dy = matrix(a[0], "dy"), x = matrix(a[1], "x");
+    const Stream stream(a[4], dy.t);
     const at::ScalarType in = dy.t.scalar_type(), dtype = dtype_of(a[3], at::kFloat);
     same_type(x.t, in, "x");
     same(x.rows, dy.rows, "rows of x");
@@ -352,10 +369,9 @@ BOUND(grouped_weight_grad, 5)
     TORCH_CHECK_VALUE(groups >= 0, "offsets: one value at least is wanted");
     const int32_t *offsets = ints(a[2], "offsets", groups + 1);
     at::Tensor dw = fresh({groups, N, ld}, dtype, dy.t);
-    void *stream = stream_of(a[4], dy.t);
     call("gemm_grouped_weight_grad", [&] {
         return gemm_grouped_weight_grad(type, dw_type, groups, offsets, N, K, dy.data(), dy.ld, x.data(), x.ld, dy.rows,
-                                        dw.data_ptr(), ld, N * ld, stream);
+                                        dw.data_ptr(), ld, N * ld, stream.handle);
     });
     return wrap(ld == K ? dw : dw.narrow(2, 0, K));
 END_BOUND
@@ -363,6 +379,7 @@ END_BOUND
 // x, w, a, b, segments, adapters, scales, out_dtype, stream
 BOUND(lora_linear, 9)
     const Matrix x = matrix(a[0], "x"), w = matrix(a[1], "w"), A = matrix(a[2], "a", 3), B = matrix(a[3], "b", 3);
+    const Stream stream(a[8], x.t);
     const at::ScalarType in = x.t.scalar_type(), dtype = dtype_of(a[7], in);
     same_type(w.t, in, "w");
     same_type(A.t, in, "a");
@@ -379,11 +396,10 @@ BOUND(lora_linear, 9)
     const float *scales = floats(a[6], "scales", count, true);
     Padded y = padded(T, N, dtype, x.t);
     at::Tensor work = fresh({gemm_lora_work_bytes(T, N, K, requests, R)}, at::kByte, x.t);
-    void *stream = stream_of(a[8], x.t);
     call("gemm_lora_linear", [&] {
         return gemm_lora_linear(type, y_type, T, N, K, x.data(), x.ld, w.data(), w.ld, requests, segments, adapters, count, R,
                                 A.data(), A.ld, A.t.stride(0), B.data(), B.ld, B.t.stride(0), scales, y.t.data_ptr(), y.ld,
-                                work.data_ptr(), stream);
+                                work.data_ptr(), stream.handle);
     });
     return wrap(y.t);
 END_BOUND
