@@ -180,24 +180,21 @@ __device__ void route_token(const RouteArgs &a, int64_t t, int lane, float *scra
     float x[V], s[V];
     load_row<V>(a, t, lane, x);
     scores<V>(a.score, x, s);
-    uint32_t key[V];  // of the value the choice goes by
+    // what a run's value is made of, and the key of what the choice goes by
+    float value[V];
+    uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = lane * V + v;
-        float c = x[v];
-        if (a.bias != nullptr && e < E && c > -INFINITY) c = s[v] + __ldg(a.bias + e);
-        key[v] = e < E ? order_key(c) : 0u;
+        const bool live = e < E && x[v] > -INFINITY;
+        value[v] = !live ? -INFINITY : a.bias != nullptr ? s[v] + __ldg(a.bias + e) : s[v];
+        if (isnan(value[v])) value[v] = -INFINITY;
+        key[v] = order_key(a.bias != nullptr ? value[v] : live ? x[v] : -INFINITY);
     }
     if (a.groups > 1) {
         const int size = E / a.groups;
         // whole lanes a run, a power of two of them: reduced by shuffles
         const int lanes = size % V == 0 && ((size / V) & (size / V - 1)) == 0 ? size / V : 0;
-        float value[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = lane * V + v;
-            value[v] = key[v] == 0u ? -INFINITY : a.bias != nullptr ? s[v] + __ldg(a.bias + e) : s[v];
-        }
         uint32_t gkey = run_keys<V>(a, value, lane, lanes, scratch);
         uint32_t kept = 0u;  // bit of the lane that holds the run's key
         for (int n = 0; n < a.groups_kept; ++n) {
@@ -220,9 +217,11 @@ __device__ void route_token(const RouteArgs &a, int64_t t, int lane, float *scra
             }
         }
     }
-    // Lane j keeps choice j.
+    // Lane j keeps choice j; its score comes from shared memory in the end.
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (lane * V + v < E) scratch[lane * V + v] = s[v];
     int my_id = -1;
-    float my_s = 0.0f, sum = 0.0f;
     for (int j = 0; j < a.top_k; ++j) {
         uint32_t best = key[0];
 #pragma unroll
@@ -231,26 +230,21 @@ __device__ void route_token(const RouteArgs &a, int64_t t, int lane, float *scra
         if (top == 0u) break;
         const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
         int at = 0;
-        float sv = 0.0f;
         if (lane == owner) {
 #pragma unroll
             for (int v = V - 1; v >= 0; --v)  // the lowest of equals
-                if (key[v] == top) {
-                    at = v;
-                    sv = s[v];
-                }
+                if (key[v] == top) at = v;
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (v == at) key[v] = 0u;
         }
         const int e = __shfl_sync(kFull, owner * V + at, owner);
-        sv = __shfl_sync(kFull, sv, owner);
-        if (lane == j) {
-            my_id = e;
-            my_s = sv;
-        }
-        sum += sv;
+        if (lane == j) my_id = e;
     }
+    __syncwarp();
+    const float my_s = my_id >= 0 ? scratch[my_id] : 0.0f;
+    const float sum = warp_sum(my_s);
+    __syncwarp();  // scratch is read before the next token overwrites it
     if (lane < a.top_k) {
         float w = my_s;
         if (a.renormalise) w = sum > 0.0f ? my_s / sum : 0.0f;
