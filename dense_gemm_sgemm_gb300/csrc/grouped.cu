@@ -52,7 +52,7 @@ cudaError_t allow_large_cluster_once(const void *kernel)
 // 14 / 28, 64 tokens 30 / 37, 96 tokens 45 / 36.
 bool takes_few_rows(const DeviceInfo &dev, const GroupedArgs &a)
 {
-    if (a.K == 0 || a.x_rows == 0) return true;
+    if (a.K == 0) return true;
     if (a.opW != GEMM_OP_T) return false;
     const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;  // at most that many have rows
     // GEMM_GB300_GROUPED_FEW=n (sweeps only): the few-rows kernel up to n rows a group
@@ -64,6 +64,7 @@ bool takes_few_rows(const DeviceInfo &dev, const GroupedArgs &a)
 gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &call, cudaStream_t stream)
 {
     GroupedArgs a = call;
+    if (a.x_rows == 0) a.K = 0;  // every row is outside X: zeros, and W is not read
     const int64_t groups = a.y_rows < a.groups ? a.y_rows : a.groups;
     cudaError_t e = cudaSuccess;
     if (takes_few_rows(dev, a)) {
@@ -74,7 +75,7 @@ gemm_status_t launch_grouped(const DeviceInfo &dev, const GroupedArgs &call, cud
         // laying the rows out first (64 groups of 512 rows, 2 x 1024 x 2048 gated: gathered 617 us,
         // contiguous 206 us and the copy), small ones gather.
         if (a.rows != nullptr && a.work != nullptr && a.y_rows > 64 * groups) {
-            const int64_t ld = (a.K + 7) / 8 * 8;
+            const int64_t ld = (a.K + 63) / 64 * 64;  // whole 128-byte lines, as the copies read them
             e = launch_gather(a, a.work, ld, stream);
             a.X = a.work;
             a.ldx = ld;

@@ -116,8 +116,8 @@ __device__ __forceinline__ uint32_t pack_16(float lo, float hi, bool bf16)
     return uint32_t(to_16(lo, bf16)) | uint32_t(to_16(hi, bf16)) << 16;
 }
 
-// The ring: as many stages of kStageA + b_bytes as fit.  A slice takes about 1.5 us from its copies'
-// issue to its release, so the bytes in flight are what small tiles are short of.
+// The ring: as many stages of kStageA + b_bytes as fit, for the bytes in flight that small tiles are
+// short of (128 groups of 4 rows, 2048 x 2048: 158 us, with five stages 167).
 __host__ __device__ constexpr int ring_stages(int b_bytes)
 {
     return kRingBytes / (kStageA + b_bytes) < kMaxStages ? kRingBytes / (kStageA + b_bytes) : kMaxStages;
@@ -275,7 +275,8 @@ __device__ __forceinline__ void commit_both(uint32_t bar)
 
 // The warp has its accumulator columns in registers: one arrival on the issuer's barrier, which may be
 // the peer's.  Released at CTA scope only: a release at cluster scope would wait for the warp's global
-// stores (8000 cycles a tile in all, against 3000).
+// stores (the weight gradient of 32 groups of 64 rows, 2048 x 1024, took 57 us with such an arrival
+// after the stores, 47 with this one before them).
 __device__ __forceinline__ void release_accumulator(uint32_t bar_cluster, int lane)
 {
     tc_fence_before();
@@ -459,7 +460,8 @@ struct TileRequests {
     __device__ __forceinline__ TileRequests(const LinearParams &params, const LinearUnit &x, int l)
         : p(params), t0(x.first), t1(x.first + x.tokens), lane(l), skip(x.split)
     {
-        // requests that end at or before the tile's first token, 32 candidates at a time: whole runs, then the run that is left
+        // requests that end at or before the tile's first token, 32 candidates at a time: whole runs,
+        // then the run that is left
         q0 = 0;
         for (int n = p.requests; n > 0;) {
             const int run = (n + 31) / 32, last = (lane + 1) * run - 1;
@@ -1317,8 +1319,9 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, Tiling 
     }
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
-    // no more pairs than there can be units
+    // no more pairs than there can be units, which are counted in 32 bits
     const int64_t most = ((a.y_rows < a.groups ? a.y_rows : a.groups) + a.y_rows / p.cap) * p.ftiles * p.splits;
+    if (most >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     return launch_chained(kernel, dim3(unsigned(2 * (most < pairs ? most : pairs))), kThreads, kSmemBytes, 2, stream, mw, mx, mb,
                           mi, my, p);
 }

@@ -475,9 +475,9 @@ cudaError_t launch_plan_t(const RouteArgs &a, cudaStream_t stream)
     const int64_t per_cta = V > 0 ? 2 * kWarps : 128 * kWarps;
     int ranks = 1;
     while (ranks < plan_cluster<V> && a.T * (V > 0 ? 1 : a.top_k) > ranks * per_cta) ranks *= 2;
-    if (plan_cluster<V> > 8 && ranks > 8) {
-        e = allow_large_cluster_once(plan_kernel<V>);
-        if (e != cudaSuccess) return e;
+    if (ranks > 8 && allow_large_cluster_once(plan_kernel<V>) != cudaSuccess) {
+        cudaGetLastError();
+        ranks = 8;
     }
     return launch_chained(plan_kernel<V>, dim3(ranks), kWarps * 32, smem, ranks, stream, a);
 }

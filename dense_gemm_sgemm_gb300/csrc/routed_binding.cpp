@@ -348,7 +348,7 @@ BOUND(grouped_linear, 9)
         ldp = m.ld;
     }
     at::Tensor work;  // space to lay gathered rows out in, where the library would use it
-    if (rows != nullptr && y_rows > 64 * groups) work = fresh({y_rows * ((K + 7) & ~int64_t(7))}, in, x.t);
+    if (rows != nullptr && y_rows > 64 * groups) work = fresh({y_rows * ((K + 63) & ~int64_t(63))}, in, x.t);
     call("gemm_grouped_linear", [&] {
         return gemm_grouped_linear(type, y_type, groups, offsets, op, gated, N, K, x.data(), x.ld, x.rows, rows, w.data(), w.ld,
                                    w.t.stride(0), y.t.data_ptr(), y.ld, y_rows, pre, ldp,

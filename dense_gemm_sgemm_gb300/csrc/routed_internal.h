@@ -203,7 +203,7 @@ struct GroupedArgs {
     void *pre;
     int64_t ldp;
     Adapters ad;
-    // gathered rows: y_rows x (K rounded up to 8) elements; adapters: split_bytes() of partial sums; or
+    // gathered rows: y_rows x (K rounded up to 64) elements; adapters: split_bytes() of partial sums; or
     // NULL
     void *work;
 };

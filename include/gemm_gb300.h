@@ -415,7 +415,7 @@ GEMM_API gemm_status_t gemm_gated_silu_backward(gemm_type_t type, gemm_type_t dh
  * offsets (groups + 1 values) must not decrease; values are clamped to [0, y_rows].  Y must not
  * overlap the inputs.  K == 0 writes zeros.
  *
- * work: y_rows * (K rounded up to a multiple of 8) elements of `type` for the call to use, or NULL.
+ * work: y_rows * (K rounded up to a multiple of 64) elements of `type` for the call to use, or NULL.
  * With it, gathered rows (rows not NULL) of more than 64 positions per group on average are laid
  * out contiguously first, which is faster than gathering them in the product; the result is the
  * same.

@@ -134,6 +134,18 @@ def test_rows_past_32_bits():
     assert torch.equal(back[P - 2], y[0]) and torch.equal(back[0], y[P // 2 - 1])
 
 
+@pytest.mark.parametrize("opW", ["T", "N"])
+def test_no_rows_to_read(opW):
+    # every position's row is outside an empty x: zeros, and the weights (fewer rows stored than the
+    # other op would read) are left alone
+    w = _rand(2, 8, 520) if opW == "N" else _rand(2, 520, 8)
+    x = torch.empty(0, 8, dtype=torch.float16, device="cuda")
+    off = torch.tensor([0, 3, 200], dtype=torch.int32, device="cuda")
+    rows = torch.zeros(200, dtype=torch.int32, device="cuda")
+    y = g.grouped_linear(x, w, off, rows=rows, opW=opW)
+    assert y.shape == (200, 520) and (y == 0).all()
+
+
 def test_refusals():
     x, w = _rand(8, 16), _rand(2, 24, 16)
     off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
