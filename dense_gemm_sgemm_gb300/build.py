@@ -84,7 +84,7 @@ def _link_binding(obj):
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     # the library by its name, found beside the binding; torch's are loaded by importing torch
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", OUT_DIR, f"-l:{LIB_NAME}",
-           "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+           "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}{r.stderr}")

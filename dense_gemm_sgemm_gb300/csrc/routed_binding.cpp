@@ -5,6 +5,7 @@
 // Nothing is computed in this file; every function ends in one call of include/gemm_gb300.h.
 #include <ATen/Functions.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -135,9 +136,10 @@ struct Stream {
     }
 };
 
+// New memory from torch's allocator (without the dispatcher's way to the same function).
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like)
 {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 // Rows on 16-byte boundaries: the leading dimension a multiple of 8 elements.
 struct Padded {
