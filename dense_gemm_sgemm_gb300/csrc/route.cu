@@ -409,27 +409,25 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
     const int64_t t = int64_t(blockIdx.x) * kRouteWarps + warp;
     if (t >= a.T) return;
     const int E = a.E, k = a.top_k;
+    extern __shared__ float route_smem[];
+    float *row = route_smem + warp * E;  // by expert: scores, then gradients of scores
     float x[V], s[V], ds[V];
     load_row<V>(a, t, lane, x);
     scores<V>(a.score, x, s);
 #pragma unroll
-    for (int v = 0; v < V; ++v) ds[v] = 0.0f;
+    for (int v = 0; v < V; ++v)
+        if (lane * V + v < E) row[lane * V + v] = s[v];
+    __syncwarp();
     // lane j holds choice j: its expert, score and gradient
     int id = -1;
     float dw = 0.0f, sel = 0.0f;
     if (lane < k) {
         id = ids[t * k + lane];
         if (id < 0 || id >= E) id = -1;
-        if (id >= 0) dw = dweights[t * k + lane];
-    }
-    for (int j = 0; j < k; ++j) {
-        const int e = __shfl_sync(kFull, id, j);
-        float sv = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (lane * V + v == e) sv = s[v];
-        sv = __shfl_sync(kFull, sv, e >= 0 ? e / V : 0);
-        if (lane == j && id >= 0) sel = sv;
+        if (id >= 0) {
+            dw = dweights[t * k + lane];
+            sel = row[id];
+        }
     }
     float g = a.scale * dw;
     if (a.renormalise) {
@@ -438,13 +436,25 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
         const float mean = warp_sum(dw * p);
         g = S > 0.0f ? a.scale * (dw - mean) / S : 0.0f;
     }
-    for (int j = 0; j < k; ++j) {
-        const int e = __shfl_sync(kFull, id, j);
-        const float gj = __shfl_sync(kFull, g, j);
+    __syncwarp();
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (lane * V + v == e) ds[v] += gj;
+    for (int v = 0; v < V; ++v)
+        if (lane * V + v < E) row[lane * V + v] = 0.0f;
+    __syncwarp();
+    // an expert named twice gets the sum, in the order of the choices
+    const unsigned same = __match_any_sync(kFull, id);
+    if (__any_sync(kFull, id >= 0 && (same & (same - 1u)) != 0u)) {
+        float all = 0.0f;
+        for (int j = 0; j < k; ++j) {
+            const float gj = __shfl_sync(kFull, g, j);
+            if ((same >> j) & 1u) all += gj;
+        }
+        g = all;
     }
+    if (id >= 0 && lane == __ffs(same) - 1) row[id] = g;
+    __syncwarp();
+#pragma unroll
+    for (int v = 0; v < V; ++v) ds[v] = lane * V + v < E ? row[lane * V + v] : 0.0f;
     float mean = 0.0f;  // sum of ds * s; 0 by its definition when the weights are renormalised
     if (a.score == GEMM_SCORE_SOFTMAX && !a.renormalise) {
 #pragma unroll
@@ -548,8 +558,8 @@ cudaError_t launch_route_backward(const RouteArgs &call, const float *dweights, 
     const bool wide = wide_rows(a.type, dlogits, ldd);
     return by_values_per_lane(a.E, [&](auto v) {
         const unsigned blocks = unsigned((a.T + kRouteWarps - 1) / kRouteWarps);
-        return launch_chained(route_backward_kernel<decltype(v)::value>, dim3(blocks), kRouteWarps * 32, 0, 1, stream, a,
-                              dweights, ids, dlogits, ldd, wide);
+        return launch_chained(route_backward_kernel<decltype(v)::value>, dim3(blocks), kRouteWarps * 32,
+                              size_t(kRouteWarps) * a.E * 4, 1, stream, a, dweights, ids, dlogits, ldd, wide);
     });
 }
 

@@ -196,3 +196,16 @@ def test_gradient_16_bit(dtype):
     _weights_of(xd, ids.long(), "softmax", False, 1.0).backward(dw.double())
     size = dw.abs().max().double() * torch.softmax(xd, 1).detach()
     ref.assert_within(got, xd.grad, 2 * 64 * 2.0 ** -24 * size, "dlogits")
+
+
+def test_gradient_of_an_expert_named_twice():
+    # given choices may repeat an expert: its gradients add up
+    x = torch.randn(3, 12, generator=torch.Generator().manual_seed(4))
+    ids = torch.tensor([[5, 5, 5], [2, 7, 2], [-1, 3, 3]], dtype=torch.int32)
+    dw = torch.tensor([[1.0, -2.0, 0.5], [0.25, 1.0, 3.0], [9.0, 1.0, 1.0]])
+    for score in ("softmax", "sigmoid"):
+        for renormalise in (True, False):
+            got = g.moe_route_backward(dw.cuda(), x.cuda(), ids.cuda(), score=score, renormalise=renormalise)
+            xd = x.double().requires_grad_(True)
+            _weights_of(xd, ids.long(), score, renormalise, 1.0).backward(dw.double())
+            assert (got.double().cpu() - xd.grad).abs().max() <= 64 * 2.0 ** -24 * 10
