@@ -160,7 +160,7 @@ def whole_job_value(local_total_ms, steps, flops_per_step, world, device=None):
 # The CUDA sources each profiled kernel is built from (its launch planning included).
 KERNEL_SOURCES = {
     "sgemm_ffma": ("sgemm_*", "gemm_internal.h"),
-    "hgemm_tcgen05": ("hgemm_tcgen05.cu", "gemm_internal.h"),
+    "hgemm_tcgen05": ("hgemm_tcgen05.cu", "tcgen05_ptx.cuh", "tensor_map.h", "gemm_internal.h"),
 }
 
 
