@@ -21,7 +21,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRowStride = 36;  // floats between tokens of a warp's partial tile: 8 t + g, no bank twice
+// Floats between tokens of a warp's partial tile of MT x 16 rows: 8 t + g, no bank twice.
+template <int MT> constexpr int kRowStride = MT <= 2 ? 36 : 68;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Rows that one warp reads once: no line of L1 for them.
@@ -38,7 +39,7 @@ __device__ __forceinline__ uint4 load_stream(const void *p)
 // this lane's group in the lower and upper half of tile mt; x[nt]: the token row of this lane's
 // group, NULL for a column of zeros.
 //
-// Registers of loads in flight: 96, or 64 where a CTA's 16 warps leave a thread 128 registers.
+// FLIGHT: registers of loads in flight, 64 where a CTA's 16 warps leave a thread 128 registers.
 template <class T, int MT, int NT, int FLIGHT = 96>
 __device__ __forceinline__ void warp_product(const T *const (&w)[MT][2], const T *const (&x)[NT], int64_t kb,
                                              int64_t ke, int64_t K, int lane, float (&acc)[MT][NT][4])
@@ -94,7 +95,7 @@ __device__ __forceinline__ void put_partial(float *part, const float (&acc)[MT][
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                part[(n * 8 + 2 * t + (c & 1)) * kRowStride + m * 16 + g + 8 * (c >> 1)] = acc[m][n][c];
+                part[(n * 8 + 2 * t + (c & 1)) * kRowStride<MT> + m * 16 + g + 8 * (c >> 1)] = acc[m][n][c];
 }
 
 __device__ __forceinline__ int32_t clamp_to(int32_t v, int64_t hi) { return v < 0 ? 0 : v > hi ? int32_t(hi) : v; }
@@ -137,7 +138,8 @@ __device__ __forceinline__ bool nonempty_group(const GroupedArgs &a, int i, int 
 template <class T, class Y, int NT, bool GATED>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(const GroupedArgs a, const int ks)
 {
-    extern __shared__ float parts[];  // kWarps x (8 NT) x kRowStride
+    extern __shared__ float parts[];  // kWarps x (8 NT) x kStride
+    constexpr int kStride = kRowStride<2>;
     constexpr int kTokens = 8 * NT;
     constexpr int kFeat = GATED ? 16 : 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
                 for (int c = 0; c < 4; ++c) acc[m][n][c] = 0.0f;
         warp_product<T, 2, NT>(w, x, kb, ke, a.K, lane, acc);
         __syncthreads();  // the partial tiles of the previous tokens have been read
-        put_partial<2, NT>(parts + warp * kTokens * kRowStride, acc, lane);
+        put_partial<2, NT>(parts + warp * kTokens * kStride, acc, lane);
         // adapters: their inner products come from the kernel before this one
         if (a.ad.b != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
         __syncthreads();
@@ -190,11 +192,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
             const int64_t feat = int64_t(blockIdx.x) * block_feat + f;
             if (n0 + n >= rows || feat >= a.N) continue;
             const int64_t p = first + n0 + n;
-            const float *src = parts + ((f / kFeat) * ks * kTokens + n) * kRowStride + f % kFeat;
+            const float *src = parts + ((f / kFeat) * ks * kTokens + n) * kStride + f % kFeat;
             float v = 0.0f, u = 0.0f;
             for (int q = 0; q < ks; ++q) {
-                v += src[q * kTokens * kRowStride];
-                if (GATED) u += src[q * kTokens * kRowStride + 16];
+                v += src[q * kTokens * kStride];
+                if (GATED) u += src[q * kTokens * kStride + 16];
             }
             if (GATED) {
                 if (a.pre != nullptr) {
@@ -238,9 +240,9 @@ template <class T, int PARTS> __device__ __forceinline__ void split(float x, uin
 }
 
 // Inner products of the adapters: inner[t][r] = scale * sum_k X[t][k] A_a[r][k] for 16 MT ranks of up to
-// 8 NT GROUPS tokens of one request: GROUPS sets of warps take 8 NT tokens each, and K is split over
-// the warps of a set.  Bound by latency for few tokens, so 16 warps share K; for a prompt by what the
-// CTAs draw from L2, so two sets share the reads of the adapter's rows.
+// 8 NT tokens of one request, K split over the WARPS of the CTA.  Bound by latency for few tokens, where
+// 16 warps share K; for a prompt by what the CTAs draw from L2, where one CTA takes 64 ranks, so that
+// its tokens' rows are read once (launch_shrink_t's callers give the figures).
 //
 // CTA i takes item i of an enumeration that needs no scan: cutting the tokens both at multiples of the
 // tile and at the request boundaries, request s has the items t = segments[s] / tile + s ..
@@ -248,13 +250,11 @@ template <class T, int PARTS> __device__ __forceinline__ void split(float x, uin
 //
 // PARTS = 0 writes the few-rows form of the inner products, else the tcgen05 form (InnerLayout), for
 // which 8 NT is 32.
-constexpr int kShrinkWarps = 16;
-template <class T, int MT, int NT, int PARTS, int GROUPS>
-__global__ void __launch_bounds__(32 * kShrinkWarps) shrink_kernel(const ShrinkArgs a)
+template <class T, int MT, int NT, int PARTS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) shrink_kernel(const ShrinkArgs a)
 {
-    extern __shared__ float parts[];  // kShrinkWarps x (8 NT) x kRowStride
-    constexpr int kThreads = 32 * kShrinkWarps;
-    constexpr int kSet = 8 * NT, kTokens = kSet * GROUPS, kSplit = kShrinkWarps / GROUPS;
+    extern __shared__ float parts[];  // WARPS x (8 NT) x kStride
+    constexpr int kThreads = 32 * WARPS, kTokens = 8 * NT, kStride = kRowStride<MT>;
     chain_wait();  // the product that follows may start on its weights and rows; it waits for inner
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     auto seg = [&](int q) { return clamp_to(__ldg(a.segments + q), a.T); };
@@ -291,12 +291,11 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) shrink_kernel(const ShrinkA
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) w[m][h] = A + int64_t(min(r0 + 16 * m + 8 * h + g, a.R - 1)) * a.lda;
-    // tokens by their place in the tile, so that a set's columns are a block of the tile
-    const int set = warp / kSplit;
+    // tokens by their place in the tile, so that a tile is a block of the planes
     const T *x[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int t = tile * kTokens + set * kSet + 8 * n + g;
+        const int t = tile * kTokens + 8 * n + g;
         x[n] = t >= t0 && t < t1 ? static_cast<const T *>(a.X) + int64_t(t) * a.ldx : nullptr;
     }
     float acc[MT][NT][4];
@@ -307,27 +306,26 @@ __global__ void __launch_bounds__(32 * kShrinkWarps) shrink_kernel(const ShrinkA
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[m][n][c] = 0.0f;
     const int64_t chunks = (a.K + 31) / 32;
-    const int64_t kb = chunks * (warp % kSplit) / kSplit * 32, ke = min(chunks * (warp % kSplit + 1) / kSplit * 32, a.K);
-    warp_product<T, MT, NT, 64>(w, x, kb, ke, a.K, lane, acc);
-    put_partial<MT, NT>(parts + warp * kSet * kRowStride, acc, lane);
+    const int64_t kb = chunks * warp / WARPS * 32, ke = min(chunks * (warp + 1) / WARPS * 32, a.K);
+    warp_product<T, MT, NT, WARPS == 16 ? 64 : 128>(w, x, kb, ke, a.K, lane, acc);
+    put_partial<MT, NT>(parts + warp * kTokens * kStride, acc, lane);
     __syncthreads();
     const float scale = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
     const int ranks = min(16 * MT, a.R - r0);
     auto sum = [&](int n, int r) {  // of token n of the tile
-        const float *src = parts + (n / kSet * kSplit * kSet + n % kSet) * kRowStride + r;
+        const float *src = parts + n * kStride + r;
         float v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kSplit; ++q) v += src[q * kSet * kRowStride];
+        for (int q = 0; q < WARPS; ++q) v += src[q * kTokens * kStride];
         return scale * v;
     };
     if constexpr (PARTS > 0) {
-        static_assert(kSet == 32, "blocks of 32 tokens");
+        static_assert(kTokens == 32, "blocks of 32 tokens");
         const InnerLayout in = inner_layout(a.T, a.requests, a.R, PARTS);
         uint16_t *plane = static_cast<uint16_t *>(a.planes) + int64_t(r0 / 64) * in.plane_rows * 64;
-        const int64_t row0 = (int64_t(tile) * GROUPS + lo) * 32;  // of the tile's first block
+        const int64_t row0 = (int64_t(tile) + lo) * 32;
         for (int i = threadIdx.x; i < kTokens * 16 * MT; i += kThreads) {
             const int r = i % (16 * MT), n = i / (16 * MT), t = tile * kTokens + n;
-            if ((t | 31) < t0 || (t & ~31) >= t1) continue;  // a block without tokens of the request
             uint16_t part[PARTS];
             split<T, PARTS>(r < ranks && t >= t0 && t < t1 ? sum(n, r) : 0.0f, part);
 #pragma unroll
@@ -351,7 +349,7 @@ cudaError_t launch_few_rows(const DeviceInfo &dev, const GroupedArgs &a, int64_t
     int ks = 1;
     while (ks < kWarps && 2 * groups * runs * depth * ks <= 16 * int64_t(dev.num_sms) && a.K / (2 * ks) >= 256) ks *= 2;
     const int64_t per = kWarps / ks;
-    const size_t smem = size_t(kWarps) * 8 * NT * kRowStride * sizeof(float);
+    const size_t smem = size_t(kWarps) * 8 * NT * kRowStride<2> * sizeof(float);
     auto *kernel = few_rows_kernel<T, Y, NT, GATED>;
     const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
@@ -376,23 +374,28 @@ template <class T, class Y> cudaError_t few_rows_t(const DeviceInfo &dev, const 
     return go(std::integral_constant<int, 8>{});
 }
 
-template <class T, int MT, int NT, int PARTS, int GROUPS> cudaError_t launch_shrink_t(const ShrinkArgs &a, cudaStream_t stream)
+template <class T, int MT, int NT, int PARTS, int WARPS> cudaError_t launch_shrink_t(const ShrinkArgs &a, cudaStream_t stream)
 {
-    constexpr size_t smem = size_t(kShrinkWarps) * 8 * NT * kRowStride * sizeof(float);
-    auto *kernel = shrink_kernel<T, MT, NT, PARTS, GROUPS>;
+    constexpr size_t smem = size_t(WARPS) * 8 * NT * kRowStride<MT> * sizeof(float);
+    auto *kernel = shrink_kernel<T, MT, NT, PARTS, WARPS>;
     const cudaError_t e = allow_smem_once(kernel, 100 * 1024);
     if (e != cudaSuccess) return e;
     static_assert(smem <= 100 * 1024, "dynamic shared memory");
-    const dim3 grid(unsigned(a.T / (8 * NT * GROUPS) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
-    return launch_chained(kernel, grid, 32 * kShrinkWarps, smem, 1, stream, a);
+    const dim3 grid(unsigned(a.T / (8 * NT) + a.requests), unsigned((a.R + 16 * MT - 1) / (16 * MT)));
+    return launch_chained(kernel, grid, 32 * WARPS, smem, 1, stream, a);
 }
 
+// Ranks a CTA and warps, measured as whole calls (us).  Up to 16 ranks 16 warps: 4096 tokens of 3
+// requests, 4096 x 4096, 91 against 100 with 8.  More ranks 8 warps with twice the registers: the same
+// at rank 32 94 against 107, 300 tokens of 20 requests 27 against 29.  64 ranks a CTA where most
+// requests fill a tile of 32 tokens: 8192 tokens of 7 requests, rank 64, 256 x 4096, 58 against 67, 512
+// of 8 21 against 28, but 512 tokens of 64 requests 53 against 43 with 32 ranks.
 template <class T, int NT, int PARTS> cudaError_t shrink_by_rank(const ShrinkArgs &a, cudaStream_t stream)
 {
-    if (a.R <= 16) return launch_shrink_t<T, 1, NT, PARTS, 1>(a, stream);
-    // two sets of 32 tokens where most requests fill them
-    if (NT == 4 && a.T >= 64 * int64_t(a.requests)) return launch_shrink_t<T, 2, NT, PARTS, 2>(a, stream);
-    return launch_shrink_t<T, 2, NT, PARTS, 1>(a, stream);
+    if (a.R <= 16) return launch_shrink_t<T, 1, NT, PARTS, 16>(a, stream);
+    if constexpr (PARTS == 0) return launch_shrink_t<T, 2, NT, PARTS, 16>(a, stream);
+    else if (a.R > 32 && a.T >= 64 * int64_t(a.requests)) return launch_shrink_t<T, 4, NT, PARTS, 8>(a, stream);
+    else return launch_shrink_t<T, 2, NT, PARTS, 8>(a, stream);
 }
 
 template <class T> cudaError_t shrink_t(const ShrinkArgs &a, cudaStream_t stream)
