@@ -131,6 +131,52 @@ __device__ __forceinline__ bool nonempty_group(const GroupedArgs &a, int i, int 
     return false;
 }
 
+// low[q] += B_a[feature] . inner[position] of output q, which `place` locates (false: no such output).
+// The adapter of the position, then its row of B: two latencies, so COUNT outputs share them.
+// Outputs without an adapter read the first one's and take nothing from it.
+template <class T, int COUNT, class Place>
+__device__ __forceinline__ void add_adapters(const GroupedArgs &a, float (&low)[COUNT], Place place)
+{
+    const T *b[COUNT];
+    const float *inner[COUNT];
+    bool has[COUNT];
+#pragma unroll
+    for (int q = 0; q < COUNT; ++q) {
+        int64_t p, feat;
+        has[q] = place(q, p, feat);
+        if (!has[q]) p = feat = 0;
+        int which = __ldcg(a.ad.which + p);
+        has[q] = has[q] && unsigned(which) < unsigned(a.ad.count);
+        if (!has[q]) which = 0;
+        b[q] = static_cast<const T *>(a.ad.b) + int64_t(which) * a.ad.strideb + feat * a.ad.ldb;
+        inner[q] = static_cast<const float *>(a.ad.inner) + p * a.ad.rank;
+    }
+    const bool whole = a.ad.rank % 8 == 0;
+    for (int j = 0; j < a.ad.rank; j += 8) {
+        uint4 e[COUNT];
+        float x[COUNT][8];
+#pragma unroll
+        for (int q = 0; q < COUNT; ++q) {
+            if (whole) {
+                e[q] = __ldg(reinterpret_cast<const uint4 *>(b[q] + j));
+                reinterpret_cast<float4 *>(x[q])[0] = __ldcg(reinterpret_cast<const float4 *>(inner[q] + j));
+                reinterpret_cast<float4 *>(x[q])[1] = __ldcg(reinterpret_cast<const float4 *>(inner[q] + j) + 1);
+            } else {
+                e[q] = load_tail(b[q], j, a.ad.rank);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x[q][c] = j + c < a.ad.rank ? __ldcg(inner[q] + j + c) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < COUNT; ++q) {
+            const T *v = reinterpret_cast<const T *>(&e[q]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (has[q]) low[q] = fmaf(to_f32(v[c]), x[q][c], low[q]);
+        }
+    }
+}
+
 // CTA: (8 / KS) runs of feature rows (32, or 16 gate rows with their 16 up rows) of one group times
 // all of its tokens, 8 * NT at a time; KS warps share a run, each summing its part of K.
 //
@@ -187,40 +233,40 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
         // adapters: their inner products come from the kernel before this one
         if (a.ad.b != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
         __syncthreads();
-        for (int i = threadIdx.x; i < block_feat * kTokens; i += kThreads) {
-            const int f = i % block_feat, n = i / block_feat;
-            const int64_t feat = int64_t(blockIdx.x) * block_feat + f;
-            if (n0 + n >= rows || feat >= a.N) continue;
-            const int64_t p = first + n0 + n;
-            const float *src = parts + ((f / kFeat) * ks * kTokens + n) * kStride + f % kFeat;
-            float v = 0.0f, u = 0.0f;
-            for (int q = 0; q < ks; ++q) {
-                v += src[q * kTokens * kStride];
-                if (GATED) u += src[q * kTokens * kStride + 16];
-            }
-            if (GATED) {
-                if (a.pre != nullptr) {
-                    T *pre = static_cast<T *>(a.pre) + p * a.ldp + feat;
-                    pre[0] = from_f32<T>(v);
-                    pre[a.N] = from_f32<T>(u);
-                }
-                v = v * sigmoid(v) * u;
-            }
-            if (a.ad.b != nullptr) {
-                const int which = __ldcg(a.ad.which + p);
-                if (unsigned(which) < unsigned(a.ad.count)) {
-                    const T *b = static_cast<const T *>(a.ad.b) + int64_t(which) * a.ad.strideb + feat * a.ad.ldb;
-                    const float *inner = static_cast<const float *>(a.ad.inner) + p * a.ad.rank;
-                    for (int j = 0; j < a.ad.rank; j += 8) {
-                        const uint4 q = load_tail(b, j, a.ad.rank);
-                        const T *e = reinterpret_cast<const T *>(&q);
+        for (int i0 = threadIdx.x; i0 < block_feat * kTokens; i0 += NT * kThreads) {
+            float low[NT];  // the adapters' part of the thread's next NT outputs
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            if (j + c < a.ad.rank) v = fmaf(to_f32(e[c]), __ldcg(inner + j + c), v);
-                    }
-                }
+            for (int q = 0; q < NT; ++q) low[q] = 0.0f;
+            if (a.ad.b != nullptr) {
+                add_adapters<T, NT>(a, low, [&](int q, int64_t &p, int64_t &feat) {
+                    const int i = i0 + q * kThreads, n = i / block_feat;
+                    p = first + n0 + n;
+                    feat = int64_t(blockIdx.x) * block_feat + i % block_feat;
+                    return n < kTokens && n0 + n < rows && feat < a.N;
+                });
             }
-            static_cast<Y *>(a.Y)[p * a.ldy + feat] = from_f32<Y>(v);
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                const int i = i0 + q * kThreads, f = i % block_feat, n = i / block_feat;
+                const int64_t feat = int64_t(blockIdx.x) * block_feat + f;
+                if (n >= kTokens || n0 + n >= rows || feat >= a.N) continue;
+                const int64_t p = first + n0 + n;
+                const float *src = parts + ((f / kFeat) * ks * kTokens + n) * kStride + f % kFeat;
+                float v = 0.0f, u = 0.0f;
+                for (int c = 0; c < ks; ++c) {
+                    v += src[c * kTokens * kStride];
+                    if (GATED) u += src[c * kTokens * kStride + 16];
+                }
+                if (GATED) {
+                    if (a.pre != nullptr) {
+                        T *pre = static_cast<T *>(a.pre) + p * a.ldp + feat;
+                        pre[0] = from_f32<T>(v);
+                        pre[a.N] = from_f32<T>(u);
+                    }
+                    v = v * sigmoid(v) * u;
+                }
+                static_cast<Y *>(a.Y)[p * a.ldy + feat] = from_f32<Y>(v + low[q]);
+            }
         }
     }
     // a CTA without tokens of its own still orders this launch behind the one before it
