@@ -48,8 +48,8 @@ cudaError_t allow_large_cluster_once(const void *kernel)
 // The few-rows kernel takes the calls that leave the tcgen05 kernel's pairs of SMs without tiles.
 // Both read every weight once from memory; measured, 8 of 64 experts of 2048 x 1024, gated product,
 // us few / many: 1 token 17.5 / 18.0, 4 tokens 43 / 42, 16 tokens 85 / 77, and with 128 experts
-// 64 tokens 200 / 170, 512 tokens 445 / 186.  One matrix of 4096 x 4096 with adapters: 16 tokens
-// 14 / 28, 64 tokens 30 / 37, 96 tokens 45 / 36.
+// 64 tokens 200 / 170, 512 tokens 445 / 186.  One matrix of 4096 x 4096 with adapters: 24 tokens
+// 12 / 16, 64 tokens 21 / 28, 80 tokens 32 / 28, 128 tokens 34 / 29.
 bool takes_few_rows(const DeviceInfo &dev, const GroupedArgs &a)
 {
     if (a.K == 0) return true;
