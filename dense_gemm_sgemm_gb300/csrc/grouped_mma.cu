@@ -181,6 +181,9 @@ __device__ __forceinline__ void add_adapters(const GroupedArgs &a, float (&low)[
 // all of its tokens, 8 * NT at a time; KS warps share a run, each summing its part of K.
 //
 // With one token column set (NT = 1) two CTAs share an SM: 128 KB of weights in flight.
+//
+// Bound by memory, and for few groups by latency around it: 8 tokens of 8 of 64 experts, 2048 weight
+// rows x 2048, gated, take 15.8 us for 67 MB (4.2 TB/s; 9.9 us at the measured bandwidth).
 template <class T, class Y, int NT, bool GATED>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(const GroupedArgs a, const int ks)
 {
@@ -288,7 +291,8 @@ template <class T, int PARTS> __device__ __forceinline__ void split(float x, uin
 // Inner products of the adapters: inner[t][r] = scale * sum_k X[t][k] A_a[r][k] for 16 MT ranks of up to
 // 8 NT tokens of one request, K split over the WARPS of the CTA.  Bound by latency for few tokens, where
 // 16 warps share K; for a prompt by what the CTAs draw from L2, where one CTA takes 64 ranks, so that
-// its tokens' rows are read once (launch_shrink_t's callers give the figures).
+// its tokens' rows are read once (launch_shrink_t's callers give the figures).  4096 tokens of 3
+// requests, rank 64, K = 2048: 13 us, 51 MB drawn from L2.
 //
 // CTA i takes item i of an enumeration that needs no scan: cutting the tokens both at multiples of the
 // tile and at the request boundaries, request s has the items t = segments[s] / tile + s ..

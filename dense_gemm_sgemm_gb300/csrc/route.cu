@@ -6,14 +6,17 @@
 // choice compares 32-bit keys (the fp32 value with its bits mapped to unsigned order, 0 for an expert
 // that is out), so one pick is one integer warp maximum and a ballot, whose lowest lane holds the
 // lowest index.  Runs of experts that are whole lanes, a power of two of them, are reduced by
-// shuffles, others through shared memory.  Bound by instructions, about 900 a token of 256 experts.
+// shuffles, others through shared memory.  Bound by instructions: 16384 tokens of 256 experts, sigmoid,
+// bias, 8 in 4 of 8 runs, take 25 us at 72% of the issue slots, 1370 instructions a token, a third of
+// them in the eight picks.
 //
 // The plan is a stable counting sort of the slots by expert in one launch: one cluster of CTAs, every
 // warp owning a contiguous run of slots and a histogram row of its own in shared memory.  Pass 1
 // counts (match.any gives the lanes of a warp that hold the same expert) and keeps each slot's rank
 // in its warp; the histograms are scanned over warps, CTAs (through distributed shared
-// memory) and experts; pass 2 adds them.  No atomics, so the order never varies.  With few tokens
-// the same launch routes them first (the warp's slots are then its own tokens').
+// memory) and experts; pass 2 adds them.  No atomics, so the order never varies.  Bound by latency on
+// 16 SMs: 131072 slots of 256 experts take 21 us.  With few tokens the same launch routes them first
+// (the warp's slots are then its own tokens').
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -400,6 +403,11 @@ __global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArg
     if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// Gradient of the weights w_j = scale * s_j (/ S, the sum of the chosen scores, when renormalised) for
+// one token a warp: ds_j = scale * dw_j, or scale * (dw_j - sum_i dw_i s_i / S) / S; then
+// dx_e = s_e (ds_e - sum ds s) for softmax, ds_e s_e (1 - s_e) for sigmoid.  Lane j takes choice j and
+// puts its gradient by expert into shared memory, so that every lane stores its own experts in wide
+// pieces.  Bound by the launch and the latency of one row: 8191 tokens of 128 experts, top 6, 5.0 us.
 template <int V>
 __global__ void __launch_bounds__(kRouteWarps * 32)
 route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *ids, void *dlogits, int64_t ldd, bool wide)
