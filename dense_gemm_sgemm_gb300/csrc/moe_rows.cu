@@ -38,7 +38,8 @@ __device__ __forceinline__ void place(int64_t cols, int64_t &row, int64_t &piece
     }
 }
 
-// Thread: VEC columns of one token; the k rows of a token are read by the same threads.
+// Thread: VEC columns of one token; the k rows of a token are read by the same threads.  8192 tokens of
+// 4 rows x 2048 to bf16: 49 us from fp32 rows (6.2 TB/s), 34 from bf16 rows (5.0).
 template <class R, class Y, int VEC>
 __global__ void __launch_bounds__(kThreads)
 combine_kernel(int64_t T, int64_t cols, int k, const R *rows, int64_t ldr, int64_t positions, const int32_t *where,
@@ -96,12 +97,47 @@ sum_kernel(int64_t rows, int64_t cols, int count, const float *part, int64_t ldp
     put<Y, VEC>(y + r * ldy + c, acc);
 }
 
-// Warp: one slot.  out[where] = w * x[token]; dweights != NULL also takes the dot product of
-// x[token] and rows[where].
+// Thread: VEC columns of one token, read once and written to kSpread of its slots' positions:
+// out[where] = w * x[token].  8192 tokens x 2048, bf16, 4 slots each: 26.5 us (6.3 TB/s); a warp a slot,
+// which reads the token once for each, 44 us.
+constexpr int kSpread = 8;
+template <class X, int VEC>
+__global__ void __launch_bounds__(kThreads)
+dispatch_kernel(int64_t T, int64_t cols, int k, const X *x, int64_t ldx, int64_t positions, const int32_t *where,
+                const float *weights, X *out, int64_t ldo)
+{
+    chain_wait();
+    int64_t t, c;
+    place(cols, t, c);
+    c *= VEC;
+    if (t >= T) return;
+    float v[VEC];
+    get<X, VEC>(x + t * ldx + c, v);
+    const int j0 = blockIdx.y * kSpread;
+    int32_t p[kSpread];
+    float w[kSpread];
+#pragma unroll
+    for (int j = 0; j < kSpread; ++j) {  // the look-ups in flight together
+        p[j] = j0 + j < k ? __ldg(where + t * k + j0 + j) : -1;
+        w[j] = j0 + j < k && weights != nullptr ? __ldg(weights + t * k + j0 + j) : 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kSpread; ++j) {
+        if (p[j] < 0 || p[j] >= positions) continue;
+        float u[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) u[i] = v[i] * w[j];
+        put<X, VEC>(out + p[j] * ldo + c, u);
+    }
+}
+
+// Warp: one slot, since the dot product of x[token] and rows[where] runs over the row;
+// out[where] = w * x[token] beside it.  8192 tokens of 4 bf16 rows x 2048: 47 us (6.4 TB/s).
 template <class X, class R, int VEC>
 __global__ void __launch_bounds__(kThreads)
-dispatch_kernel(int64_t slots, int64_t cols, int k, const X *x, int64_t ldx, const R *rows, int64_t ldr,
-                int64_t positions, const int32_t *where, const float *weights, X *out, int64_t ldo, float *dweights)
+combine_backward_kernel(int64_t slots, int64_t cols, int k, const X *x, int64_t ldx, const R *rows, int64_t ldr,
+                        int64_t positions, const int32_t *where, const float *weights, X *out, int64_t ldo,
+                        float *dweights)
 {
     chain_wait();
     const int64_t s = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
@@ -114,16 +150,14 @@ dispatch_kernel(int64_t slots, int64_t cols, int k, const X *x, int64_t ldx, con
         const float w = weights != nullptr ? weights[s] : 1.0f;
         const X *src = x + (s / k) * ldx;
         X *dst = out + p * ldo;
-        const R *row = dweights != nullptr ? rows + p * ldr : nullptr;
+        const R *row = rows + p * ldr;
 #pragma unroll 4
         for (int64_t c = lane; c < cols; c += 32) {
             float v[VEC], r[VEC];
             get<X, VEC>(src + c * VEC, v);
-            if (row != nullptr) {
-                get<R, VEC>(row + c * VEC, r);
+            get<R, VEC>(row + c * VEC, r);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) dot = fmaf(v[i], r[i], dot);
-            }
+            for (int i = 0; i < VEC; ++i) dot = fmaf(v[i], r[i], dot);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[i] *= w;
             put<X, VEC>(dst + c * VEC, v);
@@ -159,6 +193,8 @@ gather_kernel(const int32_t *offsets, int groups, int64_t positions, const uint1
     if (c < K) dst[c] = there ? src[c] : uint16_t(0);
 }
 
+// Thread: VEC columns of a position: with s = 1 / (1 + e^-gate), dgate = dh up s (1 + gate (1 - s)) and
+// dup = dh gate s.  32768 rows of 2 x 1024, bf16: 52 us (6.4 TB/s).
 template <class X, class D, int VEC>
 __global__ void __launch_bounds__(kThreads)
 gated_silu_backward_kernel(int64_t rows, int64_t cols, int64_t I, const X *pre, int64_t ldp, const D *dh, int64_t lddh,
@@ -245,12 +281,20 @@ cudaError_t launch_dispatch(int type, int rows_type, int64_t T, int64_t H, int t
     const bool vec = H % 8 == 0 && wide(x, ldx) && wide(out, ldo) && (rows == nullptr || wide(rows, ldr));
     const int64_t cols = vec ? H / 8 : H;
     unsigned blocks;
-    if (!grid_of(T * top_k, kThreads / 32, blocks)) return cudaErrorInvalidConfiguration;
+    // dispatch alone: a thread a piece of a token; with the weights' gradient: a warp a slot
+    if (dweights == nullptr ? !grid_of(T * cols, kThreads, blocks) : !grid_of(T * top_k, kThreads / 32, blocks))
+        return cudaErrorInvalidConfiguration;
     return by_type(type, [&](auto a) {
+        using X = decltype(a);
+        if (dweights == nullptr) {
+            const dim3 grid(blocks, unsigned((top_k + kSpread - 1) / kSpread));
+            auto *kernel = vec ? dispatch_kernel<X, 8> : dispatch_kernel<X, 1>;
+            return launch_chained(kernel, grid, kThreads, 0, 1, stream, T, cols, top_k, static_cast<const X *>(x), ldx,
+                                  positions, where, weights, static_cast<X *>(out), ldo);
+        }
         return by_type(rows_type, [&](auto r) {
-            using X = decltype(a);
             using R = decltype(r);
-            auto *kernel = vec ? dispatch_kernel<X, R, 8> : dispatch_kernel<X, R, 1>;
+            auto *kernel = vec ? combine_backward_kernel<X, R, 8> : combine_backward_kernel<X, R, 1>;
             return launch_chained(kernel, dim3(blocks), kThreads, 0, 1, stream, T * top_k, cols, top_k, static_cast<const X *>(x), ldx,
                                                     static_cast<const R *>(rows), ldr, positions, where, weights,
                                                     static_cast<X *>(out), ldo, dweights);
