@@ -298,8 +298,8 @@ template <class T, int PARTS> __device__ __forceinline__ void split(float x, uin
 // tile and at the request boundaries, request s has the items t = segments[s] / tile + s ..
 // segments[s + 1] / tile + s, so the request of item i is the last s whose first item is <= i.
 //
-// PARTS = 0 writes the few-rows form of the inner products, else the tcgen05 form (InnerLayout), for
-// which 8 NT is 32.
+// PARTS = 0 writes the few-rows form of the inner products, else the tcgen05 form (InnerLayout: the parts
+// and the fp32 values), for which 8 NT is 32.
 template <class T, int MT, int NT, int PARTS, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) shrink_kernel(const ShrinkArgs a)
 {
@@ -372,12 +372,16 @@ __global__ void __launch_bounds__(32 * WARPS) shrink_kernel(const ShrinkArgs a)
     if constexpr (PARTS > 0) {
         static_assert(kTokens == 32, "blocks of 32 tokens");
         const InnerLayout in = inner_layout(a.T, a.requests, a.R, PARTS);
+        float *values = reinterpret_cast<float *>(static_cast<char *>(a.planes) + in.values_at());
         uint16_t *plane = static_cast<uint16_t *>(a.planes) + int64_t(r0 / 64) * in.plane_rows * 64;
         const int64_t row0 = (int64_t(tile) + lo) * 32;
         for (int i = threadIdx.x; i < kTokens * 16 * MT; i += kThreads) {
             const int r = i % (16 * MT), n = i / (16 * MT), t = tile * kTokens + n;
+            const bool there = r < ranks && t >= t0 && t < t1;
+            const float v = there ? sum(n, r) : 0.0f;
+            if (there) values[int64_t(t) * a.R + r0 + r] = v;
             uint16_t part[PARTS];
-            split<T, PARTS>(r < ranks && t >= t0 && t < t1 ? sum(n, r) : 0.0f, part);
+            split<T, PARTS>(v, part);
 #pragma unroll
             for (int q = 0; q < PARTS; ++q)
                 plane[int64_t(q) * in.blocks * in.plane_rows * 64 + (row0 + n) * 64 + r0 % 64 + r] = part[q];

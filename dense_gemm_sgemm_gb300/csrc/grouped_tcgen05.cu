@@ -19,7 +19,10 @@
 // columns of the request only (see TileRequests); the kernel ahead computes the inner products in
 // 16-bit parts that sum to them (launch_shrink).  On the CUDA cores of the epilogue this product was
 // bound by broadcasting the inner products from shared memory (8192 tokens, rank 64, 4096 x 4096:
-// 341 us), with mma.sync there by tcgen05, which goes first (371 us).
+// 341 us), with mma.sync there by tcgen05, which goes first (371 us).  An infinity or NaN in an adapter's
+// B would spoil the columns of its neighbours, where it meets zeros: the epilogue notes the tiles whose
+// sums are not finite, and the pair computes those a second time with such adapters' products in fp32
+// on the CUDA cores (TileRequests).
 //
 // Weight gradient.  dW_g[n][k] sums over the group's positions, the K dimension of this product,
 // both operands "transposed" (MN-major).  Slices are 64 positions; the last one of a group also holds
@@ -31,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cstdlib>
 #include <cstring>
 
@@ -143,6 +147,7 @@ struct Shared {
     uint8_t *epi;
     volatile uint32_t *tmem_slot;
     volatile int *abort_flag;
+    uint32_t *again;  // two words: which of the pair's tiles to compute again
     int *first, *start;
     int stages, b_bytes;
     __device__ __forceinline__ Shared(uint8_t *raw, int stage_b_bytes)
@@ -157,6 +162,7 @@ struct Shared {
         bar0 = smem_u32(bars);
         tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBarBytes - 16);
         abort_flag = reinterpret_cast<volatile int *>(bars + kBarBytes - 8);
+        again = reinterpret_cast<uint32_t *>(bars + kBarBytes - 32);
         first = reinterpret_cast<int *>(bars + kBarBytes);
         start = first + kMaxGroups + 2;
     }
@@ -170,7 +176,7 @@ struct Shared {
     __device__ __forceinline__ uint32_t stage_a(int s) const { return a + uint32_t(s * kStageA); }
     __device__ __forceinline__ uint32_t stage_b(int s) const { return b + uint32_t(s * b_bytes); }
 };
-static_assert(8 * (4 * kMaxStages + 5) <= kBarBytes - 16, "barrier area");
+static_assert(8 * (4 * kMaxStages + 5) <= kBarBytes - 32, "barrier area");
 
 // Barriers, the groups' first positions and first units, TMEM; ends with the pair in step.
 // units_of(rows): work units of a group of that many rows.  CHAIN: waits for the kernel ahead.
@@ -192,6 +198,7 @@ __device__ __forceinline__ uint32_t set_up(const Shared &sh, const int32_t *offs
         }
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
+        sh.again[0] = sh.again[1] = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     cluster_sync();  // a pair allocates TMEM together, and its barriers exist before the peer uses them
@@ -326,6 +333,9 @@ struct LinearParams {
     const int32_t *segments, *adapters;
     int requests, n_adapters, rank, parts;
     int plane_rows;
+    const float *values;  // their fp32 values, a row of `rank` for every token
+    const void *b;
+    int64_t ldb, strideb;
     unsigned int *status;
     uint64_t timeout_ns;
     int inject_stall;  // test hook: the producer never fills its first slice
@@ -446,19 +456,45 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile
 
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
+// Whether an adapter's rows of B for a tile of 256 features hold an infinity or NaN.
+__device__ __noinline__ bool unfit(const LinearParams &p, int adapter, int feature_tile, int lane)
+{
+    const uint32_t exponent = p.bf16 ? 0x7f80u : 0x7c00u;  // all ones: no finite number
+    const int64_t f0 = int64_t(feature_tile) * 256;
+    const int rows = int(min(p.N - f0, int64_t(256))), pieces = (p.rank + 7) / 8;
+    const uint16_t *b = static_cast<const uint16_t *>(p.b) + adapter * p.strideb + f0 * p.ldb;
+    bool found = false;
+    for (int i = lane; i < rows * pieces; i += 32) {
+        const uint4 v = load_tail(b + i / pieces * p.ldb, i % pieces * 8, p.rank);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) found |= (w[c] & exponent) == exponent || ((w[c] >> 16) & exponent) == exponent;
+    }
+    return __any_sync(kFull, found);
+}
+
 // The requests that share a tile's tokens and have an adapter, in order, those of the unit's split of
 // them; the roles' warps walk them in step, 32 requests looked up at a time.
 //
 // A request's slices: for every 64 ranks, its inner products' parts in turn, as many parts behind one
 // another in the token half of a stage as fit (all of them for a short request), each multiplied with
 // the same adapter rows.
+//
+// The columns of a request's slices are whole blocks of 32, in which other requests' tokens are zeros, so
+// an infinity or NaN among the adapter's rows would make NaN of them.  A tile whose sums are not all
+// finite is computed a second time (`careful`), in which requests whose product is unfit for the tensor
+// cores are left out of the slices and added to the sums by the epilogue (add_late).  What the other
+// requests get does not depend on them in a bit: the same slices in the same order.  Where all values are
+// finite this costs about 1 us a call; 8192 tokens, rank 64, 4096 x 4096 take 204 us, 923 with an infinity
+// in one of 7 requests' adapters and 4.8 ms with one in all of them.
 struct TileRequests {
     const LinearParams &p;
-    int t0, t1, q0, lane, skip;
-    unsigned left;
+    int t0, t1, q0, lane, skip, feature_tile;
+    bool careful;
+    unsigned left, late;  // of the 32 requests at q0: those to come, those left out of the slices
     int lo, hi, ad;  // of request q0 + lane: its tokens within the tile and its adapter
-    __device__ __forceinline__ TileRequests(const LinearParams &params, const LinearUnit &x, int l)
-        : p(params), t0(x.first), t1(x.first + x.tokens), lane(l), skip(x.split)
+    __device__ __forceinline__ TileRequests(const LinearParams &params, const LinearUnit &x, int l, bool second)
+        : p(params), t0(x.first), t1(x.first + x.tokens), lane(l), skip(x.split), feature_tile(x.feature_tile), careful(second)
     {
         // requests that end at or before the tile's first token, 32 candidates at a time: whole runs,
         // then the run that is left
@@ -483,12 +519,17 @@ struct TileRequests {
             ad = __ldg(p.adapters + q);
         }
         left = __ballot_sync(kFull, lo < hi && unsigned(ad) < unsigned(p.n_adapters));
+        late = 0u;
+        if (careful)
+            for (unsigned look = left; look != 0u; look &= look - 1u) {
+                const int at = __ffs(look) - 1;
+                if (unfit(p, __shfl_sync(kFull, ad, at), feature_tile, lane)) late |= 1u << at;
+            }
         more = __any_sync(kFull, q == q0 + 31 && q + 1 < p.requests && clamp_to(__ldg(p.segments + q + 1), p.y_rows) < t1);
     }
     bool more;
-    // Next request: its adapter, the columns [c0, c0 + n) of the tile that hold its tokens, multiples of
-    // 32, and the first of the rows of its inner products.
-    __device__ __forceinline__ bool next(int &adapter, int &c0, int &n, int &row)
+    // Next of the split's requests, by its lane.
+    __device__ __forceinline__ bool advance(int &at)
     {
         for (;; --skip) {
             while (left == 0u) {
@@ -500,8 +541,30 @@ struct TileRequests {
             left &= left - 1u;
         }
         skip = p.splits - 1;
-        const int at = __ffs(left) - 1;
+        at = __ffs(left) - 1;
         left &= left - 1u;
+        return true;
+    }
+    // Next request that is left out: its adapter and its tokens within the tile.
+    __device__ __forceinline__ bool next_late(int &adapter, int &first, int &end)
+    {
+        int at;
+        do {
+            if (!advance(at)) return false;
+        } while (!((late >> at) & 1u));
+        adapter = __shfl_sync(kFull, ad, at);
+        first = __shfl_sync(kFull, lo, at);
+        end = __shfl_sync(kFull, hi, at);
+        return true;
+    }
+    // Next request with slices: its adapter, the columns [c0, c0 + n) of the tile that hold its tokens,
+    // multiples of 32, and the first of the rows of its inner products.
+    __device__ __forceinline__ bool next(int &adapter, int &c0, int &n, int &row)
+    {
+        int at;
+        do {
+            if (!advance(at)) return false;
+        } while ((late >> at) & 1u);
         adapter = __shfl_sync(kFull, ad, at);
         const int b0 = __shfl_sync(kFull, lo, at) / 32, b1 = (__shfl_sync(kFull, hi, at) + 31) / 32;
         c0 = b0 * 32 - t0;
@@ -515,11 +578,59 @@ struct TileRequests {
 
 // Looked up at a unit's start, while its first slices are on their way; the other forms have none.
 struct NoRequests {
-    __device__ __forceinline__ NoRequests(const LinearParams &, const LinearUnit &, int) {}
+    __device__ __forceinline__ NoRequests(const LinearParams &, const LinearUnit &, int, bool) {}
     __device__ __forceinline__ bool next(int &, int &, int &, int &) { return false; }
     __device__ __forceinline__ int parts_a_slice(int) const { return 1; }
 };
 template <int EPI> using RequestsOf = typename std::conditional<EPI == kAdapted, TileRequests, NoRequests>::type;
+
+// Adds the products of the requests that a tile's second computation leaves out to `sums`, 32 tokens from
+// `first` of the lane's feature f + lane as [token][lane]: fp32 values and sums, as the few-rows kernel's.
+__device__ __noinline__ void add_late(const LinearParams &p, const LinearUnit x, float *sums, int first, int tokens, int64_t f, int lane)
+{
+    TileRequests requests(p, x, lane, true);
+    int adapter, t0, t1;
+    while (requests.next_late(adapter, t0, t1)) {
+        if (f + lane >= p.N) continue;
+        const uint16_t *b = static_cast<const uint16_t *>(p.b) + adapter * p.strideb + (f + lane) * p.ldb;
+        for (int t = max(t0, first); t < min(t1, first + min(tokens, 32)); ++t) {
+            const float *values = p.values + int64_t(t) * p.rank;
+            float low = 0.0f;
+            for (int j = 0; j < p.rank; j += 8) {
+                const uint4 e = load_tail(b, j, p.rank);
+                const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint16_t u = uint16_t(w[c / 2] >> (16 * (c & 1)));
+                    const float v = p.bf16 ? __bfloat162float(__ushort_as_bfloat16(u)) : __half2float(__ushort_as_half(u));
+                    if (j + c < p.rank) low = fmaf(v, __ldcg(values + j + c), low);
+                }
+            }
+            sums[(t - first) * 32 + lane] += low;
+        }
+    }
+}
+
+// The tiles that the pair computes again, by their number modulo 64: those that the epilogue of either CTA
+// noted; none after a failure.  Both CTAs come here with all threads and get the same.
+__device__ __forceinline__ uint64_t tiles_again(const Shared &sh)
+{
+    __syncwarp();
+    cluster_sync();
+    uint64_t all = 0;
+    uint32_t stop = 0;
+#pragma unroll
+    for (uint32_t r = 0; r < 2; ++r) {
+        uint32_t lo, hi, flag;
+        const uint32_t at = map_to_rank(smem_u32(sh.again), r);
+        const uint32_t abort_at = map_to_rank(smem_u32(const_cast<int *>(sh.abort_flag)), r);
+        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(flag) : "r"(abort_at) : "memory");
+        all |= uint64_t(hi) << 32 | lo;
+        stop |= flag;
+    }
+    return stop != 0u ? 0ull : all;
+}
 
 // W_MN: W stored K x N (features contiguous).
 //
@@ -531,7 +642,7 @@ template <int W_MN, int EPI, bool Y_F32>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x,
                       const __grid_constant__ CUtensorMap map_b, const __grid_constant__ TokenMaps map_inner,
-                      const __grid_constant__ CUtensorMap map_y, const LinearParams p)
+                      const __grid_constant__ CUtensorMap map_y, const __grid_constant__ LinearParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const Shared sh(smem_raw, p.cap * 64);
@@ -545,302 +656,325 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     constexpr int kFeatures = EPI == kGated ? 128 : 256;  // of a unit
     const int blocks = EPI == kAdapted ? (p.rank + 63) / 64 : 1;  // of 64 ranks
 
-    if (warp == 0) {
-        // ---------------- weight producer (warps in step, one elected lane copying)
-        const bool leader = elect_one();
-        const uint32_t full0 = map_to_rank(sh.full(0), 0);  // the first CTA's
-        Ring ring(sh.stages);
-        bool ok = true;
-        int group = 0;
-        if (leader) tma_prefetch_desc(&map_w);
-        for (int u = unit0; ok && u < units; u += step) {
-            const LinearUnit x = linear_unit(p, sh, u, group);
-            RequestsOf<EPI> requests(p, x, lane);
-            const int f0 = x.feature_tile * kFeatures + int(rank) * (kFeatures / 2);
-            const int wg = p.shared_w ? 0 : x.group;
-            const uint32_t bytes = 2u * (kStageA + uint32_t(x.width) * 64u);
-            for (int kb = x.kb0; kb < x.kb1; ++kb) {
-                ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                if (__any_sync(kFull, !ok)) {
-                    ok = false;
-                    break;
-                }
-                if (leader) {
-                    if (rank == 0) mbar_expect_tx(sh.full(ring.stage), bytes);
-                    if (!(p.inject_stall && kb == x.kb0 && u == unit0)) {
-                        const uint32_t full = full0 + 8u * ring.stage, a = sh.stage_a(ring.stage);
-                        if (W_MN) {  // two boxes of 64 features x 64 k
-                            tma_load_3d_pair(a, &map_w, full, f0, kb * 64, wg);
-                            tma_load_3d_pair(a + 8192, &map_w, full, f0 + 64, kb * 64, wg);
-                        } else if (EPI == kGated) {  // 64 gate rows and their up rows
-                            tma_load_3d_pair(a, &map_w, full, kb * 64, f0, wg);
-                            tma_load_3d_pair(a + 8192, &map_w, full, kb * 64, int(p.N) + f0, wg);
-                        } else {
-                            tma_load_3d_pair(a, &map_w, full, kb * 64, f0, wg);
-                        }
-                    }
-                }
-                __syncwarp();
-                ring.next();
-            }
-            if (EPI == kAdapted && ok) {
-                int ad, c0, n, row;
-                while (ok && requests.next(ad, c0, n, row)) {
-                    const int most = requests.parts_a_slice(n);
-                    for (int r0 = 0, i = 0; ok && r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
-                        ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                        if (__any_sync(kFull, !ok)) {
-                            ok = false;
-                            break;
-                        }
-                        if (leader) {
-                            const uint32_t rows = uint32_t(n) * uint32_t(min(most, p.parts - i));
-                            if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2u * (kStageA + rows * 64u));
-                            tma_load_3d_pair(sh.stage_a(ring.stage), &map_b, full0 + 8u * ring.stage, r0, f0, ad);
-                        }
-                        __syncwarp();
-                        ring.next();
-                    }
-                }
-            }
-        }
-        if (leader) finish_producer(sh, watch, ring, ok);
-    } else if (warp == kTokenWarp) {
-        // ---------------- token producer
-        const bool leader = elect_one();
-        const uint32_t full0 = map_to_rank(sh.full(0), 0);
-        Ring ring(sh.stages);
-        bool ok = true;
-        int group = 0;
-        if (leader) tma_prefetch_desc(&map_x.rows[0]);
-        for (int u = unit0; ok && u < units; u += step) {
-            const LinearUnit x = linear_unit(p, sh, u, group);
-            RequestsOf<EPI> requests(p, x, lane);
-            const int half = x.width / 2;                     // tokens this CTA loads
-            const int row0 = x.first + int(rank) * half, end = x.first + x.tokens;
-            int4 from = make_int4(0, 0, 0, 0);
-            if (p.rows != nullptr && 4 * lane < half) {       // a row outside x is read as zeros
-                int r[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int q = row0 + 4 * lane + i;
-                    r[i] = q < end ? __ldg(p.rows + q) : -1;
-                    if (r[i] < 0 || r[i] >= p.x_rows) r[i] = int(p.x_rows);
-                }
-                from = make_int4(r[0], r[1], r[2], r[3]);
-            }
-            for (int kb = x.kb0; kb < x.kb1; ++kb) {
-                ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                if (__any_sync(kFull, !ok)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t full = full0 + 8u * ring.stage, b = sh.stage_b(ring.stage);
-                if (p.rows != nullptr) {
-                    if (4 * lane < half) tma_gather4_pair(b + 512u * lane, &map_x.rows[0], full, kb * 64, from);
-                } else if (leader) {
-                    load_rows(b, map_x, full, kb * 64, row0, half);
-                }
-                __syncwarp();
-                ring.next();
-            }
-            if (EPI == kAdapted && ok) {
-                // the inner products come from the kernel ahead, which itself waited for what x comes from
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                int ad, c0, n, row;
-                while (ok && requests.next(ad, c0, n, row)) {
-                    const int most = requests.parts_a_slice(n);
-                    for (int r0 = 0, i = 0; ok && r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
-                        ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                        if (__any_sync(kFull, !ok)) {
-                            ok = false;
-                            break;
-                        }
-                        if (leader)
-                            for (int j = 0; j < most && i + j < p.parts; ++j)
-                                load_rows(sh.stage_b(ring.stage) + uint32_t(j * n) * 64u, map_inner, full0 + 8u * ring.stage, 0,
-                                          ((i + j) * blocks + r0 / 64) * p.plane_rows + row + int(rank) * (n / 2), n / 2);
-                        __syncwarp();
-                        ring.next();
-                    }
-                }
-            }
-        }
-        if (leader && !ok) finish_producer(sh, watch, ring, false);
-        // a CTA without tiles of its own still orders this launch behind the one ahead of it
-        if (EPI == kAdapted) asm volatile("griddepcontrol.wait;" ::: "memory");
-    } else if (warp == 1) {
-        if (rank == 0) {
-            // ---------------- MMA issuer: the warp in step, one elected lane issuing
+    // A role's place in the ring and the accumulators; with adapters it may go through its tiles twice.
+    Ring ring(sh.stages);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    uint64_t again = ~0ull;
+    auto wanted = [&](int n) { return EPI != kAdapted || ((again >> (n & 63)) & 1u) != 0u; };
+    for (bool careful = false;; careful = true) {
+        if (warp == 0) {
+            // ---------------- weight producer (warps in step, one elected lane copying)
             const bool leader = elect_one();
-            const uint32_t fmt = p.bf16 ? (1u << 7) | (1u << 10) : 0u;
-            // descriptors of stage 0; a later stage or K step only moves the start address
-            const uint64_t a0 = W_MN ? smem_desc(sh.a, 8192, 1024) : smem_desc(sh.a, 16, 1024);
-            const uint64_t b0 = smem_desc(sh.b, 16, 1024);
-            constexpr uint64_t kStepA = W_MN ? 2048 >> 4 : 32 >> 4, kStepB = 32 >> 4;
-            Ring ring(sh.stages);
-            int acc = 0, group = 0;
-            uint32_t acc_phase = 0;
-            bool ok = true;
-            for (int u = unit0; ok && u < units; u += step) {
+            const uint32_t full0 = map_to_rank(sh.full(0), 0);  // the first CTA's
+            int group = 0;
+            if (leader) tma_prefetch_desc(&map_w);
+            for (int u = unit0, n = 0; ok && u < units; u += step, ++n) {
+                if (!wanted(n)) continue;
                 const LinearUnit x = linear_unit(p, sh, u, group);
-                RequestsOf<EPI> requests(p, x, lane);
-                const uint32_t idesc = make_idesc(W_MN, 0, x.width, 256) | fmt;
-                ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d = tmem + uint32_t(acc * kAccCols);
+                RequestsOf<EPI> requests(p, x, lane, careful);
+                const int f0 = x.feature_tile * kFeatures + int(rank) * (kFeatures / 2);
+                const int wg = p.shared_w ? 0 : x.group;
+                const uint32_t bytes = 2u * (kStageA + uint32_t(x.width) * 64u);
                 for (int kb = x.kb0; kb < x.kb1; ++kb) {
-                    ok = watch.wait(sh.full(ring.stage), ring.phase);
-                    if (!ok) break;
-                    tc_fence_after();
+                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                    if (__any_sync(kFull, !ok)) {
+                        ok = false;
+                        break;
+                    }
                     if (leader) {
-                        const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
-                        const uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_f16<true>(d, a + k * kStepA, b + k * kStepB, idesc, kb > x.kb0 || k > 0 ? 1u : 0u);
-                        commit_both(sh.empty(ring.stage));
+                        if (rank == 0) mbar_expect_tx(sh.full(ring.stage), bytes);
+                        if (!(p.inject_stall && kb == x.kb0 && u == unit0)) {
+                            const uint32_t full = full0 + 8u * ring.stage, a = sh.stage_a(ring.stage);
+                            if (W_MN) {  // two boxes of 64 features x 64 k
+                                tma_load_3d_pair(a, &map_w, full, f0, kb * 64, wg);
+                                tma_load_3d_pair(a + 8192, &map_w, full, f0 + 64, kb * 64, wg);
+                            } else if (EPI == kGated) {  // 64 gate rows and their up rows
+                                tma_load_3d_pair(a, &map_w, full, kb * 64, f0, wg);
+                                tma_load_3d_pair(a + 8192, &map_w, full, kb * 64, int(p.N) + f0, wg);
+                            } else {
+                                tma_load_3d_pair(a, &map_w, full, kb * 64, f0, wg);
+                            }
+                        }
                     }
                     __syncwarp();
                     ring.next();
                 }
                 if (EPI == kAdapted && ok) {
-                    int ad, c0, n, row;
-                    while (ok && requests.next(ad, c0, n, row)) {
-                        const uint32_t part_idesc = make_idesc(0, 0, n, 256) | fmt;
-                        const int most = requests.parts_a_slice(n);
-                        for (int r0 = 0, i = 0; r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
-                            ok = watch.wait(sh.full(ring.stage), ring.phase);
-                            if (!ok) break;
-                            tc_fence_after();
+                    int ad, c0, cols, row;
+                    while (ok && requests.next(ad, c0, cols, row)) {
+                        const int most = requests.parts_a_slice(cols);
+                        for (int r0 = 0, i = 0; ok && r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
+                            ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                            if (__any_sync(kFull, !ok)) {
+                                ok = false;
+                                break;
+                            }
                             if (leader) {
-                                const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
-                                uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
-                                const int steps = (p.rank - r0 + 15) / 16;
-                                for (int j = 0; j < most && i + j < p.parts; ++j, b += uint32_t(n * 64) >> 4) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        if (k < steps)
-                                            umma_f16<true>(d + uint32_t(c0), a + k * kStepA, b + k * kStepB, part_idesc, 1u);
-                                }
-                                commit_both(sh.empty(ring.stage));
+                                const uint32_t rows = uint32_t(cols) * uint32_t(min(most, p.parts - i));
+                                if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2u * (kStageA + rows * 64u));
+                                tma_load_3d_pair(sh.stage_a(ring.stage), &map_b, full0 + 8u * ring.stage, r0, f0, ad);
                             }
                             __syncwarp();
                             ring.next();
                         }
                     }
                 }
-                if (!ok) break;
-                if (leader) commit_both(sh.acc_full(acc));
+            }
+            if (leader) finish_producer(sh, watch, ring, ok);
+        } else if (warp == kTokenWarp) {
+            // ---------------- token producer
+            const bool leader = elect_one();
+            const uint32_t full0 = map_to_rank(sh.full(0), 0);
+            int group = 0;
+            if (leader) tma_prefetch_desc(&map_x.rows[0]);
+            for (int u = unit0, n = 0; ok && u < units; u += step, ++n) {
+                if (!wanted(n)) continue;
+                const LinearUnit x = linear_unit(p, sh, u, group);
+                RequestsOf<EPI> requests(p, x, lane, careful);
+                const int half = x.width / 2;                     // tokens this CTA loads
+                const int row0 = x.first + int(rank) * half, end = x.first + x.tokens;
+                int4 from = make_int4(0, 0, 0, 0);
+                if (p.rows != nullptr && 4 * lane < half) {       // a row outside x is read as zeros
+                    int r[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int q = row0 + 4 * lane + i;
+                        r[i] = q < end ? __ldg(p.rows + q) : -1;
+                        if (r[i] < 0 || r[i] >= p.x_rows) r[i] = int(p.x_rows);
+                    }
+                    from = make_int4(r[0], r[1], r[2], r[3]);
+                }
+                for (int kb = x.kb0; kb < x.kb1; ++kb) {
+                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                    if (__any_sync(kFull, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + 8u * ring.stage, b = sh.stage_b(ring.stage);
+                    if (p.rows != nullptr) {
+                        if (4 * lane < half) tma_gather4_pair(b + 512u * lane, &map_x.rows[0], full, kb * 64, from);
+                    } else if (leader) {
+                        load_rows(b, map_x, full, kb * 64, row0, half);
+                    }
+                    __syncwarp();
+                    ring.next();
+                }
+                if (EPI == kAdapted && ok) {
+                    // the inner products come from the kernel ahead, which itself waited for what x comes from
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    int ad, c0, cols, row;
+                    while (ok && requests.next(ad, c0, cols, row)) {
+                        const int most = requests.parts_a_slice(cols);
+                        for (int r0 = 0, i = 0; ok && r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
+                            ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                            if (__any_sync(kFull, !ok)) {
+                                ok = false;
+                                break;
+                            }
+                            if (leader)
+                                for (int j = 0; j < most && i + j < p.parts; ++j)
+                                    load_rows(sh.stage_b(ring.stage) + uint32_t(j * cols) * 64u, map_inner, full0 + 8u * ring.stage, 0,
+                                              ((i + j) * blocks + r0 / 64) * p.plane_rows + row + int(rank) * (cols / 2), cols / 2);
+                            __syncwarp();
+                            ring.next();
+                        }
+                    }
+                }
+            }
+            if (leader && !ok) finish_producer(sh, watch, ring, false);
+            // a CTA without tiles of its own still orders this launch behind the one ahead of it
+            if (EPI == kAdapted) asm volatile("griddepcontrol.wait;" ::: "memory");
+        } else if (warp == 1) {
+            if (rank == 0) {
+                // ---------------- MMA issuer: the warp in step, one elected lane issuing
+                const bool leader = elect_one();
+                const uint32_t fmt = p.bf16 ? (1u << 7) | (1u << 10) : 0u;
+                // descriptors of stage 0; a later stage or K step only moves the start address
+                const uint64_t a0 = W_MN ? smem_desc(sh.a, 8192, 1024) : smem_desc(sh.a, 16, 1024);
+                const uint64_t b0 = smem_desc(sh.b, 16, 1024);
+                constexpr uint64_t kStepA = W_MN ? 2048 >> 4 : 32 >> 4, kStepB = 32 >> 4;
+                int group = 0;
+                for (int u = unit0, n = 0; ok && u < units; u += step, ++n) {
+                    if (!wanted(n)) continue;
+                    const LinearUnit x = linear_unit(p, sh, u, group);
+                    RequestsOf<EPI> requests(p, x, lane, careful);
+                    const uint32_t idesc = make_idesc(W_MN, 0, x.width, 256) | fmt;
+                    ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + uint32_t(acc * kAccCols);
+                    for (int kb = x.kb0; kb < x.kb1; ++kb) {
+                        ok = watch.wait(sh.full(ring.stage), ring.phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
+                            const uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_f16<true>(d, a + k * kStepA, b + k * kStepB, idesc, kb > x.kb0 || k > 0 ? 1u : 0u);
+                            commit_both(sh.empty(ring.stage));
+                        }
+                        __syncwarp();
+                        ring.next();
+                    }
+                    if (EPI == kAdapted && ok) {
+                        int ad, c0, cols, row;
+                        while (ok && requests.next(ad, c0, cols, row)) {
+                            const uint32_t part_idesc = make_idesc(0, 0, cols, 256) | fmt;
+                            const int most = requests.parts_a_slice(cols);
+                            for (int r0 = 0, i = 0; r0 < p.rank; (i += most) >= p.parts ? (i = 0, r0 += 64) : 0) {
+                                ok = watch.wait(sh.full(ring.stage), ring.phase);
+                                if (!ok) break;
+                                tc_fence_after();
+                                if (leader) {
+                                    const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
+                                    uint64_t b = b0 + uint32_t(ring.stage * (sh.b_bytes >> 4));
+                                    const int steps = (p.rank - r0 + 15) / 16;
+                                    for (int j = 0; j < most && i + j < p.parts; ++j, b += uint32_t(cols * 64) >> 4) {
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k)
+                                            if (k < steps)
+                                                umma_f16<true>(d + uint32_t(c0), a + k * kStepA, b + k * kStepB, part_idesc, 1u);
+                                    }
+                                    commit_both(sh.empty(ring.stage));
+                                }
+                                __syncwarp();
+                                ring.next();
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    if (leader) commit_both(sh.acc_full(acc));
+                    if (++acc == 2) {
+                        acc = 0;
+                        acc_phase ^= 1u;
+                    }
+                }
+                if (!ok && leader) drain_issuer(sh);
+            }
+        } else {
+            // ---------------- epilogue: TMEM lanes 32 * quarter .. of this CTA's 128 rows
+            const int quarter = warp & 3, half = (warp - 2) >> 2;
+            uint8_t *tile = sh.epi + (warp - 2) * 4096;
+            Staging<Y_F32> staging(tile, lane);
+            int group = 0;
+            const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
+            const int64_t ldy = p.ldy * (Y_F32 ? 4 : 2);
+            auto put = [&](const float (&v)[32], int first, int tokens, int64_t f, int split) {
+                if (f >= p.N) return;
+                if (p.y_tma && tokens >= 32) {
+                    uint8_t *piece = staging.next();
+                    stage_tokens<Y_F32>(v, piece, lane, p.bf16);
+                    staging.store(&map_y, piece, int(f), first, split);
+                } else {
+                    uint8_t *Y = static_cast<uint8_t *>(p.Y) + split * p.split_stride * (Y_F32 ? 4 : 2);
+                    store_tokens<Y_F32>(v, staging.all(), lane, Y, ldy, first, tokens, f, p.N, p.bf16);
+                }
+            };
+            for (int u = unit0, n = 0; u < units; u += step, ++n) {
+                if (!wanted(n)) continue;
+                const LinearUnit x = linear_unit(p, sh, u, group);
+                const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
+                if (epilogue_any(!got)) {  // the warps give up together
+                    watch.raise();
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * kAccCols);
+                if (EPI == kGated) {
+                    // quarters 0, 1 hold gate rows, 2, 3 the up rows of the same features; of two
+                    // pieces of 32 tokens the gate's warp finishes the first, the up's warp the second
+                    const bool up = quarter >= 2;
+                    const int64_t f = int64_t(x.feature_tile) * 128 + int64_t(rank) * 64 + (quarter & 1) * 32;
+                    const int meet = 2 + 2 * half + (quarter & 1);  // named barrier of the two warps
+                    float *own = reinterpret_cast<float *>(tile);
+                    const float *other = reinterpret_cast<const float *>(sh.epi + ((warp - 2) ^ 2) * 4096);
+                    if (64 * half >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
+#pragma unroll 1
+                    for (int c = 64 * half; c < x.width; c += 128) {
+                        const bool two = c + 32 < x.width;
+                        float v0[32], v1[32];
+                        __syncwarp();
+                        tmem_ld_32(taddr + c, v0);
+                        if (two) tmem_ld_32(taddr + c + 32, v1);
+                        if (c + 128 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
+                        staging.all();
+                        if (p.pre != nullptr) {
+                            uint8_t *pre = static_cast<uint8_t *>(p.pre) + (up ? p.N * 2 : 0);
+                            if (f + 32 <= p.N && p.N % 8 == 0) {
+                                store_tokens<false>(v0, tile, lane, pre, p.ldp * 2, x.first + c, x.tokens - c, f, p.N, p.bf16);
+                                if (two)
+                                    store_tokens<false>(v1, tile, lane, pre, p.ldp * 2, x.first + c + 32, x.tokens - c - 32, f,
+                                                        p.N, p.bf16);
+                            } else if (f + lane < p.N) {  // the up half's pieces may not be 16-byte aligned
+                                uint16_t *dst = reinterpret_cast<uint16_t *>(pre) + int64_t(x.first + c) * p.ldp + f + lane;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    if (c + i < x.tokens) dst[i * p.ldp] = to_16(v0[i], p.bf16);
+                                    if (two && c + 32 + i < x.tokens) dst[(32 + i) * p.ldp] = to_16(v1[i], p.bf16);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        if (up) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) own[i * 32 + lane] = v0[i];
+                        } else if (two) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) own[i * 32 + lane] = v1[i];
+                        }
+                        asm volatile("bar.sync %0, 64;" ::"r"(meet) : "memory");
+                        if (!up) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v0[i] = silu(v0[i]) * other[i * 32 + lane];
+                        } else if (two) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v0[i] = silu(other[i * 32 + lane]) * v1[i];
+                        }
+                        asm volatile("bar.sync %0, 64;" ::"r"(meet) : "memory");
+                        const int at = up ? c + 32 : c;
+                        if (!up || two) put(v0, x.first + at, x.tokens - at, f, 0);
+                    }
+                } else {
+                    const int64_t f = int64_t(x.feature_tile) * 256 + int64_t(rank) * 128 + quarter * 32;
+                    if (32 * half >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
+#pragma unroll 1
+                    for (int c = 32 * half; c < x.width; c += 64) {
+                        float v[32];
+                        __syncwarp();
+                        tmem_ld_32(taddr + c, v);
+                        if (c + 64 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
+                        if (EPI == kAdapted && !careful) {
+                            bool finite = true;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) finite = finite && fabsf(v[i]) <= FLT_MAX;
+                            if (__any_sync(kFull, !finite) && lane == 0) atomicOr(sh.again + ((n >> 5) & 1), 1u << (n & 31));
+                        } else if (EPI == kAdapted) {
+                            float *sums = reinterpret_cast<float *>(staging.all());
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sums[i * 32 + lane] = v[i];
+                            __syncwarp();
+                            add_late(p, x, sums, x.first + c, x.tokens - c, f, lane);
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = sums[i * 32 + lane];
+                            __syncwarp();
+                        }
+                        put(v, x.first + c, x.tokens - c, f, x.split);
+                    }
+                }
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
-            if (!ok && leader) drain_issuer(sh);
+            staging.finish();
         }
-    } else {
-        // ---------------- epilogue: TMEM lanes 32 * quarter .. of this CTA's 128 rows
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        uint8_t *tile = sh.epi + (warp - 2) * 4096;
-        Staging<Y_F32> staging(tile, lane);
-        int acc = 0, group = 0;
-        uint32_t acc_phase = 0;
-        const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
-        const int64_t ldy = p.ldy * (Y_F32 ? 4 : 2);
-        auto put = [&](const float (&v)[32], int first, int tokens, int64_t f, int split) {
-            if (f >= p.N) return;
-            if (p.y_tma && tokens >= 32) {
-                uint8_t *piece = staging.next();
-                stage_tokens<Y_F32>(v, piece, lane, p.bf16);
-                staging.store(&map_y, piece, int(f), first, split);
-            } else {
-                uint8_t *Y = static_cast<uint8_t *>(p.Y) + split * p.split_stride * (Y_F32 ? 4 : 2);
-                store_tokens<Y_F32>(v, staging.all(), lane, Y, ldy, first, tokens, f, p.N, p.bf16);
-            }
-        };
-        for (int u = unit0; u < units; u += step) {
-            const LinearUnit x = linear_unit(p, sh, u, group);
-            const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
-            if (epilogue_any(!got)) {  // the warps give up together
-                watch.raise();
-                break;
-            }
-            tc_fence_after();
-            const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * kAccCols);
-            if (EPI == kGated) {
-                // quarters 0, 1 hold gate rows, 2, 3 the up rows of the same features; of two
-                // pieces of 32 tokens the gate's warp finishes the first, the up's warp the second
-                const bool up = quarter >= 2;
-                const int64_t f = int64_t(x.feature_tile) * 128 + int64_t(rank) * 64 + (quarter & 1) * 32;
-                const int meet = 2 + 2 * half + (quarter & 1);  // named barrier of the two warps
-                float *own = reinterpret_cast<float *>(tile);
-                const float *other = reinterpret_cast<const float *>(sh.epi + ((warp - 2) ^ 2) * 4096);
-                if (64 * half >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
-#pragma unroll 1
-                for (int c = 64 * half; c < x.width; c += 128) {
-                    const bool two = c + 32 < x.width;
-                    float v0[32], v1[32];
-                    __syncwarp();
-                    tmem_ld_32(taddr + c, v0);
-                    if (two) tmem_ld_32(taddr + c + 32, v1);
-                    if (c + 128 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
-                    staging.all();
-                    if (p.pre != nullptr) {
-                        uint8_t *pre = static_cast<uint8_t *>(p.pre) + (up ? p.N * 2 : 0);
-                        if (f + 32 <= p.N && p.N % 8 == 0) {
-                            store_tokens<false>(v0, tile, lane, pre, p.ldp * 2, x.first + c, x.tokens - c, f, p.N, p.bf16);
-                            if (two)
-                                store_tokens<false>(v1, tile, lane, pre, p.ldp * 2, x.first + c + 32, x.tokens - c - 32, f,
-                                                    p.N, p.bf16);
-                        } else if (f + lane < p.N) {  // the up half's pieces may not be 16-byte aligned
-                            uint16_t *dst = reinterpret_cast<uint16_t *>(pre) + int64_t(x.first + c) * p.ldp + f + lane;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (c + i < x.tokens) dst[i * p.ldp] = to_16(v0[i], p.bf16);
-                                if (two && c + 32 + i < x.tokens) dst[(32 + i) * p.ldp] = to_16(v1[i], p.bf16);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    if (up) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) own[i * 32 + lane] = v0[i];
-                    } else if (two) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) own[i * 32 + lane] = v1[i];
-                    }
-                    asm volatile("bar.sync %0, 64;" ::"r"(meet) : "memory");
-                    if (!up) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v0[i] = silu(v0[i]) * other[i * 32 + lane];
-                    } else if (two) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v0[i] = silu(other[i * 32 + lane]) * v1[i];
-                    }
-                    asm volatile("bar.sync %0, 64;" ::"r"(meet) : "memory");
-                    const int at = up ? c + 32 : c;
-                    if (!up || two) put(v0, x.first + at, x.tokens - at, f, 0);
-                }
-            } else {
-                const int64_t f = int64_t(x.feature_tile) * 256 + int64_t(rank) * 128 + quarter * 32;
-                if (32 * half >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
-#pragma unroll 1
-                for (int c = 32 * half; c < x.width; c += 64) {
-                    float v[32];
-                    __syncwarp();
-                    tmem_ld_32(taddr + c, v);
-                    if (c + 64 >= x.width) release_accumulator(acc_empty0 + 8u * acc, lane);
-                    put(v, x.first + c, x.tokens - c, f, x.split);
-                }
-            }
-            if (++acc == 2) {
-                acc = 0;
-                acc_phase ^= 1u;
-            }
-        }
-        staging.finish();
+        if (EPI != kAdapted || careful || (again = tiles_again(sh)) == 0u) break;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     tear_down(tmem);
 }
@@ -1324,6 +1458,10 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, Tiling 
         p.rank = a.ad.rank;
         p.parts = in.parts;
         p.plane_rows = int(in.plane_rows);
+        p.values = reinterpret_cast<const float *>(static_cast<const char *>(a.ad.inner) + in.values_at());
+        p.b = a.ad.b;
+        p.ldb = a.ad.ldb;
+        p.strideb = a.ad.strideb;
     }
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);

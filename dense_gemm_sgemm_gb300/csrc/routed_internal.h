@@ -166,17 +166,20 @@ cudaError_t launch_gated_silu_backward(int type, int dh_type, int64_t rows, int6
 // For the tcgen05 kernel: 16-bit parts that sum to the fp32 value, part i of 64 ranks in plane i *
 // blocks + block, rows of 64; tokens in blocks of 32, where block b of request q is rows 32 (b + q) ..
 // of a plane and tokens of other requests are zeros, so that one request's blocks are contiguous.
+// Behind the planes the fp32 values, as the few-rows kernel takes them: where a part or a zero does not
+// stand for its value (0 * inf) the tcgen05 kernel's epilogue takes them too (TileRequests).
 struct InnerLayout {
     int parts, blocks;
-    int64_t plane_rows;
-    __host__ __device__ int64_t bytes() const { return plane_rows * 128 * parts * blocks; }
+    int64_t plane_rows, values;
+    __host__ __device__ int64_t values_at() const { return plane_rows * 128 * parts * blocks; }
+    __host__ __device__ int64_t bytes() const { return values_at() + 4 * values; }
 };
 // Parts: fp16's two hold 22 bits.  bf16's two hold 16, 2^8 times finer than a 16-bit output; an fp32
 // output takes three.
 inline int inner_parts(int type, int y_type) { return type == GEMM_TYPE_BF16 && y_type == GEMM_TYPE_F32 ? 3 : 2; }
 __host__ __device__ inline InnerLayout inner_layout(int64_t tokens, int64_t requests, int64_t rank, int parts)
 {
-    return InnerLayout{parts, int((rank + 63) / 64), (tokens / 32 + requests) * 32};
+    return InnerLayout{parts, int((rank + 63) / 64), (tokens / 32 + requests) * 32, tokens * rank};
 }
 struct Adapters {
     const void *b;  // NULL: no adapters
@@ -249,7 +252,7 @@ struct ShrinkArgs {
     const float *scales;
     float *inner;    // few-rows form, NULL: the other
     int32_t *which;
-    void *planes;    // tcgen05 form, of `parts`
+    void *planes;    // tcgen05 form, of `parts`, and the fp32 values
     int n_parts;
 };
 cudaError_t launch_shrink(const ShrinkArgs &a, cudaStream_t stream);

@@ -454,7 +454,8 @@ GEMM_API gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw
  * owns tokens segments[q] .. segments[q + 1] - 1 (requests + 1 values that do not decrease,
  * clamped to [0, T]) and uses adapter adapters[q]; an adapter outside [0, n_adapters) means none,
  * as does lying in no request.  scales: n_adapters floats, NULL: 1.  An adapter of a rank below R
- * is padded with zero rows of A_a.
+ * is padded with zero rows of A_a.  An infinity or NaN in an adapter or in a token's row of X reaches
+ * the tokens that use it only.
  *
  * The inner products scales[a] * X A^T are summed in fp32.  For many tokens they enter the second
  * product as sums of 16-bit parts: of bf16 to 16 bits (24 when Y is fp32), of fp16 to 22 bits, where
