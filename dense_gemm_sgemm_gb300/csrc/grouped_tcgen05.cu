@@ -22,7 +22,7 @@
 // 341 us), with mma.sync there by tcgen05, which goes first (371 us).  An infinity or NaN in an adapter's
 // B would spoil the columns of its neighbours, where it meets zeros: the epilogue notes the tiles whose
 // sums are not finite, and the pair computes those a second time with such adapters' products in fp32
-// on the CUDA cores (TileRequests).
+// on the CUDA cores, as well as those whose inner products the 16-bit parts cannot hold (TileRequests).
 //
 // Weight gradient.  dW_g[n][k] sums over the group's positions, the K dimension of this product,
 // both operands "transposed" (MN-major).  Slices are 64 positions; the last one of a group also holds
@@ -456,8 +456,9 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint8_t *tile
 
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
 
-// Whether an adapter's rows of B for a tile of 256 features hold an infinity or NaN.
-__device__ __noinline__ bool unfit(const LinearParams &p, int adapter, int feature_tile, int lane)
+// Whether the tensor cores cannot form a request's product: an adapter's rows of B for a tile of 256
+// features hold an infinity or NaN, or a finite inner product of tokens [t0, t1) has an infinite part.
+__device__ __noinline__ bool unfit(const LinearParams &p, int adapter, int feature_tile, int t0, int t1, int lane)
 {
     const uint32_t exponent = p.bf16 ? 0x7f80u : 0x7c00u;  // all ones: no finite number
     const int64_t f0 = int64_t(feature_tile) * 256;
@@ -470,6 +471,10 @@ __device__ __noinline__ bool unfit(const LinearParams &p, int adapter, int featu
 #pragma unroll
         for (int c = 0; c < 4; ++c) found |= (w[c] & exponent) == exponent || ((w[c] >> 16) & exponent) == exponent;
     }
+    for (int64_t i = int64_t(t0) * p.rank + lane; i < int64_t(t1) * p.rank; i += 32) {
+        const float v = __ldcg(p.values + i);
+        found |= fabsf(v) <= FLT_MAX && (to_16(v, p.bf16) & exponent) == exponent;
+    }
     return __any_sync(kFull, found);
 }
 
@@ -481,7 +486,8 @@ __device__ __noinline__ bool unfit(const LinearParams &p, int adapter, int featu
 // the same adapter rows.
 //
 // The columns of a request's slices are whole blocks of 32, in which other requests' tokens are zeros, so
-// an infinity or NaN among the adapter's rows would make NaN of them.  A tile whose sums are not all
+// an infinity or NaN among the adapter's rows would make NaN of them; and fp16's parts of an inner product
+// beyond 65504, or bf16's of one close to fp32's largest, are infinite though their value is not.  A tile whose sums are not all
 // finite is computed a second time (`careful`), in which requests whose product is unfit for the tensor
 // cores are left out of the slices and added to the sums by the epilogue (add_late).  What the other
 // requests get does not depend on them in a bit: the same slices in the same order.  Where all values are
@@ -523,7 +529,8 @@ struct TileRequests {
         if (careful)
             for (unsigned look = left; look != 0u; look &= look - 1u) {
                 const int at = __ffs(look) - 1;
-                if (unfit(p, __shfl_sync(kFull, ad, at), feature_tile, lane)) late |= 1u << at;
+                if (unfit(p, __shfl_sync(kFull, ad, at), feature_tile, __shfl_sync(kFull, lo, at), __shfl_sync(kFull, hi, at), lane))
+                    late |= 1u << at;
             }
         more = __any_sync(kFull, q == q0 + 31 && q + 1 < p.requests && clamp_to(__ldg(p.segments + q + 1), p.y_rows) < t1);
     }

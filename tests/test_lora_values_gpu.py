@@ -121,3 +121,33 @@ def test_whole_batches_of_bad_values_expire_no_wait(T, requests, R):
     x[:] = math.nan
     assert torch.isnan(g.lora_linear(x, w, a, b, cuts, who)).all()
     assert g.gemm_get_device_status() == 0
+
+
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+def test_inner_products_beyond_fp16(batch, out_dtype):
+    # inner products of about 10^5, on both sides of fp16's largest, times small B: ordinary results
+    lengths, who = BATCHES[batch]
+    for R in (8, 40, 128):
+        c = _case(lengths, who, R, 264, 200, torch.float16, seed=R)
+        c["a"][0] *= 20000.0
+        c["x"] *= 4.0
+        c["b"] *= 2.0 ** -9
+        seg = c["segments"].tolist()
+        inner = torch.cat([c["x"][seg[q]:seg[q + 1]].double() @ c["a"][0].double().T for q, i in enumerate(who) if i == 0])
+        assert (inner.abs() > 65520).any() and (inner.abs() < 65504).any()
+        _check(c, R, out_dtype)
+
+
+@pytest.mark.parametrize("tokens", [3, 100])
+def test_inner_products_beyond_bf16(tokens):
+    # fp32 values above bf16's largest: inner = scale
+    x = torch.ones(tokens, 8, dtype=torch.bfloat16)
+    x[:, 1:] = 0.0
+    a, b = torch.zeros(1, 8, 8, dtype=torch.bfloat16), torch.zeros(1, 40, 8, dtype=torch.bfloat16)
+    a[0, 2, 0], b[0, :, 2] = 1.0, 2.0 ** -120
+    w = torch.zeros(40, 8, dtype=torch.bfloat16)
+    scale = torch.tensor([3.4e38])
+    y = g.lora_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), torch.tensor([0, tokens], dtype=torch.int32, device="cuda"),
+                      torch.zeros(1, dtype=torch.int32, device="cuda"), scales=scale.cuda(), out_dtype=torch.float32)
+    assert torch.equal(y.cpu(), (scale * 2.0 ** -120).expand(tokens, 40))
