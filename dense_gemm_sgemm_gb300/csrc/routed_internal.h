@@ -174,7 +174,9 @@ struct InnerLayout {
     __host__ __device__ int64_t values_at() const { return plane_rows * 128 * parts * blocks; }
     __host__ __device__ int64_t bytes() const { return values_at() + 4 * values; }
 };
-// Parts: fp16's two hold 22 bits.  bf16's two hold 16, 2^8 times finer than a 16-bit output; an fp32
+// Parts: fp16's two hold 22 bits from 2^-3 up and the multiples of 2^-24 below it, an error of 2^-25 at
+// most: next to the products that they are added to that matters to values of that size only, and a third
+// part would have the same spacing.  bf16's two hold 16, 2^8 times finer than a 16-bit output; an fp32
 // output takes three.
 inline int inner_parts(int type, int y_type) { return type == GEMM_TYPE_BF16 && y_type == GEMM_TYPE_F32 ? 3 : 2; }
 __host__ __device__ inline InnerLayout inner_layout(int64_t tokens, int64_t requests, int64_t rank, int parts)

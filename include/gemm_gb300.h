@@ -458,8 +458,10 @@ GEMM_API gemm_status_t gemm_grouped_weight_grad(gemm_type_t type, gemm_type_t dw
  * the tokens that use it only.
  *
  * The inner products scales[a] * X A^T are summed in fp32.  For many tokens they enter the second
- * product as sums of 16-bit parts: of bf16 to 16 bits (24 when Y is fp32), of fp16 to 22 bits, below
- * 2^-14 to 2^-25; those that the parts cannot hold (beyond 65504) stay in fp32.
+ * product as sums of 16-bit parts: of bf16 to 16 bits (24 when Y is fp32); of fp16 to 22 bits from
+ * 2^-3 up, and to 2^-25 below it, where the second part's own spacing is 2^-24 whatever the value (12 bits
+ * are left at 2^-13: inner products that small want a larger A and a smaller B); those that the parts
+ * cannot hold (beyond 65504) stay in fp32.
  *
  * work: gemm_lora_work_bytes(T, N, K, requests, R) bytes for the call to use (not kept; NULL when
  * there are no requests, no adapters, or R or K is 0).  That function gives the bytes for the current

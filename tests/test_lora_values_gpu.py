@@ -151,3 +151,24 @@ def test_inner_products_beyond_bf16(tokens):
     y = g.lora_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), torch.tensor([0, tokens], dtype=torch.int32, device="cuda"),
                       torch.zeros(1, dtype=torch.int32, device="cuda"), scales=scale.cuda(), out_dtype=torch.float32)
     assert torch.equal(y.cpu(), (scale * 2.0 ** -120).expand(tokens, 40))
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(torch.float16, torch.float32), (torch.bfloat16, torch.float32),
+                                             (torch.bfloat16, torch.bfloat16)])
+@pytest.mark.parametrize("tokens", [40, 130])
+def test_precision_of_the_inner_products(dtype, out_dtype, tokens):
+    # x = a = b = 1 and one adapter a token: the outputs are the inner products, which are the scales
+    gen = torch.Generator().manual_seed(tokens)
+    scales = torch.exp2(torch.rand(tokens, generator=gen) * 31 - 16) * torch.where(torch.rand(tokens, generator=gen) < 0.5, -1, 1)
+    one = torch.ones(tokens, 8, 8, dtype=dtype, device="cuda")[..., :1]
+    y = g.lora_linear(one[:, 0], torch.zeros(8, 8, dtype=dtype, device="cuda")[:, :1], one[:, :1], one,
+                      torch.arange(tokens + 1, dtype=torch.int32, device="cuda"),
+                      torch.arange(tokens, dtype=torch.int32, device="cuda"), scales=scales.cuda(), out_dtype=out_dtype)
+    v = scales.double().abs()
+    if tokens <= 64:
+        bound = torch.zeros_like(v)  # fp32
+    elif dtype is torch.float16:
+        bound = torch.maximum(v * 2.0 ** -22, torch.tensor(2.0 ** -25))
+    else:
+        bound = v * (2.0 ** -24 if out_dtype is torch.float32 else 2.0 ** -16)
+    ref.assert_within(y.cpu(), scales.double()[:, None].expand(-1, 8), bound[:, None].expand(-1, 8))
