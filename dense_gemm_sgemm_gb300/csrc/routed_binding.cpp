@@ -9,6 +9,7 @@
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Device.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -22,11 +23,23 @@ namespace {
 
 PyObject *g_error = nullptr;  // GemmError
 
-const at::Tensor &tensor(PyObject *o, const char *what)
+// The device of a call's operands: its first tensor's, on whose stream the kernels run.  They read the
+// others by their addresses, so a tensor of another device is refused before anything is launched.
+struct Device {
+    std::optional<c10::Device> of;
+    void agree(c10::Device d, const char *what)
+    {
+        if (!of) of = d;
+        TORCH_CHECK_VALUE(d == *of, what, ": on ", d, ", the call's first tensor on ", *of);
+    }
+};
+
+const at::Tensor &tensor(Device &device, PyObject *o, const char *what)
 {
     TORCH_CHECK_TYPE(THPVariable_Check(o), what, ": a torch tensor is wanted");
     const at::Tensor &t = THPVariable_Unpack(o);
     TORCH_CHECK_VALUE(t.is_cuda(), what, ": must live in CUDA device memory");
+    device.agree(t.device(), what);
     return t;
 }
 
@@ -36,9 +49,9 @@ struct Matrix {
     int64_t rows, cols, ld;
     void *data() const { return t.data_ptr(); }
 };
-Matrix matrix(PyObject *o, const char *what, int dims = 2)
+Matrix matrix(Device &device, PyObject *o, const char *what, int dims = 2)
 {
-    const at::Tensor &t = tensor(o, what);
+    const at::Tensor &t = tensor(device, o, what);
     TORCH_CHECK_VALUE(t.dim() == dims && (t.size(-1) <= 1 || t.stride(-1) == 1), what, ": ", dims,
                       "-D with unit column stride wanted");
     const int64_t rows = t.size(-2), cols = t.size(-1);
@@ -57,22 +70,22 @@ void same_type(const at::Tensor &t, at::ScalarType type, const char *what)
 }
 
 // A contiguous array of `count` values; None: NULL.
-void *array(PyObject *o, const char *what, at::ScalarType type, int64_t count, bool optional = false)
+void *array(Device &device, PyObject *o, const char *what, at::ScalarType type, int64_t count, bool optional = false)
 {
     if (optional && o == Py_None) return nullptr;
-    const at::Tensor &t = tensor(o, what);
+    const at::Tensor &t = tensor(device, o, what);
     same_type(t, type, what);
     TORCH_CHECK_VALUE(t.is_contiguous(), what, ": must be contiguous");
     same(t.numel(), count, what);
     return t.data_ptr();
 }
-int32_t *ints(PyObject *o, const char *what, int64_t count, bool optional = false)
+int32_t *ints(Device &device, PyObject *o, const char *what, int64_t count, bool optional = false)
 {
-    return static_cast<int32_t *>(array(o, what, at::kInt, count, optional));
+    return static_cast<int32_t *>(array(device, o, what, at::kInt, count, optional));
 }
-float *floats(PyObject *o, const char *what, int64_t count, bool optional = false)
+float *floats(Device &device, PyObject *o, const char *what, int64_t count, bool optional = false)
 {
-    return static_cast<float *>(array(o, what, at::kFloat, count, optional));
+    return static_cast<float *>(array(device, o, what, at::kFloat, count, optional));
 }
 
 gemm_type_t type_of(at::ScalarType t, const char *what)
@@ -188,19 +201,20 @@ void count_args(Py_ssize_t n, Py_ssize_t wanted)
     PyObject *name(PyObject *, PyObject *const *a, Py_ssize_t nargs)                \
     {                                                                               \
         HANDLE_TH_ERRORS                                                            \
-        count_args(nargs, n);
+        count_args(nargs, n);                                                       \
+        Device device;
 #define END_BOUND          \
     END_HANDLE_TH_ERRORS   \
     }
 
 // logits, top_k, bias, score, groups, groups_kept, group_top, renormalise, scale, stream
 BOUND(moe_route, 10)
-    const Matrix x = matrix(a[0], "logits");
+    const Matrix x = matrix(device, a[0], "logits");
     const Stream stream(a[9], x.t);
     const int64_t T = x.rows, E = x.cols, k = small(a[1]);
     TORCH_CHECK_VALUE(k >= 1 && k <= 1024, "top_k: ", k);
     const gemm_type_t type = type_of(x.t.scalar_type(), "logits");
-    const float *bias = floats(a[2], "bias", E, true);
+    const float *bias = floats(device, a[2], "bias", E, true);
     at::Tensor ids = fresh({T, k}, at::kInt, x.t), weights = fresh({T, k}, at::kFloat, x.t);
     at::Tensor offsets = fresh({E + 1}, at::kInt, x.t), tokens = fresh({T * k}, at::kInt, x.t), where = fresh({T, k}, at::kInt, x.t);
     const auto score = static_cast<gemm_score_t>(small(a[3]));
@@ -217,12 +231,12 @@ END_BOUND
 
 // dweights, logits, ids, score, renormalise, scale, stream
 BOUND(moe_route_backward, 7)
-    const Matrix x = matrix(a[1], "logits"), id = matrix(a[2], "ids");
+    const Matrix x = matrix(device, a[1], "logits"), id = matrix(device, a[2], "ids");
     const Stream stream(a[6], x.t);
     const int64_t T = x.rows, E = x.cols, k = id.cols;
     const gemm_type_t type = type_of(x.t.scalar_type(), "logits");
-    const float *dw = floats(a[0], "dweights", T * k);
-    const int32_t *ids = ints(a[2], "ids", T * k);
+    const float *dw = floats(device, a[0], "dweights", T * k);
+    const int32_t *ids = ints(device, a[2], "ids", T * k);
     at::Tensor out = fresh({T, E}, x.t.scalar_type(), x.t);
     const auto score = static_cast<gemm_score_t>(small(a[3]));
     const bool renormalise = truth(a[4]);
@@ -236,11 +250,11 @@ END_BOUND
 
 // ids, experts, stream
 BOUND(moe_plan, 3)
-    const Matrix id = matrix(a[0], "ids");
+    const Matrix id = matrix(device, a[0], "ids");
     const Stream stream(a[2], id.t);
     const int64_t T = id.rows, k = id.cols, E = integer(a[1]);
     TORCH_CHECK_VALUE(E >= 1 && E <= 1024, "experts: ", E);
-    const int32_t *ids = ints(a[0], "ids", T * k);
+    const int32_t *ids = ints(device, a[0], "ids", T * k);
     at::Tensor offsets = fresh({E + 1}, at::kInt, id.t), tokens = fresh({T * k}, at::kInt, id.t), where = fresh({T, k}, at::kInt, id.t);
     call("gemm_moe_plan", [&] {
         return gemm_moe_plan(T, E, int(k), ids, offsets.data_ptr<int32_t>(), tokens.data_ptr<int32_t>(),
@@ -251,12 +265,12 @@ END_BOUND
 
 // x, where, weights, stream
 BOUND(moe_dispatch, 4)
-    const Matrix x = matrix(a[0], "x"), slot = matrix(a[1], "where");
+    const Matrix x = matrix(device, a[0], "x"), slot = matrix(device, a[1], "where");
     const Stream stream(a[3], x.t);
     const int64_t T = x.rows, H = x.cols, k = slot.cols, slots = T * k;
     const gemm_type_t type = type_of(x.t.scalar_type(), "x");
-    const int32_t *where = ints(a[1], "where", slots);
-    const float *weights = floats(a[2], "weights", slots, true);
+    const int32_t *where = ints(device, a[1], "where", slots);
+    const float *weights = floats(device, a[2], "weights", slots, true);
     Padded out = padded(slots, H, x.t.scalar_type(), x.t);
     call("gemm_moe_dispatch", [&] {
         return gemm_moe_dispatch(type, T, H, int(k), x.data(), x.ld, where, weights, slots, out.t.data_ptr(), out.ld, stream.handle);
@@ -266,12 +280,12 @@ END_BOUND
 
 // rows, where, weights, out_dtype, stream
 BOUND(moe_combine, 5)
-    const Matrix r = matrix(a[0], "rows"), slot = matrix(a[1], "where");
+    const Matrix r = matrix(device, a[0], "rows"), slot = matrix(device, a[1], "where");
     const Stream stream(a[4], r.t);
     const int64_t T = slot.rows, k = slot.cols, slots = T * k;
     const gemm_type_t type = type_of(r.t.scalar_type(), "rows");
-    const int32_t *where = ints(a[1], "where", slots);
-    const float *weights = floats(a[2], "weights", slots, true);
+    const int32_t *where = ints(device, a[1], "where", slots);
+    const float *weights = floats(device, a[2], "weights", slots, true);
     const at::ScalarType dtype = dtype_of(a[3], r.t.scalar_type());
     const gemm_type_t y_type = type_of(dtype, "out_dtype");
     Padded y = padded(T, r.cols, dtype, r.t);
@@ -284,13 +298,13 @@ END_BOUND
 
 // dy, rows, where, weights, stream
 BOUND(moe_combine_backward, 5)
-    const Matrix dy = matrix(a[0], "dy"), r = matrix(a[1], "rows"), slot = matrix(a[2], "where");
+    const Matrix dy = matrix(device, a[0], "dy"), r = matrix(device, a[1], "rows"), slot = matrix(device, a[2], "where");
     const Stream stream(a[4], dy.t);
     const int64_t T = dy.rows, H = dy.cols, k = slot.cols, slots = T * k;
     same(r.cols, H, "columns of rows");
     const gemm_type_t type = type_of(dy.t.scalar_type(), "dy"), rows_type = type_of(r.t.scalar_type(), "rows");
-    const int32_t *where = ints(a[2], "where", slots);
-    const float *weights = floats(a[3], "weights", slots, true);
+    const int32_t *where = ints(device, a[2], "where", slots);
+    const float *weights = floats(device, a[3], "weights", slots, true);
     Padded drows = padded(r.rows, H, dy.t.scalar_type(), dy.t);
     at::Tensor dweights = fresh({T, k}, at::kFloat, dy.t);
     call("gemm_moe_combine_backward", [&] {
@@ -302,7 +316,7 @@ END_BOUND
 
 // pre, dh, stream
 BOUND(gated_silu_backward, 3)
-    const Matrix pre = matrix(a[0], "pre"), dh = matrix(a[1], "dh");
+    const Matrix pre = matrix(device, a[0], "pre"), dh = matrix(device, a[1], "dh");
     const Stream stream(a[2], pre.t);
     same(pre.cols % 2, 0, "odd columns of pre");
     same(dh.rows, pre.rows, "rows of dh");
@@ -318,7 +332,7 @@ END_BOUND
 
 // x, w, offsets, rows, op, gated, out_dtype, pre, stream
 BOUND(grouped_linear, 9)
-    const Matrix x = matrix(a[0], "x"), w = matrix(a[1], "w", 3);
+    const Matrix x = matrix(device, a[0], "x"), w = matrix(device, a[1], "w", 3);
     const Stream stream(a[8], x.t);
     const at::ScalarType in = x.t.scalar_type(), dtype = dtype_of(a[6], in);
     same_type(w.t, in, "w");
@@ -332,17 +346,17 @@ BOUND(grouped_linear, 9)
         same(N % 2, 0, "odd rows of gated w");
         N /= 2;
     }
-    const int32_t *offsets = ints(a[2], "offsets", groups + 1), *rows = nullptr;
+    const int32_t *offsets = ints(device, a[2], "offsets", groups + 1), *rows = nullptr;
     int64_t y_rows = x.rows;
     if (a[3] != Py_None) {
-        y_rows = tensor(a[3], "rows").numel();
-        rows = ints(a[3], "rows", y_rows);
+        y_rows = tensor(device, a[3], "rows").numel();
+        rows = ints(device, a[3], "rows", y_rows);
     }
     Padded y = padded(y_rows, N, dtype, x.t);
     void *pre = nullptr;
     int64_t ldp = 0;
     if (a[7] != Py_None) {
-        const Matrix m = matrix(a[7], "pre");
+        const Matrix m = matrix(device, a[7], "pre");
         same_type(m.t, in, "pre");
         same(m.rows, y_rows, "rows of pre");
         same(m.cols, 2 * N, "columns of pre");
@@ -361,15 +375,15 @@ END_BOUND
 
 // dy, x, offsets, out_dtype, stream
 BOUND(grouped_weight_grad, 5)
-    const Matrix dy = matrix(a[0], "dy"), x = matrix(a[1], "x");
+    const Matrix dy = matrix(device, a[0], "dy"), x = matrix(device, a[1], "x");
     const Stream stream(a[4], dy.t);
     const at::ScalarType in = dy.t.scalar_type(), dtype = dtype_of(a[3], at::kFloat);
     same_type(x.t, in, "x");
     same(x.rows, dy.rows, "rows of x");
     const gemm_type_t type = type_of(in, "dy"), dw_type = type_of(dtype, "out_dtype");
-    const int64_t groups = tensor(a[2], "offsets").numel() - 1, N = dy.cols, K = x.cols, ld = (K + 7) & ~int64_t(7);
+    const int64_t groups = tensor(device, a[2], "offsets").numel() - 1, N = dy.cols, K = x.cols, ld = (K + 7) & ~int64_t(7);
     TORCH_CHECK_VALUE(groups >= 0, "offsets: one value at least is wanted");
-    const int32_t *offsets = ints(a[2], "offsets", groups + 1);
+    const int32_t *offsets = ints(device, a[2], "offsets", groups + 1);
     at::Tensor dw = fresh({groups, N, ld}, dtype, dy.t);
     call("gemm_grouped_weight_grad", [&] {
         return gemm_grouped_weight_grad(type, dw_type, groups, offsets, N, K, dy.data(), dy.ld, x.data(), x.ld, dy.rows,
@@ -380,7 +394,7 @@ END_BOUND
 
 // x, w, a, b, segments, adapters, scales, out_dtype, stream
 BOUND(lora_linear, 9)
-    const Matrix x = matrix(a[0], "x"), w = matrix(a[1], "w"), A = matrix(a[2], "a", 3), B = matrix(a[3], "b", 3);
+    const Matrix x = matrix(device, a[0], "x"), w = matrix(device, a[1], "w"), A = matrix(device, a[2], "a", 3), B = matrix(device, a[3], "b", 3);
     const Stream stream(a[8], x.t);
     const at::ScalarType in = x.t.scalar_type(), dtype = dtype_of(a[7], in);
     same_type(w.t, in, "w");
@@ -393,9 +407,9 @@ BOUND(lora_linear, 9)
     same(B.t.size(0), count, "adapters of b");
     same(B.rows, N, "rows of b");
     same(B.cols, R, "columns of b");
-    const int64_t requests = tensor(a[5], "adapters").numel();
-    const int32_t *segments = ints(a[4], "segments", requests + 1), *adapters = ints(a[5], "adapters", requests);
-    const float *scales = floats(a[6], "scales", count, true);
+    const int64_t requests = tensor(device, a[5], "adapters").numel();
+    const int32_t *segments = ints(device, a[4], "segments", requests + 1), *adapters = ints(device, a[5], "adapters", requests);
+    const float *scales = floats(device, a[6], "scales", count, true);
     Padded y = padded(T, N, dtype, x.t);
     at::Tensor work = fresh({gemm_lora_work_bytes(T, N, K, requests, R)}, at::kByte, x.t);
     call("gemm_lora_linear", [&] {
@@ -404,6 +418,15 @@ BOUND(lora_linear, 9)
                                 work.data_ptr(), stream.handle);
     });
     return wrap(y.t);
+END_BOUND
+
+// The comparison alone, of two torch devices: first, other.
+BOUND(same_device, 2)
+    for (int i = 0; i < 2; ++i) {
+        TORCH_CHECK_TYPE(THPDevice_Check(a[i]), "a torch device is wanted");
+        device.agree(reinterpret_cast<THPDevice *>(a[i])->device, "other");
+    }
+    Py_RETURN_NONE;
 END_BOUND
 
 PyObject *set_error(PyObject *, PyObject *cls)
@@ -417,7 +440,7 @@ PyObject *set_error(PyObject *, PyObject *cls)
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(moe_route), ENTRY(moe_route_backward), ENTRY(moe_plan), ENTRY(moe_dispatch), ENTRY(moe_combine),
                          ENTRY(moe_combine_backward), ENTRY(gated_silu_backward), ENTRY(grouped_linear),
-                         ENTRY(grouped_weight_grad), ENTRY(lora_linear), {"set_error", set_error, METH_O, nullptr},
+                         ENTRY(grouped_weight_grad), ENTRY(lora_linear), ENTRY(same_device), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_routed", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
