@@ -1,10 +1,13 @@
 """Build the CUDA library in-tree: dense_gemm_sgemm_gb300/_build/libgemm_gb300.so.
 
-With it goes the Python binding of the routed products, _build/_routed.so, compiled against the
-installed torch.  Every CUDA translation unit under csrc/ is compiled for sm_103a only (tcgen05 and the other
+Every CUDA translation unit under csrc/ is compiled for sm_103a only (tcgen05 and the other
 arch-specific features need the `a` target), in parallel, and linked into one shared
 library with the static CUDA runtime.  No fast-math: denormals, IEEE division and square
 root stay on, which the strict-FP32 path relies on.
+
+With it goes the Python binding of the routed products, _build/_routed.so, compiled against the
+installed torch.  The library does not need it: where the binding cannot be built (no torch, a torch
+without CUDA, no host C++ compiler) the reason is kept beside it and raised when routed.py is imported.
 
     python -m dense_gemm_sgemm_gb300.build [--force] [--verbose-ptxas]
 """
@@ -27,6 +30,8 @@ LIB_NAME = "libgemm_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 BINDING_PATH = os.path.join(OUT_DIR, "_routed.so")
 BINDING_SRC = os.path.join(CSRC, "routed_binding.cpp")
+BINDING_ERROR = os.path.join(OUT_DIR, "_routed.error")  # why there is none
+HEADER = os.path.join(ROOT, "include", "gemm_gb300.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,16 +47,39 @@ def _sources():
 
 
 def _deps():
-    return _sources() + [BINDING_SRC] + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + sorted(
-        glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "gemm_gb300.h"),
-                                                   os.path.abspath(__file__)]
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + sorted(
+        glob.glob(os.path.join(CSRC, "*.cuh"))) + [HEADER, os.path.abspath(__file__)]
+
+
+def _newer(path, deps):
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def _read(path):
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
+def _write(path, text):
+    tmp = path + f".tmp{os.getpid()}"
+    with open(tmp, "w") as f:
+        f.write(text)
+    os.replace(tmp, path)
+
+
+def binding_current() -> bool:
+    return _newer(BINDING_PATH, [BINDING_SRC, HEADER, os.path.abspath(__file__)])
+
+
+def binding_error() -> str:
+    """Why the last build made no binding; empty if it did."""
+    return _read(BINDING_ERROR)
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB_PATH, _deps()) and binding_current()
 
 
 def _compile(nvcc, src, obj, ptxas_verbose):
@@ -65,7 +93,7 @@ def _compile(nvcc, src, obj, ptxas_verbose):
 
 
 def _compile_binding(nvcc, obj):
-    import torch
+    import torch  # an ImportError is kept like a compiler's
 
     include = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
@@ -91,25 +119,52 @@ def _link_binding(obj):
     os.replace(tmp, BINDING_PATH)
 
 
+def _finish_binding(compiled, obj):
+    """Links the binding, or keeps the reason why there is none and leaves no older one behind."""
+    try:
+        _, rc, log = compiled.result()
+        if rc != 0:
+            raise RuntimeError(f"compiling the binding failed:\n{log}")
+        _link_binding(obj)
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)
+        _write(BINDING_ERROR, str(e))
+        print(f"the routed products' Python binding was not built: {e}", file=sys.stderr)
+    else:
+        if os.path.exists(BINDING_ERROR):
+            os.remove(BINDING_ERROR)
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
-    if not force and not ptxas_verbose and up_to_date():
+    anew = force or ptxas_verbose
+    if not anew and up_to_date():
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
-    objs = []
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        binding = os.path.join(OUT_DIR, "routed_binding.o")
-        futs = [ex.submit(_compile_binding, nvcc, binding)]
-        for src in _sources():
-            obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
-            objs.append(obj)
-            futs.append(ex.submit(_compile, nvcc, src, obj, ptxas_verbose))
-        for f in futs:
-            src, rc, log = f.result()
-            if rc != 0:
-                raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{log}")
-            if log.strip() and (ptxas_verbose or not quiet):
-                print(f"--- {os.path.basename(src)}\n{log}", file=sys.stderr)
+        binding, compiled = os.path.join(OUT_DIR, "routed_binding.o"), None
+        if anew or not binding_current():
+            compiled = ex.submit(_compile_binding, nvcc, binding)
+        if anew or not _newer(LIB_PATH, _deps()):
+            _build_library(ex, nvcc, ptxas_verbose, quiet)
+        if compiled is not None:
+            _finish_binding(compiled, binding)
+    return LIB_PATH
+
+
+def _build_library(ex, nvcc, ptxas_verbose, quiet):
+    objs, futs = [], []
+    for src in _sources():
+        obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
+        objs.append(obj)
+        futs.append(ex.submit(_compile, nvcc, src, obj, ptxas_verbose))
+    for f in futs:
+        src, rc, log = f.result()
+        if rc != 0:
+            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{log}")
+        if log.strip() and (ptxas_verbose or not quiet):
+            print(f"--- {os.path.basename(src)}\n{log}", file=sys.stderr)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     # Static CUDA runtime; driver entry points (tensor-map encoding) are looked up at run
     # time through cudaGetDriverEntryPointByVersion, so the library loads without a driver.
@@ -118,8 +173,6 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding)
-    return LIB_PATH
 
 
 def main(argv=None):

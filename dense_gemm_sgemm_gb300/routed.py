@@ -20,8 +20,8 @@ import os
 
 import torch
 
+from . import build
 from ._lib import GEMM_OP_N, GEMM_OP_T, GemmError, load
-from .build import BINDING_PATH
 
 __all__ = [
     "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch", "moe_combine",
@@ -32,9 +32,11 @@ __all__ = [
 
 def _load_binding():
     load()  # the library first: without it the error is its own
-    if not os.path.exists(BINDING_PATH):
-        raise ImportError(f"{BINDING_PATH} is missing: build it with `python -m dense_gemm_sgemm_gb300.build`")
-    spec = importlib.util.spec_from_file_location("_routed", BINDING_PATH)
+    if not os.path.exists(build.BINDING_PATH):
+        reason = build.binding_error()
+        raise ImportError(f"{build.BINDING_PATH} is missing: build it with `python -m dense_gemm_sgemm_gb300.build`"
+                          + (f" (the last build made none: {reason})" if reason else ""))
+    spec = importlib.util.spec_from_file_location("_routed", build.BINDING_PATH)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.set_error(GemmError)

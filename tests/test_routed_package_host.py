@@ -1,4 +1,8 @@
 """The routed products' Python binding and its place in the package and the build, without a GPU."""
+import ctypes
+import os
+import sys
+
 import pytest
 
 from dense_gemm_sgemm_gb300 import build
@@ -21,3 +25,42 @@ def test_operands_of_two_devices_are_refused():
         same(torch.device("cuda:0"), torch.device("cuda:1"))
     with pytest.raises(TypeError):
         same("cuda:0", torch.device("cuda:0"))
+
+
+@pytest.fixture
+def elsewhere(tmp_path, monkeypatch):
+    """The build's outputs in a folder of their own, with one small source in the library's place."""
+    for name in ("LIB_PATH", "BINDING_PATH", "BINDING_ERROR", "BINDING_FOR"):
+        if hasattr(build, name):
+            monkeypatch.setattr(build, name, str(tmp_path / os.path.basename(getattr(build, name))))
+    monkeypatch.setattr(build, "OUT_DIR", str(tmp_path))
+    source = tmp_path / "one.cu"
+    source.write_text('extern "C" __attribute__((visibility("default"))) int one(void) { return 1; }')
+    monkeypatch.setattr(build, "_sources", lambda: [str(source)])
+    return tmp_path
+
+
+def test_the_library_builds_without_torch(elsewhere, monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch fails
+    assert ctypes.CDLL(build.build()).one() == 1
+    assert not os.path.exists(build.BINDING_PATH)
+    assert "torch" in build.binding_error()
+
+
+def test_the_library_builds_without_a_host_compiler(elsewhere, monkeypatch):
+    pytest.importorskip("torch")
+    monkeypatch.setenv("CXX", "false")
+    open(build.BINDING_PATH, "w").close()  # one of older sources is not left behind
+    assert ctypes.CDLL(build.build(force=True)).one() == 1
+    assert not os.path.exists(build.BINDING_PATH)
+    assert build.binding_error()
+
+
+def test_why_there_is_no_binding_is_said_on_import(elsewhere, monkeypatch):
+    pytest.importorskip("torch")
+    from dense_gemm_sgemm_gb300 import routed
+
+    monkeypatch.setenv("CXX", "false")
+    build.build()
+    with pytest.raises(ImportError, match="compiling the binding failed"):
+        routed._load_binding()
