@@ -30,6 +30,7 @@ LIB_NAME = "libgemm_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 BINDING_PATH = os.path.join(OUT_DIR, "_routed.so")
 BINDING_SRC = os.path.join(CSRC, "routed_binding.cpp")
+BINDING_FOR = os.path.join(OUT_DIR, "_routed.for")      # the torch that the binding was compiled against
 BINDING_ERROR = os.path.join(OUT_DIR, "_routed.error")  # why there is none
 HEADER = os.path.join(ROOT, "include", "gemm_gb300.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -69,17 +70,44 @@ def _write(path, text):
     os.replace(tmp, path)
 
 
+def torch_abi() -> str:
+    """What a compiled binding depends on: torch's version and C++ ABI, and Python's."""
+    try:
+        import torch
+
+        return f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, " + str(
+            sysconfig.get_config_var("SOABI"))
+    except (ImportError, OSError) as e:  # none, or one whose own libraries do not load
+        return f"no torch: {e}"
+
+
+def note_torch() -> None:
+    _write(BINDING_FOR, torch_abi())
+
+
+def built_for() -> str:
+    """torch_abi() of the build that made the binding."""
+    return _read(BINDING_FOR)
+
+
 def binding_current() -> bool:
-    return _newer(BINDING_PATH, [BINDING_SRC, HEADER, os.path.abspath(__file__)])
+    """Whether the binding on disk is of these sources and of the installed torch."""
+    return _newer(BINDING_PATH, [BINDING_SRC, HEADER, os.path.abspath(__file__)]) and built_for() == torch_abi()
 
 
 def binding_error() -> str:
     """Why the last build made no binding; empty if it did."""
-    return _read(BINDING_ERROR)
+    return _read(BINDING_ERROR).partition("\n")[2]
+
+
+def _binding_settled() -> bool:
+    # a failure is tried again when the sources or torch have changed
+    failed = _newer(BINDING_ERROR, [BINDING_SRC, HEADER, os.path.abspath(__file__)])
+    return binding_current() or (failed and _read(BINDING_ERROR).startswith(torch_abi() + "\n"))
 
 
 def up_to_date() -> bool:
-    return _newer(LIB_PATH, _deps()) and binding_current()
+    return _newer(LIB_PATH, _deps()) and _binding_settled()
 
 
 def _compile(nvcc, src, obj, ptxas_verbose):
@@ -117,6 +145,7 @@ def _link_binding(obj):
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    note_torch()
 
 
 def _finish_binding(compiled, obj):
@@ -129,7 +158,7 @@ def _finish_binding(compiled, obj):
     except (ImportError, OSError, RuntimeError) as e:
         if os.path.exists(BINDING_PATH):
             os.remove(BINDING_PATH)
-        _write(BINDING_ERROR, str(e))
+        _write(BINDING_ERROR, f"{torch_abi()}\n{e}")
         print(f"the routed products' Python binding was not built: {e}", file=sys.stderr)
     else:
         if os.path.exists(BINDING_ERROR):
@@ -144,7 +173,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
     os.makedirs(OUT_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         binding, compiled = os.path.join(OUT_DIR, "routed_binding.o"), None
-        if anew or not binding_current():
+        if anew or not _binding_settled():
             compiled = ex.submit(_compile_binding, nvcc, binding)
         if anew or not _newer(LIB_PATH, _deps()):
             _build_library(ex, nvcc, ptxas_verbose, quiet)

@@ -36,6 +36,9 @@ def _load_binding():
         reason = build.binding_error()
         raise ImportError(f"{build.BINDING_PATH} is missing: build it with `python -m dense_gemm_sgemm_gb300.build`"
                           + (f" (the last build made none: {reason})" if reason else ""))
+    if build.built_for() != build.torch_abi():
+        raise ImportError(f"{build.BINDING_PATH} was built for [{build.built_for() or 'an unknown torch'}], this is "
+                          f"[{build.torch_abi()}]: build it again with `python -m dense_gemm_sgemm_gb300.build`")
     spec = importlib.util.spec_from_file_location("_routed", build.BINDING_PATH)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

@@ -64,3 +64,44 @@ def test_why_there_is_no_binding_is_said_on_import(elsewhere, monkeypatch):
     build.build()
     with pytest.raises(ImportError, match="compiling the binding failed"):
         routed._load_binding()
+
+
+def test_another_torch_makes_the_binding_stale(elsewhere, monkeypatch):
+    torch = pytest.importorskip("torch")
+    from dense_gemm_sgemm_gb300 import routed
+
+    built = []
+
+    def compile_binding(nvcc, obj):
+        built.append(torch.__version__)
+        return build.BINDING_SRC, 0, ""
+
+    def link_binding(obj):
+        open(build.BINDING_PATH, "w").close()
+        build.note_torch()
+
+    monkeypatch.setattr(build, "_compile_binding", compile_binding)
+    monkeypatch.setattr(build, "_link_binding", link_binding)
+    build.build()
+    assert build.up_to_date()
+    build.build()
+    assert len(built) == 1
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert not build.up_to_date()
+    with pytest.raises(ImportError, match="99.0"):  # not loaded either
+        routed._load_binding()
+    build.build()
+    assert built[1:] == ["99.0"] and build.up_to_date()
+
+
+def test_a_failed_binding_is_tried_again_when_torch_changes(elsewhere, monkeypatch):
+    torch = pytest.importorskip("torch")
+    tried = []
+    monkeypatch.setattr(build, "_compile_binding", lambda nvcc, obj: (build.BINDING_SRC, 1, tried.append(1) or "no"))
+    build.build()
+    build.build()
+    assert len(tried) == 1 and build.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert not build.up_to_date()
+    build.build()
+    assert len(tried) == 2
