@@ -37,11 +37,11 @@ _ROUTED = (
     "moe_combine_backward", "gated_silu_backward", "grouped_linear", "grouped_weight_grad",
     "lora_linear",
 )
-__all__ += _ROUTED
 
 
 def __getattr__(name):
-    # routed.py needs torch at import; this package does not until a call is made
+    # routed.py needs torch at import; this package does not until a call is made, so a star import leaves
+    # these names out (`from dense_gemm_sgemm_gb300.routed import *` has them)
     if name in _ROUTED:
         from . import routed
 

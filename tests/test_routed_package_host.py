@@ -1,6 +1,7 @@
 """The routed products' Python binding and its place in the package and the build, without a GPU."""
 import ctypes
 import os
+import subprocess
 import sys
 
 import pytest
@@ -105,3 +106,29 @@ def test_a_failed_binding_is_tried_again_when_torch_changes(elsewhere, monkeypat
     assert not build.up_to_date()
     build.build()
     assert len(tried) == 2
+
+
+def test_star_import_works_without_torch_and_binding():
+    code = """
+import sys
+sys.modules["torch"] = None
+from dense_gemm_sgemm_gb300 import *
+assert gemm_version() >= 200 and "matmul" in globals()
+import dense_gemm_sgemm_gb300 as g
+try:
+    g.moe_route
+except ImportError:
+    pass
+else:
+    raise SystemExit("routed products without torch")
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=build.ROOT)
+
+
+def test_routed_names_by_attribute_and_by_name():
+    pytest.importorskip("torch")
+    import dense_gemm_sgemm_gb300 as g
+    from dense_gemm_sgemm_gb300 import moe_route, routed
+
+    assert g.moe_route is moe_route is routed.moe_route
+    assert all(getattr(g, name) is getattr(routed, name) for name in routed.__all__)
