@@ -43,7 +43,8 @@ const at::Tensor &tensor(Device &device, PyObject *o, const char *what)
     return t;
 }
 
-// A matrix with unit column stride; the stride of a single row means nothing.
+// A matrix with unit column stride.  The stride of a single row means nothing: any whole number of 16-byte
+// pieces that holds the row, so that a row of odd length is not refused for it.
 struct Matrix {
     const at::Tensor &t;
     int64_t rows, cols, ld;
@@ -56,7 +57,7 @@ Matrix matrix(Device &device, PyObject *o, const char *what, int dims = 2)
                       "-D with unit column stride wanted");
     const int64_t rows = t.size(-2), cols = t.size(-1);
     int64_t ld = t.stride(-2);
-    if (rows <= 1) ld = std::max({ld, cols, int64_t(1)});
+    if (rows <= 1) ld = std::max((cols + 7) & ~int64_t(7), int64_t(8));
     return Matrix{t, rows, cols, ld};
 }
 
