@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(32 * plan_warps<V>) plan_kernel(const RouteArg
 
 // Gradient of the weights w_j = scale * s_j (/ S, the sum of the chosen scores, when renormalised) for
 // one token a warp: ds_j = scale * dw_j, or scale * (dw_j - sum_i dw_i s_i / S) / S; then
-// dx_e = s_e (ds_e - sum ds s) for softmax, ds_e s_e (1 - s_e) for sigmoid.  Lane j takes choice j and
+// dx_e = s_e (ds_e - sum ds s) for softmax, ds_e s_e (1 - s_e) for sigmoid.  When renormalised the factors
+// s_e and 1 / S enter as the ordinary s_e / S, since 1 / S overflows where all of the chosen scores are tiny
+// (a bias chooses such experts), and sum ds s is 0 by its definition.  Lane j takes choice j and
 // puts its gradient by expert into shared memory, so that every lane stores its own experts in wide
 // pieces.  Bound by the launch and the latency of one row: 8191 tokens of 128 experts, top 6, 5.0 us.
 template <int V>
@@ -426,7 +428,7 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
     for (int v = 0; v < V; ++v)
         if (lane * V + v < E) row[lane * V + v] = s[v];
     __syncwarp();
-    // lane j holds choice j: its expert, score and gradient
+    // lane j holds choice j: its expert, score and gradient (renormalised: with the factor s)
     int id = -1;
     float dw = 0.0f, sel = 0.0f;
     if (lane < k) {
@@ -442,7 +444,7 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
         const float S = warp_sum(sel);
         const float p = S > 0.0f ? sel / S : 0.0f;
         const float mean = warp_sum(dw * p);
-        g = S > 0.0f ? a.scale * (dw - mean) / S : 0.0f;
+        g = a.scale * (dw - mean) * p;  // times s already
     }
     __syncwarp();
 #pragma unroll
@@ -463,7 +465,7 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
     __syncwarp();
 #pragma unroll
     for (int v = 0; v < V; ++v) ds[v] = lane * V + v < E ? row[lane * V + v] : 0.0f;
-    float mean = 0.0f;  // sum of ds * s; 0 by its definition when the weights are renormalised
+    float mean = 0.0f;  // sum of ds * s
     if (a.score == GEMM_SCORE_SOFTMAX && !a.renormalise) {
 #pragma unroll
         for (int v = 0; v < V; ++v) mean += ds[v] * s[v];
@@ -473,7 +475,8 @@ route_backward_kernel(const RouteArgs a, const float *dweights, const int32_t *i
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         // a masked logit has score 0 and so gradient 0
-        d[v] = a.score == GEMM_SCORE_SOFTMAX ? s[v] * (ds[v] - mean) : ds[v] * s[v] * (1.0f - s[v]);
+        if (a.score == GEMM_SCORE_SOFTMAX) d[v] = a.renormalise ? ds[v] : s[v] * (ds[v] - mean);
+        else d[v] = (a.renormalise ? ds[v] : ds[v] * s[v]) * (1.0f - s[v]);
         if (!(x[v] > -INFINITY)) d[v] = 0.0f;
     }
     if (a.type == GEMM_TYPE_F32) store_lane<float, V>(static_cast<float *>(dlogits) + t * ldd, E, lane, wide, d);
