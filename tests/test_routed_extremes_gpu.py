@@ -57,3 +57,53 @@ def test_one_row_has_no_stride():
     dw = g.grouped_weight_grad(dy.cuda(), x.cuda(), torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
     outer = dy.double().T @ x.double()
     ref.assert_within(dw[0], outer, ref.sum_bound(1) * outer.abs())
+
+
+@pytest.mark.parametrize("T,requests", [(60, 60), (4096, 5), (700, 90)])
+def test_layer_with_adapters_right_behind_what_writes_its_inputs(T, requests):
+    # the projection starts before the inner products' kernel has ended, which itself starts while the
+    # kernel ahead still runs: that one writes x, the segments or the adapters, many megabytes late
+    gen = torch.Generator().manual_seed(T)
+    H, k, n, R = 1024, 8, 6, 16
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=gen) * std).half().cuda()  # noqa: E731
+    w, a, b = rnd(264, H, std=H ** -0.5), rnd(n, R, H, std=H ** -0.5), rnd(n, 264, R, std=R ** -0.5)
+    big = 8192
+    rows = [torch.randn(big * k, H, generator=gen).half().cuda() for _ in range(2)]
+    where = torch.randperm(big * k, generator=gen).int().reshape(big, k).cuda()
+    cuts = [torch.cat([torch.tensor([0]), torch.sort(torch.randint(0, T + 1, (requests - 1,), generator=gen)).values,
+                       torch.tensor([T])]).int().cuda() for _ in range(2)]
+    who = [torch.randint(-1, n, (requests,), generator=gen).int().cuda() for _ in range(2)]
+
+    def call(i, late):
+        # `late`: the operand whose writer is the last kernel ahead
+        x = torch.empty(0)
+        segments, adapters = torch.zeros_like(cuts[0]), torch.zeros_like(who[0])
+        if late != "x":
+            x = g.moe_combine(rows[i], where)[-T:]
+        segments.copy_(cuts[i])
+        adapters.copy_(who[i])
+        if late == "x":
+            x = g.moe_combine(rows[i], where)[-T:]
+        else:
+            # a long kernel, then the operand itself
+            junk = torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(i)
+            if late == "segments":
+                segments.zero_()
+                segments.add_(cuts[i] + 0 * junk[:1].int())
+            else:
+                adapters.fill_(-1)
+                adapters.copy_(who[i] + 0 * junk[:1].int())
+        return g.lora_linear(x, w, a, b, segments, adapters)
+
+    want = []
+    for i in range(2):
+        x = g.moe_combine(rows[i], where)[-T:].clone()
+        torch.cuda.synchronize()
+        want.append(g.lora_linear(x, w, a, b, cuts[i], who[i]))
+        torch.cuda.synchronize()
+    for late in ("x", "segments", "adapters"):
+        for i in (0, 1, 0, 1):
+            y = call(i, late)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[i])
+    assert g.gemm_get_device_status() == 0
