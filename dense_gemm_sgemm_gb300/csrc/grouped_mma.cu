@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     // a linear layer with adapters follows their inner products' kernel, which waited itself: only those
     // are waited for, below
-    if (a.ad.b == nullptr) chain_wait();
+    const bool adapted = !GATED && a.ad.b != nullptr;
+    if (!adapted) chain_wait();
     else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int group, first, rows;
     if (!nonempty_group(a, blockIdx.y, lane, group, first, rows)) return;
@@ -234,13 +235,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
         __syncthreads();  // the partial tiles of the previous tokens have been read
         put_partial<2, NT>(parts + warp * kTokens * kStride, acc, lane);
         // adapters: their inner products come from the kernel before this one
-        if (a.ad.b != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (adapted) asm volatile("griddepcontrol.wait;" ::: "memory");
         __syncthreads();
         for (int i0 = threadIdx.x; i0 < block_feat * kTokens; i0 += NT * kThreads) {
             float low[NT];  // the adapters' part of the thread's next NT outputs
 #pragma unroll
             for (int q = 0; q < NT; ++q) low[q] = 0.0f;
-            if (a.ad.b != nullptr) {
+            if (adapted) {
                 add_adapters<T, NT>(a, low, [&](int q, int64_t &p, int64_t &feat) {
                     const int i = i0 + q * kThreads, n = i / block_feat;
                     p = first + n0 + n;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
         }
     }
     // a CTA without tokens of its own still orders this launch behind the one before it
-    if (a.ad.b != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (adapted) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // x = part 0 + part 1 + .. up to the last part's rounding.

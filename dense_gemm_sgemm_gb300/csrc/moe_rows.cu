@@ -163,11 +163,9 @@ combine_backward_kernel(int64_t slots, int64_t cols, int k, const X *x, int64_t 
             put<X, VEC>(dst + c * VEC, v);
         }
     }
-    if (dweights != nullptr) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) dweights[s] = dot;
-    }
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) dweights[s] = dot;
 }
 
 // Warp: one position.  out[p] = x[rows[p]], zeros where the row is outside x, for the positions of a
