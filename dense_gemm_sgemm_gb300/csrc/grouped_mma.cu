@@ -215,13 +215,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
     const int64_t kb = chunks * part / ks * 32;
     int64_t ke = chunks * (part + 1) / ks * 32;
     if (ke > a.K) ke = a.K;
-    for (int n0 = int(blockIdx.z) * kTokens; n0 < rows; n0 += int(gridDim.z) * kTokens) {
+    // unsigned: the last step may lead past 2^31
+    for (unsigned n0 = blockIdx.z * kTokens; n0 < unsigned(rows); n0 += gridDim.z * kTokens) {
         const T *x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int i = n0 + 8 * n + g;
+            const unsigned i = n0 + 8 * n + g;
             int64_t r = -1;
-            if (i < rows) r = a.rows != nullptr ? __ldg(a.rows + first + i) : first + i;
+            if (i < unsigned(rows)) r = a.rows != nullptr ? __ldg(a.rows + first + i) : int64_t(first) + i;
             x[n] = r >= 0 && r < a.x_rows ? static_cast<const T *>(a.X) + r * a.ldx : nullptr;
         }
         float acc[2][NT][4];
@@ -244,17 +245,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
             if (adapted) {
                 add_adapters<T, NT>(a, low, [&](int q, int64_t &p, int64_t &feat) {
                     const int i = i0 + q * kThreads, n = i / block_feat;
-                    p = first + n0 + n;
+                    p = int64_t(first) + n0 + n;
                     feat = int64_t(blockIdx.x) * block_feat + i % block_feat;
-                    return n < kTokens && n0 + n < rows && feat < a.N;
+                    return n < kTokens && n0 + n < unsigned(rows) && feat < a.N;
                 });
             }
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
                 const int i = i0 + q * kThreads, f = i % block_feat, n = i / block_feat;
                 const int64_t feat = int64_t(blockIdx.x) * block_feat + f;
-                if (n >= kTokens || n0 + n >= rows || feat >= a.N) continue;
-                const int64_t p = first + n0 + n;
+                if (n >= kTokens || n0 + n >= unsigned(rows) || feat >= a.N) continue;
+                const int64_t p = int64_t(first) + n0 + n;
                 const float *src = parts + ((f / kFeat) * ks * kTokens + n) * kStride + f % kFeat;
                 float v = 0.0f, u = 0.0f;
                 for (int c = 0; c < ks; ++c) {

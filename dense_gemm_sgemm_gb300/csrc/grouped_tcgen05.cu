@@ -341,6 +341,9 @@ struct LinearParams {
     int inject_stall;  // test hook: the producer never fills its first slice
 };
 
+// n / d rounded up, for n up to 2^31 - 1.
+__device__ __forceinline__ int parts_of(int n, int d) { return int((unsigned(n) + unsigned(d) - 1u) / unsigned(d)); }
+
 // A unit: one feature tile of one tile of a group's tokens, over K slices [kb0, kb1).
 struct LinearUnit {
     int group, feature_tile, first, tokens, width, split, kb0, kb1;
@@ -349,8 +352,8 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearParams &p, const S
 {
     while (u >= sh.start[group + 1]) ++group;
     const int rows = sh.first[group + 1] - sh.first[group];
-    const int tiles = (rows + p.cap - 1) / p.cap;
-    const int width = ((rows + tiles - 1) / tiles + 31) & ~31;  // even tiles; at most cap, none is empty
+    const int tiles = parts_of(rows, p.cap);
+    const int width = (parts_of(rows, tiles) + 31) & ~31;  // even tiles; at most cap, none is empty
     int r = u - sh.start[group];
     LinearUnit x;
     x.split = r % p.splits;
@@ -657,7 +660,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const uint32_t rank = cluster_ctarank();
     const int cap = p.cap, ftiles = p.ftiles * p.splits;
     const uint32_t tmem = set_up<EPI != kAdapted>(sh, p.offsets, p.groups, p.y_rows,
-                                 [=](int rows) { return (rows + cap - 1) / cap * ftiles; });
+                                 [=](int rows) { return parts_of(rows, cap) * ftiles; });
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
     const int units = sh.start[p.groups], unit0 = int(cluster_id_x()), step = int(cluster_count_x());
     constexpr int kFeatures = EPI == kGated ? 128 : 256;  // of a unit
@@ -741,13 +744,13 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 const LinearUnit x = linear_unit(p, sh, u, group);
                 RequestsOf<EPI> requests(p, x, lane, careful);
                 const int half = x.width / 2;                     // tokens this CTA loads
-                const int row0 = x.first + int(rank) * half, end = x.first + x.tokens;
+                const unsigned row0 = unsigned(x.first) + rank * half, end = x.first + x.tokens;  // row0: past 2^31 too
                 int4 from = make_int4(0, 0, 0, 0);
                 if (p.rows != nullptr && 4 * lane < half) {       // a row outside x is read as zeros
                     int r[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int q = row0 + 4 * lane + i;
+                        const unsigned q = row0 + 4 * lane + i;
                         r[i] = q < end ? __ldg(p.rows + q) : -1;
                         if (r[i] < 0 || r[i] >= p.x_rows) r[i] = int(p.x_rows);
                     }
@@ -763,7 +766,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     if (p.rows != nullptr) {
                         if (4 * lane < half) tma_gather4_pair(b + 512u * lane, &map_x.rows[0], full, kb * 64, from);
                     } else if (leader) {
-                        load_rows(b, map_x, full, kb * 64, row0, half);
+                        load_rows(b, map_x, full, kb * 64, int(row0), half);
                     }
                     __syncwarp();
                     ring.next();
@@ -1054,7 +1057,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
         for (int u = unit0; ok && u < units; u += step) {
             const GradUnit x = grad_unit(p, sh, u);
             const int c0 = (of_x ? x.tk : x.tn) * 256 + int(rank) * 128;
-            for (int i = 0; i * 64 < x.rows; ++i) {
+            for (int i = 0; i < parts_of(x.rows, 64); ++i) {
                 const int s = slice_start(x.rows, i);
                 ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                 if (__any_sync(kFull, !ok)) {
@@ -1096,7 +1099,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem + uint32_t(acc * kAccCols);
-                for (int i = 0; i * 64 < x.rows; ++i) {
+                for (int i = 0; i < parts_of(x.rows, 64); ++i) {
                     const int s = slice_start(x.rows, i);
                     ok = watch.wait(sh.full(ring.stage), ring.phase);
                     if (!ok) break;
@@ -1104,7 +1107,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
                     if (leader) {
                         const uint64_t a = a0 + uint32_t(ring.stage * (kStageA >> 4));
                         const uint64_t b = b0 + uint32_t(ring.stage * (kMaxStageB >> 4));
-                        const int steps = min(4, (x.rows - s + 15) / 16);  // 16 positions an MMA
+                        const int steps = min(4, parts_of(x.rows - s, 16));  // 16 positions an MMA
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (k < steps)
@@ -1131,7 +1134,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
         bool ok = true;
         for (int u = unit0; ok && u < units; u += step) {
             const GradUnit x = grad_unit(p, sh, u);
-            for (int i = 0; i * 64 < x.rows; ++i) {
+            for (int i = 0; i < parts_of(x.rows, 64); ++i) {
                 const int left = x.rows - slice_start(x.rows, i);
                 if (left < 64) {
                     bool got = true;
