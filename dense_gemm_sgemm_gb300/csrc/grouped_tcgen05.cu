@@ -18,11 +18,12 @@
 // of its requests' low-rank products, B_a on the m side and the inner products on the n side, over the
 // columns of the request only (see TileRequests); the kernel ahead computes the inner products in
 // 16-bit parts that sum to them (launch_shrink).  On the CUDA cores of the epilogue this product was
-// bound by broadcasting the inner products from shared memory (8192 tokens, rank 64, 4096 x 4096:
-// 341 us), with mma.sync there by tcgen05, which goes first (371 us).  An infinity or NaN in an adapter's
-// B would spoil the columns of its neighbours, where it meets zeros: the epilogue notes the tiles whose
-// sums are not finite, and the pair computes those a second time with such adapters' products in fp32
-// on the CUDA cores, as well as those whose inner products the 16-bit parts cannot hold (TileRequests).
+// bound by broadcasting the inner products from shared memory (8192 tokens, rank 64, 4096 x 4096, whole
+// calls: 369 us, as slices 226 at first), with mma.sync there by tcgen05, which goes first (371 us).  An
+// infinity or NaN in an adapter's B would spoil the columns of its neighbours, where it meets zeros: the
+// epilogue notes the tiles whose sums are not finite, and the pair computes those a second time with such
+// adapters' products in fp32 on the CUDA cores, as well as those whose inner products the 16-bit parts
+// cannot hold (TileRequests).
 //
 // Weight gradient.  dW_g[n][k] sums over the group's positions, the K dimension of this product,
 // both operands "transposed" (MN-major).  Slices are 64 positions; the last one of a group also holds
@@ -596,7 +597,8 @@ template <int EPI> using RequestsOf = typename std::conditional<EPI == kAdapted,
 
 // Adds the products of the requests that a tile's second computation leaves out to `sums`, 32 tokens from
 // `first` of the lane's feature f + lane as [token][lane]: fp32 values and sums, as the few-rows kernel's.
-__device__ __noinline__ void add_late(const LinearParams &p, const LinearUnit x, float *sums, int first, int tokens, int64_t f, int lane)
+__device__ __noinline__ void add_late(const LinearParams &p, const LinearUnit x, float *sums, int first, int tokens, int64_t f,
+                                      int lane)
 {
     TileRequests requests(p, x, lane, true);
     int adapter, t0, t1;
@@ -645,9 +647,13 @@ __device__ __forceinline__ uint64_t tiles_again(const Shared &sh)
 // W_MN: W stored K x N (features contiguous).
 //
 // Bound by the tensor pipe (75% active) and the power limit where groups are large: 32 groups of 512 rows,
-// N = K = 2048, bf16, 88.5 us (1552 TFLOP/s, 0.81 of the measured burst peak), the last wave of tiles
-// being 4% of it.  Gated 112 us (1224 TFLOP/s): a tile's epilogue takes about as long as its 32 slices.
-// 8192 tokens with adapters of rank 64, 4096 x 4096: 154 us (1785 TFLOP/s of the projection alone).
+// N = K = 2048, bf16, 87.6 us (1569 TFLOP/s, 0.81 of the measured burst peak), the last wave of tiles
+// being 4% of it.  Gated, 1024 outputs of 2048 weight rows, 89.9 us (1529 TFLOP/s, 72% active).  8192 tokens
+// with adapters of rank 64, 4096 x 4096: 157 us (1750 TFLOP/s of the projection alone).
+//
+// Every output is rounded once, from fp32.  Y in 16 bits between an expert's two products is a choice for
+// the second one's tensor cores, which read 16-bit rows: the error of the layer's output is 1.41 times that
+// of its own rounding.  An fp32 Y is to be had where no product reads it.
 template <int W_MN, int EPI, bool Y_F32>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TokenMaps map_x,
@@ -1019,7 +1025,7 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, const Shared 
 
 // First position, within the group, of a unit's i-th slice: the ragged one, if there is one, comes first,
 // so that part of its way through the cleaners passes while the slices of the unit before it are
-// multiplied (32 groups of 1023 rows, 2048 x 1024: 100 us, with it last 103; of 1024 rows 90 us).
+// multiplied (32 groups of 1023 rows, 2048 x 1024: 94 us, 3% more with it last; of 1024 rows 82 us).
 __device__ __forceinline__ int slice_start(int rows, int i)
 {
     return (rows & 63) == 0 ? i * 64 : i == 0 ? rows & ~63 : (i - 1) * 64;
@@ -1030,8 +1036,8 @@ __device__ __forceinline__ int slice_start(int rows, int i)
 // one on each CTA's own ragged barrier, from which the cleaners pass it on: the second CTA's to the
 // first's (cleaned), the first's to the full barrier.
 //
-// Bound by the tensor pipe (69% active) and the stores of dW: 32 groups of 512 positions, 2048 x 2048, 16-bit
-// dW, 92.9 us (1479 TFLOP/s, each input read once).
+// Bound by the tensor pipe (71% active) and the stores of dW: 32 groups of 512 positions, 2048 x 2048, 16-bit
+// dW, 89.7 us (1533 TFLOP/s, each input read once).
 template <bool DW_F32>
 __global__ void __launch_bounds__(kGradThreads, 1)
 grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,

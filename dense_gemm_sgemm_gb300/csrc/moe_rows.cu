@@ -39,7 +39,7 @@ __device__ __forceinline__ void place(int64_t cols, int64_t &row, int64_t &piece
 }
 
 // Thread: VEC columns of one token; the k rows of a token are read by the same threads.  8192 tokens of
-// 4 rows x 2048 to bf16: 49 us from fp32 rows (6.2 TB/s), 34 from bf16 rows (5.0).
+// 4 rows x 2048 to bf16: 50 us from fp32 rows (6.1 TB/s), 34 from bf16 rows (5.0).
 template <class R, class Y, int VEC>
 __global__ void __launch_bounds__(kThreads)
 combine_kernel(int64_t T, int64_t cols, int k, const R *rows, int64_t ldr, int64_t positions, const int32_t *where,
@@ -132,7 +132,9 @@ dispatch_kernel(int64_t T, int64_t cols, int k, const X *x, int64_t ldx, int64_t
 }
 
 // Warp: one slot, since the dot product of x[token] and rows[where] runs over the row;
-// out[where] = w * x[token] beside it.  8192 tokens of 4 bf16 rows x 2048: 47 us (6.4 TB/s).
+// out[where] = w * x[token] beside it, rounded to x's type, since the two products that read it take 16-bit
+// rows (their gradients' error grows as the layer's does).  8192 tokens of 4 bf16 rows x 2048: 47 us (6.4
+// TB/s), of fp32 rows 68 (6.4).
 template <class X, class R, int VEC>
 __global__ void __launch_bounds__(kThreads)
 combine_backward_kernel(int64_t slots, int64_t cols, int k, const X *x, int64_t ldx, const R *rows, int64_t ldr,
@@ -192,7 +194,7 @@ gather_kernel(const int32_t *offsets, int groups, int64_t positions, const uint1
 }
 
 // Thread: VEC columns of a position: with s = 1 / (1 + e^-gate), dgate = dh up s (1 + gate (1 - s)) and
-// dup = dh gate s.  32768 rows of 2 x 1024, bf16: 52 us (6.4 TB/s).
+// dup = dh gate s.  32768 rows of 2 x 1024, bf16: 57 us (5.9 TB/s).
 template <class X, class D, int VEC>
 __global__ void __launch_bounds__(kThreads)
 gated_silu_backward_kernel(int64_t rows, int64_t cols, int64_t I, const X *pre, int64_t ldp, const D *dh, int64_t lddh,

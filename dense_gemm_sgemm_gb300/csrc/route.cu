@@ -7,16 +7,16 @@
 // that is out), so one pick is one integer warp maximum and a ballot, whose lowest lane holds the
 // lowest index.  Runs of experts that are whole lanes, a power of two of them, are reduced by
 // shuffles, others through shared memory.  Bound by instructions: 16384 tokens of 256 experts, sigmoid,
-// bias, 8 in 4 of 8 runs, take 25 us at 72% of the issue slots, 1370 instructions a token, a third of
-// them in the eight picks.
+// bias, 8 in 4 of 8 runs, take 21 us (25 alone and from cold caches) at 72% of the issue slots, 1370
+// instructions a token, a third of them in the eight picks.
 //
 // The plan is a stable counting sort of the slots by expert in one launch: one cluster of CTAs, every
 // warp owning a contiguous run of slots and a histogram row of its own in shared memory.  Pass 1
 // counts (match.any gives the lanes of a warp that hold the same expert) and keeps each slot's rank
 // in its warp; the histograms are scanned over warps, CTAs (through distributed shared
 // memory) and experts; pass 2 adds them.  No atomics, so the order never varies.  Bound by latency on
-// 16 SMs: 131072 slots of 256 experts take 21 us.  With few tokens the same launch routes them first
-// (the warp's slots are then its own tokens').
+// 16 SMs: 131072 slots of 256 experts take 17.4 us (21 alone and from cold caches).  With few tokens the
+// same launch routes them first (the warp's slots are then its own tokens').
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -522,7 +522,8 @@ static bool wide_rows(int type, const void *p, int64_t ld)
 }
 
 // Few tokens: one launch routes and plans (the routing then runs on the plan's 8 CTAs only, so
-// only up to kFusedTokens tokens, and E <= 256 so that two E-sized shared rows per warp fit).
+// only up to kFusedTokens tokens, and for E <= 256: more experts would fit its shared memory, but want two
+// more instances of the kernel for calls that have not been measured).
 constexpr int64_t kFusedTokens = 512;
 
 cudaError_t launch_plan(int64_t T, int E, int top_k, const int32_t *ids, int32_t *offsets, int32_t *tokens,

@@ -6,7 +6,11 @@ functions check types and shapes, create the outputs that are not given, pass ad
 and the current CUDA stream to the library (in the compiled binding csrc/routed_binding.cpp), and
 raise TypeError or ValueError on a bad argument, GemmError on a non-OK status.  Matrices need
 unit column stride and may have padded rows; index and weight tensors are contiguous int32 and
-fp32.  An expert layer of T tokens, E experts and k experts per token:
+fp32; all tensors of a call live on one device.  grouped_linear, grouped_weight_grad and lora_linear read
+rows in 16-byte pieces: base addresses of 16 bytes and row strides of a multiple of 8 elements (a single
+row aside), so a contiguous matrix whose rows are not a multiple of 8 long, a weight too, is padded by the
+caller; what these functions return is.  Output rows of positions in no group are left as they were
+allocated.  An expert layer of T tokens, E experts and k experts per token:
 
     ids, weights, offsets, tokens, where = moe_route(logits, k)      # logits T x E
     h  = grouped_linear(x, w13, offsets, rows=tokens, gated=True)    # w13 E x 2I x H, x T x H
