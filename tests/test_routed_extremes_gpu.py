@@ -107,3 +107,42 @@ def test_layer_with_adapters_right_behind_what_writes_its_inputs(T, requests):
             torch.cuda.synchronize()
             assert torch.equal(y, want[i])
     assert g.gemm_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(5, 8, 2, 256, 128), (700, 16, 4, 512, 256), (4000, 24, 3, 1000, 264)])
+def test_chained_calls_read_what_the_call_before_wrote(T, E, k, H, I):
+    # each kernel may be on the SMs before the one ahead has ended; two inputs in turn go through the same
+    # memory, so that anything read too early is the other input's
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    w13, w2, wl = rnd(E, 2 * I, H), rnd(E, H, I), rnd(H, H)
+    a, b = rnd(6, 8, H), rnd(6, H, 8)
+    xs = [rnd(T, H) for _ in range(2)]
+    logits = [torch.randn(T, E, generator=gen, device="cuda") for _ in range(2)]
+    segments = torch.tensor([0, T // 3, T // 2, T], dtype=torch.int32, device="cuda")
+    who = torch.tensor([2, -1, 5], dtype=torch.int32, device="cuda")
+
+    def layer(i):
+        ids, wt, off, tokens, where = g.moe_route(logits[i], k)
+        pre = torch.empty(T * k, 2 * I, dtype=torch.bfloat16, device="cuda")
+        h = g.grouped_linear(xs[i], w13, off, rows=tokens, gated=True, pre=pre)
+        ys = g.grouped_linear(h, w2, off, out_dtype=torch.float32)
+        y = g.moe_combine(ys, where, wt, out_dtype=torch.bfloat16)
+        z = g.lora_linear(y, wl, a, b, segments, who)
+        drows, dwt = g.moe_combine_backward(z, ys, where, wt)
+        dw2 = g.grouped_weight_grad(drows, h, off)
+        dpre = g.gated_silu_backward(pre, g.grouped_linear(drows, w2, off, opW="N"))
+        dw13 = g.grouped_weight_grad(dpre, g.moe_dispatch(xs[i], where), off)
+        return z, dwt, dw2, dw13, g.moe_route_backward(dwt, logits[i], ids)
+
+    want = []
+    for i in range(2):
+        want.append([t.clone() for t in layer(i)])
+        torch.cuda.synchronize()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for n in range(12):
+        out = layer(n & 1)
+        for got, ref_ in zip(out, want[n & 1]):
+            wrong += (got != ref_).sum()
+        del out
+    assert int(wrong) == 0
