@@ -6,8 +6,8 @@ elementary torch operations in fp32 (``own`` false) or through the library's ent
 ``exact`` computes it in fp64.
 
 A block of 128 values along an axis, or of 128 x 128, shares one fp32 scale: the smallest power of two s,
-at least 2^-126, with max|x| <= s * m, m the largest 8-bit value (448 for e4m3, 57344 for e5m2); a value is
-stored as x / s rounded to the nearest 8-bit value, ties to even.
+at least 2^-126, with max|x| <= s * m, m the largest 8-bit value (448 for e4m3, 57344 for e5m2), and 1 for a
+block of zeros; a value is stored as x / s rounded to the nearest 8-bit value, ties to even.
 """
 import math
 
@@ -153,8 +153,10 @@ def _plain_quantize(x, block, eight):
     v = x.new_zeros(nr * b0, nc * b1, dtype=torch.float32)
     v[:r, :c] = x
     v = v.reshape(nr, b0, nc, b1)
-    power = _plain_scales(v.abs().amax(dim=(1, 3))) - (9 if eight == "e4m3" else 16)
-    scales = ((torch.clamp(power, min=-126) + 127) << 23).view(torch.float32)  # 2 ** power
+    amax = v.abs().amax(dim=(1, 3))
+    power = _plain_scales(amax) - (9 if eight == "e4m3" else 16)
+    power = torch.clamp(power, min=-126) * (amax > 0)
+    scales = ((power + 127) << 23).view(torch.float32)  # 2 ** power
     q = (v / scales[:, None, :, None]).to(_EIGHT[eight])
     return q.reshape(nr * b0, nc * b1)[:r, :c], scales
 
@@ -279,7 +281,7 @@ def _exact_values(x, block, eight):
     power = torch.clamp(power, min=-126.0)
     for _ in range(24):
         power = torch.where(amax > _two_to(power) * most, power + 1.0, power)
-    scale = _two_to(power)
+    scale = torch.where(amax > 0, _two_to(power), 1.0)
     full = scale[index]
     y = x / full
     exponent = torch.frexp(y).exponent - 1
