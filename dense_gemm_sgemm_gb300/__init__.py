@@ -16,6 +16,10 @@ Routed products (a router, the experts' products, low-rank adapters; see routed.
 
     moe_route, moe_plan, moe_dispatch, grouped_linear, moe_combine, lora_linear and the
     gradients moe_route_backward, moe_combine_backward, gated_silu_backward, grouped_weight_grad
+
+Block-scaled 8-bit products (see scaled.py):
+
+    quantize_blocks, quantize_both, dequantize_blocks, scaled_matmul
 """
 from __future__ import annotations
 
@@ -32,6 +36,7 @@ __all__ = [
     "gemm_kernel_launches", "gemm_measure_fp32_fma_peak", "gemm_sgemm_configs",
     "library_path", "load", "matmul",
 ]
+_SCALED = ("quantize_blocks", "quantize_both", "dequantize_blocks", "scaled_matmul")
 _ROUTED = (
     "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch", "moe_combine",
     "moe_combine_backward", "gated_silu_backward", "grouped_linear", "grouped_weight_grad",
@@ -40,12 +45,16 @@ _ROUTED = (
 
 
 def __getattr__(name):
-    # routed.py needs torch at import; this package does not until a call is made, so a star import leaves
-    # these names out (`from dense_gemm_sgemm_gb300.routed import *` has them)
+    # routed.py and scaled.py need torch at import; this package does not until a call is made, so a star
+    # import leaves these names out (`from dense_gemm_sgemm_gb300.routed import *` has them)
     if name in _ROUTED:
-        from . import routed
-
-        globals()[name] = getattr(routed, name)
+        from . import routed as module
+    elif name in _SCALED:
+        from . import scaled as module
+    else:
+        module = None
+    if module is not None:
+        globals()[name] = getattr(module, name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

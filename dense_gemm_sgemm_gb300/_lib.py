@@ -67,6 +67,14 @@ SIGNATURES = {
     "gemm_lora_linear": (_int, [_int, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp,
                                 _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
                                 _vp]),
+    "gemm_quantize_blocks": (_int, [_int, _int, _i64, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp, _i64,
+                                    _i64, _vp]),
+    "gemm_quantize_both": (_int, [_int, _int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp,
+                                  _i64, _vp, _i64, _i64, _vp]),
+    "gemm_dequantize_blocks": (_int, [_int, _int, _i64, _i64, _vp, _i64, _int, _int, _vp, _i64, _i64,
+                                      _vp, _i64, _vp]),
+    "gemm_scaled_matmul": (_int, [_int, _int, _int, _int, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp,
+                                  _i64, _i64, _vp, _i64, _int, _vp, _i64, _i64, _vp, _i64, _vp]),
 }
 
 class SgemmConfig(ctypes.Structure):

@@ -5,7 +5,7 @@ arch-specific features need the `a` target), in parallel, and linked into one sh
 library with the static CUDA runtime.  No fast-math: denormals, IEEE division and square
 root stay on, which the strict-FP32 path relies on.
 
-With it goes the Python binding of the routed products, _build/_routed.so, compiled against the
+With it goes the Python binding of the routed and the block-scaled products, _build/_routed.so, compiled against the
 installed torch.  The library does not need it: where the binding cannot be built (no torch, a torch
 without CUDA, no host C++ compiler) the reason is kept beside it and raised when routed.py is imported.
 
@@ -30,6 +30,7 @@ LIB_NAME = "libgemm_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 BINDING_PATH = os.path.join(OUT_DIR, "_routed.so")
 BINDING_SRC = os.path.join(CSRC, "routed_binding.cpp")
+BINDING_PARTS = os.path.join(CSRC, "scaled_binding.h")
 BINDING_FOR = os.path.join(OUT_DIR, "_routed.for")      # the torch that the binding was compiled against
 BINDING_ERROR = os.path.join(OUT_DIR, "_routed.error")  # why there is none
 HEADER = os.path.join(ROOT, "include", "gemm_gb300.h")
@@ -92,7 +93,7 @@ def built_for() -> str:
 
 def binding_current() -> bool:
     """Whether the binding on disk is of these sources and of the installed torch."""
-    return _newer(BINDING_PATH, [BINDING_SRC, HEADER, os.path.abspath(__file__)]) and built_for() == torch_abi()
+    return _newer(BINDING_PATH, [BINDING_SRC, BINDING_PARTS, HEADER, os.path.abspath(__file__)]) and built_for() == torch_abi()
 
 
 def binding_error() -> str:
@@ -102,7 +103,7 @@ def binding_error() -> str:
 
 def _binding_settled() -> bool:
     # a failure is tried again when the sources or torch have changed
-    failed = _newer(BINDING_ERROR, [BINDING_SRC, HEADER, os.path.abspath(__file__)])
+    failed = _newer(BINDING_ERROR, [BINDING_SRC, BINDING_PARTS, HEADER, os.path.abspath(__file__)])
     return binding_current() or (failed and _read(BINDING_ERROR).startswith(torch_abi() + "\n"))
 
 

@@ -41,6 +41,7 @@
 
 #include "routed_internal.h"
 #include "tcgen05_ptx.cuh"
+#include "tcgen05_roles.cuh"
 #include "tensor_map.h"
 
 namespace gemm {
@@ -81,66 +82,12 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// The waits' limit and where they report.
-struct Watch {
-    volatile int *abort_flag;
-    unsigned int *status;
-    uint64_t timeout_ns;
-    __device__ __forceinline__ void raise() const
-    {
-        *abort_flag = 1;
-        atomicOr(status, 1u);
-    }
-    template <bool CLUSTER = false> __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const
-    {
-        if (mbar_wait<CLUSTER>(bar, parity, abort_flag, timeout_ns)) return true;
-        raise();
-        return false;
-    }
-};
-
-// OR of `pred` over the epilogue warps.
-__device__ __forceinline__ bool epilogue_any(bool pred)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"(static_cast<uint32_t>(pred)), "n"(32 * kEpiWarps)
-                 : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ uint16_t to_16(float v, bool bf16)
-{
-    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-}
-
-__device__ __forceinline__ uint32_t pack_16(float lo, float hi, bool bf16)
-{
-    return uint32_t(to_16(lo, bf16)) | uint32_t(to_16(hi, bf16)) << 16;
-}
-
 // The ring: as many stages of kStageA + b_bytes as fit, for the bytes in flight that small tiles are
 // short of (128 groups of 4 rows, 2048 x 2048: 158 us, with five stages 167).
 __host__ __device__ constexpr int ring_stages(int b_bytes)
 {
     return kRingBytes / (kStageA + b_bytes) < kMaxStages ? kRingBytes / (kStageA + b_bytes) : kMaxStages;
 }
-
-// Ring position of a role: stage and the parity its next phase completes.
-struct Ring {
-    int stages, stage = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
-    __device__ __forceinline__ void next()
-    {
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
-    }
-};
 
 // Barriers and the rest of shared memory.
 struct Shared {
@@ -265,33 +212,6 @@ __device__ __forceinline__ void drain_issuer(const Shared &sh)
     mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
 }
 
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
-// Arrives on the barrier at this address in both CTAs of the pair once the MMAs issued so far have
-// completed.
-__device__ __forceinline__ void commit_both(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"(uint16_t(3))
-                 : "memory");
-}
-
-// The warp has its accumulator columns in registers: one arrival on the issuer's barrier, which may be
-// the peer's.  Released at CTA scope only: a release at cluster scope would wait for the warp's global
-// stores (the weight gradient of 32 groups of 64 rows, 2048 x 1024, took 57 us with such an arrival
-// after the stores, 47 with this one before them).
-__device__ __forceinline__ void release_accumulator(uint32_t bar_cluster, int lane)
-{
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-
 // ------------------------------------------------------------------ Y = X op(W)
 constexpr int kTokenWarp = 2 + kEpiWarps;
 constexpr int kThreads = 32 * (kTokenWarp + 1);
@@ -369,47 +289,6 @@ __device__ __forceinline__ LinearUnit linear_unit(const LinearParams &p, const S
     x.width = (x.tokens + 31) & ~31;
     return x;
 }
-
-// The epilogue warps' staging tiles and their TMA stores in flight: fp32 pieces fill a tile, 16-bit
-// pieces take its halves in turn.
-template <bool F32> struct Staging {
-    uint8_t *tile;
-    int lane, half = 0;
-    __device__ __forceinline__ Staging(uint8_t *t, int l) : tile(t), lane(l) {}
-    // The place of the next piece, once the store that last read it has done so.
-    __device__ __forceinline__ uint8_t *next()
-    {
-        if (lane == 0) {
-            if (F32) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        }
-        __syncwarp();
-        half ^= F32 ? 0 : 2048;
-        return tile + half;
-    }
-    // The whole tile, free of stores.
-    __device__ __forceinline__ uint8_t *all() const
-    {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-        return tile;
-    }
-    __device__ __forceinline__ void store(const CUtensorMap *map, const uint8_t *piece, int c0, int c1, int c2) const
-    {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_3d(map, smem_u32(piece), c0, c1, c2);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-    }
-    // Every store has been written; to be called before the CTA ends.
-    __device__ __forceinline__ void finish() const
-    {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        __syncwarp();
-    }
-};
 
 // v (this lane's feature, 32 tokens) as [token][feature].
 template <bool F32> __device__ __forceinline__ void stage_tokens(const float (&v)[32], uint8_t *piece, int lane, bool bf16)
@@ -894,7 +773,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 if (!wanted(n)) continue;
                 const LinearUnit x = linear_unit(p, sh, u, group);
                 const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
-                if (epilogue_any(!got)) {  // the warps give up together
+                if (epilogue_any<kEpiWarps>(!got)) {  // the warps give up together
                     watch.raise();
                     break;
                 }
@@ -1190,7 +1069,7 @@ grouped_grad_kernel(const __grid_constant__ CUtensorMap map_dy, const __grid_con
             const GradUnit x = grad_unit(p, sh, u);
             if (x.rows > 0) {
                 const bool got = mbar_wait(sh.acc_full(acc), acc_phase, sh.abort_flag, p.timeout_ns);
-                if (epilogue_any(!got)) {
+                if (epilogue_any<kEpiWarps>(!got)) {
                     watch.raise();
                     break;
                 }
@@ -1311,66 +1190,6 @@ bool make_map(CUtensorMap *map, const void *ptr, bool bf16, int64_t rows, int64_
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A stack of `count` row-major matrices stored to in boxes of 32 x 32.  False where TMA cannot: a box cut
-// by the right edge is written in whole 16-byte pieces, so the rows must end on one.
-bool make_store_map(CUtensorMap *map, void *ptr, int type, int64_t rows, int64_t cols, int64_t ld, int64_t count, int64_t stride,
-                    bool swizzled)
-{
-    auto fn = tensor_map_encoder();
-    const bool f32 = type == GEMM_TYPE_F32;
-    const int size = f32 ? 4 : 2;
-    if (fn == nullptr || cols * size % 16 != 0 || reinterpret_cast<uintptr_t>(ptr) % 16 != 0) return false;
-    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(count)};
-    const cuuint64_t strides[2] = {cuuint64_t(ld) * size, cuuint64_t(count > 1 ? stride : rows * ld) * size};
-    const cuuint32_t box[3] = {32, 32, 1};
-    const cuuint32_t steps[3] = {1, 1, 1};
-    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              3, ptr, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Two-CTA clusters of `kernel` that can be resident at once; 0 on failure.  `cache`: of this kernel.
-template <class K> int resident_pairs(K *kernel, int threads, int dev, std::atomic<int> (&cache)[64])
-{
-    const int known = cache[dev & 63].load(std::memory_order_acquire);
-    if (known > 0) return known;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    cache[dev & 63].store(n, std::memory_order_release);
-    return n;
-}
-
-// GEMM_GB300_TEST_INJECT_STALL: a producer never fills its first slice, and waits are short.
-void test_hooks(uint64_t &timeout_ns, int &inject_stall)
-{
-    timeout_ns = 2000000000ull;
-    inject_stall = 0;
-    if (const char *e = std::getenv("GEMM_GB300_TEST_INJECT_STALL"); e && e[0] == '1') {
-        inject_stall = 1;
-        timeout_ns = 20000000ull;
-    }
-}
-
 struct Tiling {
     int cap, splits;
 };
@@ -1417,7 +1236,7 @@ cudaError_t launch_linear_t(const DeviceInfo &dev, const GroupedArgs &a, Tiling 
 {
     static std::atomic<int> cache[64];
     auto *kernel = grouped_linear_kernel<W_MN, EPI, Y_F32>;
-    const int pairs = resident_pairs(kernel, kThreads, dev.device, cache);
+    const int pairs = resident_pairs(kernel, kThreads, kSmemBytes, dev.device, cache);
     unsigned int *status = device_status_word(dev.device);
     if (pairs <= 0 || status == nullptr) return cudaErrorInitializationError;
     const bool bf16 = a.type == GEMM_TYPE_BF16;
@@ -1530,7 +1349,7 @@ cudaError_t launch_weight_grad(const DeviceInfo &dev, const WeightGradArgs &a, c
     if (dev.smem_optin < size_t(kSmemBytes)) return cudaErrorInvalidDevice;
     const bool f32 = a.dw_type == GEMM_TYPE_F32;
     auto *kernel = f32 ? grouped_grad_kernel<true> : grouped_grad_kernel<false>;
-    const int pairs = resident_pairs(kernel, kGradThreads, dev.device, cache[f32]);
+    const int pairs = resident_pairs(kernel, kGradThreads, kSmemBytes, dev.device, cache[f32]);
     unsigned int *status = device_status_word(dev.device);
     if (pairs <= 0 || status == nullptr) return cudaErrorInitializationError;
     const bool bf16 = a.type == GEMM_TYPE_BF16;

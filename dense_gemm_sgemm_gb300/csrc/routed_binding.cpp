@@ -1,4 +1,5 @@
-// Python binding of the routed products (argument checks, outputs, the C call; see routed.py).
+// Python binding of the routed products (argument checks, outputs, the C call; see routed.py), and through
+// scaled_binding.h of the block-scaled ones.
 //
 // A decoding step makes several of these calls, each a few microseconds of GPU time.  Checked and
 // marshalled in Python one took 11 to 24 us of a Grace core, so the tensors are read here: about 5 us.
@@ -421,6 +422,8 @@ BOUND(lora_linear, 9)
     return wrap(y.t);
 END_BOUND
 
+#include "scaled_binding.h"
+
 // The comparison alone, of two torch devices: first, other.
 BOUND(same_device, 2)
     for (int i = 0; i < 2; ++i) {
@@ -441,7 +444,8 @@ PyObject *set_error(PyObject *, PyObject *cls)
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(moe_route), ENTRY(moe_route_backward), ENTRY(moe_plan), ENTRY(moe_dispatch), ENTRY(moe_combine),
                          ENTRY(moe_combine_backward), ENTRY(gated_silu_backward), ENTRY(grouped_linear),
-                         ENTRY(grouped_weight_grad), ENTRY(lora_linear), ENTRY(same_device), {"set_error", set_error, METH_O, nullptr},
+                         ENTRY(grouped_weight_grad), ENTRY(lora_linear), ENTRY(quantize_blocks), ENTRY(quantize_both),
+                         ENTRY(dequantize_blocks), ENTRY(scaled_matmul), ENTRY(same_device), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_routed", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,837 @@
+// Products of 8-bit matrices with an fp32 scale for every 128 elements along K, on the tcgen05 tensor
+// cores (semantics: include/gemm_gb300.h):
+//
+//     C[m][n] = sum over K blocks kb of sa(m, kb) * sb(n, kb) * sum over k in kb of A[m][k] * B[n][k]
+//
+// A K block is one slice of the ring: its four MMAs (kind::f8f6f4, K = 32) start a fresh accumulator in
+// tensor memory, and eight warps read it back, scale it and add it to fp32 sums in their registers, while
+// the MMAs of the next block fill another accumulator.  The tensor cores thus sum 128 products, whose terms
+// are exact, and everything longer is summed in fp32 on the CUDA cores with any fp32 scales, not only powers
+// of two.  A lane of tensor memory is one row of A, so sa is one value a thread; sb is one for a whole warp
+// where B's scales are by 128 rows, else (COLS) one a column, passed through shared memory.
+//
+// Two forms.  Pairs: two CTAs on neighbouring SMs, 256 x 256 tiles (cta_group::2), persistent, C stored by
+// TMA.  Tiles: one CTA a tile of 128 x BN, two CTAs an SM, K split over a cluster of up to eight CTAs whose
+// sums meet in distributed shared memory; for problems without enough tiles for the pairs.  With few rows of
+// A (or B) the host swaps the operands: the long side takes the 128 lanes, the short one the BN columns.
+//
+// Every wait is bounded: when one expires the kernel raises the device's error word, stops all roles, waits
+// (bounded) for its own copies and MMAs in flight, frees its TMEM and returns.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cfloat>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+
+#include "scaled_internal.h"
+#include "tcgen05_ptx.cuh"
+#include "tcgen05_roles.cuh"
+#include "tensor_map.h"
+
+namespace gemm {
+namespace {
+
+constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
+// The pair kernel's warps come in fours, so that the adding ones may have more registers than the launch
+// gives each: (4 * 40 + 8 * 232) * 32 = 12 * 32 * 168.
+constexpr int kPairFirst = 4, kPairThreads = 32 * (kPairFirst + kEpiWarps);
+constexpr int kBox = 128 * 128;  // bytes: 128 rows of a K block, or its 128 k of 128 rows
+constexpr unsigned kFull = 0xffffffffu;
+
+struct ScaledParams {
+    int64_t M, N;
+    int num_kb, tiles_m, tiles_n, splits;
+    int a_mn, b_mn;          // operands stored K x M, K x N
+    uint32_t formats;        // their 8-bit types in the instruction descriptor
+    const float *sa, *sb;
+    int64_t sa_mn, sa_k, sb_mn, sb_k;
+    int a_shift, b_shift;    // 7: a scale for 128 rows
+    void *C;
+    int64_t ldc;
+    int c_type, transposed;  // transposed: C is N x M
+    int c_tma;
+    unsigned int *status;
+    uint64_t timeout_ns;
+    int inject_stall;  // test hook: the producer never fills its first slice
+};
+
+// ------------------------------------------------------------------ PTX
+template <bool PAIR>
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                     : "memory");
+}
+
+// 16 or 32 columns of this thread's TMEM lane, on their way: not to be read before tmem_arrived().
+__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+// Waits for the loads started so far; the registers pass through it, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+// ------------------------------------------------------------------ scaling and adding a K block
+// Scales whose products with each other and with a block's sum (2^-32 to 2^39) stay well inside fp32.
+__device__ __forceinline__ bool mild(float s)
+{
+    const float a = fabsf(s);
+    return a == 0.0f || (a >= 0x1p-40f && a <= 0x1p40f);
+}
+// s = m * 2^e, m in [1/2, 1); an infinite or NaN scale is its own m.
+__device__ __forceinline__ float split(float s, int &e)
+{
+    e = 0;
+    return fabsf(s) <= FLT_MAX ? frexpf(s, &e) : s;
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(uint32_t(max(-126, min(127, e)) + 127) << 23); }
+// Two factors whose product is m * 2^e, such that neither they nor v * a, for a block's sum v, leave fp32's
+// normal range before v * a * b does: scales of any size then lose nothing but what the result cannot hold.
+__device__ __forceinline__ void factors(float m, int e, float &a, float &b)
+{
+    a = m * two_to(e / 2);
+    b = two_to(e - e / 2);
+}
+
+__device__ __forceinline__ float2 pair_of(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
+
+// The sums of one thread: row `row` of A, CW columns from `col` of B.
+template <int CW, bool COLS> struct Sums {
+    static constexpr int kChunk = CW == 32 || CW == 64 ? 32 : 16, kMine = (CW + 31) / 32;  // columns a load; a lane's share of sb
+    float2 at[CW / 2];
+    const float *pa, *pb;
+    int64_t step_a, step_b;
+    float sa, sa1;              // of the next block and the one after it
+    float sb[kMine], sb1[kMine];
+    int left;                   // blocks not yet loaded
+    int64_t pb_at[COLS ? kMine : 1];
+
+    __device__ __forceinline__ void load(float &a, float (&b)[kMine])
+    {
+        if (left > 0) {
+            a = __ldg(pa);
+            pa += step_a;
+#pragma unroll
+            for (int i = 0; i < (COLS ? kMine : 1); ++i) b[i] = __ldg(pb + pb_at[i]);
+            pb += step_b;
+            --left;
+        }
+    }
+    __device__ __forceinline__ void begin(const ScaledParams &p, int64_t row, int64_t col, int kb0, int kb1, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < CW / 2; ++i) at[i] = make_float2(0.0f, 0.0f);
+        pa = p.sa + ((row < p.M ? row : p.M - 1) >> p.a_shift) * p.sa_mn + kb0 * p.sa_k;
+        step_a = p.sa_k;
+        step_b = p.sb_k;
+        pb = p.sb + kb0 * p.sb_k;
+#pragma unroll
+        for (int i = 0; i < (COLS ? kMine : 1); ++i) {
+            int64_t c = COLS ? col + lane * kMine + i : col;
+            if (c >= p.N) c = p.N - 1;
+            pb_at[i] = (c >> p.b_shift) * p.sb_mn;
+        }
+        left = kb1 - kb0;
+        sa = sa1 = 0.0f;
+        load(sa, sb);
+        load(sa1, sb1);
+    }
+    // Adds the block in the accumulator at taddr; `release` is called once it has been read.
+    template <class F> __device__ __forceinline__ void add(uint32_t taddr, float *scratch, int lane, F release)
+    {
+        bool fine = mild(sa);
+#pragma unroll
+        for (int i = 0; i < (COLS ? kMine : 1); ++i) fine = fine && mild(sb[i]);
+        fine = __all_sync(kFull, fine);
+        int ea = 0, eb[kMine] = {};
+        float a = 0.0f, b = 0.0f, m = sa;
+        if (!fine) {
+            m = split(sa, ea);
+#pragma unroll
+            for (int i = 0; i < (COLS ? kMine : 1); ++i) sb[i] = split(sb[i], eb[i]);
+            factors(m * sb[0], ea + eb[0], a, b);  // B's scale is the warp's
+        }
+        int *exponents = reinterpret_cast<int *>(scratch + CW);
+        if constexpr (COLS) {
+            __syncwarp();
+            if (kMine * lane < CW) {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    scratch[lane * kMine + i] = sb[i];
+                    if (!fine) exponents[lane * kMine + i] = eb[i];
+                }
+            }
+            __syncwarp();
+        }
+        const float s = COLS ? sa : sa * sb[0];
+        uint32_t r[2][kChunk];
+        tmem_start(taddr, r[0]);
+#pragma unroll
+        for (int c = 0; c < CW; c += kChunk) {
+            uint32_t(&v)[kChunk] = r[(c / kChunk) & 1];
+            tmem_arrived(v);
+            if (c + kChunk < CW) tmem_start(taddr + c + kChunk, r[(c / kChunk + 1) & 1]);
+            else release();
+            if (fine) {
+                if constexpr (COLS) {
+#pragma unroll
+                    for (int i = 0; i < kChunk; i += 4) {
+                        const float4 b = *reinterpret_cast<const float4 *>(scratch + c + i);
+                        const float2 lo = __fmul2_rn(make_float2(b.x, b.y), make_float2(s, s));
+                        const float2 hi = __fmul2_rn(make_float2(b.z, b.w), make_float2(s, s));
+                        at[(c + i) / 2] = __ffma2_rn(pair_of(v[i], v[i + 1]), lo, at[(c + i) / 2]);
+                        at[(c + i) / 2 + 1] = __ffma2_rn(pair_of(v[i + 2], v[i + 3]), hi, at[(c + i) / 2 + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kChunk; i += 2)
+                        at[(c + i) / 2] = __ffma2_rn(pair_of(v[i], v[i + 1]), make_float2(s, s), at[(c + i) / 2]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) {
+                    if constexpr (COLS) factors(m * scratch[c + i], ea + exponents[c + i], a, b);
+                    float &to = (i & 1) ? at[(c + i) / 2].y : at[(c + i) / 2].x;
+                    to = fmaf(__uint_as_float(v[i]) * a, b, to);
+                }
+            }
+        }
+        sa = sa1;
+#pragma unroll
+        for (int i = 0; i < (COLS ? kMine : 1); ++i) sb[i] = sb1[i];
+        load(sa1, sb1);
+    }
+};
+
+// ------------------------------------------------------------------ copies
+// The box of an operand for block kb: 128 rows from mn0 (rows of the tensor map), or, stored K x MN, the
+// block's 128 rows from column mn0.
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t bar, int mn, int mn0, int kb)
+{
+    const int c0 = mn ? mn0 : kb * 128, c1 = mn ? kb * 128 : mn0;
+    if (PAIR) tma_load_3d_pair(dst, map, bar, c0, c1, 0);
+    else tma_load_3d(dst, map, bar, c0, c1, 0);
+}
+// Descriptor of such a box (stored K x MN its 128 columns are one 128-byte atom wide: no leading offset), and
+// its step from one K = 32 to the next.
+__device__ __forceinline__ uint64_t box_desc(uint32_t addr) { return smem_desc(addr, 16, 1024); }
+__device__ __forceinline__ uint32_t box_step(int mn) { return (mn ? 32 * 128 : 32) >> 4; }
+
+__device__ __forceinline__ uint32_t f8_idesc(const ScaledParams &p, int n, int m) { return make_idesc(p.a_mn, p.b_mn, n, m) | p.formats; }
+
+// ------------------------------------------------------------------ pairs
+// 256 x 256 tiles; accumulators of 256 columns, two of them.  A slice's MMAs are committed once: the
+// commit on its `empty` barrier tells the producers that its boxes may be overwritten and the adding warps
+// that its accumulator is full.  (A warp that waits for one phase of it cannot miss it: the stage is used
+// again only after the warp has released an accumulator that comes later.)
+template <bool COLS> struct PairSmem {
+    static constexpr int kStages = COLS ? 5 : 6, kStage = 2 * kBox;
+    static constexpr int kEpi = kEpiWarps * 4096, kScratch = COLS ? kEpiWarps * 1024 : 0, kBars = 256;
+    static constexpr int kBytes = kStages * kStage + kEpi + kScratch + kBars + 1024;
+    static_assert(kBytes <= 227 * 1024, "one CTA per SM");
+    uint32_t ring, bar0;
+    uint8_t *epi, *scratch;
+    volatile uint32_t *tmem_slot;
+    volatile int *abort_flag;
+    __device__ __forceinline__ explicit PairSmem(uint8_t *raw)
+    {
+        const uint32_t r = smem_u32(raw), base = (r + 1023u) & ~1023u;
+        uint8_t *p = raw + (base - r);
+        ring = base;
+        epi = p + kStages * kStage;
+        scratch = epi + kEpi;
+        uint8_t *bars = scratch + kScratch;
+        bar0 = smem_u32(bars);
+        tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBars - 16);
+        abort_flag = reinterpret_cast<volatile int *>(bars + kBars - 8);
+    }
+    __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
+    __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 2); }
+    __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
+    __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kBox; }
+};
+
+constexpr int kLogGroup = 3;  // tiles are visited in groups of eight tile rows
+
+template <bool COLS, bool F32>
+__global__ void __launch_bounds__(kPairThreads, 1)
+scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_c, const __grid_constant__ ScaledParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    using Smem = PairSmem<COLS>;
+    const Smem sh(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Smem::kStages; ++s) {
+            mbar_init(sh.full(s), 1);
+            mbar_init(sh.empty(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(sh.acc_empty(i), 2 * kEpiWarps);
+        mbar_init(sh.drain(), 1);
+        *sh.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    cluster_sync();
+    if (warp == 1) tmem_alloc<true>(smem_u32(const_cast<uint32_t *>(sh.tmem_slot)), 512);
+    chain_wait();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *sh.tmem_slot;
+    const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
+    const int tiles = p.tiles_m * p.tiles_n, first = int(cluster_id_x()), step = int(cluster_count_x());
+    Ring ring(Smem::kStages);
+    bool ok = true;
+
+    if (warp < kPairFirst) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
+        if (warp == 0) {
+            // ---------------- producer: this CTA's 128 rows of A and its 128 of the tile's 256 rows of B
+            const bool leader = elect_one();
+            const uint32_t full0 = map_to_rank(sh.full(0), 0);
+            if (leader) {
+                tma_prefetch_desc(&map_a);
+                tma_prefetch_desc(&map_b);
+            }
+            for (int t = first; ok && t < tiles; t += step) {
+                int64_t tm, tn;
+                raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
+                const int m0 = int(tm) * 256 + int(rank) * 128, n0 = int(tn) * 256 + int(rank) * 128;
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                    if (__any_sync(kFull, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) {
+                        if (rank == 0) mbar_expect_tx(sh.full(ring.stage), 2 * Smem::kStage);
+                        if (!(p.inject_stall && kb == 0 && t == first)) {
+                            const uint32_t full = full0 + 8u * ring.stage;
+                            load_box<true>(sh.a(ring.stage), &map_a, full, p.a_mn, m0, kb);
+                            load_box<true>(sh.b(ring.stage), &map_b, full, p.b_mn, n0, kb);
+                        }
+                    }
+                    __syncwarp();
+                    ring.next();
+                }
+            }
+            if (leader) {
+                if (!ok) {  // copies in flight get time to land
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 2000000ull) {
+                    }
+                } else {  // no commit is on its way to this CTA's barriers when it exits
+                    for (int i = 0; i < Smem::kStages; ++i) {
+                        if (!watch.wait(sh.empty(ring.stage), ring.phase ^ 1u)) break;
+                        ring.next();
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            if (rank == 0) {
+                // ---------------- MMA issuer
+                const bool leader = elect_one();
+                const uint32_t idesc = f8_idesc(p, 256, 256), step_a = box_step(p.a_mn), step_b = box_step(p.b_mn);
+                const uint64_t a0 = box_desc(sh.a(0)), b0 = box_desc(sh.b(0));
+                int acc = 0;
+                uint32_t acc_phase = 0;
+                for (int t = first; ok && t < tiles; t += step)
+                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                        ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
+                        ok = ok && watch.wait(sh.full(ring.stage), ring.phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t a = a0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+                            const uint64_t b = b0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_f8<true>(tmem + uint32_t(acc * 256), a + k * step_a, b + k * step_b, idesc, k > 0 ? 1u : 0u);
+                            commit_both(sh.empty(ring.stage));
+                        }
+                        __syncwarp();
+                        ring.next();
+                        acc ^= 1;
+                        acc_phase ^= acc == 0 ? 1u : 0u;
+                    }
+                if (!ok && leader) {  // MMAs in flight finish before TMEM is released
+                    umma_commit<true>(sh.drain());
+                    const volatile int no_abort = 0;
+                    mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;" ::: "memory");
+        // ---------------- adding warps: rows 32 * quarter .. of this CTA's 128, 128 of the 256 columns
+        const int quarter = warp & 3, half = (warp - kPairFirst) >> 2;
+        Staging<F32> staging(sh.epi + (warp - kPairFirst) * 4096, lane);
+        float *scratch = reinterpret_cast<float *>(sh.scratch + (warp - kPairFirst) * 1024);
+        const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
+        const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * 128);
+        int acc = 0;
+        for (int t = first; ok && t < tiles; t += step) {
+            int64_t tm, tn;
+            raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
+            const int64_t m0 = tm * 256 + int64_t(rank) * 128 + quarter * 32, n0 = tn * 256 + half * 128;
+            Sums<128, COLS> sums;
+            sums.begin(p, m0 + lane, n0, 0, p.num_kb, lane);
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                ok = watch.wait(sh.empty(ring.stage), ring.phase);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                tc_fence_after();
+                sums.add(taddr0 + uint32_t(acc * 256), scratch, lane, [&] { release_accumulator(acc_empty0 + 8u * acc, lane); });
+                ring.next();
+                acc ^= 1;
+            }
+            if (!ok) break;
+            if (m0 >= p.M) continue;
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                if (n0 + c >= p.N) break;
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[2 * i] = sums.at[c / 2 + i].x;
+                    v[2 * i + 1] = sums.at[c / 2 + i].y;
+                }
+                store_rows(staging, v, &map_c, p.c_tma != 0, p.C, p.ldc, m0, n0 + c, p.M, p.N, p.c_type == GEMM_TYPE_BF16, 0);
+            }
+        }
+        staging.finish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves or frees TMEM while the other may still use it
+    tc_fence_after();
+    if (warp == 1) tmem_free<true>(tmem, 512);
+}
+
+// ------------------------------------------------------------------ tiles
+// One CTA: 128 rows of A, BN of B, the K blocks of its rank in the cluster.
+template <int BN> struct TileSmem {
+    static constexpr int kCtas = BN == 128 ? 1 : 2;  // an SM: 128 columns take too many registers for two
+    static constexpr int kStage = kBox + BN * 128, kStages = BN == 128 ? 6 : BN == 64 ? 4 : 5;
+    static constexpr int kBuffers = 4, kTmem = BN * kBuffers;
+    static constexpr int kRow = BN + 4;  // floats of a row of sums: 16-byte stores by rows without bank conflicts
+    static constexpr int kBars = 256, kScratch = kEpiWarps * 512;
+    static constexpr int kBytes = kStages * kStage + kScratch + kBars + 1024;
+    static_assert(128 * kRow * 4 <= kStages * kStage && kCtas * (kBytes + 1024) <= 228 * 1024, "CTAs per SM");
+    uint32_t ring, bar0;
+    uint8_t *scratch;
+    float *sums;  // in the ring's place, once it is empty
+    volatile uint32_t *tmem_slot;
+    volatile int *abort_flag;
+    __device__ __forceinline__ explicit TileSmem(uint8_t *raw)
+    {
+        const uint32_t r = smem_u32(raw), base = (r + 1023u) & ~1023u;
+        uint8_t *p = raw + (base - r);
+        ring = base;
+        sums = reinterpret_cast<float *>(p);
+        scratch = p + kStages * kStage;
+        uint8_t *bars = scratch + kScratch;
+        bar0 = smem_u32(bars);
+        tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBars - 16);
+        abort_flag = reinterpret_cast<volatile int *>(bars + kBars - 8);
+    }
+    __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
+    __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + kBuffers); }
+    __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
+    __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kBox; }
+};
+
+template <class T>
+__device__ __forceinline__ void store4(T *to, const float4 v, int64_t left, bool whole)
+{
+    const float e[4] = {v.x, v.y, v.z, v.w};
+    if (whole && left >= 4) {
+        T out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = from_f32<T>(e[i]);
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(to) = v;
+        else *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(out);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) to[i] = from_f32<T>(e[i]);
+    }
+}
+
+// C from the sums of the cluster's CTAs, added in the order of K: this CTA's share of the tile's 128 rows.
+template <class T, int BN>
+__device__ __forceinline__ void store_tile(const ScaledParams &p, const float *sums, uint32_t rank, int64_t m0, int64_t n0)
+{
+    constexpr int kRow = BN + 4;
+    const int height = 128 / p.splits, top = int(rank) * height;
+    uint32_t base[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) base[s] = s < p.splits ? map_to_rank(smem_u32(sums), uint32_t(s)) : 0u;
+    T *C = static_cast<T *>(p.C);
+    for (int i = threadIdx.x; i < height * BN / 4; i += kThreads) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        int row, col;  // of the piece: four columns of a row, or transposed four rows of a column
+        if (p.transposed) {
+            row = top + i % (height / 4) * 4;
+            col = i / (height / 4);
+        } else {
+            row = top + i / (BN / 4);
+            col = i % (BN / 4) * 4;
+        }
+        if (m0 + row >= p.M || n0 + col >= p.N) continue;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if (s >= p.splits) break;
+            if (p.transposed) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float f;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(base[s] + uint32_t((row + j) * kRow + col) * 4u) : "memory");
+                    v[j] += f;
+                }
+            } else {
+                float4 f;
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                             : "r"(base[s] + uint32_t(row * kRow + col) * 4u)
+                             : "memory");
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+            }
+        }
+        const float4 out = make_float4(v[0], v[1], v[2], v[3]);
+        if (p.transposed) store4<T>(C + (n0 + col) * p.ldc + m0 + row, out, p.M - m0 - row, true);
+        else store4<T>(C + (m0 + row) * p.ldc + n0 + col, out, p.N - n0 - col, true);
+    }
+}
+
+template <int BN, bool COLS>
+__global__ void __launch_bounds__(kThreads, TileSmem<BN>::kCtas)
+scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ ScaledParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    using Smem = TileSmem<BN>;
+    const Smem sh(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0u;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Smem::kStages; ++s) {
+            mbar_init(sh.full(s), 1);
+            mbar_init(sh.empty(s), 1);
+        }
+        for (int i = 0; i < Smem::kBuffers; ++i) mbar_init(sh.acc_empty(i), kEpiWarps);
+        mbar_init(sh.drain(), 1);
+        *sh.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<false>(smem_u32(const_cast<uint32_t *>(sh.tmem_slot)), Smem::kTmem);
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    chain_wait();
+    const uint32_t tmem = *sh.tmem_slot;
+    const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
+    const int tile = int(blockIdx.x) / p.splits;
+    const int64_t m0 = int64_t(tile % p.tiles_m) * 128, n0 = int64_t(tile / p.tiles_m) * BN;
+    const int kb0 = int(int64_t(p.num_kb) * rank / p.splits), kb1 = int(int64_t(p.num_kb) * (rank + 1) / p.splits);
+    Ring ring(Smem::kStages);
+    bool ok = true;
+
+    if (warp == 0) {
+        // ---------------- producer
+        const bool leader = elect_one();
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+            if (__any_sync(kFull, !ok)) {
+                ok = false;
+                break;
+            }
+            if (leader) {
+                mbar_expect_tx(sh.full(ring.stage), Smem::kStage);
+                if (!(p.inject_stall && kb == kb0)) {
+                    load_box<false>(sh.a(ring.stage), &map_a, sh.full(ring.stage), p.a_mn, int(m0), kb);
+                    load_box<false>(sh.b(ring.stage), &map_b, sh.full(ring.stage), p.b_mn, int(n0), kb);
+                }
+            }
+            __syncwarp();
+            ring.next();
+        }
+        if (!ok && leader) {  // copies in flight get time to land
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 2000000ull) {
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer
+        const bool leader = elect_one();
+        const uint32_t idesc = f8_idesc(p, BN, 128), step_a = box_step(p.a_mn), step_b = box_step(p.b_mn);
+        const uint64_t a0 = box_desc(sh.a(0)), b0 = box_desc(sh.b(0));
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = watch.wait(sh.acc_empty(acc), acc_phase ^ 1u);
+            ok = ok && watch.wait(sh.full(ring.stage), ring.phase);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t a = a0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+                const uint64_t b = b0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_f8<false>(tmem + uint32_t(acc * BN), a + k * step_a, b + k * step_b, idesc, k > 0 ? 1u : 0u);
+                umma_commit<false>(sh.empty(ring.stage));
+            }
+            __syncwarp();
+            ring.next();
+            if (++acc == Smem::kBuffers) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (!ok && leader) {
+            umma_commit<false>(sh.drain());
+            const volatile int no_abort = 0;
+            mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
+        }
+    } else {
+        // ---------------- adding warps: rows 32 * quarter .., half of the columns
+        constexpr int kWide = BN / 2;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        float *scratch = reinterpret_cast<float *>(sh.scratch + (warp - 2) * 512);
+        const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * kWide);
+        int acc = 0;
+        Sums<kWide, COLS> sums;
+        sums.begin(p, m0 + quarter * 32 + lane, n0 + half * kWide, kb0, kb1, lane);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = watch.wait(sh.empty(ring.stage), ring.phase);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            tc_fence_after();
+            sums.add(taddr0 + uint32_t(acc * BN), scratch, lane, [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sh.acc_empty(acc));
+            });
+            ring.next();
+            acc = acc + 1 == Smem::kBuffers ? 0 : acc + 1;
+        }
+        // every copy has landed and every MMA has been read: the ring's memory takes the sums
+        if (ok) {
+            float *to = sh.sums + (quarter * 32 + lane) * Smem::kRow + half * kWide;
+#pragma unroll
+            for (int i = 0; i < kWide; i += 4)
+                *reinterpret_cast<float4 *>(to + i) =
+                    make_float4(sums.at[i / 2].x, sums.at[i / 2].y, sums.at[i / 2 + 1].x, sums.at[i / 2 + 1].y);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free<false>(tmem, Smem::kTmem);
+    if (p.splits > 1) cluster_sync();
+    if (*sh.abort_flag == 0) {
+        if (p.c_type == GEMM_TYPE_F32) store_tile<float, BN>(p, sh.sums, rank, m0, n0);
+        else if (p.c_type == GEMM_TYPE_F16) store_tile<__half, BN>(p, sh.sums, rank, m0, n0);
+        else store_tile<__nv_bfloat16, BN>(p, sh.sums, rank, m0, n0);
+    }
+    if (p.splits > 1) {
+        __syncwarp();
+        cluster_sync();  // the others may still read this CTA's sums
+    }
+}
+
+// ------------------------------------------------------------------ host side
+// An 8-bit row-major matrix in boxes of 128 bytes x box_rows with the 128-byte swizzle.
+bool make_map8(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+{
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), 1};
+    const cuuint64_t strides[2] = {cuuint64_t(ld), cuuint64_t(ld) * cuuint64_t(rows)};
+    const cuuint32_t box[3] = {128, cuuint32_t(box_rows), 1}, steps[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool operand_map(CUtensorMap *map, const ScaledOperand &o, int64_t mn, int64_t K, int box_rows)
+{
+    return o.mn ? make_map8(map, o.at, K, mn, o.ld, 128) : make_map8(map, o.at, mn, K, o.ld, box_rows);
+}
+
+ScaledParams params_of(const ScaledArgs &a, int tile_m, int tile_n, unsigned int *status)
+{
+    ScaledParams p{};
+    p.M = a.M;
+    p.N = a.N;
+    p.num_kb = int((a.K + 127) / 128);
+    p.tiles_m = int((a.M + tile_m - 1) / tile_m);
+    p.tiles_n = int((a.N + tile_n - 1) / tile_n);
+    p.splits = 1;
+    p.a_mn = a.a.mn;
+    p.b_mn = a.b.mn;
+    p.formats = (a.a.q_type == GEMM_TYPE_E5M2 ? 1u << 7 : 0u) | (a.b.q_type == GEMM_TYPE_E5M2 ? 1u << 10 : 0u);
+    p.sa = a.a.scales;
+    p.sa_mn = a.a.s_mn;
+    p.sa_k = a.a.s_k;
+    p.a_shift = a.a.mn_shift;
+    p.sb = a.b.scales;
+    p.sb_mn = a.b.s_mn;
+    p.sb_k = a.b.s_k;
+    p.b_shift = a.b.mn_shift;
+    p.C = a.C;
+    p.ldc = a.ldc;
+    p.c_type = a.c_type;
+    p.status = status;
+    test_hooks(p.timeout_ns, p.inject_stall);
+    return p;
+}
+
+template <bool COLS, bool F32> cudaError_t launch_pairs(const DeviceInfo &dev, const ScaledArgs &a, unsigned int *status, cudaStream_t stream)
+{
+    static std::atomic<int> cache[64];
+    using Smem = PairSmem<COLS>;
+    auto *kernel = scaled_pair_kernel<COLS, F32>;
+    const int pairs = resident_pairs(kernel, kPairThreads, Smem::kBytes, dev.device, cache);
+    if (pairs <= 0) return cudaErrorInitializationError;
+    ScaledParams p = params_of(a, 256, 256, status);
+    CUtensorMap ma, mb, mc;
+    std::memset(&mc, 0, sizeof(mc));
+    if (!operand_map(&ma, a.a, a.M, a.K, 128) || !operand_map(&mb, a.b, a.N, a.K, 128)) return cudaErrorInvalidValue;
+    p.c_tma = make_store_map(&mc, a.C, a.c_type, a.M, a.N, a.ldc, 1, 0, true);
+    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
+    if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    return launch_chained(kernel, dim3(unsigned(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, Smem::kBytes, 2, stream, ma, mb, mc, p);
+}
+
+template <int BN, bool COLS>
+cudaError_t launch_tiles(const ScaledArgs &a, int splits, int transposed, unsigned int *status, cudaStream_t stream)
+{
+    using Smem = TileSmem<BN>;
+    auto *kernel = scaled_tile_kernel<BN, COLS>;
+    const cudaError_t e = allow_smem_once(kernel, Smem::kBytes);
+    if (e != cudaSuccess) return e;
+    ScaledParams p = params_of(a, 128, BN, status);
+    p.splits = splits;
+    p.transposed = transposed;
+    CUtensorMap ma, mb;
+    if (!operand_map(&ma, a.a, a.M, a.K, 128) || !operand_map(&mb, a.b, a.N, a.K, BN)) return cudaErrorInvalidValue;
+    const int64_t ctas = int64_t(p.tiles_m) * p.tiles_n * splits;
+    if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    return launch_chained(kernel, dim3(unsigned(ctas)), kThreads, Smem::kBytes, splits, stream, ma, mb, p);
+}
+
+template <int BN>
+cudaError_t launch_tiles(const ScaledArgs &a, int splits, int transposed, unsigned int *status, cudaStream_t stream)
+{
+    return a.b.mn_shift == 0 ? launch_tiles<BN, true>(a, splits, transposed, status, stream)
+                             : launch_tiles<BN, false>(a, splits, transposed, status, stream);
+}
+
+struct Plan {
+    bool pairs, swap;
+    int bn, splits;
+};
+
+Plan plan_of(const DeviceInfo &dev, const ScaledArgs &a)
+{
+    Plan best{false, false, 128, 1};
+    const int64_t kb = (a.K + 127) / 128;
+    const int64_t t256 = ((a.M + 255) / 256) * ((a.N + 255) / 256), pairs = dev.num_sms / 2;
+    // the short side on the columns, where 32 or 64 of them hold it
+    const int64_t shorter = a.M < a.N ? a.M : a.N;
+    best.swap = a.M < a.N && a.M <= 64;
+    const ScaledOperand &b = best.swap ? a.a : a.b;
+    if (shorter <= 64 && !b.mn) best.bn = shorter <= 32 ? 32 : 64;
+    if (t256 >= pairs / 2 && shorter > 64) best.pairs = true;
+    const int64_t m = best.swap ? a.N : a.M, n = best.swap ? a.M : a.N;
+    const int64_t tiles = ((m + 127) / 128) * ((n + best.bn - 1) / best.bn);
+    while (best.splits < 8 && tiles * best.splits * 2 <= 2 * dev.num_sms && kb >= 4 * best.splits) best.splits *= 2;
+    // GEMM_GB300_SCALED_PLAN (tests and sweeps): P for pairs, or BN:splits or BN:splits:s (operands swapped)
+    if (const char *e = std::getenv("GEMM_GB300_SCALED_PLAN"); e && *e) {
+        int bn = 0, splits = 0;
+        char s = 0;
+        if (*e == 'P') {
+            best = Plan{true, false, 128, 1};
+        } else if (std::sscanf(e, "%d:%d:%c", &bn, &splits, &s) >= 2 && (bn == 32 || bn == 64 || bn == 128) &&
+                   (splits == 1 || splits == 2 || splits == 4 || splits == 8) && (bn == 128 || !(s == 's' ? a.a : a.b).mn)) {
+            best = Plan{false, s == 's', bn, splits};
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+cudaError_t launch_scaled(const DeviceInfo &dev, const ScaledArgs &a, cudaStream_t stream)
+{
+    unsigned int *status = device_status_word(dev.device);
+    if (status == nullptr) return cudaErrorInitializationError;
+    const Plan plan = plan_of(dev, a);
+    if (plan.pairs) {
+        const bool cols = a.b.mn_shift == 0, f32 = a.c_type == GEMM_TYPE_F32;
+        if (cols) return f32 ? launch_pairs<true, true>(dev, a, status, stream) : launch_pairs<true, false>(dev, a, status, stream);
+        return f32 ? launch_pairs<false, true>(dev, a, status, stream) : launch_pairs<false, false>(dev, a, status, stream);
+    }
+    ScaledArgs t = a;
+    if (plan.swap) {
+        t.M = a.N;
+        t.N = a.M;
+        t.a = a.b;
+        t.b = a.a;
+    }
+    if (plan.bn == 32) return launch_tiles<32>(t, plan.splits, plan.swap, status, stream);
+    if (plan.bn == 64) return launch_tiles<64>(t, plan.splits, plan.swap, status, stream);
+    return launch_tiles<128>(t, plan.splits, plan.swap, status, stream);
+}
+
+}  // namespace gemm

@@ -305,7 +305,13 @@ GEMM_API gemm_status_t gemm_tile_raster(int64_t t, int64_t tiles_m, int64_t tile
  * position.  Slots without an expert (-1) have no position (where = -1); arrays of T * k
  * positions are then used only up to offsets[E].
  */
-typedef enum { GEMM_TYPE_F32 = 0, GEMM_TYPE_F16 = 1, GEMM_TYPE_BF16 = 2 } gemm_type_t;
+typedef enum {
+    GEMM_TYPE_F32 = 0,
+    GEMM_TYPE_F16 = 1,
+    GEMM_TYPE_BF16 = 2,
+    GEMM_TYPE_E4M3 = 3, /* 8-bit types of the block-scaled products only */
+    GEMM_TYPE_E5M2 = 4
+} gemm_type_t;
 typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score_t;
 
 /*
@@ -478,6 +484,77 @@ GEMM_API gemm_status_t gemm_lora_linear(gemm_type_t type, gemm_type_t y_type, in
                                         const void *A, int64_t lda, int64_t strideA, const void *B,
                                         int64_t ldb, int64_t strideB, const float *scales, void *Y,
                                         int64_t ldy, void *work, void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Block-scaled 8-bit products: matrices of 8-bit floating-point values (GEMM_TYPE_E4M3, largest value
+ * 448, no infinity; GEMM_TYPE_E5M2, largest 57344) with an fp32 scale for every block of 128 elements
+ * of a row, of a column, or of 128 x 128 (fewer at the edges), and their products: a linear layer's
+ * forward pass and the gradients of its input and its weight.  The source pages have no counterpart;
+ * rows, leading dimensions, streams, statuses and asynchrony are those of the GEMM calls above.  Every
+ * array is device memory owned by the caller, no scratch memory is allocated and nothing is kept from
+ * one call for the next, so every call may be captured into a graph.
+ *
+ * Scales.  An R x C matrix in blocks of b0 x b1 has ceil(R / b0) x ceil(C / b1) scales; that of element
+ * (i, j) is scales[(i / b0) * s_row + (j / b1) * s_col], strides in elements, at least 0.  The value of
+ * an element is its 8-bit value times its scale.
+ * Alignment: 8-bit matrices 16-byte aligned with leading dimensions that are multiples of 16 (else
+ * GEMM_ERR_MISALIGNED); rows and columns are free.  Limits: rows, columns, M, N and K < 2^30.
+ */
+
+/*
+ * Quantises X (rows x cols, fp32, fp16 or bf16, any leading dimension) to Q (rows x cols of q_type) and
+ * its scales, in blocks of block_rows x block_cols: 1 x 128, 128 x 1 or 128 x 128.  A block's scale is
+ * the smallest power of two s, at least 2^-126, with max|x| <= s * (the type's largest value), over the
+ * block's finite elements; 1 where they are all zeros.  Each element is x / s rounded to the nearest
+ * 8-bit value, ties to even.  An infinity or NaN is stored as NaN and changes nothing else.
+ */
+GEMM_API gemm_status_t gemm_quantize_blocks(gemm_type_t type, gemm_type_t q_type, int64_t rows,
+                                            int64_t cols, const void *X, int64_t ldx, int block_rows,
+                                            int block_cols, void *Q, int64_t ldq, float *scales,
+                                            int64_t s_row, int64_t s_col, void *stream);
+
+/*
+ * Both ways in one pass over X: Q with scales in blocks of 1 x 128, as a product over the columns takes
+ * it, and Qc with scales_c in blocks of 128 x 1, as a product over the rows does.
+ */
+GEMM_API gemm_status_t gemm_quantize_both(gemm_type_t type, gemm_type_t q_type, int64_t rows,
+                                          int64_t cols, const void *X, int64_t ldx, void *Q,
+                                          int64_t ldq, float *scales, int64_t s_row, int64_t s_col,
+                                          void *Qc, int64_t ldqc, float *scales_c, int64_t sc_row,
+                                          int64_t sc_col, void *stream);
+
+/*
+ * Y = the values of Q (rows x cols of q_type, scales in blocks of 1 x 128, 128 x 1 or 128 x 128), each
+ * multiplied in fp32 and rounded to y_type (fp32, fp16 or bf16; any leading dimension).
+ */
+GEMM_API gemm_status_t gemm_dequantize_blocks(gemm_type_t q_type, gemm_type_t y_type, int64_t rows,
+                                              int64_t cols, const void *Q, int64_t ldq, int block_rows,
+                                              int block_cols, const float *scales, int64_t s_row,
+                                              int64_t s_col, void *Y, int64_t ldy, void *stream);
+
+/*
+ * C = op(A) * op(B) of block-scaled 8-bit matrices on the tcgen05 tensor cores, op as in the GEMM calls:
+ *     C[m][n] = sum over blocks b of 128 k:  sa(m, b) * sb(n, b) * sum over k in b of A[m][k] * B[k][n]
+ * A of a_type and B of b_type (either 8-bit type each), C of c_type (fp32, fp16 or bf16).  Along K there
+ * is a scale for every 128 elements, along M (N) one for every a_block (b_block) rows of op(A) (columns
+ * of op(B)), 1 or 128; scales are laid out by the stored matrices' rows and columns, so opA =
+ * GEMM_OP_N takes blocks of a_block x 128 of A, GEMM_OP_T of 128 x a_block.  Any fp32 scales: infinities
+ * and NaN spread as in the formula, and products of scales beyond fp32's range lose nothing that C
+ * could hold.  A linear layer (W stored N x K) takes
+ *     Y = X W^T     (N, T)   X in blocks of 1 x 128, W of 128 x 128
+ *     dX = dY W     (N, N)   dY in blocks of 1 x 128, the same W
+ *     dW = dY^T X   (T, N)   dY and X in blocks of 128 x 1
+ * Products are exact and summed by the tensor cores over a block, in fp32 over the blocks, rounded once.
+ * K == 0 writes zeros.  C must not overlap the inputs.
+ * Alignment: C 16-byte aligned, ldc a multiple of 8 elements.
+ */
+GEMM_API gemm_status_t gemm_scaled_matmul(gemm_type_t a_type, gemm_type_t b_type, gemm_type_t c_type,
+                                          gemm_op_t opA, gemm_op_t opB, int64_t M, int64_t N, int64_t K,
+                                          const void *A, int64_t lda, int a_block,
+                                          const float *a_scales, int64_t sa_row, int64_t sa_col,
+                                          const void *B, int64_t ldb, int b_block,
+                                          const float *b_scales, int64_t sb_row, int64_t sb_col, void *C,
+                                          int64_t ldc, void *stream);
 
 #ifdef __cplusplus
 }
