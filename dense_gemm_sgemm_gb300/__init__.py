@@ -20,6 +20,10 @@ Routed products (a router, the experts' products, low-rank adapters; see routed.
 Block-scaled 8-bit products (see scaled.py):
 
     quantize_blocks, quantize_both, dequantize_blocks, scaled_matmul
+
+The orthogonalised update of a weight (see update.py):
+
+    orthogonalize
 """
 from __future__ import annotations
 
@@ -45,12 +49,14 @@ _ROUTED = (
 
 
 def __getattr__(name):
-    # routed.py and scaled.py need torch at import; this package does not until a call is made, so a star
+    # routed.py, scaled.py and update.py need torch at import; this package does not until a call is made, so a star
     # import leaves these names out (`from dense_gemm_sgemm_gb300.routed import *` has them)
     if name in _ROUTED:
         from . import routed as module
     elif name in _SCALED:
         from . import scaled as module
+    elif name == "orthogonalize":
+        from . import update as module
     else:
         module = None
     if module is not None:

@@ -75,6 +75,9 @@ SIGNATURES = {
                                       _vp, _i64, _vp]),
     "gemm_scaled_matmul": (_int, [_int, _int, _int, _int, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp,
                                   _i64, _i64, _vp, _i64, _int, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "gemm_orthogonalize_work_bytes": (_i64, [_i64, _i64, _i64]),
+    "gemm_orthogonalize": (_int, [_int, _int, _i64, _i64, _i64, _vp, _i64, _i64, _int,
+                                  ctypes.POINTER(ctypes.c_float), _f32, _vp, _i64, _i64, _vp, _vp]),
 }
 
 class SgemmConfig(ctypes.Structure):

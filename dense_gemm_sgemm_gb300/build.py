@@ -5,7 +5,7 @@ arch-specific features need the `a` target), in parallel, and linked into one sh
 library with the static CUDA runtime.  No fast-math: denormals, IEEE division and square
 root stay on, which the strict-FP32 path relies on.
 
-With it goes the Python binding of the routed and the block-scaled products, _build/_routed.so, compiled against the
+With it goes the Python binding of the routed products, the block-scaled ones and the orthogonalised update, _build/_routed.so, compiled against the
 installed torch.  The library does not need it: where the binding cannot be built (no torch, a torch
 without CUDA, no host C++ compiler) the reason is kept beside it and raised when routed.py is imported.
 
@@ -30,7 +30,7 @@ LIB_NAME = "libgemm_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 BINDING_PATH = os.path.join(OUT_DIR, "_routed.so")
 BINDING_SRC = os.path.join(CSRC, "routed_binding.cpp")
-BINDING_PARTS = os.path.join(CSRC, "scaled_binding.h")
+BINDING_PARTS = os.path.join(CSRC, "training_binding.h")
 BINDING_FOR = os.path.join(OUT_DIR, "_routed.for")      # the torch that the binding was compiled against
 BINDING_ERROR = os.path.join(OUT_DIR, "_routed.error")  # why there is none
 HEADER = os.path.join(ROOT, "include", "gemm_gb300.h")

@@ -1,5 +1,5 @@
 // Python binding of the routed products (argument checks, outputs, the C call; see routed.py), and through
-// scaled_binding.h of the block-scaled ones.
+// training_binding.h of the block-scaled products and the orthogonalised update.
 //
 // A decoding step makes several of these calls, each a few microseconds of GPU time.  Checked and
 // marshalled in Python one took 11 to 24 us of a Grace core, so the tensors are read here: about 5 us.
@@ -422,7 +422,7 @@ BOUND(lora_linear, 9)
     return wrap(y.t);
 END_BOUND
 
-#include "scaled_binding.h"
+#include "training_binding.h"
 
 // The comparison alone, of two torch devices: first, other.
 BOUND(same_device, 2)
@@ -445,7 +445,7 @@ PyObject *set_error(PyObject *, PyObject *cls)
 PyMethodDef methods[] = {ENTRY(moe_route), ENTRY(moe_route_backward), ENTRY(moe_plan), ENTRY(moe_dispatch), ENTRY(moe_combine),
                          ENTRY(moe_combine_backward), ENTRY(gated_silu_backward), ENTRY(grouped_linear),
                          ENTRY(grouped_weight_grad), ENTRY(lora_linear), ENTRY(quantize_blocks), ENTRY(quantize_both),
-                         ENTRY(dequantize_blocks), ENTRY(scaled_matmul), ENTRY(same_device), {"set_error", set_error, METH_O, nullptr},
+                         ENTRY(dequantize_blocks), ENTRY(scaled_matmul), ENTRY(orthogonalize), ENTRY(same_device), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_routed", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -137,14 +137,23 @@ template <bool F32> struct Staging {
 // This lane's row m0 + lane, 32 columns from n0, of C (M x N): through the staging tile to a TMA store of a
 // 32 x 32 box (map: make_store_map, swizzled), or where TMA cannot store to 16-byte pieces of rows.  C 16-byte
 // aligned, ld a multiple of 8 elements; plane: the matrix of the map's stack, which C points to.
-template <bool F32>
+// TRANSPOSED: this lane's column n0 + lane, 32 rows from m0.
+template <bool F32, bool TRANSPOSED = false>
 __device__ __forceinline__ void store_rows(Staging<F32> &staging, const float (&v)[32], const CUtensorMap *map, bool tma, void *C,
                                            int64_t ld, int64_t m0, int64_t n0, int64_t M, int64_t N, bool bf16, int plane)
 {
     const int lane = staging.lane;
     uint8_t *piece = tma ? staging.next() : staging.all();
     uint4 *row = reinterpret_cast<uint4 *>(piece) + lane * (F32 ? 8 : 4);
-    if (F32) {
+    if (TRANSPOSED && F32) {
+        float *t = reinterpret_cast<float *>(piece) + (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i * 32 + 4 * ((lane >> 2) ^ (i & 7))] = v[i];
+    } else if (TRANSPOSED) {
+        uint16_t *t = reinterpret_cast<uint16_t *>(piece) + (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t[i * 32 + 8 * ((lane >> 3) ^ ((i >> 1) & 3))] = to_16(v[i], bf16);
+    } else if (F32) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             row[j ^ (lane & 7)] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),

@@ -1,5 +1,5 @@
-// Python binding of the block-scaled 8-bit products (see scaled.py); included by routed_binding.cpp, whose
-// helpers it uses.
+// Python binding of the block-scaled 8-bit products (see scaled.py) and of the orthogonalised update (see
+// update.py); included by routed_binding.cpp, whose helpers it uses.
 
 gemm_type_t type8_of(at::ScalarType t, const char *what)
 {
@@ -126,4 +126,30 @@ BOUND(scaled_matmul, 8)
                                   stream.handle);
     });
     return wrap(C.t);
+END_BOUND
+
+// g, steps, coefficients (a tuple of 3 * steps numbers), eps, out_dtype, stream
+BOUND(orthogonalize, 6)
+    const at::Tensor &t = tensor(device, a[0], "g");
+    TORCH_CHECK_VALUE(t.dim() == 2 || t.dim() == 3, "g: a matrix or a stack of matrices (2-D or 3-D) wanted");
+    const Matrix x = matrix(device, a[0], "g", int(t.dim()));
+    const Stream stream(a[5], t);
+    const gemm_type_t type = type_of(t.scalar_type(), "g");
+    const int steps = small(a[1]);
+    TORCH_CHECK_VALUE(PyTuple_Check(a[2]) && PyTuple_GET_SIZE(a[2]) <= 3 * 64 && PyTuple_GET_SIZE(a[2]) == 3 * Py_ssize_t(steps),
+                      "coefficients: three for each of 1 to 64 steps wanted");
+    float coefficients[3 * 64];
+    for (int i = 0; i < 3 * steps; ++i) coefficients[i] = real(PyTuple_GET_ITEM(a[2], i));
+    const float eps = real(a[3]);
+    const at::ScalarType dtype = dtype_of(a[4], at::kBFloat16);
+    const gemm_type_t y_type = type_of(dtype, "out_dtype");
+    const int64_t count = t.dim() == 3 ? t.size(0) : 1, stride = t.dim() == 3 && count > 1 ? t.stride(0) : 0;
+    const int64_t ld = std::max((x.cols + 7) & ~int64_t(7), int64_t(8));
+    at::Tensor y = t.dim() == 3 ? fresh({count, x.rows, ld}, dtype, t) : fresh({x.rows, ld}, dtype, t);
+    at::Tensor work = fresh({gemm_orthogonalize_work_bytes(count, x.rows, x.cols)}, at::kByte, t);
+    call("gemm_orthogonalize", [&] {
+        return gemm_orthogonalize(type, y_type, count, x.rows, x.cols, x.data(), x.ld, stride, steps, coefficients, eps, y.data_ptr(), ld,
+                                  x.rows * ld, work.data_ptr(), stream.handle);
+    });
+    return wrap(ld == x.cols ? y : y.narrow(-1, 0, x.cols));
 END_BOUND

@@ -556,6 +556,40 @@ GEMM_API gemm_status_t gemm_scaled_matmul(gemm_type_t a_type, gemm_type_t b_type
                                           const float *b_scales, int64_t sb_row, int64_t sb_col, void *C,
                                           int64_t ldc, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The orthogonalised update of a weight, as an optimiser takes it from the weight's gradient or its
+ * momentum: the matrix whose singular vectors are those of G and whose singular values have been driven
+ * towards 1 by an odd polynomial applied `steps` times (Newton-Schulz iteration).  For each of `count`
+ * matrices G (rows x cols, matrix i at G + i * strideG):
+ *     X = G / (||G|| + eps)                         (Frobenius norm)
+ *     A = X X^T,  X = a X + (b A + c A^2) X         `steps` times; coefficients: a, b, c of each step
+ *     Y = X
+ * with X^T in X's place, and Y transposed back, where rows > cols, which gives the same matrix from smaller
+ * products.  G and Y are fp32, fp16 or bf16 (`type`, `y_type`).  coefficients is host memory, 3 * steps floats, read
+ * before the call returns.
+ *
+ * Precision.  The norm is summed in fp32 without overflow or underflow of the squares.  The iterates are
+ * held to 22 bits; products are of fp16 values with fp32 sums, the diagonals of A and of b A + c A^2 apart from
+ * them in fp32: one product where Y is bf16 and rows and cols are above 128, else three, of the values' parts.
+ * For (3.4445, -4.7750, 2.0315) and 5 steps the result before its own rounding is within 2 * 10^-3 of the
+ * formula's (relative, in the Frobenius norm; usually a quarter of that), with three products within
+ * 2.5 * 10^-4 (usually 10^-6).  A matrix of zeros gives zeros, an infinity or NaN makes its whole matrix's result NaN and
+ * no other's.
+ *
+ * work: gemm_orthogonalize_work_bytes(count, rows, cols) bytes for the call to use (not kept), 256-byte
+ * aligned; about 16 bytes for every element of a square G.
+ * The call allocates nothing and keeps nothing, so it may be captured into a graph.
+ * GEMM_ERR_UNSUPPORTED: coefficients beyond 10^4, or under which a singular value of at most 1 may grow
+ * beyond 10^4 on the way.
+ * Alignment: Y 16-byte aligned, ldy and strideY multiples of 8 elements.  Limits: rows and cols < 2^20,
+ * count < 2^16, steps <= 64.  Y must not overlap G.
+ */
+GEMM_API int64_t gemm_orthogonalize_work_bytes(int64_t count, int64_t rows, int64_t cols);
+GEMM_API gemm_status_t gemm_orthogonalize(gemm_type_t type, gemm_type_t y_type, int64_t count,
+                                          int64_t rows, int64_t cols, const void *G, int64_t ldg, int64_t strideG, int steps,
+                                          const float *coefficients, float eps, void *Y, int64_t ldy,
+                                          int64_t strideY, void *work, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
