@@ -33,9 +33,9 @@
 namespace gemm {
 namespace {
 
-constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
+constexpr int kEpiWarps = 8;
 // The pair kernel's warps come in fours, so that the adding ones may have more registers than the launch
-// gives each: (4 * 40 + 8 * 232) * 32 = 12 * 32 * 168.
+// gives each: (4 * 72 + 8 * 216) * 32 = 12 * 32 * 168.
 constexpr int kPairFirst = 4, kPairThreads = 32 * (kPairFirst + kEpiWarps);
 constexpr int kBox = 128 * 128;  // bytes: 128 rows of a K block, or its 128 k of 128 rows
 constexpr unsigned kFull = 0xffffffffu;
@@ -73,18 +73,7 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
                      : "memory");
 }
 
-// 16 or 32 columns of this thread's TMEM lane, on their way: not to be read before tmem_arrived().
-__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-}
+// 16 columns of this thread's TMEM lane, on their way: not to be read before tmem_arrived().
 __device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -94,14 +83,6 @@ __device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[16])
                  : "r"(taddr));
 }
 // Waits for the loads started so far; the registers pass through it, so that nothing reads them earlier.
-__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
 __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -116,128 +97,212 @@ __device__ __forceinline__ bool mild(float s)
     const float a = fabsf(s);
     return a == 0.0f || (a >= 0x1p-40f && a <= 0x1p40f);
 }
-// s = m * 2^e, m in [1/2, 1); an infinite or NaN scale is its own m.
-__device__ __forceinline__ float split(float s, int &e)
+// s as two factors of half its exponent each (zero, infinite and NaN scales as 1 and s).  A block's sum times
+// both scales' first factors and then both second ones stays in fp32's range wherever the result does.
+__device__ __forceinline__ float2 halves(float s)
 {
-    e = 0;
-    return fabsf(s) <= FLT_MAX ? frexpf(s, &e) : s;
-}
-__device__ __forceinline__ float two_to(int e) { return __uint_as_float(uint32_t(max(-126, min(127, e)) + 127) << 23); }
-// Two factors whose product is m * 2^e, such that neither they nor v * a, for a block's sum v, leave fp32's
-// normal range before v * a * b does: scales of any size then lose nothing but what the result cannot hold.
-__device__ __forceinline__ void factors(float m, int e, float &a, float &b)
-{
-    a = m * two_to(e / 2);
-    b = two_to(e - e / 2);
+    const float a = fabsf(s);
+    if (!(a > 0.0f && a <= FLT_MAX)) return make_float2(1.0f, s);
+    const int e = (ilogbf(s) & ~1) / 2;
+    return make_float2(__uint_as_float(uint32_t(127 + e) << 23), s * __uint_as_float(uint32_t(127 - e) << 23));
 }
 
 __device__ __forceinline__ float2 pair_of(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
-// The sums of one thread: row `row` of A, CW columns from `col` of B.
-template <int CW, bool COLS> struct Sums {
-    static constexpr int kChunk = CW == 32 || CW == 64 ? 32 : 16, kMine = (CW + 31) / 32;  // columns a load; a lane's share of sb
-    float2 at[CW / 2];
-    const float *pa, *pb;
-    int64_t step_a, step_b;
-    float sa, sa1;              // of the next block and the one after it
-    float sb[kMine], sb1[kMine];
-    int left;                   // blocks not yet loaded
-    int64_t pb_at[COLS ? kMine : 1];
+// ------------------------------------------------------------------ scales
+// A K block's scales pass through shared memory, in slots of their own: one warp copies them (cp.async, any
+// strides) as the ring's stages become free, looks at a block's when the copies of the kDelay blocks behind it
+// are on their way, and announces it.  (With loads to the adding warps' registers one or two blocks ahead a
+// block took 750 SM cycles whatever its size; with those warps looking at them 400 more than now.)
+//
+// There is no barrier for a slot's release: a stage is free once the MMAs of its block b have completed, for
+// which the adding warps must have read block b - (accumulators) and so have added the one before that; a
+// slot is used again stages + accumulators + 1 blocks later at the earliest.
+constexpr int kDelay = 3;
 
-    __device__ __forceinline__ void load(float &a, float (&b)[kMine])
-    {
-        if (left > 0) {
-            a = __ldg(pa);
-            pa += step_a;
+// Waits for two phases, all lanes with one answer; where both are there already this costs a vote.
+__device__ __forceinline__ bool wait_both(const Watch &watch, uint32_t bar0, uint32_t phase0, uint32_t bar1, uint32_t phase1)
+{
+    const bool there = mbar_try_wait(bar0, phase0) & mbar_try_wait(bar1, phase1);
+    if (__builtin_expect(__all_sync(kFull, there), 1)) return true;
+    const bool got = watch.wait(bar0, phase0) && watch.wait(bar1, phase1);
+    return __all_sync(kFull, got) != 0;
+}
+
+// Floats of a slot: row scales, column scales (without COLS those of the two runs of 128 columns), and what the
+// adding warps multiply a row by: its scale, or without COLS its products with the column scales (PAIRS: with
+// either run's); NaN in all rows where some scale is not mild, which sends the warps to the scales themselves.
+template <bool COLS, bool PAIRS> struct Slot {
+    static constexpr int kEach = !COLS && PAIRS ? 2 : 1, kCols = 128, kRow = kCols + (COLS ? (PAIRS ? 256 : 128) : 4);
+    static constexpr int kFloats = kRow + 128 * kEach;
+};
+
+__device__ __forceinline__ void copy_scale(float *dst, const float *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ int64_t scale_row(int64_t row, int64_t rows) { return row < rows ? row : rows - 1; }
+// The scales of COUNT rows from row0 for block kb (rows outside the matrix take the last one's).
+template <int COUNT>
+__device__ __forceinline__ void copy_scales(float *dst, const float *scales, int64_t s_mn, int64_t s_k, int shift, int64_t row0,
+                                            int64_t rows, int kb, int lane)
+{
 #pragma unroll
-            for (int i = 0; i < (COLS ? kMine : 1); ++i) b[i] = __ldg(pb + pb_at[i]);
-            pb += step_b;
-            --left;
+    for (int i = 0; i < COUNT; i += 32)
+        copy_scale(dst + i + lane, scales + (scale_row(row0 + i + lane, rows) >> shift) * s_mn + kb * s_k);
+}
+
+// The warp that handles a tile's scales.  BN: columns of the tile.
+template <bool COLS, bool PAIRS, int BN, int SLOTS> struct ScaleCopies {
+    using L = Slot<COLS, PAIRS>;
+    float *slots;
+    uint32_t full0;  // barriers of the slots, one arrival each
+    int lane;
+    Ring copying{SLOTS}, looking{SLOTS};
+    int behind = 0;
+
+    __device__ __forceinline__ ScaleCopies(float *s, uint32_t bars, int l) : slots(s), full0(bars), lane(l) {}
+    __device__ __forceinline__ void copy(const ScaledParams &p, int64_t m0, int64_t n0, int kb)
+    {
+        float *slot = slots + copying.stage * L::kFloats;
+        copy_scales<128>(slot, p.sa, p.sa_mn, p.sa_k, p.a_shift, m0, p.M, kb, lane);
+        if (COLS && PAIRS) {
+            // a piece's columns side by side: 64 from column 64 h of the tile, 64 from column 128 + 64 h
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                copy_scales<64>(slot + L::kCols + 64 * i, p.sb, p.sb_mn, p.sb_k, p.b_shift, n0 + (i & 1) * 128 + (i >> 1) * 64, p.N, kb, lane);
+        } else if (COLS) {
+            copy_scales<BN>(slot + L::kCols, p.sb, p.sb_mn, p.sb_k, p.b_shift, n0, p.N, kb, lane);
+        } else if (lane < 2) {
+            copy_scale(slot + L::kCols + lane, p.sb + (scale_row(n0 + (PAIRS ? 128 * lane : 0), p.N) >> p.b_shift) * p.sb_mn + kb * p.sb_k);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        copying.next();
+        if (++behind > kDelay) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDelay) : "memory");
+            look();
         }
     }
-    __device__ __forceinline__ void begin(const ScaledParams &p, int64_t row, int64_t col, int kb0, int kb1, int lane)
+    __device__ __forceinline__ void finish()
+    {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        while (behind > 0) look();
+    }
+    __device__ __forceinline__ void look()
+    {
+        float *slot = slots + looking.stage * L::kFloats;
+        __syncwarp();
+        bool fine = true;
+        float row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            row[i] = slot[i * 32 + lane];
+            fine = fine && mild(row[i]);
+        }
+        float c0 = 1.0f, c1 = 1.0f;
+        if (COLS) {
+#pragma unroll
+            for (int i = 0; i < BN; i += 32) fine = fine && mild(slot[L::kCols + i + lane]);
+        } else {
+            c0 = slot[L::kCols];
+            c1 = slot[L::kCols + 1];
+            fine = fine && mild(c0) && mild(c1);
+        }
+        if (!__all_sync(kFull, fine)) c0 = c1 = __uint_as_float(0x7fffffffu);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *to = slot + L::kRow + L::kEach * (i * 32 + lane);
+            if (L::kEach == 2) *reinterpret_cast<float2 *>(to) = make_float2(row[i] * c0, row[i] * c1);
+            else *to = row[i] * c0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full0 + 8u * looking.stage);
+        looking.next();
+        --behind;
+    }
+};
+
+// The sums of one thread: a row of A, CW columns of B.  sb is the block's column scales (COLS), or one for
+// every 64 columns (CW = 128) or for all.
+template <int CW, bool COLS> struct Sums {
+    static constexpr int kChunk = 16, kChunks = CW / kChunk;
+    float2 at[CW / 2];
+
+    __device__ __forceinline__ void clear()
     {
 #pragma unroll
         for (int i = 0; i < CW / 2; ++i) at[i] = make_float2(0.0f, 0.0f);
-        pa = p.sa + ((row < p.M ? row : p.M - 1) >> p.a_shift) * p.sa_mn + kb0 * p.sa_k;
-        step_a = p.sa_k;
-        step_b = p.sb_k;
-        pb = p.sb + kb0 * p.sb_k;
-#pragma unroll
-        for (int i = 0; i < (COLS ? kMine : 1); ++i) {
-            int64_t c = COLS ? col + lane * kMine + i : col;
-            if (c >= p.N) c = p.N - 1;
-            pb_at[i] = (c >> p.b_shift) * p.sb_mn;
-        }
-        left = kb1 - kb0;
-        sa = sa1 = 0.0f;
-        load(sa, sb);
-        load(sa1, sb1);
     }
-    // Adds the block in the accumulator at taddr; `release` is called once it has been read.
-    template <class F> __device__ __forceinline__ void add(uint32_t taddr, float *scratch, int lane, F release)
+    // Adds columns c .. c + 15: v * s * (the columns' scales, COLS).
+    __device__ __forceinline__ void add_chunk(int c, const uint32_t (&v)[kChunk], float s, const float *sb)
     {
-        bool fine = mild(sa);
-#pragma unroll
-        for (int i = 0; i < (COLS ? kMine : 1); ++i) fine = fine && mild(sb[i]);
-        fine = __all_sync(kFull, fine);
-        int ea = 0, eb[kMine] = {};
-        float a = 0.0f, b = 0.0f, m = sa;
-        if (!fine) {
-            m = split(sa, ea);
-#pragma unroll
-            for (int i = 0; i < (COLS ? kMine : 1); ++i) sb[i] = split(sb[i], eb[i]);
-            factors(m * sb[0], ea + eb[0], a, b);  // B's scale is the warp's
-        }
-        int *exponents = reinterpret_cast<int *>(scratch + CW);
         if constexpr (COLS) {
-            __syncwarp();
-            if (kMine * lane < CW) {
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    scratch[lane * kMine + i] = sb[i];
-                    if (!fine) exponents[lane * kMine + i] = eb[i];
-                }
+            for (int i = 0; i < kChunk; i += 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(sb + c + i);
+                float2 &lo = at[(c + i) / 2], &hi = at[(c + i) / 2 + 1];
+                lo = __ffma2_rn(pair_of(v[i], v[i + 1]), __fmul2_rn(make_float2(w.x, w.y), twice(s)), lo);
+                hi = __ffma2_rn(pair_of(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(w.z, w.w), twice(s)), hi);
             }
-            __syncwarp();
+        } else {
+#pragma unroll
+            for (int i = 0; i < kChunk; i += 2) at[(c + i) / 2] = __ffma2_rn(pair_of(v[i], v[i + 1]), twice(s), at[(c + i) / 2]);
         }
-        const float s = COLS ? sa : sa * sb[0];
+    }
+    // Adds the block in the accumulator at taddr; `read` is called once it has been read.  row: of the tile's
+    // 128;  part: the first of the warp's columns;  scratch: 2 * CW floats of the warp's own
+    template <class F>
+    __device__ __forceinline__ void add(uint32_t taddr, const float *slot, int row, int part, float *scratch, int lane, F read)
+    {
+        using L = Slot<COLS, CW == 128>;
         uint32_t r[2][kChunk];
         tmem_start(taddr, r[0]);
-#pragma unroll
-        for (int c = 0; c < CW; c += kChunk) {
-            uint32_t(&v)[kChunk] = r[(c / kChunk) & 1];
-            tmem_arrived(v);
-            if (c + kChunk < CW) tmem_start(taddr + c + kChunk, r[(c / kChunk + 1) & 1]);
-            else release();
-            if (fine) {
-                if constexpr (COLS) {
-#pragma unroll
-                    for (int i = 0; i < kChunk; i += 4) {
-                        const float4 b = *reinterpret_cast<const float4 *>(scratch + c + i);
-                        const float2 lo = __fmul2_rn(make_float2(b.x, b.y), make_float2(s, s));
-                        const float2 hi = __fmul2_rn(make_float2(b.z, b.w), make_float2(s, s));
-                        at[(c + i) / 2] = __ffma2_rn(pair_of(v[i], v[i + 1]), lo, at[(c + i) / 2]);
-                        at[(c + i) / 2 + 1] = __ffma2_rn(pair_of(v[i + 2], v[i + 3]), hi, at[(c + i) / 2 + 1]);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kChunk; i += 2)
-                        at[(c + i) / 2] = __ffma2_rn(pair_of(v[i], v[i + 1]), make_float2(s, s), at[(c + i) / 2]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i) {
-                    if constexpr (COLS) factors(m * scratch[c + i], ea + exponents[c + i], a, b);
-                    float &to = (i & 1) ? at[(c + i) / 2].y : at[(c + i) / 2].x;
-                    to = fmaf(__uint_as_float(v[i]) * a, b, to);
-                }
-            }
+        const float *sb = slot + L::kCols + (COLS ? part : 0);
+        float s0, s1;
+        if (L::kEach == 2) {
+            const float2 t = *reinterpret_cast<const float2 *>(slot + L::kRow + 2 * row);
+            s0 = t.x;
+            s1 = t.y;
+        } else {
+            s0 = s1 = slot[L::kRow + row];
         }
-        sa = sa1;
+        if (__builtin_expect(s0 != s0, 0)) {
+            add_any(taddr, slot[row], sb, scratch, lane);
+            read();
+            return;
+        }
 #pragma unroll
-        for (int i = 0; i < (COLS ? kMine : 1); ++i) sb[i] = sb1[i];
-        load(sa1, sb1);
+        for (int i = 0; i < kChunks; ++i) {
+            tmem_arrived(r[i & 1]);
+            if (i + 1 < kChunks) tmem_start(taddr + (i + 1) * kChunk, r[(i + 1) & 1]);
+            else read();
+            add_chunk(i * kChunk, r[i & 1], CW == 128 && i >= 4 ? s1 : s0, sb);
+        }
+    }
+    // The same for scales of any size: first factors, then second ones.
+    __device__ __forceinline__ void add_any(uint32_t taddr, float s, const float *sb, float *scratch, int lane)
+    {
+        constexpr int kScales = COLS ? CW : 2;
+        const float2 h = halves(s);
+        __syncwarp();  // the block before it has been added
+        for (int i = lane; i < kScales; i += 32) {
+            const float2 f = halves(sb[i]);
+            scratch[i] = f.y;
+            scratch[CW + i] = f.x;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            uint32_t v[kChunk];
+            tmem_start(taddr + i * kChunk, v);
+            tmem_arrived(v);
+            const int run = CW == 128 ? i / 4 : 0;
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j)
+                v[j] = __float_as_uint(__uint_as_float(v[j]) * (h.x * scratch[CW + (COLS ? i * kChunk + j : run)]));
+            add_chunk(i * kChunk, v, COLS ? h.y : h.y * scratch[run], scratch);
+        }
     }
 };
 
@@ -259,17 +324,22 @@ __device__ __forceinline__ uint32_t box_step(int mn) { return (mn ? 32 * 128 : 3
 __device__ __forceinline__ uint32_t f8_idesc(const ScaledParams &p, int n, int m) { return make_idesc(p.a_mn, p.b_mn, n, m) | p.formats; }
 
 // ------------------------------------------------------------------ pairs
-// 256 x 256 tiles; accumulators of 256 columns, two of them.  A slice's MMAs are committed once: the
-// commit on its `empty` barrier tells the producers that its boxes may be overwritten and the adding warps
-// that its accumulator is full.  (A warp that waits for one phase of it cannot miss it: the stage is used
-// again only after the warp has released an accumulator that comes later.)
+// 256 x 256 tiles.  A K block's product is formed in two pieces of 128 columns (64 of either CTA's half of B),
+// each in one of two accumulators, so that while the four warps of one piece read theirs the tensor cores are
+// at the other.  Piece h's column j is column (j / 64) * 128 + 64 h + j % 64 of the tile.
+//
+// The second piece's commit, on the stage's `empty` barrier, tells the producer that the boxes may be
+// overwritten as well as the adding warps that the accumulator is full.  (A warp that waits for one phase of
+// it cannot miss it: the stage is used again only after the warp has released an accumulator that comes later.)
 template <bool COLS> struct PairSmem {
-    static constexpr int kStages = COLS ? 5 : 6, kStage = 2 * kBox;
-    static constexpr int kEpi = kEpiWarps * 4096, kScratch = COLS ? kEpiWarps * 1024 : 0, kBars = 256;
-    static constexpr int kBytes = kStages * kStage + kEpi + kScratch + kBars + 1024;
+    static constexpr int kStages = 5, kStage = 2 * kBox;
+    static constexpr int kSlot = Slot<COLS, true>::kFloats, kSlots = kStages + 3;
+    static constexpr int kEpi = kEpiWarps * 4096, kScratch = kEpiWarps * 2 * 128 * 4, kBars = 512;
+    static constexpr int kBytes = kStages * kStage + kEpi + kScratch + kSlots * kSlot * 4 + kBars + 1024;
     static_assert(kBytes <= 227 * 1024, "one CTA per SM");
     uint32_t ring, bar0;
-    uint8_t *epi, *scratch;
+    uint8_t *epi;
+    float *scratch, *scales;
     volatile uint32_t *tmem_slot;
     volatile int *abort_flag;
     __device__ __forceinline__ explicit PairSmem(uint8_t *raw)
@@ -278,16 +348,19 @@ template <bool COLS> struct PairSmem {
         uint8_t *p = raw + (base - r);
         ring = base;
         epi = p + kStages * kStage;
-        scratch = epi + kEpi;
-        uint8_t *bars = scratch + kScratch;
+        uint8_t *bars = epi + kEpi;
         bar0 = smem_u32(bars);
         tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBars - 16);
         abort_flag = reinterpret_cast<volatile int *>(bars + kBars - 8);
+        scales = reinterpret_cast<float *>(bars + kBars);
+        scratch = scales + kSlots * kSlot;
     }
     __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
     __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
     __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + i); }
-    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 2); }
+    __device__ __forceinline__ uint32_t first_full(int i) const { return bar0 + 8u * (2 * kStages + 4 + i); }
+    __device__ __forceinline__ uint32_t scale_full(int i) const { return bar0 + 8u * (2 * kStages + 6 + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 6 + kSlots); }
     __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
     __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kBox; }
 };
@@ -309,7 +382,9 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             mbar_init(sh.full(s), 1);
             mbar_init(sh.empty(s), 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(sh.acc_empty(i), 2 * kEpiWarps);
+        for (int i = 0; i < 4; ++i) mbar_init(sh.acc_empty(i), kEpiWarps);  // a piece's four warps of both CTAs
+        for (int i = 0; i < 2; ++i) mbar_init(sh.first_full(i), 1);
+        for (int i = 0; i < Smem::kSlots; ++i) mbar_init(sh.scale_full(i), 1);
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -327,7 +402,7 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     bool ok = true;
 
     if (warp < kPairFirst) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         if (warp == 0) {
             // ---------------- producer: this CTA's 128 rows of A and its 128 of the tile's 256 rows of B
             const bool leader = elect_one();
@@ -339,7 +414,7 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             for (int t = first; ok && t < tiles; t += step) {
                 int64_t tm, tn;
                 raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
-                const int m0 = int(tm) * 256 + int(rank) * 128, n0 = int(tn) * 256 + int(rank) * 128;
+                const int m0 = int(tm) * 256 + int(rank) * 128, n0 = int(tn) * 256;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                     if (__any_sync(kFull, !ok)) {
@@ -351,7 +426,7 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
                         if (!(p.inject_stall && kb == 0 && t == first)) {
                             const uint32_t full = full0 + 8u * ring.stage;
                             load_box<true>(sh.a(ring.stage), &map_a, full, p.a_mn, m0, kb);
-                            load_box<true>(sh.b(ring.stage), &map_b, full, p.b_mn, n0, kb);
+                            load_box<true>(sh.b(ring.stage), &map_b, full, p.b_mn, n0 + int(rank) * 128, kb);
                         }
                     }
                     __syncwarp();
@@ -370,76 +445,104 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
                     }
                 }
             }
-        } else if (warp == 1) {
-            if (rank == 0) {
-                // ---------------- MMA issuer
-                const bool leader = elect_one();
-                const uint32_t idesc = f8_idesc(p, 256, 256), step_a = box_step(p.a_mn), step_b = box_step(p.b_mn);
-                const uint64_t a0 = box_desc(sh.a(0)), b0 = box_desc(sh.b(0));
-                int acc = 0;
-                uint32_t acc_phase = 0;
-                for (int t = first; ok && t < tiles; t += step)
-                    for (int kb = 0; kb < p.num_kb; ++kb) {
-                        ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
-                        ok = ok && watch.wait(sh.full(ring.stage), ring.phase);
+        } else if (warp == 2) {
+            // ---------------- scales of this CTA's rows of A and of all the tile's of B
+            ScaleCopies<COLS, true, 256, Smem::kSlots> copies(sh.scales, sh.scale_full(0), lane);
+            for (int t = first; ok && t < tiles; t += step) {
+                int64_t tm, tn;
+                raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                    if (__any_sync(kFull, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    copies.copy(p, tm * 256 + int64_t(rank) * 128, tn * 256, kb);
+                    ring.next();
+                }
+            }
+            copies.finish();
+        } else if (warp == 1 && rank == 0) {
+            // ---------------- MMA issuer
+            const bool leader = elect_one();
+            const uint32_t idesc = f8_idesc(p, 128, 256), step_a = box_step(p.a_mn), step_b = box_step(p.b_mn);
+            const uint64_t a0 = box_desc(sh.a(0)), b0 = box_desc(sh.b(0));
+            const uint32_t piece_b = (p.b_mn ? 64 : 64 * 128) >> 4;  // 64 columns of a box, or 64 rows
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            for (int t = first; ok && t < tiles; t += step)
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    ok = watch.wait(sh.full(ring.stage), ring.phase);
+                    if (!ok) break;
+                    const uint64_t a = a0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+                    const uint64_t b = b0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && watch.wait<true>(sh.acc_empty(2 * acc + h), acc_phase ^ 1u);
                         if (!ok) break;
                         tc_fence_after();
                         if (leader) {
-                            const uint64_t a = a0 + uint32_t(ring.stage * (Smem::kStage >> 4));
-                            const uint64_t b = b0 + uint32_t(ring.stage * (Smem::kStage >> 4));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                umma_f8<true>(tmem + uint32_t(acc * 256), a + k * step_a, b + k * step_b, idesc, k > 0 ? 1u : 0u);
-                            commit_both(sh.empty(ring.stage));
+                                umma_f8<true>(tmem + uint32_t((2 * acc + h) * 128), a + k * step_a, b + h * piece_b + k * step_b, idesc,
+                                              k > 0 ? 1u : 0u);
+                            commit_both(h == 0 ? sh.first_full(acc) : sh.empty(ring.stage));
                         }
                         __syncwarp();
-                        ring.next();
-                        acc ^= 1;
-                        acc_phase ^= acc == 0 ? 1u : 0u;
                     }
-                if (!ok && leader) {  // MMAs in flight finish before TMEM is released
-                    umma_commit<true>(sh.drain());
-                    const volatile int no_abort = 0;
-                    mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
+                    if (!ok) break;
+                    ring.next();
+                    acc ^= 1;
+                    acc_phase ^= acc == 0 ? 1u : 0u;
                 }
+            if (!ok && leader) {  // MMAs in flight finish before TMEM is released
+                umma_commit<true>(sh.drain());
+                const volatile int no_abort = 0;
+                mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;" ::: "memory");
-        // ---------------- adding warps: rows 32 * quarter .. of this CTA's 128, 128 of the 256 columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+        // ---------------- adding warps: rows 32 * quarter .. of this CTA's 128, one piece's columns
         const int quarter = warp & 3, half = (warp - kPairFirst) >> 2;
         Staging<F32> staging(sh.epi + (warp - kPairFirst) * 4096, lane);
-        float *scratch = reinterpret_cast<float *>(sh.scratch + (warp - kPairFirst) * 1024);
-        const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(0), 0);
+        float *scratch = sh.scratch + (warp - kPairFirst) * 2 * 128;
+        const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(half), 0);
         const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * 128);
+        Ring slot(Smem::kSlots);
         int acc = 0;
+        uint32_t acc_phase = 0;
         for (int t = first; ok && t < tiles; t += step) {
             int64_t tm, tn;
             raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
-            const int64_t m0 = tm * 256 + int64_t(rank) * 128 + quarter * 32, n0 = tn * 256 + half * 128;
+            const int64_t m0 = tm * 256 + int64_t(rank) * 128 + quarter * 32, n0 = tn * 256 + half * 64;
             Sums<128, COLS> sums;
-            sums.begin(p, m0 + lane, n0, 0, p.num_kb, lane);
+            sums.clear();
             for (int kb = 0; kb < p.num_kb; ++kb) {
-                ok = watch.wait(sh.empty(ring.stage), ring.phase);
-                ok = __all_sync(kFull, ok);
+                ok = wait_both(watch, sh.scale_full(slot.stage), slot.phase, half == 0 ? sh.first_full(acc) : sh.empty(ring.stage),
+                               half == 0 ? acc_phase : ring.phase);
                 if (!ok) break;
                 tc_fence_after();
-                sums.add(taddr0 + uint32_t(acc * 256), scratch, lane, [&] { release_accumulator(acc_empty0 + 8u * acc, lane); });
+                sums.add(taddr0 + uint32_t(acc * 256), sh.scales + slot.stage * Smem::kSlot, quarter * 32 + lane, half * 128, scratch, lane,
+                         [&] { release_accumulator(acc_empty0 + 16u * acc, lane); });
                 ring.next();
+                slot.next();
                 acc ^= 1;
+                acc_phase ^= acc == 0 ? 1u : 0u;
             }
             if (!ok) break;
             if (m0 >= p.M) continue;
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
-                if (n0 + c >= p.N) break;
+                const int64_t n = n0 + (c / 64) * 128 + c % 64;
+                if (n >= p.N) break;
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     v[2 * i] = sums.at[c / 2 + i].x;
                     v[2 * i + 1] = sums.at[c / 2 + i].y;
                 }
-                store_rows(staging, v, &map_c, p.c_tma != 0, p.C, p.ldc, m0, n0 + c, p.M, p.N, p.c_type == GEMM_TYPE_BF16, 0);
+                store_rows(staging, v, &map_c, p.c_tma != 0, p.C, p.ldc, m0, n, p.M, p.N, p.c_type == GEMM_TYPE_BF16, 0);
             }
         }
         staging.finish();
@@ -456,14 +559,17 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 // One CTA: 128 rows of A, BN of B, the K blocks of its rank in the cluster.
 template <int BN> struct TileSmem {
     static constexpr int kCtas = BN == 128 ? 1 : 2;  // an SM: 128 columns take too many registers for two
-    static constexpr int kStage = kBox + BN * 128, kStages = BN == 128 ? 6 : BN == 64 ? 4 : 5;
+    static constexpr int kAdders = BN == 128 ? 8 : 4, kFirst = 3, kThreads = 32 * (kFirst + kAdders);
+    static constexpr int kStage = kBox + BN * 128, kStages = BN == 128 ? 6 : 4;
     static constexpr int kBuffers = 4, kTmem = BN * kBuffers;
     static constexpr int kRow = BN + 4;  // floats of a row of sums: 16-byte stores by rows without bank conflicts
-    static constexpr int kBars = 256, kScratch = kEpiWarps * 512;
-    static constexpr int kBytes = kStages * kStage + kScratch + kBars + 1024;
+    static constexpr int kSlot = Slot<true, false>::kFloats > Slot<false, false>::kFloats ? Slot<true, false>::kFloats : Slot<false, false>::kFloats;
+    static constexpr int kSlots = kStages + kBuffers + 1;
+    static constexpr int kBars = 512, kScratch = 2 * 4 * BN * 4;
+    static constexpr int kBytes = kStages * kStage + kScratch + kSlots * kSlot * 4 + kBars + 1024;
     static_assert(128 * kRow * 4 <= kStages * kStage && kCtas * (kBytes + 1024) <= 228 * 1024, "CTAs per SM");
     uint32_t ring, bar0;
-    uint8_t *scratch;
+    float *scratch, *scales;
     float *sums;  // in the ring's place, once it is empty
     volatile uint32_t *tmem_slot;
     volatile int *abort_flag;
@@ -473,16 +579,18 @@ template <int BN> struct TileSmem {
         uint8_t *p = raw + (base - r);
         ring = base;
         sums = reinterpret_cast<float *>(p);
-        scratch = p + kStages * kStage;
-        uint8_t *bars = scratch + kScratch;
+        uint8_t *bars = p + kStages * kStage;
         bar0 = smem_u32(bars);
         tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBars - 16);
         abort_flag = reinterpret_cast<volatile int *>(bars + kBars - 8);
+        scales = reinterpret_cast<float *>(bars + kBars);
+        scratch = scales + kSlots * kSlot;
     }
     __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
     __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
     __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + i); }
-    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + kBuffers); }
+    __device__ __forceinline__ uint32_t scale_full(int i) const { return bar0 + 8u * (2 * kStages + kBuffers + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + kBuffers + kSlots); }
     __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
     __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kBox; }
 };
@@ -514,7 +622,7 @@ __device__ __forceinline__ void store_tile(const ScaledParams &p, const float *s
 #pragma unroll
     for (int s = 0; s < 8; ++s) base[s] = s < p.splits ? map_to_rank(smem_u32(sums), uint32_t(s)) : 0u;
     T *C = static_cast<T *>(p.C);
-    for (int i = threadIdx.x; i < height * BN / 4; i += kThreads) {
+    for (int i = threadIdx.x; i < height * BN / 4; i += TileSmem<BN>::kThreads) {
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         int row, col;  // of the piece: four columns of a row, or transposed four rows of a column
         if (p.transposed) {
@@ -551,7 +659,7 @@ __device__ __forceinline__ void store_tile(const ScaledParams &p, const float *s
 }
 
 template <int BN, bool COLS>
-__global__ void __launch_bounds__(kThreads, TileSmem<BN>::kCtas)
+__global__ void __launch_bounds__(TileSmem<BN>::kThreads, TileSmem<BN>::kCtas)
 scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ ScaledParams p)
 {
@@ -565,7 +673,8 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             mbar_init(sh.full(s), 1);
             mbar_init(sh.empty(s), 1);
         }
-        for (int i = 0; i < Smem::kBuffers; ++i) mbar_init(sh.acc_empty(i), kEpiWarps);
+        for (int i = 0; i < Smem::kBuffers; ++i) mbar_init(sh.acc_empty(i), Smem::kAdders);
+        for (int i = 0; i < Smem::kSlots; ++i) mbar_init(sh.scale_full(i), 1);
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -643,27 +752,39 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             const volatile int no_abort = 0;
             mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
         }
-    } else {
-        // ---------------- adding warps: rows 32 * quarter .., half of the columns
-        constexpr int kWide = BN / 2;
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        float *scratch = reinterpret_cast<float *>(sh.scratch + (warp - 2) * 512);
-        const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * kWide);
-        int acc = 0;
-        Sums<kWide, COLS> sums;
-        sums.begin(p, m0 + quarter * 32 + lane, n0 + half * kWide, kb0, kb1, lane);
+    } else if (warp == 2) {
+        // ---------------- scales
+        ScaleCopies<COLS, false, BN, Smem::kSlots> copies(sh.scales, sh.scale_full(0), lane);
         for (int kb = kb0; kb < kb1; ++kb) {
-            ok = watch.wait(sh.empty(ring.stage), ring.phase);
-            ok = __all_sync(kFull, ok);
+            ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+            if (__any_sync(kFull, !ok)) break;
+            copies.copy(p, m0, n0, kb);
+            ring.next();
+        }
+        copies.finish();
+    } else {
+        // ---------------- adding warps: rows 32 * quarter .., all of the columns or half of them
+        constexpr int kWide = BN * 4 / Smem::kAdders;
+        const int quarter = warp & 3, half = (warp - Smem::kFirst) >> 2;
+        float *scratch = sh.scratch + (warp - Smem::kFirst) * 2 * kWide;
+        const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * kWide);
+        Ring slot(Smem::kSlots), acc(Smem::kBuffers);
+        Sums<kWide, COLS> sums;
+        sums.clear();
+        using L = Slot<COLS, false>;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = wait_both(watch, sh.scale_full(slot.stage), slot.phase, sh.empty(ring.stage), ring.phase);
             if (!ok) break;
             tc_fence_after();
-            sums.add(taddr0 + uint32_t(acc * BN), scratch, lane, [&] {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sh.acc_empty(acc));
-            });
+            sums.add(taddr0 + uint32_t(acc.stage * BN), sh.scales + slot.stage * L::kFloats, quarter * 32 + lane, half * kWide, scratch, lane,
+                     [&] {
+                         tc_fence_before();
+                         __syncwarp();
+                         if (lane == 0) mbar_arrive(sh.acc_empty(acc.stage));
+                     });
             ring.next();
-            acc = acc + 1 == Smem::kBuffers ? 0 : acc + 1;
+            slot.next();
+            acc.next();
         }
         // every copy has landed and every MMA has been read: the ring's memory takes the sums
         if (ok) {
@@ -767,7 +888,7 @@ cudaError_t launch_tiles(const ScaledArgs &a, int splits, int transposed, unsign
     if (!operand_map(&ma, a.a, a.M, a.K, 128) || !operand_map(&mb, a.b, a.N, a.K, BN)) return cudaErrorInvalidValue;
     const int64_t ctas = int64_t(p.tiles_m) * p.tiles_n * splits;
     if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    return launch_chained(kernel, dim3(unsigned(ctas)), kThreads, Smem::kBytes, splits, stream, ma, mb, p);
+    return launch_chained(kernel, dim3(unsigned(ctas)), Smem::kThreads, Smem::kBytes, splits, stream, ma, mb, p);
 }
 
 template <int BN>
