@@ -111,21 +111,20 @@ __device__ __forceinline__ float2 pair_of(uint32_t x, uint32_t y) { return make_
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
 // ------------------------------------------------------------------ scales
-// A K block's scales pass through shared memory, in slots of their own: one warp copies them (cp.async, any
-// strides) as the ring's stages become free, looks at a block's when the copies of the kDelay blocks behind it
-// are on their way, and announces it.  (With loads to the adding warps' registers one or two blocks ahead a
-// block took 750 SM cycles whatever its size; with those warps looking at them 400 more than now.)
-//
-// There is no barrier for a slot's release: a stage is free once the MMAs of its block b have completed, for
-// which the adding warps must have read block b - (accumulators) and so have added the one before that; a
-// slot is used again stages + accumulators + 1 blocks later at the earliest.
-constexpr int kDelay = 3;
-
-// Waits for two phases, all lanes with one answer; where both are there already this costs a vote.
-__device__ __forceinline__ bool wait_both(const Watch &watch, uint32_t bar0, uint32_t phase0, uint32_t bar1, uint32_t phase1)
+// A K block's scales pass through shared memory, in slots of their own: one warp or two copy them (cp.async,
+// any strides), look at a block's when those of a few blocks behind it are on their way, and announce it.
+// (With loads to the adding warps' registers one or two blocks ahead a block took 750 SM cycles whatever its
+// size; with those warps looking at them 400 more than now; one warp for a pair's scales took 850 a block.)
+// The adding warps release a block's slot when they have read the next block.  The ring's barriers would not
+// do: the MMAs do not wait for scales, so a stage's barrier could complete twice before this warp looks.
+// Whether two phases are complete, and a wait for both: all lanes with one answer.
+__device__ __forceinline__ bool both_there(uint32_t bar0, uint32_t phase0, uint32_t bar1, uint32_t phase1)
 {
     const bool there = mbar_try_wait(bar0, phase0) & mbar_try_wait(bar1, phase1);
-    if (__builtin_expect(__all_sync(kFull, there), 1)) return true;
+    return __all_sync(kFull, there) != 0;
+}
+__device__ __forceinline__ bool wait_both(const Watch &watch, uint32_t bar0, uint32_t phase0, uint32_t bar1, uint32_t phase1)
+{
     const bool got = watch.wait(bar0, phase0) && watch.wait(bar1, phase1);
     return __all_sync(kFull, got) != 0;
 }
@@ -143,46 +142,63 @@ __device__ __forceinline__ void copy_scale(float *dst, const float *src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ int64_t scale_row(int64_t row, int64_t rows) { return row < rows ? row : rows - 1; }
-// The scales of COUNT rows from row0 for block kb (rows outside the matrix take the last one's).
-template <int COUNT>
-__device__ __forceinline__ void copy_scales(float *dst, const float *scales, int64_t s_mn, int64_t s_k, int shift, int64_t row0,
-                                            int64_t rows, int kb, int lane)
-{
-#pragma unroll
-    for (int i = 0; i < COUNT; i += 32)
-        copy_scale(dst + i + lane, scales + (scale_row(row0 + i + lane, rows) >> shift) * s_mn + kb * s_k);
-}
 
-// The warp that handles a tile's scales.  BN: columns of the tile.
-template <bool COLS, bool PAIRS, int BN, int SLOTS> struct ScaleCopies {
+// A warp that handles a tile's scales: one block in STEP.  BN: columns of the tile;  DELAY: of its blocks that
+// are on their way while it looks at one.
+template <bool COLS, bool PAIRS, int BN, int SLOTS, int STEP, int DELAY> struct ScaleCopies {
     using L = Slot<COLS, PAIRS>;
+    static constexpr int kColumns = COLS ? BN / 32 : 1;
+    static_assert(SLOTS % STEP == 0, "every warp has slots of its own");
     float *slots;
-    uint32_t full0;  // barriers of the slots, one arrival each
-    int lane;
-    Ring copying{SLOTS}, looking{SLOTS};
-    int behind = 0;
+    uint32_t full0, empty0;  // barriers of the slots, one arrival each and the adding warps'
+    int lane, copying, looking, behind = 0;
+    uint32_t phase = 1;  // of the slots' release
+    const float *rows[4], *columns[kColumns];  // of the next block
+    int64_t step_a, step_b;
 
-    __device__ __forceinline__ ScaleCopies(float *s, uint32_t bars, int l) : slots(s), full0(bars), lane(l) {}
-    __device__ __forceinline__ void copy(const ScaledParams &p, int64_t m0, int64_t n0, int kb)
+    __device__ __forceinline__ ScaleCopies(float *s, uint32_t full, uint32_t empty, int l, int first)
+        : slots(s), full0(full), empty0(empty), lane(l), copying(first), looking(first)
     {
-        float *slot = slots + copying.stage * L::kFloats;
-        copy_scales<128>(slot, p.sa, p.sa_mn, p.sa_k, p.a_shift, m0, p.M, kb, lane);
-        if (COLS && PAIRS) {
-            // a piece's columns side by side: 64 from column 64 h of the tile, 64 from column 128 + 64 h
+    }
+    // The tile's rows of scales (rows outside the matrix take the last one's), from block kb.
+    __device__ __forceinline__ void begin(const ScaledParams &p, int64_t m0, int64_t n0, int kb)
+    {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                copy_scales<64>(slot + L::kCols + 64 * i, p.sb, p.sb_mn, p.sb_k, p.b_shift, n0 + (i & 1) * 128 + (i >> 1) * 64, p.N, kb, lane);
-        } else if (COLS) {
-            copy_scales<BN>(slot + L::kCols, p.sb, p.sb_mn, p.sb_k, p.b_shift, n0, p.N, kb, lane);
-        } else if (lane < 2) {
-            copy_scale(slot + L::kCols + lane, p.sb + (scale_row(n0 + (PAIRS ? 128 * lane : 0), p.N) >> p.b_shift) * p.sb_mn + kb * p.sb_k);
+        for (int i = 0; i < 4; ++i) rows[i] = p.sa + (scale_row(m0 + i * 32 + lane, p.M) >> p.a_shift) * p.sa_mn + kb * p.sa_k;
+#pragma unroll
+        for (int i = 0; i < kColumns; ++i) {
+            // PAIRS: a piece's columns side by side: 64 from column 64 h of the tile, 64 from column 128 + 64 h
+            const int at = !COLS ? (PAIRS ? 128 * (lane & 1) : 0) : PAIRS ? (i & 1) * 32 + (i >> 1 & 1) * 128 + (i >> 2) * 64 : i * 32;
+            columns[i] = p.sb + (scale_row(n0 + at + (COLS ? lane : 0), p.N) >> p.b_shift) * p.sb_mn + kb * p.sb_k;
+        }
+        step_a = STEP * p.sa_k;
+        step_b = STEP * p.sb_k;
+    }
+    __device__ __forceinline__ bool copy(const Watch &watch)
+    {
+        if (!__all_sync(kFull, watch.wait(empty0 + 8u * copying, phase))) return false;
+        float *slot = slots + copying * L::kFloats;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            copy_scale(slot + i * 32 + lane, rows[i]);
+            rows[i] += step_a;
+        }
+#pragma unroll
+        for (int i = 0; i < kColumns; ++i) {
+            if (COLS || lane < 2) copy_scale(slot + L::kCols + i * 32 + lane, columns[i]);
+            columns[i] += step_b;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        copying.next();
-        if (++behind > kDelay) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kDelay) : "memory");
+        copying += STEP;
+        if (copying >= SLOTS) {
+            copying -= SLOTS;
+            phase ^= 1u;
+        }
+        if (++behind > DELAY) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(DELAY) : "memory");
             look();
         }
+        return true;
     }
     __device__ __forceinline__ void finish()
     {
@@ -191,7 +207,7 @@ template <bool COLS, bool PAIRS, int BN, int SLOTS> struct ScaleCopies {
     }
     __device__ __forceinline__ void look()
     {
-        float *slot = slots + looking.stage * L::kFloats;
+        float *slot = slots + looking * L::kFloats;
         __syncwarp();
         bool fine = true;
         float row[4];
@@ -217,8 +233,8 @@ template <bool COLS, bool PAIRS, int BN, int SLOTS> struct ScaleCopies {
             else *to = row[i] * c0;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(full0 + 8u * looking.stage);
-        looking.next();
+        if (lane == 0) mbar_arrive(full0 + 8u * looking);
+        looking = looking + STEP >= SLOTS ? looking + STEP - SLOTS : looking + STEP;
         --behind;
     }
 };
@@ -250,10 +266,11 @@ template <int CW, bool COLS> struct Sums {
             for (int i = 0; i < kChunk; i += 2) at[(c + i) / 2] = __ffma2_rn(pair_of(v[i], v[i + 1]), twice(s), at[(c + i) / 2]);
         }
     }
-    // Adds the block in the accumulator at taddr; `read` is called once it has been read.  row: of the tile's
-    // 128;  part: the first of the warp's columns;  scratch: 2 * CW floats of the warp's own
-    template <class F>
-    __device__ __forceinline__ void add(uint32_t taddr, const float *slot, int row, int part, float *scratch, int lane, F read)
+    // Adds the block in the accumulator at taddr.  row: of the tile's 128;  part: the first of the warp's
+    // columns;  scratch: 2 * CW floats of the warp's own.  `peek` is called while its last columns are on their
+    // way (the answer to whether the next block is there takes as long), `read` once it has been read.
+    template <class Peek, class Read>
+    __device__ __forceinline__ void add(uint32_t taddr, const float *slot, int row, int part, float *scratch, int lane, Peek peek, Read read)
     {
         using L = Slot<COLS, CW == 128>;
         uint32_t r[2][kChunk];
@@ -270,6 +287,7 @@ template <int CW, bool COLS> struct Sums {
         if (__builtin_expect(s0 != s0, 0)) {
             add_any(taddr, slot[row], sb, scratch, lane);
             read();
+            peek();
             return;
         }
 #pragma unroll
@@ -277,6 +295,7 @@ template <int CW, bool COLS> struct Sums {
             tmem_arrived(r[i & 1]);
             if (i + 1 < kChunks) tmem_start(taddr + (i + 1) * kChunk, r[(i + 1) & 1]);
             else read();
+            if (i + 2 == kChunks || kChunks == 1) peek();
             add_chunk(i * kChunk, r[i & 1], CW == 128 && i >= 4 ? s1 : s0, sb);
         }
     }
@@ -333,7 +352,7 @@ __device__ __forceinline__ uint32_t f8_idesc(const ScaledParams &p, int n, int m
 // it cannot miss it: the stage is used again only after the warp has released an accumulator that comes later.)
 template <bool COLS> struct PairSmem {
     static constexpr int kStages = 5, kStage = 2 * kBox;
-    static constexpr int kSlot = Slot<COLS, true>::kFloats, kSlots = kStages + 3;
+    static constexpr int kSlot = Slot<COLS, true>::kFloats, kSlots = 8;
     static constexpr int kEpi = kEpiWarps * 4096, kScratch = kEpiWarps * 2 * 128 * 4, kBars = 512;
     static constexpr int kBytes = kStages * kStage + kEpi + kScratch + kSlots * kSlot * 4 + kBars + 1024;
     static_assert(kBytes <= 227 * 1024, "one CTA per SM");
@@ -360,7 +379,8 @@ template <bool COLS> struct PairSmem {
     __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + i); }
     __device__ __forceinline__ uint32_t first_full(int i) const { return bar0 + 8u * (2 * kStages + 4 + i); }
     __device__ __forceinline__ uint32_t scale_full(int i) const { return bar0 + 8u * (2 * kStages + 6 + i); }
-    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 6 + kSlots); }
+    __device__ __forceinline__ uint32_t scale_empty(int i) const { return bar0 + 8u * (2 * kStages + 6 + kSlots + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 6 + 2 * kSlots); }
     __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
     __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kBox; }
 };
@@ -384,7 +404,10 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         }
         for (int i = 0; i < 4; ++i) mbar_init(sh.acc_empty(i), kEpiWarps);  // a piece's four warps of both CTAs
         for (int i = 0; i < 2; ++i) mbar_init(sh.first_full(i), 1);
-        for (int i = 0; i < Smem::kSlots; ++i) mbar_init(sh.scale_full(i), 1);
+        for (int i = 0; i < Smem::kSlots; ++i) {
+            mbar_init(sh.scale_full(i), 1);
+            mbar_init(sh.scale_empty(i), kEpiWarps);
+        }
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -445,21 +468,17 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
                     }
                 }
             }
-        } else if (warp == 2) {
-            // ---------------- scales of this CTA's rows of A and of all the tile's of B
-            ScaleCopies<COLS, true, 256, Smem::kSlots> copies(sh.scales, sh.scale_full(0), lane);
+        } else if (warp >= 2) {
+            // ---------------- scales of this CTA's rows of A and of all the tile's of B: two warps, in turn
+            const int mine = warp - 2;
+            ScaleCopies<COLS, true, 256, Smem::kSlots, 2, 1> copies(sh.scales, sh.scale_full(0), sh.scale_empty(0), lane, mine);
+            int turn = 0;
             for (int t = first; ok && t < tiles; t += step) {
                 int64_t tm, tn;
                 raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                    if (__any_sync(kFull, !ok)) {
-                        ok = false;
-                        break;
-                    }
-                    copies.copy(p, tm * 256 + int64_t(rank) * 128, tn * 256, kb);
-                    ring.next();
-                }
+                copies.begin(p, tm * 256 + int64_t(rank) * 128, tn * 256, turn ^ mine);
+                for (int kb = 0; ok && kb < p.num_kb; ++kb, turn ^= 1)
+                    if (turn == mine) ok = copies.copy(watch);
             }
             copies.finish();
         } else if (warp == 1 && rank == 0) {
@@ -510,7 +529,7 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         const uint32_t acc_empty0 = map_to_rank(sh.acc_empty(half), 0);
         const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * 128);
         Ring slot(Smem::kSlots);
-        int acc = 0;
+        int acc = 0, added = -1;  // added: the slot of the block before
         uint32_t acc_phase = 0;
         for (int t = first; ok && t < tiles; t += step) {
             int64_t tm, tn;
@@ -518,17 +537,29 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             const int64_t m0 = tm * 256 + int64_t(rank) * 128 + quarter * 32, n0 = tn * 256 + half * 64;
             Sums<128, COLS> sums;
             sums.clear();
+            bool there = false;
             for (int kb = 0; kb < p.num_kb; ++kb) {
-                ok = wait_both(watch, sh.scale_full(slot.stage), slot.phase, half == 0 ? sh.first_full(acc) : sh.empty(ring.stage),
-                               half == 0 ? acc_phase : ring.phase);
+                // of the next block: its slot, and the barrier and phase of its accumulator
+                auto scales = [&] { return sh.scale_full(slot.stage); };
+                auto full = [&] { return half == 0 ? sh.first_full(acc) : sh.empty(ring.stage); };
+                auto phase = [&] { return half == 0 ? acc_phase : ring.phase; };
+                if (!there) ok = wait_both(watch, scales(), slot.phase, full(), phase());
                 if (!ok) break;
                 tc_fence_after();
-                sums.add(taddr0 + uint32_t(acc * 256), sh.scales + slot.stage * Smem::kSlot, quarter * 32 + lane, half * 128, scratch, lane,
-                         [&] { release_accumulator(acc_empty0 + 16u * acc, lane); });
+                const float *at = sh.scales + slot.stage * Smem::kSlot;
+                const int now = acc, reading = slot.stage;
                 ring.next();
                 slot.next();
                 acc ^= 1;
                 acc_phase ^= acc == 0 ? 1u : 0u;
+                sums.add(
+                    taddr0 + uint32_t(now * 256), at, quarter * 32 + lane, half * 128, scratch, lane,
+                    [&] { there = kb + 1 < p.num_kb && both_there(scales(), slot.phase, full(), phase()); },
+                    [&] {
+                        release_accumulator(acc_empty0 + 16u * now, lane);
+                        if (lane == 0 && added >= 0) mbar_arrive(sh.scale_empty(added));
+                        added = reading;
+                    });
             }
             if (!ok) break;
             if (m0 >= p.M) continue;
@@ -564,7 +595,7 @@ template <int BN> struct TileSmem {
     static constexpr int kBuffers = 4, kTmem = BN * kBuffers;
     static constexpr int kRow = BN + 4;  // floats of a row of sums: 16-byte stores by rows without bank conflicts
     static constexpr int kSlot = Slot<true, false>::kFloats > Slot<false, false>::kFloats ? Slot<true, false>::kFloats : Slot<false, false>::kFloats;
-    static constexpr int kSlots = kStages + kBuffers + 1;
+    static constexpr int kSlots = 8;
     static constexpr int kBars = 512, kScratch = 2 * 4 * BN * 4;
     static constexpr int kBytes = kStages * kStage + kScratch + kSlots * kSlot * 4 + kBars + 1024;
     static_assert(128 * kRow * 4 <= kStages * kStage && kCtas * (kBytes + 1024) <= 228 * 1024, "CTAs per SM");
@@ -590,7 +621,8 @@ template <int BN> struct TileSmem {
     __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
     __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + i); }
     __device__ __forceinline__ uint32_t scale_full(int i) const { return bar0 + 8u * (2 * kStages + kBuffers + i); }
-    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + kBuffers + kSlots); }
+    __device__ __forceinline__ uint32_t scale_empty(int i) const { return bar0 + 8u * (2 * kStages + kBuffers + kSlots + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + kBuffers + 2 * kSlots); }
     __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
     __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kBox; }
 };
@@ -674,7 +706,10 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             mbar_init(sh.empty(s), 1);
         }
         for (int i = 0; i < Smem::kBuffers; ++i) mbar_init(sh.acc_empty(i), Smem::kAdders);
-        for (int i = 0; i < Smem::kSlots; ++i) mbar_init(sh.scale_full(i), 1);
+        for (int i = 0; i < Smem::kSlots; ++i) {
+            mbar_init(sh.scale_full(i), 1);
+            mbar_init(sh.scale_empty(i), Smem::kAdders);
+        }
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -754,13 +789,9 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         }
     } else if (warp == 2) {
         // ---------------- scales
-        ScaleCopies<COLS, false, BN, Smem::kSlots> copies(sh.scales, sh.scale_full(0), lane);
-        for (int kb = kb0; kb < kb1; ++kb) {
-            ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-            if (__any_sync(kFull, !ok)) break;
-            copies.copy(p, m0, n0, kb);
-            ring.next();
-        }
+        ScaleCopies<COLS, false, BN, Smem::kSlots, 1, 2> copies(sh.scales, sh.scale_full(0), sh.scale_empty(0), lane, 0);
+        copies.begin(p, m0, n0, kb0);
+        for (int kb = kb0; ok && kb < kb1; ++kb) ok = copies.copy(watch);
         copies.finish();
     } else {
         // ---------------- adding warps: rows 32 * quarter .., all of the columns or half of them
@@ -769,22 +800,32 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         float *scratch = sh.scratch + (warp - Smem::kFirst) * 2 * kWide;
         const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * kWide);
         Ring slot(Smem::kSlots), acc(Smem::kBuffers);
+        int added = -1;  // the slot of the block before
         Sums<kWide, COLS> sums;
         sums.clear();
         using L = Slot<COLS, false>;
+        bool there = false;
         for (int kb = kb0; kb < kb1; ++kb) {
-            ok = wait_both(watch, sh.scale_full(slot.stage), slot.phase, sh.empty(ring.stage), ring.phase);
+            if (!there) ok = wait_both(watch, sh.scale_full(slot.stage), slot.phase, sh.empty(ring.stage), ring.phase);
             if (!ok) break;
             tc_fence_after();
-            sums.add(taddr0 + uint32_t(acc.stage * BN), sh.scales + slot.stage * L::kFloats, quarter * 32 + lane, half * kWide, scratch, lane,
-                     [&] {
-                         tc_fence_before();
-                         __syncwarp();
-                         if (lane == 0) mbar_arrive(sh.acc_empty(acc.stage));
-                     });
+            const float *at = sh.scales + slot.stage * L::kFloats;
+            const int now = acc.stage, reading = slot.stage;
             ring.next();
             slot.next();
             acc.next();
+            sums.add(
+                taddr0 + uint32_t(now * BN), at, quarter * 32 + lane, half * kWide, scratch, lane,
+                [&] { there = kb + 1 < kb1 && both_there(sh.scale_full(slot.stage), slot.phase, sh.empty(ring.stage), ring.phase); },
+                [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(sh.acc_empty(now));
+                        if (added >= 0) mbar_arrive(sh.scale_empty(added));
+                    }
+                    added = reading;
+                });
         }
         // every copy has landed and every MMA has been read: the ring's memory takes the sums
         if (ok) {
