@@ -22,13 +22,6 @@ constexpr int kThreads = 256;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 1, kColumns = 2, kTiles = 4;
 
-// |x| for the maximum of a block; infinities and NaN take no part.
-__device__ __forceinline__ float magnitude(float x)
-{
-    const float a = fabsf(x);
-    return a <= FLT_MAX ? a : 0.0f;
-}
-
 // The power of two with max <= s * 1.75 * 2^top, top the exponent of the type's largest value 1.75 * 2^top:
 // its biased exponent, at least 1 (2^-126); 127 (a scale of 1) for a block of zeros.
 __device__ __forceinline__ uint32_t scale_exponent(float max, int top)
@@ -40,26 +33,61 @@ __device__ __forceinline__ uint32_t scale_exponent(float max, int top)
 }
 __device__ __forceinline__ float power(uint32_t exponent) { return __uint_as_float(exponent << 23); }
 
-// Eight values times the reciprocal scale 2^(127 - exponent) as 8-bit codes.  An infinity is stored as NaN
-// like NaN itself: neither turns finite, e4m3 has no infinity.
-__device__ __forceinline__ uint2 codes(const float (&v)[8], const uint32_t (&exponent)[8], bool e5m2)
+// Eight consecutive elements of a row as they are in memory (16-bit types take half the registers of floats),
+// and as floats.  left: elements before the row's end.
+template <class T> struct Piece {
+    uint4 u[sizeof(T) / 2];
+    template <bool WHOLE> __device__ __forceinline__ void load(const T *p, int64_t left, bool wide)
+    {
+        if (WHOLE || (wide && left >= 8)) {
+#pragma unroll
+            for (int i = 0; i < int(sizeof(T) / 2); ++i) u[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        } else {
+            T *e = reinterpret_cast<T *>(u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : from_f32<T>(0.0f);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        const T *e = reinterpret_cast<const T *>(u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+    }
+};
+
+// The largest magnitude (fmaxf passes over NaN).
+__device__ __forceinline__ float largest(const float (&v)[8])
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+// Eight values times 2^(127 - exponent) as 8-bit codes.  An infinity is stored as NaN like NaN itself: neither
+// turns finite, e4m3 has no infinity.  infinite: whether there may be one.
+template <bool E5M2, class Exponent> __device__ __forceinline__ uint2 codes(const float (&v)[8], bool infinite, Exponent exponent)
 {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 f;
-        f.x = v[2 * i] * power(254u - exponent[2 * i]);
-        f.y = v[2 * i + 1] * power(254u - exponent[2 * i + 1]);
-        if (!(fabsf(f.x) <= FLT_MAX)) f.x = __uint_as_float(0x7fffffffu);
-        if (!(fabsf(f.y) <= FLT_MAX)) f.y = __uint_as_float(0x7fffffffu);
-        w[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+        const float2 by = make_float2(power(254u - exponent(2 * i)), power(254u - exponent(2 * i + 1)));
+        const float2 f = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), by);
+        w[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
+    }
+    if (__builtin_expect(infinite, 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (fabsf(v[2 * i]) > FLT_MAX) w[i] |= 0x7fu;
+            if (fabsf(v[2 * i + 1]) > FLT_MAX) w[i] |= 0x7f00u;
+        }
     }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-__device__ __forceinline__ void put_codes(uint8_t *q, uint2 w, int64_t left)
+template <bool WHOLE> __device__ __forceinline__ void put_codes(uint8_t *q, uint2 w, int64_t left)
 {
-    if (left >= 8) {
+    if (WHOLE || left >= 8) {
         *reinterpret_cast<uint2 *>(q) = w;
     } else {
         const uint64_t u = uint64_t(w.y) << 32 | w.x;
@@ -74,103 +102,144 @@ struct QuantizeParams {
     const void *X;
     uint8_t *Q, *Qc;
     Scales s, sc;
-    int col_blocks, wide, e5m2;
+    int col_blocks, wide;
 };
 
-// Thread (x, y) = (t % 16, t / 16): 8 columns of the rows y, y + 16, .. of a tile of 16 * I rows.  MODE: the
-// sum of the ways.  Blocks of 1 x 128 alone do not need a tile's height: few rows take I = 1, for more CTAs.
-template <class T, int MODE, int I>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantizeParams p)
+struct QuantizeSpace {
+    float column_max[16][128];
+    uint32_t column_exponent[128];
+    float warp_max[kThreads / 32];
+};
+
+// One tile.  WHOLE: it lies inside the matrix and its rows are read in 16-byte pieces.
+template <class T, int MODE, int I, bool E5M2, bool WHOLE>
+__device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t rb, int64_t cb, QuantizeSpace &space)
 {
-    __shared__ float column_max[MODE & kColumns ? 16 : 1][128];
-    __shared__ uint32_t column_exponent[128];
-    __shared__ float warp_max[kThreads / 32];
-    chain_wait();
-    const int x = threadIdx.x & 15, y = threadIdx.x >> 4, top = p.e5m2 ? 15 : 8;
-    const int64_t rb = blockIdx.x / unsigned(p.col_blocks), cb = blockIdx.x % unsigned(p.col_blocks);
+    constexpr int kTop = E5M2 ? 15 : 8;
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
     const int64_t r0 = rb * (16 * I) + y, c = cb * 128 + x * 8, left = p.cols - c;
     const T *src = static_cast<const T *>(p.X) + r0 * p.ldx + c;
-    float v[I][8];
+    Piece<T> piece[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+        piece[i].template load<WHOLE>(src + int64_t(16 * i) * p.ldx, WHOLE || r0 + 16 * i < p.rows ? left : 0, p.wide);
+    auto inside = [&](int i) { return WHOLE || (r0 + 16 * i < p.rows && left > 0); };
+    // an infinity in this thread's pieces shows in the first look, and is left out in a second one
+    float row[I], column[8];
+    bool infinite = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) column[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-        const bool in = r0 + 16 * i < p.rows;
-        if (in && p.wide && left >= 8) {
-            load8<T>(src + int64_t(16 * i) * p.ldx, v[i]);
-        } else {
+        float v[8];
+        piece[i].get(v);
+        row[i] = largest(v);
+        infinite = infinite || row[i] > FLT_MAX;
+        if ((MODE & kColumns) != 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = in && j < left ? to_f32(src[int64_t(16 * i) * p.ldx + j]) : 0.0f;
+            for (int j = 0; j < 8; ++j) column[j] = fmaxf(column[j], fabsf(v[j]));
+        }
+    }
+    if (__builtin_expect(infinite, 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) column[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            float v[8];
+            piece[i].get(v);
+            row[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float a = fabsf(v[j]) <= FLT_MAX ? fabsf(v[j]) : 0.0f;
+                row[i] = fmaxf(row[i], a);
+                column[j] = fmaxf(column[j], a);
+            }
         }
     }
     if constexpr ((MODE & kRows) != 0) {
+        float most[I];
+#pragma unroll
+        for (int i = 0; i < I; ++i) most[i] = row[i];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < I; ++i) most[i] = fmaxf(most[i], __shfl_xor_sync(kFull, most[i], o));
+        uint8_t *q = p.Q + r0 * p.ldq + c;
+        float *at = p.s.at + r0 * p.s.row + cb * p.s.col;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            float m = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-            const uint32_t e = scale_exponent(m, top);
-            const uint32_t all[8] = {e, e, e, e, e, e, e, e};
-            const int64_t r = r0 + 16 * i;
-            if (r >= p.rows) continue;
-            if (x == 0) p.s.at[r * p.s.row + cb * p.s.col] = power(e);
-            if (left > 0) put_codes(p.Q + r * p.ldq + c, codes(v[i], all, p.e5m2), left);
+            const uint32_t e = scale_exponent(most[i], kTop);
+            float v[8];
+            piece[i].get(v);
+            const uint2 w = codes<E5M2>(v, infinite, [=](int) { return e; });
+            if (x == 0 && (WHOLE || r0 + 16 * i < p.rows)) at[int64_t(16 * i) * p.s.row] = power(e);
+            if (inside(i)) put_codes<WHOLE>(q + int64_t(16 * i) * p.ldq, w, left);
         }
     }
     if constexpr ((MODE & kTiles) != 0) {
         float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
+        for (int i = 0; i < I; ++i) m = fmaxf(m, row[i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+        if ((threadIdx.x & 31) == 0) space.warp_max[threadIdx.x >> 5] = m;
         __syncthreads();
-        m = warp_max[0];
+        m = space.warp_max[0];
 #pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) m = fmaxf(m, warp_max[i]);
-        const uint32_t e = scale_exponent(m, top);
-        const uint32_t all[8] = {e, e, e, e, e, e, e, e};
+        for (int i = 1; i < kThreads / 32; ++i) m = fmaxf(m, space.warp_max[i]);
+        const uint32_t e = scale_exponent(m, kTop);
         if (threadIdx.x == 0) p.s.at[rb * p.s.row + cb * p.s.col] = power(e);
+        uint8_t *q = p.Q + r0 * p.ldq + c;
 #pragma unroll
-        for (int i = 0; i < I; ++i)
-            if (r0 + 16 * i < p.rows && left > 0)
-                put_codes(p.Q + (r0 + 16 * i) * p.ldq + c, codes(v[i], all, p.e5m2), left);
+        for (int i = 0; i < I; ++i) {
+            float v[8];
+            piece[i].get(v);
+            const uint2 w = codes<E5M2>(v, infinite, [=](int) { return e; });
+            if (inside(i)) put_codes<WHOLE>(q + int64_t(16 * i) * p.ldq, w, left);
+        }
     }
     if constexpr ((MODE & kColumns) != 0) {
-        float m[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < I; ++i) m[j] = fmaxf(m[j], magnitude(v[i][j]));
-        }
-        float4 *to = reinterpret_cast<float4 *>(&column_max[y][x * 8]);
-        to[0] = make_float4(m[0], m[1], m[2], m[3]);
-        to[1] = make_float4(m[4], m[5], m[6], m[7]);
+        float4 *to = reinterpret_cast<float4 *>(&space.column_max[y][x * 8]);
+        to[0] = make_float4(column[0], column[1], column[2], column[3]);
+        to[1] = make_float4(column[4], column[5], column[6], column[7]);
         __syncthreads();
         if (threadIdx.x < 128) {
-            float most = 0.0f;
+            float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) most = fmaxf(most, column_max[i][threadIdx.x]);
-            const uint32_t e = scale_exponent(most, top);
-            column_exponent[threadIdx.x] = e;
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, space.column_max[i][threadIdx.x]);
+            const uint32_t e = scale_exponent(m, kTop);
+            space.column_exponent[threadIdx.x] = e;
             const int64_t col = cb * 128 + threadIdx.x;
-            if (col < p.cols) p.sc.at[rb * p.sc.row + col * p.sc.col] = power(e);
+            if (WHOLE || col < p.cols) p.sc.at[rb * p.sc.row + col * p.sc.col] = power(e);
         }
         __syncthreads();
         uint32_t e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = column_exponent[x * 8 + j];
+        for (int j = 0; j < 8; ++j) e[j] = space.column_exponent[x * 8 + j];
+        uint8_t *q = p.Qc + r0 * p.ldqc + c;
 #pragma unroll
-        for (int i = 0; i < I; ++i)
-            if (r0 + 16 * i < p.rows && left > 0)
-                put_codes(p.Qc + (r0 + 16 * i) * p.ldqc + c, codes(v[i], e, p.e5m2), left);
+        for (int i = 0; i < I; ++i) {
+            float v[8];
+            piece[i].get(v);
+            const uint2 w = codes<E5M2>(v, infinite, [&](int j) { return e[j]; });
+            if (inside(i)) put_codes<WHOLE>(q + int64_t(16 * i) * p.ldqc, w, left);
+        }
     }
 }
 
-template <class T> cudaError_t quantize(const QuantizeArgs &a, cudaStream_t stream)
+// Thread (x, y) = (t % 16, t / 16): 8 columns of the rows y, y + 16, .. of a tile of 16 * I rows.  MODE: the
+// sum of the ways.  Blocks of 1 x 128 alone do not need a tile's height: few rows take I = 1, for more CTAs.
+template <class T, int MODE, int I, bool E5M2>
+__global__ void __launch_bounds__(kThreads, MODE & kColumns || sizeof(T) == 4 ? 2 : 3) quantize_kernel(const __grid_constant__ QuantizeParams p)
+{
+    __shared__ QuantizeSpace space;
+    chain_wait();
+    const int64_t rb = blockIdx.x / unsigned(p.col_blocks), cb = blockIdx.x % unsigned(p.col_blocks);
+    if (p.wide && (rb + 1) * 16 * I <= p.rows && (cb + 1) * 128 <= p.cols) quantize_tile<T, MODE, I, E5M2, true>(p, rb, cb, space);
+    else quantize_tile<T, MODE, I, E5M2, false>(p, rb, cb, space);
+}
+
+template <class T, bool E5M2> cudaError_t quantize(const QuantizeArgs &a, cudaStream_t stream)
 {
     QuantizeParams p{};
     p.rows = a.rows;
@@ -183,7 +252,6 @@ template <class T> cudaError_t quantize(const QuantizeArgs &a, cudaStream_t stre
     p.Qc = static_cast<uint8_t *>(a.Qc);
     p.ldqc = a.ldqc;
     p.sc = a.sc;
-    p.e5m2 = a.q_type == GEMM_TYPE_E5M2;
     p.wide = reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.ldx * int64_t(sizeof(T)) % 16 == 0;
     const int64_t blocks = (a.cols + 127) / 128;
     p.col_blocks = int(blocks);
@@ -193,60 +261,66 @@ template <class T> cudaError_t quantize(const QuantizeArgs &a, cudaStream_t stre
     const int64_t height = few ? 16 : 128, grid = (a.rows + height - 1) / height * blocks;
     if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     const dim3 g{unsigned(grid)};
-    if (few) return launch_chained(quantize_kernel<T, kRows, 1>, g, kThreads, 0, 1, stream, p);
-    if (rows_alone) return launch_chained(quantize_kernel<T, kRows, 8>, g, kThreads, 0, 1, stream, p);
-    if (a.Q == nullptr) return launch_chained(quantize_kernel<T, kColumns, 8>, g, kThreads, 0, 1, stream, p);
-    if (a.Qc == nullptr) return launch_chained(quantize_kernel<T, kTiles, 8>, g, kThreads, 0, 1, stream, p);
-    return launch_chained(quantize_kernel<T, kRows + kColumns, 8>, g, kThreads, 0, 1, stream, p);
+    if (few) return launch_chained(quantize_kernel<T, kRows, 1, E5M2>, g, kThreads, 0, 1, stream, p);
+    if (rows_alone) return launch_chained(quantize_kernel<T, kRows, 8, E5M2>, g, kThreads, 0, 1, stream, p);
+    if (a.Q == nullptr) return launch_chained(quantize_kernel<T, kColumns, 8, E5M2>, g, kThreads, 0, 1, stream, p);
+    if (a.Qc == nullptr) return launch_chained(quantize_kernel<T, kTiles, 8, E5M2>, g, kThreads, 0, 1, stream, p);
+    return launch_chained(quantize_kernel<T, kRows + kColumns, 8, E5M2>, g, kThreads, 0, 1, stream, p);
+}
+template <class T> cudaError_t quantize(const QuantizeArgs &a, cudaStream_t stream)
+{
+    return a.q_type == GEMM_TYPE_E5M2 ? quantize<T, true>(a, stream) : quantize<T, false>(a, stream);
 }
 
-// Thread: 16 columns of one row.  A 128-wide block's scale serves all of them.
-template <class Y>
-__global__ void __launch_bounds__(kThreads)
-dequantize_kernel(int64_t rows, int64_t cols, const uint8_t *Q, int64_t ldq, const Scales s, Y *y, int64_t ldy,
-                  int wide, int e5m2)
+// Thread (x, y) of a CTA: 8 columns of the rows y, y + 16, .. of a tile of 128 x 128, whose scales are one a
+// row, one a column or one; eight pieces in flight.
+template <class Y, bool E5M2>
+__global__ void __launch_bounds__(kThreads, 4)
+dequantize_kernel(int64_t rows, int64_t cols, unsigned col_blocks, const uint8_t *Q, int64_t ldq, const __grid_constant__ Scales s, Y *y,
+                  int64_t ldy, int wide)
 {
     chain_wait();
-    const int64_t r = int64_t(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 4);
-    if (r >= rows) return;
-    const float *at = s.at + (r >> s.row_shift) * s.row;
-    for (int64_t c = (int64_t(blockIdx.y) * 16 + (threadIdx.x & 15)) * 16; c < cols; c += int64_t(gridDim.y) * 256) {
-        const int64_t left = cols - c;
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (left >= 16) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(Q + r * ldq + c));
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    const int64_t rb = blockIdx.x / col_blocks, cb = blockIdx.x % col_blocks;
+    const int64_t r0 = rb * 128 + (threadIdx.x >> 4), c = cb * 128 + (threadIdx.x & 15) * 8, left = cols - c;
+    if (left <= 0) return;
+    uint2 w[8];
+    float row[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 16 * i;
+        w[i] = make_uint2(0u, 0u);
+        row[i] = 1.0f;
+        if (r >= rows) continue;
+        const uint8_t *q = Q + r * ldq + c;
+        if (left >= 8) {
+            w[i] = __ldg(reinterpret_cast<const uint2 *>(q));
         } else {
-            for (int i = 0; i < left; ++i) w[i / 4] |= uint32_t(Q[r * ldq + c + i]) << (8 * (i & 3));
+            for (int j = 0; j < left; ++j) (j < 4 ? w[i].x : w[i].y) |= uint32_t(q[j]) << (8 * (j & 3));
         }
-        float f[2][8];
+        if (s.col_shift != 0) row[i] = __ldg(s.at + (r >> s.row_shift) * s.row + cb * s.col);
+    }
+    float column[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint16_t two = uint16_t(w[i / 2] >> (16 * (i & 1)));
-            const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(two, e5m2 ? __NV_E5M2 : __NV_E4M3));
-            const float2 v = __half22float2(h);
-            f[i / 4][2 * (i % 4)] = v.x;
-            f[i / 4][2 * (i % 4) + 1] = v.y;
-        }
-        if (s.col_shift != 0) {
-            const float m = __ldg(at + (c >> s.col_shift) * s.col);
+    for (int j = 0; j < 8; ++j) column[j] = s.col_shift == 0 && j < left ? __ldg(s.at + rb * s.row + (c + j) * s.col) : 1.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i / 8][i % 8] *= m;
-        } else {
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 16 * i;
+        if (r >= rows) break;
+        float f[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i < left) f[i / 8][i % 8] *= __ldg(at + (c + i) * s.col);
+        for (int j = 0; j < 4; ++j) {
+            const uint16_t two = uint16_t((j < 2 ? w[i].x : w[i].y) >> (16 * (j & 1)));
+            const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, E5M2 ? __NV_E5M2 : __NV_E4M3)));
+            f[2 * j] = v.x * row[i] * column[2 * j];  // one of the two scales is 1
+            f[2 * j + 1] = v.y * row[i] * column[2 * j + 1];
         }
         Y *to = y + r * ldy + c;
+        if (wide && left >= 8) {
+            store8<Y>(to, f);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (wide && left >= 8 * (h + 1)) {
-                store8<Y>(to + 8 * h, f[h]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (8 * h + i < left) to[8 * h + i] = from_f32<Y>(f[h][i]);
-            }
+            for (int j = 0; j < 8; ++j)
+                if (j < left) to[j] = from_f32<Y>(f[j]);
         }
     }
 }
@@ -256,11 +330,10 @@ cudaError_t dequantize(int q_type, int64_t rows, int64_t cols, const void *Q, in
                        cudaStream_t stream)
 {
     const int wide = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy * int64_t(sizeof(Y)) % 16 == 0;
-    const int64_t tall = (rows + 15) / 16, across = (cols + 255) / 256;
-    if (tall >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    const dim3 grid(unsigned(tall), unsigned(across < 65535 ? across : 65535));
-    return launch_chained(dequantize_kernel<Y>, grid, kThreads, 0, 1, stream, rows, cols, static_cast<const uint8_t *>(Q), ldq, s,
-                          static_cast<Y *>(y), ldy, wide, int(q_type == GEMM_TYPE_E5M2));
+    const int64_t blocks = (cols + 127) / 128, grid = (rows + 127) / 128 * blocks;
+    if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    return launch_chained(q_type == GEMM_TYPE_E5M2 ? dequantize_kernel<Y, true> : dequantize_kernel<Y, false>, dim3(unsigned(grid)), kThreads,
+                          0, 1, stream, rows, cols, unsigned(blocks), static_cast<const uint8_t *>(Q), ldq, s, static_cast<Y *>(y), ldy, wide);
 }
 
 }  // namespace

@@ -73,13 +73,24 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
                      : "memory");
 }
 
-// 16 columns of this thread's TMEM lane, on their way: not to be read before tmem_arrived().
+// 16 or 32 columns of this thread's TMEM lane, on their way: not to be read before tmem_arrived().
 __device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
                    "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(taddr));
 }
 // Waits for the loads started so far; the registers pass through it, so that nothing reads them earlier.
@@ -89,6 +100,16 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16])
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                    "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
+
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
 
 // ------------------------------------------------------------------ scaling and adding a K block
 // Scales whose products with each other and with a block's sum (2^-32 to 2^39) stay well inside fp32.
@@ -242,7 +263,7 @@ template <bool COLS, bool PAIRS, int BN, int SLOTS, int STEP, int DELAY> struct 
 // The sums of one thread: a row of A, CW columns of B.  sb is the block's column scales (COLS), or one for
 // every 64 columns (CW = 128) or for all.
 template <int CW, bool COLS> struct Sums {
-    static constexpr int kChunk = 16, kChunks = CW / kChunk;
+    static constexpr int kChunk = CW == 128 && !COLS ? 32 : 16, kChunks = CW / kChunk;
     float2 at[CW / 2];
 
     __device__ __forceinline__ void clear()
@@ -296,7 +317,7 @@ template <int CW, bool COLS> struct Sums {
             if (i + 1 < kChunks) tmem_start(taddr + (i + 1) * kChunk, r[(i + 1) & 1]);
             else read();
             if (i + 2 == kChunks || kChunks == 1) peek();
-            add_chunk(i * kChunk, r[i & 1], CW == 128 && i >= 4 ? s1 : s0, sb);
+            add_chunk(i * kChunk, r[i & 1], CW == 128 && i * kChunk >= 64 ? s1 : s0, sb);
         }
     }
     // The same for scales of any size: first factors, then second ones.
@@ -316,7 +337,7 @@ template <int CW, bool COLS> struct Sums {
             uint32_t v[kChunk];
             tmem_start(taddr + i * kChunk, v);
             tmem_arrived(v);
-            const int run = CW == 128 ? i / 4 : 0;
+            const int run = CW == 128 ? i * kChunk / 64 : 0;
 #pragma unroll
             for (int j = 0; j < kChunk; ++j)
                 v[j] = __float_as_uint(__uint_as_float(v[j]) * (h.x * scratch[CW + (COLS ? i * kChunk + j : run)]));
@@ -385,7 +406,13 @@ template <bool COLS> struct PairSmem {
     __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kBox; }
 };
 
-constexpr int kLogGroup = 3;  // tiles are visited in groups of eight tile rows
+// Tile t of the visiting order, groups of eight tile rows column by column (raster() in 32 bits).
+__device__ __forceinline__ void tile_of(unsigned t, unsigned tiles_m, unsigned tiles_n, int &tm, int &tn)
+{
+    const unsigned group = t / (8 * tiles_n), r = t - group * 8 * tiles_n, rows = min(8u, tiles_m - 8 * group);
+    tm = int(8 * group + r % rows);
+    tn = int(r / rows);
+}
 
 template <bool COLS, bool F32>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -435,9 +462,9 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
                 tma_prefetch_desc(&map_b);
             }
             for (int t = first; ok && t < tiles; t += step) {
-                int64_t tm, tn;
-                raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
-                const int m0 = int(tm) * 256 + int(rank) * 128, n0 = int(tn) * 256;
+                int tm, tn;
+                tile_of(t, p.tiles_m, p.tiles_n, tm, tn);
+                const int m0 = tm * 256 + int(rank) * 128, n0 = tn * 256;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                     if (__any_sync(kFull, !ok)) {
@@ -474,9 +501,9 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             ScaleCopies<COLS, true, 256, Smem::kSlots, 2, 1> copies(sh.scales, sh.scale_full(0), sh.scale_empty(0), lane, mine);
             int turn = 0;
             for (int t = first; ok && t < tiles; t += step) {
-                int64_t tm, tn;
-                raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
-                copies.begin(p, tm * 256 + int64_t(rank) * 128, tn * 256, turn ^ mine);
+                int tm, tn;
+                tile_of(t, p.tiles_m, p.tiles_n, tm, tn);
+                copies.begin(p, int64_t(tm) * 256 + rank * 128, int64_t(tn) * 256, turn ^ mine);
                 for (int kb = 0; ok && kb < p.num_kb; ++kb, turn ^= 1)
                     if (turn == mine) ok = copies.copy(watch);
             }
@@ -532,9 +559,9 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         int acc = 0, added = -1;  // added: the slot of the block before
         uint32_t acc_phase = 0;
         for (int t = first; ok && t < tiles; t += step) {
-            int64_t tm, tn;
-            raster(t, p.tiles_m, p.tiles_n, kLogGroup, tm, tn);
-            const int64_t m0 = tm * 256 + int64_t(rank) * 128 + quarter * 32, n0 = tn * 256 + half * 64;
+            int tm, tn;
+            tile_of(t, p.tiles_m, p.tiles_n, tm, tn);
+            const int64_t m0 = int64_t(tm) * 256 + rank * 128 + quarter * 32, n0 = int64_t(tn) * 256 + half * 64;
             Sums<128, COLS> sums;
             sums.clear();
             bool there = false;
