@@ -26,36 +26,63 @@ constexpr int kThreeProducts = 128;  // sides up to it take three products
 // moved by 2^86.
 struct Squares {
     float low = 0.0f, mid = 0.0f, high = 0.0f;
-    __device__ __forceinline__ void add(float x)
+    // Eight values, together in the common case.
+    __device__ __forceinline__ void add(const float (&v)[8])
     {
-        const float a = fabsf(x);
-        if (a < 0x1p-40f) low = fmaf(a * 0x1p86f, a * 0x1p86f, low);
-        else if (a > 0x1p40f) high = fmaf(a * 0x1p-86f, a * 0x1p-86f, high);
-        else mid = fmaf(x, x, mid);  // NaN too
+        float least = FLT_MAX, most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = fabsf(v[i]);
+            least = fminf(least, a == 0.0f ? 1.0f : a);
+            most = fmaxf(most, a);
+        }
+        if (least >= 0x1p-40f && most <= 0x1p40f) {  // NaN too
+            float a = v[0] * v[0], b = v[1] * v[1];
+#pragma unroll
+            for (int i = 2; i < 8; i += 2) {
+                a = fmaf(v[i], v[i], a);
+                b = fmaf(v[i + 1], v[i + 1], b);
+            }
+            mid += a + b;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = fabsf(v[i]);
+            if (a < 0x1p-40f) low = fmaf(a * 0x1p86f, a * 0x1p86f, low);
+            else if (a > 0x1p40f) high = fmaf(a * 0x1p-86f, a * 0x1p-86f, high);
+            else mid = fmaf(v[i], v[i], mid);
+        }
     }
 };
 
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-squares_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, double *partial)
+squares_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, int log_across, double *partial)
 {
     __shared__ double sums[kThreads / 32];
     chain_wait();
     const T *g = G + int64_t(blockIdx.y) * stride;
     Squares s;
-    const int64_t pieces = (cols + 7) / 8, total = rows * pieces;
-    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < total; i += int64_t(gridDim.x) * kThreads) {
-        const int64_t r = i / pieces, c = (i - r * pieces) * 8;
-        float v[8];
-        if (wide && c + 8 <= cols) {
-            load8<T>(g + r * ld + c, v);
-        } else {
+    // 8 elements of four rows at a time: rows y, y + tall, .., columns in pieces x, x + across, ..
+    const int across = 1 << log_across, x = threadIdx.x & (across - 1), tall = kThreads >> log_across;
+    const int64_t step = int64_t(gridDim.x) * tall;
+    for (int64_t r0 = int64_t(blockIdx.x) * tall + (threadIdx.x >> log_across); r0 < rows; r0 += 4 * step)
+        for (int64_t c = 8 * x; c < cols; c += 8 * across) {
+            float v[4][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? to_f32(g[r * ld + c + j]) : 0.0f;
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = r0 + i * step;
+                if (r < rows && wide && c + 8 <= cols) {
+                    load8<T>(g + r * ld + c, v[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = r < rows && c + j < cols ? to_f32(g[r * ld + c + j]) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.add(v[i]);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s.add(v[j]);
-    }
     double all = double(s.mid) + double(s.low) * 0x1p-172 + double(s.high) * 0x1p172;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
@@ -164,10 +191,12 @@ template <class T> cudaError_t normalise(const OrthogonalArgs &a, const Orthogon
     const T *G = static_cast<const T *>(a.G);
     const int wide = reinterpret_cast<uintptr_t>(G) % 16 == 0 && a.ldg * int64_t(sizeof(T)) % 16 == 0 &&
                      (a.count == 1 || a.strideg * int64_t(sizeof(T)) % 16 == 0);
-    const int64_t pieces = a.rows * ((a.cols + 7) / 8), wanted = (pieces + 4 * kThreads - 1) / (4 * kThreads);
-    const int blocks = int(wanted < kNormBlocks ? wanted : kNormBlocks);
+    int log_across = 0;  // threads along a row
+    while (log_across < 8 && (8 << log_across) < a.cols) ++log_across;
+    const int64_t rows_a_block = 4 * (kThreads >> log_across), wanted = (a.rows + rows_a_block - 1) / rows_a_block;
+    const int blocks = int(wanted < kNormBlocks ? wanted : kNormBlocks);  // whatever the count: a stack gives each matrix's own result
     cudaError_t e = launch_chained(squares_kernel<T>, dim3(unsigned(blocks), unsigned(a.count)), kThreads, 0, 1, stream, a.rows, a.cols,
-                                   G, a.ldg, a.strideg, wide, partial);
+                                   G, a.ldg, a.strideg, wide, log_across, partial);
     if (e != cudaSuccess) return e;
     const dim3 grid{unsigned((a.cols + 63) / 64), unsigned((a.rows + 63) / 64), unsigned(a.count)};
     return launch_chained(a.rows > a.cols ? split_kernel<T, true> : split_kernel<T, false>, grid, kThreads, 0, 1, stream, a.rows, a.cols,

@@ -16,7 +16,7 @@ struct OrthogonalLayout {
     int64_t x[2], e, f, dd, df, unit, partial;  // byte offsets; unit: 1 / c of each matrix (Norm); partial sums
     int64_t bytes;
 };
-constexpr int kNormBlocks = 128;  // at most, of a matrix's sum of squares
+constexpr int kNormBlocks = 304;  // at most, of a matrix's sum of squares
 OrthogonalLayout orthogonal_layout(int64_t count, int64_t rows, int64_t cols);
 
 struct OrthogonalArgs {

@@ -332,13 +332,13 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     }
                     store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, mirror);
                 } else if constexpr (WHAT == kSquare) {
-                    const float *d = p.d + x.which * p.ldn + n0;
+                    const float others = n0 + lane < p.n ? __ldcg(p.d + x.which * p.ldn + n0 + lane) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         // of A: E here, d on the diagonal, where E is 0; of A^2: (d_i + d_j) E + E E, d^2 + E E
                         const bool diagonal = m == n0 + i;
                         const float e = (old.high(i) + old.low(i)) * p.from_e, beside = three ? e : old.high(i) * p.from_e;
-                        const float other = n0 + i < p.n ? __ldcg(d + i) : 0.0f;
+                        const float other = __shfl_sync(kFull, others, i);
                         const float square = fmaf(v[i], scale, diagonal ? mine * mine : beside * (mine + other));
                         v[i] = fmaf(p.b, diagonal ? mine : e, p.c * square);
                         if (diagonal) {
