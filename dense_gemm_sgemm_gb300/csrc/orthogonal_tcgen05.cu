@@ -292,30 +292,34 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         const uint32_t acc_empty0 = PAIR ? map_to_rank(sh.acc_empty(0), 0) : sh.acc_empty(0);
         for (int u = first; u < units; u += step) {
             const Unit x = unit_of<kSymmetric>(p, u);
+            const int m0 = x.tm * kTile + int(rank) * 128 + quarter * 32, m = m0 + lane;
+            const bool mirror = kSymmetric && x.tm != x.tn, row = m < p.n;
+            // what the epilogue reads is on its way during the products and the stores before it
+            Parts old;
+            auto inside = [&](int n0) { return m0 < p.n && n0 < (kSymmetric ? p.n : p.k); };
+            auto fetch = [&](int n0) {
+                if (WHAT == kGram || !inside(n0)) return;
+                if (!row) old.clear();
+                else if (WHAT == kSquare) old.load(p.e + (int64_t(x.which) * p.n + m) * p.ldn + n0, p.part_e);
+                else old.load(p.x + (int64_t(x.which) * p.n + m) * p.ldk + n0, p.part_x);
+            };
+            fetch(x.tn * kTile + half * kHalf);
+            const float unit = p.unit != nullptr ? __ldg(p.unit + x.which) : 1.0f;
+            float mine = 0.0f;  // d or f of this row
+            if (WHAT == kSquare && row) mine = __ldcg(p.d + x.which * p.ldn + m);
+            if (WHAT >= kUpdate && row) mine = __ldcg(p.f + x.which * p.ldn + m);
             ok = __all_sync(kFull, watch.wait(sh.acc_full(acc), acc_phase));
             if (!ok) break;
             tc_fence_after();
             const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * kTile + half * kHalf);
-            const int m0 = x.tm * kTile + int(rank) * 128 + quarter * 32, m = m0 + lane;
-            const bool mirror = kSymmetric && x.tm != x.tn, row = m < p.n;
-            const float unit = p.unit != nullptr ? __ldg(p.unit + x.which) : 1.0f;
             const float scale = WHAT == kGram ? p.from_acc * unit * unit : WHAT == kSquare ? p.from_acc : p.from_acc * unit;
             const bool three = p.products == 3;
-            float mine = 0.0f;  // d or f of this row
-            if (WHAT == kSquare && row) mine = __ldcg(p.d + x.which * p.ldn + m);
-            if (WHAT >= kUpdate && row) mine = __ldcg(p.f + x.which * p.ldn + m);
             const float from_x = p.from_x * unit, high = (p.a + mine) * from_x, low = three ? high : p.a * from_x;  // kUpdate
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
                 const int n0 = x.tn * kTile + half * kHalf + c;
-                const bool in = m0 < p.n && n0 < (kSymmetric ? p.n : p.k);
+                const bool in = inside(n0);
                 float v[32];
-                Parts old;
-                if (WHAT != kGram && in) {
-                    if (!row) old.clear();
-                    else if (WHAT == kSquare) old.load(p.e + (int64_t(x.which) * p.n + m) * p.ldn + n0, p.part_e);
-                    else old.load(p.x + (int64_t(x.which) * p.n + m) * p.ldk + n0, p.part_x);
-                }
                 __syncwarp();
                 tmem_ld_32(taddr + c, v);
                 if (c + 32 >= kHalf) release_accumulator(acc_empty0 + 8u * acc, lane);
@@ -347,10 +351,12 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                         }
                         v[i] *= p.to;
                     }
+                    if (c + 32 < kHalf) fetch(n0 + 32);
                     store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, three, mirror);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(high, old.high(i), fmaf(low, old.low(i), v[i] * scale)) * p.to;
+                    if (c + 32 < kHalf) fetch(n0 + 32);
                     if constexpr (WHAT == kUpdate) {
                         store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, false);
                     } else {
