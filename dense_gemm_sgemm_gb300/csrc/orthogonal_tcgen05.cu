@@ -42,9 +42,9 @@ namespace gemm {
 namespace {
 
 constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
-constexpr int kOperand = 128 * 128, kStage = 2 * kOperand, kStages = 6;  // bytes: 128 rows of 64 fp16 of either operand
-constexpr int kEpi = kEpiWarps * 4096, kBars = 256;
-constexpr int kSmemBytes = kStages * kStage + kEpi + kBars + 1024;
+constexpr int kOperand = 128 * 128, kStage = 2 * kOperand, kStages = 5;  // bytes: 128 rows of 64 fp16 of either operand
+constexpr int kEpi = kEpiWarps * 4096, kIn = kEpiWarps * 4096, kBars = 256;  // what the epilogue stores, and reads
+constexpr int kSmemBytes = kStages * kStage + kEpi + kIn + kBars + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kGram = 0, kSquare = 1, kUpdate = 2, kResult = 3, kResultTurned = 4;
@@ -68,9 +68,25 @@ struct StepParams {
     int inject_stall;  // test hook: the producer never fills its first slice
 };
 
+// Box of a 4-D tensor map: columns within a block of 64, rows, blocks of columns, plane.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2, int c3)
+{
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                     "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                     "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                     : "memory");
+}
+
 struct Smem {
     uint32_t ring, bar0;
-    uint8_t *epi;
+    uint8_t *epi, *in;
     volatile uint32_t *tmem_slot;
     volatile int *abort_flag;
     __device__ __forceinline__ explicit Smem(uint8_t *raw)
@@ -79,7 +95,8 @@ struct Smem {
         uint8_t *p = raw + (base - r);
         ring = base;
         epi = p + kStages * kStage;
-        uint8_t *bars = epi + kEpi;
+        in = epi + kEpi;
+        uint8_t *bars = in + kIn;
         bar0 = smem_u32(bars);
         tmem_slot = reinterpret_cast<volatile uint32_t *>(bars + kBars - 16);
         abort_flag = reinterpret_cast<volatile int *>(bars + kBars - 8);
@@ -88,7 +105,8 @@ struct Smem {
     __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
     __device__ __forceinline__ uint32_t acc_full(int i) const { return bar0 + 8u * (2 * kStages + i); }
     __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar0 + 8u * (2 * kStages + 2 + i); }
-    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4); }
+    __device__ __forceinline__ uint32_t fetched(int w) const { return bar0 + 8u * (2 * kStages + 4 + w); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4 + kEpiWarps); }
     __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
     __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kOperand; }
 };
@@ -116,21 +134,17 @@ template <bool SYMMETRIC> __device__ __forceinline__ Unit unit_of(const StepPara
     return x;
 }
 
-// The parts of 32 elements of a row; the rows are padded to whole pieces.
+// The parts of 32 elements of a row, from a warp's two boxes of 32 rows in the 64-byte swizzle.
 struct Parts {
     uint4 h[4], l[4];
-    __device__ __forceinline__ void load(const __half *at, int64_t part)
+    __device__ __forceinline__ void load(const uint8_t *in, int lane)
     {
+        const uint4 *row = reinterpret_cast<const uint4 *>(in) + lane * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            h[i] = __ldcg(reinterpret_cast<const uint4 *>(at) + i);
-            l[i] = __ldcg(reinterpret_cast<const uint4 *>(at + part) + i);
+            h[i] = row[i ^ ((lane >> 1) & 3)];
+            l[i] = row[128 + (i ^ ((lane >> 1) & 3))];
         }
-    }
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = l[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ float high(int i) const { return __half2float(reinterpret_cast<const __half *>(h)[i]); }
     __device__ __forceinline__ float low(int i) const { return __half2float(reinterpret_cast<const __half *>(l)[i]); }
@@ -154,7 +168,8 @@ __device__ __forceinline__ void store_parts(Staging<false> &staging, float (&v)[
 template <bool PAIR, int WHAT, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
 orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ StepParams p)
+                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_in,
+                  const __grid_constant__ StepParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const Smem sh(smem_raw);
@@ -171,6 +186,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             mbar_init(sh.acc_full(i), 1);
             mbar_init(sh.acc_empty(i), (PAIR ? 2 : 1) * kEpiWarps);
         }
+        for (int w = 0; w < kEpiWarps; ++w) mbar_init(sh.fetched(w), 1);
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -193,46 +209,34 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     bool ok = true;
 
     if (warp == 0) {
-        // ---------------- producer: 128 rows of A, 128 rows (or columns of K x N) of B
-        const bool leader = elect_one();
-        const uint32_t full0 = PAIR ? map_to_rank(sh.full(0), 0) : sh.full(0);
-        if (leader) {
+        // ---------------- producer, one lane: 128 rows of A, 128 rows (or columns of K x N) of B
+        if (elect_one()) {
             tma_prefetch_desc(&map_a);
             tma_prefetch_desc(&map_b);
-        }
-        for (int u = first; ok && u < units; u += step) {
-            const Unit x = unit_of<kSymmetric>(p, u);
-            const int m0 = x.tm * kTile + int(rank) * 128, n0 = x.tn * kTile + int(rank) * 128;
-            for (int i = 0; i < slices; ++i) {
-                const int product = i / p.num_kb, kb = i - product * p.num_kb;
-                const int plane_a = x.which + (product == 2 ? p.count : 0), plane_b = x.which + (product == 1 ? p.count : 0);
-                ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-                if (__any_sync(kFull, !ok)) {
-                    ok = false;
-                    break;
-                }
-                if (leader) {
-                    if (rank == 0) mbar_expect_tx(sh.full(ring.stage), (PAIR ? 2 : 1) * kStage);
-                    if (!(p.inject_stall && i == 0 && u == first)) {
-                        const uint32_t full = full0 + 8u * ring.stage, a = sh.a(ring.stage), b = sh.b(ring.stage);
-                        auto load = [&](uint32_t dst, const CUtensorMap *map, int c0, int c1, int plane) {
-                            if (PAIR) tma_load_3d_pair(dst, map, full, c0, c1, plane);
-                            else tma_load_3d(dst, map, full, c0, c1, plane);
-                        };
-                        load(a, &map_a, kb * 64, m0, plane_a);
-                        if (kTurnB) {
-                            load(b, &map_b, n0, kb * 64, plane_b);
-                            load(b + kOperand / 2, &map_b, n0 + 64, kb * 64, plane_b);
-                        } else {
-                            load(b, &map_b, kb * 64, n0, plane_b);
+            const uint32_t full0 = PAIR ? map_to_rank(sh.full(0), 0) : sh.full(0);
+            bool starve = p.inject_stall != 0;
+            for (int u = first; ok && u < units; u += step) {
+                const Unit x = unit_of<kSymmetric>(p, u);
+                const int m0 = x.tm * kTile + int(rank) * 128, n0 = x.tn * kTile + int(rank) * 128;
+                for (int product = 0; ok && product < p.products; ++product) {  // high high, high low, low high
+                    const int plane_a = x.which + (product == 2 ? p.count : 0), plane_b = x.which + (product == 1 ? p.count : 0);
+                    for (int k = 0; k < 64 * p.num_kb; k += 64) {
+                        ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                        if (!ok) break;
+                        if (rank == 0) mbar_expect_tx(sh.full(ring.stage), (PAIR ? 2 : 1) * kStage);
+                        if (!starve) {
+                            const uint32_t full = full0 + 8u * ring.stage, a = sh.a(ring.stage), b = sh.b(ring.stage);
+                            if (PAIR) tma_load_3d_pair(a, &map_a, full, k, m0, plane_a);
+                            else tma_load_3d(a, &map_a, full, k, m0, plane_a);
+                            if (kTurnB) tma_load_4d<PAIR>(b, &map_b, full, 0, k, n0 / 64, plane_b);
+                            else if (PAIR) tma_load_3d_pair(b, &map_b, full, k, n0, plane_b);
+                            else tma_load_3d(b, &map_b, full, k, n0, plane_b);
                         }
+                        starve = false;
+                        ring.next();
                     }
                 }
-                __syncwarp();
-                ring.next();
             }
-        }
-        if (leader) {
             if (!ok) {  // copies in flight get time to land
                 const uint64_t t0 = global_timer_ns();
                 while (global_timer_ns() - t0 < 2000000ull) {
@@ -246,49 +250,52 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         }
     } else if (warp == 1) {
         if (rank == 0) {
-            // ---------------- MMA issuer
-            const bool leader = elect_one();
-            const uint32_t idesc = make_idesc(0, kTurnB, kTile, kTile);
-            const uint64_t a0 = smem_desc(sh.a(0), 16, 1024), b0 = smem_desc(sh.b(0), kTurnB ? kOperand / 2 : 16, 1024);
-            constexpr uint32_t kStepA = 32 >> 4, kStepB = (kTurnB ? 2048 : 32) >> 4;
-            auto commit = [&](uint32_t bar) {
-                if (PAIR) commit_both(bar);
-                else umma_commit<false>(bar);
-            };
-            for (int u = first; ok && u < units; u += step) {
-                ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
-                if (!ok) break;
-                tc_fence_after();
-                for (int i = 0; i < slices; ++i) {
-                    ok = watch.wait(sh.full(ring.stage), ring.phase);
+            // ---------------- MMA issuer, one lane
+            if (elect_one()) {
+                const uint32_t idesc = make_idesc(0, kTurnB, kTile, kTile);
+                const uint64_t a0 = smem_desc(sh.a(0), 16, 1024), b0 = smem_desc(sh.b(0), kTurnB ? kOperand / 2 : 16, 1024);
+                constexpr uint32_t kStepA = 32 >> 4, kStepB = (kTurnB ? 2048 : 32) >> 4;
+                auto commit = [&](uint32_t bar) {
+                    if (PAIR) commit_both(bar);
+                    else umma_commit<false>(bar);
+                };
+                for (int u = first; ok && u < units; u += step) {
+                    ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    if (leader) {
+                    const uint32_t d = tmem + uint32_t(acc * kTile);
+                    uint32_t more = 0u;
+                    for (int i = 0; i < slices; ++i) {
+                        ok = watch.wait(sh.full(ring.stage), ring.phase);
+                        if (!ok) break;
+                        tc_fence_after();
                         const uint64_t a = a0 + uint32_t(ring.stage * (kStage >> 4)), b = b0 + uint32_t(ring.stage * (kStage >> 4));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_f16<PAIR>(tmem + uint32_t(acc * kTile), a + k * kStepA, b + k * kStepB, idesc,
-                                           i > 0 || k > 0 ? 1u : 0u);
+                        for (int k = 0; k < 4; ++k) {
+                            umma_f16<PAIR>(d, a + k * kStepA, b + k * kStepB, idesc, more);
+                            more = 1u;
+                        }
                         commit(sh.empty(ring.stage));
+                        ring.next();
                     }
-                    __syncwarp();
-                    ring.next();
+                    if (!ok) break;
+                    commit(sh.acc_full(acc));
+                    acc ^= 1;
+                    acc_phase ^= acc == 0 ? 1u : 0u;
                 }
-                if (!ok) break;
-                if (leader) commit(sh.acc_full(acc));
-                acc ^= 1;
-                acc_phase ^= acc == 0 ? 1u : 0u;
-            }
-            if (!ok && leader) {  // MMAs in flight finish before TMEM is released
-                umma_commit<PAIR>(sh.drain());
-                const volatile int no_abort = 0;
-                mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
+                if (!ok) {  // MMAs in flight finish before TMEM is released
+                    umma_commit<PAIR>(sh.drain());
+                    const volatile int no_abort = 0;
+                    mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
+                }
             }
         }
     } else {
         // ---------------- epilogue: rows 32 * quarter .. of this CTA's 128, half of the tile's columns
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         Staging<F32> staging(sh.epi + (warp - 2) * 4096, lane);
+        const uint8_t *in = sh.in + (warp - 2) * 4096;
+        uint32_t in_phase = 0;
         const uint32_t acc_empty0 = PAIR ? map_to_rank(sh.acc_empty(0), 0) : sh.acc_empty(0);
         for (int u = first; u < units; u += step) {
             const Unit x = unit_of<kSymmetric>(p, u);
@@ -299,9 +306,13 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             auto inside = [&](int n0) { return m0 < p.n && n0 < (kSymmetric ? p.n : p.k); };
             auto fetch = [&](int n0) {
                 if (WHAT == kGram || !inside(n0)) return;
-                if (!row) old.clear();
-                else if (WHAT == kSquare) old.load(p.e + (int64_t(x.which) * p.n + m) * p.ldn + n0, p.part_e);
-                else old.load(p.x + (int64_t(x.which) * p.n + m) * p.ldk + n0, p.part_x);
+                __syncwarp();  // the boxes before have been read
+                if (lane == 0) {
+                    const uint32_t dst = smem_u32(in), bar = sh.fetched(warp - 2);
+                    mbar_expect_tx(bar, 4096);
+                    tma_load_3d(dst, &map_in, bar, n0, m0, x.which);
+                    tma_load_3d(dst + 2048, &map_in, bar, n0, m0, p.count + x.which);
+                }
             };
             fetch(x.tn * kTile + half * kHalf);
             const float unit = p.unit != nullptr ? __ldg(p.unit + x.which) : 1.0f;
@@ -318,12 +329,18 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
                 const int n0 = x.tn * kTile + half * kHalf + c;
-                const bool in = inside(n0);
+                const bool wanted = inside(n0);
                 float v[32];
                 __syncwarp();
                 tmem_ld_32(taddr + c, v);
                 if (c + 32 >= kHalf) release_accumulator(acc_empty0 + 8u * acc, lane);
-                if (!in) continue;
+                if (!wanted) continue;
+                if (WHAT != kGram) {
+                    ok = __all_sync(kFull, watch.wait(sh.fetched(warp - 2), in_phase));
+                    if (!ok) break;
+                    in_phase ^= 1u;
+                    old.load(in, lane);
+                }
                 if constexpr (WHAT == kGram) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -367,6 +384,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     }
                 }
             }
+            if (!ok) break;
             acc ^= 1;
             acc_phase ^= acc == 0 ? 1u : 0u;
         }
@@ -393,6 +411,19 @@ bool make_map16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, i
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same matrices read as K x N operands, two blocks of 64 columns x 64 rows a box.  Columns between the
+// matrix's end and its padded rows' end are read as they are: they only meet columns of the result beyond it.
+bool make_map_columns(CUtensorMap *map, const void *ptr, int64_t rows, int64_t ld, int64_t count)
+{
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(ld / 64), cuuint64_t(count)};
+    const cuuint64_t strides[3] = {cuuint64_t(ld) * 2, 128, cuuint64_t(ld) * cuuint64_t(rows) * 2};
+    const cuuint32_t box[4] = {64, 64, 2, 1}, steps[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Pairs of SMs where the tiles' waves cost less.  A slice of 64 k takes a pair 560 SM cycles, a single CTA
 // 330; a tile costs about 8 slices more than it has.
 bool pairs_pay(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool symmetric, int64_t slices)
@@ -410,7 +441,7 @@ bool pairs_pay(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool 
 }
 
 template <bool PAIR, int WHAT, bool F32>
-cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, StepParams p,
+cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, StepParams p,
                            int64_t columns, cudaStream_t stream)
 {
     constexpr int kTile = PAIR ? 256 : 128;
@@ -431,15 +462,15 @@ cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CU
     if (per * p.count >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     p.per = int(per);
     const int64_t units = per * p.count, grid = (units < room ? units : room) * (PAIR ? 2 : 1);
-    return launch_chained(kernel, dim3(unsigned(grid)), kThreads, kSmemBytes, PAIR ? 2 : 1, stream, a, b, out, p);
+    return launch_chained(kernel, dim3(unsigned(grid)), kThreads, kSmemBytes, PAIR ? 2 : 1, stream, a, b, out, in, p);
 }
 template <int WHAT, bool F32 = false>
-cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const StepParams &p,
+cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, const StepParams &p,
                            int64_t columns, cudaStream_t stream)
 {
     return pairs_pay(dev, p.count, p.n, columns, WHAT <= kSquare, p.num_kb * p.products)
-               ? launch_product<true, WHAT, F32>(dev, a, b, out, p, columns, stream)
-               : launch_product<false, WHAT, F32>(dev, a, b, out, p, columns, stream);
+               ? launch_product<true, WHAT, F32>(dev, a, b, out, in, p, columns, stream)
+               : launch_product<false, WHAT, F32>(dev, a, b, out, in, p, columns, stream);
 }
 
 }  // namespace
@@ -469,12 +500,13 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
     const float *unit = s.first ? reinterpret_cast<const float *>(w + l.unit) : nullptr;
-    CUtensorMap x_rows, x_cols, e_rows, f_rows, e_out, f_out, x_out, y_out;
+    CUtensorMap x_rows, x_cols, e_rows, f_rows, e_out, f_out, x_in, x_out, y_out;
     std::memset(&y_out, 0, sizeof(y_out));
-    if (!make_map16(&x_rows, p.x, l.n, l.k, l.ldk, 2 * l.count, 128) || !make_map16(&x_cols, p.x, l.n, l.k, l.ldk, 2 * l.count, 64) ||
+    if (!make_map16(&x_rows, p.x, l.n, l.k, l.ldk, 2 * l.count, 128) || !make_map_columns(&x_cols, p.x, l.n, l.ldk, 2 * l.count) ||
         !make_map16(&e_rows, p.e, l.n, l.n, l.ldn, 2 * l.count, 128) || !make_map16(&f_rows, w + l.f, l.n, l.n, l.ldn, 2 * l.count, 128) ||
         !make_store_map(&e_out, w + l.e, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, 2 * l.count, l.n * l.ldn, true) ||
         !make_store_map(&f_out, w + l.f, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, 2 * l.count, l.n * l.ldn, true) ||
+        !make_store_map(&x_in, w + l.x[from], GEMM_TYPE_F16, l.n, l.ldk, l.ldk, 2 * l.count, l.n * l.ldk, true) ||
         !make_store_map(&x_out, w + l.x[from ^ 1], GEMM_TYPE_F16, l.n, l.ldk, l.ldk, 2 * l.count, l.n * l.ldk, true))
         return cudaErrorInvalidValue;
 
@@ -483,7 +515,7 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     gram.unit = unit;
     gram.from_acc = 1.0f / (s.x_scale * s.x_scale);
     gram.to = s.e_scale;
-    cudaError_t e = launch_product<kGram>(dev, x_rows, x_rows, e_out, gram, l.n, stream);
+    cudaError_t e = launch_product<kGram>(dev, x_rows, x_rows, e_out, x_in, gram, l.n, stream);
     if (e != cudaSuccess) return e;
 
     StepParams square = p;
@@ -491,7 +523,7 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     square.from_e = 1.0f / s.e_scale;
     square.from_acc = square.from_e * square.from_e;
     square.to = s.f_scale;
-    e = launch_product<kSquare>(dev, e_rows, e_rows, f_out, square, l.n, stream);
+    e = launch_product<kSquare>(dev, e_rows, e_rows, f_out, e_out, square, l.n, stream);
     if (e != cudaSuccess) return e;
 
     StepParams update = p;
@@ -500,7 +532,7 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     update.from_x = 1.0f / s.x_scale;
     update.from_acc = update.from_x / s.f_scale;
     update.to = s.last ? 1.0f : s.next_scale;
-    if (!s.last) return launch_product<kUpdate>(dev, f_rows, x_cols, x_out, update, l.k, stream);
+    if (!s.last) return launch_product<kUpdate>(dev, f_rows, x_cols, x_out, x_in, update, l.k, stream);
     update.Y = a.Y;
     update.ldy = a.ldy;
     update.stridey = a.stridey;
@@ -509,10 +541,10 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     update.y_tma = make_store_map(&y_out, a.Y, a.y_type, a.rows, a.cols, a.ldy, l.count, a.stridey, true);
     update.y_bf16 = a.y_type == GEMM_TYPE_BF16;
     if (a.y_type == GEMM_TYPE_F32)
-        return a.rows > a.cols ? launch_product<kResultTurned, true>(dev, f_rows, x_cols, y_out, update, l.k, stream)
-                               : launch_product<kResult, true>(dev, f_rows, x_cols, y_out, update, l.k, stream);
-    return a.rows > a.cols ? launch_product<kResultTurned>(dev, f_rows, x_cols, y_out, update, l.k, stream)
-                           : launch_product<kResult>(dev, f_rows, x_cols, y_out, update, l.k, stream);
+        return a.rows > a.cols ? launch_product<kResultTurned, true>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream)
+                               : launch_product<kResult, true>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream);
+    return a.rows > a.cols ? launch_product<kResultTurned>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream)
+                           : launch_product<kResult>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream);
 }
 
 }  // namespace gemm
