@@ -262,8 +262,8 @@ template <bool COLS, bool PAIRS, int BN, int SLOTS, int STEP, int DELAY> struct 
 
 // The sums of one thread: a row of A, CW columns of B.  sb is the block's column scales (COLS), or one for
 // every 64 columns (CW = 128) or for all.
-template <int CW, bool COLS> struct Sums {
-    static constexpr int kChunk = CW == 128 && !COLS ? 32 : 16, kChunks = CW / kChunk;
+template <int CW, bool COLS, bool PAIRS> struct Sums {
+    static constexpr int kChunk = PAIRS && !COLS ? 32 : 16, kChunks = CW / kChunk;
     float2 at[CW / 2];
 
     __device__ __forceinline__ void clear()
@@ -293,7 +293,7 @@ template <int CW, bool COLS> struct Sums {
     template <class Peek, class Read>
     __device__ __forceinline__ void add(uint32_t taddr, const float *slot, int row, int part, float *scratch, int lane, Peek peek, Read read)
     {
-        using L = Slot<COLS, CW == 128>;
+        using L = Slot<COLS, PAIRS>;
         uint32_t r[2][kChunk];
         tmem_start(taddr, r[0]);
         const float *sb = slot + L::kCols + (COLS ? part : 0);
@@ -317,7 +317,7 @@ template <int CW, bool COLS> struct Sums {
             if (i + 1 < kChunks) tmem_start(taddr + (i + 1) * kChunk, r[(i + 1) & 1]);
             else read();
             if (i + 2 == kChunks || kChunks == 1) peek();
-            add_chunk(i * kChunk, r[i & 1], CW == 128 && i * kChunk >= 64 ? s1 : s0, sb);
+            add_chunk(i * kChunk, r[i & 1], PAIRS && i * kChunk >= 64 ? s1 : s0, sb);
         }
     }
     // The same for scales of any size: first factors, then second ones.
@@ -337,7 +337,7 @@ template <int CW, bool COLS> struct Sums {
             uint32_t v[kChunk];
             tmem_start(taddr + i * kChunk, v);
             tmem_arrived(v);
-            const int run = CW == 128 ? i * kChunk / 64 : 0;
+            const int run = PAIRS ? i * kChunk / 64 : 0;
 #pragma unroll
             for (int j = 0; j < kChunk; ++j)
                 v[j] = __float_as_uint(__uint_as_float(v[j]) * (h.x * scratch[CW + (COLS ? i * kChunk + j : run)]));
@@ -562,7 +562,7 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             int tm, tn;
             tile_of(t, p.tiles_m, p.tiles_n, tm, tn);
             const int64_t m0 = int64_t(tm) * 256 + rank * 128 + quarter * 32, n0 = int64_t(tn) * 256 + half * 64;
-            Sums<128, COLS> sums;
+            Sums<128, COLS, true> sums;
             sums.clear();
             bool there = false;
             for (int kb = 0; kb < p.num_kb; ++kb) {
@@ -616,16 +616,15 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 // ------------------------------------------------------------------ tiles
 // One CTA: 128 rows of A, BN of B, the K blocks of its rank in the cluster.
 template <int BN> struct TileSmem {
-    static constexpr int kCtas = BN == 128 ? 1 : 2;  // an SM: 128 columns take too many registers for two
-    static constexpr int kAdders = BN == 128 ? 8 : 4, kFirst = 3, kThreads = 32 * (kFirst + kAdders);
-    static constexpr int kStage = kBox + BN * 128, kStages = BN == 128 ? 6 : 4;
+    static constexpr int kFirst = 4, kThreads = 32 * (kFirst + kEpiWarps);
+    static constexpr int kStage = kBox + BN * 128, kStages = BN == 128 ? 6 : BN == 64 ? 8 : 9;
     static constexpr int kBuffers = 4, kTmem = BN * kBuffers;
     static constexpr int kRow = BN + 4;  // floats of a row of sums: 16-byte stores by rows without bank conflicts
     static constexpr int kSlot = Slot<true, false>::kFloats > Slot<false, false>::kFloats ? Slot<true, false>::kFloats : Slot<false, false>::kFloats;
     static constexpr int kSlots = 8;
-    static constexpr int kBars = 512, kScratch = 2 * 4 * BN * 4;
+    static constexpr int kBars = 512, kScratch = kEpiWarps * 2 * BN * 4;
     static constexpr int kBytes = kStages * kStage + kScratch + kSlots * kSlot * 4 + kBars + 1024;
-    static_assert(128 * kRow * 4 <= kStages * kStage && kCtas * (kBytes + 1024) <= 228 * 1024, "CTAs per SM");
+    static_assert(128 * kRow * 4 <= kStages * kStage && kBytes <= 227 * 1024, "one CTA per SM");
     uint32_t ring, bar0;
     float *scratch, *scales;
     float *sums;  // in the ring's place, once it is empty
@@ -718,7 +717,7 @@ __device__ __forceinline__ void store_tile(const ScaledParams &p, const float *s
 }
 
 template <int BN, bool COLS>
-__global__ void __launch_bounds__(TileSmem<BN>::kThreads, TileSmem<BN>::kCtas)
+__global__ void __launch_bounds__(TileSmem<BN>::kThreads, 1)
 scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ ScaledParams p)
 {
@@ -732,10 +731,10 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
             mbar_init(sh.full(s), 1);
             mbar_init(sh.empty(s), 1);
         }
-        for (int i = 0; i < Smem::kBuffers; ++i) mbar_init(sh.acc_empty(i), Smem::kAdders);
+        for (int i = 0; i < Smem::kBuffers; ++i) mbar_init(sh.acc_empty(i), kEpiWarps / 2);
         for (int i = 0; i < Smem::kSlots; ++i) {
             mbar_init(sh.scale_full(i), 1);
-            mbar_init(sh.scale_empty(i), Smem::kAdders);
+            mbar_init(sh.scale_empty(i), kEpiWarps / 2);
         }
         mbar_init(sh.drain(), 1);
         *sh.abort_flag = 0;
@@ -758,109 +757,112 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     Ring ring(Smem::kStages);
     bool ok = true;
 
-    if (warp == 0) {
-        // ---------------- producer
-        const bool leader = elect_one();
-        for (int kb = kb0; kb < kb1; ++kb) {
-            ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
-            if (__any_sync(kFull, !ok)) {
-                ok = false;
-                break;
-            }
-            if (leader) {
-                mbar_expect_tx(sh.full(ring.stage), Smem::kStage);
-                if (!(p.inject_stall && kb == kb0)) {
-                    load_box<false>(sh.a(ring.stage), &map_a, sh.full(ring.stage), p.a_mn, int(m0), kb);
-                    load_box<false>(sh.b(ring.stage), &map_b, sh.full(ring.stage), p.b_mn, int(n0), kb);
+    if (warp < Smem::kFirst) {
+        if (BN == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+        if (warp == 0) {
+            // ---------------- producer, one lane
+            if (elect_one()) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
+                    if (!ok) break;
+                    mbar_expect_tx(sh.full(ring.stage), Smem::kStage);
+                    if (!(p.inject_stall && kb == kb0)) {
+                        load_box<false>(sh.a(ring.stage), &map_a, sh.full(ring.stage), p.a_mn, int(m0), kb);
+                        load_box<false>(sh.b(ring.stage), &map_b, sh.full(ring.stage), p.b_mn, int(n0), kb);
+                    }
+                    ring.next();
+                }
+                if (!ok) {  // copies in flight get time to land
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 2000000ull) {
+                    }
                 }
             }
-            __syncwarp();
-            ring.next();
-        }
-        if (!ok && leader) {  // copies in flight get time to land
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < 2000000ull) {
+        } else if (warp == 1) {
+            // ---------------- MMA issuer, one lane
+            if (elect_one()) {
+                const uint32_t idesc = f8_idesc(p, BN, 128), step_a = box_step(p.a_mn), step_b = box_step(p.b_mn);
+                const uint64_t a0 = box_desc(sh.a(0)), b0 = box_desc(sh.b(0));
+                Ring acc(Smem::kBuffers);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = watch.wait(sh.acc_empty(acc.stage), acc.phase ^ 1u);
+                    ok = ok && watch.wait(sh.full(ring.stage), ring.phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t a = a0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+                    const uint64_t b = b0 + uint32_t(ring.stage * (Smem::kStage >> 4));
+    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8<false>(tmem + uint32_t(acc.stage * BN), a + k * step_a, b + k * step_b, idesc, k > 0 ? 1u : 0u);
+                    umma_commit<false>(sh.empty(ring.stage));
+                    ring.next();
+                    acc.next();
+                }
+                if (!ok) {
+                    umma_commit<false>(sh.drain());
+                    const volatile int no_abort = 0;
+                    mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
+                }
             }
+        } else {
+            // ---------------- scales: two warps, in turn
+            const int mine = warp - 2;
+            ScaleCopies<COLS, false, BN, Smem::kSlots, 2, 1> copies(sh.scales, sh.scale_full(0), sh.scale_empty(0), lane, mine);
+            copies.begin(p, m0, n0, kb0 + mine);
+            for (int kb = kb0 + mine; ok && kb < kb1; kb += 2) ok = copies.copy(watch);
+            copies.finish();
         }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer
-        const bool leader = elect_one();
-        const uint32_t idesc = f8_idesc(p, BN, 128), step_a = box_step(p.a_mn), step_b = box_step(p.b_mn);
-        const uint64_t a0 = box_desc(sh.a(0)), b0 = box_desc(sh.b(0));
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            ok = watch.wait(sh.acc_empty(acc), acc_phase ^ 1u);
-            ok = ok && watch.wait(sh.full(ring.stage), ring.phase);
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-                const uint64_t a = a0 + uint32_t(ring.stage * (Smem::kStage >> 4));
-                const uint64_t b = b0 + uint32_t(ring.stage * (Smem::kStage >> 4));
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_f8<false>(tmem + uint32_t(acc * BN), a + k * step_a, b + k * step_b, idesc, k > 0 ? 1u : 0u);
-                umma_commit<false>(sh.empty(ring.stage));
-            }
-            __syncwarp();
-            ring.next();
-            if (++acc == Smem::kBuffers) {
-                acc = 0;
-                acc_phase ^= 1u;
-            }
-        }
-        if (!ok && leader) {
-            umma_commit<false>(sh.drain());
-            const volatile int no_abort = 0;
-            mbar_wait(sh.drain(), 0, &no_abort, 100000000ull);
-        }
-    } else if (warp == 2) {
-        // ---------------- scales
-        ScaleCopies<COLS, false, BN, Smem::kSlots, 1, 2> copies(sh.scales, sh.scale_full(0), sh.scale_empty(0), lane, 0);
-        copies.begin(p, m0, n0, kb0);
-        for (int kb = kb0; ok && kb < kb1; ++kb) ok = copies.copy(watch);
-        copies.finish();
     } else {
-        // ---------------- adding warps: rows 32 * quarter .., all of the columns or half of them
-        constexpr int kWide = BN * 4 / Smem::kAdders;
-        const int quarter = warp & 3, half = (warp - Smem::kFirst) >> 2;
-        float *scratch = sh.scratch + (warp - Smem::kFirst) * 2 * kWide;
-        const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(half * kWide);
-        Ring slot(Smem::kSlots), acc(Smem::kBuffers);
-        int added = -1;  // the slot of the block before
-        Sums<kWide, COLS> sums;
-        sums.clear();
+        if (BN == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+        // ---------------- adding warps: rows 32 * quarter .., every second block
+        const int quarter = warp & 3, group = (warp - Smem::kFirst) >> 2;
+        float *scratch = sh.scratch + (warp - Smem::kFirst) * 2 * BN;
+        const uint32_t taddr0 = tmem + (uint32_t(quarter * 32) << 16);
         using L = Slot<COLS, false>;
+        Sums<BN, COLS, false> sums;
+        sums.clear();
+        if (group == 1) ring.next();
         bool there = false;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            if (!there) ok = wait_both(watch, sh.scale_full(slot.stage), slot.phase, sh.empty(ring.stage), ring.phase);
+        for (int i = group; i < kb1 - kb0; i += 2) {
+            auto there_or = [&](int b, bool wait) {
+                const uint32_t scales = sh.scale_full(b & 7), full = sh.empty(ring.stage), phase = uint32_t(b >> 3) & 1u;
+                return wait ? wait_both(watch, scales, phase, full, ring.phase) : both_there(scales, phase, full, ring.phase);
+            };
+            if (!there) ok = there_or(i, true);
             if (!ok) break;
             tc_fence_after();
-            const float *at = sh.scales + slot.stage * L::kFloats;
-            const int now = acc.stage, reading = slot.stage;
             ring.next();
-            slot.next();
-            acc.next();
+            ring.next();
             sums.add(
-                taddr0 + uint32_t(now * BN), at, quarter * 32 + lane, half * kWide, scratch, lane,
-                [&] { there = kb + 1 < kb1 && both_there(sh.scale_full(slot.stage), slot.phase, sh.empty(ring.stage), ring.phase); },
+                taddr0 + uint32_t((i & 3) * BN), sh.scales + (i & 7) * L::kFloats, quarter * 32 + lane, 0, scratch, lane,
+                [&] { there = i + 2 < kb1 - kb0 && there_or(i + 2, false); },
                 [&] {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(sh.acc_empty(now));
-                        if (added >= 0) mbar_arrive(sh.scale_empty(added));
+                        mbar_arrive(sh.acc_empty(i & 3));
+                        if (i >= 2) mbar_arrive(sh.scale_empty((i - 2) & 7));  // of the block before
                     }
-                    added = reading;
                 });
         }
-        // every copy has landed and every MMA has been read: the ring's memory takes the sums
-        if (ok) {
-            float *to = sh.sums + (quarter * 32 + lane) * Smem::kRow + half * kWide;
+        // every copy has landed and every MMA of this group has been read; once both groups are here the ring's
+        // memory takes the sums, those of the even blocks first
+        float *to = sh.sums + (quarter * 32 + lane) * Smem::kRow;
+        const bool failed = __any_sync(kFull, !ok);
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+        if (group == 0 && !failed) {
 #pragma unroll
-            for (int i = 0; i < kWide; i += 4)
+            for (int i = 0; i < BN; i += 4)
                 *reinterpret_cast<float4 *>(to + i) =
                     make_float4(sums.at[i / 2].x, sums.at[i / 2].y, sums.at[i / 2 + 1].x, sums.at[i / 2 + 1].y);
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+        if (group == 1 && !failed && kb1 - kb0 > 1) {
+#pragma unroll
+            for (int i = 0; i < BN; i += 4) {
+                float4 &v = *reinterpret_cast<float4 *>(to + i);
+                v = make_float4(v.x + sums.at[i / 2].x, v.y + sums.at[i / 2].y, v.z + sums.at[i / 2 + 1].x, v.w + sums.at[i / 2 + 1].y);
+            }
         }
     }
     __syncwarp();
