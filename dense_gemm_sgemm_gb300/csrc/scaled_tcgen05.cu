@@ -973,20 +973,41 @@ struct Plan {
     int bn, splits;
 };
 
+// The form of least modelled time, in us.  A tile's CTA takes `base` (`swapped` more, to store turned) and `block` a
+// K block, the sum of a cluster's parts `join`; CTAs run one an SM.  A pair's tile takes 0.5 a block, 0.72 with
+// column scales.  Tiles' copies reach 5.5 TB/s.  Fitted to 35 shapes from 1 x 512 x 512 to 3000 x 4096 x 4096, each with up to 16 plans:
+// the plan taken is on average 3% slower than the fastest (64 x 8192 x 4096: 64 columns unsplit 11.7, the halves
+// of 128 columns 13.1, swapped 14.3; 1 x 4096 x 4096: swapped, 4 parts 8.1, 2 parts 8.4, unswapped 10.1).
 Plan plan_of(const DeviceInfo &dev, const ScaledArgs &a)
 {
-    Plan best{false, false, 128, 1};
-    const int64_t kb = (a.K + 127) / 128;
-    const int64_t t256 = ((a.M + 255) / 256) * ((a.N + 255) / 256), pairs = dev.num_sms / 2;
-    // the short side on the columns, where 32 or 64 of them hold it
-    const int64_t shorter = a.M < a.N ? a.M : a.N;
-    best.swap = a.M < a.N && a.M <= 64;
-    const ScaledOperand &b = best.swap ? a.a : a.b;
-    if (shorter <= 64 && !b.mn) best.bn = shorter <= 32 ? 32 : 64;
-    if (t256 >= pairs / 2 && shorter > 64) best.pairs = true;
-    const int64_t m = best.swap ? a.N : a.M, n = best.swap ? a.M : a.N;
-    const int64_t tiles = ((m + 127) / 128) * ((n + best.bn - 1) / best.bn);
-    while (best.splits < 8 && tiles * best.splits * 2 <= 2 * dev.num_sms && kb >= 4 * best.splits) best.splits *= 2;
+    struct Form {
+        int bn;
+        double base, swapped, block, cols, join;
+    };
+    static constexpr Form kForms[3] = {{32, 3.7, 0.8, 0.20, 0.04, 1.0}, {64, 3.9, 1.3, 0.25, 0.10, 1.7}, {128, 5.2, 2.0, 0.33, 0.06, 2.6}};
+    auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+    const int64_t kb = up(a.K, 128);
+    const double copies = double(a.M + a.N) * double(a.K) / 5.5e6;
+    const int64_t pairs = dev.num_sms / 2;
+    Plan best{true, false, 128, 1};
+    double least = 4.7 + double(up(up(a.M, 256) * up(a.N, 256), pairs)) * (double(kb) * (a.b.mn_shift == 0 ? 0.72 : 0.5) + 0.3);
+    for (int swap = 0; swap < 2; ++swap) {
+        const ScaledOperand &b = swap ? a.a : a.b;
+        const int64_t m = swap ? a.N : a.M, n = swap ? a.M : a.N;
+        for (const Form &f : kForms) {
+            if (f.bn < 128 && b.mn) continue;  // an operand stored K x N comes in boxes of 128 columns
+            const int64_t tiles = up(m, 128) * up(n, f.bn);
+            for (int splits = 1; splits <= 8 && splits <= kb; splits *= 2) {
+                const double blocks = double(up(kb, splits)) * (f.block + (b.mn_shift == 0 ? f.cols : 0.0));
+                const double waves = double(up(tiles * splits, dev.num_sms));
+                const double cost = waves * (f.base + (swap ? f.swapped : 0.0)) + (waves * blocks > copies ? waves * blocks : copies) + (splits > 1 ? f.join : 0.0);
+                if (cost < least) {
+                    least = cost;
+                    best = Plan{false, swap != 0, f.bn, splits};
+                }
+            }
+        }
+    }
     // GEMM_GB300_SCALED_PLAN (tests and sweeps): P for pairs, or BN:splits or BN:splits:s (operands swapped)
     if (const char *e = std::getenv("GEMM_GB300_SCALED_PLAN"); e && *e) {
         int bn = 0, splits = 0;

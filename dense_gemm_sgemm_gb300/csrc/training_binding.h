@@ -38,6 +38,12 @@ BlockScales scales_of(Device &device, PyObject *o, const Matrix &q, const char *
                        block_along(t.size(1), q.cols, what)};
 }
 
+// New memory of given strides (without the dispatcher's views: they cost a microsecond each).
+at::Tensor strided(at::IntArrayRef shape, at::IntArrayRef strides, at::ScalarType type, const at::Tensor &like)
+{
+    return at::Tensor(at::detail::empty_strided_cuda(shape, strides, type, like.device()));
+}
+
 // New 8-bit memory with rows on 16-byte pieces, and new scales for blocks of rows x cols: those of 1 x 128
 // with the rows next to one another, as the products read them.
 struct Quantized {
@@ -46,10 +52,9 @@ struct Quantized {
     Quantized(const Matrix &x, int rows, int cols, at::ScalarType type)
     {
         ld = std::max((x.cols + 15) & ~int64_t(15), int64_t(16));
-        q = fresh({x.rows, ld}, type, x.t);
-        if (ld != x.cols) q = q.narrow(1, 0, x.cols);
+        q = ld == x.cols ? fresh({x.rows, ld}, type, x.t) : strided({x.rows, x.cols}, {ld, 1}, type, x.t);
         const int64_t across = cols == 1 ? x.cols : blocks_of(x.cols), down = rows == 1 ? x.rows : blocks_of(x.rows);
-        s = rows == 1 ? fresh({across, down}, at::kFloat, x.t).t() : fresh({down, across}, at::kFloat, x.t);
+        s = rows == 1 ? strided({down, across}, {1, std::max(down, int64_t(1))}, at::kFloat, x.t) : fresh({down, across}, at::kFloat, x.t);
     }
 };
 
@@ -145,11 +150,12 @@ BOUND(orthogonalize, 6)
     const gemm_type_t y_type = type_of(dtype, "out_dtype");
     const int64_t count = t.dim() == 3 ? t.size(0) : 1, stride = t.dim() == 3 && count > 1 ? t.stride(0) : 0;
     const int64_t ld = std::max((x.cols + 7) & ~int64_t(7), int64_t(8));
-    at::Tensor y = t.dim() == 3 ? fresh({count, x.rows, ld}, dtype, t) : fresh({x.rows, ld}, dtype, t);
+    at::Tensor y = t.dim() == 3 ? strided({count, x.rows, x.cols}, {std::max(x.rows * ld, ld), ld, 1}, dtype, t)
+                                : strided({x.rows, x.cols}, {ld, 1}, dtype, t);
     at::Tensor work = fresh({gemm_orthogonalize_work_bytes(count, x.rows, x.cols)}, at::kByte, t);
     call("gemm_orthogonalize", [&] {
         return gemm_orthogonalize(type, y_type, count, x.rows, x.cols, x.data(), x.ld, stride, steps, coefficients, eps, y.data_ptr(), ld,
                                   x.rows * ld, work.data_ptr(), stream.handle);
     });
-    return wrap(ld == x.cols ? y : y.narrow(-1, 0, x.cols));
+    return wrap(y);
 END_BOUND

@@ -33,7 +33,7 @@ def quantize_blocks(x, block=(1, 128), *, dtype=torch.float8_e4m3fn, stream=None
     x rows x cols (fp32, fp16 or bf16); q of dtype (float8_e4m3fn or float8_e5m2) and x's shape; scales
     fp32, ceil(rows / block[0]) x ceil(cols / block[1]), powers of two.
     """
-    rows, cols = _one_of(_BLOCKS, tuple(block), "block")
+    rows, cols = _one_of(_BLOCKS, block if type(block) is tuple else tuple(block), "block")
     return _routed.quantize_blocks(x, rows, cols, dtype, stream)
 
 
