@@ -20,8 +20,9 @@
 // in fp16 or fp32 take three products of the parts (high high + high low + low high): 10^-4 at most, for
 // rank-one matrices, 10^-6 for most.  They run as three times the K slices.
 //
-// A and B are symmetric: only tiles on and below the diagonal are computed, each stored twice, which halves
-// two of the three products.
+// A and B are symmetric: only tiles on and below the diagonal are computed and stored, which halves two of the
+// three products.  What a product needs of the others it reads from the tile on the other side of the diagonal,
+// turned: the tensor cores take either order of an operand, slice by slice.
 //
 // Two forms, as the GEMM's: two CTAs on neighbouring SMs per 256 x 256 tile (cta_group::2), or one CTA per
 // 128 x 128 tile; persistent, two accumulators, so that a tile's epilogue runs beside the next one's MMAs.
@@ -53,6 +54,7 @@ struct StepParams {
     int64_t n, k, ldk, ldn;  // sides and rows of the work matrices
     int count, tiles_m, tiles_n, per, num_kb;  // tiles of a matrix, K slices of one product
     int products;            // 1, or 3 of the parts
+    int shift_a, shift_b;    // of a symmetric operand, whose tiles (of 2^shift) above the diagonal are not stored; else 0
     int64_t part_x, part_e;  // elements from the high part to the low one
     const __half *x, *e;
     float *d, *f;
@@ -83,6 +85,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
                      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
                      : "memory");
 }
+
+// Whether columns k .. of rows m .. of a symmetric operand stored in tiles on and below the diagonal lie above
+// it: they are read as rows k .. of columns m .., turned (MN-major).  m: the first row of the product's tile, for
+// both CTAs of a pair: where the operand's tiles are smaller, the second CTA's are then on the diagonal at most.
+__device__ __forceinline__ bool above(int k, int m, int shift) { return shift != 0 && k >> shift > m >> shift; }
 
 struct Smem {
     uint32_t ring, bar0;
@@ -150,26 +157,39 @@ struct Parts {
     __device__ __forceinline__ float low(int i) const { return __half2float(reinterpret_cast<const __half *>(l)[i]); }
 };
 
-// Stores 32 columns of a row as their fp16 parts, the low one too if it is wanted, and with mirror as 32 rows
-// of a column as well.
+// Stores 32 columns of a row as their fp16 parts, the low one too if it is wanted.
 __device__ __forceinline__ void store_parts(Staging<false> &staging, float (&v)[32], const CUtensorMap *map, int m0, int n0, int high,
-                                            int low, bool both, bool mirror)
+                                            int low, bool both)
 {
     store_rows<false>(staging, v, map, true, nullptr, 0, m0, n0, 0, 0, false, high);
-    if (mirror) store_rows<false, true>(staging, v, map, true, nullptr, 0, n0, m0, 0, 0, false, high);
     if (both) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] -= __half2float(__float2half_rn(v[i]));
+        for (int i = 0; i < 32; i += 2) {
+            const float2 h = __half22float2(__floats2half2_rn(v[i], v[i + 1]));
+            v[i] -= h.x;
+            v[i + 1] -= h.y;
+        }
         store_rows<false>(staging, v, map, true, nullptr, 0, m0, n0, 0, 0, false, low);
-        if (mirror) store_rows<false, true>(staging, v, map, true, nullptr, 0, n0, m0, 0, 0, false, low);
     }
+}
+// Moves the diagonal out of a 32 x 32 piece on it: this lane's element to `to`, zero in its place.
+__device__ __forceinline__ void take_diagonal(float (&v)[32], int lane, float *to, bool row)
+{
+    float d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (lane == i) {
+            d = v[i];
+            v[i] = 0.0f;
+        }
+    if (row) *to = d;
 }
 
 template <bool PAIR, int WHAT, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
 orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_in,
-                  const __grid_constant__ StepParams p)
+                  const __grid_constant__ CUtensorMap map_turned, const __grid_constant__ StepParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const Smem sh(smem_raw);
@@ -226,9 +246,11 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                         if (rank == 0) mbar_expect_tx(sh.full(ring.stage), (PAIR ? 2 : 1) * kStage);
                         if (!starve) {
                             const uint32_t full = full0 + 8u * ring.stage, a = sh.a(ring.stage), b = sh.b(ring.stage);
-                            if (PAIR) tma_load_3d_pair(a, &map_a, full, k, m0, plane_a);
+                            if (above(k, x.tm * kTile, p.shift_a)) tma_load_4d<PAIR>(a, &map_turned, full, 0, k, m0 / 64, plane_a);
+                            else if (PAIR) tma_load_3d_pair(a, &map_a, full, k, m0, plane_a);
                             else tma_load_3d(a, &map_a, full, k, m0, plane_a);
                             if (kTurnB) tma_load_4d<PAIR>(b, &map_b, full, 0, k, n0 / 64, plane_b);
+                            else if (above(k, x.tn * kTile, p.shift_b)) tma_load_4d<PAIR>(b, &map_turned, full, 0, k, n0 / 64, plane_b);
                             else if (PAIR) tma_load_3d_pair(b, &map_b, full, k, n0, plane_b);
                             else tma_load_3d(b, &map_b, full, k, n0, plane_b);
                         }
@@ -252,9 +274,9 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         if (rank == 0) {
             // ---------------- MMA issuer, one lane
             if (elect_one()) {
-                const uint32_t idesc = make_idesc(0, kTurnB, kTile, kTile);
-                const uint64_t a0 = smem_desc(sh.a(0), 16, 1024), b0 = smem_desc(sh.b(0), kTurnB ? kOperand / 2 : 16, 1024);
-                constexpr uint32_t kStepA = 32 >> 4, kStepB = (kTurnB ? 2048 : 32) >> 4;
+                // either operand by rows, or turned: its 64 k are rows of two blocks of 64 columns
+                const uint64_t by_rows = smem_desc(sh.ring, 16, 1024), turned = smem_desc(sh.ring, kOperand / 2, 1024);
+                const uint32_t idesc = make_idesc(0, 0, kTile, kTile);
                 auto commit = [&](uint32_t bar) {
                     if (PAIR) commit_both(bar);
                     else umma_commit<false>(bar);
@@ -264,15 +286,20 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + uint32_t(acc * kTile);
+                    const Unit x = unit_of<kSymmetric>(p, u);
                     uint32_t more = 0u;
-                    for (int i = 0; i < slices; ++i) {
+                    for (int i = 0, k = 0; i < slices; ++i, k = k + 64 == 64 * p.num_kb ? 0 : k + 64) {
                         ok = watch.wait(sh.full(ring.stage), ring.phase);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t a = a0 + uint32_t(ring.stage * (kStage >> 4)), b = b0 + uint32_t(ring.stage * (kStage >> 4));
+                        const bool turn_a = above(k, x.tm * kTile, p.shift_a), turn_b = kTurnB || above(k, x.tn * kTile, p.shift_b);
+                        const uint64_t a = (turn_a ? turned : by_rows) + uint32_t(ring.stage * (kStage >> 4));
+                        const uint64_t b = (turn_b ? turned : by_rows) + uint32_t(ring.stage * (kStage >> 4) + (kOperand >> 4));
+                        const uint32_t step_a = (turn_a ? 2048 : 32) >> 4, step_b = (turn_b ? 2048 : 32) >> 4;
+                        const uint32_t how = idesc | uint32_t(turn_a) << 15 | uint32_t(turn_b) << 16;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            umma_f16<PAIR>(d, a + k * kStepA, b + k * kStepB, idesc, more);
+                        for (int q = 0; q < 4; ++q) {
+                            umma_f16<PAIR>(d, a + q * step_a, b + q * step_b, how, more);
                             more = 1u;
                         }
                         commit(sh.empty(ring.stage));
@@ -300,7 +327,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         for (int u = first; u < units; u += step) {
             const Unit x = unit_of<kSymmetric>(p, u);
             const int m0 = x.tm * kTile + int(rank) * 128 + quarter * 32, m = m0 + lane;
-            const bool mirror = kSymmetric && x.tm != x.tn, row = m < p.n;
+            const bool row = m < p.n;
             // what the epilogue reads is on its way during the products and the stores before it
             Parts old;
             auto inside = [&](int n0) { return m0 < p.n && n0 < (kSymmetric ? p.n : p.k); };
@@ -342,40 +369,42 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     old.load(in, lane);
                 }
                 if constexpr (WHAT == kGram) {
+                    if (n0 == m0) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        v[i] *= scale;
-                        if (m == n0 + i) {
-                            if (row) p.d[x.which * p.ldn + m] = v[i];
-                            v[i] = 0.0f;
-                        }
-                        v[i] *= p.to;
+                        for (int i = 0; i < 32; ++i) v[i] *= scale;
+                        take_diagonal(v, lane, p.d + x.which * p.ldn + m, row);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] *= p.to;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = v[i] * scale * p.to;
                     }
-                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, mirror);
+                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true);
                 } else if constexpr (WHAT == kSquare) {
                     const float others = n0 + lane < p.n ? __ldcg(p.d + x.which * p.ldn + n0 + lane) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         // of A: E here, d on the diagonal, where E is 0; of A^2: (d_i + d_j) E + E E, d^2 + E E
-                        const bool diagonal = m == n0 + i;
-                        const float e = (old.high(i) + old.low(i)) * p.from_e, beside = three ? e : old.high(i) * p.from_e;
-                        const float other = __shfl_sync(kFull, others, i);
-                        const float square = fmaf(v[i], scale, diagonal ? mine * mine : beside * (mine + other));
-                        v[i] = fmaf(p.b, diagonal ? mine : e, p.c * square);
-                        if (diagonal) {
-                            if (row) p.f[x.which * p.ldn + m] = v[i];
-                            v[i] = 0.0f;
-                        }
-                        v[i] *= p.to;
+                        const float hi = old.high(i) * p.from_e, e = fmaf(old.low(i), p.from_e, hi);
+                        const float square = fmaf(three ? e : hi, mine + __shfl_sync(kFull, others, i), v[i] * scale);
+                        v[i] = fmaf(p.b, e, p.c * square);
                     }
+                    if (n0 == m0) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (lane == i) v[i] += fmaf(p.b, mine, p.c * mine * mine);
+                        take_diagonal(v, lane, p.f + x.which * p.ldn + m, row);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= p.to;
                     if (c + 32 < kHalf) fetch(n0 + 32);
-                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, three, mirror);
+                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, three);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(high, old.high(i), fmaf(low, old.low(i), v[i] * scale)) * p.to;
                     if (c + 32 < kHalf) fetch(n0 + 32);
                     if constexpr (WHAT == kUpdate) {
-                        store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, false);
+                        store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true);
                     } else {
                         uint8_t *Y = static_cast<uint8_t *>(p.Y) + x.which * p.stridey * (F32 ? 4 : 2);
                         constexpr bool kTurned = WHAT == kResultTurned;
@@ -441,7 +470,7 @@ bool pairs_pay(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool 
 }
 
 template <bool PAIR, int WHAT, bool F32>
-cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, StepParams p,
+cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, const CUtensorMap &turned, StepParams p,
                            int64_t columns, cudaStream_t stream)
 {
     constexpr int kTile = PAIR ? 256 : 128;
@@ -462,15 +491,14 @@ cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CU
     if (per * p.count >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     p.per = int(per);
     const int64_t units = per * p.count, grid = (units < room ? units : room) * (PAIR ? 2 : 1);
-    return launch_chained(kernel, dim3(unsigned(grid)), kThreads, kSmemBytes, PAIR ? 2 : 1, stream, a, b, out, in, p);
+    return launch_chained(kernel, dim3(unsigned(grid)), kThreads, kSmemBytes, PAIR ? 2 : 1, stream, a, b, out, in, turned, p);
 }
 template <int WHAT, bool F32 = false>
-cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, const StepParams &p,
+cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, const CUtensorMap &turned, const StepParams &p, bool pairs,
                            int64_t columns, cudaStream_t stream)
 {
-    return pairs_pay(dev, p.count, p.n, columns, WHAT <= kSquare, p.num_kb * p.products)
-               ? launch_product<true, WHAT, F32>(dev, a, b, out, in, p, columns, stream)
-               : launch_product<false, WHAT, F32>(dev, a, b, out, in, p, columns, stream);
+    return pairs ? launch_product<true, WHAT, F32>(dev, a, b, out, in, turned, p, columns, stream)
+                 : launch_product<false, WHAT, F32>(dev, a, b, out, in, turned, p, columns, stream);
 }
 
 }  // namespace
@@ -500,9 +528,10 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
     const float *unit = s.first ? reinterpret_cast<const float *>(w + l.unit) : nullptr;
-    CUtensorMap x_rows, x_cols, e_rows, f_rows, e_out, f_out, x_in, x_out, y_out;
+    CUtensorMap x_rows, x_cols, e_rows, e_cols, f_rows, f_cols, e_out, f_out, x_in, x_out, y_out;
     std::memset(&y_out, 0, sizeof(y_out));
-    if (!make_map16(&x_rows, p.x, l.n, l.k, l.ldk, 2 * l.count, 128) || !make_map_columns(&x_cols, p.x, l.n, l.ldk, 2 * l.count) ||
+    if (!make_map16(&x_rows, p.x, l.n, l.k, l.ldk, 2 * l.count, 128) || !make_map_columns(&x_cols, p.x, l.n, l.ldk, 2 * l.count) || !make_map_columns(&e_cols, p.e, l.n, l.ldn, 2 * l.count) ||
+        !make_map_columns(&f_cols, w + l.f, l.n, l.ldn, 2 * l.count) ||
         !make_map16(&e_rows, p.e, l.n, l.n, l.ldn, 2 * l.count, 128) || !make_map16(&f_rows, w + l.f, l.n, l.n, l.ldn, 2 * l.count, 128) ||
         !make_store_map(&e_out, w + l.e, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, 2 * l.count, l.n * l.ldn, true) ||
         !make_store_map(&f_out, w + l.f, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, 2 * l.count, l.n * l.ldn, true) ||
@@ -515,7 +544,9 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     gram.unit = unit;
     gram.from_acc = 1.0f / (s.x_scale * s.x_scale);
     gram.to = s.e_scale;
-    cudaError_t e = launch_product<kGram>(dev, x_rows, x_rows, e_out, x_in, gram, l.n, stream);
+    // the square's tiles are the Gram matrix's: what it reads beside them must be stored
+    const bool pairs = pairs_pay(dev, l.count, l.n, l.n, true, gram.num_kb * p.products);
+    cudaError_t e = launch_product<kGram>(dev, x_rows, x_rows, e_out, x_in, x_cols, gram, pairs, l.n, stream);
     if (e != cudaSuccess) return e;
 
     StepParams square = p;
@@ -523,7 +554,8 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     square.from_e = 1.0f / s.e_scale;
     square.from_acc = square.from_e * square.from_e;
     square.to = s.f_scale;
-    e = launch_product<kSquare>(dev, e_rows, e_rows, f_out, e_out, square, l.n, stream);
+    square.shift_a = square.shift_b = pairs ? 8 : 7;
+    e = launch_product<kSquare>(dev, e_rows, e_rows, f_out, e_out, e_cols, square, pairs, l.n, stream);
     if (e != cudaSuccess) return e;
 
     StepParams update = p;
@@ -532,7 +564,9 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     update.from_x = 1.0f / s.x_scale;
     update.from_acc = update.from_x / s.f_scale;
     update.to = s.last ? 1.0f : s.next_scale;
-    if (!s.last) return launch_product<kUpdate>(dev, f_rows, x_cols, x_out, x_in, update, l.k, stream);
+    update.shift_a = square.shift_a;
+    const bool wide = pairs_pay(dev, l.count, l.n, l.k, false, update.num_kb * p.products);
+    if (!s.last) return launch_product<kUpdate>(dev, f_rows, x_cols, x_out, x_in, f_cols, update, wide, l.k, stream);
     update.Y = a.Y;
     update.ldy = a.ldy;
     update.stridey = a.stridey;
@@ -541,10 +575,10 @@ cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &
     update.y_tma = make_store_map(&y_out, a.Y, a.y_type, a.rows, a.cols, a.ldy, l.count, a.stridey, true);
     update.y_bf16 = a.y_type == GEMM_TYPE_BF16;
     if (a.y_type == GEMM_TYPE_F32)
-        return a.rows > a.cols ? launch_product<kResultTurned, true>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream)
-                               : launch_product<kResult, true>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream);
-    return a.rows > a.cols ? launch_product<kResultTurned>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream)
-                           : launch_product<kResult>(dev, f_rows, x_cols, y_out, x_in, update, l.k, stream);
+        return a.rows > a.cols ? launch_product<kResultTurned, true>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream)
+                               : launch_product<kResult, true>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream);
+    return a.rows > a.cols ? launch_product<kResultTurned>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream)
+                           : launch_product<kResult>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream);
 }
 
 }  // namespace gemm

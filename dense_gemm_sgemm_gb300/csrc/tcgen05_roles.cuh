@@ -49,7 +49,12 @@ __device__ __forceinline__ uint16_t to_16(float v, bool bf16)
 
 __device__ __forceinline__ uint32_t pack_16(float lo, float hi, bool bf16)
 {
-    return uint32_t(to_16(lo, bf16)) | uint32_t(to_16(hi, bf16)) << 16;
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // Ring position of a role: stage and the parity its next phase completes.

@@ -75,7 +75,7 @@ def test_against_the_formula(g, monkeypatch, shape, pair):
     assert g.gemm_get_device_status() == 0
 
 
-@pytest.mark.parametrize("shape", [(2048, 1024), (1024, 4096), (2500, 2500)])
+@pytest.mark.parametrize("shape", [(2048, 1024), (1024, 4096), (2500, 2500), (1100, 1300), (1900, 900)])
 def test_large_matrices(g, shape):
     for kind in ("normal", "low"):
         m = matrix(*shape, kind)
