@@ -56,33 +56,32 @@ struct Squares {
     }
 };
 
-template <class T>
+// Thread: every so many 16-byte pieces of eight elements, four in flight.  I: what the pieces are counted in.
+template <class T, class I>
 __global__ void __launch_bounds__(kThreads)
-squares_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, int log_across, double *partial)
+squares_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, double *partial)
 {
     __shared__ double sums[kThreads / 32];
     chain_wait();
     const T *g = G + int64_t(blockIdx.y) * stride;
     Squares s;
-    // 8 elements of four rows at a time: rows y, y + tall, .., columns in pieces x, x + across, ..
-    const int across = 1 << log_across, x = threadIdx.x & (across - 1), tall = kThreads >> log_across;
-    const int64_t step = int64_t(gridDim.x) * tall;
-    for (int64_t r0 = int64_t(blockIdx.x) * tall + (threadIdx.x >> log_across); r0 < rows; r0 += 4 * step)
-        for (int64_t c = 8 * x; c < cols; c += 8 * across) {
-            float v[4][8];
+    const I pieces = I((cols + 7) / 8), total = I(rows) * pieces, step = I(gridDim.x) * kThreads;
+    for (I i0 = I(blockIdx.x) * kThreads + threadIdx.x; i0 < total; i0 += 4 * step) {
+        float v[4][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t r = r0 + i * step;
-                if (r < rows && wide && c + 8 <= cols) {
-                    load8<T>(g + r * ld + c, v[i]);
-                } else {
+        for (int q = 0; q < 4; ++q) {
+            const I i = i0 + I(q) * step, r = i / pieces;
+            const int64_t c = int64_t(i - r * pieces) * 8;
+            if (i < total && wide && c + 8 <= cols) {
+                load8<T>(g + int64_t(r) * ld + c, v[q]);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] = r < rows && c + j < cols ? to_f32(g[r * ld + c + j]) : 0.0f;
-                }
+                for (int j = 0; j < 8; ++j) v[q][j] = i < total && c + j < cols ? to_f32(g[int64_t(r) * ld + c + j]) : 0.0f;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s.add(v[i]);
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s.add(v[q]);
+    }
     double all = double(s.mid) + double(s.low) * 0x1p-172 + double(s.high) * 0x1p172;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
@@ -127,6 +126,21 @@ split_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride,
     __shared__ float factor[2];
     chain_wait();
     const int64_t which = blockIdx.z;
+    const T *g = G + which * stride;
+    __half *x = X + which * n * ldx;
+    const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
+    const int piece = threadIdx.x & 7, line = threadIdx.x >> 3;  // 8 elements of one of 32 rows
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t r = r0 + line + 32 * h, c = c0 + piece * 8;
+        if (r < rows && wide && c + 8 <= cols) {
+            load8<T>(g + r * ld + c, v[h]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[h][j] = r < rows && c + j < cols ? to_f32(g[r * ld + c + j]) : 0.0f;
+        }
+    }
     if (threadIdx.x < 32) {
         double s = 0.0;
         for (int i = threadIdx.x; i < blocks; i += 32) s += partial[which * kNormBlocks + i];
@@ -142,29 +156,18 @@ split_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride,
     }
     __syncthreads();
     const float f0 = factor[0], f1 = factor[1];
-    const T *g = G + which * stride;
-    __half *x = X + which * n * ldx;
-    const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
-    const int piece = threadIdx.x & 7, line = threadIdx.x >> 3;  // 8 elements of one of 32 rows
 #pragma unroll
-    for (int h = 0; h < 64; h += 32) {
-        const int64_t r = r0 + line + h, c = c0 + piece * 8;
-        float v[8];
-        if (r < rows && wide && c + 8 <= cols) {
-            load8<T>(g + r * ld + c, v);
-        } else {
+    for (int h = 0; h < 2; ++h) {
+        const int64_t r = r0 + line + 32 * h, c = c0 + piece * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = r < rows && c + j < cols ? to_f32(g[r * ld + c + j]) : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * f0 * f1;
+        for (int j = 0; j < 8; ++j) v[h][j] = v[h][j] * f0 * f1;
         if (TURN) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) tile[line + h][piece * 8 + j] = v[j];
+            for (int j = 0; j < 8; ++j) tile[line + 32 * h][piece * 8 + j] = v[h][j];
         } else if (r < rows && c < cols) {  // up to the padded row's end
             __half high[8], low[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) parts(v[j], high[j], low[j]);
+            for (int j = 0; j < 8; ++j) parts(v[h][j], high[j], low[j]);
             *reinterpret_cast<uint4 *>(x + r * ldx + c) = *reinterpret_cast<const uint4 *>(high);
             *reinterpret_cast<uint4 *>(x + part_stride + r * ldx + c) = *reinterpret_cast<const uint4 *>(low);
         }
@@ -191,12 +194,14 @@ template <class T> cudaError_t normalise(const OrthogonalArgs &a, const Orthogon
     const T *G = static_cast<const T *>(a.G);
     const int wide = reinterpret_cast<uintptr_t>(G) % 16 == 0 && a.ldg * int64_t(sizeof(T)) % 16 == 0 &&
                      (a.count == 1 || a.strideg * int64_t(sizeof(T)) % 16 == 0);
-    int log_across = 0;  // threads along a row
-    while (log_across < 8 && (8 << log_across) < a.cols) ++log_across;
-    const int64_t rows_a_block = 4 * (kThreads >> log_across), wanted = (a.rows + rows_a_block - 1) / rows_a_block;
+    const int64_t pieces = a.rows * ((a.cols + 7) / 8), wanted = (pieces + 4 * kThreads - 1) / (4 * kThreads);
     const int blocks = int(wanted < kNormBlocks ? wanted : kNormBlocks);  // whatever the count: a stack gives each matrix's own result
-    cudaError_t e = launch_chained(squares_kernel<T>, dim3(unsigned(blocks), unsigned(a.count)), kThreads, 0, 1, stream, a.rows, a.cols,
-                                   G, a.ldg, a.strideg, wide, log_across, partial);
+    const dim3 parts(unsigned(blocks), unsigned(a.count));
+    // 32-bit places leave room for the last step beyond the end
+    cudaError_t e = pieces < (int64_t(1) << 31) ? launch_chained(squares_kernel<T, unsigned>, parts, kThreads, 0, 1, stream, a.rows, a.cols, G,
+                                                                 a.ldg, a.strideg, wide, partial)
+                                                : launch_chained(squares_kernel<T, int64_t>, parts, kThreads, 0, 1, stream, a.rows, a.cols, G,
+                                                                 a.ldg, a.strideg, wide, partial);
     if (e != cudaSuccess) return e;
     const dim3 grid{unsigned((a.cols + 63) / 64), unsigned((a.rows + 63) / 64), unsigned(a.count)};
     return launch_chained(a.rows > a.cols ? split_kernel<T, true> : split_kernel<T, false>, grid, kThreads, 0, 1, stream, a.rows, a.cols,
