@@ -321,7 +321,7 @@ gemm_status_t gemm_orthogonalize(gemm_type_t type, gemm_type_t y_type, int64_t c
         if (!(std::fabs(a) <= 1e4f && std::fabs(b) <= 1e4f && std::fabs(c) <= 1e4f)) return GEMM_ERR_UNSUPPORTED;
         OrthogonalStep &p = plan[i];
         p = OrthogonalStep{a, b, c, i == 0 ? float(1 << kFirstScale) : plan[i - 1].next_scale, scale_for(r * r),
-                           scale_for(1.02 * largest_inner(b, c, r)), 1.0f, products, i == 0, i == steps - 1};
+                           scale_for(1.02 * largest_inner(b, c, r)), 1.0f, products};
         r = 1.02 * largest_value(a, b, c, r);
         if (!(r <= 1e4)) return GEMM_ERR_UNSUPPORTED;
         p.next_scale = scale_for(r);
@@ -338,7 +338,7 @@ gemm_status_t gemm_orthogonalize(gemm_type_t type, gemm_type_t y_type, int64_t c
     const OrthogonalArgs a{type, y_type, count, rows, cols, G, ldg, strideG, Y, ldy, strideY, eps, work};
     const OrthogonalLayout l = orthogonal_layout(count, rows, cols);
     cudaError_t e = launch_normalise(a, l, st);
-    for (int i = 0; e == cudaSuccess && i < steps; ++i) e = launch_orthogonal_step(dev, a, l, plan[i], i & 1, st);
+    if (e == cudaSuccess) e = launch_orthogonal_steps(dev, a, l, plan, steps, st);
     if (e != cudaSuccess) cudaGetLastError();
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }

@@ -33,15 +33,15 @@ struct OrthogonalArgs {
 constexpr int kFirstScale = 14;
 cudaError_t launch_normalise(const OrthogonalArgs &a, const OrthogonalLayout &l, cudaStream_t stream);
 
-// One step X' = (a + b A + c A^2) X, A = X X^T.  x_scale, e_scale, f_scale, next_scale: the powers of two by
+// A step X' = (a + b A + c A^2) X, A = X X^T.  x_scale, e_scale, f_scale, next_scale: the powers of two by
 // which the parts in memory are larger than what they stand for.
 struct OrthogonalStep {
     float a, b, c;
     float x_scale, e_scale, f_scale, next_scale;
-    int products;     // 1, or 3 of the parts
-    int first, last;  // first: X in memory is to be multiplied by 1 / c of its matrix
+    int products;  // 1, or 3 of the parts
 };
-cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &a, const OrthogonalLayout &l, const OrthogonalStep &s,
-                                   int from, cudaStream_t stream);
+// The first step's X in memory is to be multiplied by 1 / c of its matrix (unit), the last one writes Y.
+cudaError_t launch_orthogonal_steps(const DeviceInfo &dev, const OrthogonalArgs &a, const OrthogonalLayout &l, const OrthogonalStep *plan,
+                                    int steps, cudaStream_t stream);
 
 }  // namespace gemm

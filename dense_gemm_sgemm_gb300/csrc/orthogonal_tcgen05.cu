@@ -24,7 +24,7 @@
 // three products.  What a product needs of the others it reads from the tile on the other side of the diagonal,
 // turned: the tensor cores take either order of an operand, slice by slice.
 //
-// Two forms, as the GEMM's: two CTAs on neighbouring SMs per 256 x 256 tile (cta_group::2), or one CTA per
+// Three forms: two CTAs on neighbouring SMs per tile of 256 x 256 or 256 x 128 (cta_group::2), or one CTA per
 // 128 x 128 tile; persistent, two accumulators, so that a tile's epilogue runs beside the next one's MMAs.
 // Every wait is bounded: when one expires the kernel raises the device's error word, stops all roles, waits
 // (bounded) for its own copies and MMAs in flight, frees its TMEM and returns.
@@ -42,21 +42,26 @@
 namespace gemm {
 namespace {
 
-constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
-constexpr int kOperand = 128 * 128, kStage = 2 * kOperand, kStages = 5;  // bytes: 128 rows of 64 fp16 of either operand
+constexpr int kEpiWarps = 8, kFirst = 3, kThreads = 32 * (kFirst + kEpiWarps);  // kFirst: the first epilogue warp
+constexpr int kOperandA = 128 * 128;  // bytes: 128 rows of 64 fp16
 constexpr int kEpi = kEpiWarps * 4096, kIn = kEpiWarps * 4096, kBars = 256;  // what the epilogue stores, and reads
-constexpr int kSmemBytes = kStages * kStage + kEpi + kIn + kBars + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+// The forms: a CTA's 128 x 128, a pair's 256 x 128, a pair's 256 x 256.
+template <int FORM> struct Shape {
+    static constexpr bool kPair = FORM > 0;
+    static constexpr int kM = kPair ? 256 : 128, kN = FORM == 2 ? 256 : 128, kRowsB = kPair ? kN / 2 : kN;  // rows of B a CTA holds
+    static constexpr int kStage = kOperandA + kRowsB * 128, kStages = FORM == 1 ? 6 : 5;
+    static constexpr int kBytes = kStages * kStage + kEpi + kIn + kBars + 1024;
+    static_assert(kBytes <= 227 * 1024, "one CTA per SM");
+};
+constexpr int kMostBytes = Shape<2>::kBytes;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kGram = 0, kSquare = 1, kUpdate = 2, kResult = 3, kResultTurned = 4;
 
 struct StepParams {
-    int64_t n, k, ldk, ldn;  // sides and rows of the work matrices
+    int64_t n, k, ldn;       // sides, and distance of two matrices' diagonals
     int count, tiles_m, tiles_n, per, num_kb;  // tiles of a matrix, K slices of one product
     int products;            // 1, or 3 of the parts
     int shift_a, shift_b;    // of a symmetric operand, whose tiles (of 2^shift) above the diagonal are not stored; else 0
-    int64_t part_x, part_e;  // elements from the high part to the low one
-    const __half *x, *e;
     float *d, *f;
     const float *unit;  // NULL: 1
     float a, b, c;
@@ -91,7 +96,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // both CTAs of a pair: where the operand's tiles are smaller, the second CTA's are then on the diagonal at most.
 __device__ __forceinline__ bool above(int k, int m, int shift) { return shift != 0 && k >> shift > m >> shift; }
 
-struct Smem {
+template <int FORM> struct Smem {
+    static constexpr int kStages = Shape<FORM>::kStages, kStage = Shape<FORM>::kStage;
     uint32_t ring, bar0;
     uint8_t *epi, *in;
     volatile uint32_t *tmem_slot;
@@ -115,24 +121,26 @@ struct Smem {
     __device__ __forceinline__ uint32_t fetched(int w) const { return bar0 + 8u * (2 * kStages + 4 + w); }
     __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4 + kEpiWarps); }
     __device__ __forceinline__ uint32_t a(int s) const { return ring + uint32_t(s * kStage); }
-    __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kOperand; }
+    __device__ __forceinline__ uint32_t b(int s) const { return a(s) + kOperandA; }
 };
 
-// Unit u: a matrix and a tile of it; of the symmetric products the tiles on and below the diagonal.
+// Unit u: a matrix and a tile of it; of the symmetric products the tiles on and below the diagonal, of which a
+// row of tiles has W = kM / kN more than the one before (the last columns of the last row may lie outside).
 struct Unit {
     int which, tm, tn;
 };
-template <bool SYMMETRIC> __device__ __forceinline__ Unit unit_of(const StepParams &p, int u)
+template <bool SYMMETRIC, int W> __device__ __forceinline__ Unit unit_of(const StepParams &p, int u)
 {
     Unit x;
     x.which = u / p.per;
     const int t = u - x.which * p.per;
     if (SYMMETRIC) {
-        int m = int((sqrtf(8.0f * float(t) + 1.0f) - 1.0f) * 0.5f);
-        while (m * (m + 1) / 2 > t) --m;
-        while ((m + 1) * (m + 2) / 2 <= t) ++m;
+        const float s = float(t) / W;
+        int m = int((sqrtf(8.0f * s + 1.0f) - 1.0f) * 0.5f);
+        while (W * (m * (m + 1) / 2) > t) --m;
+        while (W * ((m + 1) * (m + 2) / 2) <= t) ++m;
         x.tm = m;
-        x.tn = t - m * (m + 1) / 2;
+        x.tn = t - W * (m * (m + 1) / 2);
     } else {  // groups of eight tile rows share their columns of X in L2
         const int group = t / (8 * p.tiles_n), rows = min(8, p.tiles_m - 8 * group), r = t - group * 8 * p.tiles_n;
         x.tm = 8 * group + r % rows;
@@ -185,16 +193,20 @@ __device__ __forceinline__ void take_diagonal(float (&v)[32], int lane, float *t
     if (row) *to = d;
 }
 
-template <bool PAIR, int WHAT, bool F32>
+template <int FORM, int WHAT, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
 orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_in,
-                  const __grid_constant__ CUtensorMap map_turned, const __grid_constant__ StepParams p)
+                  const __grid_constant__ CUtensorMap turned_a, const __grid_constant__ CUtensorMap turned_b,
+                  const __grid_constant__ StepParams p)
 {
     extern __shared__ uint8_t smem_raw[];
-    const Smem sh(smem_raw);
+    using S = Shape<FORM>;
+    const Smem<FORM> sh(smem_raw);
+    constexpr bool PAIR = S::kPair;
+    constexpr int kStage = S::kStage, kStages = S::kStages;
     constexpr bool kSymmetric = WHAT <= kSquare, kTurnB = !kSymmetric;  // B = X is stored K x N
-    constexpr int kTile = PAIR ? 256 : 128, kTmem = 2 * kTile, kHalf = kTile / 2;  // kHalf: columns of an epilogue warp
+    constexpr int kTmem = 2 * S::kN, kHalf = S::kN / 2;  // kHalf: columns of an epilogue warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     if (threadIdx.x == 0) {
@@ -228,31 +240,30 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     uint32_t acc_phase = 0;
     bool ok = true;
 
-    if (warp == 0) {
-        // ---------------- producer, one lane: 128 rows of A, 128 rows (or columns of K x N) of B
+    if (warp == 0 || warp == 2) {
+        // ---------------- producers, one lane each: 128 rows of A; rows of B (or columns of K x N).  (One for both
+        // takes longer to issue a slice's copies than the tensor cores to multiply it.)
         if (elect_one()) {
-            tma_prefetch_desc(&map_a);
-            tma_prefetch_desc(&map_b);
+            const bool of_a = warp == 0;
+            tma_prefetch_desc(of_a ? &map_a : &map_b);
             const uint32_t full0 = PAIR ? map_to_rank(sh.full(0), 0) : sh.full(0);
             bool starve = p.inject_stall != 0;
             for (int u = first; ok && u < units; u += step) {
-                const Unit x = unit_of<kSymmetric>(p, u);
-                const int m0 = x.tm * kTile + int(rank) * 128, n0 = x.tn * kTile + int(rank) * 128;
+                const Unit x = unit_of<kSymmetric, S::kM / S::kN>(p, u);
+                const int row = of_a ? x.tm * S::kM + int(rank) * 128 : x.tn * S::kN + int(rank) * S::kRowsB;
+                const int of_tile = of_a ? x.tm * S::kM : x.tn * S::kN, shift = of_a ? p.shift_a : p.shift_b;
                 for (int product = 0; ok && product < p.products; ++product) {  // high high, high low, low high
-                    const int plane_a = x.which + (product == 2 ? p.count : 0), plane_b = x.which + (product == 1 ? p.count : 0);
+                    const int plane = x.which + (product == (of_a ? 2 : 1) ? p.count : 0);
                     for (int k = 0; k < 64 * p.num_kb; k += 64) {
                         ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                         if (!ok) break;
-                        if (rank == 0) mbar_expect_tx(sh.full(ring.stage), (PAIR ? 2 : 1) * kStage);
+                        if (of_a && rank == 0) mbar_expect_tx(sh.full(ring.stage), (PAIR ? 2 : 1) * kStage);
                         if (!starve) {
-                            const uint32_t full = full0 + 8u * ring.stage, a = sh.a(ring.stage), b = sh.b(ring.stage);
-                            if (above(k, x.tm * kTile, p.shift_a)) tma_load_4d<PAIR>(a, &map_turned, full, 0, k, m0 / 64, plane_a);
-                            else if (PAIR) tma_load_3d_pair(a, &map_a, full, k, m0, plane_a);
-                            else tma_load_3d(a, &map_a, full, k, m0, plane_a);
-                            if (kTurnB) tma_load_4d<PAIR>(b, &map_b, full, 0, k, n0 / 64, plane_b);
-                            else if (above(k, x.tn * kTile, p.shift_b)) tma_load_4d<PAIR>(b, &map_turned, full, 0, k, n0 / 64, plane_b);
-                            else if (PAIR) tma_load_3d_pair(b, &map_b, full, k, n0, plane_b);
-                            else tma_load_3d(b, &map_b, full, k, n0, plane_b);
+                            const uint32_t full = full0 + 8u * ring.stage, dst = of_a ? sh.a(ring.stage) : sh.b(ring.stage);
+                            if ((!of_a && kTurnB) || above(k, of_tile, shift))
+                                tma_load_4d<PAIR>(dst, of_a ? &turned_a : kTurnB ? &map_b : &turned_b, full, 0, k, row / 64, plane);
+                            else if (PAIR) tma_load_3d_pair(dst, of_a ? &map_a : &map_b, full, k, row, plane);
+                            else tma_load_3d(dst, of_a ? &map_a : &map_b, full, k, row, plane);
                         }
                         starve = false;
                         ring.next();
@@ -263,7 +274,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 const uint64_t t0 = global_timer_ns();
                 while (global_timer_ns() - t0 < 2000000ull) {
                 }
-            } else {  // no commit is on its way to this CTA's barriers when it exits
+            } else if (of_a) {  // no commit is on its way to this CTA's barriers when it exits
                 for (int i = 0; i < kStages; ++i) {
                     if (!watch.wait(sh.empty(ring.stage), ring.phase ^ 1u)) break;
                     ring.next();
@@ -275,8 +286,8 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             // ---------------- MMA issuer, one lane
             if (elect_one()) {
                 // either operand by rows, or turned: its 64 k are rows of two blocks of 64 columns
-                const uint64_t by_rows = smem_desc(sh.ring, 16, 1024), turned = smem_desc(sh.ring, kOperand / 2, 1024);
-                const uint32_t idesc = make_idesc(0, 0, kTile, kTile);
+                const uint64_t by_rows = smem_desc(sh.ring, 16, 1024), turned = smem_desc(sh.ring, kOperandA / 2, 1024);
+                const uint32_t idesc = make_idesc(0, 0, S::kN, S::kM);
                 auto commit = [&](uint32_t bar) {
                     if (PAIR) commit_both(bar);
                     else umma_commit<false>(bar);
@@ -285,16 +296,16 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     ok = watch.wait<true>(sh.acc_empty(acc), acc_phase ^ 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + uint32_t(acc * kTile);
-                    const Unit x = unit_of<kSymmetric>(p, u);
+                    const uint32_t d = tmem + uint32_t(acc * S::kN);
+                    const Unit x = unit_of<kSymmetric, S::kM / S::kN>(p, u);
                     uint32_t more = 0u;
                     for (int i = 0, k = 0; i < slices; ++i, k = k + 64 == 64 * p.num_kb ? 0 : k + 64) {
                         ok = watch.wait(sh.full(ring.stage), ring.phase);
                         if (!ok) break;
                         tc_fence_after();
-                        const bool turn_a = above(k, x.tm * kTile, p.shift_a), turn_b = kTurnB || above(k, x.tn * kTile, p.shift_b);
+                        const bool turn_a = above(k, x.tm * S::kM, p.shift_a), turn_b = kTurnB || above(k, x.tn * S::kN, p.shift_b);
                         const uint64_t a = (turn_a ? turned : by_rows) + uint32_t(ring.stage * (kStage >> 4));
-                        const uint64_t b = (turn_b ? turned : by_rows) + uint32_t(ring.stage * (kStage >> 4) + (kOperand >> 4));
+                        const uint64_t b = (turn_b ? turned : by_rows) + uint32_t(ring.stage * (kStage >> 4) + (kOperandA >> 4));
                         const uint32_t step_a = (turn_a ? 2048 : 32) >> 4, step_b = (turn_b ? 2048 : 32) >> 4;
                         const uint32_t how = idesc | uint32_t(turn_a) << 15 | uint32_t(turn_b) << 16;
 #pragma unroll
@@ -319,14 +330,14 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         }
     } else {
         // ---------------- epilogue: rows 32 * quarter .. of this CTA's 128, half of the tile's columns
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        Staging<F32> staging(sh.epi + (warp - 2) * 4096, lane);
-        const uint8_t *in = sh.in + (warp - 2) * 4096;
+        const int quarter = warp & 3, half = (warp - kFirst) >> 2;
+        Staging<F32> staging(sh.epi + (warp - kFirst) * 4096, lane);
+        const uint8_t *in = sh.in + (warp - kFirst) * 4096;
         uint32_t in_phase = 0;
         const uint32_t acc_empty0 = PAIR ? map_to_rank(sh.acc_empty(0), 0) : sh.acc_empty(0);
         for (int u = first; u < units; u += step) {
-            const Unit x = unit_of<kSymmetric>(p, u);
-            const int m0 = x.tm * kTile + int(rank) * 128 + quarter * 32, m = m0 + lane;
+            const Unit x = unit_of<kSymmetric, S::kM / S::kN>(p, u);
+            const int m0 = x.tm * S::kM + int(rank) * 128 + quarter * 32, m = m0 + lane;
             const bool row = m < p.n;
             // what the epilogue reads is on its way during the products and the stores before it
             Parts old;
@@ -335,13 +346,13 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 if (WHAT == kGram || !inside(n0)) return;
                 __syncwarp();  // the boxes before have been read
                 if (lane == 0) {
-                    const uint32_t dst = smem_u32(in), bar = sh.fetched(warp - 2);
+                    const uint32_t dst = smem_u32(in), bar = sh.fetched(warp - kFirst);
                     mbar_expect_tx(bar, 4096);
                     tma_load_3d(dst, &map_in, bar, n0, m0, x.which);
                     tma_load_3d(dst + 2048, &map_in, bar, n0, m0, p.count + x.which);
                 }
             };
-            fetch(x.tn * kTile + half * kHalf);
+            fetch(x.tn * S::kN + half * kHalf);
             const float unit = p.unit != nullptr ? __ldg(p.unit + x.which) : 1.0f;
             float mine = 0.0f;  // d or f of this row
             if (WHAT == kSquare && row) mine = __ldcg(p.d + x.which * p.ldn + m);
@@ -349,13 +360,13 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             ok = __all_sync(kFull, watch.wait(sh.acc_full(acc), acc_phase));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * kTile + half * kHalf);
+            const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * S::kN + half * kHalf);
             const float scale = WHAT == kGram ? p.from_acc * unit * unit : WHAT == kSquare ? p.from_acc : p.from_acc * unit;
             const bool three = p.products == 3;
             const float from_x = p.from_x * unit, high = (p.a + mine) * from_x, low = three ? high : p.a * from_x;  // kUpdate
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
-                const int n0 = x.tn * kTile + half * kHalf + c;
+                const int n0 = x.tn * S::kN + half * kHalf + c;
                 const bool wanted = inside(n0);
                 float v[32];
                 __syncwarp();
@@ -363,7 +374,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 if (c + 32 >= kHalf) release_accumulator(acc_empty0 + 8u * acc, lane);
                 if (!wanted) continue;
                 if (WHAT != kGram) {
-                    ok = __all_sync(kFull, watch.wait(sh.fetched(warp - 2), in_phase));
+                    ok = __all_sync(kFull, watch.wait(sh.fetched(warp - kFirst), in_phase));
                     if (!ok) break;
                     in_phase ^= 1u;
                     old.load(in, lane);
@@ -439,146 +450,185 @@ bool make_map16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, i
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-// The same matrices read as K x N operands, two blocks of 64 columns x 64 rows a box.  Columns between the
+// The same matrices read as K x N operands, `blocks` blocks of 64 columns x 64 rows a box.  Columns between the
 // matrix's end and its padded rows' end are read as they are: they only meet columns of the result beyond it.
-bool make_map_columns(CUtensorMap *map, const void *ptr, int64_t rows, int64_t ld, int64_t count)
+bool make_map_columns(CUtensorMap *map, const void *ptr, int64_t rows, int64_t ld, int64_t count, int blocks)
 {
     auto fn = tensor_map_encoder();
     if (fn == nullptr) return false;
     const cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(ld / 64), cuuint64_t(count)};
     const cuuint64_t strides[3] = {cuuint64_t(ld) * 2, 128, cuuint64_t(ld) * cuuint64_t(rows) * 2};
-    const cuuint32_t box[4] = {64, 64, 2, 1}, steps[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 64, cuuint32_t(blocks), 1}, steps[4] = {1, 1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Pairs of SMs where the tiles' waves cost less.  A slice of 64 k takes a pair 560 SM cycles, a single CTA
-// 330; a tile costs about 8 slices more than it has.
-bool pairs_pay(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool symmetric, int64_t slices)
+int rows_b(int form) { return form == 1 ? 64 : 128; }
+
+// The form whose tiles' waves cost least.  A slice of 64 k takes 600 SM cycles of a pair on 256 x 256, 420 on
+// 256 x 128, and of single CTAs 560 where they keep L2 busy, 330 where there are few; a tile costs about 8 slices
+// more than it has.  (2048 x 4096: Gram matrix in 128 x 128 20.7 us; 4096 x 4096: update in 256 x 256 93 us.)
+int form_of(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool symmetric, int64_t slices)
 {
-    auto tiles = [&](int64_t t) {
-        const int64_t i = (m + t - 1) / t, j = (n + t - 1) / t;
-        return count * (symmetric ? i * (i + 1) / 2 : i * j);
-    };
-    const int64_t pairs = dev.num_sms / 2;
-    const double two = double((tiles(256) + pairs - 1) / pairs) * double(slices + 8) * 560.0;
-    const double one = double((tiles(128) + dev.num_sms - 1) / dev.num_sms) * double(slices + 8) * 330.0;
-    // GEMM_GB300_ORTHOGONAL_PAIR=0|1 (tests and sweeps): never, or always
-    if (const char *e = std::getenv("GEMM_GB300_ORTHOGONAL_PAIR"); e && (*e == '0' || *e == '1')) return *e == '1';
-    return two < one;
+    // GEMM_GB300_ORTHOGONAL_FORM=0|1|2 (tests and sweeps): always this one
+    if (const char *e = std::getenv("GEMM_GB300_ORTHOGONAL_FORM"); e && *e >= '0' && *e <= '2') return *e - '0';
+    int best = 0;
+    double least = 1e300;
+    for (int form = 0; form < 3; ++form) {
+        const int64_t tm = form ? 256 : 128, tn = form == 2 ? 256 : 128, i = (m + tm - 1) / tm, j = (n + tn - 1) / tn;
+        const int64_t tiles = count * (symmetric ? tm / tn * i * (i + 1) / 2 : i * j), room = form ? dev.num_sms / 2 : dev.num_sms;
+        const double slice = form == 2 ? 600.0 : form == 1 ? 420.0 : tiles > room / 2 ? 560.0 : 330.0;
+        const double cost = double((tiles + room - 1) / room) * double(slices + 8) * slice;
+        if (cost < least) {
+            least = cost;
+            best = form;
+        }
+    }
+    return best;
 }
 
-template <bool PAIR, int WHAT, bool F32>
-cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, const CUtensorMap &turned, StepParams p,
-                           int64_t columns, cudaStream_t stream)
+struct ProductMaps {
+    CUtensorMap a, b, out, in, turned_a, turned_b;
+};
+
+template <int FORM, int WHAT, bool F32>
+cudaError_t launch_form(const DeviceInfo &dev, const ProductMaps &maps, StepParams p, int64_t columns, cudaStream_t stream)
 {
-    constexpr int kTile = PAIR ? 256 : 128;
-    auto *kernel = orthogonal_kernel<PAIR, WHAT, F32>;
+    using S = Shape<FORM>;
+    auto *kernel = orthogonal_kernel<FORM, WHAT, F32>;
     int room;
-    if (PAIR) {
+    if (S::kPair) {
         static std::atomic<int> cache[64];
-        room = resident_pairs(kernel, kThreads, kSmemBytes, dev.device, cache);
+        room = resident_pairs(kernel, kThreads, S::kBytes, dev.device, cache);
         if (room <= 0) return cudaErrorInitializationError;
     } else {
-        const cudaError_t e = allow_smem_once(kernel, kSmemBytes);
+        const cudaError_t e = allow_smem_once(kernel, S::kBytes);
         if (e != cudaSuccess) return e;
         room = dev.num_sms;
     }
-    p.tiles_m = int((p.n + kTile - 1) / kTile);
-    p.tiles_n = int((columns + kTile - 1) / kTile);
-    const int64_t per = WHAT <= kSquare ? int64_t(p.tiles_m) * (p.tiles_m + 1) / 2 : int64_t(p.tiles_m) * p.tiles_n;
+    p.tiles_m = int((p.n + S::kM - 1) / S::kM);
+    p.tiles_n = int((columns + S::kN - 1) / S::kN);
+    const int64_t per = WHAT <= kSquare ? int64_t(S::kM / S::kN) * p.tiles_m * (p.tiles_m + 1) / 2 : int64_t(p.tiles_m) * p.tiles_n;
     if (per * p.count >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     p.per = int(per);
-    const int64_t units = per * p.count, grid = (units < room ? units : room) * (PAIR ? 2 : 1);
-    return launch_chained(kernel, dim3(unsigned(grid)), kThreads, kSmemBytes, PAIR ? 2 : 1, stream, a, b, out, in, turned, p);
+    const int64_t units = per * p.count, grid = (units < room ? units : room) * (S::kPair ? 2 : 1);
+    return launch_chained(kernel, dim3(unsigned(grid)), kThreads, S::kBytes, S::kPair ? 2 : 1, stream, maps.a, maps.b, maps.out, maps.in,
+                          maps.turned_a, maps.turned_b, p);
 }
 template <int WHAT, bool F32 = false>
-cudaError_t launch_product(const DeviceInfo &dev, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &out, const CUtensorMap &in, const CUtensorMap &turned, const StepParams &p, bool pairs,
-                           int64_t columns, cudaStream_t stream)
+cudaError_t launch_product(const DeviceInfo &dev, int form, const ProductMaps &maps, const StepParams &p, int64_t columns, cudaStream_t stream)
 {
-    return pairs ? launch_product<true, WHAT, F32>(dev, a, b, out, in, turned, p, columns, stream)
-                 : launch_product<false, WHAT, F32>(dev, a, b, out, in, turned, p, columns, stream);
+    if (form == 0) return launch_form<0, WHAT, F32>(dev, maps, p, columns, stream);
+    if (form == 1) return launch_form<1, WHAT, F32>(dev, maps, p, columns, stream);
+    return launch_form<2, WHAT, F32>(dev, maps, p, columns, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_orthogonal_step(const DeviceInfo &dev, const OrthogonalArgs &a, const OrthogonalLayout &l, const OrthogonalStep &s,
-                                   int from, cudaStream_t stream)
+cudaError_t launch_orthogonal_steps(const DeviceInfo &dev, const OrthogonalArgs &a, const OrthogonalLayout &l, const OrthogonalStep *plan,
+                                    int steps, cudaStream_t stream)
 {
     unsigned int *status = device_status_word(dev.device);
-    if (status == nullptr || dev.smem_optin < size_t(kSmemBytes)) return cudaErrorInitializationError;
+    if (status == nullptr || dev.smem_optin < size_t(kMostBytes)) return cudaErrorInitializationError;
     char *w = static_cast<char *>(a.work);
     StepParams p{};
     p.n = l.n;
     p.k = l.k;
-    p.ldk = l.ldk;
     p.ldn = l.ldn;
     p.count = int(l.count);
-    p.part_x = l.count * l.n * l.ldk;
-    p.part_e = l.count * l.n * l.ldn;
-    p.x = reinterpret_cast<const __half *>(w + l.x[from]);
-    p.e = reinterpret_cast<const __half *>(w + l.e);
     p.d = reinterpret_cast<float *>(w + l.dd);
     p.f = reinterpret_cast<float *>(w + l.df);
-    p.products = s.products;
-    p.a = s.a;
-    p.b = s.b;
-    p.c = s.c;
+    p.products = plan[0].products;
+    p.Y = a.Y;
+    p.ldy = a.ldy;
+    p.stridey = a.stridey;
+    p.y_rows = a.rows;
+    p.y_cols = a.cols;
+    p.y_bf16 = a.y_type == GEMM_TYPE_BF16;
     p.status = status;
     test_hooks(p.timeout_ns, p.inject_stall);
-    const float *unit = s.first ? reinterpret_cast<const float *>(w + l.unit) : nullptr;
-    CUtensorMap x_rows, x_cols, e_rows, e_cols, f_rows, f_cols, e_out, f_out, x_in, x_out, y_out;
-    std::memset(&y_out, 0, sizeof(y_out));
-    if (!make_map16(&x_rows, p.x, l.n, l.k, l.ldk, 2 * l.count, 128) || !make_map_columns(&x_cols, p.x, l.n, l.ldk, 2 * l.count) || !make_map_columns(&e_cols, p.e, l.n, l.ldn, 2 * l.count) ||
-        !make_map_columns(&f_cols, w + l.f, l.n, l.ldn, 2 * l.count) ||
-        !make_map16(&e_rows, p.e, l.n, l.n, l.ldn, 2 * l.count, 128) || !make_map16(&f_rows, w + l.f, l.n, l.n, l.ldn, 2 * l.count, 128) ||
-        !make_store_map(&e_out, w + l.e, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, 2 * l.count, l.n * l.ldn, true) ||
-        !make_store_map(&f_out, w + l.f, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, 2 * l.count, l.n * l.ldn, true) ||
-        !make_store_map(&x_in, w + l.x[from], GEMM_TYPE_F16, l.n, l.ldk, l.ldk, 2 * l.count, l.n * l.ldk, true) ||
-        !make_store_map(&x_out, w + l.x[from ^ 1], GEMM_TYPE_F16, l.n, l.ldk, l.ldk, 2 * l.count, l.n * l.ldk, true))
-        return cudaErrorInvalidValue;
-
-    StepParams gram = p;
-    gram.num_kb = int((l.k + 63) / 64);
-    gram.unit = unit;
-    gram.from_acc = 1.0f / (s.x_scale * s.x_scale);
-    gram.to = s.e_scale;
+    const int slices_k = int((l.k + 63) / 64), slices_n = int((l.n + 63) / 64);
     // the square's tiles are the Gram matrix's: what it reads beside them must be stored
-    const bool pairs = pairs_pay(dev, l.count, l.n, l.n, true, gram.num_kb * p.products);
-    cudaError_t e = launch_product<kGram>(dev, x_rows, x_rows, e_out, x_in, x_cols, gram, pairs, l.n, stream);
-    if (e != cudaSuccess) return e;
+    const int symmetric = form_of(dev, l.count, l.n, l.n, true, slices_k * p.products);
+    const int wide = form_of(dev, l.count, l.n, l.k, false, slices_n * p.products);
+    const int shift = symmetric ? 8 : 7;
 
-    StepParams square = p;
-    square.num_kb = int((l.n + 63) / 64);
-    square.from_e = 1.0f / s.e_scale;
-    square.from_acc = square.from_e * square.from_e;
-    square.to = s.f_scale;
-    square.shift_a = square.shift_b = pairs ? 8 : 7;
-    e = launch_product<kSquare>(dev, e_rows, e_rows, f_out, e_out, e_cols, square, pairs, l.n, stream);
-    if (e != cudaSuccess) return e;
+    // X's two sets, in turn, E and F
+    const int64_t planes = 2 * l.count;
+    ProductMaps gram[2], square, update[2];
+    CUtensorMap y_out;
+    std::memset(&y_out, 0, sizeof(y_out));
+    std::memset(&square, 0, sizeof(square));
+    bool ok = make_map16(&square.a, w + l.e, l.n, l.n, l.ldn, planes, 128) &&
+              make_map16(&square.b, w + l.e, l.n, l.n, l.ldn, planes, rows_b(symmetric)) &&
+              make_map_columns(&square.turned_a, w + l.e, l.n, l.ldn, planes, 2) &&
+              make_map_columns(&square.turned_b, w + l.e, l.n, l.ldn, planes, rows_b(symmetric) / 64) &&
+              make_store_map(&square.in, w + l.e, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, planes, l.n * l.ldn, true) &&
+              make_store_map(&square.out, w + l.f, GEMM_TYPE_F16, l.n, l.ldn, l.ldn, planes, l.n * l.ldn, true);
+    std::memset(update, 0, sizeof(update));
+    ok = ok && make_map16(&update[0].a, w + l.f, l.n, l.n, l.ldn, planes, 128) &&
+         make_map_columns(&update[0].turned_a, w + l.f, l.n, l.ldn, planes, 2);
+    update[1] = update[0];
+    std::memset(gram, 0, sizeof(gram));
+    for (int i = 0; ok && i < (steps > 1 ? 2 : 1); ++i) {
+        ok = make_map16(&gram[i].a, w + l.x[i], l.n, l.k, l.ldk, planes, 128) &&
+             make_map16(&gram[i].b, w + l.x[i], l.n, l.k, l.ldk, planes, rows_b(symmetric)) &&
+             make_map_columns(&update[i].b, w + l.x[i], l.n, l.ldk, planes, rows_b(wide) / 64) &&
+             make_store_map(&update[i].in, w + l.x[i], GEMM_TYPE_F16, l.n, l.ldk, l.ldk, planes, l.n * l.ldk, true);
+        gram[i].out = square.in;
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    update[0].out = update[1].in;
+    update[1].out = update[0].in;
+    p.y_tma = make_store_map(&y_out, a.Y, a.y_type, a.rows, a.cols, a.ldy, l.count, a.stridey, true);
 
-    StepParams update = p;
-    update.num_kb = square.num_kb;
-    update.unit = unit;
-    update.from_x = 1.0f / s.x_scale;
-    update.from_acc = update.from_x / s.f_scale;
-    update.to = s.last ? 1.0f : s.next_scale;
-    update.shift_a = square.shift_a;
-    const bool wide = pairs_pay(dev, l.count, l.n, l.k, false, update.num_kb * p.products);
-    if (!s.last) return launch_product<kUpdate>(dev, f_rows, x_cols, x_out, x_in, f_cols, update, wide, l.k, stream);
-    update.Y = a.Y;
-    update.ldy = a.ldy;
-    update.stridey = a.stridey;
-    update.y_rows = a.rows;
-    update.y_cols = a.cols;
-    update.y_tma = make_store_map(&y_out, a.Y, a.y_type, a.rows, a.cols, a.ldy, l.count, a.stridey, true);
-    update.y_bf16 = a.y_type == GEMM_TYPE_BF16;
-    if (a.y_type == GEMM_TYPE_F32)
-        return a.rows > a.cols ? launch_product<kResultTurned, true>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream)
-                               : launch_product<kResult, true>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream);
-    return a.rows > a.cols ? launch_product<kResultTurned>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream)
-                           : launch_product<kResult>(dev, f_rows, x_cols, y_out, x_in, f_cols, update, wide, l.k, stream);
+    for (int i = 0; i < steps; ++i) {
+        const OrthogonalStep &s = plan[i];
+        p.a = s.a;
+        p.b = s.b;
+        p.c = s.c;
+        const float *unit = i == 0 ? reinterpret_cast<const float *>(w + l.unit) : nullptr;
+        StepParams q = p;
+        q.num_kb = slices_k;
+        q.unit = unit;
+        q.from_acc = 1.0f / (s.x_scale * s.x_scale);
+        q.to = s.e_scale;
+        cudaError_t e = launch_product<kGram>(dev, symmetric, gram[i & 1], q, l.n, stream);
+        if (e != cudaSuccess) return e;
+
+        q = p;
+        q.num_kb = slices_n;
+        q.from_e = 1.0f / s.e_scale;
+        q.from_acc = q.from_e * q.from_e;
+        q.to = s.f_scale;
+        q.shift_a = q.shift_b = shift;
+        e = launch_product<kSquare>(dev, symmetric, square, q, l.n, stream);
+        if (e != cudaSuccess) return e;
+
+        q = p;
+        q.num_kb = slices_n;
+        q.unit = unit;
+        q.from_x = 1.0f / s.x_scale;
+        q.from_acc = q.from_x / s.f_scale;
+        q.shift_a = shift;
+        ProductMaps &maps = update[i & 1];
+        if (i + 1 < steps) {
+            q.to = s.next_scale;
+            e = launch_product<kUpdate>(dev, wide, maps, q, l.k, stream);
+        } else {
+            q.to = 1.0f;
+            maps.out = y_out;
+            const bool turned = a.rows > a.cols;
+            if (a.y_type == GEMM_TYPE_F32)
+                e = turned ? launch_product<kResultTurned, true>(dev, wide, maps, q, l.k, stream)
+                           : launch_product<kResult, true>(dev, wide, maps, q, l.k, stream);
+            else
+                e = turned ? launch_product<kResultTurned>(dev, wide, maps, q, l.k, stream)
+                           : launch_product<kResult>(dev, wide, maps, q, l.k, stream);
+        }
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace gemm

@@ -62,10 +62,10 @@ SHAPES = [(1, 1), (1, 7), (7, 1), (2, 3), (16, 16), (33, 65), (65, 33), (128, 12
           (1000, 520), (640, 640)]
 
 
-@pytest.mark.parametrize("pair", ["", "0", "1"])
+@pytest.mark.parametrize("form", ["", "0", "1", "2"])
 @pytest.mark.parametrize("shape", SHAPES)
-def test_against_the_formula(g, monkeypatch, shape, pair):
-    monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_PAIR", pair)
+def test_against_the_formula(g, monkeypatch, shape, form):
+    monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_FORM", form)
     for kind in ("normal", "low", "one", "graded"):
         for dtype in (torch.float32, torch.bfloat16) if kind == "normal" else (torch.float32,):
             m = matrix(*shape, kind, dtype=dtype)
@@ -97,10 +97,10 @@ def test_one_step_element_by_element(g):
         assert ((got - wanted).abs() <= HALF_STEP[torch.bfloat16] * wanted.abs() + 8 * 2.0 ** -11 * size + 1e-9).all()
 
 
-@pytest.mark.parametrize("pair", ["0", "1"])
+@pytest.mark.parametrize("form", ["0", "1", "2"])
 @pytest.mark.parametrize("shape", [(3, 40, 60), (5, 300, 130), (2, 256, 256), (17, 16, 24)])
-def test_stacks(g, monkeypatch, shape, pair):
-    monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_PAIR", pair)
+def test_stacks(g, monkeypatch, shape, form):
+    monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_FORM", form)
     r = torch.Generator().manual_seed(3)
     m = torch.randn(shape, generator=r).cuda() * 10.0 ** torch.arange(shape[0]).reshape(-1, 1, 1).cuda().fmod(7)
     y = g.orthogonalize(m)
@@ -164,8 +164,8 @@ def test_repeats_streams_graphs_and_expired_waits(g, monkeypatch):
         held.copy_(matrix(300, 500, seed=seed))
         graph.replay()
         assert torch.equal(y, g.orthogonalize(held))
-    for pair in "01":
-        monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_PAIR", pair)
+    for form in "012":
+        monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_FORM", form)
         monkeypatch.setenv("GEMM_GB300_TEST_INJECT_STALL", "1")
         g.orthogonalize(m, steps=1)
         assert g.gemm_get_device_status() == 5
