@@ -305,7 +305,7 @@ const char *gemm_status_string(gemm_status_t status)
     return "unknown gemm_status_t";
 }
 
-int gemm_version(void) { return 200; }
+int gemm_version(void) { return 300; }
 
 uint64_t gemm_kernel_launches(void) { return gemm::launches_so_far(); }
 

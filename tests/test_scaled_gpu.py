@@ -296,3 +296,66 @@ def test_other_streams_and_expired_waits(g, monkeypatch):
         monkeypatch.delenv("GEMM_GB300_TEST_INJECT_STALL")
         assert torch.equal(g.scaled_matmul(a, sa, b, sb), wanted)
         assert g.gemm_get_device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [
+    lambda q, s, w, ws: (q[:, :200], s, w, ws),                       # inner dimensions differ
+    lambda q, s, w, ws: (q, s[:, :1], w, ws),                         # too few scales
+    lambda q, s, w, ws: (q, s.half(), w, ws),                         # scales of another type
+    lambda q, s, w, ws: (q, s[:, 0], w, ws),                          # not 2-D
+    lambda q, s, w, ws: (q, s.repeat_interleave(128, 1)[:, :256], w, ws),  # one for every element
+    lambda q, s, w, ws: (q.float(), s, w, ws),                        # not 8-bit
+    lambda q, s, w, ws: (q, s, w.t(), ws.t()),                        # column stride
+    lambda q, s, w, ws: (q, s.cpu(), w, ws),                          # another device
+])
+def test_bad_arguments_are_refused(g, bad):
+    q, s = g.quantize_blocks(torch.randn(40, 256, device="cuda"))
+    w, ws = g.quantize_blocks(torch.randn(200, 256, device="cuda"), (128, 128))
+    with pytest.raises((ValueError, TypeError)):
+        g.scaled_matmul(*bad(q, s, w, ws))
+    with pytest.raises((ValueError, TypeError)):
+        g.scaled_matmul(q, s, w, ws, out_dtype=torch.float64)
+    with pytest.raises(g.GemmError, match="MISALIGNED"):  # rows off 16-byte boundaries
+        g.scaled_matmul(q[:, 8:], s, w[:, 8:], ws)
+
+
+def test_many_calls_at_once(g):
+    # on two streams, plans of every form, through memory that the calls before have used
+    r = gen(11)
+    cases = []
+    for M, N, K, block in [(1, 700, 900, 128), (64, 1500, 1100, 128), (700, 800, 600, 1), (1500, 1300, 300, 128), (2600, 2200, 260, 128)]:
+        a, sa = ref.operand(r, M, K, False, 1, E4)
+        b, sb = ref.operand(r, N, K, False, block, E4)
+        cases.append((on_gpu(a, sa, b, sb), ref.product(a, sa, b, sb)[0].float().cuda()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(60):
+        operands, wanted = cases[i * 7 % 5]
+        got.append((g.scaled_matmul(*operands, out_dtype=torch.float32, stream=streams[i % 2]), wanted))
+    torch.cuda.synchronize()
+    assert all(torch.equal(c, wanted) for c, wanted in got)
+    assert g.gemm_get_device_status() == 0
+
+
+def test_offsets_past_32_bits(g):
+    # rows whose elements lie more than 2^31 (and bytes more than 2^32) behind the first
+    rows, cols = 70000, 32768
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, rows, 10000):
+        x[i:i + 10000] = torch.randn(min(10000, rows - i), cols, device="cuda").bfloat16()
+    q, s = g.quantize_blocks(x)
+    last = slice(rows - 130, rows)
+    same_codes(q[last], s[last], x[last].cpu(), (1, 128), E4)
+    back = g.dequantize_blocks(q, s)
+    assert torch.equal(back[last].cpu(), ref.values(q[last].cpu(), s[last].cpu()).bfloat16())
+    del back
+    w, ws = g.quantize_blocks(torch.randn(40, cols, device="cuda") / 181, (128, 128))
+    y = g.scaled_matmul(q, s, w, ws, out_dtype=torch.float32)
+    wanted, bound = ref.product(q[last], s[last].contiguous(), w, ws)
+    assert ((y[last].double() - wanted).abs() <= bound).all()
+    del y, q, s
+    # more than 2^31 results
+    a, sa = g.quantize_blocks(torch.ones(66000, 128, device="cuda"))
+    c = g.scaled_matmul(a, sa, a, sa)
+    assert bool((c[65900:] == 128).all()) and bool((c[:100] == 128).all())

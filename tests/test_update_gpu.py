@@ -172,3 +172,47 @@ def test_repeats_streams_graphs_and_expired_waits(g, monkeypatch):
         monkeypatch.delenv("GEMM_GB300_TEST_INJECT_STALL")
         assert torch.equal(first, g.orthogonalize(m))
         assert g.gemm_get_device_status() == 0
+
+
+def test_bad_arguments_are_refused(g):
+    m = torch.randn(30, 40, device="cuda")
+    for bad in (dict(steps=0), dict(steps=65), dict(eps=-1.0), dict(coefficients=(100.0, 100.0, 100.0)),
+                dict(coefficients=(float("nan"), 0.0, 0.0)), dict(coefficients=[(1.5, -0.5, 0.0)]), dict(out_dtype=torch.float64)):
+        with pytest.raises((ValueError, TypeError, g.GemmError)):
+            g.orthogonalize(m, **bad)
+    for x in (m[0], m.double(), m.t(), m.cpu(), m[None, None]):
+        with pytest.raises((ValueError, TypeError)):
+            g.orthogonalize(x)
+
+
+def test_two_streams_and_two_graphs(g):
+    # work space is each call's own: calls that overlap, and graphs that share torch's memory pool
+    ms = [matrix(300, 400, seed=s) for s in range(4)]
+    wanted = [g.orthogonalize(m) for m in ms]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [g.orthogonalize(ms[i % 4], stream=streams[i % 2]) for i in range(16)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, wanted[i % 4]) for i, y in enumerate(got))
+    graphs, outs, pool = [], [], torch.cuda.graph_pool_handle()
+    for m in ms[:2]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            outs.append(g.orthogonalize(m))
+        graphs.append(graph)
+    for _ in range(3):
+        for i in (0, 1):
+            graphs[i].replay()
+            assert torch.equal(outs[i], wanted[i])
+
+
+def test_gradient_descends_along_the_update(g):
+    # the update of a full-rank gradient has singular values near 1, whatever the gradient's were
+    m = matrix(300, 200, "graded")
+    s = torch.linalg.svdvals(g.orthogonalize(m, steps=12, coefficients=(1.5, -0.5, 0.0), out_dtype=torch.float32).double())
+    t = torch.linalg.svdvals(m.double() / m.double().norm())
+    for _ in range(12):
+        t = 1.5 * t - 0.5 * t ** 3
+    # singular values differ by the 2-norm of the error at most; each of 12 steps adds 2^-21 of the norm and grows what
+    # the steps before it added by the cubic's slope, 1.5 at most: less than 3 * 1.5^12 * 2^-21
+    assert (s - t.sort(descending=True).values).abs().max() <= 3 * 1.5 ** 12 * 2.0 ** -21
