@@ -157,22 +157,35 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
         }
     }
     if constexpr ((MODE & kRows) != 0) {
+        // Lanes that are o apart share what is left of their rows: each hands the other one half and keeps the
+        // maxima of the other half, so that with eight rows lane x ends with row 4 (x / 8 % 2) + 2 (x / 4 % 2) +
+        // x / 2 % 2 and one exponent to find, which the others then ask it for (16 exchanges a thread, not 32).
         float most[I];
 #pragma unroll
         for (int i = 0; i < I; ++i) most[i] = row[i];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
+        for (int o = 8, n = I / 2; o > 0; o >>= 1, n /= 2) {
+            if (n > 0) {
 #pragma unroll
-            for (int i = 0; i < I; ++i) most[i] = fmaxf(most[i], __shfl_xor_sync(kFull, most[i], o));
+                for (int i = 0; i < n; ++i) {
+                    const float mine = x & o ? most[i + n] : most[i], theirs = x & o ? most[i] : most[i + n];
+                    most[i] = fmaxf(mine, __shfl_xor_sync(kFull, theirs, o));
+                }
+            } else {
+                most[0] = fmaxf(most[0], __shfl_xor_sync(kFull, most[0], o));
+            }
+        }
+        static_assert(I == 8 || I == 1, "the lane of a row");
+        const uint32_t exponent = scale_exponent(most[0], kTop);
+        const int64_t mine = I == 1 ? r0 : r0 + 16 * ((x >> 3) * 4 + (x >> 2 & 1) * 2 + (x >> 1 & 1));
+        if ((I == 1 ? x : x & 1) == 0 && (WHOLE || mine < p.rows)) p.s.at[mine * p.s.row + cb * p.s.col] = power(exponent);
         uint8_t *q = p.Q + r0 * p.ldq + c;
-        float *at = p.s.at + r0 * p.s.row + cb * p.s.col;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            const uint32_t e = scale_exponent(most[i], kTop);
+            const uint32_t e = I == 1 ? exponent : __shfl_sync(kFull, exponent, (i >> 2) * 8 + (i >> 1 & 1) * 4 + (i & 1) * 2, 16);
             float v[8];
             piece[i].get(v);
             const uint2 w = codes<E5M2>(v, infinite, [=](int) { return e; });
-            if (x == 0 && (WHOLE || r0 + 16 * i < p.rows)) at[int64_t(16 * i) * p.s.row] = power(e);
             if (inside(i)) put_codes<WHOLE>(q + int64_t(16 * i) * p.ldq, w, left);
         }
     }

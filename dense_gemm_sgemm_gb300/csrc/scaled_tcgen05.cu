@@ -43,6 +43,8 @@ constexpr unsigned kFull = 0xffffffffu;
 struct ScaledParams {
     int64_t M, N;
     int num_kb, tiles_m, tiles_n, splits;
+    int tiles;               // of a pair's, that pairs take
+    int tail;                // the first of them that single CTAs take, or -1: their tiles are a grid of their own
     int a_mn, b_mn;          // operands stored K x M, K x N
     uint32_t formats;        // their 8-bit types in the instruction descriptor
     const float *sa, *sb;
@@ -447,7 +449,7 @@ scaled_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     tc_fence_after();
     const uint32_t tmem = *sh.tmem_slot;
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
-    const int tiles = p.tiles_m * p.tiles_n, first = int(cluster_id_x()), step = int(cluster_count_x());
+    const int tiles = p.tiles, first = int(cluster_id_x()), step = int(cluster_count_x());
     Ring ring(Smem::kStages);
     bool ok = true;
 
@@ -726,6 +728,18 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     const Smem sh(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0u;
+    const int tile = int(blockIdx.x) / p.splits;
+    int64_t m0, n0;
+    if (p.tail < 0) {
+        m0 = int64_t(tile % p.tiles_m) * 128;
+        n0 = int64_t(tile / p.tiles_m) * BN;
+    } else {  // a quarter of a pair's tile
+        int tm, tn;
+        tile_of(p.tail + tile / 4, p.tiles_m, p.tiles_n, tm, tn);
+        m0 = int64_t(tm) * 256 + (tile & 1) * 128;
+        n0 = int64_t(tn) * 256 + (tile & 2) * 64;
+        if (m0 >= p.M || n0 >= p.N) return;  // with its whole cluster
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < Smem::kStages; ++s) {
             mbar_init(sh.full(s), 1);
@@ -748,11 +762,11 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    chain_wait();
+    // after pairs: nothing is read that their kernel writes, and it began only when all ahead of it had ended
+    if (p.tail < 0) chain_wait();
+    else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = *sh.tmem_slot;
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
-    const int tile = int(blockIdx.x) / p.splits;
-    const int64_t m0 = int64_t(tile % p.tiles_m) * 128, n0 = int64_t(tile / p.tiles_m) * BN;
     const int kb0 = int(int64_t(p.num_kb) * rank / p.splits), kb1 = int(int64_t(p.num_kb) * (rank + 1) / p.splits);
     Ring ring(Smem::kStages);
     bool ok = true;
@@ -791,7 +805,7 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
                     tc_fence_after();
                     const uint64_t a = a0 + uint32_t(ring.stage * (Smem::kStage >> 4));
                     const uint64_t b = b0 + uint32_t(ring.stage * (Smem::kStage >> 4));
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < 4; ++k)
                         umma_f8<false>(tmem + uint32_t(acc.stage * BN), a + k * step_a, b + k * step_b, idesc, k > 0 ? 1u : 0u);
                     umma_commit<false>(sh.empty(ring.stage));
@@ -880,6 +894,7 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
         __syncwarp();
         cluster_sync();  // the others may still read this CTA's sums
     }
+    if (p.tail >= 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // what follows waits for this kernel alone
 }
 
 // ------------------------------------------------------------------ host side
@@ -908,6 +923,7 @@ ScaledParams params_of(const ScaledArgs &a, int tile_m, int tile_n, unsigned int
     p.tiles_m = int((a.M + tile_m - 1) / tile_m);
     p.tiles_n = int((a.N + tile_n - 1) / tile_n);
     p.splits = 1;
+    p.tail = -1;
     p.a_mn = a.a.mn;
     p.b_mn = a.b.mn;
     p.formats = (a.a.q_type == GEMM_TYPE_E5M2 ? 1u << 7 : 0u) | (a.b.q_type == GEMM_TYPE_E5M2 ? 1u << 10 : 0u);
@@ -927,7 +943,9 @@ ScaledParams params_of(const ScaledArgs &a, int tile_m, int tile_n, unsigned int
     return p;
 }
 
-template <bool COLS, bool F32> cudaError_t launch_pairs(const DeviceInfo &dev, const ScaledArgs &a, unsigned int *status, cudaStream_t stream)
+// tail: of K, for the tiles beyond the last full wave, which single CTAs take then; 0: pairs take all.
+template <bool COLS, bool F32>
+cudaError_t launch_pairs(const DeviceInfo &dev, const ScaledArgs &a, int tail, unsigned int *status, cudaStream_t stream)
 {
     static std::atomic<int> cache[64];
     using Smem = PairSmem<COLS>;
@@ -941,7 +959,16 @@ template <bool COLS, bool F32> cudaError_t launch_pairs(const DeviceInfo &dev, c
     p.c_tma = make_store_map(&mc, a.C, a.c_type, a.M, a.N, a.ldc, 1, 0, true);
     const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
     if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    return launch_chained(kernel, dim3(unsigned(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, Smem::kBytes, 2, stream, ma, mb, mc, p);
+    const int64_t left = tail > 0 && tiles > pairs ? tiles % pairs : 0;
+    p.tiles = int(tiles - left);
+    cudaError_t e = launch_chained(kernel, dim3(unsigned(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, Smem::kBytes, 2, stream, ma, mb, mc, p);
+    if (e != cudaSuccess || left == 0) return e;
+    using Tile = TileSmem<128>;
+    auto *rest = scaled_tile_kernel<128, COLS>;
+    if ((e = allow_smem_once(rest, Tile::kBytes)) != cudaSuccess) return e;
+    p.tail = p.tiles;
+    p.splits = tail;
+    return launch_chained(rest, dim3(unsigned(4 * left * tail)), Tile::kThreads, Tile::kBytes, tail, stream, ma, mb, p);
 }
 
 template <int BN, bool COLS>
@@ -970,7 +997,7 @@ cudaError_t launch_tiles(const ScaledArgs &a, int splits, int transposed, unsign
 
 struct Plan {
     bool pairs, swap;
-    int bn, splits;
+    int bn, splits;  // splits with pairs: of the tail, 0 without one
 };
 
 // The form of least modelled time, in us.  A tile's CTA takes `base` (`swapped` more, to store turned) and `block` a
@@ -989,8 +1016,19 @@ Plan plan_of(const DeviceInfo &dev, const ScaledArgs &a)
     const int64_t kb = up(a.K, 128);
     const double copies = double(a.M + a.N) * double(a.K) / 5.5e6;
     const int64_t pairs = dev.num_sms / 2;
-    Plan best{true, false, 128, 1};
-    double least = 4.7 + double(up(up(a.M, 256) * up(a.N, 256), pairs)) * (double(kb) * (a.b.mn_shift == 0 ? 0.72 : 0.5) + 0.3);
+    Plan best{true, false, 128, 0};
+    const int64_t big = up(a.M, 256) * up(a.N, 256), left = big > pairs ? big % pairs : 0;
+    const double wave = double(kb) * (a.b.mn_shift == 0 ? 0.72 : 0.5) + 0.3;
+    double least = 4.7 + double(up(big, pairs)) * wave;
+    for (int splits = 1; left > 0 && splits <= 8 && splits <= kb; splits *= 2) {
+        const Form &f = kForms[2];
+        const double cost = 4.7 + double(big / pairs) * wave + (splits > 1 ? f.join : 0.0) +
+                            double(up(4 * left * splits, dev.num_sms)) * (f.base + double(up(kb, splits)) * (f.block + (a.b.mn_shift == 0 ? f.cols : 0.0)));
+        if (cost < least) {
+            least = cost;
+            best.splits = splits;
+        }
+    }
     for (int swap = 0; swap < 2; ++swap) {
         const ScaledOperand &b = swap ? a.a : a.b;
         const int64_t m = swap ? a.N : a.M, n = swap ? a.M : a.N;
@@ -1008,12 +1046,14 @@ Plan plan_of(const DeviceInfo &dev, const ScaledArgs &a)
             }
         }
     }
-    // GEMM_GB300_SCALED_PLAN (tests and sweeps): P for pairs, or BN:splits or BN:splits:s (operands swapped)
+    // GEMM_GB300_SCALED_PLAN (tests and sweeps): P or P:splits of the tail for pairs, or BN:splits or
+    // BN:splits:s (operands swapped)
     if (const char *e = std::getenv("GEMM_GB300_SCALED_PLAN"); e && *e) {
         int bn = 0, splits = 0;
         char s = 0;
         if (*e == 'P') {
-            best = Plan{true, false, 128, 1};
+            best = Plan{true, false, 128, 0};
+            if (std::sscanf(e, "P:%d", &splits) == 1 && (splits == 1 || splits == 2 || splits == 4 || splits == 8)) best.splits = splits;
         } else if (std::sscanf(e, "%d:%d:%c", &bn, &splits, &s) >= 2 && (bn == 32 || bn == 64 || bn == 128) &&
                    (splits == 1 || splits == 2 || splits == 4 || splits == 8) && (bn == 128 || !(s == 's' ? a.a : a.b).mn)) {
             best = Plan{false, s == 's', bn, splits};
@@ -1031,8 +1071,8 @@ cudaError_t launch_scaled(const DeviceInfo &dev, const ScaledArgs &a, cudaStream
     const Plan plan = plan_of(dev, a);
     if (plan.pairs) {
         const bool cols = a.b.mn_shift == 0, f32 = a.c_type == GEMM_TYPE_F32;
-        if (cols) return f32 ? launch_pairs<true, true>(dev, a, status, stream) : launch_pairs<true, false>(dev, a, status, stream);
-        return f32 ? launch_pairs<false, true>(dev, a, status, stream) : launch_pairs<false, false>(dev, a, status, stream);
+        if (cols) return f32 ? launch_pairs<true, true>(dev, a, plan.splits, status, stream) : launch_pairs<true, false>(dev, a, plan.splits, status, stream);
+        return f32 ? launch_pairs<false, true>(dev, a, plan.splits, status, stream) : launch_pairs<false, false>(dev, a, plan.splits, status, stream);
     }
     ScaledArgs t = a;
     if (plan.swap) {

@@ -161,6 +161,52 @@ def test_large_problem_with_several_tiles_a_pair(g):
     assert torch.equal(run(g, a, sa, b, sb, out_dtype=torch.float32), wanted.float())
 
 
+@pytest.mark.parametrize("splits", [1, 2, 8])
+@pytest.mark.parametrize("ops", ["NT", "NN", "TN"])
+def test_tiles_beyond_the_last_full_wave(g, monkeypatch, splits, ops):
+    monkeypatch.setenv("GEMM_GB300_SCALED_PLAN", f"P:{splits}")
+    r = gen(31)
+    for M, N, bblk in [(2500, 2200, 128), (2050, 2580, 1)]:  # 90 and 99 tiles, quarters of some outside the matrix
+        a, sa = ref.operand(r, M, 1100, ops[0] == "T", 1, E4)
+        b, sb = ref.operand(r, N, 1100, ops[1] == "N", bblk, E4)
+        wanted, _ = ref.product(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), ops[0], ops[1])
+        for t in (torch.float32, torch.bfloat16):
+            assert torch.equal(run(g, a, sa, b, sb, opA=ops[0], opB=ops[1], out_dtype=t), wanted.to(t)), (M, N, t)
+    assert g.gemm_get_device_status() == 0
+
+
+def test_tail_of_single_tiles_in_a_chain(g, monkeypatch):
+    # what is right ahead of and behind the two kernels, over the same memory, eagerly and replayed
+    monkeypatch.setenv("GEMM_GB300_SCALED_PLAN", "P:2")
+    r = gen(32)
+    x = torch.randn(2500, 2304, generator=r).bfloat16().cuda()
+    q, s = g.quantize_blocks(torch.randn(2200, 2304, generator=r).cuda(), (128, 128))
+
+    def chain():
+        y = x
+        for _ in range(3):
+            y = g.scaled_matmul(*g.quantize_blocks(y), *((q, s) if y is x else (q2, s2)))
+        return y
+
+    q2, s2 = g.quantize_blocks(torch.randn(2200, 2200, generator=r).cuda(), (128, 128))
+    torch.cuda.synchronize()
+    wanted = x
+    for w in ((q, s), (q2, s2), (q2, s2)):
+        xq = g.quantize_blocks(wanted)
+        torch.cuda.synchronize()
+        wanted = g.scaled_matmul(*xq, *w)
+        torch.cuda.synchronize()
+    for _ in range(5):
+        assert torch.equal(chain(), wanted)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = chain()
+    for _ in range(5):
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y, wanted)
+
+
 @pytest.mark.parametrize("plan", ["P", "128:2", "32:1:s"])
 @pytest.mark.parametrize("bblk", [1, 128])
 def test_scales_of_any_size(g, monkeypatch, plan, bblk):
