@@ -48,6 +48,12 @@ template <class T> struct Piece {
             for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : from_f32<T>(0.0f);
         }
     }
+    // Lets the compiler convert them again instead of keeping all of them as floats.
+    __device__ __forceinline__ void again()
+    {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T) / 2); ++i) asm volatile("" : "+r"(u[i].x), "+r"(u[i].y), "+r"(u[i].z), "+r"(u[i].w));
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
         const T *e = reinterpret_cast<const T *>(u);
@@ -184,6 +190,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
         for (int i = 0; i < I; ++i) {
             const uint32_t e = I == 1 ? exponent : __shfl_sync(kFull, exponent, (i >> 2) * 8 + (i >> 1 & 1) * 4 + (i & 1) * 2, 16);
             float v[8];
+            if (sizeof(T) == 2) piece[i].again();
             piece[i].get(v);
             const uint2 w = codes<E5M2>(v, infinite, [=](int) { return e; });
             if (inside(i)) put_codes<WHOLE>(q + int64_t(16 * i) * p.ldq, w, left);
@@ -206,6 +213,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             float v[8];
+            if (sizeof(T) == 2) piece[i].again();
             piece[i].get(v);
             const uint2 w = codes<E5M2>(v, infinite, [=](int) { return e; });
             if (inside(i)) put_codes<WHOLE>(q + int64_t(16 * i) * p.ldq, w, left);
@@ -233,6 +241,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             float v[8];
+            if (sizeof(T) == 2) piece[i].again();
             piece[i].get(v);
             const uint2 w = codes<E5M2>(v, infinite, [&](int j) { return e[j]; });
             if (inside(i)) put_codes<WHOLE>(q + int64_t(16 * i) * p.ldqc, w, left);
@@ -243,7 +252,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
 // Thread (x, y) = (t % 16, t / 16): 8 columns of the rows y, y + 16, .. of a tile of 16 * I rows.  MODE: the
 // sum of the ways.  Blocks of 1 x 128 alone do not need a tile's height: few rows take I = 1, for more CTAs.
 template <class T, int MODE, int I, bool E5M2>
-__global__ void __launch_bounds__(kThreads, MODE & kColumns || sizeof(T) == 4 ? 2 : 3) quantize_kernel(const __grid_constant__ QuantizeParams p)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 || MODE == kRows + kColumns ? 2 : 3) quantize_kernel(const __grid_constant__ QuantizeParams p)
 {
     __shared__ QuantizeSpace space;
     chain_wait();
@@ -283,6 +292,18 @@ template <class T, bool E5M2> cudaError_t quantize(const QuantizeArgs &a, cudaSt
 template <class T> cudaError_t quantize(const QuantizeArgs &a, cudaStream_t stream)
 {
     return a.q_type == GEMM_TYPE_E5M2 ? quantize<T, true>(a, stream) : quantize<T, false>(a, stream);
+}
+
+// Eight values to a boundary of as many.  fp32: one 32-byte store, since two of 16 each leave half sectors to L2
+// (16384 x 4096: 67 us).
+template <class Y> __device__ __forceinline__ void store_piece(Y *to, const float (&f)[8])
+{
+    if constexpr (sizeof(Y) == 4)
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]),
+                     "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
+    else
+        store8<Y>(to, f);
 }
 
 // Thread (x, y) of a CTA: 8 columns of the rows y, y + 16, .. of a tile of 128 x 128, whose scales are one a
@@ -329,7 +350,7 @@ dequantize_kernel(int64_t rows, int64_t cols, unsigned col_blocks, const uint8_t
         }
         Y *to = y + r * ldy + c;
         if (wide && left >= 8) {
-            store8<Y>(to, f);
+            store_piece<Y>(to, f);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -342,7 +363,7 @@ template <class Y>
 cudaError_t dequantize(int q_type, int64_t rows, int64_t cols, const void *Q, int64_t ldq, const Scales &s, void *y, int64_t ldy,
                        cudaStream_t stream)
 {
-    const int wide = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy * int64_t(sizeof(Y)) % 16 == 0;
+    const int wide = reinterpret_cast<uintptr_t>(y) % (8 * sizeof(Y)) == 0 && ldy % 8 == 0;
     const int64_t blocks = (cols + 127) / 128, grid = (rows + 127) / 128 * blocks;
     if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     return launch_chained(q_type == GEMM_TYPE_E5M2 ? dequantize_kernel<Y, true> : dequantize_kernel<Y, false>, dim3(unsigned(grid)), kThreads,
