@@ -45,11 +45,14 @@ namespace {
 constexpr int kEpiWarps = 8, kFirst = 3, kThreads = 32 * (kFirst + kEpiWarps);  // kFirst: the first epilogue warp
 constexpr int kOperandA = 128 * 128;  // bytes: 128 rows of 64 fp16
 constexpr int kEpi = kEpiWarps * 4096, kIn = kEpiWarps * 4096, kBars = 256;  // what the epilogue stores, and reads
-// The forms: a CTA's 128 x 128, a pair's 256 x 128, a pair's 256 x 256.
+// The forms: a CTA's 128 x 128, a pair's 256 x 128, a pair's 256 x 256, a CTA's 128 x 64.
+constexpr bool is_pair(int form) { return form == 1 || form == 2; }
+constexpr int tile_m(int form) { return is_pair(form) ? 256 : 128; }
+constexpr int tile_n(int form) { return form == 2 ? 256 : form == 3 ? 64 : 128; }
 template <int FORM> struct Shape {
-    static constexpr bool kPair = FORM > 0;
-    static constexpr int kM = kPair ? 256 : 128, kN = FORM == 2 ? 256 : 128, kRowsB = kPair ? kN / 2 : kN;  // rows of B a CTA holds
-    static constexpr int kStage = kOperandA + kRowsB * 128, kStages = FORM == 1 ? 6 : 5;
+    static constexpr bool kPair = is_pair(FORM);
+    static constexpr int kM = tile_m(FORM), kN = tile_n(FORM), kRowsB = kPair ? kN / 2 : kN;  // rows of B a CTA holds
+    static constexpr int kStage = kOperandA + kRowsB * 128, kStages = FORM & 1 ? 6 : 5;
     static constexpr int kBytes = kStages * kStage + kEpi + kIn + kBars + 1024;
     static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
@@ -463,22 +466,29 @@ bool make_map_columns(CUtensorMap *map, const void *ptr, int64_t rows, int64_t l
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int rows_b(int form) { return form == 1 ? 64 : 128; }
+int rows_b(int form) { return form & 1 ? 64 : 128; }
 
-// The form whose tiles' waves cost least.  A slice of 64 k takes 600 SM cycles of a pair on 256 x 256, 420 on
-// 256 x 128, and of single CTAs 560 where they keep L2 busy, 330 where there are few; a tile costs about 8 slices
-// more than it has.  (2048 x 4096: Gram matrix in 128 x 128 20.7 us; 4096 x 4096: update in 256 x 256 93 us.)
-int form_of(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool symmetric, int64_t slices)
+// The form whose waves of tiles cost least: a tile takes `slice` SM cycles a slice of 64 k and as much for `more`
+// slices beyond its own.  The symmetric products take one form, for the `slices` of both (other: the square's).
+// Fitted to 29 shapes, from 64 x 64 to 4096 x 4096 and stacks of up to 60, each in all 16 pairs of forms: the ones
+// taken are on average 0.1% slower than the fastest pair.  (Whole calls: 256 x 512 74 us with 128 x 64, 91 with
+// 128 x 128, 99 and 134 with pairs; 2048 x 4096 with 256 x 256 and the symmetric ones in 128 x 128 305 us, the other
+// forms throughout 347 to 516; 4096 x 4096 in 256 x 256 960 us.)
+int form_of(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool symmetric, int64_t slices, int64_t other)
 {
-    // GEMM_GB300_ORTHOGONAL_FORM=0|1|2 (tests and sweeps): always this one
-    if (const char *e = std::getenv("GEMM_GB300_ORTHOGONAL_FORM"); e && *e >= '0' && *e <= '2') return *e - '0';
+    // GEMM_GB300_ORTHOGONAL_FORM=0 to 3 (tests and sweeps): always this one; two digits: symmetric ones', the update's
+    if (const char *e = std::getenv("GEMM_GB300_ORTHOGONAL_FORM"); e && *e >= '0' && *e <= '3') {
+        const char c = !symmetric && e[1] >= '0' && e[1] <= '3' ? e[1] : *e;
+        return c - '0';
+    }
     int best = 0;
     double least = 1e300;
-    for (int form = 0; form < 3; ++form) {
-        const int64_t tm = form ? 256 : 128, tn = form == 2 ? 256 : 128, i = (m + tm - 1) / tm, j = (n + tn - 1) / tn;
-        const int64_t tiles = count * (symmetric ? tm / tn * i * (i + 1) / 2 : i * j), room = form ? dev.num_sms / 2 : dev.num_sms;
-        const double slice = form == 2 ? 600.0 : form == 1 ? 420.0 : tiles > room / 2 ? 560.0 : 330.0;
-        const double cost = double((tiles + room - 1) / room) * double(slices + 8) * slice;
+    static constexpr double kMore[4] = {5.5, 8.0, 10.5, 1.0}, kSlice[4] = {385.0, 365.0, 565.0, 380.0};
+    for (int form = 0; form < 4; ++form) {
+        const int64_t tm = tile_m(form), tn = tile_n(form), i = (m + tm - 1) / tm, j = (n + tn - 1) / tn;
+        const int64_t tiles = count * (symmetric ? tm / tn * i * (i + 1) / 2 : i * j), room = is_pair(form) ? dev.num_sms / 2 : dev.num_sms;
+        const double each = double(slices) + kMore[form] + (symmetric ? double(other) + kMore[form] : 0.0);
+        const double cost = double((tiles + room - 1) / room) * each * kSlice[form];
         if (cost < least) {
             least = cost;
             best = form;
@@ -520,7 +530,8 @@ cudaError_t launch_product(const DeviceInfo &dev, int form, const ProductMaps &m
 {
     if (form == 0) return launch_form<0, WHAT, F32>(dev, maps, p, columns, stream);
     if (form == 1) return launch_form<1, WHAT, F32>(dev, maps, p, columns, stream);
-    return launch_form<2, WHAT, F32>(dev, maps, p, columns, stream);
+    if (form == 2) return launch_form<2, WHAT, F32>(dev, maps, p, columns, stream);
+    return launch_form<3, WHAT, F32>(dev, maps, p, columns, stream);
 }
 
 }  // namespace
@@ -549,9 +560,9 @@ cudaError_t launch_orthogonal_steps(const DeviceInfo &dev, const OrthogonalArgs 
     test_hooks(p.timeout_ns, p.inject_stall);
     const int slices_k = int((l.k + 63) / 64), slices_n = int((l.n + 63) / 64);
     // the square's tiles are the Gram matrix's: what it reads beside them must be stored
-    const int symmetric = form_of(dev, l.count, l.n, l.n, true, slices_k * p.products);
-    const int wide = form_of(dev, l.count, l.n, l.k, false, slices_n * p.products);
-    const int shift = symmetric ? 8 : 7;
+    const int symmetric = form_of(dev, l.count, l.n, l.n, true, slices_k * p.products, slices_n * p.products);
+    const int wide = form_of(dev, l.count, l.n, l.k, false, slices_n * p.products, 0);
+    const int shift = is_pair(symmetric) ? 8 : 7;
 
     // X's two sets, in turn, E and F
     const int64_t planes = 2 * l.count;

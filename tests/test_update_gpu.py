@@ -62,7 +62,7 @@ SHAPES = [(1, 1), (1, 7), (7, 1), (2, 3), (16, 16), (33, 65), (65, 33), (128, 12
           (1000, 520), (640, 640)]
 
 
-@pytest.mark.parametrize("form", ["", "0", "1", "2"])
+@pytest.mark.parametrize("form", ["", "0", "1", "2", "3"])
 @pytest.mark.parametrize("shape", SHAPES)
 def test_against_the_formula(g, monkeypatch, shape, form):
     monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_FORM", form)
@@ -97,7 +97,7 @@ def test_one_step_element_by_element(g):
         assert ((got - wanted).abs() <= HALF_STEP[torch.bfloat16] * wanted.abs() + 8 * 2.0 ** -11 * size + 1e-9).all()
 
 
-@pytest.mark.parametrize("form", ["0", "1", "2"])
+@pytest.mark.parametrize("form", ["0", "1", "2", "3"])
 @pytest.mark.parametrize("shape", [(3, 40, 60), (5, 300, 130), (2, 256, 256), (17, 16, 24)])
 def test_stacks(g, monkeypatch, shape, form):
     monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_FORM", form)
@@ -164,7 +164,7 @@ def test_repeats_streams_graphs_and_expired_waits(g, monkeypatch):
         held.copy_(matrix(300, 500, seed=seed))
         graph.replay()
         assert torch.equal(y, g.orthogonalize(held))
-    for form in "012":
+    for form in "0123":
         monkeypatch.setenv("GEMM_GB300_ORTHOGONAL_FORM", form)
         monkeypatch.setenv("GEMM_GB300_TEST_INJECT_STALL", "1")
         g.orthogonalize(m, steps=1)
