@@ -24,8 +24,14 @@
 // three products.  What a product needs of the others it reads from the tile on the other side of the diagonal,
 // turned: the tensor cores take either order of an operand, slice by slice.
 //
-// Three forms: two CTAs on neighbouring SMs per tile of 256 x 256 or 256 x 128 (cta_group::2), or one CTA per
-// 128 x 128 tile; persistent, two accumulators, so that a tile's epilogue runs beside the next one's MMAs.
+// Four forms: two CTAs on neighbouring SMs per tile of 256 x 256 or 256 x 128 (cta_group::2), or one CTA per
+// 128 x 128 or 128 x 64 tile; persistent, two accumulators, so that a tile's epilogue runs beside the next one's MMAs.
+//
+// What bounds them (GB300; a step's three products, bf16 result).  4096 x 4096: 47, 51 and 93 us, 76, 70 and 77% of
+// the measured bf16 rate: the slices' hand-over (565 SM cycles for 512 of MMAs) and the power limit.  2048 x 4096: 21,
+// 16.5 and 32 us: 0.9 and less of a wave.  256 x 512: about 4.5 us each, of which the MMAs are 0.3: a launch's
+// hand-over (1.4 to 2.1), the first copies, one epilogue and its stores.
+//
 // Every wait is bounded: when one expires the kernel raises the device's error word, stops all roles, waits
 // (bounded) for its own copies and MMAs in flight, frees its TMEM and returns.
 #include <cuda_runtime.h>

@@ -1,5 +1,5 @@
-// Declarations shared by the block-scaled 8-bit products and the orthogonalised update.  The launchers
-// take validated arguments (scaled_api.cu).
+// Declarations of the block-scaled 8-bit matrices and their products.  The launchers take validated
+// arguments (scaled_api.cu).
 #pragma once
 
 #include <cuda_fp8.h>

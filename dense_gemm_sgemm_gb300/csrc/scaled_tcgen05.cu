@@ -7,13 +7,26 @@
 // tensor memory, and eight warps read it back, scale it and add it to fp32 sums in their registers, while
 // the MMAs of the next block fill another accumulator.  The tensor cores thus sum 128 products, whose terms
 // are exact, and everything longer is summed in fp32 on the CUDA cores with any fp32 scales, not only powers
-// of two.  A lane of tensor memory is one row of A, so sa is one value a thread; sb is one for a whole warp
-// where B's scales are by 128 rows, else (COLS) one a column, passed through shared memory.
+// of two.  A lane of tensor memory is one row of A, so its scale is one value a thread; B's are one a column
+// (COLS), read from shared memory beside the sums, or one for all 128 columns, multiplied into the row's before.
 //
 // Two forms.  Pairs: two CTAs on neighbouring SMs, 256 x 256 tiles (cta_group::2), persistent, C stored by
-// TMA.  Tiles: one CTA a tile of 128 x BN, two CTAs an SM, K split over a cluster of up to eight CTAs whose
-// sums meet in distributed shared memory; for problems without enough tiles for the pairs.  With few rows of
-// A (or B) the host swaps the operands: the long side takes the 128 lanes, the short one the BN columns.
+// TMA; the eight adding warps share a block's columns.  Tiles: one CTA a tile of 128 x BN, K split over a cluster
+// of up to eight CTAs whose sums meet in distributed shared memory; the adding warps form two groups that take
+// blocks in turn.  Tiles take problems without enough tiles for the pairs, and the tiles beyond the pairs' last
+// full wave.  With few rows of A (or B) the host swaps the operands: the long side takes the 128 lanes, the short
+// one the BN columns.
+//
+// What bounds them (GB300).  Pairs, 16384 x 4096 x 4096, B's scales by 128 x 128: 209 us, 2630 TFLOP/s, about 900 SM
+// cycles a block, of which the MMAs need 512 and the copies from L2 (64 KB a pair) 625: the adding warps, which
+// read 256 columns of all lanes from tensor memory and issue as many multiply-adds; with a scale for every column
+// of B 319 us, since each pair of sums takes a product more and its scales from shared memory.  4096 x 4096 x 8192,
+// scales of both by column, fp32 out: 183 us in pairs alone, 168 with the last wave's 28 tiles in single CTAs.
+// Tiles: latency: 1 x 4096 x 4096 8.0 us (2.1 TB/s of weight), 64 x 8192 x 4096 11.7 (2.9 TB/s), 512 x 4096 x 1024
+// 8.5: 4 to 5 us of launch, first copies, and joining and storing the sums, and 0.2 to 0.35 us a block.
+// Tried and dropped: 16 adding warps of 64 columns each (242 us, registers too few), 256-column pieces, loads of the
+// scales to registers (750 cycles a block whatever its size), one-lane producers and issuers in the pair kernel
+// (the adding warps then spill more).
 //
 // Every wait is bounded: when one expires the kernel raises the device's error word, stops all roles, waits
 // (bounded) for its own copies and MMAs in flight, frees its TMEM and returns.
@@ -33,7 +46,7 @@
 namespace gemm {
 namespace {
 
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8;  // adding warps
 // The pair kernel's warps come in fours, so that the adding ones may have more registers than the launch
 // gives each: (4 * 72 + 8 * 216) * 32 = 12 * 32 * 168.
 constexpr int kPairFirst = 4, kPairThreads = 32 * (kPairFirst + kEpiWarps);
@@ -111,7 +124,6 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
                    "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                    "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-
 
 // ------------------------------------------------------------------ scaling and adding a K block
 // Scales whose products with each other and with a block's sum (2^-32 to 2^39) stay well inside fp32.
@@ -263,7 +275,7 @@ template <bool COLS, bool PAIRS, int BN, int SLOTS, int STEP, int DELAY> struct 
 };
 
 // The sums of one thread: a row of A, CW columns of B.  sb is the block's column scales (COLS), or one for
-// every 64 columns (CW = 128) or for all.
+// each run of 64 columns (PAIRS) or for all.
 template <int CW, bool COLS, bool PAIRS> struct Sums {
     static constexpr int kChunk = PAIRS && !COLS ? 32 : 16, kChunks = CW / kChunk;
     float2 at[CW / 2];
@@ -273,7 +285,7 @@ template <int CW, bool COLS, bool PAIRS> struct Sums {
 #pragma unroll
         for (int i = 0; i < CW / 2; ++i) at[i] = make_float2(0.0f, 0.0f);
     }
-    // Adds columns c .. c + 15: v * s * (the columns' scales, COLS).
+    // Adds columns c .. : v * s * (the columns' scales, COLS).
     __device__ __forceinline__ void add_chunk(int c, const uint32_t (&v)[kChunk], float s, const float *sb)
     {
         if constexpr (COLS) {
@@ -656,10 +668,10 @@ template <int BN> struct TileSmem {
 };
 
 template <class T>
-__device__ __forceinline__ void store4(T *to, const float4 v, int64_t left, bool whole)
+__device__ __forceinline__ void store4(T *to, const float4 v, int64_t left)
 {
     const float e[4] = {v.x, v.y, v.z, v.w};
-    if (whole && left >= 4) {
+    if (left >= 4) {
         T out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = from_f32<T>(e[i]);
@@ -713,8 +725,8 @@ __device__ __forceinline__ void store_tile(const ScaledParams &p, const float *s
             }
         }
         const float4 out = make_float4(v[0], v[1], v[2], v[3]);
-        if (p.transposed) store4<T>(C + (n0 + col) * p.ldc + m0 + row, out, p.M - m0 - row, true);
-        else store4<T>(C + (m0 + row) * p.ldc + n0 + col, out, p.N - n0 - col, true);
+        if (p.transposed) store4<T>(C + (n0 + col) * p.ldc + m0 + row, out, p.M - m0 - row);
+        else store4<T>(C + (m0 + row) * p.ldc + n0 + col, out, p.N - n0 - col);
     }
 }
 
@@ -762,9 +774,12 @@ scaled_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // after pairs: nothing is read that their kernel writes, and it began only when all ahead of it had ended
-    if (p.tail < 0) chain_wait();
-    else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.tail < 0) {
+        chain_wait();
+    } else {  // after pairs: nothing is read that they write, and they let this kernel begin when all ahead of them had ended
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        __threadfence();
+    }
     const uint32_t tmem = *sh.tmem_slot;
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
     const int kb0 = int(int64_t(p.num_kb) * rank / p.splits), kb1 = int(int64_t(p.num_kb) * (rank + 1) / p.splits);
@@ -1002,9 +1017,11 @@ struct Plan {
 
 // The form of least modelled time, in us.  A tile's CTA takes `base` (`swapped` more, to store turned) and `block` a
 // K block, the sum of a cluster's parts `join`; CTAs run one an SM.  A pair's tile takes 0.5 a block, 0.72 with
-// column scales.  Tiles' copies reach 5.5 TB/s.  Fitted to 35 shapes from 1 x 512 x 512 to 3000 x 4096 x 4096, each with up to 16 plans:
-// the plan taken is on average 3% slower than the fastest (64 x 8192 x 4096: 64 columns unsplit 11.7, the halves
-// of 128 columns 13.1, swapped 14.3; 1 x 4096 x 4096: swapped, 4 parts 8.1, 2 parts 8.4, unswapped 10.1).
+// column scales.  Tiles' copies reach 5.5 TB/s.  Fitted to 35 shapes from 1 x 512 x 512 to 3000 x 4096 x 4096, each
+// with up to 16 plans: the plan taken is on average 3% slower than the fastest (64 x 8192 x 4096: 64 columns unsplit
+// 11.7, the halves of 128 columns 13.1, swapped 14.3; 1 x 4096 x 4096: swapped, 4 parts 8.1, 2 parts 8.4, unswapped
+// 10.1).  The tiles beyond the last full wave in single CTAs: 2304 x 2304 x 4096, 5 tiles, 33.5 us with pairs alone,
+// 32.4, 30.2 and 29.1 with 1, 2 and 4 parts of K; 8192 x 4096 x 4096, 56 tiles, 110 with pairs alone, 121 and more.
 Plan plan_of(const DeviceInfo &dev, const ScaledArgs &a)
 {
     struct Form {
