@@ -27,7 +27,8 @@ constexpr int kThreeProducts = 128;  // sides up to it take three products
 
 // ------------------------------------------------------------------ norm
 // Squares of values far from 1 leave fp32's range: values below 2^-40 and above 2^40 are summed apart,
-// moved by 2^86.
+// moved by 2^86.  (All three stay in range for 2^33 elements.  Doubles from the partial sums on cost 1.2 us in
+// either kernel.)
 struct Squares {
     float low = 0.0f, mid = 0.0f, high = 0.0f;
     // Eight values, together in the common case.
@@ -58,14 +59,24 @@ struct Squares {
             else mid = fmaf(v[i], v[i], mid);
         }
     }
+    __device__ __forceinline__ void add_lanes()
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            low += __shfl_xor_sync(kFull, low, o);
+            mid += __shfl_xor_sync(kFull, mid, o);
+            high += __shfl_xor_sync(kFull, high, o);
+        }
+    }
+    __device__ __forceinline__ void add(const float4 &v) { low += v.x, mid += v.y, high += v.z; }
 };
 
 // Thread: every so many 16-byte pieces of eight elements, four in flight.  I: what the pieces are counted in.
 template <class T, class I>
 __global__ void __launch_bounds__(kThreads)
-squares_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, double *partial)
+squares_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, float4 *partial)
 {
-    __shared__ double sums[kThreads / 32];
+    __shared__ float4 sums[kThreads / 32];
     chain_wait();
     const T *g = G + int64_t(blockIdx.y) * stride;
     Squares s;
@@ -86,14 +97,13 @@ squares_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t strid
 #pragma unroll
         for (int q = 0; q < 4; ++q) s.add(v[q]);
     }
-    double all = double(s.mid) + double(s.low) * 0x1p-172 + double(s.high) * 0x1p172;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = all;
+    s.add_lanes();
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_float4(s.low, s.mid, s.high, 0.0f);
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < kThreads / 32; ++i) all += sums[i];
-        partial[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = all;
+#pragma unroll
+        for (int i = 1; i < kThreads / 32; ++i) s.add(sums[i]);
+        partial[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = make_float4(s.low, s.mid, s.high, 0.0f);
     }
 }
 
@@ -101,14 +111,26 @@ struct Norm {
     int exponent;  // 2^exponent <= norm < 2^(exponent + 1)
     float unit;    // 2^exponent / norm, NaN where the norm is no finite number
 };
-__device__ __forceinline__ Norm norm_of(double squares, float eps)
+__device__ __forceinline__ Norm norm_of(const Squares &s, float eps)
 {
-    const double norm = sqrt(squares) + double(eps);
-    if (!(norm <= DBL_MAX)) return Norm{0, __uint_as_float(0x7fffffffu)};
-    if (norm == 0.0) return Norm{0, 1.0f};
+    // the norm is sqrt(square) * 2^moved; what the sums of smaller values lose on the way is far below its rounding
+    float square = s.low;
+    int moved = -86;
+    if (!(s.high == 0.0f)) {  // an infinity and NaN too
+        square = fmaf(s.mid * 0x1p-86f, 0x1p-86f, s.high);
+        moved = 86;
+    } else if (s.mid > 0.0f || (eps >= 0x1p14f)) {
+        square = fmaf(s.low * 0x1p-86f, 0x1p-86f, s.mid);
+        moved = 0;
+    }
+    if (!(s.mid >= 0.0f && s.low >= 0.0f)) square = s.mid + s.low;  // NaN
+    // a quarter of both, so that their sum stays finite
+    const float by = moved == 86 ? 0x1p-88f : moved == 0 ? 0x1p-2f : 0x1p84f, norm = fmaf(sqrtf(square), 0.25f, eps * by);
+    if (!(norm <= FLT_MAX)) return Norm{0, __uint_as_float(0x7fffffffu)};
+    if (norm == 0.0f) return Norm{0, 1.0f};
     int e;
-    const double m = frexp(norm, &e);  // in [1/2, 1)
-    return Norm{e - 1, float(0.5 / m)};
+    const float m = frexpf(norm, &e);  // in [1/2, 1)
+    return Norm{e + 1 + moved, 0.5f / m};
 }
 
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float(uint32_t(max(-126, min(127, e)) + 127) << 23); }
@@ -123,7 +145,7 @@ __device__ __forceinline__ void parts(float x, __half &high, __half &low)
 // Tiles of 64 x 64 elements of G to the parts of X, TURN: transposed through shared memory.
 template <class T, bool TURN>
 __global__ void __launch_bounds__(kThreads)
-split_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, int blocks, const double *partial, float eps,
+split_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride, int wide, int blocks, const float4 *partial, float eps,
              __half *X, int64_t ldx, int64_t n, int64_t part_stride, float *unit)
 {
     __shared__ float tile[TURN ? 64 : 1][65];
@@ -146,10 +168,9 @@ split_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride,
         }
     }
     if (threadIdx.x < 32) {
-        double s = 0.0;
-        for (int i = threadIdx.x; i < blocks; i += 32) s += partial[which * kNormBlocks + i];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+        Squares s;
+        for (int i = threadIdx.x; i < blocks; i += 32) s.add(partial[which * kNormBlocks + i]);
+        s.add_lanes();
         if (threadIdx.x == 0) {
             const Norm norm = norm_of(s, eps);
             const int e = kFirstScale - norm.exponent;  // in two factors, which fp32 holds
@@ -194,7 +215,7 @@ split_kernel(int64_t rows, int64_t cols, const T *G, int64_t ld, int64_t stride,
 template <class T> cudaError_t normalise(const OrthogonalArgs &a, const OrthogonalLayout &l, cudaStream_t stream)
 {
     char *w = static_cast<char *>(a.work);
-    double *partial = reinterpret_cast<double *>(w + l.partial);
+    float4 *partial = reinterpret_cast<float4 *>(w + l.partial);
     const T *G = static_cast<const T *>(a.G);
     const int wide = reinterpret_cast<uintptr_t>(G) % 16 == 0 && a.ldg * int64_t(sizeof(T)) % 16 == 0 &&
                      (a.count == 1 || a.strideg * int64_t(sizeof(T)) % 16 == 0);
@@ -209,7 +230,7 @@ template <class T> cudaError_t normalise(const OrthogonalArgs &a, const Orthogon
     if (e != cudaSuccess) return e;
     const dim3 grid{unsigned((a.cols + 63) / 64), unsigned((a.rows + 63) / 64), unsigned(a.count)};
     return launch_chained(a.rows > a.cols ? split_kernel<T, true> : split_kernel<T, false>, grid, kThreads, 0, 1, stream, a.rows, a.cols,
-                          G, a.ldg, a.strideg, wide, blocks, static_cast<const double *>(partial), a.eps,
+                          G, a.ldg, a.strideg, wide, blocks, static_cast<const float4 *>(partial), a.eps,
                           reinterpret_cast<__half *>(w + l.x[0]), l.ldk, l.n, l.count * l.n * l.ldk,
                           reinterpret_cast<float *>(w + l.unit));
 }
@@ -281,7 +302,7 @@ OrthogonalLayout orthogonal_layout(int64_t count, int64_t rows, int64_t cols)
     l.dd = take(count * l.ldn * 4);
     l.df = take(count * l.ldn * 4);
     l.unit = take(count * 4);
-    l.partial = take(count * kNormBlocks * 8);
+    l.partial = take(count * kNormBlocks * int64_t(sizeof(float4)));
     return l;
 }
 
