@@ -573,8 +573,8 @@ GEMM_API gemm_status_t gemm_scaled_matmul(gemm_type_t a_type, gemm_type_t b_type
  * them in fp32: one product where Y is bf16 and rows and cols are above 128, else three, of the values' parts.
  * For (3.4445, -4.7750, 2.0315) and 5 steps the result before its own rounding is within 2 * 10^-3 of the
  * formula's (relative, in the Frobenius norm; usually a quarter of that), with three products within
- * 2.5 * 10^-4 (usually 10^-6).  A matrix of zeros gives zeros, an infinity or NaN makes its whole matrix's result NaN and
- * no other's.
+ * 2.5 * 10^-4 (usually 10^-6), while eps is at most 10^4 ||G||: elements of X below 2^-38 are lost.  A matrix of
+ * zeros gives zeros, an infinity or NaN makes its whole matrix's result NaN and no other's.
  *
  * work: gemm_orthogonalize_work_bytes(count, rows, cols) bytes for the call to use (not kept), 256-byte
  * aligned; about 16 bytes for every element of a square G.

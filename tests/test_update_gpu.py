@@ -129,6 +129,39 @@ def test_any_magnitude(g, scale):
         near(g.orthogonalize(m, eps=scale), m, eps=scale)
 
 
+def test_norms_across_ranges(g):
+    # squares are summed in three ranges, of magnitudes below 2^-40, up to 2^40 and above: matrices with parts of the
+    # norm in two of them, and with the ends of fp32
+    r = torch.Generator().manual_seed(9)
+    sign = torch.randint(0, 2, (96, 160), generator=r).cuda() * 2.0 - 1.0
+    for low, high in ((9.0e-13, 9.2e-13), (1.0e12, 1.2e12), (1e-20, 1e-12), (1.0, 1e13), (1e-45, 1e-44), (2.5e38, 3.4e38), (1e-30, 1e30)):
+        m = sign * low
+        m[::3, ::2] *= high / low if high / low < 3e38 else 1e20
+        m = m.clamp(-3.4e38, 3.4e38)
+        for eps in (0.0, 1e-7 if low > 1e-15 else 0.0):
+            x = m.double() / (m.double().norm() + eps)
+            for _ in range(5):
+                a = x @ x.T
+                x = QUINTIC[0] * x + (QUINTIC[1] * a + QUINTIC[2] * a @ a) @ x
+            near(g.orthogonalize(m, eps=eps), m, wanted=x)
+    # eps beside the norm, and up to 10^4 times it, in each range
+    for scale in (1e-30, 1e-3, 1e20):
+        m = matrix(96, 160) * scale
+        for ratio in (1e-3, 1.0, 1e4):
+            eps = ratio * float(m.double().norm())
+            eps = torch.tensor(eps, dtype=torch.float32).item()
+            near(g.orthogonalize(m, eps=eps), m, eps=eps)
+    # a norm that is not a number: in each range, beside values of the others
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for scale in (1e-30, 1.0, 1e20):
+            m = matrix(40, 60) * scale
+            m[3, 5] = bad
+            assert torch.isnan(g.orthogonalize(m)).all()
+            m[7, 7] = 1e25
+            assert torch.isnan(g.orthogonalize(m)).all()
+    assert torch.equal(g.orthogonalize(torch.zeros(9, 9, device="cuda"), eps=3e38), torch.zeros(9, 9, device="cuda").bfloat16())
+
+
 def test_zeros_infinities_and_strides(g):
     m = torch.randn(4, 70, 90, generator=torch.Generator().manual_seed(1)).cuda()
     m[1] = 0.0
