@@ -67,7 +67,18 @@ template <class T> struct Piece {
     }
 };
 
-// The largest magnitude (fmaxf passes over NaN).
+// Two 16-bit elements.
+template <class T> struct Two {};
+template <> struct Two<__half> {
+    using type = __half2;
+    static __device__ __forceinline__ type zero() { return __floats2half2_rn(0.0f, 0.0f); }
+};
+template <> struct Two<__nv_bfloat16> {
+    using type = __nv_bfloat162;
+    static __device__ __forceinline__ type zero() { return __floats2bfloat162_rn(0.0f, 0.0f); }
+};
+
+// The largest magnitude (fmaxf, as __hmax2, passes over NaN).
 __device__ __forceinline__ float largest(const float (&v)[8])
 {
     float m = 0.0f;
@@ -138,17 +149,38 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
     // an infinity in this thread's pieces shows in the first look, and is left out in a second one
     float row[I], column[8];
     bool infinite = false;
+    if constexpr (sizeof(T) == 2) {  // maxima of two elements at once, in their own type
+        using T2 = typename Two<T>::type;
+        const T2 zero = Two<T>::zero();
+        T2 most[4] = {zero, zero, zero, zero};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) column[j] = 0.0f;
+        for (int i = 0; i < I; ++i) {
+            const T2 *e = reinterpret_cast<const T2 *>(piece[i].u);
+            T2 m = zero;
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-        float v[8];
-        piece[i].get(v);
-        row[i] = largest(v);
-        infinite = infinite || row[i] > FLT_MAX;
-        if ((MODE & kColumns) != 0) {
+            for (int j = 0; j < 4; ++j) {
+                const T2 a = __habs2(e[j]);
+                m = __hmax2(m, a);
+                if ((MODE & kColumns) != 0) most[j] = __hmax2(most[j], a);
+            }
+            row[i] = fmaxf(to_f32(m.x), to_f32(m.y));
+            infinite = infinite || row[i] > FLT_MAX;
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) column[j] = fmaxf(column[j], fabsf(v[j]));
+        for (int j = 0; j < 8; ++j) column[j] = to_f32(j & 1 ? most[j / 2].y : most[j / 2].x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) column[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            float v[8];
+            piece[i].get(v);
+            row[i] = largest(v);
+            infinite = infinite || row[i] > FLT_MAX;
+            if ((MODE & kColumns) != 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) column[j] = fmaxf(column[j], fabsf(v[j]));
+            }
         }
     }
     if (__builtin_expect(infinite, 0)) {
