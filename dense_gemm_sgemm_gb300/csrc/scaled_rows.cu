@@ -289,7 +289,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
 // Thread (x, y) = (t % 16, t / 16): 8 columns of the rows y, y + 16, .. of a tile of 16 * I rows.  MODE: the
 // sum of the ways.  Blocks of 1 x 128 alone do not need a tile's height: few rows take I = 1, for more CTAs.
 template <class T, int MODE, int I, bool E5M2>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 || MODE == kRows + kColumns ? 2 : 3) quantize_kernel(const __grid_constant__ QuantizeParams p)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) quantize_kernel(const __grid_constant__ QuantizeParams p)
 {
     __shared__ QuantizeSpace space;
     chain_wait();
