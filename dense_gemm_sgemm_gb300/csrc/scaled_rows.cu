@@ -199,6 +199,11 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
             }
         }
     }
+    if constexpr ((MODE & kColumns) != 0) {
+        float4 *to = reinterpret_cast<float4 *>(&space.column_max[y][x * 8]);
+        to[0] = make_float4(column[0], column[1], column[2], column[3]);
+        to[1] = make_float4(column[4], column[5], column[6], column[7]);
+    }
     if constexpr ((MODE & kRows) != 0) {
         // Lanes that are o apart share what is left of their rows: each hands the other one half and keeps the
         // maxima of the other half, so that with eight rows lane x ends with row 4 (x / 8 % 2) + 2 (x / 4 % 2) +
@@ -257,9 +262,6 @@ __device__ __forceinline__ void quantize_tile(const QuantizeParams &p, int64_t r
         }
     }
     if constexpr ((MODE & kColumns) != 0) {
-        float4 *to = reinterpret_cast<float4 *>(&space.column_max[y][x * 8]);
-        to[0] = make_float4(column[0], column[1], column[2], column[3]);
-        to[1] = make_float4(column[4], column[5], column[6], column[7]);
         __syncthreads();
         if (threadIdx.x < 128) {
             float m = 0.0f;
