@@ -9,11 +9,12 @@
 // Bound by memory: every element is read once, written once per way of quantising.  A CTA holds a tile of
 // 128 x 128 elements in registers (64 a thread), from which the maxima along rows (shuffles), along
 // columns and of the tile (shared memory) all follow in the one pass.  16384 x 4096 (GB300, copies 6.77 TB/s): bf16
-// by rows 33 us (6.0 TB/s), 128 x 128 32 (6.3), columns 35.5 (5.7), rows and columns 51.5 (5.2: two CTAs an SM, whose
-// conversions and exchanges are not hidden); fp32 50, 50, 51 and 62 (6.5 to 6.7); read back to bf16 32 (6.3), to fp32
-// 51 (6.6).  64 x 4096 by rows: 1.8 us, a launch and one chain of latencies.  Rows that do not begin on 16-byte
-// boundaries are read element by element (4095 x 4097: 14.5 to 26 us in bf16; through the aligned pieces around
-// them, shifted, it was no faster and fp32 a third slower).
+// by rows 32 us (6.4 TB/s), 128 x 128 32 (6.3), columns 33 (6.1), rows and columns 43 (6.3); fp32 50, 50, 51 and 62
+// (6.5 to 6.7); read back to bf16 32 (6.3), to fp32 51 (6.6).  64 x 4096 by rows: 1.8 us, a launch and one chain of
+// latencies.  For 16-bit types three CTAs an SM have to fit (two: 35 to 50 us), hence the maxima in pairs, the
+// conversions repeated rather than kept, and the column maxima handed over before the rows.  Rows that do not begin
+// on 16-byte boundaries are read element by element (4095 x 4097: 14.5 to 26 us in bf16; through the aligned
+// pieces around them, shifted, it was no faster and fp32 a third slower).
 #include <cuda_runtime.h>
 
 #include <cfloat>
