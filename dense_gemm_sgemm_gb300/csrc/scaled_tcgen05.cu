@@ -17,7 +17,7 @@
 // full wave.  With few rows of A (or B) the host swaps the operands: the long side takes the 128 lanes, the short
 // one the BN columns.
 //
-// What bounds them (GB300).  Pairs, 16384 x 4096 x 4096, B's scales by 128 x 128: 209 us, 2630 TFLOP/s, about 900 SM
+// What bounds them (GB300).  Pairs, 16384 x 4096 x 4096, B's scales by 128 x 128: 209 to 215 us, 2560 to 2630 TFLOP/s, about 900 SM
 // cycles a block, of which the MMAs need 512 and the copies from L2 (64 KB a pair) 625: the adding warps, which
 // read 256 columns of all lanes from tensor memory and issue as many multiply-adds; with a scale for every column
 // of B 319 us, since each pair of sums takes a product more and its scales from shared memory.  4096 x 4096 x 8192,
