@@ -83,6 +83,33 @@ def test_non_finite_values_stay_alone(g, block, dtype):
     assert torch.isnan(q.float()).sum() == 3
 
 
+@pytest.mark.parametrize("dtype", [E4, E5])
+@pytest.mark.parametrize("t", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(256, 384), (200, 300), (16, 256), (2050, 264)])
+def test_non_finite_and_tiny_values_of_every_type(g, shape, t, dtype):
+    # both ways at once: infinities and NaN in whole pieces, rows, columns and blocks, and values down to the type's least
+    r = gen(33)
+    x = torch.randn(shape, generator=r) * 2.0 ** torch.randint(-12, 13, shape, generator=r)
+    least = {torch.float32: 2.0 ** -149, torch.float16: 2.0 ** -24, torch.bfloat16: 2.0 ** -133}[t]
+    x[:, 16:24] = least * torch.randint(-3, 4, (shape[0], 8), generator=r)
+    x[9] = least * torch.randint(0, 3, (shape[1],), generator=r)
+    x[5, :] = float("nan")
+    x[11, 8:16] = float("inf")
+    x[3, 40:48] = torch.tensor([float("nan"), -float("inf")]).repeat(4)
+    x[:, 130] = -float("inf")
+    x[:, 131] = float("nan")
+    if shape[0] >= 256:
+        x[128:256, 128:256] = float("nan")
+    x[torch.rand(shape, generator=r) < 0.01] = float("nan")
+    x = x.clamp(-65504, 65504).to(t) if t == torch.float16 else x.to(t)
+    x[2, 3], x[2, 200] = float("inf"), -float("inf")
+    q, s, qc, sc = g.quantize_both(x.cuda(), dtype=dtype)
+    same_codes(q, s, x, (1, 128), dtype)
+    same_codes(qc, sc, x, (128, 1), dtype)
+    for block in BLOCKS:
+        same_codes(*g.quantize_blocks(x.cuda(), block, dtype=dtype), x, block, dtype)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_any_stride_and_alignment(g, dtype):
     room = torch.randn(400, 333, generator=gen()).to(dtype).cuda()
@@ -205,6 +232,26 @@ def test_tail_of_single_tiles_in_a_chain(g, monkeypatch):
         y.zero_()
         graph.replay()
         assert torch.equal(y, wanted)
+
+
+def test_tails_of_two_streams_at_once(g, monkeypatch):
+    monkeypatch.setenv("GEMM_GB300_SCALED_PLAN", "P:4")
+    r = gen(34)
+    w = g.quantize_blocks(torch.randn(2300, 1536, generator=r).cuda(), (128, 128))
+    xs = [torch.randn(2304, 1536, generator=r).bfloat16().cuda() for _ in range(2)]
+    wanted = [g.quantize_blocks(g.scaled_matmul(*g.quantize_blocks(x), *w)) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(15):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(g.quantize_blocks(g.scaled_matmul(*g.quantize_blocks(xs[i]), *w)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for q, s in got[i]:
+            assert torch.equal(q.view(torch.uint8), wanted[i][0].view(torch.uint8)) and torch.equal(s, wanted[i][1])
+    assert g.gemm_get_device_status() == 0
 
 
 @pytest.mark.parametrize("plan", ["P", "128:2", "32:1:s"])
