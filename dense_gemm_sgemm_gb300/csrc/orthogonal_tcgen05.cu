@@ -22,7 +22,10 @@
 //
 // A and B are symmetric: only tiles on and below the diagonal are computed and stored, which halves two of the
 // three products.  What a product needs of the others it reads from the tile on the other side of the diagonal,
-// turned: the tensor cores take either order of an operand, slice by slice.
+// turned: the tensor cores take either order of an operand, slice by slice.  Within a tile on the diagonal the 32 x 32
+// above it are stored turned too, from those below: with three products an element and its mirror image are summed
+// in different orders, and of the two one is kept.  So it makes no difference which of them a form reads, and a
+// result is the same to the bit in every form, and with it alone and in any stack.
 //
 // Four forms: two CTAs on neighbouring SMs per tile of 256 x 256 or 256 x 128 (cta_group::2), or one CTA per
 // 128 x 128 or 128 x 64 tile; persistent, two accumulators, so that a tile's epilogue runs beside the next one's MMAs.
@@ -174,11 +177,13 @@ struct Parts {
     __device__ __forceinline__ float low(int i) const { return __half2float(reinterpret_cast<const __half *>(l)[i]); }
 };
 
-// Stores 32 columns of a row as their fp16 parts, the low one too if it is wanted.
+// Stores 32 columns of a row as their fp16 parts, the low one too if it is wanted; turned: on the other side of the
+// diagonal as well.
 __device__ __forceinline__ void store_parts(Staging<false> &staging, float (&v)[32], const CUtensorMap *map, int m0, int n0, int high,
-                                            int low, bool both)
+                                            int low, bool both, bool turned)
 {
     store_rows<false>(staging, v, map, true, nullptr, 0, m0, n0, 0, 0, false, high);
+    if (turned) store_rows<false, true>(staging, v, map, true, nullptr, 0, n0, m0, 0, 0, false, high);
     if (both) {
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
@@ -187,6 +192,7 @@ __device__ __forceinline__ void store_parts(Staging<false> &staging, float (&v)[
             v[i + 1] -= h.y;
         }
         store_rows<false>(staging, v, map, true, nullptr, 0, m0, n0, 0, 0, false, low);
+        if (turned) store_rows<false, true>(staging, v, map, true, nullptr, 0, n0, m0, 0, 0, false, low);
     }
 }
 // Moves the diagonal out of a 32 x 32 piece on it: this lane's element to `to`, zero in its place.
@@ -200,6 +206,17 @@ __device__ __forceinline__ void take_diagonal(float (&v)[32], int lane, float *t
             v[i] = 0.0f;
         }
     if (row) *to = d;
+}
+// A 32 x 32 piece on the diagonal: what is above it, from below it.  tile: 4 KB of the warp's own.
+__device__ __forceinline__ void mirror(float (&v)[32], int lane, float *tile)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) tile[lane * 32 + (i ^ lane)] = v[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i > lane) v[i] = tile[i * 32 + (lane ^ i)];
+    __syncwarp();
 }
 
 template <int FORM, int WHAT, bool F32>
@@ -350,7 +367,8 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             const bool row = m < p.n;
             // what the epilogue reads is on its way during the products and the stores before it
             Parts old;
-            auto inside = [&](int n0) { return m0 < p.n && n0 < (kSymmetric ? p.n : p.k); };
+            const int columns = x.tn * S::kN + half * kHalf;
+            auto inside = [&](int n0) { return m0 < p.n && n0 < (kSymmetric ? min(p.n, int64_t(m0) + 32) : p.k); };
             auto fetch = [&](int n0) {
                 if (WHAT == kGram || !inside(n0)) return;
                 __syncwarp();  // the boxes before have been read
@@ -361,7 +379,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     tma_load_3d(dst + 2048, &map_in, bar, n0, m0, p.count + x.which);
                 }
             };
-            fetch(x.tn * S::kN + half * kHalf);
+            fetch(columns);
             const float unit = p.unit != nullptr ? __ldg(p.unit + x.which) : 1.0f;
             float mine = 0.0f;  // d or f of this row
             if (WHAT == kSquare && row) mine = __ldcg(p.d + x.which * p.ldn + m);
@@ -375,8 +393,8 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             const float from_x = p.from_x * unit, high = (p.a + mine) * from_x, low = three ? high : p.a * from_x;  // kUpdate
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
-                const int n0 = x.tn * S::kN + half * kHalf + c;
-                const bool wanted = inside(n0);
+                const int n0 = columns + c;
+                const bool wanted = inside(n0), under = n0 < m0 && n0 / S::kM == m0 / S::kM;  // under the diagonal, on its tile
                 float v[32];
                 __syncwarp();
                 tmem_ld_32(taddr + c, v);
@@ -393,13 +411,14 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] *= scale;
                         take_diagonal(v, lane, p.d + x.which * p.ldn + m, row);
+                        mirror(v, lane, reinterpret_cast<float *>(staging.all()));
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] *= p.to;
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = v[i] * scale * p.to;
                     }
-                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true);
+                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, under);
                 } else if constexpr (WHAT == kSquare) {
                     const float others = n0 + lane < p.n ? __ldcg(p.d + x.which * p.ldn + n0 + lane) : 0.0f;
 #pragma unroll
@@ -414,17 +433,18 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                         for (int i = 0; i < 32; ++i)
                             if (lane == i) v[i] += fmaf(p.b, mine, p.c * mine * mine);
                         take_diagonal(v, lane, p.f + x.which * p.ldn + m, row);
+                        mirror(v, lane, reinterpret_cast<float *>(staging.all()));
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= p.to;
                     if (c + 32 < kHalf) fetch(n0 + 32);
-                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, three);
+                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, three, under);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(high, old.high(i), fmaf(low, old.low(i), v[i] * scale)) * p.to;
                     if (c + 32 < kHalf) fetch(n0 + 32);
                     if constexpr (WHAT == kUpdate) {
-                        store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true);
+                        store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, false);
                     } else {
                         uint8_t *Y = static_cast<uint8_t *>(p.Y) + x.which * p.stridey * (F32 ? 4 : 2);
                         constexpr bool kTurned = WHAT == kResultTurned;
