@@ -23,7 +23,6 @@ constexpr int64_t kMaxSide = (int64_t(1) << 20) - 1;
 constexpr int64_t kMaxLd = int64_t(1) << 35;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int kMaxSteps = 64;
-constexpr int kThreeProducts = 128;  // sides up to it take three products
 
 // ------------------------------------------------------------------ norm
 // Squares of values far from 1 leave fp32's range: values below 2^-40 and above 2^40 are summed apart,
@@ -336,8 +335,6 @@ gemm_status_t gemm_orthogonalize(gemm_type_t type, gemm_type_t y_type, int64_t c
     if (s != GEMM_OK) return s;
     if (ldg < (cols > 1 ? cols : 1) || ldy < (cols > 1 ? cols : 1)) return GEMM_ERR_INVALID_VALUE;
     if (ldg > kMaxLd || ldy > kMaxLd || strideG > kMaxStride || strideY > kMaxStride || steps > kMaxSteps) return GEMM_ERR_UNSUPPORTED;
-    // one product where the result's own rounding hides its error (orthogonal_tcgen05.cu)
-    const int products = y_type == GEMM_TYPE_BF16 && (rows < cols ? rows : cols) > kThreeProducts ? 1 : 3;
     // the singular values stay within r, with some room for rounding
     OrthogonalStep plan[kMaxSteps];
     double r = 1.0;
@@ -346,7 +343,7 @@ gemm_status_t gemm_orthogonalize(gemm_type_t type, gemm_type_t y_type, int64_t c
         if (!(std::fabs(a) <= 1e4f && std::fabs(b) <= 1e4f && std::fabs(c) <= 1e4f)) return GEMM_ERR_UNSUPPORTED;
         OrthogonalStep &p = plan[i];
         p = OrthogonalStep{a, b, c, i == 0 ? float(1 << kFirstScale) : plan[i - 1].next_scale, scale_for(r * r),
-                           scale_for(1.02 * largest_inner(b, c, r)), 1.0f, products};
+                           scale_for(1.02 * largest_inner(b, c, r)), 1.0f};
         r = 1.02 * largest_value(a, b, c, r);
         if (!(r <= 1e4)) return GEMM_ERR_UNSUPPORTED;
         p.next_scale = scale_for(r);

@@ -38,7 +38,6 @@ cudaError_t launch_normalise(const OrthogonalArgs &a, const OrthogonalLayout &l,
 struct OrthogonalStep {
     float a, b, c;
     float x_scale, e_scale, f_scale, next_scale;
-    int products;  // 1, or 3 of the parts
 };
 // The first step's X in memory is to be multiplied by 1 / c of its matrix (unit), the last one writes Y.
 cudaError_t launch_orthogonal_steps(const DeviceInfo &dev, const OrthogonalArgs &a, const OrthogonalLayout &l, const OrthogonalStep *plan,

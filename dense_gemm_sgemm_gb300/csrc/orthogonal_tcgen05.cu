@@ -5,20 +5,17 @@
 //     square   B = b A + c A^2         likewise f and F
 //     update   X' = (a + f) X + F X    two fp16 parts; the last step writes the result
 //
-// A result in bf16 takes one fp16 product each, with fp32 sums.  Rounding all of A and B to fp16 would lose
-// too much: their diagonals dominate and change by up to 2^-12 of themselves.  So what multiplies a whole row
-// or column stays out of the products: with A = d + E, A^2 = d^2 + (d_i + d_j) E + E E, and of B X the
-// diagonal's part f X; a X and b A take both parts of X and E (22 bits).  The terms beside a product take the
-// high part that the product takes: what is then missing of A^2 and B X is (A dE + dE A) and B dX, dE and dX
-// the low parts, which vanish where A and B do; with both parts beside high products a rank-one G grew a second
-// singular value (up to 4 * 10^-2 of the result's norm).  Over five steps of the usual coefficients this is off
-// by 0.1 to 1.5 * 10^-3 of the result's norm (random, low-rank, rank-one, graded spectra, 256 rows and more),
-// where rounding the result to bf16 is 1.7 * 10^-3; with the diagonals inside the products it is up to 2.6,
-// with bf16 iterates 12 to 55 * 10^-3.
+// Each is three products of the parts (high low + low high + high high), as three times the K slices.  One fp16 product
+// of the high parts would not do even for a bf16 result: where elements are equal in magnitude their roundings are
+// equal too and do not average out, and the steps multiply them (a constant 512 x 512 came to 1.3 * 10^-2 of the
+// result's norm, a matrix of equal rows to 6 * 10^-3, where rounding the result to bf16 is 1.7 * 10^-3 at most).  Nor
+// would two, with one operand's low part left out.  The small products come first: the tensor cores' fp32 sums round
+// towards zero at every 16 k, and after the large product each of their additions would lose a step of the whole sum
+// (equal rows, 4096 x 4096: 2.1 * 10^-3, now 3 * 10^-4; the formula in fp32 3.3 * 10^-4).  What is left is 10^-6 for
+// most matrices of 1000 rows, 3 * 10^-5 for 4096, and up to 1.5 * 10^-3 for 4096 x 4096 of rank two.
 //
-// Small matrices, whose roundings do not average out and whose products are short of work anyway, and results
-// in fp16 or fp32 take three products of the parts (high high + high low + low high): 10^-4 at most, for
-// rank-one matrices, 10^-6 for most.  They run as three times the K slices.
+// What multiplies a whole row or column stays out of the products: with A = d + E, A^2 = d^2 + (d_i + d_j) E + E E, and
+// of B X the diagonal's part f X, so the products' roundings are those of the rest, and d and f are held in fp32.
 //
 // A and B are symmetric: only tiles on and below the diagonal are computed and stored, which halves two of the
 // three products.  What a product needs of the others it reads from the tile on the other side of the diagonal,
@@ -30,10 +27,11 @@
 // Four forms: two CTAs on neighbouring SMs per tile of 256 x 256 or 256 x 128 (cta_group::2), or one CTA per
 // 128 x 128 or 128 x 64 tile; persistent, two accumulators, so that a tile's epilogue runs beside the next one's MMAs.
 //
-// What bounds them (GB300; a step's three products, bf16 result).  4096 x 4096: 47, 51 and 93 us, 76, 70 and 77% of
-// the measured bf16 rate: the slices' hand-over (565 SM cycles for 512 of MMAs) and the power limit.  2048 x 4096: 21,
-// 16.5 and 32 us: 0.9 and less of a wave.  256 x 512: about 4.5 us each, of which the MMAs are 0.3: a launch's
-// hand-over (1.4 to 2.1), the first copies, one epilogue and its stores.
+// What bounds them (GB300; the three products of a step, each alone).  4096 x 4096: 126, 126 and 250 us, 1.65 to 1.74
+// PFLOP/s, the tensor pipe 88 to 94% active; one after another the power limit takes 10% more.  2048 x 4096: 44, 30
+// and 67 us: 72 tiles of 256 x 128 in one wave, whose epilogue nothing hides, and 128 of 256 x 256 on 76 pairs.
+// 256 x 512: about 6 us each in the chain, of which the MMAs are 1: a launch's hand-over (1.4 to 2.1), the first
+// copies, one epilogue and its stores.
 //
 // Every wait is bounded: when one expires the kernel raises the device's error word, stops all roles, waits
 // (bounded) for its own copies and MMAs in flight, frees its TMEM and returns.
@@ -67,12 +65,12 @@ template <int FORM> struct Shape {
 };
 constexpr int kMostBytes = Shape<2>::kBytes;
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kProducts = 3;  // of the parts
 constexpr int kGram = 0, kSquare = 1, kUpdate = 2, kResult = 3, kResultTurned = 4;
 
 struct StepParams {
     int64_t n, k, ldn;       // sides, and distance of two matrices' diagonals
     int count, tiles_m, tiles_n, per, num_kb;  // tiles of a matrix, K slices of one product
-    int products;            // 1, or 3 of the parts
     int shift_a, shift_b;    // of a symmetric operand, whose tiles (of 2^shift) above the diagonal are not stored; else 0
     float *d, *f;
     const float *unit;  // NULL: 1
@@ -177,23 +175,20 @@ struct Parts {
     __device__ __forceinline__ float low(int i) const { return __half2float(reinterpret_cast<const __half *>(l)[i]); }
 };
 
-// Stores 32 columns of a row as their fp16 parts, the low one too if it is wanted; turned: on the other side of the
-// diagonal as well.
+// Stores 32 columns of a row as their fp16 parts; turned: on the other side of the diagonal as well.
 __device__ __forceinline__ void store_parts(Staging<false> &staging, float (&v)[32], const CUtensorMap *map, int m0, int n0, int high,
-                                            int low, bool both, bool turned)
+                                            int low, bool turned)
 {
     store_rows<false>(staging, v, map, true, nullptr, 0, m0, n0, 0, 0, false, high);
     if (turned) store_rows<false, true>(staging, v, map, true, nullptr, 0, n0, m0, 0, 0, false, high);
-    if (both) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float2 h = __half22float2(__floats2half2_rn(v[i], v[i + 1]));
-            v[i] -= h.x;
-            v[i + 1] -= h.y;
-        }
-        store_rows<false>(staging, v, map, true, nullptr, 0, m0, n0, 0, 0, false, low);
-        if (turned) store_rows<false, true>(staging, v, map, true, nullptr, 0, n0, m0, 0, 0, false, low);
+    for (int i = 0; i < 32; i += 2) {
+        const float2 h = __half22float2(__floats2half2_rn(v[i], v[i + 1]));
+        v[i] -= h.x;
+        v[i + 1] -= h.y;
     }
+    store_rows<false>(staging, v, map, true, nullptr, 0, m0, n0, 0, 0, false, low);
+    if (turned) store_rows<false, true>(staging, v, map, true, nullptr, 0, n0, m0, 0, 0, false, low);
 }
 // Moves the diagonal out of a 32 x 32 piece on it: this lane's element to `to`, zero in its place.
 __device__ __forceinline__ void take_diagonal(float (&v)[32], int lane, float *to, bool row)
@@ -258,7 +253,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *sh.tmem_slot;
     const Watch watch{sh.abort_flag, p.status, p.timeout_ns};
-    const int slices = p.num_kb * p.products;  // high high, high low, low high
+    const int slices = p.num_kb * kProducts;
     const int units = p.count * p.per, first = PAIR ? int(cluster_id_x()) : int(blockIdx.x),
               step = PAIR ? int(cluster_count_x()) : int(gridDim.x);
     Ring ring(kStages);
@@ -278,8 +273,8 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 const Unit x = unit_of<kSymmetric, S::kM / S::kN>(p, u);
                 const int row = of_a ? x.tm * S::kM + int(rank) * 128 : x.tn * S::kN + int(rank) * S::kRowsB;
                 const int of_tile = of_a ? x.tm * S::kM : x.tn * S::kN, shift = of_a ? p.shift_a : p.shift_b;
-                for (int product = 0; ok && product < p.products; ++product) {  // high high, high low, low high
-                    const int plane = x.which + (product == (of_a ? 2 : 1) ? p.count : 0);
+                for (int product = 0; ok && product < kProducts; ++product) {  // high low, low high, high high
+                    const int plane = x.which + (product == (of_a ? 1 : 0) ? p.count : 0);
                     for (int k = 0; k < 64 * p.num_kb; k += 64) {
                         ok = watch.wait(sh.empty(ring.stage), ring.phase ^ 1u);
                         if (!ok) break;
@@ -389,8 +384,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             tc_fence_after();
             const uint32_t taddr = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(acc * S::kN + half * kHalf);
             const float scale = WHAT == kGram ? p.from_acc * unit * unit : WHAT == kSquare ? p.from_acc : p.from_acc * unit;
-            const bool three = p.products == 3;
-            const float from_x = p.from_x * unit, high = (p.a + mine) * from_x, low = three ? high : p.a * from_x;  // kUpdate
+            const float from_x = (p.a + mine) * (p.from_x * unit);  // kUpdate
 #pragma unroll 1
             for (int c = 0; c < kHalf; c += 32) {
                 const int n0 = columns + c;
@@ -418,14 +412,14 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = v[i] * scale * p.to;
                     }
-                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, under);
+                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, under);
                 } else if constexpr (WHAT == kSquare) {
                     const float others = n0 + lane < p.n ? __ldcg(p.d + x.which * p.ldn + n0 + lane) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         // of A: E here, d on the diagonal, where E is 0; of A^2: (d_i + d_j) E + E E, d^2 + E E
-                        const float hi = old.high(i) * p.from_e, e = fmaf(old.low(i), p.from_e, hi);
-                        const float square = fmaf(three ? e : hi, mine + __shfl_sync(kFull, others, i), v[i] * scale);
+                        const float e = (old.high(i) + old.low(i)) * p.from_e;
+                        const float square = fmaf(e, mine + __shfl_sync(kFull, others, i), v[i] * scale);
                         v[i] = fmaf(p.b, e, p.c * square);
                     }
                     if (n0 == m0) {
@@ -438,13 +432,13 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= p.to;
                     if (c + 32 < kHalf) fetch(n0 + 32);
-                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, three, under);
+                    store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, under);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = fmaf(high, old.high(i), fmaf(low, old.low(i), v[i] * scale)) * p.to;
+                    for (int i = 0; i < 32; ++i) v[i] = fmaf(from_x, old.high(i) + old.low(i), v[i] * scale) * p.to;
                     if (c + 32 < kHalf) fetch(n0 + 32);
                     if constexpr (WHAT == kUpdate) {
-                        store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, true, false);
+                        store_parts(staging, v, &map_out, m0, n0, x.which, p.count + x.which, false);
                     } else {
                         uint8_t *Y = static_cast<uint8_t *>(p.Y) + x.which * p.stridey * (F32 ? 4 : 2);
                         constexpr bool kTurned = WHAT == kResultTurned;
@@ -496,10 +490,11 @@ int rows_b(int form) { return form & 1 ? 64 : 128; }
 
 // The form whose waves of tiles cost least: a tile takes `slice` SM cycles a slice of 64 k and as much for `more`
 // slices beyond its own.  The symmetric products take one form, for the `slices` of both (other: the square's).
-// Fitted to 29 shapes, from 64 x 64 to 4096 x 4096 and stacks of up to 60, each in all 16 pairs of forms: the ones
-// taken are on average 0.1% slower than the fastest pair.  (Whole calls: 256 x 512 74 us with 128 x 64, 91 with
-// 128 x 128, 99 and 134 with pairs; 2048 x 4096 with 256 x 256 and the symmetric ones in 128 x 128 305 us, the other
-// forms throughout 347 to 516; 4096 x 4096 in 256 x 256 960 us.)
+// Fitted to 29 shapes, from 64 x 64 to 4096 x 4096 and stacks of up to 60, each in all 16 pairs of forms; of 17 of them the
+// ones taken are on average 0.9% slower than the fastest pair.  (Whole calls: 256 x 512 104 us with 128 x 64, 128 with
+// 128 x 128, 137 and 197 with pairs; 2048 x 4096 with 256 x 256 and the symmetric ones in 256 x 128 657 us, the other
+// forms throughout 782 to 1316; 4096 x 4096 in 256 x 256 2510 to 2750 us; 16 of 1000 x 520 455, where 256 x 256 for the
+// update alone would take 416.)
 int form_of(const DeviceInfo &dev, int64_t count, int64_t m, int64_t n, bool symmetric, int64_t slices, int64_t other)
 {
     // GEMM_GB300_ORTHOGONAL_FORM=0 to 3 (tests and sweeps): always this one; two digits: symmetric ones', the update's
@@ -575,7 +570,6 @@ cudaError_t launch_orthogonal_steps(const DeviceInfo &dev, const OrthogonalArgs 
     p.count = int(l.count);
     p.d = reinterpret_cast<float *>(w + l.dd);
     p.f = reinterpret_cast<float *>(w + l.df);
-    p.products = plan[0].products;
     p.Y = a.Y;
     p.ldy = a.ldy;
     p.stridey = a.stridey;
@@ -586,8 +580,8 @@ cudaError_t launch_orthogonal_steps(const DeviceInfo &dev, const OrthogonalArgs 
     test_hooks(p.timeout_ns, p.inject_stall);
     const int slices_k = int((l.k + 63) / 64), slices_n = int((l.n + 63) / 64);
     // the square's tiles are the Gram matrix's: what it reads beside them must be stored
-    const int symmetric = form_of(dev, l.count, l.n, l.n, true, slices_k * p.products, slices_n * p.products);
-    const int wide = form_of(dev, l.count, l.n, l.k, false, slices_n * p.products, 0);
+    const int symmetric = form_of(dev, l.count, l.n, l.n, true, slices_k * kProducts, slices_n * kProducts);
+    const int wide = form_of(dev, l.count, l.n, l.k, false, slices_n * kProducts, 0);
     const int shift = is_pair(symmetric) ? 8 : 7;
 
     // X's two sets, in turn, E and F

@@ -24,8 +24,7 @@ def orthogonalize(g, *, steps=5, coefficients=_QUINTIC, eps=1e-7, out_dtype=torc
     """The update of g (rows x cols, or a stack of such matrices; fp32, fp16 or bf16), in out_dtype and g's shape.
 
     coefficients: (a, b, c) of a X + (b A + c A A) X, A = X X^T, or one such triple for each step.
-    out_dtype: bfloat16, whose rounding the products' precision goes by, or float32 or float16 at three times
-    the work.
+    out_dtype: bfloat16, float32 or float16, to which the same result is rounded.
     """
     each = tuple(coefficients)
     if each and not isinstance(each[0], (tuple, list)):

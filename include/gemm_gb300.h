@@ -569,12 +569,14 @@ GEMM_API gemm_status_t gemm_scaled_matmul(gemm_type_t a_type, gemm_type_t b_type
  * before the call returns.
  *
  * Precision.  The norm is summed in fp32 without overflow or underflow of the squares.  The iterates are
- * held to 22 bits; products are of fp16 values with fp32 sums, the diagonals of A and of b A + c A^2 apart from
- * them in fp32: one product where Y is bf16 and rows and cols are above 128, else three, of the values' parts.
- * For (3.4445, -4.7750, 2.0315) and 5 steps the result before its own rounding is within 2 * 10^-3 of the
- * formula's (relative, in the Frobenius norm; usually a quarter of that), with three products within
- * 2.5 * 10^-4 (usually 10^-6), while eps is at most 10^4 ||G||: elements of X below 2^-38 are lost.  A matrix of
- * zeros gives zeros, an infinity or NaN makes its whole matrix's result NaN and no other's.
+ * held to 22 bits; products are of fp16 values with fp32 sums, three products of the values' parts each, the
+ * diagonals of A and of b A + c A^2 apart from them in fp32.  For (3.4445, -4.7750, 2.0315) and 5 steps the
+ * result before its own rounding is within 2.5 * 10^-4 + 7.5 * 10^-7 max(rows, cols) of the formula's
+ * (relative, in the Frobenius norm), the second term for the roundings of long sums; usually about 10^-6, up
+ * to 3 * 10^-5 for 4096 rows, as with the formula in fp32.  That holds while eps is at most 10^4 ||G||: elements
+ * of X below 2^-38 are lost.  A matrix of zeros gives zeros, an infinity or NaN makes its whole matrix's result
+ * NaN and no other's.  A result does not depend on the stack that its matrix is in, and a bf16 or fp16 result
+ * is the fp32 one rounded.
  *
  * work: gemm_orthogonalize_work_bytes(count, rows, cols) bytes for the call to use (not kept), 256-byte
  * aligned; about 16 bytes for every element of a square G.
