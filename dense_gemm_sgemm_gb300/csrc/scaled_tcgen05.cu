@@ -132,13 +132,14 @@ __device__ __forceinline__ bool mild(float s)
     const float a = fabsf(s);
     return a == 0.0f || (a >= 0x1p-40f && a <= 0x1p40f);
 }
-// s as two factors of half its exponent each (zero, infinite and NaN scales as 1 and s).  A block's sum times
-// both scales' first factors and then both second ones stays in fp32's range wherever the result does.
+// s as two factors of half its exponent each (zero, infinite and NaN scales as 1 and s), the second one below 2^64,
+// so that the product of two of them is finite.  A block's sum times one scale's first factor, the other's, and then
+// both second ones stays in fp32's range wherever the result does, and a sum of zero stays zero.
 __device__ __forceinline__ float2 halves(float s)
 {
     const float a = fabsf(s);
     if (!(a > 0.0f && a <= FLT_MAX)) return make_float2(1.0f, s);
-    const int e = (ilogbf(s) & ~1) / 2;
+    const int e = (ilogbf(s) + 1) >> 1;
     return make_float2(__uint_as_float(uint32_t(127 + e) << 23), s * __uint_as_float(uint32_t(127 - e) << 23));
 }
 
@@ -354,7 +355,7 @@ template <int CW, bool COLS, bool PAIRS> struct Sums {
             const int run = PAIRS ? i * kChunk / 64 : 0;
 #pragma unroll
             for (int j = 0; j < kChunk; ++j)
-                v[j] = __float_as_uint(__uint_as_float(v[j]) * (h.x * scratch[CW + (COLS ? i * kChunk + j : run)]));
+                v[j] = __float_as_uint(__uint_as_float(v[j]) * h.x * scratch[CW + (COLS ? i * kChunk + j : run)]);
             add_chunk(i * kChunk, v, COLS ? h.y : h.y * scratch[run], scratch);
         }
     }
