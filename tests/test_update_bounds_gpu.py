@@ -121,3 +121,21 @@ def test_a_matrix_of_a_stack_is_the_same_as_alone(g, shape, dtype):
     y = g.orthogonalize(m, out_dtype=dtype)
     for i in (0, 1, shape[0] - 1):
         assert torch.equal(y[i], g.orthogonalize(m[i], out_dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("each", [[(0.5, 0.0, 0.0)] * 20, [(0.01, 0.0, 0.0)] * 4, [(0.0, -0.03, 0.0), (0.0, 1.0, 0.0)], [(0.0, 0.0, 0.0)],
+                                  [(0.02, 0.0, 0.0), (2.0, -1.5, 0.5)]])
+def test_steps_that_shrink_the_iterate(g, each, dtype):
+    # what an iterate loses is in proportion to its own bound, whatever that is; a step's three products and
+    # epilogues are off by less than 2^-20, which no step here grows to more than 9 times (the fifth power's 5, the cube's 3)
+    for m in (normal(200, 300), torch.ones(300, 140, device="cuda")):
+        x = m.double() / (m.double().norm() + 1e-7)
+        for a, b, c in each:
+            s = x @ x.T
+            x = a * x + (b * s + c * s @ s) @ x
+        got = g.orthogonalize(m, steps=len(each), coefficients=each, out_dtype=dtype)
+        rounding = (x.to(dtype).double() - x).norm()
+        assert (got.double() - x).norm() <= rounding + 2 * len(each) * 9 * 2.0 ** -20 * x.norm()
+    with pytest.raises(g.GemmError):
+        g.orthogonalize(m, steps=64, coefficients=(0.5, 0.0, 0.0))
