@@ -95,11 +95,8 @@ BOUND(dequantize_blocks, 4)
     const Matrix q = matrix8(device, a[0], "q");
     const Stream stream(a[3], q.t);
     const gemm_type_t q_type = type8_of(q.t.scalar_type(), "q");
-    BlockScales s = scales_of(device, a[1], q, "scales");
-    if (s.rows == 1 && s.cols == 1) {  // a single row or column, whose scales may be read as those of blocks
-        TORCH_CHECK_VALUE(q.rows <= 1 || q.cols <= 1, "scales: one for every element");
-        (q.rows <= 1 ? s.rows : s.cols) = 128;
-    }
+    const BlockScales s = scales_of(device, a[1], q, "scales");
+    TORCH_CHECK_VALUE(s.rows == 128 || s.cols == 128, "scales: one for every element");
     const at::ScalarType dtype = dtype_of(a[2], at::kBFloat16);
     const gemm_type_t y_type = type_of(dtype, "out_dtype");
     Padded y = padded(q.rows, q.cols, dtype, q.t);

@@ -44,3 +44,15 @@ def test_every_pair_of_scales(g, monkeypatch, plan, b_block):
         near = wanted.abs() <= MOST * (1 - 2.0 ** -22)
         assert ((c.double() - wanted).abs()[near] <= 3 * 2.0 ** -24 * wanted.abs()[near] + 2.0 ** -149).all()
     assert g.gemm_get_device_status() == 0
+
+
+def test_reading_back_takes_one_scale_for_a_block(g):
+    r = torch.Generator().manual_seed(3)
+    for rows, cols in ((2, 2), (5, 300), (300, 2)):  # one for every element
+        q = g.quantize_blocks(torch.randn(rows, cols, generator=r).cuda())[0]
+        with pytest.raises(ValueError, match="every element"):
+            g.dequantize_blocks(q, torch.ones(rows, cols, device="cuda"))
+    for rows, cols in ((1, 1), (1, 300), (300, 1)):  # of a single row or column: those of blocks across it
+        q = g.quantize_blocks(torch.randn(rows, cols, generator=r).cuda())[0]
+        s = torch.rand(rows, cols, generator=r).cuda()
+        assert torch.equal(g.dequantize_blocks(q, s, out_dtype=torch.float32), q.float() * s)
