@@ -25,7 +25,7 @@ constexpr int kThreads = 32 * kWarps;
 template <int MT> constexpr int kRowStride = MT <= 2 ? 36 : 68;
 constexpr unsigned kFull = 0xffffffffu;
 
-// Rows that one warp reads once: no line of L1 for them.
+// Rows of weights that one warp reads once: no line of L1 for them.
 __device__ __forceinline__ uint4 load_stream(const void *p)
 {
     uint4 v;
@@ -67,7 +67,7 @@ __device__ __forceinline__ void warp_product(const T *const (&w)[MT][2], const T
                 for (int h = 0; h < 2; ++h) a[u][m][h] = load_stream(w[m][h] + k + 32 * u + t8);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                b[u][n] = x[n] != nullptr ? __ldg(reinterpret_cast<const uint4 *>(x[n] + k + 32 * u + t8)) : zero;
+                b[u][n] = x[n] != nullptr ? load_now(reinterpret_cast<const uint4 *>(x[n] + k + 32 * u + t8)) : zero;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) multiply(a[u], b[u]);
@@ -114,8 +114,8 @@ __device__ __forceinline__ bool nonempty_group(const GroupedArgs &a, int i, int 
         const int e = e0 + lane;
         int lo = 0, hi = 0;
         if (e < a.groups) {
-            lo = clamp_to(__ldg(a.offsets + e), a.y_rows);
-            hi = clamp_to(__ldg(a.offsets + e + 1), a.y_rows);
+            lo = clamp_to(load_now(a.offsets + e), a.y_rows);
+            hi = clamp_to(load_now(a.offsets + e + 1), a.y_rows);
         }
         const unsigned has = __ballot_sync(kFull, hi > lo);
         const int n = __popc(has);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) few_rows_kernel(con
         for (int n = 0; n < NT; ++n) {
             const unsigned i = n0 + 8 * n + g;
             int64_t r = -1;
-            if (i < unsigned(rows)) r = a.rows != nullptr ? __ldg(a.rows + first + i) : int64_t(first) + i;
+            if (i < unsigned(rows)) r = a.rows != nullptr ? load_now(a.rows + first + i) : int64_t(first) + i;
             x[n] = r >= 0 && r < a.x_rows ? static_cast<const T *>(a.X) + r * a.ldx : nullptr;
         }
         float acc[2][NT][4];
@@ -309,10 +309,10 @@ __global__ void __launch_bounds__(32 * WARPS) shrink_kernel(const ShrinkArgs a)
     constexpr int kThreads = 32 * WARPS, kTokens = 8 * NT, kStride = kRowStride<MT>;
     chain_wait();  // the product that follows may start on its weights and rows; it waits for inner
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    auto seg = [&](int q) { return clamp_to(__ldg(a.segments + q), a.T); };
+    auto seg = [&](int q) { return clamp_to(load_now(a.segments + q), a.T); };
     if (PARTS == 0 && blockIdx.y == 0) {  // tokens of no request
         if (blockIdx.x == 0)
-            for (int t = threadIdx.x; t < seg(0); t += kThreads) a.which[t] = -1;
+            for (int t = threadIdx.x, end = seg(0); t < end; t += kThreads) a.which[t] = -1;
         if (blockIdx.x == gridDim.x - 1)
             for (int t = seg(a.requests) + threadIdx.x; t < a.T; t += kThreads) a.which[t] = -1;
     }
@@ -330,11 +330,12 @@ __global__ void __launch_bounds__(32 * WARPS) shrink_kernel(const ShrinkArgs a)
     const int t0 = max(seg(lo), tile * kTokens);
     const int t1 = int(min(int64_t(seg(lo + 1)), int64_t(tile + 1) * kTokens));
     if (t0 >= t1) return;
-    int ad = __ldg(a.adapters + lo);
+    int ad = load_now(a.adapters + lo);
     if (unsigned(ad) >= unsigned(a.n_adapters)) ad = -1;
     if (PARTS == 0 && blockIdx.y == 0)
         for (int t = t0 + int(threadIdx.x); t < t1; t += kThreads) a.which[t] = ad;
     if (ad < 0) return;
+    const float scale = a.scales != nullptr ? load_now(a.scales + ad) : 1.0f;  // on its way during the product
 
     const int r0 = blockIdx.y * 16 * MT;
     const T *A = static_cast<const T *>(a.A) + int64_t(ad) * a.stridea;
@@ -362,7 +363,6 @@ __global__ void __launch_bounds__(32 * WARPS) shrink_kernel(const ShrinkArgs a)
     warp_product<T, MT, NT, WARPS == 16 ? 64 : 128>(w, x, kb, ke, a.K, lane, acc);
     put_partial<MT, NT>(parts + warp * kTokens * kStride, acc, lane);
     __syncthreads();
-    const float scale = a.scales != nullptr ? __ldg(a.scales + ad) : 1.0f;
     const int ranks = min(16 * MT, a.R - r0);
     auto sum = [&](int n, int r) {  // of token n of the tile
         const float *src = parts + n * kStride + r;

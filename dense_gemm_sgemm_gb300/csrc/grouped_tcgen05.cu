@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t set_up(const Shared &sh, const int32_t *offs
     if (CHAIN) chain_wait();
     else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int g = threadIdx.x; g <= groups; g += blockDim.x)
-        sh.first[g] = offsets != nullptr ? clamp_to(__ldg(offsets + g), positions) : g == 0 ? 0 : int(positions);
+        sh.first[g] = offsets != nullptr ? clamp_to(load_now(offsets + g), positions) : g == 0 ? 0 : int(positions);
     __syncthreads();
     if (warp == 0) {
         int carry = 0;
@@ -390,7 +390,7 @@ struct TileRequests {
         q0 = 0;
         for (int n = p.requests; n > 0;) {
             const int run = (n + 31) / 32, last = (lane + 1) * run - 1;
-            const bool done = last < n && clamp_to(__ldg(p.segments + q0 + last + 1), p.y_rows) <= t0;
+            const bool done = last < n && clamp_to(load_now(p.segments + q0 + last + 1), p.y_rows) <= t0;
             const int c = __popc(__ballot_sync(kFull, done));
             q0 += c * run;
             n = (c + 1) * run <= n ? run - 1 : n - c * run;
@@ -403,9 +403,9 @@ struct TileRequests {
         lo = hi = 0;
         ad = -1;
         if (q < p.requests) {
-            lo = max(clamp_to(__ldg(p.segments + q), p.y_rows), t0);
-            hi = min(clamp_to(__ldg(p.segments + q + 1), p.y_rows), t1);
-            ad = __ldg(p.adapters + q);
+            lo = max(clamp_to(load_now(p.segments + q), p.y_rows), t0);
+            hi = min(clamp_to(load_now(p.segments + q + 1), p.y_rows), t1);
+            ad = load_now(p.adapters + q);
         }
         left = __ballot_sync(kFull, lo < hi && unsigned(ad) < unsigned(p.n_adapters));
         late = 0u;
@@ -415,7 +415,7 @@ struct TileRequests {
                 if (unfit(p, __shfl_sync(kFull, ad, at), feature_tile, __shfl_sync(kFull, lo, at), __shfl_sync(kFull, hi, at), lane))
                     late |= 1u << at;
             }
-        more = __any_sync(kFull, q == q0 + 31 && q + 1 < p.requests && clamp_to(__ldg(p.segments + q + 1), p.y_rows) < t1);
+        more = __any_sync(kFull, q == q0 + 31 && q + 1 < p.requests && clamp_to(load_now(p.segments + q + 1), p.y_rows) < t1);
     }
     bool more;
     // Next of the split's requests, by its lane.
@@ -636,7 +636,7 @@ grouped_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const unsigned q = row0 + 4 * lane + i;
-                        r[i] = q < end ? __ldg(p.rows + q) : -1;
+                        r[i] = q < end ? load_now(p.rows + q) : -1;
                         if (r[i] < 0 || r[i] >= p.x_rows) r[i] = int(p.x_rows);
                     }
                     from = make_int4(r[0], r[1], r[2], r[3]);

@@ -118,8 +118,8 @@ dispatch_kernel(int64_t T, int64_t cols, int k, const X *x, int64_t ldx, int64_t
     float w[kSpread];
 #pragma unroll
     for (int j = 0; j < kSpread; ++j) {  // the look-ups in flight together
-        p[j] = j0 + j < k ? __ldg(where + t * k + j0 + j) : -1;
-        w[j] = j0 + j < k && weights != nullptr ? __ldg(weights + t * k + j0 + j) : 1.0f;
+        p[j] = j0 + j < k ? load_now(where + t * k + j0 + j) : -1;
+        w[j] = j0 + j < k && weights != nullptr ? load_now(weights + t * k + j0 + j) : 1.0f;
     }
 #pragma unroll
     for (int j = 0; j < kSpread; ++j) {
@@ -179,14 +179,14 @@ gather_kernel(const int32_t *offsets, int groups, int64_t positions, const uint1
     chain_wait();
     const int64_t p = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (p >= positions || p >= __ldg(offsets + groups)) return;
-    const int r = __ldg(rows + p);
+    if (p >= positions || p >= load_now(offsets + groups)) return;
+    const int r = load_now(rows + p);
     const bool there = r >= 0 && r < x_rows;
     const uint16_t *src = x + int64_t(there ? r : 0) * ldx;
     uint16_t *dst = out + p * ldo;
 #pragma unroll 4
     for (int64_t c = 8 * lane; c + 8 <= K; c += 256) {
-        const uint4 v = there ? __ldg(reinterpret_cast<const uint4 *>(src + c)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = there ? load_now(reinterpret_cast<const uint4 *>(src + c)) : make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4 *>(dst + c) = v;
     }
     const int64_t c = (K & ~int64_t(7)) + lane;

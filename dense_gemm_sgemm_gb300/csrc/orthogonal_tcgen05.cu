@@ -375,7 +375,7 @@ orthogonal_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 }
             };
             fetch(columns);
-            const float unit = p.unit != nullptr ? __ldg(p.unit + x.which) : 1.0f;
+            const float unit = p.unit != nullptr ? load_now(p.unit + x.which) : 1.0f;
             float mine = 0.0f;  // d or f of this row
             if (WHAT == kSquare && row) mine = __ldcg(p.d + x.which * p.ldn + m);
             if (WHAT >= kUpdate && row) mine = __ldcg(p.f + x.which * p.ldn + m);

@@ -66,7 +66,7 @@ __device__ __forceinline__ void load_lane(const T *row, int E, int lane, bool wi
     if (wide && lane * V + V <= E && kPiece * sizeof(T) == 16) {
 #pragma unroll
         for (int v = 0; v < V; v += kPiece) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(row + lane * V + v));
+            const uint4 q = load_now(reinterpret_cast<const uint4 *>(row + lane * V + v));
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) x[v + i] = to_f32(reinterpret_cast<const T *>(&q)[i]);
         }
@@ -190,7 +190,7 @@ __device__ void route_token(const RouteArgs &a, int64_t t, int lane, float *scra
     for (int v = 0; v < V; ++v) {
         const int e = lane * V + v;
         const bool live = e < E && x[v] > -INFINITY;
-        value[v] = !live ? -INFINITY : a.bias != nullptr ? s[v] + __ldg(a.bias + e) : s[v];
+        value[v] = !live ? -INFINITY : a.bias != nullptr ? s[v] + load_now(a.bias + e) : s[v];
         if (isnan(value[v])) value[v] = -INFINITY;
         key[v] = order_key(a.bias != nullptr ? value[v] : live ? x[v] : -INFINITY);
     }

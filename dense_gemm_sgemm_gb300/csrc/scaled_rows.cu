@@ -47,7 +47,7 @@ template <class T> struct Piece {
     {
         if (WHOLE || (wide && left >= 8)) {
 #pragma unroll
-            for (int i = 0; i < int(sizeof(T) / 2); ++i) u[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            for (int i = 0; i < int(sizeof(T) / 2); ++i) u[i] = load_now(reinterpret_cast<const uint4 *>(p) + i);
         } else {
             T *e = reinterpret_cast<T *>(u);
 #pragma unroll
@@ -367,15 +367,15 @@ dequantize_kernel(int64_t rows, int64_t cols, unsigned col_blocks, const uint8_t
         if (r >= rows) continue;
         const uint8_t *q = Q + r * ldq + c;
         if (left >= 8) {
-            w[i] = __ldg(reinterpret_cast<const uint2 *>(q));
+            w[i] = load_now(reinterpret_cast<const uint2 *>(q));
         } else {
             for (int j = 0; j < left; ++j) (j < 4 ? w[i].x : w[i].y) |= uint32_t(q[j]) << (8 * (j & 3));
         }
-        if (s.col_shift != 0) row[i] = __ldg(s.at + (r >> s.row_shift) * s.row + cb * s.col);
+        if (s.col_shift != 0) row[i] = load_now(s.at + (r >> s.row_shift) * s.row + cb * s.col);
     }
     float column[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) column[j] = s.col_shift == 0 && j < left ? __ldg(s.at + rb * s.row + (c + j) * s.col) : 1.0f;
+    for (int j = 0; j < 8; ++j) column[j] = s.col_shift == 0 && j < left ? load_now(s.at + rb * s.row + (c + j) * s.col) : 1.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = r0 + 16 * i;

@@ -56,3 +56,21 @@ def test_reading_back_takes_one_scale_for_a_block(g):
         q = g.quantize_blocks(torch.randn(rows, cols, generator=r).cuda())[0]
         s = torch.rand(rows, cols, generator=r).cuda()
         assert torch.equal(g.dequantize_blocks(q, s, out_dtype=torch.float32), q.float() * s)
+
+
+def test_chained_calls_read_what_the_call_before_wrote(g):
+    # every call takes its place on the SMs while the one before still runs, and writes to memory read a few calls ago
+    def chain(x, wait):
+        for i in range(60):
+            block = ((1, 128), (128, 1), (128, 128))[i % 3]
+            q, s = g.quantize_blocks(x, block, dtype=(torch.float8_e4m3fn, torch.float8_e5m2)[i % 2])
+            wait()
+            x = g.dequantize_blocks(q, s, out_dtype=torch.float32)
+            wait()
+            x = g.orthogonalize(x, steps=1, coefficients=(-0.9, 0.1, 0.0), out_dtype=torch.float32)
+            wait()
+        return x
+
+    for shape in ((130, 300), (500, 260)):
+        x = torch.randn(shape, generator=torch.Generator().manual_seed(5)).cuda()
+        assert torch.equal(chain(x, lambda: None), chain(x, torch.cuda.synchronize))
