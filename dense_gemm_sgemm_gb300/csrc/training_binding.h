@@ -7,12 +7,21 @@ gemm_type_t type8_of(at::ScalarType t, const char *what)
     return t == at::kFloat8_e4m3fn ? GEMM_TYPE_E4M3 : GEMM_TYPE_E5M2;
 }
 
+// These calls record no gradient: a tensor that would have one is refused rather than its gradient dropped in silence.
+const at::Tensor &constant(const at::Tensor &t, const char *what)
+{
+    TORCH_CHECK_VALUE(!(t.requires_grad() && c10::GradMode::is_enabled()), what,
+                      ": requires a gradient, which this call does not record (torch.no_grad() takes its value)");
+    return t;
+}
+
 int64_t blocks_of(int64_t size) { return (size + 127) / 128; }
 
 // An 8-bit matrix: as matrix(), rows on 16-byte pieces being 16 elements.
 Matrix matrix8(Device &device, PyObject *o, const char *what)
 {
     Matrix m = matrix(device, o, what);
+    constant(m.t, what);
     if (m.rows <= 1) m.ld = std::max((m.cols + 15) & ~int64_t(15), int64_t(16));
     return m;
 }
@@ -31,7 +40,7 @@ int block_along(int64_t count, int64_t size, const char *what)
 }
 BlockScales scales_of(Device &device, PyObject *o, const Matrix &q, const char *what)
 {
-    const at::Tensor &t = tensor(device, o, what);
+    const at::Tensor &t = constant(tensor(device, o, what), what);
     same_type(t, at::kFloat, what);
     TORCH_CHECK_VALUE(t.dim() == 2, what, ": 2-D wanted");
     return BlockScales{t.data_ptr<float>(), t.stride(0), t.stride(1), block_along(t.size(0), q.rows, what),
@@ -61,6 +70,7 @@ struct Quantized {
 // x, block_rows, block_cols, dtype, stream
 BOUND(quantize_blocks, 5)
     const Matrix x = matrix(device, a[0], "x");
+    constant(x.t, "x");
     const Stream stream(a[4], x.t);
     const int rows = small(a[1]), cols = small(a[2]);
     const gemm_type_t type = type_of(x.t.scalar_type(), "x");
@@ -77,6 +87,7 @@ END_BOUND
 // x, dtype, stream
 BOUND(quantize_both, 3)
     const Matrix x = matrix(device, a[0], "x");
+    constant(x.t, "x");
     const Stream stream(a[2], x.t);
     const gemm_type_t type = type_of(x.t.scalar_type(), "x");
     const at::ScalarType dtype = dtype_of(a[1], at::kFloat8_e4m3fn);
@@ -132,7 +143,7 @@ END_BOUND
 
 // g, steps, coefficients (a tuple of 3 * steps numbers), eps, out_dtype, stream
 BOUND(orthogonalize, 6)
-    const at::Tensor &t = tensor(device, a[0], "g");
+    const at::Tensor &t = constant(tensor(device, a[0], "g"), "g");
     TORCH_CHECK_VALUE(t.dim() == 2 || t.dim() == 3, "g: a matrix or a stack of matrices (2-D or 3-D) wanted");
     const Matrix x = matrix(device, a[0], "g", int(t.dim()));
     const Stream stream(a[5], t);

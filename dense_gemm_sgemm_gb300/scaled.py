@@ -6,8 +6,9 @@ and shapes, create the outputs, pass addresses, strides and the current CUDA str
 the compiled binding), and raise TypeError or ValueError on a bad argument, GemmError on a non-OK status.
 Matrices need unit column stride; 8-bit ones have rows on 16-byte boundaries (a row stride that is a
 multiple of 16), as what these functions return does.  Scales are 2-D fp32 tensors of any strides, one
-for every block; their shape tells the block.  All tensors of a call live on one device.  A linear
-layer y = x w^T, its weight quantised once, and the gradients of its input and weight:
+for every block; their shape tells the block.  All tensors of a call live on one device.  No gradient is
+recorded: outside torch.no_grad() a tensor that requires one is refused.  A linear layer y = x w^T, its
+weight quantised once, and the gradients of its input and weight:
 
     wq, ws = quantize_blocks(w, (128, 128))                          # w N x K
     xq, xs, xc, xcs = quantize_both(x)                               # x T x K

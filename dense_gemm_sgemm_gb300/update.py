@@ -3,7 +3,8 @@
 Tensor-level face of gemm_orthogonalize of include/gemm_gb300.h, which states its formula, precision and
 limits.  The function checks types and shapes, creates the output and the call's work space, passes
 addresses, strides and the current CUDA stream to the library (in the compiled binding), and raises
-TypeError or ValueError on a bad argument, GemmError on a non-OK status.  One step of an optimiser with
+TypeError or ValueError on a bad argument (outside torch.no_grad() a g that requires a gradient is one: none
+is recorded), GemmError on a non-OK status.  One step of an optimiser with
 momentum m of a weight w (both fp32) and gradient g:
 
     m.mul_(0.95).add_(g)
