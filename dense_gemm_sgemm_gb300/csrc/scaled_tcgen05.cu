@@ -133,8 +133,9 @@ __device__ __forceinline__ bool mild(float s)
     return a == 0.0f || (a >= 0x1p-40f && a <= 0x1p40f);
 }
 // s as two factors of half its exponent each (zero, infinite and NaN scales as 1 and s), the second one below 2^64,
-// so that the product of two of them is finite.  A block's sum times one scale's first factor, the other's, and then
-// both second ones stays in fp32's range wherever the result does, and a sum of zero stays zero.
+// so that the product of two of them is finite.  A block's sum times both scales' first factors and then both second
+// ones stays in fp32's range wherever the result does.  (Two first factors of 2^64, rounded towards zero, are fp32's
+// largest value, so that a sum of zero stays zero; any other is beyond fp32's range either way.)
 __device__ __forceinline__ float2 halves(float s)
 {
     const float a = fabsf(s);
@@ -355,7 +356,7 @@ template <int CW, bool COLS, bool PAIRS> struct Sums {
             const int run = PAIRS ? i * kChunk / 64 : 0;
 #pragma unroll
             for (int j = 0; j < kChunk; ++j)
-                v[j] = __float_as_uint(__uint_as_float(v[j]) * h.x * scratch[CW + (COLS ? i * kChunk + j : run)]);
+                v[j] = __float_as_uint(__uint_as_float(v[j]) * __fmul_rz(h.x, scratch[CW + (COLS ? i * kChunk + j : run)]));
             add_chunk(i * kChunk, v, COLS ? h.y : h.y * scratch[run], scratch);
         }
     }
