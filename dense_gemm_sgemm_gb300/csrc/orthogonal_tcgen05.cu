@@ -491,7 +491,7 @@ int rows_b(int form) { return form & 1 ? 64 : 128; }
 // The form whose waves of tiles cost least: a tile takes `slice` SM cycles a slice of 64 k and as much for `more`
 // slices beyond its own.  The symmetric products take one form, for the `slices` of both (other: the square's).
 // Fitted to 29 shapes, from 64 x 64 to 4096 x 4096 and stacks of up to 60, each in all 16 pairs of forms; of 17 of them the
-// ones taken are on average 0.9% slower than the fastest pair.  (Whole calls: 256 x 512 104 us with 128 x 64, 128 with
+// ones taken are on average 0.8% slower than the fastest pair.  (Whole calls: 256 x 512 104 us with 128 x 64, 128 with
 // 128 x 128, 137 and 197 with pairs; 2048 x 4096 with 256 x 256 and the symmetric ones in 256 x 128 657 us, the other
 // forms throughout 782 to 1316; 4096 x 4096 in 256 x 256 2510 to 2750 us; 16 of 1000 x 520 455, where 256 x 256 for the
 // update alone would take 416.)

@@ -17,13 +17,13 @@
 // full wave.  With few rows of A (or B) the host swaps the operands: the long side takes the 128 lanes, the short
 // one the BN columns.
 //
-// What bounds them (GB300).  Pairs, 16384 x 4096 x 4096, B's scales by 128 x 128: 209 to 215 us, 2560 to 2630 TFLOP/s, about 900 SM
-// cycles a block, of which the MMAs need 512 and the copies from L2 (64 KB a pair) 625: the adding warps, which
+// What bounds them (GB300).  Pairs, 16384 x 4096 x 4096, B's scales by 128 x 128: 209 to 221 us (the device's temperature), 2490
+// to 2630 TFLOP/s, about 900 SM cycles a block, of which the MMAs need 512 and the copies from L2 (64 KB a pair) 625: the adding warps, which
 // read 256 columns of all lanes from tensor memory and issue as many multiply-adds; with a scale for every column
 // of B 319 us, since each pair of sums takes a product more and its scales from shared memory.  4096 x 4096 x 8192,
 // scales of both by column, fp32 out: 183 us in pairs alone, 168 with the last wave's 28 tiles in single CTAs.
-// Tiles: latency: 1 x 4096 x 4096 8.0 us (2.1 TB/s of weight), 64 x 8192 x 4096 11.7 (2.9 TB/s), 512 x 4096 x 1024
-// 8.5: 4 to 5 us of launch, first copies, and joining and storing the sums, and 0.2 to 0.35 us a block.
+// Tiles: latency: 1 x 4096 x 4096 6.9 us (2.4 TB/s of weight), 64 x 8192 x 4096 10.6 (3.2 TB/s), 512 x 4096 x 1024
+// 8.2: 4 to 5 us of launch, first copies, and joining and storing the sums, and 0.2 to 0.35 us a block.
 // Tried and dropped: 16 adding warps of 64 columns each (242 us, registers too few), 256-column pieces, loads of the
 // scales to registers (750 cycles a block whatever its size), one-lane producers and issuers in the pair kernel
 // (the adding warps then spill more).
@@ -1021,8 +1021,8 @@ struct Plan {
 // K block, the sum of a cluster's parts `join`; CTAs run one an SM.  A pair's tile takes 0.5 a block, 0.72 with
 // column scales.  Tiles' copies reach 5.5 TB/s.  Fitted to 35 shapes from 1 x 512 x 512 to 3000 x 4096 x 4096, each
 // with up to 16 plans: the plan taken is on average 3% slower than the fastest (64 x 8192 x 4096: 64 columns unsplit
-// 11.7, the halves of 128 columns 13.1, swapped 14.3; 1 x 4096 x 4096: swapped, 4 parts 8.1, 2 parts 8.4, unswapped
-// 10.1).  The tiles beyond the last full wave in single CTAs: 2304 x 2304 x 4096, 5 tiles, 33.5 us with pairs alone,
+// 10.6, the halves of 128 columns 11.3, swapped 12.7; 1 x 4096 x 4096: swapped, 4 parts 7.0, 2 parts 7.9, unswapped 15.6
+// and more).  The tiles beyond the last full wave in single CTAs: 2304 x 2304 x 4096, 5 tiles, 33.5 us with pairs alone,
 // 32.4, 30.2 and 29.1 with 1, 2 and 4 parts of K; 8192 x 4096 x 4096, 56 tiles, 110 with pairs alone, 121 and more.
 Plan plan_of(const DeviceInfo &dev, const ScaledArgs &a)
 {
