@@ -263,13 +263,14 @@ double largest_inner(double b, double c, double r)
     return most;
 }
 // The power of two that brings values up to `bound` close to, and not over, 60000 in fp16.  The iterates' bounds are
-// kLeastBound or more, so those of A are its square or more; for b A + c A^2, which may vanish, 2^-60 stands for less.
-// Two such scales' product and its inverse are in fp32's range.
-constexpr double kLeastBound = 0x1p-20;
+// kLeastBound or more, so those of A are its square or more; for b A + c A^2, which may vanish, kLeastResult stands for
+// less: what its parts then lose is below 2^-100, far below any result.  Two such scales' product and its inverse are
+// in fp32's range.
+constexpr double kLeastBound = 0x1p-20, kLeastResult = 0x1p-60;
 float scale_for(double bound)
 {
     int e;
-    std::frexp(60000.0 / std::fmax(bound, 0x1p-60), &e);
+    std::frexp(60000.0 / std::fmax(bound, kLeastResult), &e);
     return float(std::ldexp(1.0, e - 1));
 }
 
@@ -348,7 +349,7 @@ gemm_status_t gemm_orthogonalize(gemm_type_t type, gemm_type_t y_type, int64_t c
         p = OrthogonalStep{a, b, c, i == 0 ? float(1 << kFirstScale) : plan[i - 1].next_scale, scale_for(r * r),
                            scale_for(1.02 * largest_inner(b, c, r)), 1.0f};
         r = 1.02 * largest_value(a, b, c, r);
-        if (!(r <= 1e4) || (i + 1 < steps && r < kLeastBound)) return GEMM_ERR_UNSUPPORTED;
+        if (!(r <= 1e4) || (i + 1 < steps ? r < kLeastBound : r > 0.0 && r < kLeastResult)) return GEMM_ERR_UNSUPPORTED;
         p.next_scale = scale_for(r);
     }
     if (count == 0 || rows == 0 || cols == 0) return GEMM_OK;

@@ -582,7 +582,8 @@ GEMM_API gemm_status_t gemm_scaled_matmul(gemm_type_t a_type, gemm_type_t b_type
  * aligned; about 16 bytes for every element of a square G.
  * The call allocates nothing and keeps nothing, so it may be captured into a graph.
  * GEMM_ERR_UNSUPPORTED: coefficients beyond 10^4, or under which a singular value of at most 1 may grow
- * beyond 10^4 on the way, or none can be above 2^-20 after a step that is not the last.
+ * beyond 10^4 on the way, or none can be above 2^-20 after a step that is not the last, or
+ * above 2^-60 after the last (unless its coefficients are all zero).
  * Alignment: Y 16-byte aligned, ldy and strideY multiples of 8 elements.  Limits: rows and cols < 2^20,
  * count < 2^16, steps <= 64.  Y must not overlap G.
  */

@@ -125,7 +125,7 @@ def test_a_matrix_of_a_stack_is_the_same_as_alone(g, shape, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("each", [[(0.5, 0.0, 0.0)] * 20, [(0.01, 0.0, 0.0)] * 4, [(0.0, -0.03, 0.0), (0.0, 1.0, 0.0)], [(0.0, 0.0, 0.0)],
-                                  [(0.02, 0.0, 0.0), (2.0, -1.5, 0.5)]])
+                                  [(0.02, 0.0, 0.0), (2.0, -1.5, 0.5)], [(0.0, 1e-17, 0.0)], [(0.0, 0.0, -1e-17)]])
 def test_steps_that_shrink_the_iterate(g, each, dtype):
     # what an iterate loses is in proportion to its own bound, whatever that is; a step's three products and
     # epilogues are off by less than 2^-20, which no step here grows to more than 9 times (the fifth power's 5, the cube's 3)

@@ -19,6 +19,8 @@ def lib():
     # iterates that shrink out of what two fp16 parts hold: every singular value is below 2^-20 before the last step
     (UNSUPPORTED, [(0.5, 0.0, 0.0)] * 64), (UNSUPPORTED, [(0.5, 0.0, 0.0)] * 22), (UNSUPPORTED, [(1e-4, 0.0, 0.0)] * 3),
     (UNSUPPORTED, [(0.0, 0.0, 0.0)] * 2), (UNSUPPORTED, [(0.0, 0.01, 0.0)] * 3),
+    # results below what the parts of b A + c A^2 hold
+    (UNSUPPORTED, [(0.0, 1e-30, 0.0)]), (UNSUPPORTED, [(1e-4, 0.0, 0.0), (0.0, 0.0, 1e-3)]), (OK, [(0.0, 1e-17, 0.0)]), (OK, [(1.0, 1e-30, 0.0)]),
     (OK, [(0.5, 0.0, 0.0)] * 20), (OK, [(1e-4, 0.0, 0.0)] * 2), (OK, [(0.0, 0.0, 0.0)]), (OK, [(0.0, 0.01, 0.0)] * 2),
     (OK, [(1.5, -0.5, 0.0)] * 64), (OK, [(3.4445, -4.7750, 2.0315)] * 64),
 ])
